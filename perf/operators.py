@@ -1,0 +1,481 @@
+"""The sequence operators at the sizes of real use: cross attention of candidates
+over a sample's behaviour states (with a learned bias by buckets of elapsed time),
+and the gated linear recurrence that makes such states; forward, training and
+single-step serving, each with a plain form in elementary torch operations.
+
+A case's `lengths` seeds its jagged lengths, so that a case's work is the same for
+every seed of its values."""
+import math
+import random
+
+import torch
+
+own = False
+
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _attention(name, train, dtype, samples, q, k, heads, kv_heads, dim, buckets, masked, lengths):
+    return {"name": name, "op": "attention", "train": train, "dtype": dtype, "samples": samples,
+            "q_lo": q[0], "q_hi": q[1], "k_lo": k[0], "k_hi": k[1], "heads": heads,
+            "kv_heads": kv_heads, "dim": dim, "buckets": buckets, "masked": masked,
+            "lengths": lengths}
+
+
+def _recurrence(name, op, train, dtype, samples, n, channels, state, masked, lengths):
+    return {"name": name, "op": op, "train": train, "dtype": dtype, "samples": samples,
+            "k_lo": n[0], "k_hi": n[1], "channels": channels, "state": state, "masked": masked,
+            "lengths": lengths}
+
+
+def listed():
+    return [
+        # one user's request with one candidate over a short history: latency alone counts
+        _attention("attend_one_user", False, "bf16", 1, (1, 1), (50, 50), 4, 4, 32, 16, 0.0, 1),
+        # a serving batch: a few candidates a user over histories of the long-sequence
+        # workload's lengths, some positions masked away; the reading of k and v counts
+        _attention("attend_serving_batch", False, "bf16", 512, (1, 8), (200, 2000), 4, 4, 64, 32,
+                   0.1, 2),
+        # lifelong histories, one candidate each, shared key heads: a split over the keys
+        _attention("attend_lifelong", False, "bf16", 4, (1, 1), (60000, 131072), 8, 2, 128, 0, 0.0,
+                   3),
+        # ranking of several hundred candidates a user: products on both sides
+        _attention("attend_candidates", False, "bf16", 32, (100, 500), (200, 2000), 4, 4, 64, 32,
+                   0.1, 4),
+        # full precision, a head size that is no power of two, samples without candidates or history
+        _attention("attend_odd_f32", False, "f32", 37, (0, 40), (0, 333), 6, 3, 40, 17, 0.2, 5),
+        # a training step of the ranking model on the workload's lengths
+        _attention("train_ranking", True, "bf16", 64, (20, 100), (200, 2000), 4, 4, 64, 32, 0.1, 6),
+        # training with a query at nearly every position of another long sequence
+        _attention("train_two_sequences", True, "bf16", 8, (1500, 2048), (1500, 2048), 8, 8, 128,
+                   32, 0.0, 7),
+        # full-precision training of a small model with shared key heads and empty histories
+        _attention("train_small_f32", True, "f32", 16, (1, 64), (0, 500), 4, 2, 32, 12, 0.1, 8),
+        # one event for each of a batch of users: the state moves one step, latency alone counts
+        _recurrence("step_users", "step", False, "bf16", 64, (1, 1), 256, True, 0.0, 9),
+        # states of a batch of histories, some positions masked, from stored states
+        _recurrence("scan_histories", "scan", False, "bf16", 256, (200, 2000), 256, True, 0.1, 10),
+        # a training step of the encoder on the workload's lengths
+        _recurrence("train_scan", "scan", True, "bf16", 128, (200, 2000), 512, False, 0.0, 11),
+        # one lifelong history in full precision: the scan itself has to be split
+        _recurrence("train_lifelong_f32", "scan", True, "f32", 1, (65537, 65537), 384, True, 0.0,
+                    12),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    lengths = rng.randrange(1, 1 << 20)
+    masked = rng.choice([0.0, 0.1, 0.3])
+    op = rng.choice(["attention", "attention", "attention", "scan", "scan", "step"])
+    train = op != "step" and rng.random() < 0.5
+    if op == "attention":
+        kv = rng.choice([1, 2, 3, 4, 8])
+        heads = kv * rng.choice([1, 1, 2, 4])
+        dim = rng.choice([16, 24, 32, 40, 64, 64, 80, 96, 128])
+        k_hi = _log(rng, 20, 20000)
+        q_hi = _log(rng, 1, min(2048, k_hi))
+        # at most this many padded pairs over all heads, and rows of k, so that no
+        # drawn case costs more than the largest listed ones
+        pairs = (2 ** 27 if dtype == "bf16" else 2 ** 25) // (1 if dim <= 64 else 2)
+        most = min(512, pairs // (heads * q_hi * k_hi), 2 ** 28 // (kv * dim * k_hi))
+        while most < 1:
+            q_hi, k_hi = max(1, q_hi // 2), max(20, k_hi // 2)
+            most = min(512, pairs // (heads * q_hi * k_hi), 2 ** 28 // (kv * dim * k_hi))
+        return _without_name(_attention("", train, dtype, _log(rng, 1, most) if most > 1 else 1,
+                                        (rng.randint(0, q_hi) if q_hi > 1 else 1, q_hi),
+                                        (rng.randint(0, k_hi), k_hi), heads, kv, dim,
+                                        rng.choice([0, 9, 16, 32, 33]), masked, lengths))
+    channels = rng.choice([24, 64, 96, 128, 200, 256, 384, 512])
+    if op == "step":
+        return _without_name(_recurrence("", op, False, dtype, _log(rng, 1, 2048), (1, 1),
+                                         channels, True, 0.0, lengths))
+    hi = _log(rng, 16, 70000)
+    most = max(1, 2 ** 26 // (channels * hi * (1 if dtype == "bf16" else 2)))
+    return _without_name(_recurrence("", op, train, dtype, min(2048, _log(rng, 1, most)) if most > 1
+                                     else 1, (rng.randint(0, hi), hi), channels,
+                                     rng.random() < 0.5, masked, lengths))
+
+
+def _without_name(case):
+    return {key: value for key, value in case.items() if key != "name"}
+
+
+# ------------------------------------------------------------------- inputs
+
+def _lengths(case):
+    """The case's (query, key) lengths of each sample."""
+    rng = random.Random(case["lengths"])
+    k = [rng.randint(case["k_lo"], case["k_hi"]) for _ in range(case["samples"])]
+    q = [rng.randint(case["q_lo"], case["q_hi"]) for _ in k] if "q_lo" in case else [0] * len(k)
+    return q, k
+
+
+def _offsets(lengths, device):
+    total = [0]
+    for n in lengths:
+        total.append(total[-1] + n)
+    return torch.tensor(total, dtype=torch.int32, device=device)
+
+
+def _boundaries(n):
+    """n int32 boundaries, ascending: a few below zero, the rest spread over the
+    logarithm of the elapsed seconds up to about four months."""
+    neg = n // 4
+    pos = [int(round(math.exp(math.log(10.0) + (math.log(1e7) - math.log(10.0)) * j
+                              / max(1, n - neg - 1)))) for j in range(n - neg)]
+    below = [-int(round(10.0 * 20.0 ** j)) for j in range(min(neg, 6))]
+    below += [-40_000_000 - j for j in range(max(0, neg - 6))]
+    return sorted(below + pos)
+
+
+def _mask(case, offsets, n, gen, device):
+    """One byte a position, zero where it is out; the second sample loses all of its positions."""
+    if not case["masked"]:
+        return None
+    mask = (torch.rand(n, generator=gen, device=device) >= case["masked"]).to(torch.uint8)
+    if case["samples"] > 1:
+        mask[int(offsets[1]):int(offsets[2])] = 0
+    return mask
+
+
+def prepare(case, seed):
+    device = torch.device("cuda" if torch.cuda.is_available() else "cpu")
+    gen = torch.Generator(device=device).manual_seed(seed)
+    dtype, train = DTYPES[case["dtype"]], case["train"]
+
+    def normal(*shape, mean=0.0, std=1.0, dtype=dtype):
+        t = torch.randn(*shape, generator=gen, device=device)
+        return t.mul_(std).add_(mean).to(dtype)
+
+    q_len, k_len = _lengths(case)
+    nq, nk = sum(q_len), sum(k_len)
+    s = {"case": case, "k_max": max(k_len)}
+    if case["op"] != "attention":
+        c = case["channels"]
+        s["offsets"] = _offsets(k_len, device)
+        s["mask"] = _mask(case, s["offsets"], nk, gen, device)
+        s["x"] = normal(nk, c).requires_grad_(train)
+        s["gate"] = normal(nk, c, mean=2.0, std=2.0).requires_grad_(train)   # mostly remembering
+        s["state"] = (normal(case["samples"], c, dtype=torch.float32).requires_grad_(train)
+                      if case["state"] else None)
+        if train:
+            s["dy"] = normal(nk, c)
+            s["dlast"] = normal(case["samples"], c, dtype=torch.float32)
+        return s
+    h, hkv, d = case["heads"], case["kv_heads"], case["dim"]
+    s["q_max"] = max(q_len)
+    s["q_offsets"], s["k_offsets"] = _offsets(q_len, device), _offsets(k_len, device)
+    s["mask"] = _mask(case, s["k_offsets"], nk, gen, device)
+    s["q"] = normal(nq, h, d, std=1.5).requires_grad_(train)
+    s["k"] = normal(nk, hkv, d).requires_grad_(train)
+    s["v"] = normal(nk, hkv, d).requires_grad_(train)
+    s["bias"] = s["boundaries"] = s["q_pos"] = s["k_pos"] = None
+    if case["buckets"]:
+        s["boundaries"] = torch.tensor(_boundaries(case["buckets"] - 1), dtype=torch.int32,
+                                       device=device)
+        s["bias"] = normal(case["buckets"], h, dtype=torch.float32).requires_grad_(train)
+        # behaviours follow each other with gaps of an hour on average, in order of
+        # time; candidates of a request come within the hour after the last one,
+        # and long query sequences run alongside the keys
+        gaps = torch.empty(nk, device=device).exponential_(1 / 3600.0, generator=gen).to(torch.int64)
+        at = torch.cumsum(gaps, 0)
+        ko = s["k_offsets"].long()
+        sample_k = torch.repeat_interleave(torch.arange(case["samples"], device=device),
+                                           ko[1:] - ko[:-1], output_size=nk)
+        first = torch.cat([at, at.new_zeros(1)])[ko[:-1].clamp(max=max(nk - 1, 0))]
+        at = at - first[sample_k]
+        s["k_pos"] = at.to(torch.int32)
+        qo = s["q_offsets"].long()
+        sample_q = torch.repeat_interleave(torch.arange(case["samples"], device=device),
+                                           qo[1:] - qo[:-1], output_size=nq)
+        span = torch.zeros(case["samples"], dtype=torch.int64, device=device)
+        span = span.scatter_reduce(0, sample_k, at, "amax")
+        if case["q_hi"] > 600:
+            index = torch.arange(nq, device=device) - qo[:-1][sample_q]
+            pos = index * span[sample_q] // (qo[1:] - qo[:-1])[sample_q].clamp(min=1)
+        else:
+            pos = span[sample_q] + torch.randint(1, 3600, (nq,), generator=gen, device=device)
+        s["q_pos"] = pos.to(torch.int32)
+    if train:
+        s["dout"] = normal(nq, h, d)
+    return s
+
+
+# -------------------------------------------------------------- plain forms
+
+def _padded(offsets, longest, n):
+    """Row of each (sample, place), and whether there is one."""
+    start = offsets[:-1].long()[:, None]
+    place = torch.arange(longest, device=offsets.device)
+    there = place < (offsets[1:].long()[:, None] - start)
+    return (start + place).clamp(max=max(n - 1, 0)) * there, there
+
+
+def _plain_attention(s):
+    case = s["case"]
+    hkv, d = case["kv_heads"], case["dim"]
+    g = case["heads"] // hkv
+    q, k, v = (s[n].detach() for n in ("q", "k", "v"))
+    nq, nk, b, dtype = q.shape[0], k.shape[0], case["samples"], q.dtype
+    scale = 1.0 / math.sqrt(d)
+    if not nq or not nk:
+        out = {"out": torch.zeros_like(q)}
+        if case["train"]:
+            out.update(dq=torch.zeros_like(q), dk=torch.zeros_like(k), dv=torch.zeros_like(v))
+            if s["bias"] is not None:
+                out["dbias"] = torch.zeros_like(s["bias"])
+        return out
+    qi, q_there = _padded(s["q_offsets"], s["q_max"], nq)
+    ki, k_there = _padded(s["k_offsets"], s["k_max"], nk)
+    kept = k_there if s["mask"] is None else k_there & (s["mask"][ki] != 0)
+
+    def queries(t):        # [b, hkv, g * lq, d]
+        t = t.float()[qi] * q_there[:, :, None, None]
+        return t.view(b, -1, hkv, g, d).permute(0, 2, 3, 1, 4).reshape(b, hkv, -1, d)
+
+    def keys(t):           # [b, hkv, lk, d]
+        return (t.float()[ki] * kept[:, :, None, None]).permute(0, 2, 1, 3).contiguous()
+
+    def rows(t):           # back to [nq, heads, d]
+        t = t.view(b, hkv, g, -1, d).permute(0, 3, 1, 2, 4).reshape(b, -1, hkv * g, d)
+        return t[q_there].to(dtype)
+
+    def key_rows(t):       # back to [nk, hkv, d]
+        return t.permute(0, 2, 1, 3)[k_there].to(dtype)
+
+    qf, kf, vf = queries(q), keys(k), keys(v)
+    score = torch.matmul(qf, kf.transpose(-1, -2).contiguous()) * scale
+    bucket = None
+    if s["bias"] is not None:
+        apart = s["q_pos"].long()[qi][:, :, None] - s["k_pos"].long()[ki][:, None, :]
+        bucket = torch.bucketize(apart, s["boundaries"].long(), right=True)
+        table = s["bias"].detach().t().contiguous()                     # [heads, buckets]
+        score += table[:, bucket].view(hkv, g, b, -1, s["k_max"]).permute(2, 0, 1, 3, 4).reshape(
+            score.shape)
+    score = score.masked_fill(~kept[:, None, None, :], -math.inf)
+    top = score.amax(-1, keepdim=True)
+    p = torch.exp(score - torch.where(top == -math.inf, torch.zeros_like(top), top))
+    total = p.sum(-1, keepdim=True)
+    p = p / torch.where(total == 0, torch.ones_like(total), total)
+    out = {"out": rows(torch.matmul(p, vf))}
+    if not case["train"]:
+        return out
+    df = queries(s["dout"])
+    dp = torch.matmul(df, vf.transpose(-1, -2).contiguous())
+    ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+    out["dq"] = rows(torch.matmul(ds, kf) * scale)
+    out["dk"] = key_rows(torch.matmul(ds.transpose(-1, -2).contiguous(), qf) * scale)
+    out["dv"] = key_rows(torch.matmul(p.transpose(-1, -2).contiguous(), df))
+    if bucket is not None:
+        ds = ds.view(b, hkv * g, -1, s["k_max"])
+        out["dbias"] = torch.stack([(ds * (bucket == m)[:, None]).sum((0, 2, 3))
+                                    for m in range(case["buckets"])])
+    return out
+
+
+def _plain_scan(keep, add, longest, reverse):
+    """h_t = keep_t h_(t-1) + add_t over axis 0 (h_(t+1) where reverse), by doubling the
+    span that each position has taken in; keep is 0 where a sample begins."""
+    span = 1
+    while span < longest:
+        pad = torch.zeros_like(add[:span])
+        if reverse:
+            add = add + keep * torch.cat([add[span:], pad])
+            keep = keep * torch.cat([keep[span:], pad])
+        else:
+            add = add + keep * torch.cat([pad, add[:-span]])
+            keep = keep * torch.cat([pad, keep[:-span]])
+        span *= 2
+    return add
+
+
+def _plain_recurrence(s):
+    case = s["case"]
+    x, gate = s["x"].detach().float(), s["gate"].detach().float()
+    if case["op"] == "step":
+        s["state"].copy_(torch.sigmoid(gate) * s["state"] + torch.sigmoid(-gate) * x)
+        return {"y": s["state"].to(s["x"].dtype), "last": s["state"]}
+    n, c, b, dtype = x.shape[0], case["channels"], case["samples"], s["x"].dtype
+    off = s["offsets"].long()
+    state = s["state"].detach() if s["state"] is not None else x.new_zeros(b, c)
+    there = off[1:] > off[:-1]
+    first, last = off[:-1][there], off[1:][there] - 1
+    a, na = torch.sigmoid(gate), torch.sigmoid(-gate)
+    if s["mask"] is not None:
+        kept = (s["mask"] != 0)[:, None]
+        a, na = torch.where(kept, a, torch.ones_like(a)), torch.where(kept, na, torch.zeros_like(a))
+    add, keep = na * x, a.clone()
+    add[first] += a[first] * state[there]
+    keep[first] = 0
+    h = _plain_scan(keep, add, s["k_max"], False)
+    final = state.clone()
+    final[there] = h[last]
+    out = {"y": h.to(dtype), "last": final}
+    if not case["train"]:
+        return out
+    add = s["dy"].float()
+    add[last] += s["dlast"][there]
+    keep = torch.cat([a[1:], a.new_zeros(1, c)])[:n]
+    keep[last] = 0
+    grad = _plain_scan(keep, add, s["k_max"], True)
+    before = torch.cat([x.new_zeros(1, c), h])[:n]
+    before[first] = state[there]
+    out["dx"] = (na * grad).to(dtype)
+    out["dgate"] = (a * na * (before - x) * grad).to(dtype)
+    if s["state"] is not None:
+        dstate = s["dlast"].clone()
+        dstate[there] = a[first] * grad[first]
+        out["dstate"] = dstate
+    return out
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(s):
+    case = s["case"]
+    if not own:
+        return _plain_attention(s) if case["op"] == "attention" else _plain_recurrence(s)
+    import embedding_columns_amd as E
+    if case["op"] == "step":
+        y = E.gated_recurrence_step(s["x"], s["gate"], s["state"])
+        return {"y": y, "last": s["state"]}
+    if case["op"] == "scan":
+        y, last = E.gated_recurrence(s["x"], s["gate"], s["offsets"], state=s["state"],
+                                     mask=s["mask"])
+        if not case["train"]:
+            return {"y": y, "last": last}
+        wanted = [s["x"], s["gate"]] + ([s["state"]] if s["state"] is not None else [])
+        grads = torch.autograd.grad([y, last], wanted, [s["dy"], s["dlast"]])
+        return {"y": y, "last": last, **dict(zip(("dx", "dgate", "dstate"), grads))}
+    out = E.cross_attention(s["q"], s["k"], s["v"], s["q_offsets"], s["k_offsets"], mask=s["mask"],
+                            bias=s["bias"], boundaries=s["boundaries"], q_pos=s["q_pos"],
+                            k_pos=s["k_pos"])
+    if not case["train"]:
+        return {"out": out}
+    wanted = [s["q"], s["k"], s["v"]] + ([s["bias"]] if s["bias"] is not None else [])
+    grads = torch.autograd.grad(out, wanted, s["dout"])
+    return {"out": out, **dict(zip(("dq", "dk", "dv", "dbias"), grads))}
+
+
+def work(case):
+    size = 2 if case["dtype"] == "bf16" else 4
+    q_len, k_len = _lengths(case)
+    nq, nk, b = sum(q_len), sum(k_len), case["samples"]
+    masks = nk if case["masked"] else 0
+    if case["op"] != "attention":
+        c = case["channels"]
+        states = 4 * b * c * (2 if case["state"] else 1)
+        if not case["train"]:
+            return {"bytes": 3 * nk * c * size + states + masks, "flops": 10 * nk * c}
+        return {"bytes": 6 * nk * c * size + 2 * states + masks, "flops": 30 * nk * c}
+    h, hkv, d = case["heads"], case["kv_heads"], case["dim"]
+    pairs = sum(x * y for x, y in zip(q_len, k_len))
+    n_bytes = size * d * (2 * nq * h + 2 * nk * hkv) + masks + 4 * (nq + nk) * bool(case["buckets"])
+    if not case["train"]:
+        return {"bytes": n_bytes, "flops": 4 * d * h * pairs}
+    return {"bytes": n_bytes + size * d * (2 * nq * h + 2 * nk * hkv), "flops": 14 * d * h * pairs}
+
+
+# ---------------------------------------------------- the definitions in 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    return _exact_attention(s) if case["op"] == "attention" else _exact_recurrence(s)
+
+
+def _exact_attention(s):
+    """Sample by sample, head by head of the keys, from the definition of the softmax."""
+    case = s["case"]
+    hkv, d, train = case["kv_heads"], case["dim"], case["train"]
+    g = case["heads"] // hkv
+    q, k, v = (s[n].detach().double() for n in ("q", "k", "v"))
+    out = {"out": torch.zeros_like(q)}
+    if train:
+        dout = s["dout"].double()
+        out.update(dq=torch.zeros_like(q), dk=torch.zeros_like(k), dv=torch.zeros_like(v))
+    biased = s["bias"] is not None
+    if biased:
+        table = s["bias"].detach().double()
+        if train:
+            out["dbias"] = torch.zeros_like(table)
+    qo, ko = s["q_offsets"].tolist(), s["k_offsets"].tolist()
+    for b in range(case["samples"]):
+        rows = slice(qo[b], qo[b + 1])
+        cols = torch.arange(ko[b], ko[b + 1], device=k.device)
+        if s["mask"] is not None:
+            cols = cols[s["mask"][ko[b]:ko[b + 1]] != 0]
+        if qo[b + 1] == qo[b] or not cols.numel():
+            continue
+        if biased:
+            apart = s["q_pos"][rows].long()[:, None] - s["k_pos"][cols].long()[None, :]
+            bucket = torch.zeros_like(apart)
+            for edge in s["boundaries"].tolist():
+                bucket += apart >= edge
+        kb, vb = k[cols].transpose(0, 1).contiguous(), v[cols].transpose(0, 1).contiguous()
+        dkb, dvb = torch.zeros_like(kb), torch.zeros_like(vb)
+        for head in range(hkv * g):
+            kh, vh = kb[head // g], vb[head // g]
+            w = q[rows, head] @ kh.t() / math.sqrt(d)
+            if biased:
+                w = w + table[:, head][bucket]
+            p = torch.softmax(w, 1)
+            out["out"][rows, head] = p @ vh
+            if not train:
+                continue
+            do = dout[rows, head]
+            dp = do @ vh.t()
+            ds = p * dp - p * (out["out"][rows, head] * do).sum(1, keepdim=True)
+            out["dq"][rows, head] = ds @ kh / math.sqrt(d)
+            dkb[head // g] += ds.t() @ q[rows, head] / math.sqrt(d)
+            dvb[head // g] += p.t() @ do
+            if biased:
+                out["dbias"][:, head] += torch.bincount(bucket.flatten(), ds.flatten(),
+                                                        case["buckets"])
+        if train:
+            out["dk"][cols], out["dv"][cols] = dkb.transpose(0, 1), dvb.transpose(0, 1)
+    return out
+
+
+def _exact_recurrence(s):
+    """Step by step through time, all samples side by side."""
+    case = s["case"]
+    b, c = case["samples"], case["channels"]
+    off = s["offsets"].long()
+    n = off[1:] - off[:-1]
+    x, gate = s["x"].detach().double(), s["gate"].detach().double()
+    h = s["state"].detach().double().clone() if s["state"] is not None else x.new_zeros(b, c)
+    a = 1 / (1 + torch.exp(-gate))
+    na = 1 / (1 + torch.exp(gate))
+    if s["mask"] is not None:
+        a[s["mask"] == 0], na[s["mask"] == 0] = 1.0, 0.0
+    order = torch.argsort(n, descending=True)              # at step t the first alive[t] samples run
+    start, h = off[:-1][order], h[order]
+    alive = (n[None, :] > torch.arange(s["k_max"], device=n.device)[:, None]).sum(1).tolist()
+    y, before = torch.zeros_like(x), torch.zeros_like(x)
+    for t, m in enumerate(alive):
+        at = start[:m] + t
+        before[at] = h[:m]
+        h[:m] = a[at] * h[:m] + na[at] * x[at]
+        y[at] = h[:m]
+    back = torch.argsort(order)
+    out = {"y": y, "last": h[back]}
+    if not case["train"]:
+        return out
+    grad = s["dlast"].double()[order]                      # what reaches the state after step t
+    dy, total = s["dy"].double(), torch.zeros_like(x)
+    for t in range(s["k_max"] - 1, -1, -1):
+        m = alive[t]
+        at = start[:m] + t
+        through = grad[:m] + dy[at]
+        total[at] = through
+        grad[:m] = a[at] * through
+    out["dx"] = na * total
+    out["dgate"] = a * na * (before - x) * total
+    if s["state"] is not None:
+        out["dstate"] = grad[back]
+    return out
