@@ -318,8 +318,7 @@ def _plain_recurrence(s):
     out = {"y": h.to(dtype), "last": final}
     if not case["train"]:
         return out
-    add = s["dy"].float()
-    add[last] += s["dlast"][there]
+    add = s["dy"].float().index_add(0, last, s["dlast"][there])
     keep = torch.cat([a[1:], a.new_zeros(1, c)])[:n]
     keep[last] = 0
     grad = _plain_scan(keep, add, s["k_max"], True)
