@@ -1,4 +1,5 @@
-"""Fused multi-column embedding stage for AMD MI355X (gfx950).
+"""Fused multi-column embedding stage for AMD MI355X (gfx950), and the sequence
+operators that read a jagged sequence without pooling it.
 
 Thin ctypes binding over the C ABI in include/emb.h (libemb.so, built from
 csrc/).  Every step of the forward and backward runs in the library's HIP
@@ -25,6 +26,10 @@ __all__ = [
     "emb_table_evict",
     "emb_table_save", "emb_table_load", "emb_last_error", "EmbeddingColumns", "KeyedTable",
     "EmbeddingStage",
+    "emb_attention_query", "emb_attention_forward", "emb_attention_backward",
+    "emb_recurrence_query", "emb_recurrence_forward", "emb_recurrence_backward",
+    "emb_recurrence_step", "AttentionDesc", "RecurrenceDesc", "cross_attention",
+    "gated_recurrence", "gated_recurrence_step", "CrossAttention", "GatedRecurrence",
     "HASH", "IDENTITY", "BUCKET", "KEYED", "SUM", "MEAN", "F32", "BF16", "OPT_EMIT", "OPT_SGD",
     "OPT_ADAGRAD", "ROW_DROPPED", "ROW_DEFAULT", "STAT_COUNT",
 ]
@@ -68,6 +73,25 @@ class WorkspaceView(C.Structure):
     _fields_ = [("keys", C.c_void_p), ("bags", C.c_void_p), ("bag_n", C.c_void_p)]
 
 
+class AttentionDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("heads", C.c_int32), ("kv_heads", C.c_int32),
+                ("dim", C.c_int32), ("samples", C.c_int32), ("buckets", C.c_int32),
+                ("scale", C.c_float), ("reserved", C.c_int32), ("n_q", C.c_int64),
+                ("n_k", C.c_int64), ("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p),
+                ("q_stride", C.c_int64), ("q_head_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("k_head_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("v_head_stride", C.c_int64), ("q_offsets", C.c_void_p),
+                ("k_offsets", C.c_void_p), ("mask", C.c_void_p), ("q_pos", C.c_void_p),
+                ("k_pos", C.c_void_p), ("boundaries", C.c_void_p), ("bias", C.c_void_p)]
+
+
+class RecurrenceDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("samples", C.c_int32), ("channels", C.c_int32),
+                ("reserved", C.c_int32), ("n", C.c_int64), ("x", C.c_void_p),
+                ("gate", C.c_void_p), ("x_stride", C.c_int64), ("gate_stride", C.c_int64),
+                ("offsets", C.c_void_p), ("mask", C.c_void_p), ("state", C.c_void_p)]
+
+
 _lib = None
 _VP, _I32, _I64, _F = C.c_void_p, C.c_int32, C.c_int64, C.c_float
 _SIGS = {
@@ -101,6 +125,16 @@ _SIGS = {
     "emb_table_evict": [_VP, _I64, _VP, _VP, _VP, _VP],
     "emb_table_save": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP],
     "emb_table_load": [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP],
+    "emb_attention_query": [C.POINTER(AttentionDesc), C.POINTER(C.c_size_t),
+                            C.POINTER(C.c_size_t)],
+    "emb_attention_forward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, C.c_size_t, _VP],
+    "emb_attention_backward": [C.POINTER(AttentionDesc), _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP,
+                               _VP, C.c_size_t, _VP],
+    "emb_recurrence_query": [C.POINTER(RecurrenceDesc), C.POINTER(_I64), C.POINTER(C.c_size_t)],
+    "emb_recurrence_forward": [C.POINTER(RecurrenceDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
+    "emb_recurrence_backward": [C.POINTER(RecurrenceDesc), _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                C.c_size_t, _VP],
+    "emb_recurrence_step": [_I32, _I64, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _VP],
 }
 
 
@@ -313,6 +347,53 @@ def emb_table_save(table, keys, counts, seen, admitted, values, n_out, stream=No
 def emb_table_load(table, keys, counts, seen, admitted, values, n, stats=None, stream=None):
     _check(lib().emb_table_load(table, _ptr(keys), _ptr(counts), _ptr(seen), _ptr(admitted),
                                 _ptr(values), n, _ptr(stats), _stream(stream)))
+
+
+def emb_attention_query(desc):
+    fb, bb = C.c_size_t(), C.c_size_t()
+    _check(lib().emb_attention_query(C.byref(desc), C.byref(fb), C.byref(bb)))
+    return fb.value, bb.value
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def emb_attention_forward(desc, out, lse=None, workspace=None, stream=None):
+    _check(lib().emb_attention_forward(C.byref(desc), _ptr(out), _ptr(lse), _ptr(workspace),
+                                       _bytes(workspace), _stream(stream)))
+
+
+def emb_attention_backward(desc, lse, dout, dq, dk=None, dv=None, dbias=None, workspace=None,
+                           stream=None):
+    _check(lib().emb_attention_backward(C.byref(desc), _ptr(lse), _rows_ptr(dout, 3),
+                                        dout.stride(0), dout.stride(1), _ptr(dq), _ptr(dk),
+                                        _ptr(dv), _ptr(dbias), _ptr(workspace), _bytes(workspace),
+                                        _stream(stream)))
+
+
+def emb_recurrence_query(desc):
+    rows, wb = _I64(), C.c_size_t()
+    _check(lib().emb_recurrence_query(C.byref(desc), C.byref(rows), C.byref(wb)))
+    return rows.value, wb.value
+
+
+def emb_recurrence_forward(desc, y, last, saved=None, workspace=None, stream=None):
+    _check(lib().emb_recurrence_forward(C.byref(desc), _ptr(y), _ptr(last), _ptr(saved),
+                                        _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def emb_recurrence_backward(desc, saved, dy, dlast, dx, dgate, dstate=None, workspace=None,
+                            stream=None):
+    _check(lib().emb_recurrence_backward(C.byref(desc), _ptr(saved), _ptr(dy), _ptr(dlast),
+                                         _ptr(dx), _ptr(dgate), _ptr(dstate), _ptr(workspace),
+                                         _bytes(workspace), _stream(stream)))
+
+
+def emb_recurrence_step(x, gate, state, y, stream=None):
+    _check(lib().emb_recurrence_step(_SEQ_DTYPE[x.dtype], x.shape[0], x.shape[1], _rows_ptr(x, 2),
+                                     x.stride(0), _rows_ptr(gate, 2), gate.stride(0), _ptr(state),
+                                     _ptr(y), _stream(stream)))
 
 
 # ------------------------------------------------------------- convenience
@@ -575,3 +656,241 @@ class KeyedTable:
         emb_table_export(self.table, keys, counts, rows, n)
         k = int(n.item())
         return keys[:k], counts[:k], rows[:k]
+
+
+# ------------------------------------------------------ sequence operators
+
+_SEQ_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _rows_ptr(t, ndim):
+    """Address of a tensor whose last dimension is contiguous (the others may be strided)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("the sequence operators run on the GPU: pass device tensors")
+    if t.dim() != ndim:
+        raise ValueError(f"expected {ndim} dimensions, got shape {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _want(t, name, dtype, shape, device):
+    """Address of a contiguous tensor of exactly this type and shape; None for None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+        raise ValueError(f"{name}: expected {dtype} {shape} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _same(first, others):
+    if first.dtype not in _SEQ_DTYPE:
+        raise ValueError(f"the sequence operators take float32 or bfloat16, got {first.dtype}")
+    for t in others:
+        if t.dtype != first.dtype or t.device != first.device:
+            raise ValueError("tensors of one call must share their type and device")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current device")
+
+
+def _offsets_ptr(t, name, device):
+    if t.dim() != 1 or t.numel() < 1:
+        raise ValueError(f"{name}: expected [samples + 1] offsets")
+    return _want(t, name, torch.int32, (t.numel(),), device)
+
+
+def _mask_ptr(mask, n, device):
+    if mask is not None and mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    return _want(mask, "mask", torch.uint8, (n,), device)
+
+
+def _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos, scale):
+    qp, kp, vp = _rows_ptr(q, 3), _rows_ptr(k, 3), _rows_ptr(v, 3)
+    _same(q, (k, v))
+    nq, heads, dim = q.shape
+    nk, kv_heads, kdim = k.shape
+    if kdim != dim or v.shape != k.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+    dev = q.device
+    samples = q_offsets.numel() - 1
+    if k_offsets.numel() != samples + 1:
+        raise ValueError("q_offsets and k_offsets must have one length")
+    buckets = 0
+    if bias is not None:
+        if boundaries is None or q_pos is None or k_pos is None:
+            raise ValueError("a bias needs boundaries, q_pos and k_pos")
+        buckets = bias.shape[0]
+        if buckets < 1:
+            raise ValueError("a bias needs at least one bucket")
+    d = AttentionDesc(_SEQ_DTYPE[q.dtype], heads, kv_heads, dim, samples, buckets,
+                      dim ** -0.5 if scale is None else scale, 0, nq, nk, qp, kp, vp, q.stride(0),
+                      q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
+                      _offsets_ptr(q_offsets, "q_offsets", dev),
+                      _offsets_ptr(k_offsets, "k_offsets", dev), _mask_ptr(mask, nk, dev))
+    if buckets:
+        d.q_pos = _want(q_pos, "q_pos", torch.int32, (nq,), dev)
+        d.k_pos = _want(k_pos, "k_pos", torch.int32, (nk,), dev)
+        d.boundaries = _want(boundaries, "boundaries", torch.int32, (buckets - 1,), dev)
+        d.bias = _want(bias, "bias", torch.float32, (buckets, heads), dev)
+    return d
+
+
+class CrossAttention(torch.autograd.Function):
+    """cross_attention as an autograd node: gradients of q, k, v and the bias table."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, scale):
+        desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
+                               scale)
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        need, ctx.need = emb_attention_query(desc)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        emb_attention_forward(desc, out, lse, ws)
+        ctx.save_for_backward(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos,
+                              lse)
+        ctx.scale = scale
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, lse = ctx.saved_tensors
+        desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
+                               ctx.scale)
+        if dout.dtype != q.dtype:
+            raise TypeError("the output's gradient must have the output's type")
+        if dout.shape[-1] > 1 and dout.stride(-1) != 1:
+            dout = dout.contiguous()
+        _, want_k, want_v, want_bias = ctx.needs_input_grad[:4]
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dk = dv = dbias = None
+        if want_k or want_v:
+            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        if bias is not None and want_bias:
+            dbias = torch.empty(bias.shape, dtype=torch.float32, device=q.device)
+        ws = torch.empty(ctx.need, dtype=torch.uint8, device=q.device) if ctx.need else None
+        emb_attention_backward(desc, lse, dout, dq, dk, dv, dbias, ws)
+        return (dq, dk, dv, dbias) + (None,) * 7
+
+
+def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundaries=None,
+                    q_pos=None, k_pos=None, scale=None):
+    """Attention of every sample's query rows over its key rows, both jagged.
+
+    q [n_q, heads, dim], k and v [n_k, kv_heads, dim] (float32 or bfloat16; heads a
+    multiple of kv_heads, dim <= 128; any strides with the last dimension contiguous);
+    q_offsets, k_offsets: int32 [samples + 1].  mask: uint8 or bool [n_k], 0 takes a key
+    out.  bias: fp32 [buckets, heads], learned; the pair (i, j) gets row
+    #{m : boundaries[m] <= q_pos[i] - k_pos[j]} of it (boundaries int32 [buckets - 1]
+    ascending, positions int32).  scale: dim ** -0.5 unless given.  Returns
+    [n_q, heads, dim]; a row without any key gives zero.  Differentiable in q, k, v and
+    bias; runs on the current stream."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, v, bias)):
+        return CrossAttention.apply(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos,
+                                    k_pos, scale)
+    desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
+                           scale)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    need = emb_attention_query(desc)[0]
+    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    emb_attention_forward(desc, out, None, ws)
+    return out
+
+
+def _recurrence_desc(x, gate, offsets, state, mask):
+    xp, gp = _rows_ptr(x, 2), _rows_ptr(gate, 2)
+    _same(x, (gate,))
+    if gate.shape != x.shape:
+        raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
+    n, channels = x.shape
+    samples = offsets.numel() - 1
+    return RecurrenceDesc(_SEQ_DTYPE[x.dtype], samples, channels, 0, n, xp, gp, x.stride(0),
+                          gate.stride(0),
+                          _offsets_ptr(offsets, "offsets", x.device), _mask_ptr(mask, n, x.device),
+                          _want(state, "state", torch.float32, (samples, channels), x.device))
+
+
+class GatedRecurrence(torch.autograd.Function):
+    """gated_recurrence as an autograd node: gradients of x, gate and the first state."""
+
+    @staticmethod
+    def forward(ctx, x, gate, state, offsets, mask):
+        desc = _recurrence_desc(x, gate, offsets, state, mask)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        last = torch.empty(desc.samples, desc.channels, dtype=torch.float32, device=x.device)
+        rows, ctx.need = emb_recurrence_query(desc)
+        saved = torch.empty(rows, desc.channels, dtype=torch.float32, device=x.device)
+        ws = torch.empty(ctx.need, dtype=torch.uint8, device=x.device) if ctx.need else None
+        emb_recurrence_forward(desc, y, last, saved, ws)
+        ctx.save_for_backward(x, gate, state, offsets, mask, saved)
+        ctx.set_materialize_grads(False)
+        return y, last
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dlast):
+        x, gate, state, offsets, mask, saved = ctx.saved_tensors
+        desc = _recurrence_desc(x, gate, offsets, state, mask)
+        if dy is None:
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        if dy.dtype != x.dtype:
+            raise TypeError("the output's gradient must have the output's type")
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dstate = None
+        if state is not None and ctx.needs_input_grad[2]:
+            dstate = torch.empty_like(state)
+        ws = torch.empty(ctx.need, dtype=torch.uint8, device=x.device) if ctx.need else None
+        emb_recurrence_backward(desc, saved, dy.contiguous(),
+                                None if dlast is None else dlast.contiguous(), dx, dgate, dstate, ws)
+        return dx, dgate, dstate, None, None
+
+
+def gated_recurrence(x, gate, offsets, state=None, mask=None):
+    """h_t = a_t h_(t-1) + (1 - a_t) x_t with a_t = sigmoid(gate_t), over every sample's rows.
+
+    x, gate: [n, channels] (float32 or bfloat16; rows may be strided); offsets: int32
+    [samples + 1]; state: fp32 [samples, channels] before the first rows (None: zero);
+    mask: uint8 or bool [n], 0 keeps the state as it is.  Returns (y [n, channels], the
+    states at every row, last fp32 [samples, channels], those after the last rows).
+    Differentiable in x, gate and state; runs on the current stream."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, gate, state)):
+        return GatedRecurrence.apply(x, gate, state, offsets, mask)
+    desc = _recurrence_desc(x, gate, offsets, state, mask)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    last = torch.empty(desc.samples, desc.channels, dtype=torch.float32, device=x.device)
+    need = emb_recurrence_query(desc)[1]
+    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    emb_recurrence_forward(desc, y, last, None, ws)
+    return y, last
+
+
+def gated_recurrence_step(x, gate, state, out=None):
+    """One step of the recurrence for a batch of states (serving): x, gate [rows, channels],
+    state fp32 [rows, channels], updated in place; returns it in x's type.  Not
+    differentiable."""
+    _rows_ptr(x, 2), _rows_ptr(gate, 2)
+    _same(x, (gate,))
+    if gate.shape != x.shape:
+        raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
+    _want(state, "state", torch.float32, tuple(x.shape), x.device)
+    if state is None:
+        raise TypeError("state: expected a torch.Tensor")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _want(out, "out", x.dtype, tuple(x.shape), x.device)
+    if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
+        raise ValueError("gated_recurrence_step has no gradient: use gated_recurrence")
+    emb_recurrence_step(x, gate, state, out)
+    return out

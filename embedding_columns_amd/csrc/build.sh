@@ -10,5 +10,6 @@ hipcc --offload-arch=gfx950 -O3 -std=c++17 -fPIC -shared \
     -Wall -Wno-unused-function \
     -I"$root/include" -I"$here" \
     "$here/plan.cpp" "$here/forward.hip" "$here/backward.hip" "$here/table.hip" "$here/noalloc.hip" "$here/copy.hip" \
+    "$here/attention.hip" "$here/recurrence.hip" \
     -o "$tmp"
 mv -f "$tmp" "$out"

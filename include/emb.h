@@ -419,6 +419,98 @@ emb_status emb_table_load(emb_table *table, const int64_t *keys, const int32_t *
                           const int32_t *seen, const uint8_t *admitted, const float *values,
                           int64_t n, int64_t *stats, void *stream);
 
+/*
+ * Sequence operators: what reads a jagged behaviour sequence without pooling it.
+ * They share the conventions above.  Rows of all samples lie one after another, and
+ * sample b owns rows offsets[b] .. offsets[b+1] (int32, ascending, [samples + 1]);
+ * rows that no sample owns give zero.  dtype (EMB_F32 or EMB_BF16) is that of the
+ * activations; everything that accumulates is fp32.
+ *
+ * Cross attention with a learned bias by buckets of the distance in position
+ * (elapsed time, or steps).  Query head h of a sample's query row i reads key head
+ * h / (heads / kv_heads) of the sample's key rows j:
+ *   s_ij = scale q_i.k_j + bias[bucket(q_pos_i - k_pos_j), h],  o_i = sum_j softmax_j(s_ij) v_j
+ *   bucket(x) = #{m : boundaries[m] <= x}, as for EMB_COL_BUCKET; x saturates to int32.
+ * Masked keys take no part, whatever their rows hold.  A query row without any key
+ * gives o_i = 0 (and lse_i = -inf).
+ */
+typedef struct emb_attention {   /* host */
+    int32_t dtype;               /* EMB_F32 | EMB_BF16: q, k, v, out and their gradients      */
+    int32_t heads, kv_heads;     /* heads: a multiple of kv_heads                             */
+    int32_t dim;                 /* head size, 1 .. 128                                       */
+    int32_t samples;
+    int32_t buckets;             /* rows of the bias table, <= 256 and <= 4096 / (heads /     */
+                                 /* kv_heads); 0: no bias                                    */
+    float scale;                 /* > 0                                                      */
+    int32_t reserved;
+    int64_t n_q, n_k;            /* query rows, key rows                                     */
+    const void *q;               /* [n_q, heads, dim]    elements of a head contiguous; rows  */
+    const void *k;               /* [n_k, kv_heads, dim] and heads any stride apart, given in */
+    const void *v;               /* [n_k, kv_heads, dim] elements                             */
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+    const int32_t *q_offsets, *k_offsets;  /* [samples + 1]                                  */
+    const uint8_t *mask;         /* [n_k], 0 takes a key out; or NULL                         */
+    const int32_t *q_pos, *k_pos;          /* [n_q], [n_k]: with a bias                        */
+    const int32_t *boundaries;   /* [buckets - 1], ascending                                  */
+    const float *bias;           /* [buckets, heads]                                          */
+} emb_attention;
+
+/* Workspace bytes of the forward and the backward call (host only). */
+emb_status emb_attention_query(const emb_attention *a, size_t *forward_bytes /* host */,
+                               size_t *backward_bytes /* host */);
+
+/* out: [n_q, heads, dim] contiguous, aligned to four elements.  lse: [n_q, heads], the
+ * natural logarithm of each row's sum of exponentials, which the backward needs, or
+ * NULL.  workspace: 256-byte aligned, or NULL when the query says 0 bytes. */
+emb_status emb_attention_forward(const emb_attention *a, void *out, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/* dq: [n_q, heads, dim]; dk, dv: [n_k, kv_heads, dim] (both, or both NULL); dbias: fp32
+ * [buckets, heads] or NULL.  All contiguous, overwritten, and the same bits for the same
+ * inputs.  dout: as q, with its own strides. */
+emb_status emb_attention_backward(const emb_attention *a, const float *lse, const void *dout,
+                                  int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
+                                  void *dv, float *dbias, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
+ * Gated linear recurrence over each sample's rows, every channel by itself:
+ *   a_t = sigmoid(gate_t),  h_t = a_t h_(t-1) + (1 - a_t) x_t,  y_t = h_t
+ * from the sample's state (or zero).  A masked row keeps the state (a_t = 1), whatever
+ * x and gate hold there.
+ */
+typedef struct emb_recurrence {  /* host */
+    int32_t dtype;               /* EMB_F32 | EMB_BF16: x, gate, y and their gradients        */
+    int32_t samples, channels;
+    int32_t reserved;
+    int64_t n;                   /* rows                                                     */
+    const void *x, *gate;        /* [n, channels], rows x_stride / gate_stride elements apart */
+    int64_t x_stride, gate_stride;
+    const int32_t *offsets;      /* [samples + 1]                                            */
+    const uint8_t *mask;         /* [n] or NULL                                              */
+    const float *state;          /* [samples, channels] or NULL (zero)                        */
+} emb_recurrence;
+
+/* saved_rows: rows of `saved`; workspace_bytes: of the forward and of the backward. */
+emb_status emb_recurrence_query(const emb_recurrence *r, int64_t *saved_rows /* host */,
+                                size_t *workspace_bytes /* host */);
+
+/* y: [n, channels]; last: fp32 [samples, channels], the states after the last rows;
+ * saved: fp32 [saved_rows, channels] for the backward, or NULL. */
+emb_status emb_recurrence_forward(const emb_recurrence *r, void *y, float *last, float *saved,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* dy, dx, dgate: [n, channels] contiguous; dlast, dstate: fp32 [samples, channels] or NULL. */
+emb_status emb_recurrence_backward(const emb_recurrence *r, const float *saved, const void *dy,
+                                   const float *dlast, void *dx, void *dgate, float *dstate,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* One step of `rows` states at once (serving): state fp32 [rows, channels] is updated in
+ * place, y [rows, channels] gets it in dtype. */
+emb_status emb_recurrence_step(int32_t dtype, int64_t rows, int32_t channels, const void *x,
+                               int64_t x_stride, const void *gate, int64_t gate_stride, float *state,
+                               void *y, void *stream);
+
 /* Message for the last non-OK status on this host thread. */
 const char *emb_last_error(void);
 
