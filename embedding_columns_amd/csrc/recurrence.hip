@@ -7,7 +7,9 @@
 
 namespace emb {
 
-constexpr int kScanSteps = 16;   // consecutive steps a wavefront holds in registers
+constexpr int kScanSteps = 16;   // consecutive steps a wavefront of the forward holds in registers
+constexpr int kBackSteps = 8;    // ... of the backward, which holds twice as much per step
+constexpr int kSaved = 8;        // the forward saves the state before every kSaved steps
 
 struct ScanArgs {
     const void *x, *gate;        // [n, channels], rows xs / gs elements apart
@@ -17,13 +19,12 @@ struct ScanArgs {
     const float *state;          // [samples, channels] or NULL
     void *y;                     // [n, channels]
     float *last;                 // [samples, channels]
-    float *ckpt;                 // state before each group of kScanSteps steps, or NULL
+    float *ckpt;                 // state before each group of kSaved steps, or NULL
     const void *dy;              // backward
     const float *dlast;
     void *dx, *dgate;
     float *dstate;
     float *sum_a, *sum_h;        // [tiles, channels]: what a chunk does to the state it is given
-    float *carry;                // [tiles, channels]: the state a chunk is given
     int64_t n, tiles;
     int32_t samples, channels;
     int32_t chunk;               // rows per chunk; 0: a whole sample at once
@@ -37,54 +38,62 @@ __device__ __forceinline__ void sigmoid_pair(float g, float &a, float &na)
     const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
     a = g >= 0.f ? big : small;
     na = g >= 0.f ? small : big;
-    if (g != g) a = na = g;
 }
 
+// VEC neighbouring channels of one row as they lie in memory, and as floats
 template <typename T, int VEC>
 struct Chan;
 template <>
 struct Chan<float, 1> {
-    static __device__ __forceinline__ void load(const float *p, float *v) { v[0] = *gp(p); }
-    static __device__ __forceinline__ void store(float *p, const float *v) { *gp(p) = v[0]; }
+    typedef float Raw;
+    static __device__ __forceinline__ void open(Raw r, float *v) { v[0] = r; }
+    static __device__ __forceinline__ Raw pack(const float *v) { return v[0]; }
 };
 template <>
 struct Chan<float, 2> {
-    static __device__ __forceinline__ void load(const float *p, float *v)
+    typedef float2 Raw;
+    static __device__ __forceinline__ void open(Raw r, float *v)
     {
-        const float2 w = *gp(reinterpret_cast<const float2 *>(p));
-        v[0] = w.x;
-        v[1] = w.y;
+        v[0] = r.x;
+        v[1] = r.y;
     }
-    static __device__ __forceinline__ void store(float *p, const float *v)
-    {
-        *gp(reinterpret_cast<float2 *>(p)) = make_float2(v[0], v[1]);
-    }
+    static __device__ __forceinline__ Raw pack(const float *v) { return make_float2(v[0], v[1]); }
 };
 template <>
 struct Chan<uint16_t, 1> {
-    static __device__ __forceinline__ void load(const uint16_t *p, float *v) { v[0] = bf16_lo(*gp(p)); }
-    static __device__ __forceinline__ void store(uint16_t *p, const float *v) { *gp(p) = bf16_rne(v[0]); }
+    typedef uint16_t Raw;
+    static __device__ __forceinline__ void open(Raw r, float *v) { v[0] = bf16_lo(r); }
+    static __device__ __forceinline__ Raw pack(const float *v) { return bf16_rne(v[0]); }
 };
 template <>
 struct Chan<uint16_t, 2> {
-    static __device__ __forceinline__ void load(const uint16_t *p, float *v)
+    typedef uint32_t Raw;
+    static __device__ __forceinline__ void open(Raw r, float *v)
     {
-        const uint32_t w = *gp(reinterpret_cast<const uint32_t *>(p));
-        v[0] = bf16_lo(w);
-        v[1] = bf16_hi(w);
+        v[0] = bf16_lo(r);
+        v[1] = bf16_hi(r);
     }
-    static __device__ __forceinline__ void store(uint16_t *p, const float *v)
-    {
-        *gp(reinterpret_cast<uint32_t *>(p)) = bf16x2_rne(v[0], v[1]);
-    }
+    static __device__ __forceinline__ Raw pack(const float *v) { return bf16x2_rne(v[0], v[1]); }
 };
+
+// row (uniform) and channel c (per lane) of a tensor
+template <typename R, typename T>
+__device__ __forceinline__ R row_load(const T *p, int64_t row, int64_t stride, uint32_t c)
+{
+    return *gp(reinterpret_cast<const R *>(p + row * stride + c));
+}
+template <typename R, typename T>
+__device__ __forceinline__ void row_store(T *p, int64_t row, int64_t stride, uint32_t c, R v)
+{
+    *gp(reinterpret_cast<R *>(p + row * stride + c)) = v;
+}
 
 // Which rows a workgroup walks: one sample, or one chunk of one.
 struct ScanSpan {
     int64_t begin, end;      // rows
     int64_t first;           // first row of the sample
-    int64_t seg_end;
-    int64_t tile;
+    int64_t tile, tile0;     // chunk number, that of the sample's first chunk
+    int64_t chunks;          // of the sample
     int seg;
 };
 
@@ -93,89 +102,156 @@ __device__ __forceinline__ bool scan_span(const ScanArgs &A, int64_t block, Scan
     s.tile = block;
     if (A.chunk == 0) {
         s.seg = (int)block;
+        s.tile0 = block;
+        s.chunks = 1;
         s.first = s.begin = seg_edge(A.off, A.samples, A.n, s.seg);
-        s.end = s.seg_end = seg_edge(A.off, A.samples, A.n, s.seg + 1);
+        s.end = seg_edge(A.off, A.samples, A.n, s.seg + 1);
         return true;
     }
     const SegTile t = seg_find(A.off, A.samples, A.n, 1, A.chunk, block);
     s.seg = t.seg;
     s.first = t.base;
-    s.seg_end = t.base + t.rows;
+    s.tile0 = t.base / A.chunk + t.seg;
+    s.chunks = (t.rows + A.chunk - 1) / A.chunk;
     s.begin = t.base + t.row0;
-    s.end = t.row0 + A.chunk < t.rows ? s.begin + A.chunk : s.seg_end;
-    return t.row0 < t.rows;
+    s.end = t.row0 + A.chunk < t.rows ? s.begin + A.chunk : t.base + t.rows;
+    // an empty sample keeps its first chunk: it hands the state through
+    return t.row0 < t.rows || (t.rows == 0 && t.row0 == 0);
+}
+
+// The saved state of the group of kSaved rows that begins at `row`
+__device__ __forceinline__ int64_t saved_row(const ScanSpan &s, int64_t row)
+{
+    return s.first / kSaved + s.seg + (row - s.first) / kSaved;
 }
 
 enum { kScanWhole = 0, kScanSum = 1, kScanApply = 2 };
+
+// What the pairs (A, H) of the sample's chunks before this one (after it, in the
+// backward) make of the state v: each wavefront folds its share of the pairs, and the
+// W results meet in LDS.
+template <int VEC, int W, bool REVERSE>
+__device__ __forceinline__ void chunk_state(const ScanArgs &A, const ScanSpan &s, int w, uint32_t c,
+                                            float (&pa)[W][64 * VEC], float (&ph)[W][64 * VEC], float *v)
+{
+    const int64_t here = s.tile - s.tile0, n = REVERSE ? s.chunks - 1 - here : here, C = A.channels;
+    const int64_t i0 = n * w / W, i1 = n * (w + 1) / W;
+    const int lane = lane_id();
+    float a[VEC], h[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; e++) {
+        a[e] = 1.f;
+        h[e] = 0.f;
+    }
+    constexpr int kAhead = 8;    // pairs loaded before the first is needed
+    for (int64_t i = i0; i < i1; i += kAhead) {
+        float ra[kAhead][VEC], rh[kAhead][VEC];
+#pragma unroll
+        for (int j = 0; j < kAhead; j++) {
+            const int64_t k = i + j < i1 ? i + j : i1 - 1;
+            const int64_t t = s.tile0 + (REVERSE ? s.chunks - 1 - k : k);
+#pragma unroll
+            for (int e = 0; e < VEC; e++) {
+                ra[j][e] = row_load<float>(A.sum_a, t, C, c + e);
+                rh[j][e] = row_load<float>(A.sum_h, t, C, c + e);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; j++)
+            if (i + j < i1)
+#pragma unroll
+                for (int e = 0; e < VEC; e++) {
+                    h[e] = fmaf(ra[j][e], h[e], rh[j][e]);
+                    a[e] *= ra[j][e];
+                }
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; e++) {
+        pa[w][lane * VEC + e] = a[e];
+        ph[w][lane * VEC + e] = h[e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < W; u++)
+#pragma unroll
+        for (int e = 0; e < VEC; e++) v[e] = fmaf(pa[u][lane * VEC + e], v[e], ph[u][lane * VEC + e]);
+    __syncthreads();
+}
 
 // W wavefronts walk a sample (or chunk) in blocks of W * kScanSteps rows: each
 // loads its own kScanSteps rows of 64 * VEC channels, scans them from a zero state
 // into (A, H) with h_out = A h_in + H, the W pairs meet in LDS, and each wavefront
 // applies its rows from the state that the pairs before it give.  One pass over the
-// data; the state stays in fp32 registers.
+// data; the state stays in fp32 registers.  Rows past the end and masked ones load
+// some other row of the sample and count as a = 1, x = 0; the next block's rows are
+// loaded before this block's arithmetic.
 template <typename T, int VEC, int W, int PHASE>
-__global__ __launch_bounds__(64 * W) void scan_forward(ScanArgs A)
+__global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_forward(ScanArgs A)
 {
+    typedef Chan<T, VEC> CH;
+    typedef typename CH::Raw Raw;
     __shared__ float pa[2][W][64 * VEC], ph[2][W][64 * VEC];
     const int lane = lane_id(), w = uniform((int)(threadIdx.x >> 6));
-    const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * VEC;
-    const bool live = c < A.channels;
+    const uint32_t cw = (blockIdx.y * 64 + lane) * VEC;
+    const bool live = cw < (uint32_t)A.channels;
+    const uint32_t c = live ? cw : 0;      // lanes past the last channel repeat the first
     const int64_t C = A.channels;
     ScanSpan s;
     if (!scan_span(A, blockIdx.x, s)) return;
     const T *x = static_cast<const T *>(A.x), *gate = static_cast<const T *>(A.gate);
     T *y = static_cast<T *>(A.y);
-    const bool nobody = s.seg == 0 || s.seg == A.samples + 1;
-    if (nobody) {
+    if (s.seg == 0 || s.seg == A.samples + 1) {
+        const float z[VEC] = {};
         if (PHASE != kScanSum && live)
-            for (int64_t t = s.begin + w; t < s.end; t += W) {
-                float z[VEC] = {};
-                Chan<T, VEC>::store(y + t * C + c, z);
-            }
+            for (int64_t t = s.begin + w; t < s.end; t += W) row_store(y, t, C, c, CH::pack(z));
         return;
     }
     float h[VEC], ta[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
-        h[v] = 0.f;
+        h[v] = PHASE != kScanSum && A.state ? A.state[(int64_t)(s.seg - 1) * C + c + v] : 0.f;
         ta[v] = 1.f;
-        if (PHASE == kScanWhole && A.state && live) h[v] = A.state[(int64_t)(s.seg - 1) * C + c + v];
-        if (PHASE == kScanApply && live) h[v] = A.carry[s.tile * C + c + v];
     }
+    if (PHASE == kScanApply) chunk_state<VEC, W, false>(A, s, w, c, pa[0], ph[0], h);
+
+    Raw xn[kScanSteps], gn[kScanSteps];
+    uint32_t keep = 0;
+    auto load = [&](int64_t t0) {
+        const int64_t mine = t0 + w * kScanSteps;
+        keep = lane < kScanSteps && mine + lane < s.end ? (A.mask ? *gp(A.mask + mine + lane) : 1) : 0;
+#pragma unroll
+        for (int i = 0; i < kScanSteps; i++) {
+            const int64_t row = mine + i < s.end ? mine + i : s.end - 1;
+            xn[i] = row_load<Raw>(x, row, A.xs, c);
+            gn[i] = row_load<Raw>(gate, row, A.gs, c);
+        }
+    };
+    if (s.begin < s.end) load(s.begin);
     int buf = 0;
     for (int64_t t0 = s.begin; t0 < s.end; t0 += W * kScanSteps, buf ^= 1) {
         const int64_t mine = t0 + w * kScanSteps;
-        float xs[kScanSteps][VEC], gs[kScanSteps][VEC];
-        uint32_t kept = 0;
-        if (lane < kScanSteps && mine + lane < s.end) kept = A.mask ? *gp(A.mask + mine + lane) != 0 : 1;
-        const uint32_t bits = (uint32_t)__ballot(kept);
-#pragma unroll
-        for (int i = 0; i < kScanSteps; i++) {
-#pragma unroll
-            for (int v = 0; v < VEC; v++) xs[i][v] = gs[i][v] = 0.f;
-            if (live && (bits >> i & 1)) {
-                Chan<T, VEC>::load(x + (mine + i) * A.xs + c, xs[i]);
-                Chan<T, VEC>::load(gate + (mine + i) * A.gs + c, gs[i]);
-            }
-        }
-        float la[VEC], lh[VEC];
+        const uint32_t bits = (uint32_t)__ballot(keep != 0);
+        float xs[kScanSteps][VEC], as[kScanSteps][VEC], la[VEC], lh[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
             la[v] = 1.f;
             lh[v] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kScanSteps; i++)
+        for (int i = 0; i < kScanSteps; i++) {
+            const bool on = bits >> i & 1;
+            CH::open(xn[i], xs[i]);
+            CH::open(gn[i], as[i]);
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
-                float a, na;
-                sigmoid_pair(gs[i][v], a, na);
-                const bool on = bits >> i & 1;
-                gs[i][v] = on ? a : 1.f;
-                xs[i][v] = on ? na * xs[i][v] : 0.f;
-                lh[v] = fmaf(gs[i][v], lh[v], xs[i][v]);
-                la[v] *= gs[i][v];
+                float na;
+                sigmoid_pair(on ? as[i][v] : INFINITY, as[i][v], na);
+                xs[i][v] = na * (on ? xs[i][v] : 0.f);
+                lh[v] = fmaf(as[i][v], lh[v], xs[i][v]);
+                la[v] *= as[i][v];
             }
+        }
+        if (t0 + W * kScanSteps < s.end) load(t0 + W * kScanSteps);
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
             pa[buf][w][lane * VEC + v] = la[v];
@@ -195,26 +271,24 @@ __global__ __launch_bounds__(64 * W) void scan_forward(ScanArgs A)
                 if (PHASE == kScanSum) ta[v] *= ua;
             }
         if (PHASE == kScanSum) continue;
-        if (A.ckpt && live && mine < s.end) {
-            // groups of kScanSteps rows counted from the sample's first row
-            const int64_t g = s.first / kScanSteps + s.seg + (mine - s.first) / kScanSteps;
-#pragma unroll
-            for (int v = 0; v < VEC; v++) A.ckpt[g * C + c + v] = in[v];
-        }
 #pragma unroll
         for (int i = 0; i < kScanSteps; i++) {
+            if (A.ckpt && i % kSaved == 0 && live && mine + i < s.end)
 #pragma unroll
-            for (int v = 0; v < VEC; v++) in[v] = fmaf(gs[i][v], in[v], xs[i][v]);
-            if (live && mine + i < s.end) Chan<T, VEC>::store(y + (mine + i) * C + c, in);
+                for (int v = 0; v < VEC; v++) row_store(A.ckpt, saved_row(s, mine + i), C, c + v, in[v]);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) in[v] = fmaf(as[i][v], in[v], xs[i][v]);
+            if (live && mine + i < s.end) row_store(y, mine + i, C, c, CH::pack(in));
         }
     }
     if (!live || w != 0) return;
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
-        if (PHASE == kScanWhole) A.last[(int64_t)(s.seg - 1) * C + c + v] = h[v];
+        if (PHASE == kScanWhole || (PHASE == kScanApply && s.tile - s.tile0 >= s.chunks - 1))
+            A.last[(int64_t)(s.seg - 1) * C + c + v] = h[v];
         if (PHASE == kScanSum) {
-            A.sum_a[s.tile * C + c + v] = ta[v];
-            A.sum_h[s.tile * C + c + v] = h[v];
+            row_store(A.sum_a, s.tile, C, c + v, ta[v]);
+            row_store(A.sum_h, s.tile, C, c + v, h[v]);
         }
     }
 }
@@ -222,87 +296,90 @@ __global__ __launch_bounds__(64 * W) void scan_forward(ScanArgs A)
 // The backward pass walks the same blocks from the last to the first.  With
 // u_t = a_t g_t the carried quantity, g_t = dy_t + u_(t+1) is the gradient of h_t,
 // again a linear recurrence.  The states h_(t-1) that dgate needs are scanned again
-// from the saved state before each group of kScanSteps rows: 1/16 of the states in
-// fp32 is less to write and read than all of them in bf16, and exact.
+// from the saved state before each group of kSaved rows: an eighth of the states in
+// fp32 is a quarter of what all of them in bf16 would cost, and exact.
 template <typename T, int VEC, int W, int PHASE>
-__global__ __launch_bounds__(64 * W) void scan_backward(ScanArgs A)
+__global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_backward(ScanArgs A)
 {
+    typedef Chan<T, VEC> CH;
+    typedef typename CH::Raw Raw;
     __shared__ float pa[2][W][64 * VEC], ph[2][W][64 * VEC];
     const int lane = lane_id(), w = uniform((int)(threadIdx.x >> 6));
-    const int64_t c = ((int64_t)blockIdx.y * 64 + lane) * VEC;
-    const bool live = c < A.channels;
+    const uint32_t cw = (blockIdx.y * 64 + lane) * VEC;
+    const bool live = cw < (uint32_t)A.channels;
+    const uint32_t c = live ? cw : 0;
     const int64_t C = A.channels;
     ScanSpan s;
     if (!scan_span(A, blockIdx.x, s)) return;
     const T *x = static_cast<const T *>(A.x), *gate = static_cast<const T *>(A.gate);
     const T *dy = static_cast<const T *>(A.dy);
     T *dx = static_cast<T *>(A.dx), *dgate = static_cast<T *>(A.dgate);
-    const bool nobody = s.seg == 0 || s.seg == A.samples + 1;
-    if (nobody) {
+    if (s.seg == 0 || s.seg == A.samples + 1) {
+        const float z[VEC] = {};
         if (PHASE != kScanSum && live)
             for (int64_t t = s.begin + w; t < s.end; t += W) {
-                float z[VEC] = {};
-                Chan<T, VEC>::store(dx + t * C + c, z);
-                Chan<T, VEC>::store(dgate + t * C + c, z);
+                row_store(dx, t, C, c, CH::pack(z));
+                row_store(dgate, t, C, c, CH::pack(z));
             }
         return;
     }
     float u[VEC], ta[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
-        u[v] = 0.f;
+        u[v] = PHASE != kScanSum && A.dlast ? A.dlast[(int64_t)(s.seg - 1) * C + c + v] : 0.f;
         ta[v] = 1.f;
-        if (PHASE == kScanWhole && A.dlast && live) u[v] = A.dlast[(int64_t)(s.seg - 1) * C + c + v];
-        if (PHASE == kScanApply && live) u[v] = A.carry[s.tile * C + c + v];
     }
-    constexpr int kBlockRows = W * kScanSteps;
-    const int64_t blocks = s.end > s.begin ? (s.end - s.begin + kBlockRows - 1) / kBlockRows : 0;
+    if (PHASE == kScanApply) chunk_state<VEC, W, true>(A, s, w, c, pa[0], ph[0], u);
+
+    constexpr int kRows = W * kBackSteps;
+    const int64_t blocks = s.end > s.begin ? (s.end - s.begin + kRows - 1) / kRows : 0;
+    Raw xn[kBackSteps], gn[kBackSteps], dn[kBackSteps];
+    float hn[VEC];
+    uint32_t keep = 0;
+    auto load = [&](int64_t b) {
+        const int64_t mine = s.begin + b * kRows + w * kBackSteps;
+        keep = lane < kBackSteps && mine + lane < s.end ? (A.mask ? *gp(A.mask + mine + lane) : 1) : 0;
+#pragma unroll
+        for (int i = 0; i < kBackSteps; i++) {
+            const int64_t row = mine + i < s.end ? mine + i : s.end - 1;
+            if (PHASE != kScanSum) xn[i] = row_load<Raw>(x, row, A.xs, c);
+            gn[i] = row_load<Raw>(gate, row, A.gs, c);
+            dn[i] = row_load<Raw>(dy, row, C, c);
+        }
+#pragma unroll
+        for (int v = 0; v < VEC; v++)
+            if (PHASE != kScanSum)
+                hn[v] = row_load<float>(A.ckpt, saved_row(s, mine < s.end ? mine : s.begin), C, c + v);
+    };
+    if (blocks) load(blocks - 1);
     int buf = 0;
     for (int64_t b = blocks - 1; b >= 0; b--, buf ^= 1) {
-        const int64_t mine = s.begin + b * kBlockRows + w * kScanSteps;
-        float xs[kScanSteps][VEC], as[kScanSteps][VEC], ds[kScanSteps][VEC];
-        uint32_t kept = 0;
-        const bool inside = lane < kScanSteps && mine + lane < s.end;
-        if (inside) kept = A.mask ? *gp(A.mask + mine + lane) != 0 : 1;
-        const uint32_t bits = (uint32_t)__ballot(kept), rows = (uint32_t)__ballot(inside);
-        float hin[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; v++) hin[v] = 0.f;
-        if (PHASE != kScanSum && live && mine < s.end) {
-            const int64_t g = s.first / kScanSteps + s.seg + (mine - s.first) / kScanSteps;
-#pragma unroll
-            for (int v = 0; v < VEC; v++) hin[v] = A.ckpt[g * C + c + v];
-        }
-#pragma unroll
-        for (int i = 0; i < kScanSteps; i++) {
-#pragma unroll
-            for (int v = 0; v < VEC; v++) xs[i][v] = as[i][v] = ds[i][v] = 0.f;
-            if (live && (bits >> i & 1)) {
-                if (PHASE != kScanSum) Chan<T, VEC>::load(x + (mine + i) * A.xs + c, xs[i]);
-                Chan<T, VEC>::load(gate + (mine + i) * A.gs + c, as[i]);
-            }
-            if (live && (rows >> i & 1)) Chan<T, VEC>::load(dy + (mine + i) * C + c, ds[i]);
-        }
-        float la[VEC], lu[VEC], na[kScanSteps][VEC];
+        const int64_t mine = s.begin + b * kRows + w * kBackSteps;
+        const uint32_t bits = (uint32_t)__ballot(keep != 0);
+        float xs[kBackSteps][VEC], as[kBackSteps][VEC], na[kBackSteps][VEC], ds[kBackSteps][VEC], hin[VEC];
+        float la[VEC], lu[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
             la[v] = 1.f;
             lu[v] = 0.f;
+            hin[v] = PHASE != kScanSum ? hn[v] : 0.f;
         }
 #pragma unroll
-        for (int i = kScanSteps - 1; i >= 0; i--)
+        for (int i = kBackSteps - 1; i >= 0; i--) {
+            const bool on = bits >> i & 1, in = mine + i < s.end;
+            CH::open(gn[i], as[i]);
+            CH::open(dn[i], ds[i]);
+            if (PHASE != kScanSum) CH::open(xn[i], xs[i]);
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
-                float a;
-                sigmoid_pair(as[i][v], a, na[i][v]);
-                if (!(bits >> i & 1)) {
-                    a = 1.f;
-                    na[i][v] = 0.f;
-                }
-                as[i][v] = a;
-                lu[v] = a * (ds[i][v] + lu[v]);
-                la[v] *= a;
+                sigmoid_pair(on ? as[i][v] : INFINITY, as[i][v], na[i][v]);
+                ds[i][v] = in ? ds[i][v] : 0.f;
+                if (PHASE != kScanSum) xs[i][v] = on ? xs[i][v] : 0.f;
+                lu[v] = as[i][v] * (ds[i][v] + lu[v]);
+                la[v] *= as[i][v];
             }
+        }
+        if (b > 0) load(b - 1);
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
             pa[buf][w][lane * VEC + v] = la[v];
@@ -324,7 +401,7 @@ __global__ __launch_bounds__(64 * W) void scan_backward(ScanArgs A)
         if (PHASE == kScanSum) continue;
         // forward again: xs becomes h_(t-1) - x_t, what dgate multiplies
 #pragma unroll
-        for (int i = 0; i < kScanSteps; i++)
+        for (int i = 0; i < kBackSteps; i++)
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 const float before = hin[v];
@@ -332,67 +409,31 @@ __global__ __launch_bounds__(64 * W) void scan_backward(ScanArgs A)
                 xs[i][v] = before - xs[i][v];
             }
 #pragma unroll
-        for (int i = kScanSteps - 1; i >= 0; i--) {
-            float g[VEC], gx[VEC], gg[VEC];
+        for (int i = kBackSteps - 1; i >= 0; i--) {
+            float gx[VEC], gg[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
-                g[v] = ds[i][v] + in[v];
-                in[v] = as[i][v] * g[v];
-                gx[v] = na[i][v] * g[v];
-                gg[v] = as[i][v] * na[i][v] * xs[i][v] * g[v];
-                if (!(bits >> i & 1)) gx[v] = gg[v] = 0.f;
+                const float g = ds[i][v] + in[v];
+                in[v] = as[i][v] * g;
+                gx[v] = na[i][v] * g;                        // a masked row has na = 0
+                gg[v] = as[i][v] * xs[i][v] * gx[v];
             }
-            if (live && (rows >> i & 1)) {
-                Chan<T, VEC>::store(dx + (mine + i) * C + c, gx);
-                Chan<T, VEC>::store(dgate + (mine + i) * C + c, gg);
+            if (live && mine + i < s.end) {
+                row_store(dx, mine + i, C, c, CH::pack(gx));
+                row_store(dgate, mine + i, C, c, CH::pack(gg));
             }
         }
     }
     if (!live || w != 0) return;
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
-        if (PHASE == kScanWhole && A.dstate) A.dstate[(int64_t)(s.seg - 1) * C + c + v] = u[v];
+        if (A.dstate && (PHASE == kScanWhole || (PHASE == kScanApply && s.tile == s.tile0)))
+            A.dstate[(int64_t)(s.seg - 1) * C + c + v] = u[v];
         if (PHASE == kScanSum) {
-            A.sum_a[s.tile * C + c + v] = ta[v];
-            A.sum_h[s.tile * C + c + v] = u[v];
+            row_store(A.sum_a, s.tile, C, c + v, ta[v]);
+            row_store(A.sum_h, s.tile, C, c + v, u[v]);
         }
     }
-}
-
-// Between the two passes of a split scan: one lane per (sample, channel) takes the
-// state through the chunks' pairs and leaves each chunk the state it starts from.
-template <bool REVERSE>
-__global__ __launch_bounds__(64) void scan_carry(ScanArgs A)
-{
-    const int64_t c = (int64_t)blockIdx.y * 64 + lane_id(), C = A.channels;
-    if (c >= C) return;
-    const int64_t b = blockIdx.x, seg = b + 1;
-    const int64_t first = seg_edge(A.off, A.samples, A.n, seg);
-    const int64_t end = seg_edge(A.off, A.samples, A.n, seg + 1);
-    const int64_t k = end > first ? (end - first + A.chunk - 1) / A.chunk : 0;
-    const int64_t t0 = first / A.chunk + seg;
-    const float *start = REVERSE ? A.dlast : A.state;
-    float h = start ? start[b * C + c] : 0.f;
-    constexpr int kAhead = 8;    // pairs loaded before the first is needed
-    for (int64_t i = 0; i < k; i += kAhead) {
-        float a[kAhead], s[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; j++)
-            if (i + j < k) {
-                const int64_t t = t0 + (REVERSE ? k - 1 - i - j : i + j);
-                a[j] = *gp(A.sum_a + t * C + c);
-                s[j] = *gp(A.sum_h + t * C + c);
-            }
-#pragma unroll
-        for (int j = 0; j < kAhead; j++)
-            if (i + j < k) {
-                const int64_t t = t0 + (REVERSE ? k - 1 - i - j : i + j);
-                A.carry[t * C + c] = h;
-                h = fmaf(a[j], h, s[j]);
-            }
-    }
-    float *out = REVERSE ? A.dstate : A.last;
-    if (out) out[b * C + c] = h;
 }
 
 template <typename T, int VEC>
@@ -403,18 +444,20 @@ __global__ __launch_bounds__(256) void scan_step(const T *x, const T *gate, int6
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= rows * per) return;
     const int64_t b = i / per, c = (i - b * per) * VEC;
+    typedef Chan<T, VEC> CH;
+    typedef Chan<float, VEC> CF;
     float xv[VEC], gv[VEC], h[VEC];
-    Chan<T, VEC>::load(x + b * xs + c, xv);
-    Chan<T, VEC>::load(gate + b * gs + c, gv);
-    Chan<float, VEC>::load(state + b * C + c, h);
+    CH::open(*gp(reinterpret_cast<const typename CH::Raw *>(x + b * xs + c)), xv);
+    CH::open(*gp(reinterpret_cast<const typename CH::Raw *>(gate + b * gs + c)), gv);
+    CF::open(*gp(reinterpret_cast<const typename CF::Raw *>(state + b * C + c)), h);
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
         float a, na;
         sigmoid_pair(gv[v], a, na);
         h[v] = fmaf(a, h[v], na * xv[v]);
     }
-    Chan<float, VEC>::store(state + b * C + c, h);
-    Chan<T, VEC>::store(y + b * C + c, h);
+    *gp(reinterpret_cast<typename CF::Raw *>(state + b * C + c)) = CF::pack(h);
+    *gp(reinterpret_cast<typename CH::Raw *>(y + b * C + c)) = CH::pack(h);
 }
 
 }  // namespace emb
@@ -444,7 +487,7 @@ ScanPlan scan_plan(const emb_recurrence *r)
         p.chunk = 512;
         p.tiles = seg_tiles(r->n, r->samples, 1, p.chunk);
     }
-    p.ckpt_rows = seg_tiles(r->n, r->samples, 1, kScanSteps);
+    p.ckpt_rows = seg_tiles(r->n, r->samples, 1, kSaved);
     return p;
 }
 
@@ -477,7 +520,7 @@ size_t pad256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t scan_workspace(const emb_recurrence *r, const ScanPlan &p)
 {
-    return p.chunk ? 3 * pad256((size_t)p.tiles * r->channels * 4) : 0;
+    return p.chunk ? 2 * pad256((size_t)p.tiles * r->channels * 4) : 0;
 }
 
 // channels in pairs: an even count, and every row aligned to a pair
@@ -496,17 +539,14 @@ emb_status scan_launch_w(const ScanArgs &A, bool backward, hipStream_t st)
 {
     const int64_t blocks = (A.channels + 64 * VEC - 1) / (64 * VEC);
     const dim3 grid((unsigned)A.tiles, (unsigned)blocks), block(64 * W);
-    const dim3 cgrid((unsigned)A.samples, (unsigned)((A.channels + 63) / 64));
     if (A.chunk == 0) {
         if (backward) hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanWhole>), grid, block, 0, st, A);
         else hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanWhole>), grid, block, 0, st, A);
     } else if (backward) {
         hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanSum>), grid, block, 0, st, A);
-        hipLaunchKernelGGL((scan_carry<true>), cgrid, dim3(64), 0, st, A);
         hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanApply>), grid, block, 0, st, A);
     } else {
         hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanSum>), grid, block, 0, st, A);
-        hipLaunchKernelGGL((scan_carry<false>), cgrid, dim3(64), 0, st, A);
         hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanApply>), grid, block, 0, st, A);
     }
     const hipError_t e = hipGetLastError();
@@ -549,7 +589,6 @@ ScanArgs scan_args(const emb_recurrence *r, const ScanPlan &p, void *ws)
         const size_t part = pad256((size_t)p.tiles * r->channels * 4);
         A.sum_a = reinterpret_cast<float *>(ws);
         A.sum_h = reinterpret_cast<float *>(static_cast<char *>(ws) + part);
-        A.carry = reinterpret_cast<float *>(static_cast<char *>(ws) + 2 * part);
     }
     return A;
 }
