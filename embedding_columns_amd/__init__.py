@@ -128,7 +128,7 @@ _SIGS = {
     "emb_attention_query": [C.POINTER(AttentionDesc), C.POINTER(C.c_size_t),
                             C.POINTER(C.c_size_t)],
     "emb_attention_forward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, C.c_size_t, _VP],
-    "emb_attention_backward": [C.POINTER(AttentionDesc), _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP,
+    "emb_attention_backward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP,
                                _VP, C.c_size_t, _VP],
     "emb_recurrence_query": [C.POINTER(RecurrenceDesc), C.POINTER(_I64), C.POINTER(C.c_size_t)],
     "emb_recurrence_forward": [C.POINTER(RecurrenceDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
@@ -364,9 +364,9 @@ def emb_attention_forward(desc, out, lse=None, workspace=None, stream=None):
                                        _bytes(workspace), _stream(stream)))
 
 
-def emb_attention_backward(desc, lse, dout, dq, dk=None, dv=None, dbias=None, workspace=None,
+def emb_attention_backward(desc, out, lse, dout, dq, dk=None, dv=None, dbias=None, workspace=None,
                            stream=None):
-    _check(lib().emb_attention_backward(C.byref(desc), _ptr(lse), _rows_ptr(dout, 3),
+    _check(lib().emb_attention_backward(C.byref(desc), _ptr(out), _ptr(lse), _rows_ptr(dout, 3),
                                         dout.stride(0), dout.stride(1), _ptr(dq), _ptr(dk),
                                         _ptr(dv), _ptr(dbias), _ptr(workspace), _bytes(workspace),
                                         _stream(stream)))
@@ -756,14 +756,15 @@ class CrossAttention(torch.autograd.Function):
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
         emb_attention_forward(desc, out, lse, ws)
         ctx.save_for_backward(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos,
-                              lse)
+                              out, lse)
         ctx.scale = scale
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, lse = ctx.saved_tensors
+        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, out, lse = (
+            ctx.saved_tensors)
         desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
                                ctx.scale)
         if dout.dtype != q.dtype:
@@ -779,7 +780,7 @@ class CrossAttention(torch.autograd.Function):
         if bias is not None and want_bias:
             dbias = torch.empty(bias.shape, dtype=torch.float32, device=q.device)
         ws = torch.empty(ctx.need, dtype=torch.uint8, device=q.device) if ctx.need else None
-        emb_attention_backward(desc, lse, dout, dq, dk, dv, dbias, ws)
+        emb_attention_backward(desc, out, lse, dout, dq, dk, dv, dbias, ws)
         return (dq, dk, dv, dbias) + (None,) * 7
 
 

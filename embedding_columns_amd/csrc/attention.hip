@@ -32,6 +32,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kBucketsMax = 256;
 constexpr int kBiasWords = 4096;        // heads per key head x buckets held in LDS
 constexpr int kAttnThreads = 256;
+constexpr int kSplitsMax = 128;
 
 struct AttnArgs {
     const void *q, *k, *v, *dout;
@@ -43,7 +44,7 @@ struct AttnArgs {
     int64_t nq, nk;
     int32_t samples, heads, kv_heads, group, dim, buckets;
     float scale, c;                             // c = scale * log2(e)
-    int32_t vec;                                // rows can be read 16 bytes at a time
+    int32_t vec, ovec;                          // rows (of out) can be read 16 bytes at a time
     int32_t splits;
     int64_t tiles;
     void *out;                                  // [n_q, heads, dim]
@@ -127,30 +128,41 @@ struct Mma<uint16_t> {
             for (int j = 0; j < 4; j++) r.w[kc][j] = bf16x2_rne(p[8 * kc + 2 * j], p[8 * kc + 2 * j + 1]);
         return r;
     }
-    // acc[d, lane] += sum over the block's 32 keys of tile[key, d] w[key, lane], for
-    // d = 32 db ..: the tile's rows `r0 ..` are read transposed
+    // 32 rows of a tile from r0, elements 32 db .. of each, transposed, as first operand:
+    // times(): acc[d, lane] += sum over the block's 32 keys of tile[key, d] w[key, lane]
     template <int DP>
-    static __device__ __forceinline__ void transposed(f32x16_t &acc, const u32x4_t *tile, int r0, int db,
-                                                      const Pack &w)
-    {
-        using TL = Tile<uint16_t, DP>;
-        const int l = lane_id(), h = l >> 5;
+    struct Rows {
+        s16x8_t a[2];
+        __device__ __forceinline__ Rows(const u32x4_t *tile, int r0, int db)
+        {
+            using TL = Tile<uint16_t, DP>;
+            const int l = lane_id(), h = l >> 5;
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) {
-            s16x8_t a;
-#pragma unroll
-            for (int jb = 0; jb < 2; jb++) {
+            for (int j = 0; j < 4; j++) {
+                const int kc = j >> 1, jb = j & 1;
                 const int row = r0 + 16 * kc + 8 * jb + 4 * h + ((l & 15) >> 2);
                 const int col = 32 * db + 16 * ((l >> 4) & 1) + 4 * (l & 3);
                 const char *p = reinterpret_cast<const char *>(tile + TL::at(row, col >> 3)) + (col & 7) * 2;
                 const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (__attribute__((address_space(3))) s16x4_t *)(p));
 #pragma unroll
-                for (int e = 0; e < 4; e++) a[4 * jb + e] = v[e];
+                for (int e = 0; e < 4; e++) a[kc][4 * jb + e] = v[e];
             }
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                          __builtin_bit_cast(bf16x8_t, w.w[kc]), acc, 0, 0, 0);
         }
+        __device__ __forceinline__ void times(f32x16_t &acc, const Pack &w) const
+        {
+#pragma unroll
+            for (int kc = 0; kc < 2; kc++)
+                acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a[kc]),
+                                                              __builtin_bit_cast(bf16x8_t, w.w[kc]), acc, 0, 0, 0);
+        }
+    };
+    static __device__ __forceinline__ float dot(u32x4_t a, u32x4_t b)
+    {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) s += bf16_lo(a[j]) * bf16_lo(b[j]) + bf16_hi(a[j]) * bf16_hi(b[j]);
+        return s;
     }
     static __device__ __forceinline__ void store4(uint16_t *p, const float *v)
     {
@@ -172,17 +184,30 @@ struct Mma<float> {
     };
     static __device__ __forceinline__ Pack pack(const f32x16_t &p) { return Pack{p}; }
     template <int DP>
-    static __device__ __forceinline__ void transposed(f32x16_t &acc, const u32x4_t *tile, int r0, int db,
-                                                      const Pack &w)
-    {
-        using TL = Tile<float, DP>;
-        const int l = lane_id(), h = l >> 5, d = 32 * db + (l & 31);
+    struct Rows {
+        f32x16_t a;
+        __device__ __forceinline__ Rows(const u32x4_t *tile, int r0, int db)
+        {
+            using TL = Tile<float, DP>;
+            const int l = lane_id(), h = l >> 5, d = 32 * db + (l & 31);
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int row = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
-            const float a = reinterpret_cast<const float *>(tile + TL::at(row, d >> 2))[d & 3];
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a, w.w[i], acc, 0, 0, 0);
+            for (int i = 0; i < 16; i++) {
+                const int row = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
+                a[i] = reinterpret_cast<const float *>(tile + TL::at(row, d >> 2))[d & 3];
+            }
         }
+        __device__ __forceinline__ void times(f32x16_t &acc, const Pack &w) const
+        {
+#pragma unroll
+            for (int i = 0; i < 16; i++) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[i], w.w[i], acc, 0, 0, 0);
+        }
+    };
+    static __device__ __forceinline__ float dot(u32x4_t a, u32x4_t b)
+    {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; j++) s = fmaf(__uint_as_float(a[j]), __uint_as_float(b[j]), s);
+        return s;
     }
     static __device__ __forceinline__ void store4(float *p, const float *v)
     {
@@ -221,26 +246,55 @@ __device__ __forceinline__ f32x16_t block_order(const float *v)
 }
 __device__ __forceinline__ int block_key(int i) { return 8 * (i >> 2) + 4 * (lane_id() >> 5) + (i & 3); }
 
-__device__ __forceinline__ float both_halves_max(float x) { return fmaxf(x, __shfl_xor(x, 32)); }
-__device__ __forceinline__ float both_halves_sum(float x) { return x + __shfl_xor(x, 32); }
+// x combined with the other half's value of the same lane & 31
+__device__ __forceinline__ float both_halves_max(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_halves_sum(float x)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Sum over the wavefront, minimum and maximum over its halves, with DPP moves: inside
+// quads, half rows, rows of 16, then the last lane of a row into the next.
+#define EMB_DPP(x, ctrl, rows) __builtin_amdgcn_update_dpp(x, x, ctrl, rows, 0xF, false)
 __device__ __forceinline__ float wave_sum(float x)
 {
+    auto add = [](float v, int moved) { return v + __int_as_float(moved); };
+    x = add(x, EMB_DPP(__float_as_int(x), 0xB1, 0xF));
+    x = add(x, EMB_DPP(__float_as_int(x), 0x4E, 0xF));
+    x = add(x, EMB_DPP(__float_as_int(x), 0x141, 0xF));
+    x = add(x, EMB_DPP(__float_as_int(x), 0x140, 0xF));
+    // every lane now holds its row's sum
+    float r = 0.f;
 #pragma unroll
-    for (int s = 32; s; s >>= 1) x += __shfl_xor(x, s);
-    return x;
+    for (int l = 15; l < 64; l += 16) r += __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), l));
+    return r;
 }
-__device__ __forceinline__ int min32(int x)     // over the 32 lanes of a half
+struct Range {
+    int lo, hi;
+};
+// of the lanes of half 0 and of half 1
+__device__ __forceinline__ void half_ranges(int x, Range &r0, Range &r1)
 {
-#pragma unroll
-    for (int s = 16; s; s >>= 1) x = min(x, __shfl_xor(x, s));
-    return x;
+    int a = x, b = x;
+    a = min(a, EMB_DPP(a, 0xB1, 0xF));
+    b = max(b, EMB_DPP(b, 0xB1, 0xF));
+    a = min(a, EMB_DPP(a, 0x4E, 0xF));
+    b = max(b, EMB_DPP(b, 0x4E, 0xF));
+    a = min(a, EMB_DPP(a, 0x141, 0xF));
+    b = max(b, EMB_DPP(b, 0x141, 0xF));
+    a = min(a, EMB_DPP(a, 0x140, 0xF));
+    b = max(b, EMB_DPP(b, 0x140, 0xF));
+    r0.lo = min(__builtin_amdgcn_readlane(a, 0), __builtin_amdgcn_readlane(a, 16));
+    r0.hi = max(__builtin_amdgcn_readlane(b, 0), __builtin_amdgcn_readlane(b, 16));
+    r1.lo = min(__builtin_amdgcn_readlane(a, 32), __builtin_amdgcn_readlane(a, 48));
+    r1.hi = max(__builtin_amdgcn_readlane(b, 32), __builtin_amdgcn_readlane(b, 48));
 }
-__device__ __forceinline__ int max32(int x)
-{
-#pragma unroll
-    for (int s = 16; s; s >>= 1) x = max(x, __shfl_xor(x, s));
-    return x;
-}
+#undef EMB_DPP
 
 // ------------------------------------------------------------------ the bias
 
@@ -272,57 +326,75 @@ __device__ __forceinline__ int bucket_of(const Buckets &B, int x)
     return uniform(min(n, B.n));
 }
 
-// --------------------------------------------------------------- key tiles
+// ------------------------------------------------------ rows into LDS tiles
 
-// What a stage of key rows brings besides K and V.
-template <int KT>
-struct KeyMeta {
-    float out[KT];       // 0, or -inf where the key is masked or past the end
-    int pos[KT];
-    int lo[KT / 32], hi[KT / 32];   // range of positions of each 32 keys
-};
+// A 16-byte piece per lane from memory straight into 1 KB of LDS at `to`: lane l's
+// piece lands at to + 16 l.  `off` counts bytes from the descriptor's base (plus the
+// uniform `more`); an offset of kNowhere is out of the descriptor's range, reads no
+// memory and lands as zeros.  The load is asynchronous (vmcnt): the compiler does not
+// know of it, so the reader waits itself (arrived) before it reads.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ void load_to_lds(i32x4_t rsrc, uint32_t to, uint32_t off, uint32_t more)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(off), "s"(rsrc), "s"(more)
+                 : "memory");
+}
+// ... and before the tile it read from is overwritten, its LDS reads have to be done too
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
 
-// Loads keys [k0 + st .. + KT) of a sample that ends at k1 into LDS.  Masked keys
-// and those past the end are zeros whatever the memory holds: their scores get -inf
-// from the accumulator's initial value, and a probability of zero must not meet an
-// infinity or NaN of V.
-template <typename T, int DP, int KT>
-__device__ __forceinline__ void stage_keys(const AttnArgs &A, int kvh, int64_t k0, int64_t k1, u32x4_t *lk,
-                                           u32x4_t *lv, KeyMeta<KT> &M)
+__device__ __forceinline__ i32x4_t row_rsrc(const void *base)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    i32x4_t r;
+    r[0] = uniform((int)(uint32_t)b);
+    r[1] = uniform((int)(uint32_t)(b >> 32) & 0xFFFF);
+    r[2] = (int)kNowhere;
+    r[3] = kBufFlags;
+    return r;
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p);
+}
+
+// Brings ROWS rows (of `rows` that begin at element pointer `base`, `stride` elements
+// apart) into a tile's rows r0 .., by one wavefront; row r whose bit in `keep` is clear
+// becomes zeros and is not read.  Masked rows have to be zeros: a probability of zero
+// must not meet an infinity or NaN.
+template <typename T, int DP, int ROWS>
+__device__ __forceinline__ void bring_rows(const T *base, int64_t stride, int dim, bool vec, uint64_t keep,
+                                           u32x4_t *tile, int r0)
 {
     using TL = Tile<T, DP>;
-    const T *k = static_cast<const T *>(A.k) + kvh * A.kh, *v = static_cast<const T *>(A.v) + kvh * A.vh;
-    const int t = threadIdx.x;
-    static_assert(KT * TL::CH % kAttnThreads == 0, "whole chunks per thread");
-#pragma unroll 8
-    for (int i = t; i < KT * TL::CH; i += kAttnThreads) {
-        const int r = i / TL::CH, c = i % TL::CH;
-        const int64_t row = k0 + r;
-        u32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-        if (row < k1 && (!A.mask || *gp(A.mask + row))) {
-            a = load_chunk(k + row * A.ks, c, A.dim, A.vec);
-            b = load_chunk(v + row * A.vs, c, A.dim, A.vec);
+    constexpr int PER = 64 / TL::CH;                    // rows per load
+    const int l = lane_id(), rl = l / TL::CH;
+    const int c0 = (l % TL::CH) ^ swizzle<TL::CH>(rl);  // swizzle is a xor of row bits
+    u32x4_t *to = tile + r0 * TL::CH;
+    if (vec) {
+        const i32x4_t rsrc = row_rsrc(base);
+        const uint32_t lds = lds_address(to), mine = (uint32_t)(rl * (int)stride) * sizeof(T);
+        const uint64_t bits = keep >> rl;
+#pragma unroll
+        for (int j = 0; j < ROWS / PER; j++) {
+            const int c = c0 ^ swizzle<TL::CH>((r0 + j * PER) & 15);
+            const bool in = (bits >> (j * PER) & 1) && c * TL::E < dim;
+            load_to_lds(rsrc, lds + j * 1024, in ? mine + c * 16 : kNowhere,
+                        (uint32_t)(j * PER * (int)stride) * sizeof(T));
         }
-        lk[TL::at(r, c)] = a;
-        lv[TL::at(r, c)] = b;
+        return;
     }
-    if (t < KT) {
-        const int64_t row = k0 + t;
-        const bool in = row < k1 && (!A.mask || *gp(A.mask + row));
-        M.out[t] = in ? 0.f : -INFINITY;
-        if (A.bias) {
-            const int p = *gp(A.kp + (row < k1 ? row : k1 - 1));
-            M.pos[t] = p;
-            const int lo = min32(p), hi = max32(p);
-            if ((t & 31) == 0) {
-                M.lo[t / 32] = lo;
-                M.hi[t / 32] = hi;
-            }
-        }
+#pragma unroll 2
+    for (int j = 0; j < ROWS / PER; j++) {
+        const int r = j * PER + rl, c = c0 ^ swizzle<TL::CH>((r0 + j * PER) & 15);
+        u32x4_t v = {0, 0, 0, 0};
+        if (keep >> r & 1) v = load_chunk(base + r * stride, c, dim, false);
+        to[j * 64 + l] = v;
     }
 }
 
-// The range of stages a split takes of `n` stages.
+// The range of pieces a split takes of `n`.
 __device__ __forceinline__ void split_range(int64_t n, int split, int splits, int64_t &a, int64_t &b)
 {
     a = n * split / splits;
@@ -335,7 +407,7 @@ struct Row {
     int64_t q;       // row of q
     int head, g;     // query head, its number inside the group
     int pos;
-    int lo, hi;      // range of positions of the wavefront's rows
+    Range r;         // of positions of the wavefront's rows
 };
 
 __device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, int kvh, int64_t r0)
@@ -349,8 +421,8 @@ __device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, in
     R.q = s.base + i;
     R.head = kvh * A.group + R.g;
     R.pos = A.bias ? A.qp[R.q] : 0;
-    R.lo = uniform(min32(R.pos));
-    R.hi = uniform(max32(R.pos));
+    Range other;
+    half_ranges(R.pos, R.r, other);
     return R;
 }
 
@@ -369,17 +441,19 @@ __device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *row, int dim,
 // t_i = c' s_i + b'.  Where all pairs of the block fall in one bucket (most blocks:
 // buckets widen with the distance) the bias is one number a row and costs nothing;
 // otherwise each boundary inside the block's range is a compare and a select.
+// `kpos`: 32 words of LDS of this wavefront, `kp`: position of key lane & 31.
 __device__ __forceinline__ void add_bias(const AttnArgs &A, const Buckets &B, const float *lb, const int *lbnd,
-                                         const Row &R, const int *kpos, int klo, int khi, f32x16_t &s, float &c,
-                                         float &b)
+                                         const Row &R, int *kpos, int kp, Range k, f32x16_t &s, float &c, float &b)
 {
     c = A.c;
     b = 0.f;
     if (!A.bias) return;
-    const int lo = bucket_of(B, sub_sat(R.lo, khi)), hi = bucket_of(B, sub_sat(R.hi, klo));
+    const int lo = bucket_of(B, sub_sat(R.r.lo, k.hi)), hi = bucket_of(B, sub_sat(R.r.hi, k.lo));
     const float *mine = lb + R.g;
     b = mine[lo * A.group];
     if (lo == hi) return;
+    kpos[lane_id() & 31] = kp;
+    wave_sync();
     int x[16];
     f32x16_t t;
 #pragma unroll
@@ -387,6 +461,7 @@ __device__ __forceinline__ void add_bias(const AttnArgs &A, const Buckets &B, co
         x[i] = sub_sat(R.pos, kpos[block_key(i)]);
         t[i] = b;
     }
+    wave_sync();
     for (int m = lo; m < hi; m++) {
         const int edge = lbnd[m];
         const float v = mine[(m + 1) * A.group];
@@ -410,32 +485,165 @@ __device__ __forceinline__ void stage_bias(const AttnArgs &A, int kvh, float *lb
     for (int i = threadIdx.x; i < A.buckets - 1; i += kAttnThreads) lbnd[i] = A.bnd[i];
 }
 
-// keys per stage of the kernels that walk the keys
-template <typename T, int WM>
-constexpr int key_stage()
+// What the kernels that walk the keys share.  WM = 4: the four wavefronts take 32 query
+// rows each, share tiles of KT keys, and meet at a barrier per tile.  WM = 1 (few rows
+// per sample): all take the same 32 rows; each walks every fourth 32 keys with tiles of
+// its own and no barrier, and the four results meet at the end.  Either way the next
+// tile is on its way into the other buffer while one is worked on (kBufs = 2, where
+// two fit into LDS).
+template <typename T, int DP, int WM>
+struct KeyWalk {
+    using TL = Tile<T, DP>;
+    static constexpr int KT = WM == 4 && sizeof(T) == 2 ? 64 : 32;
+    static constexpr int kOwners = WM == 4 ? 1 : 4;             // sets of tiles
+    static constexpr int kWords = KT * TL::CH;                  // of K or V, 16 bytes each
+    static constexpr int kBufs = kOwners * 4 * kWords * 16 <= 131072 ? 2 : 1;
+    static constexpr int kLds = kOwners * kBufs * 2 * kWords;
+    static_assert(KT / (WM == 4 ? 4 : 1) >= 64 / TL::CH, "a load covers whole rows of one wavefront's share");
+
+    u32x4_t *mine;           // this wavefront's tiles
+    const AttnArgs &A;
+    int kvh, w;
+    int64_t k0, k1, at, end; // keys of the sample; tiles [at, end) of KT keys to go
+    int buf;
+    uint64_t keep;           // keys of the current tile that take part
+    int pos;                 // position of the current tile's key lane (KT = 64) or lane & 31
+    // of the tile after the current one
+    uint64_t keep_next;
+    int pos_next;
+    int raw_keep, raw_pos;   // loads in flight for the tile after that
+
+    __device__ __forceinline__ KeyWalk(const AttnArgs &a, u32x4_t *lds, int kvh_, int w_, int64_t k0_, int64_t k1_,
+                                       int split)
+        : A(a), kvh(kvh_), w(w_), k0(k0_), k1(k1_), buf(0)
+    {
+        mine = lds + (WM == 4 ? 0 : w * (kLds / 4));
+        split_range(k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0, split, A.splits, at, end);
+        if (WM == 1) at += w;
+    }
+    static constexpr int kStep = WM == 1 ? 4 : 1;
+
+    __device__ __forceinline__ const u32x4_t *k_tile() const { return mine + buf * 2 * kWords; }
+    __device__ __forceinline__ const u32x4_t *v_tile() const { return mine + buf * 2 * kWords + kWords; }
+
+    // mask and position of the keys of a tile, one key a lane
+    __device__ __forceinline__ void look(int64_t tile)
+    {
+        const int64_t key = k0 + tile * KT + (lane_id() & (KT - 1));
+        const bool in = tile < end && key < k1;
+        raw_keep = in ? (A.mask ? *gp(A.mask + key) : 1) : 0;
+        if (A.bias) raw_pos = *gp(A.kp + (key < k1 ? key : k1 - 1));
+    }
+    __device__ __forceinline__ void seen()
+    {
+        keep_next = __ballot(raw_keep != 0);
+        if (KT == 32) keep_next &= 0xFFFFFFFFull;
+        pos_next = raw_pos;
+    }
+    __device__ __forceinline__ void bring(int64_t tile, int to)
+    {
+        if (tile >= end) return;
+        const T *k = static_cast<const T *>(A.k) + kvh * A.kh + (k0 + tile * KT) * A.ks;
+        const T *v = static_cast<const T *>(A.v) + kvh * A.vh + (k0 + tile * KT) * A.vs;
+        u32x4_t *lk = mine + to * 2 * kWords, *lv = lk + kWords;
+        if (WM == 4) {       // a quarter of the tile each
+            constexpr int R = KT / 4;
+            bring_rows<T, DP, R>(k + w * R * A.ks, A.ks, A.dim, A.vec, keep_next >> (w * R), lk, w * R);
+            bring_rows<T, DP, R>(v + w * R * A.vs, A.vs, A.dim, A.vec, keep_next >> (w * R), lv, w * R);
+        } else {
+            bring_rows<T, DP, KT>(k, A.ks, A.dim, A.vec, keep_next, lk, 0);
+            bring_rows<T, DP, KT>(v, A.vs, A.dim, A.vec, keep_next, lv, 0);
+        }
+    }
+    __device__ __forceinline__ void start()
+    {
+        raw_pos = 0;
+        if (at >= end) return;
+        look(at);
+        seen();
+        if (kBufs == 2) bring(at, 0);
+        look(at + kStep);
+    }
+    // the current tile is in LDS after this, and the next on its way
+    __device__ __forceinline__ void enter()
+    {
+        keep = keep_next;
+        pos = pos_next;
+        if (kBufs == 1) {
+            arrived();
+            if (WM == 4) __syncthreads();
+            bring(at, 0);
+        }
+        arrived();
+        if (WM == 4) __syncthreads();
+        else wave_sync();
+        seen();
+        if (kBufs == 2) bring(at + kStep, buf ^ 1);
+        look(at + 2 * kStep);
+    }
+    __device__ __forceinline__ void leave()
+    {
+        at += kStep;
+        if (kBufs == 2) buf ^= 1;
+    }
+};
+
+// The four wavefronts' blocks x (DP elements of 32 rows each) summed through LDS;
+// wavefront w gets elements 32 d + 8 w + 4 h + e of row lane & 31 in r[d][e].
+template <int DP>
+__device__ __forceinline__ void sum_waves(float *lds, const f32x16_t (&x)[DP / 32], int w, float (&r)[DP / 32][4])
 {
-    return WM == 4 ? (sizeof(T) == 2 ? 64 : 32) : 128;
+    const int lane = lane_id(), h = lane >> 5;
+#pragma unroll
+    for (int d = 0; d < DP / 32; d++) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; i++) lds[(w * 32 + block_key(i)) * 32 + (lane & 31)] = x[d][i];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float z = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; u++) z += lds[(u * 32 + 8 * w + 4 * h + e) * 32 + (lane & 31)];
+            r[d][e] = z;
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_part(T *row, int col, int dim, const float *v)
+{
+    if (col + 4 <= dim && dim % 4 == 0) Mma<T>::store4(row + col, v);
+    else
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (col + e < dim) Mma<T>::store1(row + col + e, v[e]);
+}
+
+// 1 / l, zero for a row without keys; NaN stays
+__device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float log_sum(float m, float l)
+{
+    return l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ------------------------------------------------------------------ forward
 
-// WM = 4: the four wavefronts take 32 rows each and all keys.  WM = 1 (few rows per
-// sample): one set of 32 rows, and each wavefront takes every fourth 32 keys; the
-// four partial results meet in LDS.  With splits > 1 several workgroups share the
-// keys of one set of rows and attn_join finishes.
+// The running maximum m of a row may lag behind by 2^kLag: the weights stay far from
+// overflow, and the accumulators are rescaled only when it has to move.
+constexpr float kLag = 8.f;
+
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads) void attn_forward(AttnArgs A)
 {
-    using TL = Tile<T, DP>;
-    constexpr int KT = key_stage<T, WM>();
-    constexpr int kTileWords = 2 * KT * TL::CH;
-    constexpr int kJoinWords = WM == 1 ? 4 * 32 * DP / 4 : 0;
-    __shared__ u32x4_t lds[kTileWords > kJoinWords ? kTileWords : kJoinWords];
-    __shared__ KeyMeta<KT> M;
+    using KW = KeyWalk<T, DP, WM>;
+    constexpr int SUBS = KW::KT / 32;
+    __shared__ u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];    // 16 KB for sum_waves
     __shared__ int lbnd[kBucketsMax];
+    __shared__ int kpos[4][32];
+    __shared__ float kout[4][32];
     __shared__ float jm[4][32], jl[4][32];
     extern __shared__ float lb[];
-    u32x4_t *lk = lds, *lv = lds + KT * TL::CH;
 
     const int64_t id = xcd_block(blockIdx.x, gridDim.x, 0);
     const int split = (int)(id % A.splits);
@@ -450,72 +658,84 @@ __global__ __launch_bounds__(kAttnThreads) void attn_forward(AttnArgs A)
     const int64_t k0 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg);
     const int64_t k1 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg + 1);
 
+    KW walk(A, lds, kvh, w, k0, k1, split);
+    walk.start();
     stage_bias(A, kvh, lb, lbnd);
     const Buckets B = load_buckets(A);
     const Row R = query_row(A, s, kvh, r0);
     Frag<T, DP> qf;
     load_frag<T, DP>(qf, static_cast<const T *>(A.q) + R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
+    if (WM == 1) __syncthreads();     // the bias table; with WM = 4 the walk's barriers cover it
 
     float m = -INFINITY, l = 0.f;
     f32x16_t o[DP / 32];
 #pragma unroll
     for (int d = 0; d < DP / 32; d++) o[d] = f32x16_t{};
-    bool any = false;
 
-    int64_t st0, st1;
-    split_range(k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0, split, A.splits, st0, st1);
-    for (int64_t st = st0; st < st1; st++) {
-        const int64_t kb = k0 + st * KT;
-        __syncthreads();
-        stage_keys<T, DP, KT>(A, kvh, kb, k1, lk, lv, M);
-        __syncthreads();
-        if (!busy) continue;
-        for (int sub = WM == 4 ? 0 : w; sub < (WM == 4 ? KT / 32 : w + 1); sub++) {
-            if (kb + sub * 32 >= k1) break;
-            f32x16_t sc = block_order(M.out + sub * 32);
-            any |= __ballot(M.out[sub * 32 + (lane & 31)] == 0.f) != 0;
-            products<T, DP>(sc, lk, sub * 32, qf);
-            float c, b;
-            add_bias(A, B, lb, lbnd, R, M.pos + sub * 32, M.lo[sub], M.hi[sub], sc, c, b);
-            float top = sc[0];
+    for (; walk.at < walk.end; walk.leave()) {
+        walk.enter();
+        if (!busy || walk.keep == 0) continue;
+        const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
+        Range kr[2];
+        if (A.bias) half_ranges(walk.pos, kr[0], kr[1]);
+        f32x16_t sc[SUBS];
+        float c[SUBS], b[SUBS], top = -INFINITY;
 #pragma unroll
-            for (int i = 1; i < 16; i++) top = fmaxf(top, sc[i]);
-            top = both_halves_max(fmaf(top, c, b));
-            if (__ballot(top > m)) {
-                const float mn = fmaxf(m, top);
-                const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
-                m = mn;
-                l *= alpha;
-#pragma unroll
-                for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-                    for (int i = 0; i < 16; i++) o[d][i] *= alpha;
+        for (int u = 0; u < SUBS; u++) {
+            const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
+            sc[u] = f32x16_t{};
+            if (keep != 0xFFFFFFFFu) {
+                // keys that take no part start at -inf (their K is zero)
+                kout[w][lane & 31] = keep >> (lane & 31) & 1 ? 0.f : -INFINITY;
+                wave_sync();
+                sc[u] = block_order(kout[w]);
+                wave_sync();
             }
-            const float base = b - (m == -INFINITY ? 0.f : m);
+            products<T, DP>(sc[u], lk, u * 32, qf);
+        }
+#pragma unroll
+        for (int u = 0; u < SUBS; u++) {
+            const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
+            add_bias(A, B, lb, lbnd, R, kpos[w], kp, kr[u], sc[u], c[u], b[u]);
+            float t = sc[u][0];
+#pragma unroll
+            for (int i = 1; i < 16; i++) t = fmaxf(t, sc[u][i]);
+            top = fmaxf(top, fmaf(t, c[u], b[u]));
+        }
+        top = both_halves_max(top);
+        if (__ballot(top > m + kLag)) {
+            const float mn = fmaxf(m, top);
+            const float alpha = exp2_fast(m - (mn == -INFINITY ? 0.f : mn));
+            m = mn;
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < DP / 32; d++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) o[d][i] *= alpha;
+        }
+        const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int u = 0; u < SUBS; u++) {
+            const float bu = b[u] - base;
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                sc[i] = exp2_fast(fmaf(sc[i], c, base));
-                sum += sc[i];
+                sc[u][i] = exp2_fast(fmaf(sc[u][i], c[u], bu));
+                sum += sc[u][i];
             }
             l += sum;
-            const typename Mma<T>::Pack p = Mma<T>::pack(sc);
+            const typename Mma<T>::Pack p = Mma<T>::pack(sc[u]);
 #pragma unroll
-            for (int d = 0; d < DP / 32; d++) Mma<T>::template transposed<DP>(o[d], lv, sub * 32, d, p);
+            for (int d = 0; d < DP / 32; d++) typename Mma<T>::template Rows<DP>(lv, u * 32, d).times(o[d], p);
         }
     }
     l = both_halves_sum(l);
-    if (!any) {            // no key at all: zero, also where q is not finite
-        m = -INFINITY;
-        l = 0.f;
-#pragma unroll
-        for (int d = 0; d < DP / 32; d++) o[d] = f32x16_t{};
-    }
+    const int64_t row = R.q * A.heads + R.head;
+    const int64_t at = (int64_t)split * A.nq * A.heads + row;
+    T *out = static_cast<T *>(A.out) + row * A.dim;
 
     if (WM == 1) {
         // the four wavefronts' parts of the same rows, scaled to a common maximum
-        float *lo = reinterpret_cast<float *>(lds);
-        __syncthreads();
         if (h == 0) {
             jm[w][lane & 31] = m;
             jl[w][lane & 31] = l;
@@ -531,134 +751,100 @@ __global__ __launch_bounds__(kAttnThreads) void attn_forward(AttnArgs A)
 #pragma unroll
         for (int d = 0; d < DP / 32; d++)
 #pragma unroll
-            for (int i = 0; i < 16; i++) lo[(w * DP + 32 * d + block_key(i)) * 32 + (lane & 31)] = o[d][i] * f;
-        __syncthreads();
-        // wavefront w finishes the 8 (i >> 2) groups of d with i >> 2 == w
-        m = mt;
-        l = lt;
+            for (int i = 0; i < 16; i++) o[d][i] *= f;
         float r[DP / 32][4];
-#pragma unroll
-        for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int row = 32 * d + 8 * w + 4 * h + e;
-                float x = 0.f;
-#pragma unroll
-                for (int u = 0; u < 4; u++) x += lo[(u * DP + row) * 32 + (lane & 31)];
-                r[d][e] = x;
-            }
+        sum_waves<DP>(reinterpret_cast<float *>(lds), o, w, r);
         if (!R.live) return;
-        const int64_t row = R.q * A.heads + R.head;
-        if (A.splits > 1) {
-            const int64_t at = (int64_t)split * A.nq * A.heads + row;
-#pragma unroll
-            for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) A.part[at * DP + 32 * d + 8 * w + 4 * h + e] = r[d][e];
-            if (w == 0 && h == 0) {
-                A.part_ml[2 * at] = m;
-                A.part_ml[2 * at + 1] = l;
-            }
-            return;
-        }
-        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        T *out = static_cast<T *>(A.out) + row * A.dim;
+        const float f2 = A.splits > 1 ? 1.f : inverse(lt);
 #pragma unroll
         for (int d = 0; d < DP / 32; d++) {
             const int col = 32 * d + 8 * w + 4 * h;
-            float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = r[d][e] * inv;
-            if (col + 4 <= A.dim && A.dim % 4 == 0) Mma<T>::store4(out + col, v);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (col + e < A.dim) Mma<T>::store1(out + col + e, v[e]);
+            for (int e = 0; e < 4; e++) r[d][e] *= f2;
+            if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, r[d]);
+            else store_part(out, col, A.dim, r[d]);
         }
-        if (w == 0 && h == 0 && A.lse) A.lse[row] = l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
-        return;
-    }
-
-    if (!R.live || !busy) return;
-    const int64_t row = R.q * A.heads + R.head;
-    if (A.splits > 1) {
-        const int64_t at = (int64_t)split * A.nq * A.heads + row;
+        m = mt;
+        l = lt;
+        if (w != 0) return;
+    } else {
+        if (!R.live || !busy) return;
+        const float f2 = A.splits > 1 ? 1.f : inverse(l);
 #pragma unroll
         for (int d = 0; d < DP / 32; d++)
 #pragma unroll
-            for (int i = 0; i < 16; i++) A.part[at * DP + 32 * d + block_key(i)] = o[d][i];
-        if (h == 0) {
-            A.part_ml[2 * at] = m;
-            A.part_ml[2 * at + 1] = l;
-        }
-        return;
+            for (int g = 0; g < 4; g++) {
+                const int col = 32 * d + 8 * g + 4 * h;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e] = o[d][4 * g + e] * f2;
+                if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, v);
+                else store_part(out, col, A.dim, v);
+            }
     }
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    T *out = static_cast<T *>(A.out) + row * A.dim;
-#pragma unroll
-    for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-        for (int g = 0; g < 4; g++) {
-            const int col = 32 * d + 8 * g + 4 * h;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = o[d][4 * g + e] * inv;
-            if (col + 4 <= A.dim && A.dim % 4 == 0) Mma<T>::store4(out + col, v);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (col + e < A.dim) Mma<T>::store1(out + col + e, v[e]);
-        }
-    if (h == 0 && A.lse) A.lse[row] = l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (h != 0) return;
+    if (A.splits > 1) {
+        A.part_ml[2 * at] = m;
+        A.part_ml[2 * at + 1] = l;
+    } else if (A.lse) {
+        A.lse[row] = log_sum(m, l);
+    }
 }
 
-// Joins the splits of a row: a wavefront per (row, head), a lane per element.
+// Joins the splits of a row: a workgroup per (row, head), a lane per element, the
+// wavefronts take the splits in turn.
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), n = A.nq * A.heads;
-    if (row >= n) return;
-    const int lane = lane_id();
-    float m = -INFINITY;
-    for (int u = 0; u < A.splits; u++) m = fmaxf(m, A.part_ml[2 * (u * n + row)]);
-    const float mb = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o[(DP + 63) / 64] = {};
-    for (int u = 0; u < A.splits; u++) {
-        const float f = exp2_fast(A.part_ml[2 * (u * n + row)] - mb);
-        l += A.part_ml[2 * (u * n + row) + 1] * f;
-#pragma unroll
-        for (int e = 0; e < (DP + 63) / 64; e++)
-            if (64 * e + lane < DP) o[e] += A.part[(u * n + row) * DP + 64 * e + lane] * f;
+    constexpr int G = kAttnThreads / DP;      // splits side by side
+    __shared__ float sm[kSplitsMax], sl[kSplitsMax], so[G][DP];
+    const int64_t row = blockIdx.x, n = A.nq * A.heads;
+    const int t = threadIdx.x, d = t % DP, g = t / DP;
+    for (int u = t; u < A.splits; u += kAttnThreads) {
+        sm[u] = A.part_ml[2 * (u * n + row)];
+        sl[u] = A.part_ml[2 * (u * n + row) + 1];
     }
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    T *out = static_cast<T *>(A.out) + row * A.dim;
+    __syncthreads();
+    float m = -INFINITY;
+    for (int u = 0; u < A.splits; u++) m = fmaxf(m, sm[u]);
+    const float mb = m == -INFINITY ? 0.f : m;
+    float o = 0.f;
+#pragma unroll 8
+    for (int u = g; u < A.splits; u += G) o += A.part[(u * n + row) * DP + d] * exp2_fast(sm[u] - mb);
+    so[g][d] = o;
+    __syncthreads();
+    if (g != 0) return;
+    float l = 0.f;
+    for (int u = 0; u < A.splits; u++) l += sl[u] * exp2_fast(sm[u] - mb);
+    o = 0.f;
 #pragma unroll
-    for (int e = 0; e < (DP + 63) / 64; e++)
-        if (64 * e + lane < A.dim) Mma<T>::store1(out + 64 * e + lane, o[e] * inv);
-    if (lane == 0 && A.lse) A.lse[row] = l > 0.f || l != l ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    for (int u = 0; u < G; u++) o += so[u][d];
+    if (d < A.dim) Mma<T>::store1(static_cast<T *>(A.out) + row * A.dim + d, o * inverse(l));
+    if (d == 0 && A.lse) A.lse[row] = log_sum(m, l);
 }
 
 // ------------------------------------------------------- backward: queries
 
-// dq_i = scale (sum_j p_ij dP_ij k_j - delta_i sum_j p_ij k_j) with
-// delta_i = sum_j p_ij dP_ij, all three sums in one pass over the keys.  Taking delta
-// from the probabilities that the gradients use (and not from the output, which was
-// rounded) costs a fourth product and makes the gradients of a row's scores add up
-// to zero in fp32: the bias gradient is a sum of those over many rows and would
-// otherwise drown in the rounding of the output.
+// dq_i = scale sum_j p_ij (dP_ij - delta_i) k_j.  One pass over the keys takes three sums,
+//   x_i = sum_j p_ij (dP_ij - D_i) k_j,  y_i = sum_j p_ij k_j,  e_i = sum_j p_ij (dP_ij - D_i),
+// with D_i = o_i.dO_i, which is delta_i up to the rounding of the output and of the
+// probabilities that made it: delta = D + e, dq = scale (x - e y).  Score gradients of
+// nearly the right offset keep x exact to one rounding; y is a fourth product and
+// corrects the rest.  Without it dq of bf16 inputs is off by the output's rounding
+// times |y|, and without e the bias gradient, a sum of score gradients over many rows,
+// each row's adding up to zero, would drown in that rounding.  In fp32 D is exact
+// enough for dq, and y is left out.
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads) void attn_backward_q(AttnArgs A)
 {
+    using KW = KeyWalk<T, DP, WM>;
     using TL = Tile<T, DP>;
-    constexpr int KT = key_stage<T, WM>();
-    constexpr int kTileWords = 2 * KT * TL::CH;
-    constexpr int kJoinWords = WM == 1 ? 4 * 32 * DP / 4 : 0;
-    __shared__ u32x4_t lds[kTileWords > kJoinWords ? kTileWords : kJoinWords];
-    __shared__ KeyMeta<KT> M;
+    constexpr int SUBS = KW::KT / 32;
+    __shared__ u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];
     __shared__ int lbnd[kBucketsMax];
+    __shared__ int kpos[4][32];
     __shared__ float jd[4][32];
     extern __shared__ float lb[];
-    u32x4_t *lk = lds, *lv = lds + KT * TL::CH;
 
     const int64_t id = xcd_block(blockIdx.x, gridDim.x, 0);
     const int split = (int)(id % A.splits);
@@ -673,6 +859,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_q(AttnArgs A)
     const int64_t k0 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg);
     const int64_t k1 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg + 1);
 
+    KW walk(A, lds, kvh, w, k0, k1, split);
+    walk.start();
     stage_bias(A, kvh, lb, lbnd);
     const Buckets B = load_buckets(A);
     const Row R = query_row(A, s, kvh, r0);
@@ -680,146 +868,146 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_q(AttnArgs A)
     Frag<T, DP> qf, df;
     load_frag<T, DP>(qf, static_cast<const T *>(A.q) + R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
     load_frag<T, DP>(df, static_cast<const T *>(A.dout) + R.q * A.ds + R.head * A.dh, A.dim, A.vec, R.live);
+    float D = 0.f;
+    {
+        Frag<T, DP> of;
+        load_frag<T, DP>(of, static_cast<const T *>(A.out) + row * A.dim, A.dim, A.ovec, R.live);
+#pragma unroll
+        for (int c = 0; c < TL::CH / 2; c++) D += Mma<T>::dot(of[c], df[c]);
+        D = both_halves_sum(D);
+    }
     // a row without keys has lse = -inf: exp2(score - inf) keeps its weights zero
     float lse = R.live ? A.lse[row] * kLog2e : INFINITY;
     if (lse == -INFINITY) lse = INFINITY;
+    if (WM == 1) __syncthreads();
 
-    float delta = 0.f;
-    f32x16_t x[DP / 32], y[DP / 32];       // sum p dP k, sum p k
+    constexpr bool kWithY = sizeof(T) == 2;
+    float e = 0.f;
+    f32x16_t x[DP / 32], y[DP / 32];
 #pragma unroll
     for (int d = 0; d < DP / 32; d++) x[d] = y[d] = f32x16_t{};
 
-    int64_t st0, st1;
-    split_range(k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0, split, A.splits, st0, st1);
-    for (int64_t st = st0; st < st1; st++) {
-        const int64_t kb = k0 + st * KT;
-        __syncthreads();
-        stage_keys<T, DP, KT>(A, kvh, kb, k1, lk, lv, M);
-        __syncthreads();
-        if (!busy) continue;
-        for (int sub = WM == 4 ? 0 : w; sub < (WM == 4 ? KT / 32 : w + 1); sub++) {
-            if (kb + sub * 32 >= k1) break;
-            f32x16_t sc = block_order(M.out + sub * 32), dp = f32x16_t{};
-            products<T, DP>(sc, lk, sub * 32, qf);
-            products<T, DP>(dp, lv, sub * 32, df);
+    for (; walk.at < walk.end; walk.leave()) {
+        walk.enter();
+        if (!busy || walk.keep == 0) continue;
+        const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
+        Range kr[2];
+        if (A.bias) half_ranges(walk.pos, kr[0], kr[1]);
+#pragma unroll
+        for (int u = 0; u < SUBS; u++) {
+            const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
+            f32x16_t sc = f32x16_t{}, dp;
+#pragma unroll
+            for (int i = 0; i < 16; i++) dp[i] = -D;
+            products<T, DP>(sc, lk, u * 32, qf);
+            products<T, DP>(dp, lv, u * 32, df);
             float c, b;
-            add_bias(A, B, lb, lbnd, R, M.pos + sub * 32, M.lo[sub], M.hi[sub], sc, c, b);
+            const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
+            add_bias(A, B, lb, lbnd, R, kpos[w], kp, kr[u], sc, c, b);
             b -= lse;
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-                sc[i] = exp2_fast(fmaf(sc[i], c, b));
-                dp[i] *= sc[i];
-                delta += dp[i];
+            for (int i = 0; i < 16; i++) sc[i] = exp2_fast(fmaf(sc[i], c, b));
+            if (keep != 0xFFFFFFFFu) {
+                const uint32_t mine = keep >> (4 * h);
+#pragma unroll
+                for (int i = 0; i < 16; i++) sc[i] = mine >> (8 * (i >> 2) + (i & 3)) & 1 ? sc[i] : 0.f;
             }
-            const typename Mma<T>::Pack p = Mma<T>::pack(sc), pd = Mma<T>::pack(dp);
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                dp[i] *= sc[i];
+                e += dp[i];
+            }
+            const typename Mma<T>::Pack ds = Mma<T>::pack(dp), p = Mma<T>::pack(sc);
 #pragma unroll
             for (int d = 0; d < DP / 32; d++) {
-                Mma<T>::template transposed<DP>(x[d], lk, sub * 32, d, pd);
-                Mma<T>::template transposed<DP>(y[d], lk, sub * 32, d, p);
+                const typename Mma<T>::template Rows<DP> kt(lk, u * 32, d);
+                kt.times(x[d], ds);
+                if (kWithY) kt.times(y[d], p);
             }
         }
     }
-    delta = both_halves_sum(delta);
+    e = both_halves_sum(e);
+    const int64_t at = (int64_t)split * A.nq * A.heads + row;
     T *dq = static_cast<T *>(A.dq) + row * A.dim;
     if (WM == 1) {
-        float *lo = reinterpret_cast<float *>(lds);
-        float r[2][DP / 32][4];
-        __syncthreads();
-        if (h == 0) jd[w][lane & 31] = delta;
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            if (k) __syncthreads();
-#pragma unroll
-            for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-                for (int i = 0; i < 16; i++)
-                    lo[(w * DP + 32 * d + block_key(i)) * 32 + (lane & 31)] = k ? y[d][i] : x[d][i];
-            __syncthreads();
-#pragma unroll
-            for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    float z = 0.f;
-#pragma unroll
-                    for (int u = 0; u < 4; u++) z += lo[(u * DP + 32 * d + 8 * w + 4 * h + e) * 32 + (lane & 31)];
-                    r[k][d][e] = z;
-                }
-        }
-        delta = (jd[0][lane & 31] + jd[1][lane & 31]) + (jd[2][lane & 31] + jd[3][lane & 31]);
+        if (h == 0) jd[w][lane & 31] = e;
+        float rx[DP / 32][4], ry[DP / 32][4];
+        sum_waves<DP>(reinterpret_cast<float *>(lds), x, w, rx);
+        if (kWithY) sum_waves<DP>(reinterpret_cast<float *>(lds), y, w, ry);
+        e = (jd[0][lane & 31] + jd[1][lane & 31]) + (jd[2][lane & 31] + jd[3][lane & 31]);
         if (!R.live) return;
-        if (A.splits > 1) {
-            const int64_t at = (int64_t)split * A.nq * A.heads + row;
 #pragma unroll
-            for (int d = 0; d < DP / 32; d++)
+        for (int d = 0; d < DP / 32; d++) {
+            const int col = 32 * d + 8 * w + 4 * h;
+            if (A.splits > 1) {
+                Mma<float>::store4(A.part + 2 * at * DP + col, rx[d]);
+                if (kWithY) Mma<float>::store4(A.part + (2 * at + 1) * DP + col, ry[d]);
+                continue;
+            }
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    A.part[2 * at * DP + 32 * d + 8 * w + 4 * h + e] = r[0][d][e];
-                    A.part[(2 * at + 1) * DP + 32 * d + 8 * w + 4 * h + e] = r[1][d][e];
+            for (int i = 0; i < 4; i++) rx[d][i] = A.scale * (kWithY ? rx[d][i] - e * ry[d][i] : rx[d][i]);
+            store_part(dq, col, A.dim, rx[d]);
+        }
+        if (w != 0) return;
+    } else {
+        if (!R.live || !busy) return;
+#pragma unroll
+        for (int d = 0; d < DP / 32; d++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const int col = 32 * d + 8 * g + 4 * h;
+                float v[4], z[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    v[i] = x[d][4 * g + i];
+                    z[i] = y[d][4 * g + i];
                 }
-            if (w == 0 && h == 0) A.part_ml[at] = delta;
-            return;
-        }
+                if (A.splits > 1) {
+                    Mma<float>::store4(A.part + 2 * at * DP + col, v);
+                    if (kWithY) Mma<float>::store4(A.part + (2 * at + 1) * DP + col, z);
+                    continue;
+                }
 #pragma unroll
-        for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int col = 32 * d + 8 * w + 4 * h + e;
-                if (col < A.dim) Mma<T>::store1(dq + col, A.scale * (r[0][d][e] - delta * r[1][d][e]));
+                for (int i = 0; i < 4; i++) v[i] = A.scale * (kWithY ? v[i] - e * z[i] : v[i]);
+                store_part(dq, col, A.dim, v);
             }
-        if (w == 0 && h == 0) A.delta[row] = delta;
-        return;
     }
-    if (!R.live || !busy) return;
+    if (h != 0) return;
     if (A.splits > 1) {
-        const int64_t at = (int64_t)split * A.nq * A.heads + row;
-#pragma unroll
-        for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-                A.part[2 * at * DP + 32 * d + block_key(i)] = x[d][i];
-                A.part[(2 * at + 1) * DP + 32 * d + block_key(i)] = y[d][i];
-            }
-        if (h == 0) A.part_ml[at] = delta;
-        return;
+        A.part_ml[2 * at] = D;
+        A.part_ml[2 * at + 1] = e;
+    } else {
+        A.delta[row] = D + e;
     }
-#pragma unroll
-    for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-        for (int g = 0; g < 4; g++) {
-            const int col = 32 * d + 8 * g + 4 * h;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) v[e] = A.scale * (x[d][4 * g + e] - delta * y[d][4 * g + e]);
-            if (col + 4 <= A.dim && A.dim % 4 == 0) Mma<T>::store4(dq + col, v);
-            else
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (col + e < A.dim) Mma<T>::store1(dq + col + e, v[e]);
-        }
-    if (h == 0) A.delta[row] = delta;
 }
 
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), n = A.nq * A.heads;
-    if (row >= n) return;
-    const int lane = lane_id();
-    float delta = 0.f, x[(DP + 63) / 64] = {}, y[(DP + 63) / 64] = {};
-    for (int u = 0; u < A.splits; u++) {
-        delta += A.part_ml[u * n + row];
-#pragma unroll
-        for (int e = 0; e < (DP + 63) / 64; e++)
-            if (64 * e + lane < DP) {
-                x[e] += A.part[2 * (u * n + row) * DP + 64 * e + lane];
-                y[e] += A.part[(2 * (u * n + row) + 1) * DP + 64 * e + lane];
-            }
+    constexpr int G = kAttnThreads / DP;
+    constexpr bool kWithY = sizeof(T) == 2;
+    __shared__ float so[2][G][DP];
+    const int64_t row = blockIdx.x, n = A.nq * A.heads;
+    const int t = threadIdx.x, d = t % DP, g = t / DP;
+    float x = 0.f, y = 0.f, e = 0.f;
+#pragma unroll 4
+    for (int u = g; u < A.splits; u += G) {
+        x += A.part[2 * (u * n + row) * DP + d];
+        if (kWithY) y += A.part[(2 * (u * n + row) + 1) * DP + d];
     }
-    T *dq = static_cast<T *>(A.dq) + row * A.dim;
+    so[0][g][d] = x;
+    so[1][g][d] = y;
+    __syncthreads();
+    if (g != 0) return;
+    x = y = 0.f;
 #pragma unroll
-    for (int e = 0; e < (DP + 63) / 64; e++)
-        if (64 * e + lane < A.dim) Mma<T>::store1(dq + 64 * e + lane, A.scale * (x[e] - delta * y[e]));
-    if (lane == 0) A.delta[row] = delta;
+    for (int u = 0; u < G; u++) {
+        x += so[0][u][d];
+        y += so[1][u][d];
+    }
+    for (int u = 0; u < A.splits; u++) e += A.part_ml[2 * (u * n + row) + 1];
+    if (d < A.dim) Mma<T>::store1(static_cast<T *>(A.dq) + row * A.dim + d, A.scale * (kWithY ? x - e * y : x));
+    if (d == 0) A.delta[row] = A.part_ml[2 * row] + e;
 }
 
 // ---------------------------------------------------------- backward: keys
@@ -868,8 +1056,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
     int kpos = 0, klo = 0, khi = 0;
     if (A.bias && !idle) {
         kpos = A.kp[key];
-        klo = uniform(min32(kpos));
-        khi = uniform(max32(kpos));
+        Range mine, other;
+        half_ranges(kpos, mine, other);
+        klo = mine.lo;
+        khi = mine.hi;
     }
     Frag<T, DP> kf, vf;
     load_frag<T, DP>(kf, static_cast<const T *>(A.k) + (live ? key * A.ks + kvh * A.kh : 0), A.dim, A.vec, live);
@@ -904,10 +1094,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
                 if (A.bias) {
                     const int p = A.qp[there ? qb + t : q1 - 1];
                     qpos[t] = p;
-                    const int lo = min32(p), hi = max32(p);
-                    if ((t & 31) == 0) {
-                        qlo[t / 32] = lo;
-                        qhi[t / 32] = hi;
+                    Range mine, other;
+                    half_ranges(p, mine, other);
+                    if (t == 0) {
+                        qlo[0] = mine.lo;
+                        qhi[0] = mine.hi;
                     }
                 }
             }
@@ -951,8 +1142,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
                 const typename Mma<T>::Pack p = Mma<T>::pack(sc), ds = Mma<T>::pack(dp);
 #pragma unroll
                 for (int d = 0; d < DP / 32; d++) {
-                    Mma<T>::template transposed<DP>(dv[d], ld, sub * 32, d, p);
-                    Mma<T>::template transposed<DP>(dk[d], lq, sub * 32, d, ds);
+                    typename Mma<T>::template Rows<DP>(ld, sub * 32, d).times(dv[d], p);
+                    typename Mma<T>::template Rows<DP>(lq, sub * 32, d).times(dk[d], ds);
                 }
                 if (A.dbias_part) {
                     for (int m = lo; m <= hi; m++) {
@@ -1056,7 +1247,7 @@ AttnPlan attn_plan(const emb_attention *a)
     const int64_t stages = a->n_k / samples / 128;     // of the average sample
     int64_t s = sets > 0 ? (1024 + sets - 1) / sets : 1;
     s = std::min<int64_t>(s, std::max<int64_t>(1, stages / 2));
-    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 128));
+    p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, kSplitsMax));
     p.key_tiles = seg_tiles(a->n_k, a->samples, 1, 128);
     return p;
 }
@@ -1075,7 +1266,7 @@ size_t backward_workspace(const emb_attention *a, const AttnPlan &p)
     size_t n = pad256((size_t)a->n_q * a->heads * 4);
     if (p.splits > 1) {
         const size_t rows = (size_t)p.splits * a->n_q * a->heads;
-        n += pad256(rows * padded_dim(a->dim) * 8) + pad256(rows * 4);
+        n += pad256(rows * padded_dim(a->dim) * 8) + pad256(rows * 8);
     }
     if (a->buckets) n += pad256((size_t)p.key_tiles * a->heads * a->buckets * 4);
     return n;
@@ -1124,10 +1315,11 @@ emb_status attn_pointers(const emb_attention *a)
     return EMB_OK;
 }
 
-// rows that can be read in 16-byte pieces: whole pieces per row, every row aligned
+// rows that can be read in 16-byte pieces: whole pieces per row, every row aligned, and
+// the 64 rows of a tile within the 2^31 bytes that one descriptor reaches
 bool wide_rows(const void *p, int64_t stride, int64_t head_stride, int dim, size_t el)
 {
-    return aligned(p, 16) && stride * el % 16 == 0 && head_stride * el % 16 == 0 && dim * el % 16 == 0;
+    return stride < (int64_t(1) << 31) / 64 / (int64_t)el && aligned(p, 16) && stride * el % 16 == 0 && head_stride * el % 16 == 0 && dim * el % 16 == 0;
 }
 
 AttnArgs attn_args(const emb_attention *a, const AttnPlan &p)
@@ -1183,7 +1375,7 @@ emb_status forward_run(const AttnArgs &A, const AttnPlan &p, hipStream_t st)
     if (p.wm == 4) hipLaunchKernelGGL((attn_forward<T, DP, 4>), grid, block, lds, st, A);
     else hipLaunchKernelGGL((attn_forward<T, DP, 1>), grid, block, lds, st, A);
     if (p.splits > 1)
-        hipLaunchKernelGGL((attn_join<T, DP>), dim3((unsigned)((A.nq * A.heads + 3) / 4)), block, 0, st, A);
+        hipLaunchKernelGGL((attn_join<T, DP>), dim3((unsigned)(A.nq * A.heads)), block, 0, st, A);
     return launched("attention forward");
 }
 
@@ -1198,7 +1390,7 @@ emb_status backward_run(const AttnArgs &A0, const AttnPlan &p, float *dbias, hip
         if (p.wm == 4) hipLaunchKernelGGL((attn_backward_q<T, DP, 4>), grid, block, lds, st, A);
         else hipLaunchKernelGGL((attn_backward_q<T, DP, 1>), grid, block, lds, st, A);
         if (p.splits > 1)
-            hipLaunchKernelGGL((attn_join_q<T, DP>), dim3((unsigned)((A.nq * A.heads + 3) / 4)), block, 0, st, A);
+            hipLaunchKernelGGL((attn_join_q<T, DP>), dim3((unsigned)(A.nq * A.heads)), block, 0, st, A);
     }
     A.tiles = p.key_tiles;
     if (A.dk || dbias)
@@ -1213,7 +1405,7 @@ bool grid_fits(const emb_attention *a, const AttnPlan &p)
 {
     const double most = 2147483647.0;
     return (double)p.tiles * a->kv_heads * p.splits <= most && (double)p.key_tiles * a->kv_heads <= most &&
-           (double)a->n_q * a->heads / 4 + 1 <= most;
+           (double)a->n_q * a->heads <= most;
 }
 
 }  // namespace
@@ -1264,7 +1456,7 @@ extern "C" emb_status emb_attention_forward(const emb_attention *a, void *out, f
                       : forward_run<float, 128>(A, p, st);
 }
 
-extern "C" emb_status emb_attention_backward(const emb_attention *a, const float *lse, const void *dout,
+extern "C" emb_status emb_attention_backward(const emb_attention *a, const void *out, const float *lse, const void *dout,
                                              int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
                                              void *dv, float *dbias, void *workspace, size_t workspace_bytes,
                                              void *stream)
@@ -1274,11 +1466,11 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const float
     if (s != EMB_OK) return s;
     const size_t el = a->dtype == EMB_BF16 ? 2 : 4;
     const size_t al = a->dim % 4 == 0 ? 4 * el : el;
-    if (a->n_q && (!lse || !dout || !dq))
-        return fail(EMB_ERR_INVALID_ARG, "attention: lse, dout and dq must be given");
+    if (a->n_q && (!out || !lse || !dout || !dq))
+        return fail(EMB_ERR_INVALID_ARG, "attention: out, lse, dout and dq must be given");
     if (!dk != !dv) return fail(EMB_ERR_INVALID_ARG, "attention: dk and dv are given together");
     if (dbias && !a->buckets) return fail(EMB_ERR_INVALID_ARG, "attention: dbias without a bias");
-    if (!aligned(dout, el) || !aligned(dq, al) || !aligned(dk, al) || !aligned(dv, al) || !aligned(lse, 4) ||
+    if (!aligned(dout, el) || !aligned(out, el) || !aligned(dq, al) || !aligned(dk, al) || !aligned(dv, al) || !aligned(lse, 4) ||
         !aligned(dbias, 4))
         return fail(EMB_ERR_INVALID_ARG, "attention: gradients must be aligned to four elements");
     if (dout_stride < 0 || dout_head_stride < 0) return fail(EMB_ERR_INVALID_ARG, "attention: strides must be >= 0");
@@ -1292,6 +1484,8 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const float
     A.ds = dout_stride;
     A.dh = dout_head_stride;
     A.vec = A.vec && wide_rows(dout, dout_stride, dout_head_stride, a->dim, el);
+    A.out = const_cast<void *>(out);
+    A.ovec = wide_rows(out, a->dim, a->dim, a->dim, el);
     A.lse = const_cast<float *>(lse);
     A.dq = dq;
     A.dk = dk;
@@ -1304,7 +1498,7 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const float
         A.part = reinterpret_cast<float *>(ws);
         ws += pad256(rows * padded_dim(a->dim) * 8);
         A.part_ml = reinterpret_cast<float *>(ws);
-        ws += pad256(rows * 4);
+        ws += pad256(rows * 8);
     }
     if (dbias) A.dbias_part = reinterpret_cast<float *>(ws);
     const hipStream_t st = static_cast<hipStream_t>(stream);

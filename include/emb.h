@@ -467,9 +467,9 @@ emb_status emb_attention_forward(const emb_attention *a, void *out, float *lse, 
 
 /* dq: [n_q, heads, dim]; dk, dv: [n_k, kv_heads, dim] (both, or both NULL); dbias: fp32
  * [buckets, heads] or NULL.  All contiguous, overwritten, and the same bits for the same
- * inputs.  dout: as q, with its own strides. */
-emb_status emb_attention_backward(const emb_attention *a, const float *lse, const void *dout,
-                                  int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
+ * inputs.  out, lse: what the forward gave.  dout: as q, with its own strides. */
+emb_status emb_attention_backward(const emb_attention *a, const void *out, const float *lse,
+                                  const void *dout, int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
                                   void *dv, float *dbias, void *workspace, size_t workspace_bytes,
                                   void *stream);
 
