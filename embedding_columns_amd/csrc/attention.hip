@@ -499,6 +499,12 @@ struct KeyWalk {
     static constexpr int kWords = KT * TL::CH;                  // of K or V, 16 bytes each
     static constexpr int kBufs = kOwners * 4 * kWords * 16 <= 131072 ? 2 : 1;
     static constexpr int kLds = kOwners * kBufs * 2 * kWords;
+    // Wavefronts per SIMD to build the forward for: two wherever LDS lets two workgroups on
+    // a CU.  That also caps a wavefront at 256 registers, and then the compiler keeps the
+    // accumulators where the rescaling can use them; with the full 512 it puts them in the
+    // other half of the file and moves each of them back and forth in every step (2048-row
+    // sequences, 8 heads of 128: 321 us, against 186 us).
+    static constexpr int kWaves = kLds * 16 <= 72 * 1024 && !(sizeof(T) == 4 && DP == 128) ? 2 : 1;
     static_assert(KT / (WM == 4 ? 4 : 1) >= 64 / TL::CH, "a load covers whole rows of one wavefront's share");
 
     u32x4_t *mine;           // this wavefront's tiles
@@ -634,7 +640,7 @@ __device__ __forceinline__ float log_sum(float m, float l)
 constexpr float kLag = 8.f;
 
 template <typename T, int DP, int WM>
-__global__ __launch_bounds__(kAttnThreads) void attn_forward(AttnArgs A)
+__global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_forward(AttnArgs A)
 {
     using KW = KeyWalk<T, DP, WM>;
     constexpr int SUBS = KW::KT / 32;
@@ -835,7 +841,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 // each row's adding up to zero, would drown in that rounding.  In fp32 D is exact
 // enough for dq, and y is left out.
 template <typename T, int DP, int WM>
-__global__ __launch_bounds__(kAttnThreads) void attn_backward_q(AttnArgs A)
+__global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && DP * sizeof(T) <= 128 ? 2 : 1)) void attn_backward_q(AttnArgs A)
 {
     using KW = KeyWalk<T, DP, WM>;
     using TL = Tile<T, DP>;
@@ -888,8 +894,10 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_q(AttnArgs A)
     for (int d = 0; d < DP / 32; d++) x[d] = y[d] = f32x16_t{};
 
     for (; walk.at < walk.end; walk.leave()) {
+        // no branch around the products, also where a wavefront has no rows (their weights
+        // are zeros): accumulators that live across one are moved between the halves of the
+        // register file at every step
         walk.enter();
-        if (!busy || walk.keep == 0) continue;
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
         Range kr[2];
         if (A.bias) half_ranges(walk.pos, kr[0], kr[1]);
@@ -1012,24 +1020,18 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 
 // ---------------------------------------------------------- backward: keys
 
-// query rows per stage
-template <typename T, int DP>
-constexpr int query_stage()
-{
-    return 32;
-}
-
 // A workgroup owns 128 keys of one key head, 32 a wavefront (one per lane & 31), K
 // and V in registers, and walks all query rows of the sample, one head of the group
-// after the other: dk and dv need no sum across workgroups.
+// after the other, 32 rows a stage: dk and dv need no sum across workgroups.  Rows
+// arrive in LDS a stage ahead, as the keys do in the other kernels.
 template <typename T, int DP>
-__global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
+__global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 128 ? 2 : 1)) void attn_backward_k(AttnArgs A)
 {
     using TL = Tile<T, DP>;
-    constexpr int QT = query_stage<T, DP>();
-    __shared__ u32x4_t lq[QT * TL::CH], ld[QT * TL::CH];
-    __shared__ float first[QT], ndelta[QT];    // - lse / c (or -inf), - delta
-    __shared__ int qpos[QT], qlo[QT / 32], qhi[QT / 32];
+    constexpr int kWords = 32 * TL::CH;
+    __shared__ u32x4_t lds[2][2][kWords];             // [stage & 1][q, dout]
+    __shared__ float first[2][32], ndelta[2][32];     // - lse / c (or -inf), - delta
+    __shared__ int qpos[2][32], qlo[2], qhi[2];
     __shared__ int lbnd[kBucketsMax];
     __shared__ float acc[4][kBucketsMax];
     extern __shared__ float lb[];
@@ -1039,136 +1041,177 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
     const int64_t tile = id % A.tiles;
     const SegTile s = seg_find(A.ko, A.samples, A.nk, 1, 128, tile);
     const bool idle = s.row0 >= s.rows;
-    const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
-    const bool nobody = s.seg == 0 || s.seg == A.samples + 1;
-    int64_t q0 = nobody || idle ? 0 : seg_edge(A.qo, A.samples, A.nq, s.seg);
-    int64_t q1 = nobody || idle ? 0 : seg_edge(A.qo, A.samples, A.nq, s.seg + 1);
     if (idle && !A.dbias_part) return;
+    const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
+    const bool nobody = s.seg == 0 || s.seg == A.samples + 1 || idle;
+    const int64_t q0 = nobody ? 0 : seg_edge(A.qo, A.samples, A.nq, s.seg);
+    const int64_t q1 = nobody ? 0 : seg_edge(A.qo, A.samples, A.nq, s.seg + 1);
+    const int64_t per = q1 > q0 ? (q1 - q0 + 31) / 32 : 0, stages = per * A.group;
 
+    // stage `it`: head it / per of the group, rows from q0 + 32 (it % per)
+    struct Stage {
+        int g;
+        int64_t i, row;
+    };
+    auto after = [&](Stage z) {
+        z.i++;
+        z.row += 32;
+        if (z.row >= q1) {
+            z.row = q0;
+            z.g++;
+        }
+        return z;
+    };
+    auto bring = [&](const Stage &z, int to) {
+        if (z.i >= stages) return;
+        // wavefronts 0 and 1 bring the halves of q, 2 and 3 those of dout
+        const int head = kvh * A.group + z.g, half = (w & 1) * 16;
+        const int64_t row = z.row + half, left = q1 - row;
+        const uint64_t keep = left <= 0 ? 0 : left >= 16 ? 0xFFFF : (1u << left) - 1;
+        const T *p = w < 2 ? static_cast<const T *>(A.q) + head * A.qh + row * A.qs
+                           : static_cast<const T *>(A.dout) + head * A.dh + row * A.ds;
+        bring_rows<T, DP, 16>(p, w < 2 ? A.qs : A.ds, A.dim, A.vec, keep, lds[to][w >> 1], half);
+    };
+    float n_lse = 0.f, n_delta = 0.f;
+    int n_pos = 0;
+    bool n_in = false;
+    auto look = [&](const Stage &z) {       // wavefront 0: what goes with the rows
+        if (z.i >= stages) return;
+        const int64_t row = z.row + (lane & 31);
+        n_in = row < q1;
+        const int64_t at = (n_in ? row : q1 - 1) * A.heads + kvh * A.group + z.g;
+        n_lse = *gp(A.lse + at);
+        n_delta = *gp(A.delta + at);
+        if (A.bias) n_pos = *gp(A.qp + (n_in ? row : q1 - 1));
+    };
+    auto tell = [&](int to) {
+        // a row without keys, and one past the end, start at -inf: weights of zero
+        first[to][lane & 31] = n_in && n_lse != -INFINITY ? -n_lse * kLog2e / A.c : -INFINITY;
+        ndelta[to][lane & 31] = n_in ? -n_delta : 0.f;
+        if (!A.bias) return;
+        qpos[to][lane & 31] = n_pos;
+        Range r, other;
+        half_ranges(n_pos, r, other);
+        qlo[to] = r.lo;
+        qhi[to] = r.hi;
+    };
+
+    Stage now{0, 0, q0}, next = after(now), then = after(next);
+    bring(now, 0);
+    if (w == 0) look(now);
     stage_bias(A, kvh, lb, lbnd);
     for (int i = threadIdx.x; i < 4 * kBucketsMax; i += kAttnThreads) (&acc[0][0])[i] = 0.f;
     const Buckets B = load_buckets(A);
     const int64_t r = s.row0 + 32 * w + (lane & 31);
     const bool in = r < s.rows;
     const int64_t key = s.base + (in ? r : s.rows - 1);
-    const bool busy = !idle && s.row0 + 32 * w < s.rows;
     const bool live = in && !idle && (!A.mask || A.mask[key]);
-    int kpos = 0, klo = 0, khi = 0;
+    int kpos = 0;
+    Range kr{0, 0};
     if (A.bias && !idle) {
         kpos = A.kp[key];
-        Range mine, other;
-        half_ranges(kpos, mine, other);
-        klo = mine.lo;
-        khi = mine.hi;
+        Range other;
+        half_ranges(kpos, kr, other);
     }
     Frag<T, DP> kf, vf;
     load_frag<T, DP>(kf, static_cast<const T *>(A.k) + (live ? key * A.ks + kvh * A.kh : 0), A.dim, A.vec, live);
     load_frag<T, DP>(vf, static_cast<const T *>(A.v) + (live ? key * A.vs + kvh * A.vh : 0), A.dim, A.vec, live);
+    if (w == 0) {
+        tell(0);
+        look(next);
+    }
 
     f32x16_t dk[DP / 32], dv[DP / 32];
 #pragma unroll
     for (int d = 0; d < DP / 32; d++) dk[d] = dv[d] = f32x16_t{};
+    // score gradients of the bucket at hand, a sum per lane until the bucket changes
+    int bucket = 0;
+    float run = 0.f;
+    auto settle = [&](int m, float sum) {
+        sum = wave_sum(sum);
+        if (lane == 0) acc[w][m] += sum;
+    };
 
-    for (int g = 0; g < A.group; g++) {
-        const int head = kvh * A.group + g;
-        const T *q = static_cast<const T *>(A.q) + head * A.qh, *dout = static_cast<const T *>(A.dout) + head * A.dh;
-        for (int64_t qb = q0; qb < q1; qb += QT) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < QT * TL::CH; i += kAttnThreads) {
-                const int rr = i / TL::CH, c = i % TL::CH;
-                u32x4_t a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-                if (qb + rr < q1) {
-                    a = load_chunk(q + (qb + rr) * A.qs, c, A.dim, A.vec);
-                    b = load_chunk(dout + (qb + rr) * A.ds, c, A.dim, A.vec);
+    for (; now.i < stages; now = next, next = then, then = after(then)) {
+        const int cur = (int)(now.i & 1);
+        arrived();
+        __syncthreads();
+        bring(next, cur ^ 1);
+        if (w == 0) {
+            tell(cur ^ 1);
+            look(then);
+        }
+        const u32x4_t *lq = lds[cur][0], *ld = lds[cur][1];
+        {
+            f32x16_t sc = block_order(first[cur]), dp = block_order(ndelta[cur]);
+            products<T, DP>(sc, lq, 0, kf);
+            products<T, DP>(dp, ld, 0, vf);
+            float b = live ? 0.f : -INFINITY, c = A.c;
+            int lo = 0, hi = 0, x[16];
+            if (A.bias) {
+                lo = bucket_of(B, sub_sat(qlo[cur], kr.hi));
+                hi = bucket_of(B, sub_sat(qhi[cur], kr.lo));
+                b += lb[lo * A.group + now.g];
+                if (lo != hi) {
+                    f32x16_t t;
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        x[i] = sub_sat(qpos[cur][block_key(i)], kpos);
+                        t[i] = b;
+                    }
+                    for (int m = lo; m < hi; m++) {
+                        const int edge = lbnd[m];
+                        const float v = live ? lb[(m + 1) * A.group + now.g] : -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i++) sc[i] = fmaf(sc[i], c, t[i]);
+                    c = 1.f;
+                    b = 0.f;
                 }
-                lq[TL::at(rr, c)] = a;
-                ld[TL::at(rr, c)] = b;
             }
-            if (threadIdx.x < QT) {
-                const int t = threadIdx.x;
-                const bool there = qb + t < q1;
-                const int64_t row = (qb + t) * A.heads + head;
-                const float lse = there ? A.lse[row] * kLog2e : -INFINITY;
-                first[t] = lse == -INFINITY ? -INFINITY : -lse / A.c;
-                ndelta[t] = there ? -A.delta[row] : 0.f;
-                if (A.bias) {
-                    const int p = A.qp[there ? qb + t : q1 - 1];
-                    qpos[t] = p;
-                    Range mine, other;
-                    half_ranges(p, mine, other);
-                    if (t == 0) {
-                        qlo[0] = mine.lo;
-                        qhi[0] = mine.hi;
-                    }
-                }
+#pragma unroll
+            for (int i = 0; i < 16; i++) {
+                sc[i] = exp2_fast(fmaf(sc[i], c, b));
+                dp[i] *= sc[i];
             }
-            __syncthreads();
-            if (!busy) continue;
+            const typename Mma<T>::Pack p = Mma<T>::pack(sc), ds = Mma<T>::pack(dp);
 #pragma unroll
-            for (int sub = 0; sub < QT / 32; sub++) {
-                if (qb + sub * 32 >= q1) break;
-                f32x16_t sc = block_order(first + sub * 32), dp = block_order(ndelta + sub * 32);
-                products<T, DP>(sc, lq, sub * 32, kf);
-                products<T, DP>(dp, ld, sub * 32, vf);
-                float b = live ? 0.f : -INFINITY, c = A.c;
-                int lo = 0, hi = 0, x[16];
-                if (A.bias) {
-                    lo = bucket_of(B, sub_sat(qlo[sub], khi));
-                    hi = bucket_of(B, sub_sat(qhi[sub], klo));
-                    b += lb[lo * A.group + g];
-                    if (lo != hi) {
-                        f32x16_t t;
-                        for (int i = 0; i < 16; i++) {
-                            x[i] = sub_sat(qpos[sub * 32 + block_key(i)], kpos);
-                            t[i] = b;
-                        }
-                        for (int m = lo; m < hi; m++) {
-                            const int edge = lbnd[m];
-                            const float v = live ? lb[(m + 1) * A.group + g] : -INFINITY;
+            for (int d = 0; d < DP / 32; d++) {
+                typename Mma<T>::template Rows<DP>(ld, 0, d).times(dv[d], p);
+                typename Mma<T>::template Rows<DP>(lq, 0, d).times(dk[d], ds);
+            }
+            if (A.dbias_part) {
+                if (lo != bucket) {
+                    settle(bucket, run);
+                    bucket = lo;
+                    run = 0.f;
+                }
+                for (int m = lo; m < hi; m++) {
+                    const int edge = lbnd[m];
+                    float sum = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; i++) sc[i] = fmaf(sc[i], c, t[i]);
-                        c = 1.f;
-                        b = 0.f;
+                    for (int i = 0; i < 16; i++) {
+                        const bool below = x[i] < edge;
+                        sum += below ? dp[i] : 0.f;
+                        dp[i] = below ? 0.f : dp[i];
                     }
+                    settle(m, run + sum);
+                    run = 0.f;
                 }
+                bucket = hi;
+                float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    sc[i] = exp2_fast(fmaf(sc[i], c, b));
-                    dp[i] *= sc[i];
-                }
-                const typename Mma<T>::Pack p = Mma<T>::pack(sc), ds = Mma<T>::pack(dp);
-#pragma unroll
-                for (int d = 0; d < DP / 32; d++) {
-                    typename Mma<T>::template Rows<DP>(ld, sub * 32, d).times(dv[d], p);
-                    typename Mma<T>::template Rows<DP>(lq, sub * 32, d).times(dk[d], ds);
-                }
-                if (A.dbias_part) {
-                    for (int m = lo; m <= hi; m++) {
-                        float sum = 0.f;
-                        if (m < hi) {
-                            const int edge = lbnd[m];
-#pragma unroll
-                            for (int i = 0; i < 16; i++) {
-                                const bool below = x[i] < edge;
-                                sum += below ? dp[i] : 0.f;
-                                dp[i] = below ? 0.f : dp[i];
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; i++) sum += dp[i];
-                        }
-                        sum = wave_sum(sum);
-                        if (lane == 0) acc[w][m] += sum;
-                    }
-                }
+                for (int i = 0; i < 16; i++) sum += dp[i];
+                run += sum;
             }
         }
-        if (A.dbias_part) {
+        if (A.dbias_part && next.g != now.g) {       // a head of the group is done
+            settle(bucket, run);
+            run = 0.f;
             __syncthreads();
-            float *to = A.dbias_part + (tile * A.heads + head) * A.buckets;
+            float *to = A.dbias_part + (tile * A.heads + kvh * A.group + now.g) * A.buckets;
             for (int m = threadIdx.x; m < A.buckets; m += kAttnThreads) {
                 to[m] = (acc[0][m] + acc[1][m]) + (acc[2][m] + acc[3][m]);
                 acc[0][m] = acc[1][m] = acc[2][m] = acc[3][m] = 0.f;
@@ -1176,6 +1219,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
             __syncthreads();
         }
     }
+    if (A.dbias_part && stages == 0)
+        for (int i = threadIdx.x; i < A.buckets * A.group; i += kAttnThreads)
+            A.dbias_part[(tile * A.heads + kvh * A.group) * A.buckets + i] = 0.f;
     if (!in || idle || !A.dk) return;
     T *pk = static_cast<T *>(A.dk) + (key * A.kv_heads + kvh) * A.dim;
     T *pv = static_cast<T *>(A.dv) + (key * A.kv_heads + kvh) * A.dim;
@@ -1190,33 +1236,29 @@ __global__ __launch_bounds__(kAttnThreads) void attn_backward_k(AttnArgs A)
                 a[e] = A.scale * dk[d][4 * g + e];
                 b[e] = dv[d][4 * g + e];
             }
-            if (col + 4 <= A.dim && A.dim % 4 == 0) {
-                Mma<T>::store4(pk + col, a);
-                Mma<T>::store4(pv + col, b);
-            } else
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (col + e < A.dim) {
-                        Mma<T>::store1(pk + col + e, a[e]);
-                        Mma<T>::store1(pv + col + e, b[e]);
-                    }
+            store_part(pk, col, A.dim, a);
+            store_part(pv, col, A.dim, b);
         }
 }
 
 // dbias[m, head] = sum of the workgroups' parts, in a fixed order: a workgroup per
-// (head, 64 buckets), four tiles side by side
-__global__ __launch_bounds__(kAttnThreads) void attn_join_bias(AttnArgs A, float *dbias)
+// (head, 32 buckets), 32 tiles side by side
+constexpr int kBiasJoin = 1024;
+__global__ __launch_bounds__(kBiasJoin) void attn_join_bias(AttnArgs A, float *dbias)
 {
-    __shared__ float part[4][64];
-    const int head = blockIdx.x, lane = lane_id(), w = threadIdx.x >> 6;
-    const int m = blockIdx.y * 64 + lane;
+    __shared__ float part[32][32];
+    const int head = blockIdx.x, t = threadIdx.x & 31, g = threadIdx.x >> 5;
+    const int m = blockIdx.y * 32 + t, mc = m < A.buckets ? m : A.buckets - 1;
     float sum = 0.f;
-    if (m < A.buckets)
-        for (int64_t t = w; t < A.tiles; t += 4) sum += A.dbias_part[(t * A.heads + head) * A.buckets + m];
-    part[w][lane] = sum;
+#pragma unroll 8
+    for (int64_t u = g; u < A.tiles; u += 32) sum += *gp(A.dbias_part + (u * A.heads + head) * A.buckets + mc);
+    part[g][t] = sum;
     __syncthreads();
-    if (w == 0 && m < A.buckets)
-        dbias[(int64_t)m * A.heads + head] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if (g != 0 || m >= A.buckets) return;
+    sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < 32; u++) sum += part[u][t];
+    dbias[(int64_t)m * A.heads + head] = sum;
 }
 
 }  // namespace emb
@@ -1396,7 +1438,8 @@ emb_status backward_run(const AttnArgs &A0, const AttnPlan &p, float *dbias, hip
     if (A.dk || dbias)
         hipLaunchKernelGGL((attn_backward_k<T, DP>), dim3((unsigned)(p.key_tiles * A.kv_heads)), block, lds, st, A);
     if (dbias)
-        hipLaunchKernelGGL(attn_join_bias, dim3((unsigned)A.heads, (unsigned)((A.buckets + 63) / 64)), block, 0, st, A,
+        hipLaunchKernelGGL(attn_join_bias, dim3((unsigned)A.heads, (unsigned)((A.buckets + 31) / 32)),
+                           dim3(kBiasJoin), 0, st, A,
                            dbias);
     return launched("attention backward");
 }
