@@ -127,9 +127,9 @@ _SIGS = {
     "emb_table_load": [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _VP, _VP],
     "emb_attention_query": [C.POINTER(AttentionDesc), C.POINTER(C.c_size_t),
                             C.POINTER(C.c_size_t)],
-    "emb_attention_forward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, C.c_size_t, _VP],
-    "emb_attention_backward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP,
-                               _VP, C.c_size_t, _VP],
+    "emb_attention_forward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
+    "emb_attention_backward": [C.POINTER(AttentionDesc), _VP, _VP, _VP, _VP, _I64, _I64, _VP, _VP,
+                               _VP, _VP, _VP, C.c_size_t, _VP],
     "emb_recurrence_query": [C.POINTER(RecurrenceDesc), C.POINTER(_I64), C.POINTER(C.c_size_t)],
     "emb_recurrence_forward": [C.POINTER(RecurrenceDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
     "emb_recurrence_backward": [C.POINTER(RecurrenceDesc), _VP, _VP, _VP, _VP, _VP, _VP, _VP,
@@ -359,15 +359,15 @@ def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def emb_attention_forward(desc, out, lse=None, workspace=None, stream=None):
-    _check(lib().emb_attention_forward(C.byref(desc), _ptr(out), _ptr(lse), _ptr(workspace),
-                                       _bytes(workspace), _stream(stream)))
+def emb_attention_forward(desc, out, rest=None, lse=None, workspace=None, stream=None):
+    _check(lib().emb_attention_forward(C.byref(desc), _ptr(out), _ptr(rest), _ptr(lse),
+                                       _ptr(workspace), _bytes(workspace), _stream(stream)))
 
 
-def emb_attention_backward(desc, out, lse, dout, dq, dk=None, dv=None, dbias=None, workspace=None,
+def emb_attention_backward(desc, out, rest, lse, dout, dq, dk=None, dv=None, dbias=None, workspace=None,
                            stream=None):
-    _check(lib().emb_attention_backward(C.byref(desc), _ptr(out), _ptr(lse), _rows_ptr(dout, 3),
-                                        dout.stride(0), dout.stride(1), _ptr(dq), _ptr(dk),
+    _check(lib().emb_attention_backward(C.byref(desc), _ptr(out), _ptr(rest), _ptr(lse),
+                                        _rows_ptr(dout, 3), dout.stride(0), dout.stride(1), _ptr(dq), _ptr(dk),
                                         _ptr(dv), _ptr(dbias), _ptr(workspace), _bytes(workspace),
                                         _stream(stream)))
 
@@ -754,16 +754,17 @@ class CrossAttention(torch.autograd.Function):
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         need, ctx.need = emb_attention_query(desc)
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        emb_attention_forward(desc, out, lse, ws)
+        rest = torch.empty_like(out) if q.dtype == torch.bfloat16 else None
+        emb_attention_forward(desc, out, rest, lse, ws)
         ctx.save_for_backward(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos,
-                              out, lse)
+                              out, rest, lse)
         ctx.scale = scale
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, out, lse = (
+        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, out, rest, lse = (
             ctx.saved_tensors)
         desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
                                ctx.scale)
@@ -780,7 +781,7 @@ class CrossAttention(torch.autograd.Function):
         if bias is not None and want_bias:
             dbias = torch.empty(bias.shape, dtype=torch.float32, device=q.device)
         ws = torch.empty(ctx.need, dtype=torch.uint8, device=q.device) if ctx.need else None
-        emb_attention_backward(desc, out, lse, dout, dq, dk, dv, dbias, ws)
+        emb_attention_backward(desc, out, rest, lse, dout, dq, dk, dv, dbias, ws)
         return (dq, dk, dv, dbias) + (None,) * 7
 
 
@@ -804,7 +805,7 @@ def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundar
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     need = emb_attention_query(desc)[0]
     ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    emb_attention_forward(desc, out, None, ws)
+    emb_attention_forward(desc, out, None, None, ws)
     return out
 
 

@@ -47,7 +47,7 @@ struct AttnArgs {
     int32_t vec, ovec;                          // rows (of out) can be read 16 bytes at a time
     int32_t splits;
     int64_t tiles;
-    void *out;                                  // [n_q, heads, dim]
+    void *out, *rest;                           // [n_q, heads, dim]; what rounding out left, or NULL
     float *lse;                                 // [n_q, heads]
     float *part, *part_ml;                      // split partials
     void *dq, *dk, *dv;
@@ -77,6 +77,20 @@ struct Tile {
     static constexpr int CH = DP / E;                // chunks per row
     static __device__ __forceinline__ int at(int r, int c) { return r * CH + (c ^ swizzle<CH>(r)); }
 };
+
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p);
+}
+
+// LDS addresses of a tile: the lane's part is one number, and chunk and row of a read
+// come in as a constant xor and a constant offset (the swizzle is a xor of row bits, and
+// tiles are aligned to a row).  So a read costs one xor and no register that outlives it.
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at)
+{
+    return *(__attribute__((address_space(3))) const V *)(uintptr_t)at;
+}
 
 // a row as a second operand: its even chunks in half 0, its odd ones in half 1
 template <typename T, int DP>
@@ -128,23 +142,23 @@ struct Mma<uint16_t> {
             for (int j = 0; j < 4; j++) r.w[kc][j] = bf16x2_rne(p[8 * kc + 2 * j], p[8 * kc + 2 * j + 1]);
         return r;
     }
-    // 32 rows of a tile from r0, elements 32 db .. of each, transposed, as first operand:
-    // times(): acc[d, lane] += sum over the block's 32 keys of tile[key, d] w[key, lane]
+    // 32 rows of a tile from r0 (a multiple of 32), elements 32 db .. of each, transposed, as
+    // first operand: times(): acc[d, lane] += sum over the 32 rows of tile[row, d] w[row, lane]
     template <int DP>
     struct Rows {
         s16x8_t a[2];
         __device__ __forceinline__ Rows(const u32x4_t *tile, int r0, int db)
         {
             using TL = Tile<uint16_t, DP>;
-            const int l = lane_id(), h = l >> 5;
+            // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
+            const int l = lane_id(), row = 4 * (l >> 5) + ((l & 15) >> 2), col = 16 * ((l >> 4) & 1) + 4 * (l & 3);
+            const uint32_t base = lds_address(tile) + 16 * TL::at(row, col >> 3) + (col & 7) * 2;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
                 const int kc = j >> 1, jb = j & 1;
-                const int row = r0 + 16 * kc + 8 * jb + 4 * h + ((l & 15) >> 2);
-                const int col = 32 * db + 16 * ((l >> 4) & 1) + 4 * (l & 3);
-                const char *p = reinterpret_cast<const char *>(tile + TL::at(row, col >> 3)) + (col & 7) * 2;
+                const uint32_t at = (base ^ ((4 * db) ^ swizzle<TL::CH>(8 * jb)) << 4) + (r0 + 16 * kc + 8 * jb) * TL::CH * 16;
                 const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t *)(p));
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)at);
 #pragma unroll
                 for (int e = 0; e < 4; e++) a[kc][4 * jb + e] = v[e];
             }
@@ -189,11 +203,12 @@ struct Mma<float> {
         __device__ __forceinline__ Rows(const u32x4_t *tile, int r0, int db)
         {
             using TL = Tile<float, DP>;
-            const int l = lane_id(), h = l >> 5, d = 32 * db + (l & 31);
+            const int l = lane_id(), h = l >> 5, d = l & 31;
+            const uint32_t base = lds_address(tile) + 16 * TL::at(4 * h, d >> 2) + (d & 3) * 4;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                const int row = r0 + 8 * (i >> 2) + 4 * h + (i & 3);
-                a[i] = reinterpret_cast<const float *>(tile + TL::at(row, d >> 2))[d & 3];
+                const int row = 8 * (i >> 2) + (i & 3);
+                a[i] = lds_read<float>((base ^ ((8 * db) ^ swizzle<TL::CH>(row)) << 4) + (r0 + row) * TL::CH * 16);
             }
         }
         __device__ __forceinline__ void times(f32x16_t &acc, const Pack &w) const
@@ -223,10 +238,24 @@ __device__ __forceinline__ void products(f32x16_t &acc, const u32x4_t *tile, int
                                          const Frag<T, DP> &b)
 {
     using TL = Tile<T, DP>;
-    const int l = lane_id(), h = l >> 5;
+    const int l = lane_id();
+    const uint32_t base = lds_address(tile + r0 * TL::CH) + 16 * TL::at(l & 31, l >> 5);
+#pragma unroll
+    for (int c = 0; c < TL::CH / 2; c++) Mma<T>::chunk(acc, lds_read<u32x4_t>(base ^ (c << 5)), b[c]);
+}
+
+// The same with the second operands' rows in a tile too: twice the LDS reads, but none
+// of the registers.
+template <typename T, int DP>
+__device__ __forceinline__ void products(f32x16_t &acc, const u32x4_t *tile, int r0, const u32x4_t *other, int o0)
+{
+    using TL = Tile<T, DP>;
+    const int l = lane_id();
+    const uint32_t mine = 16 * TL::at(l & 31, l >> 5);
+    const uint32_t a = lds_address(tile + r0 * TL::CH) + mine, b = lds_address(other + o0 * TL::CH) + mine;
 #pragma unroll
     for (int c = 0; c < TL::CH / 2; c++)
-        Mma<T>::chunk(acc, tile[TL::at(r0 + (l & 31), 2 * c + h)], b[c]);
+        Mma<T>::chunk(acc, lds_read<u32x4_t>(a ^ (c << 5)), lds_read<u32x4_t>(b ^ (c << 5)));
 }
 
 // 16 values of a 32-entry array in the order of a block's registers
@@ -354,11 +383,6 @@ __device__ __forceinline__ i32x4_t row_rsrc(const void *base)
     r[3] = kBufFlags;
     return r;
 }
-__device__ __forceinline__ uint32_t lds_address(const void *p)
-{
-    return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p);
-}
-
 // Brings ROWS rows (of `rows` that begin at element pointer `base`, `stride` elements
 // apart) into a tile's rows r0 .., by one wavefront; row r whose bit in `keep` is clear
 // becomes zeros and is not read.  Masked rows have to be zeros: a probability of zero
@@ -499,7 +523,7 @@ struct KeyWalk {
     static constexpr int kWords = KT * TL::CH;                  // of K or V, 16 bytes each
     static constexpr int kBufs = kOwners * 4 * kWords * 16 <= 131072 ? 2 : 1;
     static constexpr int kLds = kOwners * kBufs * 2 * kWords;
-    // Wavefronts per SIMD to build the forward for: two wherever LDS lets two workgroups on
+    // Wavefronts per SIMD to build for: two wherever LDS lets two workgroups on
     // a CU.  That also caps a wavefront at 256 registers, and then the compiler keeps the
     // accumulators where the rescaling can use them; with the full 512 it puts them in the
     // other half of the file and moves each of them back and forth in every step (2048-row
@@ -626,6 +650,18 @@ __device__ __forceinline__ void store_part(T *row, int col, int dim, const float
             if (col + e < dim) Mma<T>::store1(row + col + e, v[e]);
 }
 
+// ... of the output, with what the rounding leaves of each element beside it
+template <typename T>
+__device__ __forceinline__ void store_out(const AttnArgs &A, int64_t row, int col, const float *v)
+{
+    store_part(static_cast<T *>(A.out) + row * A.dim, col, A.dim, v);
+    if (sizeof(T) == 4 || !A.rest) return;
+    float r[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) r[e] = v[e] - bf16_lo(bf16_rne(v[e]));
+    store_part(static_cast<T *>(A.rest) + row * A.dim, col, A.dim, r);
+}
+
 // 1 / l, zero for a row without keys; NaN stays
 __device__ __forceinline__ float inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
 __device__ __forceinline__ float log_sum(float m, float l)
@@ -644,7 +680,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
 {
     using KW = KeyWalk<T, DP, WM>;
     constexpr int SUBS = KW::KT / 32;
-    __shared__ u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];    // 16 KB for sum_waves
+    __shared__ __align__(1024) u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];    // 16 KB for sum_waves
     __shared__ int lbnd[kBucketsMax];
     __shared__ int kpos[4][32];
     __shared__ float kout[4][32];
@@ -738,7 +774,6 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     l = both_halves_sum(l);
     const int64_t row = R.q * A.heads + R.head;
     const int64_t at = (int64_t)split * A.nq * A.heads + row;
-    T *out = static_cast<T *>(A.out) + row * A.dim;
 
     if (WM == 1) {
         // the four wavefronts' parts of the same rows, scaled to a common maximum
@@ -768,7 +803,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
 #pragma unroll
             for (int e = 0; e < 4; e++) r[d][e] *= f2;
             if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, r[d]);
-            else store_part(out, col, A.dim, r[d]);
+            else store_out<T>(A, row, col, r[d]);
         }
         m = mt;
         l = lt;
@@ -785,7 +820,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
 #pragma unroll
                 for (int e = 0; e < 4; e++) v[e] = o[d][4 * g + e] * f2;
                 if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, v);
-                else store_part(out, col, A.dim, v);
+                else store_out<T>(A, row, col, v);
             }
     }
     if (h != 0) return;
@@ -825,28 +860,31 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
     o = 0.f;
 #pragma unroll
     for (int u = 0; u < G; u++) o += so[u][d];
-    if (d < A.dim) Mma<T>::store1(static_cast<T *>(A.out) + row * A.dim + d, o * inverse(l));
+    o *= inverse(l);
+    if (d < A.dim) {
+        Mma<T>::store1(static_cast<T *>(A.out) + row * A.dim + d, o);
+        if (sizeof(T) == 2 && A.rest)
+            Mma<T>::store1(static_cast<T *>(A.rest) + row * A.dim + d, o - bf16_lo(bf16_rne(o)));
+    }
     if (d == 0 && A.lse) A.lse[row] = log_sum(m, l);
 }
 
 // ------------------------------------------------------- backward: queries
 
-// dq_i = scale sum_j p_ij (dP_ij - delta_i) k_j.  One pass over the keys takes three sums,
-//   x_i = sum_j p_ij (dP_ij - D_i) k_j,  y_i = sum_j p_ij k_j,  e_i = sum_j p_ij (dP_ij - D_i),
-// with D_i = o_i.dO_i, which is delta_i up to the rounding of the output and of the
-// probabilities that made it: delta = D + e, dq = scale (x - e y).  Score gradients of
-// nearly the right offset keep x exact to one rounding; y is a fourth product and
-// corrects the rest.  Without it dq of bf16 inputs is off by the output's rounding
-// times |y|, and without e the bias gradient, a sum of score gradients over many rows,
-// each row's adding up to zero, would drown in that rounding.  In fp32 D is exact
-// enough for dq, and y is left out.
+// dq_i = scale sum_j p_ij (dP_ij - D_i) k_j with D_i = o_i.dO_i, and along with it
+// delta_i = D_i + sum_j p_ij (dP_ij - D_i), which the gradients of keys and bias use.
+// D is delta up to the rounding of the probabilities that made the output (the output's
+// own rounding is put back, from `rest`).  dq needs no more; but the bias gradient is
+// a sum of score gradients over many rows, each row's adding up to zero, and would drown
+// in that rounding: taken again from the probabilities in fp32, delta costs one addition
+// a pair.  (Correcting dq for it too, by sum_j p_ij k_j, would be a fourth product.)
 template <typename T, int DP, int WM>
-__global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && DP * sizeof(T) <= 128 ? 2 : 1)) void attn_backward_q(AttnArgs A)
+__global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_backward_q(AttnArgs A)
 {
     using KW = KeyWalk<T, DP, WM>;
     using TL = Tile<T, DP>;
     constexpr int SUBS = KW::KT / 32;
-    __shared__ u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];
+    __shared__ __align__(1024) u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];
     __shared__ int lbnd[kBucketsMax];
     __shared__ int kpos[4][32];
     __shared__ float jd[4][32];
@@ -880,6 +918,11 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && D
         load_frag<T, DP>(of, static_cast<const T *>(A.out) + row * A.dim, A.dim, A.ovec, R.live);
 #pragma unroll
         for (int c = 0; c < TL::CH / 2; c++) D += Mma<T>::dot(of[c], df[c]);
+        if (sizeof(T) == 2) {
+            load_frag<T, DP>(of, static_cast<const T *>(A.rest) + row * A.dim, A.dim, A.ovec, R.live);
+#pragma unroll
+            for (int c = 0; c < TL::CH / 2; c++) D += Mma<T>::dot(of[c], df[c]);
+        }
         D = both_halves_sum(D);
     }
     // a row without keys has lse = -inf: exp2(score - inf) keeps its weights zero
@@ -887,11 +930,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && D
     if (lse == -INFINITY) lse = INFINITY;
     if (WM == 1) __syncthreads();
 
-    constexpr bool kWithY = sizeof(T) == 2;
-    float e = 0.f;
-    f32x16_t x[DP / 32], y[DP / 32];
+    float e = 0.f;                         // sum p (dP - D)
+    f32x16_t x[DP / 32];
 #pragma unroll
-    for (int d = 0; d < DP / 32; d++) x[d] = y[d] = f32x16_t{};
+    for (int d = 0; d < DP / 32; d++) x[d] = f32x16_t{};
 
     for (; walk.at < walk.end; walk.leave()) {
         // no branch around the products, also where a wavefront has no rows (their weights
@@ -925,13 +967,9 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && D
                 dp[i] *= sc[i];
                 e += dp[i];
             }
-            const typename Mma<T>::Pack ds = Mma<T>::pack(dp), p = Mma<T>::pack(sc);
+            const typename Mma<T>::Pack ds = Mma<T>::pack(dp);
 #pragma unroll
-            for (int d = 0; d < DP / 32; d++) {
-                const typename Mma<T>::template Rows<DP> kt(lk, u * 32, d);
-                kt.times(x[d], ds);
-                if (kWithY) kt.times(y[d], p);
-            }
+            for (int d = 0; d < DP / 32; d++) typename Mma<T>::template Rows<DP>(lk, u * 32, d).times(x[d], ds);
         }
     }
     e = both_halves_sum(e);
@@ -939,22 +977,17 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && D
     T *dq = static_cast<T *>(A.dq) + row * A.dim;
     if (WM == 1) {
         if (h == 0) jd[w][lane & 31] = e;
-        float rx[DP / 32][4], ry[DP / 32][4];
-        sum_waves<DP>(reinterpret_cast<float *>(lds), x, w, rx);
-        if (kWithY) sum_waves<DP>(reinterpret_cast<float *>(lds), y, w, ry);
+        float r[DP / 32][4];
+        sum_waves<DP>(reinterpret_cast<float *>(lds), x, w, r);
         e = (jd[0][lane & 31] + jd[1][lane & 31]) + (jd[2][lane & 31] + jd[3][lane & 31]);
         if (!R.live) return;
 #pragma unroll
         for (int d = 0; d < DP / 32; d++) {
             const int col = 32 * d + 8 * w + 4 * h;
-            if (A.splits > 1) {
-                Mma<float>::store4(A.part + 2 * at * DP + col, rx[d]);
-                if (kWithY) Mma<float>::store4(A.part + (2 * at + 1) * DP + col, ry[d]);
-                continue;
-            }
 #pragma unroll
-            for (int i = 0; i < 4; i++) rx[d][i] = A.scale * (kWithY ? rx[d][i] - e * ry[d][i] : rx[d][i]);
-            store_part(dq, col, A.dim, rx[d]);
+            for (int i = 0; i < 4; i++) r[d][i] *= A.scale;
+            if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, r[d]);
+            else store_part(dq, col, A.dim, r[d]);
         }
         if (w != 0) return;
     } else {
@@ -964,20 +997,11 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves == 2 && D
 #pragma unroll
             for (int g = 0; g < 4; g++) {
                 const int col = 32 * d + 8 * g + 4 * h;
-                float v[4], z[4];
+                float v[4];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    v[i] = x[d][4 * g + i];
-                    z[i] = y[d][4 * g + i];
-                }
-                if (A.splits > 1) {
-                    Mma<float>::store4(A.part + 2 * at * DP + col, v);
-                    if (kWithY) Mma<float>::store4(A.part + (2 * at + 1) * DP + col, z);
-                    continue;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[i] = A.scale * (kWithY ? v[i] - e * z[i] : v[i]);
-                store_part(dq, col, A.dim, v);
+                for (int i = 0; i < 4; i++) v[i] = A.scale * x[d][4 * g + i];
+                if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, v);
+                else store_part(dq, col, A.dim, v);
             }
     }
     if (h != 0) return;
@@ -993,28 +1017,20 @@ template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 {
     constexpr int G = kAttnThreads / DP;
-    constexpr bool kWithY = sizeof(T) == 2;
-    __shared__ float so[2][G][DP];
+    __shared__ float so[G][DP];
     const int64_t row = blockIdx.x, n = A.nq * A.heads;
     const int t = threadIdx.x, d = t % DP, g = t / DP;
-    float x = 0.f, y = 0.f, e = 0.f;
-#pragma unroll 4
-    for (int u = g; u < A.splits; u += G) {
-        x += A.part[2 * (u * n + row) * DP + d];
-        if (kWithY) y += A.part[(2 * (u * n + row) + 1) * DP + d];
-    }
-    so[0][g][d] = x;
-    so[1][g][d] = y;
+    float x = 0.f, e = 0.f;
+#pragma unroll 8
+    for (int u = g; u < A.splits; u += G) x += A.part[(u * n + row) * DP + d];
+    so[g][d] = x;
     __syncthreads();
     if (g != 0) return;
-    x = y = 0.f;
+    x = 0.f;
 #pragma unroll
-    for (int u = 0; u < G; u++) {
-        x += so[0][u][d];
-        y += so[1][u][d];
-    }
+    for (int u = 0; u < G; u++) x += so[u][d];
     for (int u = 0; u < A.splits; u++) e += A.part_ml[2 * (u * n + row) + 1];
-    if (d < A.dim) Mma<T>::store1(static_cast<T *>(A.dq) + row * A.dim + d, A.scale * (kWithY ? x - e * y : x));
+    if (d < A.dim) Mma<T>::store1(static_cast<T *>(A.dq) + row * A.dim + d, x);
     if (d == 0) A.delta[row] = A.part_ml[2 * row] + e;
 }
 
@@ -1024,12 +1040,16 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 // and V in registers, and walks all query rows of the sample, one head of the group
 // after the other, 32 rows a stage: dk and dv need no sum across workgroups.  Rows
 // arrive in LDS a stage ahead, as the keys do in the other kernels.
+// Rows of 256 bytes leave V in LDS: with V in registers too they would need more than
+// 256, and past those the accumulators move back and forth (see KeyWalk::kWaves).
 template <typename T, int DP>
-__global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 128 ? 2 : 1)) void attn_backward_k(AttnArgs A)
+__global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void attn_backward_k(AttnArgs A)
 {
     using TL = Tile<T, DP>;
+    constexpr bool kSpill = DP * sizeof(T) == 256;
+    __shared__ __align__(1024) u32x4_t lvk[kSpill ? 128 * TL::CH : 1];
     constexpr int kWords = 32 * TL::CH;
-    __shared__ u32x4_t lds[2][2][kWords];             // [stage & 1][q, dout]
+    __shared__ __align__(1024) u32x4_t lds[2][2][kWords];             // [stage & 1][q, dout]
     __shared__ float first[2][32], ndelta[2][32];     // - lse / c (or -inf), - delta
     __shared__ int qpos[2][32], qlo[2], qhi[2];
     __shared__ int lbnd[kBucketsMax];
@@ -1116,6 +1136,11 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 128 ? 2 : 1)) void
     Frag<T, DP> kf, vf;
     load_frag<T, DP>(kf, static_cast<const T *>(A.k) + (live ? key * A.ks + kvh * A.kh : 0), A.dim, A.vec, live);
     load_frag<T, DP>(vf, static_cast<const T *>(A.v) + (live ? key * A.vs + kvh * A.vh : 0), A.dim, A.vec, live);
+    if (kSpill) {
+#pragma unroll
+        for (int c = 0; c < TL::CH / 2; c++) lvk[TL::at(32 * w + (lane & 31), 2 * c + h)] = vf[c];
+        wave_sync();
+    }
     if (w == 0) {
         tell(0);
         look(next);
@@ -1145,7 +1170,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 128 ? 2 : 1)) void
         {
             f32x16_t sc = block_order(first[cur]), dp = block_order(ndelta[cur]);
             products<T, DP>(sc, lq, 0, kf);
-            products<T, DP>(dp, ld, 0, vf);
+            if (kSpill) products<T, DP>(dp, ld, 0, lvk, 32 * w);
+            else products<T, DP>(dp, ld, 0, vf);
             float b = live ? 0.f : -INFINITY, c = A.c;
             int lo = 0, hi = 0, x[16];
             if (A.bias) {
@@ -1308,7 +1334,7 @@ size_t backward_workspace(const emb_attention *a, const AttnPlan &p)
     size_t n = pad256((size_t)a->n_q * a->heads * 4);
     if (p.splits > 1) {
         const size_t rows = (size_t)p.splits * a->n_q * a->heads;
-        n += pad256(rows * padded_dim(a->dim) * 8) + pad256(rows * 8);
+        n += pad256(rows * padded_dim(a->dim) * 4) + pad256(rows * 8);
     }
     if (a->buckets) n += pad256((size_t)p.key_tiles * a->heads * a->buckets * 4);
     return n;
@@ -1465,16 +1491,17 @@ extern "C" emb_status emb_attention_query(const emb_attention *a, size_t *forwar
     return EMB_OK;
 }
 
-extern "C" emb_status emb_attention_forward(const emb_attention *a, void *out, float *lse, void *workspace,
-                                            size_t workspace_bytes, void *stream)
+extern "C" emb_status emb_attention_forward(const emb_attention *a, void *out, void *rest, float *lse,
+                                            void *workspace, size_t workspace_bytes, void *stream)
 {
     emb_status s = attn_check(a);
     if (s == EMB_OK) s = attn_pointers(a);
     if (s != EMB_OK) return s;
     if (a->n_q == 0) return EMB_OK;
     const size_t el = a->dtype == EMB_BF16 ? 2 : 4;
-    if (!out || !aligned(out, a->dim % 4 == 0 ? 4 * el : el) || !aligned(lse, 4))
-        return fail(EMB_ERR_INVALID_ARG, "attention: out must be given and aligned to four elements");
+    const size_t al = a->dim % 4 == 0 ? 4 * el : el;
+    if (!out || !aligned(out, al) || !aligned(rest, al) || !aligned(lse, 4))
+        return fail(EMB_ERR_INVALID_ARG, "attention: out must be given, out and rest aligned to four elements");
     const AttnPlan p = attn_plan(a);
     if (!grid_fits(a, p)) return fail(EMB_ERR_UNSUPPORTED, "attention: more than 2^31 - 1 workgroups");
     const size_t need = forward_workspace(a, p);
@@ -1482,6 +1509,7 @@ extern "C" emb_status emb_attention_forward(const emb_attention *a, void *out, f
         return fail(EMB_ERR_WORKSPACE, "attention: the workspace is smaller than the query returned, or not 256-byte aligned");
     AttnArgs A = attn_args(a, p);
     A.out = out;
+    A.rest = rest;
     A.lse = lse;
     if (need) {
         A.part = static_cast<float *>(workspace);
@@ -1499,7 +1527,7 @@ extern "C" emb_status emb_attention_forward(const emb_attention *a, void *out, f
                       : forward_run<float, 128>(A, p, st);
 }
 
-extern "C" emb_status emb_attention_backward(const emb_attention *a, const void *out, const float *lse, const void *dout,
+extern "C" emb_status emb_attention_backward(const emb_attention *a, const void *out, const void *rest, const float *lse, const void *dout,
                                              int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
                                              void *dv, float *dbias, void *workspace, size_t workspace_bytes,
                                              void *stream)
@@ -1511,9 +1539,11 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const void 
     const size_t al = a->dim % 4 == 0 ? 4 * el : el;
     if (a->n_q && (!out || !lse || !dout || !dq))
         return fail(EMB_ERR_INVALID_ARG, "attention: out, lse, dout and dq must be given");
+    if (a->n_q && a->dtype == EMB_BF16 && !rest)
+        return fail(EMB_ERR_INVALID_ARG, "attention: the bf16 backward needs rest");
     if (!dk != !dv) return fail(EMB_ERR_INVALID_ARG, "attention: dk and dv are given together");
     if (dbias && !a->buckets) return fail(EMB_ERR_INVALID_ARG, "attention: dbias without a bias");
-    if (!aligned(dout, el) || !aligned(out, el) || !aligned(dq, al) || !aligned(dk, al) || !aligned(dv, al) || !aligned(lse, 4) ||
+    if (!aligned(dout, el) || !aligned(out, el) || !aligned(rest, el) || !aligned(dq, al) || !aligned(dk, al) || !aligned(dv, al) || !aligned(lse, 4) ||
         !aligned(dbias, 4))
         return fail(EMB_ERR_INVALID_ARG, "attention: gradients must be aligned to four elements");
     if (dout_stride < 0 || dout_head_stride < 0) return fail(EMB_ERR_INVALID_ARG, "attention: strides must be >= 0");
@@ -1528,7 +1558,8 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const void 
     A.dh = dout_head_stride;
     A.vec = A.vec && wide_rows(dout, dout_stride, dout_head_stride, a->dim, el);
     A.out = const_cast<void *>(out);
-    A.ovec = wide_rows(out, a->dim, a->dim, a->dim, el);
+    A.rest = const_cast<void *>(rest);
+    A.ovec = wide_rows(out, a->dim, a->dim, a->dim, el) && wide_rows(rest, a->dim, a->dim, a->dim, el);
     A.lse = const_cast<float *>(lse);
     A.dq = dq;
     A.dk = dk;
@@ -1539,7 +1570,7 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const void 
     if (p.splits > 1) {
         const size_t rows = (size_t)p.splits * a->n_q * a->heads;
         A.part = reinterpret_cast<float *>(ws);
-        ws += pad256(rows * padded_dim(a->dim) * 8);
+        ws += pad256(rows * padded_dim(a->dim) * 4);
         A.part_ml = reinterpret_cast<float *>(ws);
         ws += pad256(rows * 8);
     }

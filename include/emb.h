@@ -459,17 +459,18 @@ typedef struct emb_attention {   /* host */
 emb_status emb_attention_query(const emb_attention *a, size_t *forward_bytes /* host */,
                                size_t *backward_bytes /* host */);
 
-/* out: [n_q, heads, dim] contiguous, aligned to four elements.  lse: [n_q, heads], the
- * natural logarithm of each row's sum of exponentials, which the backward needs, or
- * NULL.  workspace: 256-byte aligned, or NULL when the query says 0 bytes. */
-emb_status emb_attention_forward(const emb_attention *a, void *out, float *lse, void *workspace,
-                                 size_t workspace_bytes, void *stream);
+/* out: [n_q, heads, dim] contiguous, aligned to four elements.  For the backward, or
+ * NULL: rest, as out, what rounding out to bf16 left of each element (EMB_BF16 only);
+ * lse: [n_q, heads], the natural logarithm of each row's sum of exponentials.
+ * workspace: 256-byte aligned, or NULL when the query says 0 bytes. */
+emb_status emb_attention_forward(const emb_attention *a, void *out, void *rest, float *lse,
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /* dq: [n_q, heads, dim]; dk, dv: [n_k, kv_heads, dim] (both, or both NULL); dbias: fp32
  * [buckets, heads] or NULL.  All contiguous, overwritten, and the same bits for the same
- * inputs.  out, lse: what the forward gave.  dout: as q, with its own strides. */
-emb_status emb_attention_backward(const emb_attention *a, const void *out, const float *lse,
-                                  const void *dout, int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
+ * inputs.  out, rest (NULL for EMB_F32), lse: what the forward gave.  dout: as q, with its own strides. */
+emb_status emb_attention_backward(const emb_attention *a, const void *out, const void *rest,
+                                  const float *lse, const void *dout, int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
                                   void *dv, float *dbias, void *workspace, size_t workspace_bytes,
                                   void *stream);
 
