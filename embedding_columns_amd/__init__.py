@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -182,7 +183,13 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's handle without building a Stream object (1/20 of the time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -662,6 +669,13 @@ class KeyedTable:
 
 _SEQ_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 
+# The descriptors above as one packed record: half the time of a ctypes constructor,
+# and these calls can be as short as the kernels they start.
+_ATTENTION = struct.Struct("6if i 2q 3Q 6q 7Q")
+_RECURRENCE = struct.Struct("4i q 2Q 2q 3Q")
+assert _ATTENTION.size == C.sizeof(AttentionDesc)
+assert _RECURRENCE.size == C.sizeof(RecurrenceDesc)
+
 
 def _rows_ptr(t, ndim):
     """Address of a tensor whose last dimension is contiguous (the others may be strided)."""
@@ -671,18 +685,18 @@ def _rows_ptr(t, ndim):
         raise ValueError("the sequence operators run on the GPU: pass device tensors")
     if t.dim() != ndim:
         raise ValueError(f"expected {ndim} dimensions, got shape {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError("the last dimension must be contiguous")
     return t.data_ptr()
 
 
 def _want(t, name, dtype, shape, device):
-    """Address of a contiguous tensor of exactly this type and shape; None for None."""
+    """Address of a contiguous tensor of exactly this type and shape; 0 for None."""
     if t is None:
-        return None
+        return 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: expected {dtype} {shape} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     if not t.is_contiguous():
@@ -690,57 +704,70 @@ def _want(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-def _same(first, others):
-    if first.dtype not in _SEQ_DTYPE:
-        raise ValueError(f"the sequence operators take float32 or bfloat16, got {first.dtype}")
+def _same(first, *others):
+    dtype, device = first.dtype, first.device
+    if dtype not in _SEQ_DTYPE:
+        raise ValueError(f"the sequence operators take float32 or bfloat16, got {dtype}")
     for t in others:
-        if t.dtype != first.dtype or t.device != first.device:
+        if t.dtype is not dtype or t.device != device:
             raise ValueError("tensors of one call must share their type and device")
-    if first.device.index != torch.cuda.current_device():
+    if device.index != torch.cuda.current_device():
         raise ValueError("tensors must be on the current device")
+    return device
 
 
 def _offsets_ptr(t, name, device):
     if t.dim() != 1 or t.numel() < 1:
         raise ValueError(f"{name}: expected [samples + 1] offsets")
-    return _want(t, name, torch.int32, (t.numel(),), device)
+    return _want(t, name, torch.int32, t.shape, device)
 
 
 def _mask_ptr(mask, n, device):
-    if mask is not None and mask.dtype == torch.bool:
+    if mask is None:
+        return 0
+    if mask.dtype is torch.bool:
         mask = mask.view(torch.uint8)
     return _want(mask, "mask", torch.uint8, (n,), device)
 
 
+def _scratch(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
 def _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos, scale):
     qp, kp, vp = _rows_ptr(q, 3), _rows_ptr(k, 3), _rows_ptr(v, 3)
-    _same(q, (k, v))
+    dev = _same(q, k, v)
     nq, heads, dim = q.shape
     nk, kv_heads, kdim = k.shape
     if kdim != dim or v.shape != k.shape:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
-    dev = q.device
     samples = q_offsets.numel() - 1
     if k_offsets.numel() != samples + 1:
         raise ValueError("q_offsets and k_offsets must have one length")
-    buckets = 0
+    buckets = pq = pk = pb = pt = 0
     if bias is not None:
         if boundaries is None or q_pos is None or k_pos is None:
             raise ValueError("a bias needs boundaries, q_pos and k_pos")
         buckets = bias.shape[0]
         if buckets < 1:
             raise ValueError("a bias needs at least one bucket")
-    d = AttentionDesc(_SEQ_DTYPE[q.dtype], heads, kv_heads, dim, samples, buckets,
-                      dim ** -0.5 if scale is None else scale, 0, nq, nk, qp, kp, vp, q.stride(0),
-                      q.stride(1), k.stride(0), k.stride(1), v.stride(0), v.stride(1),
-                      _offsets_ptr(q_offsets, "q_offsets", dev),
-                      _offsets_ptr(k_offsets, "k_offsets", dev), _mask_ptr(mask, nk, dev))
-    if buckets:
-        d.q_pos = _want(q_pos, "q_pos", torch.int32, (nq,), dev)
-        d.k_pos = _want(k_pos, "k_pos", torch.int32, (nk,), dev)
-        d.boundaries = _want(boundaries, "boundaries", torch.int32, (buckets - 1,), dev)
-        d.bias = _want(bias, "bias", torch.float32, (buckets, heads), dev)
-    return d
+        pq = _want(q_pos, "q_pos", torch.int32, (nq,), dev)
+        pk = _want(k_pos, "k_pos", torch.int32, (nk,), dev)
+        pb = _want(boundaries, "boundaries", torch.int32, (buckets - 1,), dev)
+        pt = _want(bias, "bias", torch.float32, (buckets, heads), dev)
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    return AttentionDesc.from_buffer_copy(_ATTENTION.pack(
+        _SEQ_DTYPE[q.dtype], heads, kv_heads, dim, samples, buckets,
+        dim ** -0.5 if scale is None else scale, 0, nq, nk, qp, kp, vp, sq[0], sq[1], sk[0], sk[1],
+        sv[0], sv[1], _offsets_ptr(q_offsets, "q_offsets", dev),
+        _offsets_ptr(k_offsets, "k_offsets", dev), _mask_ptr(mask, nk, dev), pq, pk, pb, pt))
+
+
+def _second_order():
+    """Backward passes run without grad mode, except under create_graph=True."""
+    if torch.is_grad_enabled():
+        raise RuntimeError("the sequence operators have first derivatives only: their backward "
+                           "cannot run with create_graph=True")
 
 
 class CrossAttention(torch.autograd.Function):
@@ -751,38 +778,40 @@ class CrossAttention(torch.autograd.Function):
         desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
                                scale)
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        rest = torch.empty_like(out) if q.dtype is torch.bfloat16 else None
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
         need, ctx.need = emb_attention_query(desc)
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        rest = torch.empty_like(out) if q.dtype == torch.bfloat16 else None
-        emb_attention_forward(desc, out, rest, lse, ws)
+        emb_attention_forward(desc, out, rest, lse, _scratch(need, q.device))
+        # the saved tensors keep alive, and unchanged, what the descriptor points to
         ctx.save_for_backward(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos,
                               out, rest, lse)
-        ctx.scale = scale
+        ctx.desc = desc
         return out
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
-        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, out, rest, lse = (
-            ctx.saved_tensors)
-        desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
-                               ctx.scale)
-        if dout.dtype != q.dtype:
+        _second_order()
+        q, k, _, bias, _, _, _, _, _, _, out, rest, lse = ctx.saved_tensors
+        device = q.device
+        if dout.dtype is not q.dtype:
             raise TypeError("the output's gradient must have the output's type")
-        if dout.shape[-1] > 1 and dout.stride(-1) != 1:
+        if dout.stride(-1) != 1 and dout.shape[-1] > 1:
             dout = dout.contiguous()
-        _, want_k, want_v, want_bias = ctx.needs_input_grad[:4]
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        want = ctx.needs_input_grad
+        dq = torch.empty(q.shape, dtype=q.dtype, device=device)
         dk = dv = dbias = None
-        if want_k or want_v:
-            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device)
-        if bias is not None and want_bias:
-            dbias = torch.empty(bias.shape, dtype=torch.float32, device=q.device)
-        ws = torch.empty(ctx.need, dtype=torch.uint8, device=q.device) if ctx.need else None
-        emb_attention_backward(desc, out, rest, lse, dout, dq, dk, dv, dbias, ws)
-        return (dq, dk, dv, dbias) + (None,) * 7
+        if want[1] or want[2]:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=device)
+            dv = torch.empty(k.shape, dtype=q.dtype, device=device)
+        if bias is not None and want[3]:
+            dbias = torch.empty(bias.shape, dtype=torch.float32, device=device)
+        emb_attention_backward(ctx.desc, out, rest, lse, dout, dq, dk, dv, dbias,
+                               _scratch(ctx.need, device))
+        return dq, dk, dv, dbias, None, None, None, None, None, None, None
+
+
+def _needs_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundaries=None,
@@ -797,29 +826,27 @@ def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundar
     ascending, positions int32).  scale: dim ** -0.5 unless given.  Returns
     [n_q, heads, dim]; a row without any key gives zero.  Differentiable in q, k, v and
     bias; runs on the current stream."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, v, bias)):
+    if _needs_grad(q, k, v, bias):
         return CrossAttention.apply(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos,
                                     k_pos, scale)
     desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
                            scale)
     out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    need = emb_attention_query(desc)[0]
-    ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    emb_attention_forward(desc, out, None, None, ws)
+    emb_attention_forward(desc, out, None, None, _scratch(emb_attention_query(desc)[0], q.device))
     return out
 
 
 def _recurrence_desc(x, gate, offsets, state, mask):
     xp, gp = _rows_ptr(x, 2), _rows_ptr(gate, 2)
-    _same(x, (gate,))
+    dev = _same(x, gate)
     if gate.shape != x.shape:
         raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
     n, channels = x.shape
     samples = offsets.numel() - 1
-    return RecurrenceDesc(_SEQ_DTYPE[x.dtype], samples, channels, 0, n, xp, gp, x.stride(0),
-                          gate.stride(0),
-                          _offsets_ptr(offsets, "offsets", x.device), _mask_ptr(mask, n, x.device),
-                          _want(state, "state", torch.float32, (samples, channels), x.device))
+    return RecurrenceDesc.from_buffer_copy(_RECURRENCE.pack(
+        _SEQ_DTYPE[x.dtype], samples, channels, 0, n, xp, gp, x.stride(0), gate.stride(0),
+        _offsets_ptr(offsets, "offsets", dev), _mask_ptr(mask, n, dev),
+        _want(state, "state", torch.float32, (samples, channels), dev)))
 
 
 class GatedRecurrence(torch.autograd.Function):
@@ -828,33 +855,35 @@ class GatedRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, state, offsets, mask):
         desc = _recurrence_desc(x, gate, offsets, state, mask)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        last = torch.empty(desc.samples, desc.channels, dtype=torch.float32, device=x.device)
+        device = x.device
+        y = torch.empty(x.shape, dtype=x.dtype, device=device)
+        last = torch.empty((desc.samples, desc.channels), dtype=torch.float32, device=device)
         rows, ctx.need = emb_recurrence_query(desc)
-        saved = torch.empty(rows, desc.channels, dtype=torch.float32, device=x.device)
-        ws = torch.empty(ctx.need, dtype=torch.uint8, device=x.device) if ctx.need else None
-        emb_recurrence_forward(desc, y, last, saved, ws)
+        saved = torch.empty((rows, desc.channels), dtype=torch.float32, device=device)
+        emb_recurrence_forward(desc, y, last, saved, _scratch(ctx.need, device))
+        # the saved tensors keep alive, and unchanged, what the descriptor points to
         ctx.save_for_backward(x, gate, state, offsets, mask, saved)
+        ctx.desc = desc
         ctx.set_materialize_grads(False)
         return y, last
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dlast):
-        x, gate, state, offsets, mask, saved = ctx.saved_tensors
-        desc = _recurrence_desc(x, gate, offsets, state, mask)
+        _second_order()
+        x, _, state, _, _, saved = ctx.saved_tensors
+        device = x.device
         if dy is None:
-            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
-        if dy.dtype != x.dtype:
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=device)
+        if dy.dtype is not x.dtype:
             raise TypeError("the output's gradient must have the output's type")
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dgate = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dgate = torch.empty(x.shape, dtype=x.dtype, device=device)
         dstate = None
         if state is not None and ctx.needs_input_grad[2]:
             dstate = torch.empty_like(state)
-        ws = torch.empty(ctx.need, dtype=torch.uint8, device=x.device) if ctx.need else None
-        emb_recurrence_backward(desc, saved, dy.contiguous(),
-                                None if dlast is None else dlast.contiguous(), dx, dgate, dstate, ws)
+        emb_recurrence_backward(ctx.desc, saved, dy.contiguous(),
+                                None if dlast is None else dlast.contiguous(), dx, dgate, dstate,
+                                _scratch(ctx.need, device))
         return dx, dgate, dstate, None, None
 
 
@@ -866,14 +895,13 @@ def gated_recurrence(x, gate, offsets, state=None, mask=None):
     mask: uint8 or bool [n], 0 keeps the state as it is.  Returns (y [n, channels], the
     states at every row, last fp32 [samples, channels], those after the last rows).
     Differentiable in x, gate and state; runs on the current stream."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, gate, state)):
+    if _needs_grad(x, gate, state):
         return GatedRecurrence.apply(x, gate, state, offsets, mask)
     desc = _recurrence_desc(x, gate, offsets, state, mask)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    last = torch.empty(desc.samples, desc.channels, dtype=torch.float32, device=x.device)
-    need = emb_recurrence_query(desc)[1]
-    ws = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
-    emb_recurrence_forward(desc, y, last, None, ws)
+    device = x.device
+    y = torch.empty(x.shape, dtype=x.dtype, device=device)
+    last = torch.empty((desc.samples, desc.channels), dtype=torch.float32, device=device)
+    emb_recurrence_forward(desc, y, last, None, _scratch(emb_recurrence_query(desc)[1], device))
     return y, last
 
 
@@ -882,17 +910,17 @@ def gated_recurrence_step(x, gate, state, out=None):
     state fp32 [rows, channels], updated in place; returns it in x's type.  Not
     differentiable."""
     _rows_ptr(x, 2), _rows_ptr(gate, 2)
-    _same(x, (gate,))
+    dev = _same(x, gate)
     if gate.shape != x.shape:
         raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
-    _want(state, "state", torch.float32, tuple(x.shape), x.device)
     if state is None:
         raise TypeError("state: expected a torch.Tensor")
+    _want(state, "state", torch.float32, x.shape, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
     else:
-        _want(out, "out", x.dtype, tuple(x.shape), x.device)
-    if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
+        _want(out, "out", x.dtype, x.shape, dev)
+    if _needs_grad(x, gate, state):
         raise ValueError("gated_recurrence_step has no gradient: use gated_recurrence")
     emb_recurrence_step(x, gate, state, out)
     return out

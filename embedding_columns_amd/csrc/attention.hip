@@ -1307,14 +1307,13 @@ AttnPlan attn_plan(const emb_attention *a)
     AttnPlan p{};
     const int group = a->heads / a->kv_heads;
     const int64_t rows = a->n_q * group, samples = a->samples > 0 ? a->samples : 1;
-    p.wm = rows / samples > 64 ? 4 : 1;
+    const int64_t keys = a->n_k / samples;             // of the average sample
+    const int64_t busy = std::min<int64_t>(samples, a->n_q);
+    auto sets = [&](int per) { return std::max(rows / per + busy / 2, busy) * a->kv_heads; };
+    p.wm = sets(128) >= 384 && rows / samples > 64 ? 4 : 1;
     p.tiles = seg_tiles(a->n_q, a->samples, group, 32 * p.wm);
-    const int64_t sets = (rows / (32 * p.wm) > std::min<int64_t>(samples, a->n_q) ? rows / (32 * p.wm)
-                                                                                  : std::min<int64_t>(samples, a->n_q)) *
-                         a->kv_heads;
-    const int64_t stages = a->n_k / samples / 128;     // of the average sample
-    int64_t s = sets > 0 ? (1024 + sets - 1) / sets : 1;
-    s = std::min<int64_t>(s, std::max<int64_t>(1, stages / 2));
+    int64_t s = sets(32 * p.wm) > 0 ? 512 / sets(32 * p.wm) : 1;
+    s = std::min<int64_t>(s, keys / 256);
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, kSplitsMax));
     p.key_tiles = seg_tiles(a->n_k, a->samples, 1, 128);
     return p;
