@@ -45,7 +45,7 @@ struct AttnArgs {
     int32_t samples, heads, kv_heads, group, dim, buckets;
     float scale, c;                             // c = scale * log2(e)
     int32_t vec, ovec;                          // rows (of out) can be read 16 bytes at a time
-    int32_t splits;
+    int32_t splits, chunk;
     int64_t tiles;
     void *out, *rest;                           // [n_q, heads, dim]; what rounding out left, or NULL
     float *lse;                                 // [n_q, heads]
@@ -418,6 +418,22 @@ __device__ __forceinline__ void bring_rows(const T *base, int64_t stride, int di
     }
 }
 
+// What a workgroup does: tiles of one key head are neighbours in the order of work, and
+// pieces of `chunk` of that order go to the XCDs in turn.
+struct Task {
+    int split, kvh;
+    int64_t tile;
+};
+__device__ __forceinline__ Task task(const AttnArgs &A)
+{
+    const uint32_t id = (uint32_t)xcd_block(blockIdx.x, gridDim.x, A.chunk), rest = id / (uint32_t)A.splits;
+    Task t;
+    t.split = (int)(id - rest * (uint32_t)A.splits);
+    t.kvh = (int)(rest / (uint32_t)A.tiles);
+    t.tile = rest - (uint32_t)t.kvh * (uint32_t)A.tiles;
+    return t;
+}
+
 // The range of pieces a split takes of `n`.
 __device__ __forceinline__ void split_range(int64_t n, int split, int splits, int64_t &a, int64_t &b)
 {
@@ -687,11 +703,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     __shared__ float jm[4][32], jl[4][32];
     extern __shared__ float lb[];
 
-    const int64_t id = xcd_block(blockIdx.x, gridDim.x, 0);
-    const int split = (int)(id % A.splits);
-    const int64_t rest = id / A.splits;
-    const int kvh = (int)(rest / A.tiles);
-    const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, rest % A.tiles);
+    const Task job = task(A);
+    const int split = job.split, kvh = job.kvh;
+    if (kvh >= A.kv_heads) return;
+    const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, job.tile);
     if (s.row0 >= s.rows) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
     const int64_t r0 = s.row0 + (WM == 4 ? w * 32 : 0);
@@ -890,11 +905,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     __shared__ float jd[4][32];
     extern __shared__ float lb[];
 
-    const int64_t id = xcd_block(blockIdx.x, gridDim.x, 0);
-    const int split = (int)(id % A.splits);
-    const int64_t rest = id / A.splits;
-    const int kvh = (int)(rest / A.tiles);
-    const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, rest % A.tiles);
+    const Task job = task(A);
+    const int split = job.split, kvh = job.kvh;
+    if (kvh >= A.kv_heads) return;
+    const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, job.tile);
     if (s.row0 >= s.rows) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
     const int64_t r0 = s.row0 + (WM == 4 ? w * 32 : 0);
@@ -1056,9 +1070,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     __shared__ float acc[4][kBucketsMax];
     extern __shared__ float lb[];
 
-    const int64_t id = xcd_block(blockIdx.x, gridDim.x, 0);
-    const int kvh = (int)(id / A.tiles);
-    const int64_t tile = id % A.tiles;
+    const Task job = task(A);
+    const int kvh = job.kvh;
+    const int64_t tile = job.tile;
+    if (kvh >= A.kv_heads) return;
     const SegTile s = seg_find(A.ko, A.samples, A.nk, 1, 128, tile);
     const bool idle = s.row0 >= s.rows;
     if (idle && !A.dbias_part) return;
@@ -1424,6 +1439,7 @@ AttnArgs attn_args(const emb_attention *a, const AttnPlan &p)
             wide_rows(a->v, a->v_stride, a->v_head_stride, a->dim, el);
     A.splits = p.splits;
     A.tiles = p.tiles;
+    A.chunk = p.splits > 1 ? 16 : 0;
     return A;
 }
 
@@ -1438,7 +1454,7 @@ template <typename T, int DP>
 emb_status forward_run(const AttnArgs &A, const AttnPlan &p, hipStream_t st)
 {
     const size_t lds = (size_t)A.buckets * A.group * 4;
-    const dim3 grid((unsigned)(p.tiles * A.kv_heads * p.splits)), block(kAttnThreads);
+    const dim3 grid((unsigned)xcd_grid(p.tiles * A.kv_heads * p.splits, A.chunk)), block(kAttnThreads);
     if (p.wm == 4) hipLaunchKernelGGL((attn_forward<T, DP, 4>), grid, block, lds, st, A);
     else hipLaunchKernelGGL((attn_forward<T, DP, 1>), grid, block, lds, st, A);
     if (p.splits > 1)
@@ -1453,15 +1469,16 @@ emb_status backward_run(const AttnArgs &A0, const AttnPlan &p, float *dbias, hip
     const size_t lds = (size_t)A.buckets * A.group * 4;
     const dim3 block(kAttnThreads);
     if (A.nq) {
-        const dim3 grid((unsigned)(p.tiles * A.kv_heads * p.splits));
+        const dim3 grid((unsigned)xcd_grid(p.tiles * A.kv_heads * p.splits, A.chunk));
         if (p.wm == 4) hipLaunchKernelGGL((attn_backward_q<T, DP, 4>), grid, block, lds, st, A);
         else hipLaunchKernelGGL((attn_backward_q<T, DP, 1>), grid, block, lds, st, A);
         if (p.splits > 1)
             hipLaunchKernelGGL((attn_join_q<T, DP>), dim3((unsigned)(A.nq * A.heads)), block, 0, st, A);
     }
     A.tiles = p.key_tiles;
+    A.splits = 1;
     if (A.dk || dbias)
-        hipLaunchKernelGGL((attn_backward_k<T, DP>), dim3((unsigned)(p.key_tiles * A.kv_heads)), block, lds, st, A);
+        hipLaunchKernelGGL((attn_backward_k<T, DP>), dim3((unsigned)xcd_grid(p.key_tiles * A.kv_heads, A.chunk)), block, lds, st, A);
     if (dbias)
         hipLaunchKernelGGL(attn_join_bias, dim3((unsigned)A.heads, (unsigned)((A.buckets + 31) / 32)),
                            dim3(kBiasJoin), 0, st, A,
