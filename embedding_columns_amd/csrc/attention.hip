@@ -327,33 +327,67 @@ __device__ __forceinline__ void half_ranges(int x, Range &r0, Range &r1)
 
 // ------------------------------------------------------------------ the bias
 
-// The boundaries, one or more a lane, so that the bucket of a uniform distance is
-// a count over ballots.
-struct Buckets {
+// The bias table of a key head's group, times log2(e), and the boundaries, in LDS; the
+// boundaries also in registers, one or more a lane, so that the bucket of a uniform
+// distance is a count over ballots.  Loads are issued first (take) and used later
+// (put): nothing they need depends on the offsets.
+struct Bias {
     int b[kBucketsMax / 64];
     int n;               // boundaries
+    float first;         // this thread's first entry of the table
+
+    static __device__ __forceinline__ int64_t entry(const AttnArgs &A, int kvh, int i)
+    {
+        const int m = i / A.group, g = i - m * A.group;
+        return (int64_t)m * A.heads + kvh * A.group + g;
+    }
+    __device__ __forceinline__ void take(const AttnArgs &A, int kvh)
+    {
+        n = A.bias ? A.buckets - 1 : 0;
+        first = 0.f;
+#pragma unroll
+        for (int t = 0; t < kBucketsMax / 64; t++) {
+            const int j = 64 * t + lane_id();
+            b[t] = j < n ? *gp(A.bnd + j) : INT32_MAX;
+        }
+        if ((int)threadIdx.x < A.buckets * A.group) first = *gp(A.bias + entry(A, kvh, threadIdx.x));
+    }
+    __device__ __forceinline__ void put(const AttnArgs &A, int kvh, float *lb, int *lbnd) const
+    {
+        if (!A.bias) return;
+        const int t = threadIdx.x, all = A.buckets * A.group;
+        if (t < all) lb[t] = first * kLog2e;
+        for (int i = t + kAttnThreads; i < all; i += kAttnThreads) lb[i] = *gp(A.bias + entry(A, kvh, i)) * kLog2e;
+        if (t < 64)
+#pragma unroll
+            for (int u = 0; u < kBucketsMax / 64; u++)
+                if (64 * u + t < n) lbnd[64 * u + t] = b[u];
+    }
+    __device__ __forceinline__ int bucket(int x) const
+    {
+        int c = 0;
+#pragma unroll
+        for (int t = 0; t < kBucketsMax / 64; t++)
+            if (64 * t < n) c += __popcll(__ballot(b[t] <= x));
+        return uniform(min(c, n));
+    }
 };
 
-__device__ __forceinline__ Buckets load_buckets(const AttnArgs &A)
-{
-    Buckets B;
-    B.n = A.bias ? A.buckets - 1 : 0;
-#pragma unroll
-    for (int t = 0; t < kBucketsMax / 64; t++) {
-        const int j = 64 * t + lane_id();
-        B.b[t] = j < B.n ? A.bnd[j] : INT32_MAX;
-    }
-    return B;
-}
+// The bucket that the last blocks of scores fell into whole, as the range of distances
+// it covers.  Neighbouring blocks mostly share a bucket (buckets widen with the
+// distance), and then two compares a block say so.
+struct BucketRun {
+    int m, lo, last;     // bucket, and its distances lo .. last
 
-__device__ __forceinline__ int bucket_of(const Buckets &B, int x)
-{
-    int n = 0;
-#pragma unroll
-    for (int t = 0; t < kBucketsMax / 64; t++)
-        if (64 * t < B.n) n += __popcll(__ballot(B.b[t] <= x));
-    return uniform(min(n, B.n));
-}
+    __device__ __forceinline__ void set(const Bias &B, const int *lbnd, int bucket)
+    {
+        m = bucket;
+        lo = m > 0 ? lbnd[m - 1] : INT32_MIN;
+        last = m < B.n ? lbnd[m] - 1 : INT32_MAX;     // a bucket in use ends above INT32_MIN
+    }
+    // lanes whose distances a .. b all lie in the bucket
+    __device__ __forceinline__ uint64_t covers(int a, int b) const { return __ballot(a >= lo && b <= last); }
+};
 
 // ------------------------------------------------------ rows into LDS tiles
 
@@ -448,6 +482,12 @@ struct Row {
     int head, g;     // query head, its number inside the group
     int pos;
     Range r;         // of positions of the wavefront's rows
+
+    __device__ __forceinline__ void range()
+    {
+        Range other;
+        half_ranges(pos, r, other);
+    }
 };
 
 __device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, int kvh, int64_t r0)
@@ -460,9 +500,7 @@ __device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, in
     R.g = (int)(rc - i * A.group);
     R.q = s.base + i;
     R.head = kvh * A.group + R.g;
-    R.pos = A.bias ? A.qp[R.q] : 0;
-    Range other;
-    half_ranges(R.pos, R.r, other);
+    R.pos = A.bias ? *gp(A.qp + R.q) : 0;
     return R;
 }
 
@@ -477,20 +515,22 @@ __device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *row, int dim,
     }
 }
 
-// Scores in units of log2: t_i = c s_i + bias * log2(e), returned as (s, c', b') with
-// t_i = c' s_i + b'.  Where all pairs of the block fall in one bucket (most blocks:
-// buckets widen with the distance) the bias is one number a row and costs nothing;
-// otherwise each boundary inside the block's range is a compare and a select.
+// Scores in units of log2: t_i = c s_i + bias * log2(e), as (s, c', b') with
+// t_i = c' s_i + b'.  Where all pairs of the block fall in one bucket the bias is one
+// number a row and costs nothing; otherwise each boundary inside the block's range is a
+// compare and a select.  This is the second case, or a change of bucket: `run` is the
+// bucket of the block's smallest distance afterwards, b its bias.
 // `kpos`: 32 words of LDS of this wavefront, `kp`: position of key lane & 31.
-__device__ __forceinline__ void add_bias(const AttnArgs &A, const Buckets &B, const float *lb, const int *lbnd,
-                                         const Row &R, int *kpos, int kp, Range k, f32x16_t &s, float &c, float &b)
+__device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, const float *lb, const int *lbnd,
+                                           const Row &R, int *kpos, int kp, BucketRun &run, f32x16_t &s, float &c,
+                                           float &b, float &next)
 {
-    c = A.c;
-    b = 0.f;
-    if (!A.bias) return;
-    const int lo = bucket_of(B, sub_sat(R.r.lo, k.hi)), hi = bucket_of(B, sub_sat(R.r.hi, k.lo));
+    Range k, other;
+    half_ranges(kp, k, other);
+    const int lo = B.bucket(sub_sat(R.r.lo, k.hi)), hi = B.bucket(sub_sat(R.r.hi, k.lo));
     const float *mine = lb + R.g;
-    b = mine[lo * A.group];
+    run.set(B, lbnd, lo);
+    next = b = mine[lo * A.group];
     if (lo == hi) return;
     kpos[lane_id() & 31] = kp;
     wave_sync();
@@ -512,17 +552,6 @@ __device__ __forceinline__ void add_bias(const AttnArgs &A, const Buckets &B, co
     for (int i = 0; i < 16; i++) s[i] = fmaf(s[i], c, t[i]);
     c = 1.f;
     b = 0.f;
-}
-
-// The bias table of a key head's group, times log2(e), and the boundaries, in LDS.
-__device__ __forceinline__ void stage_bias(const AttnArgs &A, int kvh, float *lb, int *lbnd)
-{
-    if (!A.bias) return;
-    for (int i = threadIdx.x; i < A.buckets * A.group; i += kAttnThreads) {
-        const int m = i / A.group, g = i - m * A.group;
-        lb[i] = A.bias[(int64_t)m * A.heads + kvh * A.group + g] * kLog2e;
-    }
-    for (int i = threadIdx.x; i < A.buckets - 1; i += kAttnThreads) lbnd[i] = A.bnd[i];
 }
 
 // What the kernels that walk the keys share.  WM = 4: the four wavefronts take 32 query
@@ -547,38 +576,46 @@ struct KeyWalk {
     static constexpr int kWaves = kLds * 16 <= 72 * 1024 && !(sizeof(T) == 4 && DP == 128) ? 2 : 1;
     static_assert(KT / (WM == 4 ? 4 : 1) >= 64 / TL::CH, "a load covers whole rows of one wavefront's share");
 
+    static constexpr int kStep = WM == 1 ? 4 : 1;
+    static constexpr int R = WM == 4 ? KT / 4 : KT;     // rows of a tile that a wavefront brings
+
     u32x4_t *mine;           // this wavefront's tiles
     const AttnArgs &A;
-    int kvh, w;
-    int64_t k0, k1, at, end; // keys of the sample; tiles [at, end) of KT keys to go
-    int buf;
+    int w, buf;
+    int64_t at, end;         // tiles [at, end) of KT keys to go
+    const T *k, *v;          // rows to bring next
+    int64_t look_key, k1;    // key to look at next; end of the sample
     uint64_t keep;           // keys of the current tile that take part
     int pos;                 // position of the current tile's key lane (KT = 64) or lane & 31
-    // of the tile after the current one
-    uint64_t keep_next;
+    uint64_t keep_next;      // of the tile after the current one
     int pos_next;
     int raw_keep, raw_pos;   // loads in flight for the tile after that
 
-    __device__ __forceinline__ KeyWalk(const AttnArgs &a, u32x4_t *lds, int kvh_, int w_, int64_t k0_, int64_t k1_,
+    __device__ __forceinline__ KeyWalk(const AttnArgs &a, u32x4_t *lds, int kvh, int w_, int64_t k0, int64_t k1_,
                                        int split)
-        : A(a), kvh(kvh_), w(w_), k0(k0_), k1(k1_), buf(0)
+        : A(a), w(w_), buf(0), k1(k1_), raw_pos(0)
     {
         mine = lds + (WM == 4 ? 0 : w * (kLds / 4));
         split_range(k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0, split, A.splits, at, end);
         if (WM == 1) at += w;
+        const int64_t key = k0 + at * KT, row = key + (WM == 4 ? w * R : 0);
+        look_key = key + (lane_id() & (KT - 1));
+        k = static_cast<const T *>(A.k) + kvh * A.kh + row * A.ks;
+        v = static_cast<const T *>(A.v) + kvh * A.vh + row * A.vs;
     }
-    static constexpr int kStep = WM == 1 ? 4 : 1;
 
     __device__ __forceinline__ const u32x4_t *k_tile() const { return mine + buf * 2 * kWords; }
     __device__ __forceinline__ const u32x4_t *v_tile() const { return mine + buf * 2 * kWords + kWords; }
 
-    // mask and position of the keys of a tile, one key a lane
-    __device__ __forceinline__ void look(int64_t tile)
+    // mask and position of the keys of a tile, one key a lane; past the sample's end
+    // the last key is looked at again
+    __device__ __forceinline__ void look()
     {
-        const int64_t key = k0 + tile * KT + (lane_id() & (KT - 1));
-        const bool in = tile < end && key < k1;
+        const bool in = look_key < k1;
+        const int64_t key = in ? look_key : k1 - 1;
         raw_keep = in ? (A.mask ? *gp(A.mask + key) : 1) : 0;
-        if (A.bias) raw_pos = *gp(A.kp + (key < k1 ? key : k1 - 1));
+        if (A.bias) raw_pos = *gp(A.kp + key);
+        look_key += kStep * KT;
     }
     __device__ __forceinline__ void seen()
     {
@@ -586,29 +623,22 @@ struct KeyWalk {
         if (KT == 32) keep_next &= 0xFFFFFFFFull;
         pos_next = raw_pos;
     }
-    __device__ __forceinline__ void bring(int64_t tile, int to)
+    __device__ __forceinline__ void bring(int to)
     {
-        if (tile >= end) return;
-        const T *k = static_cast<const T *>(A.k) + kvh * A.kh + (k0 + tile * KT) * A.ks;
-        const T *v = static_cast<const T *>(A.v) + kvh * A.vh + (k0 + tile * KT) * A.vs;
         u32x4_t *lk = mine + to * 2 * kWords, *lv = lk + kWords;
-        if (WM == 4) {       // a quarter of the tile each
-            constexpr int R = KT / 4;
-            bring_rows<T, DP, R>(k + w * R * A.ks, A.ks, A.dim, A.vec, keep_next >> (w * R), lk, w * R);
-            bring_rows<T, DP, R>(v + w * R * A.vs, A.vs, A.dim, A.vec, keep_next >> (w * R), lv, w * R);
-        } else {
-            bring_rows<T, DP, KT>(k, A.ks, A.dim, A.vec, keep_next, lk, 0);
-            bring_rows<T, DP, KT>(v, A.vs, A.dim, A.vec, keep_next, lv, 0);
-        }
+        const int r0 = WM == 4 ? w * R : 0;
+        bring_rows<T, DP, R>(k, A.ks, A.dim, A.vec, keep_next >> r0, lk, r0);
+        bring_rows<T, DP, R>(v, A.vs, A.dim, A.vec, keep_next >> r0, lv, r0);
+        k += kStep * KT * A.ks;
+        v += kStep * KT * A.vs;
     }
     __device__ __forceinline__ void start()
     {
-        raw_pos = 0;
         if (at >= end) return;
-        look(at);
+        look();
         seen();
-        if (kBufs == 2) bring(at, 0);
-        look(at + kStep);
+        if (kBufs == 2) bring(0);
+        look();
     }
     // the current tile is in LDS after this, and the next on its way
     __device__ __forceinline__ void enter()
@@ -618,14 +648,14 @@ struct KeyWalk {
         if (kBufs == 1) {
             arrived();
             if (WM == 4) __syncthreads();
-            bring(at, 0);
+            bring(0);
         }
         arrived();
         if (WM == 4) __syncthreads();
         else wave_sync();
         seen();
-        if (kBufs == 2) bring(at + kStep, buf ^ 1);
-        look(at + 2 * kStep);
+        if (kBufs == 2 && at + kStep < end) bring(buf ^ 1);
+        look();
     }
     __device__ __forceinline__ void leave()
     {
@@ -706,6 +736,8 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     const Task job = task(A);
     const int split = job.split, kvh = job.kvh;
     if (kvh >= A.kv_heads) return;
+    Bias B;
+    B.take(A, kvh);
     const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, job.tile);
     if (s.row0 >= s.rows) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
@@ -715,14 +747,16 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     const int64_t k0 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg);
     const int64_t k1 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg + 1);
 
-    KW walk(A, lds, kvh, w, k0, k1, split);
-    walk.start();
-    stage_bias(A, kvh, lb, lbnd);
-    const Buckets B = load_buckets(A);
-    const Row R = query_row(A, s, kvh, r0);
+    Row R = query_row(A, s, kvh, r0);
     Frag<T, DP> qf;
     load_frag<T, DP>(qf, static_cast<const T *>(A.q) + R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
+    KW walk(A, lds, kvh, w, k0, k1, split);
+    walk.start();
+    B.put(A, kvh, lb, lbnd);
+    R.range();
     if (WM == 1) __syncthreads();     // the bias table; with WM = 4 the walk's barriers cover it
+    BucketRun run{0, INT32_MAX, INT32_MIN};
+    float b_run = 0.f;
 
     float m = -INFINITY, l = 0.f;
     f32x16_t o[DP / 32];
@@ -733,10 +767,9 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         walk.enter();
         if (!busy || walk.keep == 0) continue;
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
-        Range kr[2];
-        if (A.bias) half_ranges(walk.pos, kr[0], kr[1]);
         f32x16_t sc[SUBS];
         float c[SUBS], b[SUBS], top = -INFINITY;
+        uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : 0;
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
@@ -752,8 +785,13 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         }
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
-            const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
-            add_bias(A, B, lb, lbnd, R, kpos[w], kp, kr[u], sc[u], c[u], b[u]);
+            c[u] = A.c;
+            b[u] = b_run;
+            if (A.bias && ~in_run >> (32 * u) & 0xFFFFFFFFu) {
+                const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
+                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc[u], c[u], b[u], b_run);
+                if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
+            }
             float t = sc[u][0];
 #pragma unroll
             for (int i = 1; i < 16; i++) t = fmaxf(t, sc[u][i]);
@@ -908,6 +946,8 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     const Task job = task(A);
     const int split = job.split, kvh = job.kvh;
     if (kvh >= A.kv_heads) return;
+    Bias B;
+    B.take(A, kvh);
     const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, job.tile);
     if (s.row0 >= s.rows) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
@@ -917,16 +957,16 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     const int64_t k0 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg);
     const int64_t k1 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg + 1);
 
-    KW walk(A, lds, kvh, w, k0, k1, split);
-    walk.start();
-    stage_bias(A, kvh, lb, lbnd);
-    const Buckets B = load_buckets(A);
-    const Row R = query_row(A, s, kvh, r0);
+    Row R = query_row(A, s, kvh, r0);
     const int64_t row = R.q * A.heads + R.head;
     Frag<T, DP> qf, df;
     load_frag<T, DP>(qf, static_cast<const T *>(A.q) + R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
     load_frag<T, DP>(df, static_cast<const T *>(A.dout) + R.q * A.ds + R.head * A.dh, A.dim, A.vec, R.live);
-    float D = 0.f;
+    float lse = R.live ? *gp(A.lse + row) : INFINITY, D = 0.f;
+    KW walk(A, lds, kvh, w, k0, k1, split);
+    walk.start();
+    B.put(A, kvh, lb, lbnd);
+    R.range();
     {
         Frag<T, DP> of;
         load_frag<T, DP>(of, static_cast<const T *>(A.out) + row * A.dim, A.dim, A.ovec, R.live);
@@ -940,9 +980,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         D = both_halves_sum(D);
     }
     // a row without keys has lse = -inf: exp2(score - inf) keeps its weights zero
-    float lse = R.live ? A.lse[row] * kLog2e : INFINITY;
-    if (lse == -INFINITY) lse = INFINITY;
+    lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
     if (WM == 1) __syncthreads();
+    BucketRun run{0, INT32_MAX, INT32_MIN};
+    float b_run = 0.f;
 
     float e = 0.f;                         // sum p (dP - D)
     f32x16_t x[DP / 32];
@@ -955,8 +996,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         // register file at every step
         walk.enter();
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
-        Range kr[2];
-        if (A.bias) half_ranges(walk.pos, kr[0], kr[1]);
+        uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : 0;
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
@@ -965,9 +1005,12 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
             for (int i = 0; i < 16; i++) dp[i] = -D;
             products<T, DP>(sc, lk, u * 32, qf);
             products<T, DP>(dp, lv, u * 32, df);
-            float c, b;
-            const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
-            add_bias(A, B, lb, lbnd, R, kpos[w], kp, kr[u], sc, c, b);
+            float c = A.c, b = b_run;
+            if (A.bias && ~in_run >> (32 * u) & 0xFFFFFFFFu) {
+                const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
+                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc, c, b, b_run);
+                if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
+            }
             b -= lse;
 #pragma unroll
             for (int i = 0; i < 16; i++) sc[i] = exp2_fast(fmaf(sc[i], c, b));
@@ -1074,6 +1117,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     const int kvh = job.kvh;
     const int64_t tile = job.tile;
     if (kvh >= A.kv_heads) return;
+    Bias B;
+    B.take(A, kvh);
     const SegTile s = seg_find(A.ko, A.samples, A.nk, 1, 128, tile);
     const bool idle = s.row0 >= s.rows;
     if (idle && !A.dbias_part) return;
@@ -1134,20 +1179,13 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     Stage now{0, 0, q0}, next = after(now), then = after(next);
     bring(now, 0);
     if (w == 0) look(now);
-    stage_bias(A, kvh, lb, lbnd);
-    for (int i = threadIdx.x; i < 4 * kBucketsMax; i += kAttnThreads) (&acc[0][0])[i] = 0.f;
-    const Buckets B = load_buckets(A);
+    if (A.dbias_part)
+        for (int i = threadIdx.x; i < 4 * kBucketsMax; i += kAttnThreads) (&acc[0][0])[i] = 0.f;
     const int64_t r = s.row0 + 32 * w + (lane & 31);
     const bool in = r < s.rows;
     const int64_t key = s.base + (in ? r : s.rows - 1);
-    const bool live = in && !idle && (!A.mask || A.mask[key]);
-    int kpos = 0;
-    Range kr{0, 0};
-    if (A.bias && !idle) {
-        kpos = A.kp[key];
-        Range other;
-        half_ranges(kpos, kr, other);
-    }
+    const int kpos = A.bias && !idle ? *gp(A.kp + key) : 0;
+    const bool live = in && !idle && (!A.mask || *gp(A.mask + key));
     Frag<T, DP> kf, vf;
     load_frag<T, DP>(kf, static_cast<const T *>(A.k) + (live ? key * A.ks + kvh * A.kh : 0), A.dim, A.vec, live);
     load_frag<T, DP>(vf, static_cast<const T *>(A.v) + (live ? key * A.vs + kvh * A.vh : 0), A.dim, A.vec, live);
@@ -1155,6 +1193,12 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
 #pragma unroll
         for (int c = 0; c < TL::CH / 2; c++) lvk[TL::at(32 * w + (lane & 31), 2 * c + h)] = vf[c];
         wave_sync();
+    }
+    B.put(A, kvh, lb, lbnd);
+    Range kr{0, 0};
+    if (A.bias) {
+        Range other;
+        half_ranges(kpos, kr, other);
     }
     if (w == 0) {
         tell(0);
@@ -1165,8 +1209,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
 #pragma unroll
     for (int d = 0; d < DP / 32; d++) dk[d] = dv[d] = f32x16_t{};
     // score gradients of the bucket at hand, a sum per lane until the bucket changes
-    int bucket = 0;
-    float run = 0.f;
+    BucketRun run{0, INT32_MAX, INT32_MIN};
+    float b_run = live ? 0.f : -INFINITY, sum_run = 0.f;
     auto settle = [&](int m, float sum) {
         sum = wave_sum(sum);
         if (lane == 0) acc[w][m] += sum;
@@ -1187,12 +1231,18 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
             products<T, DP>(sc, lq, 0, kf);
             if (kSpill) products<T, DP>(dp, ld, 0, lvk, 32 * w);
             else products<T, DP>(dp, ld, 0, vf);
-            float b = live ? 0.f : -INFINITY, c = A.c;
-            int lo = 0, hi = 0, x[16];
-            if (A.bias) {
-                lo = bucket_of(B, sub_sat(qlo[cur], kr.hi));
-                hi = bucket_of(B, sub_sat(qhi[cur], kr.lo));
-                b += lb[lo * A.group + now.g];
+            float b = b_run, c = A.c;
+            int lo = run.m, hi = run.m, x[16];
+            if (A.bias && ~run.covers(sub_sat(qlo[cur], kpos), sub_sat(qhi[cur], kpos)) != 0) {
+                lo = B.bucket(sub_sat(qlo[cur], kr.hi));
+                hi = B.bucket(sub_sat(qhi[cur], kr.lo));
+                if (A.dbias_part && lo != run.m) {
+                    settle(run.m, sum_run);
+                    sum_run = 0.f;
+                }
+                run.set(B, lbnd, hi);
+                b = live ? lb[lo * A.group + now.g] : -INFINITY;
+                b_run = b;
                 if (lo != hi) {
                     f32x16_t t;
 #pragma unroll
@@ -1202,9 +1252,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                     }
                     for (int m = lo; m < hi; m++) {
                         const int edge = lbnd[m];
-                        const float v = live ? lb[(m + 1) * A.group + now.g] : -INFINITY;
+                        b_run = live ? lb[(m + 1) * A.group + now.g] : -INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
+                        for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? b_run : t[i];
                     }
 #pragma unroll
                     for (int i = 0; i < 16; i++) sc[i] = fmaf(sc[i], c, t[i]);
@@ -1224,11 +1274,6 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                 typename Mma<T>::template Rows<DP>(lq, 0, d).times(dk[d], ds);
             }
             if (A.dbias_part) {
-                if (lo != bucket) {
-                    settle(bucket, run);
-                    bucket = lo;
-                    run = 0.f;
-                }
                 for (int m = lo; m < hi; m++) {
                     const int edge = lbnd[m];
                     float sum = 0.f;
@@ -1238,19 +1283,20 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                         sum += below ? dp[i] : 0.f;
                         dp[i] = below ? 0.f : dp[i];
                     }
-                    settle(m, run + sum);
-                    run = 0.f;
+                    settle(m, sum_run + sum);
+                    sum_run = 0.f;
                 }
-                bucket = hi;
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 16; i++) sum += dp[i];
-                run += sum;
+                sum_run += sum;
             }
         }
+        const int last_m = run.m;
+        if (next.g != now.g) run = BucketRun{last_m, INT32_MAX, INT32_MIN};     // another head, another bias
         if (A.dbias_part && next.g != now.g) {       // a head of the group is done
-            settle(bucket, run);
-            run = 0.f;
+            settle(last_m, sum_run);
+            sum_run = 0.f;
             __syncthreads();
             float *to = A.dbias_part + (tile * A.heads + kvh * A.group + now.g) * A.buckets;
             for (int m = threadIdx.x; m < A.buckets; m += kAttnThreads) {
