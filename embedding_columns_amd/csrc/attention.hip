@@ -41,12 +41,12 @@ struct AttnArgs {
     const uint8_t *mask;                        // [n_k] or NULL
     const int32_t *qp, *kp, *bnd;               // positions, boundaries [buckets - 1]
     const float *bias;                          // [buckets, heads] or NULL
-    int64_t nq, nk;
+    int32_t nq, nk;
     int32_t samples, heads, kv_heads, group, dim, buckets;
     float scale, c;                             // c = scale * log2(e)
     int32_t vec, ovec;                          // rows (of out) can be read 16 bytes at a time
     int32_t splits, chunk;
-    int64_t tiles;
+    int32_t tiles;
     void *out, *rest;                           // [n_q, heads, dim]; what rounding out left, or NULL
     float *lse;                                 // [n_q, heads]
     float *part, *part_ml;                      // split partials
@@ -455,8 +455,7 @@ __device__ __forceinline__ void bring_rows(const T *base, int64_t stride, int di
 // What a workgroup does: tiles of one key head are neighbours in the order of work, and
 // pieces of `chunk` of that order go to the XCDs in turn.
 struct Task {
-    int split, kvh;
-    int64_t tile;
+    int split, kvh, tile;
 };
 __device__ __forceinline__ Task task(const AttnArgs &A)
 {
@@ -464,21 +463,22 @@ __device__ __forceinline__ Task task(const AttnArgs &A)
     Task t;
     t.split = (int)(id - rest * (uint32_t)A.splits);
     t.kvh = (int)(rest / (uint32_t)A.tiles);
-    t.tile = rest - (uint32_t)t.kvh * (uint32_t)A.tiles;
+    t.tile = (int)(rest - (uint32_t)t.kvh * (uint32_t)A.tiles);
     return t;
 }
 
 // The range of pieces a split takes of `n`.
-__device__ __forceinline__ void split_range(int64_t n, int split, int splits, int64_t &a, int64_t &b)
+__device__ __forceinline__ void split_range(int n, int split, int splits, int &a, int &b)
 {
-    a = n * split / splits;
-    b = n * (split + 1) / splits;
+    a = (int)((uint64_t)n * split / (uint32_t)splits);
+    b = (int)((uint64_t)n * (split + 1) / (uint32_t)splits);
+    if (splits == 1) a = 0, b = n;
 }
 
 // The 32 query rows of a wavefront, one per lane & 31 (both halves hold the same).
 struct Row {
     bool live;
-    int64_t q;       // row of q
+    int q;           // row of q
     int head, g;     // query head, its number inside the group
     int pos;
     Range r;         // of positions of the wavefront's rows
@@ -490,13 +490,13 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, int kvh, int64_t r0)
+__device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, int kvh, int r0)
 {
     Row R;
-    const int64_t r = r0 + (lane_id() & 31);
+    const int r = r0 + (lane_id() & 31);
     R.live = r < s.rows;
-    const int64_t rc = R.live ? r : s.rows - 1;      // a row past the end repeats the last
-    const int64_t i = rc / A.group;
+    const uint32_t rc = R.live ? r : s.rows - 1;     // a row past the end repeats the last
+    const uint32_t i = A.group == 1 ? rc : rc / (uint32_t)A.group;
     R.g = (int)(rc - i * A.group);
     R.q = s.base + i;
     R.head = kvh * A.group + R.g;
@@ -582,23 +582,23 @@ struct KeyWalk {
     u32x4_t *mine;           // this wavefront's tiles
     const AttnArgs &A;
     int w, buf;
-    int64_t at, end;         // tiles [at, end) of KT keys to go
+    int at, end;             // tiles [at, end) of KT keys to go
     const T *k, *v;          // rows to bring next
-    int64_t look_key, k1;    // key to look at next; end of the sample
+    int look_key, k1;    // key to look at next; end of the sample
     uint64_t keep;           // keys of the current tile that take part
     int pos;                 // position of the current tile's key lane (KT = 64) or lane & 31
     uint64_t keep_next;      // of the tile after the current one
     int pos_next;
     int raw_keep, raw_pos;   // loads in flight for the tile after that
 
-    __device__ __forceinline__ KeyWalk(const AttnArgs &a, u32x4_t *lds, int kvh, int w_, int64_t k0, int64_t k1_,
-                                       int split)
+    __device__ __forceinline__ KeyWalk(const AttnArgs &a, u32x4_t *lds, int kvh, int w_, int k0, int k1_, int split)
         : A(a), w(w_), buf(0), k1(k1_), raw_pos(0)
     {
         mine = lds + (WM == 4 ? 0 : w * (kLds / 4));
         split_range(k1 > k0 ? (k1 - k0 + KT - 1) / KT : 0, split, A.splits, at, end);
         if (WM == 1) at += w;
-        const int64_t key = k0 + at * KT, row = key + (WM == 4 ? w * R : 0);
+        const int key = k0 + at * KT;
+        const int64_t row = key + (WM == 4 ? w * R : 0);
         look_key = key + (lane_id() & (KT - 1));
         k = static_cast<const T *>(A.k) + kvh * A.kh + row * A.ks;
         v = static_cast<const T *>(A.v) + kvh * A.vh + row * A.vs;
@@ -612,7 +612,7 @@ struct KeyWalk {
     __device__ __forceinline__ void look()
     {
         const bool in = look_key < k1;
-        const int64_t key = in ? look_key : k1 - 1;
+        const int key = in ? look_key : k1 - 1;
         raw_keep = in ? (A.mask ? *gp(A.mask + key) : 1) : 0;
         if (A.bias) raw_pos = *gp(A.kp + key);
         look_key += kStep * KT;
@@ -738,19 +738,16 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     if (kvh >= A.kv_heads) return;
     Bias B;
     B.take(A, kvh);
-    const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, job.tile);
+    const SegTile s = seg_find<WM * 32>(A.qo, A.nq, A.ko, A.nk, A.samples, A.group, job.tile);
     if (s.row0 >= s.rows) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
-    const int64_t r0 = s.row0 + (WM == 4 ? w * 32 : 0);
+    const int r0 = s.row0 + (WM == 4 ? w * 32 : 0);
     const bool busy = r0 < s.rows;
-    const bool nobody = s.seg == 0 || s.seg == A.samples + 1;
-    const int64_t k0 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg);
-    const int64_t k1 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg + 1);
 
     Row R = query_row(A, s, kvh, r0);
     Frag<T, DP> qf;
-    load_frag<T, DP>(qf, static_cast<const T *>(A.q) + R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
-    KW walk(A, lds, kvh, w, k0, k1, split);
+    load_frag<T, DP>(qf, static_cast<const T *>(A.q) + (int64_t)R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
+    KW walk(A, lds, kvh, w, s.o0, s.o1, split);
     walk.start();
     B.put(A, kvh, lb, lbnd);
     R.range();
@@ -825,7 +822,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         }
     }
     l = both_halves_sum(l);
-    const int64_t row = R.q * A.heads + R.head;
+    const int64_t row = (int64_t)R.q * A.heads + R.head;
     const int64_t at = (int64_t)split * A.nq * A.heads + row;
 
     if (WM == 1) {
@@ -892,7 +889,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 {
     constexpr int G = kAttnThreads / DP;      // splits side by side
     __shared__ float sm[kSplitsMax], sl[kSplitsMax], so[G][DP];
-    const int64_t row = blockIdx.x, n = A.nq * A.heads;
+    const int64_t row = blockIdx.x, n = (int64_t)A.nq * A.heads;
     const int t = threadIdx.x, d = t % DP, g = t / DP;
     for (int u = t; u < A.splits; u += kAttnThreads) {
         sm[u] = A.part_ml[2 * (u * n + row)];
@@ -948,22 +945,19 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     if (kvh >= A.kv_heads) return;
     Bias B;
     B.take(A, kvh);
-    const SegTile s = seg_find(A.qo, A.samples, A.nq, A.group, WM * 32, job.tile);
+    const SegTile s = seg_find<WM * 32>(A.qo, A.nq, A.ko, A.nk, A.samples, A.group, job.tile);
     if (s.row0 >= s.rows) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
-    const int64_t r0 = s.row0 + (WM == 4 ? w * 32 : 0);
+    const int r0 = s.row0 + (WM == 4 ? w * 32 : 0);
     const bool busy = r0 < s.rows;
-    const bool nobody = s.seg == 0 || s.seg == A.samples + 1;
-    const int64_t k0 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg);
-    const int64_t k1 = nobody ? 0 : seg_edge(A.ko, A.samples, A.nk, s.seg + 1);
 
     Row R = query_row(A, s, kvh, r0);
-    const int64_t row = R.q * A.heads + R.head;
+    const int64_t row = (int64_t)R.q * A.heads + R.head;
     Frag<T, DP> qf, df;
-    load_frag<T, DP>(qf, static_cast<const T *>(A.q) + R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
-    load_frag<T, DP>(df, static_cast<const T *>(A.dout) + R.q * A.ds + R.head * A.dh, A.dim, A.vec, R.live);
+    load_frag<T, DP>(qf, static_cast<const T *>(A.q) + (int64_t)R.q * A.qs + R.head * A.qh, A.dim, A.vec, R.live);
+    load_frag<T, DP>(df, static_cast<const T *>(A.dout) + (int64_t)R.q * A.ds + R.head * A.dh, A.dim, A.vec, R.live);
     float lse = R.live ? *gp(A.lse + row) : INFINITY, D = 0.f;
-    KW walk(A, lds, kvh, w, k0, k1, split);
+    KW walk(A, lds, kvh, w, s.o0, s.o1, split);
     walk.start();
     B.put(A, kvh, lb, lbnd);
     R.range();
@@ -997,7 +991,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         walk.enter();
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
         uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : 0;
-#pragma unroll
+#pragma unroll(DP * sizeof(T) > 128 ? 1 : SUBS)
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
             f32x16_t sc = f32x16_t{}, dp;
@@ -1075,7 +1069,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 {
     constexpr int G = kAttnThreads / DP;
     __shared__ float so[G][DP];
-    const int64_t row = blockIdx.x, n = A.nq * A.heads;
+    const int64_t row = blockIdx.x, n = (int64_t)A.nq * A.heads;
     const int t = threadIdx.x, d = t % DP, g = t / DP;
     float x = 0.f, e = 0.f;
 #pragma unroll 8
@@ -1115,23 +1109,21 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
 
     const Task job = task(A);
     const int kvh = job.kvh;
-    const int64_t tile = job.tile;
+    const int tile = job.tile;
     if (kvh >= A.kv_heads) return;
     Bias B;
     B.take(A, kvh);
-    const SegTile s = seg_find(A.ko, A.samples, A.nk, 1, 128, tile);
+    const SegTile s = seg_find<128>(A.ko, A.nk, A.qo, A.nq, A.samples, 1, tile);
     const bool idle = s.row0 >= s.rows;
     if (idle && !A.dbias_part) return;
     const int lane = lane_id(), h = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
-    const bool nobody = s.seg == 0 || s.seg == A.samples + 1 || idle;
-    const int64_t q0 = nobody ? 0 : seg_edge(A.qo, A.samples, A.nq, s.seg);
-    const int64_t q1 = nobody ? 0 : seg_edge(A.qo, A.samples, A.nq, s.seg + 1);
-    const int64_t per = q1 > q0 ? (q1 - q0 + 31) / 32 : 0, stages = per * A.group;
+    const int q0 = s.o0, q1 = idle ? s.o0 : s.o1;
+    const int64_t stages = (int64_t)((q1 - q0 + 31) / 32) * A.group;
 
-    // stage `it`: head it / per of the group, rows from q0 + 32 (it % per)
+    // a stage: head g of the group, 32 rows from `row`
     struct Stage {
-        int g;
-        int64_t i, row;
+        int g, row;
+        int64_t i;
     };
     auto after = [&](Stage z) {
         z.i++;
@@ -1146,10 +1138,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         if (z.i >= stages) return;
         // wavefronts 0 and 1 bring the halves of q, 2 and 3 those of dout
         const int head = kvh * A.group + z.g, half = (w & 1) * 16;
-        const int64_t row = z.row + half, left = q1 - row;
+        const int row = z.row + half, left = q1 - row;
         const uint64_t keep = left <= 0 ? 0 : left >= 16 ? 0xFFFF : (1u << left) - 1;
-        const T *p = w < 2 ? static_cast<const T *>(A.q) + head * A.qh + row * A.qs
-                           : static_cast<const T *>(A.dout) + head * A.dh + row * A.ds;
+        const T *p = w < 2 ? static_cast<const T *>(A.q) + head * A.qh + (int64_t)row * A.qs
+                           : static_cast<const T *>(A.dout) + head * A.dh + (int64_t)row * A.ds;
         bring_rows<T, DP, 16>(p, w < 2 ? A.qs : A.ds, A.dim, A.vec, keep, lds[to][w >> 1], half);
     };
     float n_lse = 0.f, n_delta = 0.f;
@@ -1157,9 +1149,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     bool n_in = false;
     auto look = [&](const Stage &z) {       // wavefront 0: what goes with the rows
         if (z.i >= stages) return;
-        const int64_t row = z.row + (lane & 31);
+        const int row = z.row + (lane & 31);
         n_in = row < q1;
-        const int64_t at = (n_in ? row : q1 - 1) * A.heads + kvh * A.group + z.g;
+        const int64_t at = (int64_t)(n_in ? row : q1 - 1) * A.heads + kvh * A.group + z.g;
         n_lse = *gp(A.lse + at);
         n_delta = *gp(A.delta + at);
         if (A.bias) n_pos = *gp(A.qp + (n_in ? row : q1 - 1));
@@ -1176,12 +1168,12 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         qhi[to] = r.hi;
     };
 
-    Stage now{0, 0, q0}, next = after(now), then = after(next);
+    Stage now{0, q0, 0}, next = after(now), then = after(next);
     bring(now, 0);
     if (w == 0) look(now);
     if (A.dbias_part)
         for (int i = threadIdx.x; i < 4 * kBucketsMax; i += kAttnThreads) (&acc[0][0])[i] = 0.f;
-    const int64_t r = s.row0 + 32 * w + (lane & 31);
+    const int r = s.row0 + 32 * w + (lane & 31);
     const bool in = r < s.rows;
     const int64_t key = s.base + (in ? r : s.rows - 1);
     const int kpos = A.bias && !idle ? *gp(A.kp + key) : 0;
@@ -1298,7 +1290,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
             settle(last_m, sum_run);
             sum_run = 0.f;
             __syncthreads();
-            float *to = A.dbias_part + (tile * A.heads + kvh * A.group + now.g) * A.buckets;
+            float *to = A.dbias_part + ((int64_t)tile * A.heads + kvh * A.group + now.g) * A.buckets;
             for (int m = threadIdx.x; m < A.buckets; m += kAttnThreads) {
                 to[m] = (acc[0][m] + acc[1][m]) + (acc[2][m] + acc[3][m]);
                 acc[0][m] = acc[1][m] = acc[2][m] = acc[3][m] = 0.f;
@@ -1308,7 +1300,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     }
     if (A.dbias_part && stages == 0)
         for (int i = threadIdx.x; i < A.buckets * A.group; i += kAttnThreads)
-            A.dbias_part[(tile * A.heads + kvh * A.group) * A.buckets + i] = 0.f;
+            A.dbias_part[((int64_t)tile * A.heads + kvh * A.group) * A.buckets + i] = 0.f;
     if (!in || idle || !A.dk) return;
     T *pk = static_cast<T *>(A.dk) + (key * A.kv_heads + kvh) * A.dim;
     T *pv = static_cast<T *>(A.dv) + (key * A.kv_heads + kvh) * A.dim;
@@ -1338,7 +1330,7 @@ __global__ __launch_bounds__(kBiasJoin) void attn_join_bias(AttnArgs A, float *d
     const int m = blockIdx.y * 32 + t, mc = m < A.buckets ? m : A.buckets - 1;
     float sum = 0.f;
 #pragma unroll 8
-    for (int64_t u = g; u < A.tiles; u += 32) sum += *gp(A.dbias_part + (u * A.heads + head) * A.buckets + mc);
+    for (int u = g; u < A.tiles; u += 32) sum += *gp(A.dbias_part + ((int64_t)u * A.heads + head) * A.buckets + mc);
     part[g][t] = sum;
     __syncthreads();
     if (g != 0 || m >= A.buckets) return;
@@ -1410,8 +1402,9 @@ emb_status attn_check(const emb_attention *a)
     if (a->dim > 128) return fail(EMB_ERR_UNSUPPORTED, "attention: dim must be <= 128");
     if (a->samples < 0 || a->n_q < 0 || a->n_k < 0)
         return fail(EMB_ERR_INVALID_ARG, "attention: samples, n_q and n_k must be >= 0");
-    if (a->n_q >= (int64_t(1) << 31) - 1 || a->n_k >= (int64_t(1) << 31) - 1 || a->samples >= (1 << 30))
-        return fail(EMB_ERR_UNSUPPORTED, "attention: n_q and n_k must be < 2^31 - 1 and samples < 2^30 (int32 offsets)");
+    if (a->n_q > kRowsMost / (a->heads / a->kv_heads) || a->n_k > kRowsMost || a->samples > (1 << 30))
+        return fail(EMB_ERR_UNSUPPORTED,
+                    "attention: n_q heads / kv_heads and n_k must be <= 2^31 - 65536, samples <= 2^30");
     if (a->heads > 65535) return fail(EMB_ERR_UNSUPPORTED, "attention: heads must be <= 65535");
     if (!(a->scale >= 1e-18f && a->scale <= 1e18f))
         return fail(EMB_ERR_INVALID_ARG, "attention: scale must be in [1e-18, 1e18]");
@@ -1470,8 +1463,8 @@ AttnArgs attn_args(const emb_attention *a, const AttnPlan &p)
     A.kp = a->k_pos;
     A.bnd = a->boundaries;
     A.bias = a->buckets ? a->bias : nullptr;
-    A.nq = a->n_q;
-    A.nk = a->n_k;
+    A.nq = (int32_t)a->n_q;
+    A.nk = (int32_t)a->n_k;
     A.samples = a->samples;
     A.heads = a->heads;
     A.kv_heads = a->kv_heads;
@@ -1484,7 +1477,7 @@ AttnArgs attn_args(const emb_attention *a, const AttnPlan &p)
             wide_rows(a->k, a->k_stride, a->k_head_stride, a->dim, el) &&
             wide_rows(a->v, a->v_stride, a->v_head_stride, a->dim, el);
     A.splits = p.splits;
-    A.tiles = p.tiles;
+    A.tiles = (int32_t)p.tiles;
     A.chunk = p.splits > 1 ? 16 : 0;
     return A;
 }
@@ -1504,7 +1497,7 @@ emb_status forward_run(const AttnArgs &A, const AttnPlan &p, hipStream_t st)
     if (p.wm == 4) hipLaunchKernelGGL((attn_forward<T, DP, 4>), grid, block, lds, st, A);
     else hipLaunchKernelGGL((attn_forward<T, DP, 1>), grid, block, lds, st, A);
     if (p.splits > 1)
-        hipLaunchKernelGGL((attn_join<T, DP>), dim3((unsigned)(A.nq * A.heads)), block, 0, st, A);
+        hipLaunchKernelGGL((attn_join<T, DP>), dim3((unsigned)((int64_t)A.nq * A.heads)), block, 0, st, A);
     return launched("attention forward");
 }
 
@@ -1519,9 +1512,9 @@ emb_status backward_run(const AttnArgs &A0, const AttnPlan &p, float *dbias, hip
         if (p.wm == 4) hipLaunchKernelGGL((attn_backward_q<T, DP, 4>), grid, block, lds, st, A);
         else hipLaunchKernelGGL((attn_backward_q<T, DP, 1>), grid, block, lds, st, A);
         if (p.splits > 1)
-            hipLaunchKernelGGL((attn_join_q<T, DP>), dim3((unsigned)(A.nq * A.heads)), block, 0, st, A);
+            hipLaunchKernelGGL((attn_join_q<T, DP>), dim3((unsigned)((int64_t)A.nq * A.heads)), block, 0, st, A);
     }
-    A.tiles = p.key_tiles;
+    A.tiles = (int32_t)p.key_tiles;
     A.splits = 1;
     if (A.dk || dbias)
         hipLaunchKernelGGL((attn_backward_k<T, DP>), dim3((unsigned)xcd_grid(p.key_tiles * A.kv_heads, A.chunk)), block, lds, st, A);

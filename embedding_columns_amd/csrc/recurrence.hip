@@ -9,6 +9,7 @@ namespace emb {
 
 constexpr int kScanSteps = 16;   // consecutive steps a wavefront of the forward holds in registers
 constexpr int kBackSteps = 8;    // ... of the backward, which holds twice as much per step
+constexpr int kChunk = 512;      // rows per chunk of a split scan
 constexpr int kSaved = 8;        // the forward saves the state before every kSaved steps
 
 struct ScanArgs {
@@ -27,7 +28,7 @@ struct ScanArgs {
     float *sum_a, *sum_h;        // [tiles, channels]: what a chunk does to the state it is given
     int64_t n, tiles;
     int32_t samples, channels;
-    int32_t chunk;               // rows per chunk; 0: a whole sample at once
+    int32_t chunk;               // samples are cut into chunks of kChunk rows
 };
 
 // sigmoid(g) and sigmoid(-g) = 1 - sigmoid(g), the small one without cancellation:
@@ -104,17 +105,17 @@ __device__ __forceinline__ bool scan_span(const ScanArgs &A, int64_t block, Scan
         s.seg = (int)block;
         s.tile0 = block;
         s.chunks = 1;
-        s.first = s.begin = seg_edge(A.off, A.samples, A.n, s.seg);
-        s.end = seg_edge(A.off, A.samples, A.n, s.seg + 1);
+        s.first = s.begin = seg_edge(A.off, A.samples, (int)A.n, s.seg);
+        s.end = seg_edge(A.off, A.samples, (int)A.n, s.seg + 1);
         return true;
     }
-    const SegTile t = seg_find(A.off, A.samples, A.n, 1, A.chunk, block);
+    const SegTile t = seg_find<kChunk>(A.off, (int)A.n, nullptr, 0, A.samples, 1, (int)block);
     s.seg = t.seg;
     s.first = t.base;
-    s.tile0 = t.base / A.chunk + t.seg;
-    s.chunks = (t.rows + A.chunk - 1) / A.chunk;
+    s.tile0 = t.base / kChunk + t.seg;
+    s.chunks = (t.rows + kChunk - 1) / kChunk;
     s.begin = t.base + t.row0;
-    s.end = t.row0 + A.chunk < t.rows ? s.begin + A.chunk : t.base + t.rows;
+    s.end = t.row0 + kChunk < t.rows ? s.begin + kChunk : t.base + t.rows;
     // an empty sample keeps its first chunk: it hands the state through
     return t.row0 < t.rows || (t.rows == 0 && t.row0 == 0);
 }
@@ -468,7 +469,7 @@ namespace {
 
 struct ScanPlan {
     int waves, vec;
-    int32_t chunk;
+    int32_t chunk;               // cut samples into chunks
     int64_t tiles, ckpt_rows;
 };
 
@@ -484,8 +485,8 @@ ScanPlan scan_plan(const emb_recurrence *r)
     p.chunk = 0;
     p.tiles = r->samples + 2;
     if (r->samples * blocks < 512 && mean >= 1024) {
-        p.chunk = 512;
-        p.tiles = seg_tiles(r->n, r->samples, 1, p.chunk);
+        p.chunk = 1;
+        p.tiles = seg_tiles(r->n, r->samples, 1, kChunk);
     }
     p.ckpt_rows = seg_tiles(r->n, r->samples, 1, kSaved);
     return p;
@@ -498,8 +499,8 @@ emb_status scan_check(const emb_recurrence *r)
     if (r->samples < 0 || r->n < 0) return fail(EMB_ERR_INVALID_ARG, "recurrence: samples and n must be >= 0");
     if (r->channels <= 0) return fail(EMB_ERR_INVALID_ARG, "recurrence: channels must be >= 1");
     if (r->channels > (1 << 20)) return fail(EMB_ERR_UNSUPPORTED, "recurrence: channels must be <= 2^20");
-    if (r->n >= (int64_t(1) << 31) - 1 || r->samples >= (1 << 30))
-        return fail(EMB_ERR_UNSUPPORTED, "recurrence: n must be < 2^31 - 1 and samples < 2^30 (int32 offsets)");
+    if (r->n > kRowsMost || r->samples > (1 << 30))
+        return fail(EMB_ERR_UNSUPPORTED, "recurrence: n must be <= 2^31 - 65536 and samples <= 2^30");
     if (r->x_stride < 0 || r->gate_stride < 0)
         return fail(EMB_ERR_INVALID_ARG, "recurrence: row strides must be >= 0");
     return EMB_OK;
