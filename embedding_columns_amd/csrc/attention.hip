@@ -43,7 +43,7 @@ struct AttnArgs {
     const float *bias;                          // [buckets, heads] or NULL
     int32_t nq, nk;
     int32_t samples, heads, kv_heads, group, dim, buckets;
-    float scale, c;                             // c = scale * log2(e)
+    float scale, rscale, c;                     // rscale = 1 / scale, c = scale * log2(e)
     int32_t vec, ovec;                          // rows (of out) can be read 16 bytes at a time
     int32_t splits, chunk;
     int32_t tiles;
@@ -287,7 +287,7 @@ __device__ __forceinline__ float both_halves_sum(float x)
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Sum over the wavefront, minimum and maximum over its halves, with DPP moves: inside
+// Sum over the wavefront, minimum and maximum over 32 lanes, with DPP moves: inside
 // quads, half rows, rows of 16, then the last lane of a row into the next.
 #define EMB_DPP(x, ctrl, rows) __builtin_amdgcn_update_dpp(x, x, ctrl, rows, 0xF, false)
 __device__ __forceinline__ float wave_sum(float x)
@@ -306,9 +306,13 @@ __device__ __forceinline__ float wave_sum(float x)
 struct Range {
     int lo, hi;
 };
-// of the lanes of half 0 and of half 1
-__device__ __forceinline__ void half_ranges(int x, Range &r0, Range &r1)
+// of the 32 values of half 0, which half 1 repeats: the ends where they are in order, as
+// positions mostly are
+__device__ __forceinline__ Range half_range(int x)
 {
+    const int before = EMB_DPP(x, 0x138, 0xF);      // wave_shr:1, lane 0 keeps its own
+    if ((uint32_t)__ballot(before <= x) == 0xFFFFFFFFu)
+        return Range{__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 31)};
     int a = x, b = x;
     a = min(a, EMB_DPP(a, 0xB1, 0xF));
     b = max(b, EMB_DPP(b, 0xB1, 0xF));
@@ -318,19 +322,20 @@ __device__ __forceinline__ void half_ranges(int x, Range &r0, Range &r1)
     b = max(b, EMB_DPP(b, 0x141, 0xF));
     a = min(a, EMB_DPP(a, 0x140, 0xF));
     b = max(b, EMB_DPP(b, 0x140, 0xF));
-    r0.lo = min(__builtin_amdgcn_readlane(a, 0), __builtin_amdgcn_readlane(a, 16));
-    r0.hi = max(__builtin_amdgcn_readlane(b, 0), __builtin_amdgcn_readlane(b, 16));
-    r1.lo = min(__builtin_amdgcn_readlane(a, 32), __builtin_amdgcn_readlane(a, 48));
-    r1.hi = max(__builtin_amdgcn_readlane(b, 32), __builtin_amdgcn_readlane(b, 48));
+    return Range{min(__builtin_amdgcn_readlane(a, 0), __builtin_amdgcn_readlane(a, 16)),
+                 max(__builtin_amdgcn_readlane(b, 0), __builtin_amdgcn_readlane(b, 16))};
 }
 #undef EMB_DPP
 
 // ------------------------------------------------------------------ the bias
 
-// The bias table of a key head's group, times log2(e), and the boundaries, in LDS; the
-// boundaries also in registers, one or more a lane, so that the bucket of a uniform
+// The bias table of a key head's group, over scale, and the boundaries, in LDS: so an
+// entry can be where a block of products starts, and the scaling brings it back.  Finite
+// entries are held to +-kBiasMost, where fp32 still tells scores apart that differ by a
+// hundredth; a weight of e^-kBiasMost beside any other is zero.  The boundaries also in registers, one or more a lane, so that the bucket of a uniform
 // distance is a count over ballots.  Loads are issued first (take) and used later
 // (put): nothing they need depends on the offsets.
+constexpr float kBiasMost = 1e5f;
 struct Bias {
     int b[kBucketsMax / 64];
     int n;               // boundaries
@@ -356,8 +361,11 @@ struct Bias {
     {
         if (!A.bias) return;
         const int t = threadIdx.x, all = A.buckets * A.group;
-        if (t < all) lb[t] = first * kLog2e;
-        for (int i = t + kAttnThreads; i < all; i += kAttnThreads) lb[i] = *gp(A.bias + entry(A, kvh, i)) * kLog2e;
+        auto held = [&](float x) {
+            return fabsf(x) > kBiasMost && fabsf(x) < INFINITY ? copysignf(kBiasMost, x) * A.rscale : x * A.rscale;
+        };
+        if (t < all) lb[t] = held(first);
+        for (int i = t + kAttnThreads; i < all; i += kAttnThreads) lb[i] = held(*gp(A.bias + entry(A, kvh, i)));
         if (t < 64)
 #pragma unroll
             for (int u = 0; u < kBucketsMax / 64; u++)
@@ -483,11 +491,7 @@ struct Row {
     int pos;
     Range r;         // of positions of the wavefront's rows
 
-    __device__ __forceinline__ void range()
-    {
-        Range other;
-        half_ranges(pos, r, other);
-    }
+    __device__ __forceinline__ void range() { r = half_range(pos); }
 };
 
 __device__ __forceinline__ Row query_row(const AttnArgs &A, const SegTile &s, int kvh, int r0)
@@ -515,43 +519,51 @@ __device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *row, int dim,
     }
 }
 
-// Scores in units of log2: t_i = c s_i + bias * log2(e), as (s, c', b') with
-// t_i = c' s_i + b'.  Where all pairs of the block fall in one bucket the bias is one
-// number a row and costs nothing; otherwise each boundary inside the block's range is a
-// compare and a select.  This is the second case, or a change of bucket: `run` is the
-// bucket of the block's smallest distance afterwards, b its bias.
+// Scores in units of log2 are t_i = c s_i + b with s_i the product (plus what the block
+// started from) and b a number per row: where all pairs of a block fall in one bucket the
+// bias is in b and costs nothing.  Where they do not, each boundary inside the block's
+// range is a compare and a select on what the block starts from, and b is zero.  This
+// is for blocks outside the bucket of `run`: afterwards `run` is the bucket of the
+// block's smallest distance and b_run its bias.
 // `kpos`: 32 words of LDS of this wavefront, `kp`: position of key lane & 31.
 __device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, const float *lb, const int *lbnd,
-                                           const Row &R, int *kpos, int kp, BucketRun &run, f32x16_t &s, float &c,
-                                           float &b, float &next)
+                                           const Row &R, int *kpos, int kp, BucketRun &run, f32x16_t &s, float &b,
+                                           float &b_run)
 {
-    Range k, other;
-    half_ranges(kp, k, other);
+    const Range k = half_range(kp);
     const int lo = B.bucket(sub_sat(R.r.lo, k.hi)), hi = B.bucket(sub_sat(R.r.hi, k.lo));
     const float *mine = lb + R.g;
+    const float base = mine[lo * A.group];
     run.set(B, lbnd, lo);
-    next = b = mine[lo * A.group];
+    b = b_run = base * A.c;
     if (lo == hi) return;
+    b = 0.f;
     kpos[lane_id() & 31] = kp;
     wave_sync();
     int x[16];
-    f32x16_t t;
+    const int h = lane_id() >> 5;
 #pragma unroll
-    for (int i = 0; i < 16; i++) {
-        x[i] = sub_sat(R.pos, kpos[block_key(i)]);
-        t[i] = b;
+    for (int g = 0; g < 4; g++) {
+        const int4 k4 = *reinterpret_cast<const int4 *>(kpos + 8 * g + 4 * h);
+        x[4 * g] = sub_sat(R.pos, k4.x);
+        x[4 * g + 1] = sub_sat(R.pos, k4.y);
+        x[4 * g + 2] = sub_sat(R.pos, k4.z);
+        x[4 * g + 3] = sub_sat(R.pos, k4.w);
     }
     wave_sync();
-    for (int m = lo; m < hi; m++) {
-        const int edge = lbnd[m];
-        const float v = mine[(m + 1) * A.group];
+    // s holds 0, or -inf where a key takes no part
+    float v = mine[(lo + 1) * A.group];
+    int edge = lbnd[lo];
+    f32x16_t t;
+#pragma unroll
+    for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : base;
+    for (int m = lo + 1; m < hi; m++) {
+        edge = lbnd[m];
+        v = mine[(m + 1) * A.group];
 #pragma unroll
         for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
     }
-#pragma unroll
-    for (int i = 0; i < 16; i++) s[i] = fmaf(s[i], c, t[i]);
-    c = 1.f;
-    b = 0.f;
+    s += t;
 }
 
 // What the kernels that walk the keys share.  WM = 4: the four wavefronts take 32 query
@@ -728,8 +740,8 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     constexpr int SUBS = KW::KT / 32;
     __shared__ __align__(1024) u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];    // 16 KB for sum_waves
     __shared__ int lbnd[kBucketsMax];
-    __shared__ int kpos[4][32];
-    __shared__ float kout[4][32];
+    __shared__ __align__(16) int kpos[4][32];
+    __shared__ __align__(16) float kout[4][32];
     __shared__ float jm[4][32], jl[4][32];
     extern __shared__ float lb[];
 
@@ -765,8 +777,8 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         if (!busy || walk.keep == 0) continue;
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
         f32x16_t sc[SUBS];
-        float c[SUBS], b[SUBS], top = -INFINITY;
-        uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : 0;
+        float b[SUBS], top = -INFINITY;
+        uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : ~0ull;
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
@@ -778,21 +790,20 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
                 sc[u] = block_order(kout[w]);
                 wave_sync();
             }
+            b[u] = b_run;
+            if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
+                const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
+                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc[u], b[u], b_run);
+                if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
+            }
             products<T, DP>(sc[u], lk, u * 32, qf);
         }
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
-            c[u] = A.c;
-            b[u] = b_run;
-            if (A.bias && ~in_run >> (32 * u) & 0xFFFFFFFFu) {
-                const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
-                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc[u], c[u], b[u], b_run);
-                if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
-            }
             float t = sc[u][0];
 #pragma unroll
             for (int i = 1; i < 16; i++) t = fmaxf(t, sc[u][i]);
-            top = fmaxf(top, fmaf(t, c[u], b[u]));
+            top = fmaxf(top, fmaf(t, A.c, b[u]));
         }
         top = both_halves_max(top);
         if (__ballot(top > m + kLag)) {
@@ -812,7 +823,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                sc[u][i] = exp2_fast(fmaf(sc[u][i], c[u], bu));
+                sc[u][i] = exp2_fast(fmaf(sc[u][i], A.c, bu));
                 sum += sc[u][i];
             }
             l += sum;
@@ -936,7 +947,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     constexpr int SUBS = KW::KT / 32;
     __shared__ __align__(1024) u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];
     __shared__ int lbnd[kBucketsMax];
-    __shared__ int kpos[4][32];
+    __shared__ __align__(16) int kpos[4][32];
     __shared__ float jd[4][32];
     extern __shared__ float lb[];
 
@@ -990,24 +1001,24 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         // register file at every step
         walk.enter();
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
-        uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : 0;
-#pragma unroll(DP * sizeof(T) > 128 ? 1 : SUBS)
+        uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : ~0ull;
+#pragma unroll DP * sizeof(T) > 128 ? 1 : SUBS
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
             f32x16_t sc = f32x16_t{}, dp;
 #pragma unroll
             for (int i = 0; i < 16; i++) dp[i] = -D;
-            products<T, DP>(sc, lk, u * 32, qf);
-            products<T, DP>(dp, lv, u * 32, df);
-            float c = A.c, b = b_run;
-            if (A.bias && ~in_run >> (32 * u) & 0xFFFFFFFFu) {
+            float b = b_run;
+            if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
                 const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
-                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc, c, b, b_run);
+                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc, b, b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
+            products<T, DP>(sc, lk, u * 32, qf);
+            products<T, DP>(dp, lv, u * 32, df);
             b -= lse;
 #pragma unroll
-            for (int i = 0; i < 16; i++) sc[i] = exp2_fast(fmaf(sc[i], c, b));
+            for (int i = 0; i < 16; i++) sc[i] = exp2_fast(fmaf(sc[i], A.c, b));
             if (keep != 0xFFFFFFFFu) {
                 const uint32_t mine = keep >> (4 * h);
 #pragma unroll
@@ -1087,6 +1098,20 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 
 // ---------------------------------------------------------- backward: keys
 
+// distances of 16 query rows (in the order of a block) from the lane's key
+__device__ __forceinline__ void distances(const int *qpos, int kpos, int (&x)[16])
+{
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+        const int4 q = *reinterpret_cast<const int4 *>(qpos + 8 * g + 4 * h);
+        x[4 * g] = sub_sat(q.x, kpos);
+        x[4 * g + 1] = sub_sat(q.y, kpos);
+        x[4 * g + 2] = sub_sat(q.z, kpos);
+        x[4 * g + 3] = sub_sat(q.w, kpos);
+    }
+}
+
 // A workgroup owns 128 keys of one key head, 32 a wavefront (one per lane & 31), K
 // and V in registers, and walks all query rows of the sample, one head of the group
 // after the other, 32 rows a stage: dk and dv need no sum across workgroups.  Rows
@@ -1101,8 +1126,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     __shared__ __align__(1024) u32x4_t lvk[kSpill ? 128 * TL::CH : 1];
     constexpr int kWords = 32 * TL::CH;
     __shared__ __align__(1024) u32x4_t lds[2][2][kWords];             // [stage & 1][q, dout]
-    __shared__ float first[2][32], ndelta[2][32];     // - lse / c (or -inf), - delta
-    __shared__ int qpos[2][32], qlo[2], qhi[2];
+    __shared__ __align__(16) float first[2][32], ndelta[2][32];     // - lse / c (or -inf), - delta
+    __shared__ __align__(16) int qpos[2][32];
+    __shared__ int qlo[2], qhi[2];
     __shared__ int lbnd[kBucketsMax];
     __shared__ float acc[4][kBucketsMax];
     extern __shared__ float lb[];
@@ -1162,8 +1188,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         ndelta[to][lane & 31] = n_in ? -n_delta : 0.f;
         if (!A.bias) return;
         qpos[to][lane & 31] = n_pos;
-        Range r, other;
-        half_ranges(n_pos, r, other);
+        const Range r = half_range(n_pos);
         qlo[to] = r.lo;
         qhi[to] = r.hi;
     };
@@ -1188,10 +1213,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     }
     B.put(A, kvh, lb, lbnd);
     Range kr{0, 0};
-    if (A.bias) {
-        Range other;
-        half_ranges(kpos, kr, other);
-    }
+    if (A.bias) kr = half_range(kpos);
     if (w == 0) {
         tell(0);
         look(next);
@@ -1203,9 +1225,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     // score gradients of the bucket at hand, a sum per lane until the bucket changes
     BucketRun run{0, INT32_MAX, INT32_MIN};
     float b_run = live ? 0.f : -INFINITY, sum_run = 0.f;
+    // (an LDS addition without an answer; only this wavefront adds to its own row, in order)
     auto settle = [&](int m, float sum) {
         sum = wave_sum(sum);
-        if (lane == 0) acc[w][m] += sum;
+        if (lane == 0) __hip_atomic_fetch_add(&acc[w][m], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
 
     for (; now.i < stages; now = next, next = then, then = after(then)) {
@@ -1220,12 +1243,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         const u32x4_t *lq = lds[cur][0], *ld = lds[cur][1];
         {
             f32x16_t sc = block_order(first[cur]), dp = block_order(ndelta[cur]);
-            products<T, DP>(sc, lq, 0, kf);
-            if (kSpill) products<T, DP>(dp, ld, 0, lvk, 32 * w);
-            else products<T, DP>(dp, ld, 0, vf);
-            float b = b_run, c = A.c;
-            int lo = run.m, hi = run.m, x[16];
+            float b = b_run;
+            int lo = run.m, hi = run.m;
             if (A.bias && ~run.covers(sub_sat(qlo[cur], kpos), sub_sat(qhi[cur], kpos)) != 0) {
+                // as mixed_bias, with one key and 16 rows a lane
                 lo = B.bucket(sub_sat(qlo[cur], kr.hi));
                 hi = B.bucket(sub_sat(qhi[cur], kr.lo));
                 if (A.dbias_part && lo != run.m) {
@@ -1233,30 +1254,33 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                     sum_run = 0.f;
                 }
                 run.set(B, lbnd, hi);
-                b = live ? lb[lo * A.group + now.g] : -INFINITY;
-                b_run = b;
+                float v = lb[lo * A.group + now.g];
                 if (lo != hi) {
+                    int x[16];
+                    distances(qpos[cur], kpos, x);
+                    const float base = v;
+                    int edge = lbnd[lo];
+                    v = lb[(lo + 1) * A.group + now.g];
                     f32x16_t t;
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        x[i] = sub_sat(qpos[cur][block_key(i)], kpos);
-                        t[i] = b;
-                    }
-                    for (int m = lo; m < hi; m++) {
-                        const int edge = lbnd[m];
-                        b_run = live ? lb[(m + 1) * A.group + now.g] : -INFINITY;
+                    for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : base;
+                    for (int m = lo + 1; m < hi; m++) {
+                        edge = lbnd[m];
+                        v = lb[(m + 1) * A.group + now.g];
 #pragma unroll
-                        for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? b_run : t[i];
+                        for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
                     }
-#pragma unroll
-                    for (int i = 0; i < 16; i++) sc[i] = fmaf(sc[i], c, t[i]);
-                    c = 1.f;
-                    b = 0.f;
+                    sc += t;
                 }
+                b_run = live ? v * A.c : -INFINITY;
+                b = lo == hi ? b_run : live ? 0.f : -INFINITY;
             }
+            products<T, DP>(sc, lq, 0, kf);
+            if (kSpill) products<T, DP>(dp, ld, 0, lvk, 32 * w);
+            else products<T, DP>(dp, ld, 0, vf);
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                sc[i] = exp2_fast(fmaf(sc[i], c, b));
+                sc[i] = exp2_fast(fmaf(sc[i], A.c, b));
                 dp[i] *= sc[i];
             }
             const typename Mma<T>::Pack p = Mma<T>::pack(sc), ds = Mma<T>::pack(dp);
@@ -1266,17 +1290,21 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                 typename Mma<T>::template Rows<DP>(lq, 0, d).times(dk[d], ds);
             }
             if (A.dbias_part) {
-                for (int m = lo; m < hi; m++) {
-                    const int edge = lbnd[m];
-                    float sum = 0.f;
+                if (lo != hi) {
+                    int x[16];
+                    distances(qpos[cur], kpos, x);
+                    for (int m = lo; m < hi; m++) {
+                        const int edge = lbnd[m];
+                        float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const bool below = x[i] < edge;
-                        sum += below ? dp[i] : 0.f;
-                        dp[i] = below ? 0.f : dp[i];
+                        for (int i = 0; i < 16; i++) {
+                            const bool below = x[i] < edge;
+                            sum += below ? dp[i] : 0.f;
+                            dp[i] = below ? 0.f : dp[i];
+                        }
+                        settle(m, sum_run + sum);
+                        sum_run = 0.f;
                     }
-                    settle(m, sum_run + sum);
-                    sum_run = 0.f;
                 }
                 float sum = 0.f;
 #pragma unroll
@@ -1472,6 +1500,7 @@ AttnArgs attn_args(const emb_attention *a, const AttnPlan &p)
     A.dim = a->dim;
     A.buckets = a->buckets;
     A.scale = a->scale;
+    A.rscale = 1.f / a->scale;
     A.c = a->scale * kLog2e;
     A.vec = wide_rows(a->q, a->q_stride, a->q_head_stride, a->dim, el) &&
             wide_rows(a->k, a->k_stride, a->k_head_stride, a->dim, el) &&
