@@ -843,6 +843,8 @@ def _recurrence_desc(x, gate, offsets, state, mask):
         raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
     n, channels = x.shape
     samples = offsets.numel() - 1
+    if n > 1 and (x.stride(0) < channels or gate.stride(0) < channels):
+        raise ValueError("rows of x and gate must not overlap: pass contiguous tensors")
     return RecurrenceDesc.from_buffer_copy(_RECURRENCE.pack(
         _SEQ_DTYPE[x.dtype], samples, channels, 0, n, xp, gp, x.stride(0), gate.stride(0),
         _offsets_ptr(offsets, "offsets", dev), _mask_ptr(mask, n, dev),

@@ -7,10 +7,11 @@
 
 namespace emb {
 
-constexpr int kScanSteps = 16;   // consecutive steps a wavefront of the forward holds in registers
-constexpr int kBackSteps = 8;    // ... of the backward, which holds twice as much per step
+constexpr int kSteps = 8;        // consecutive rows a half wavefront holds in registers; the
+                                 // forward saves the state before every such group
+constexpr int kWaves = 8;        // wavefronts of a workgroup on longer samples
 constexpr int kChunk = 512;      // rows per chunk of a split scan
-constexpr int kSaved = 8;        // the forward saves the state before every kSaved steps
+constexpr int kOrderMost = 2048; // samples that scan_order sorts
 
 struct ScanArgs {
     const void *x, *gate;        // [n, channels], rows xs / gs elements apart
@@ -20,7 +21,7 @@ struct ScanArgs {
     const float *state;          // [samples, channels] or NULL
     void *y;                     // [n, channels]
     float *last;                 // [samples, channels]
-    float *ckpt;                 // state before each group of kSaved steps, or NULL
+    float *ckpt;                 // state before each group of kSteps rows, or NULL
     const void *dy;              // backward
     const float *dlast;
     void *dx, *dgate;
@@ -29,6 +30,7 @@ struct ScanArgs {
     int64_t n, tiles;
     int32_t samples, channels;
     int32_t chunk;               // samples are cut into chunks of kChunk rows
+    int32_t *order;              // segments, the longest first, or NULL
 };
 
 // sigmoid(g) and sigmoid(-g) = 1 - sigmoid(g), the small one without cancellation:
@@ -47,12 +49,14 @@ struct Chan;
 template <>
 struct Chan<float, 1> {
     typedef float Raw;
+    typedef uint32_t Bits;
     static __device__ __forceinline__ void open(Raw r, float *v) { v[0] = r; }
     static __device__ __forceinline__ Raw pack(const float *v) { return v[0]; }
 };
 template <>
 struct Chan<float, 2> {
     typedef float2 Raw;
+    typedef i32x2_t Bits;
     static __device__ __forceinline__ void open(Raw r, float *v)
     {
         v[0] = r.x;
@@ -63,12 +67,14 @@ struct Chan<float, 2> {
 template <>
 struct Chan<uint16_t, 1> {
     typedef uint16_t Raw;
+    typedef uint16_t Bits;
     static __device__ __forceinline__ void open(Raw r, float *v) { v[0] = bf16_lo(r); }
     static __device__ __forceinline__ Raw pack(const float *v) { return bf16_rne(v[0]); }
 };
 template <>
 struct Chan<uint16_t, 2> {
     typedef uint32_t Raw;
+    typedef uint32_t Bits;
     static __device__ __forceinline__ void open(Raw r, float *v)
     {
         v[0] = bf16_lo(r);
@@ -77,39 +83,81 @@ struct Chan<uint16_t, 2> {
     static __device__ __forceinline__ Raw pack(const float *v) { return bf16x2_rne(v[0], v[1]); }
 };
 
-// row (uniform) and channel c (per lane) of a tensor
-template <typename R, typename T>
-__device__ __forceinline__ R row_load(const T *p, int64_t row, int64_t stride, uint32_t c)
+__device__ __forceinline__ uint32_t buf_load(__amdgpu_buffer_rsrc_t r, int at, uint32_t)
 {
-    return *gp(reinterpret_cast<const R *>(p + row * stride + c));
+    return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
 }
-template <typename R, typename T>
-__device__ __forceinline__ void row_store(T *p, int64_t row, int64_t stride, uint32_t c, R v)
+__device__ __forceinline__ uint16_t buf_load(__amdgpu_buffer_rsrc_t r, int at, uint16_t)
 {
-    *gp(reinterpret_cast<R *>(p + row * stride + c)) = v;
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
 }
+__device__ __forceinline__ i32x2_t buf_load(__amdgpu_buffer_rsrc_t r, int at, i32x2_t)
+{
+    return __builtin_bit_cast(i32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+}
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int at, uint32_t v)
+{
+    __builtin_amdgcn_raw_buffer_store_b32(v, r, at, 0, 0);
+}
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int at, uint16_t v)
+{
+    __builtin_amdgcn_raw_buffer_store_b16(v, r, at, 0, 0);
+}
+__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int at, i32x2_t v)
+{
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, v), r, at, 0, 0);
+}
+
+// The rows of a block of the walk in one tensor, through a buffer descriptor that ends
+// with the sample (or chunk): rows past the end read zeros and drop stores, and so do
+// lanes past the last channel, whose offset lies past every end.
+template <typename T, int VEC>
+struct Rows {
+    typedef Chan<T, VEC> CH;
+    __amdgpu_buffer_rsrc_t rsrc;
+    int at, stride;
+    __device__ __forceinline__ Rows(const void *p, int64_t stride_, int row, int rows, int first, int c, bool live)
+    {
+        stride = (int)stride_ * (int)sizeof(T);
+        rsrc = row_buffer(static_cast<const T *>(p) + row * stride_, 0, rows * stride);
+        at = live ? first * stride + c * (int)sizeof(T) : INT32_MIN;
+        // one addition per row, where it is used: taken out of the walk's loop, the offsets of
+        // all rows of all tensors would be 40 registers
+        asm volatile("" : "+v"(at));
+    }
+    // (an offset past the end stays one: rows and strides keep it below 2^31)
+    __device__ __forceinline__ typename CH::Raw load(int i) const
+    {
+        return __builtin_bit_cast(typename CH::Raw, buf_load(rsrc, at + i * stride, typename CH::Bits{}));
+    }
+    __device__ __forceinline__ void store(int i, const float *v) const
+    {
+        buf_store(rsrc, at + i * stride, __builtin_bit_cast(typename CH::Bits, CH::pack(v)));
+    }
+};
 
 // Which rows a workgroup walks: one sample, or one chunk of one.
 struct ScanSpan {
-    int64_t begin, end;      // rows
-    int64_t first;           // first row of the sample
-    int64_t tile, tile0;     // chunk number, that of the sample's first chunk
-    int64_t chunks;          // of the sample
+    int begin, end;          // rows
+    int first;               // first row of the sample
+    int tile, tile0;         // chunk number, that of the sample's first chunk
+    int chunks;              // of the sample
     int seg;
 };
 
-__device__ __forceinline__ bool scan_span(const ScanArgs &A, int64_t block, ScanSpan &s)
+__device__ __forceinline__ bool scan_span(const ScanArgs &A, int block, ScanSpan &s)
 {
     s.tile = block;
     if (A.chunk == 0) {
-        s.seg = (int)block;
+        s.seg = A.order ? uniform(*gp(A.order + block)) : block;
         s.tile0 = block;
         s.chunks = 1;
-        s.first = s.begin = seg_edge(A.off, A.samples, (int)A.n, s.seg);
-        s.end = seg_edge(A.off, A.samples, (int)A.n, s.seg + 1);
+        s.first = s.begin = uniform(seg_edge(A.off, A.samples, (int)A.n, s.seg));
+        s.end = max(uniform(seg_edge(A.off, A.samples, (int)A.n, s.seg + 1)), s.begin);
         return true;
     }
-    const SegTile t = seg_find<kChunk>(A.off, (int)A.n, nullptr, 0, A.samples, 1, (int)block);
+    const SegTile t = seg_find<kChunk>(A.off, (int)A.n, nullptr, 0, A.samples, 1, block);
     s.seg = t.seg;
     s.first = t.base;
     s.tile0 = t.base / kChunk + t.seg;
@@ -120,24 +168,52 @@ __device__ __forceinline__ bool scan_span(const ScanArgs &A, int64_t block, Scan
     return t.row0 < t.rows || (t.rows == 0 && t.row0 == 0);
 }
 
-// The saved state of the group of kSaved rows that begins at `row`
-__device__ __forceinline__ int64_t saved_row(const ScanSpan &s, int64_t row)
+// The segments in the order of their lengths, the longest first: a workgroup walks a
+// whole sample, and the long ones have to start early.  The place of a segment is the
+// number of those that go before it.
+__global__ __launch_bounds__(256) void scan_order(ScanArgs A)
 {
-    return s.first / kSaved + s.seg + (row - s.first) / kSaved;
+    __shared__ int len[kOrderMost + 2];
+    const int n = A.samples + 2;
+    for (int j = threadIdx.x; j < n; j += 256)
+        len[j] = seg_edge(A.off, A.samples, (int)A.n, j + 1) - seg_edge(A.off, A.samples, (int)A.n, j);
+    __syncthreads();
+    // eight lanes a segment
+    const int i = min((int)(blockIdx.x * 32 + threadIdx.x / 8), n - 1), mine = len[i];
+    int before = 0;
+#pragma unroll 8
+    for (int j = threadIdx.x & 7; j < n; j += 8) before += len[j] > mine || (len[j] == mine && j < i);
+    before += __shfl_xor(before, 1);
+    before += __shfl_xor(before, 2);
+    before += __shfl_xor(before, 4);
+    if ((threadIdx.x & 7) == 0) A.order[before] = i;     // the last one's spare lanes repeat it
+}
+
+// The saved state of the group of kSteps rows that begins at `row`
+__device__ __forceinline__ int64_t saved_row(const ScanSpan &s, int row)
+{
+    return (int64_t)s.first / kSteps + s.seg + (row - s.first) / kSteps;
 }
 
 enum { kScanWhole = 0, kScanSum = 1, kScanApply = 2 };
 
-// What the pairs (A, H) of the sample's chunks before this one (after it, in the
-// backward) make of the state v: each wavefront folds its share of the pairs, and the
-// W results meet in LDS.
-template <int VEC, int W, bool REVERSE>
-__device__ __forceinline__ void chunk_state(const ScanArgs &A, const ScanSpan &s, int w, uint32_t c,
-                                            float (&pa)[W][64 * VEC], float (&ph)[W][64 * VEC], float *v)
+// the other half's value of the same lane & 31
+__device__ __forceinline__ float other_half(float x)
 {
-    const int64_t here = s.tile - s.tile0, n = REVERSE ? s.chunks - 1 - here : here, C = A.channels;
-    const int64_t i0 = n * w / W, i1 = n * (w + 1) / W;
-    const int lane = lane_id();
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(lane_id() < 32 ? r[1] : r[0]);
+}
+
+// What the pairs (A, H) of the sample's chunks before this one (after it, in the
+// backward) make of the state v: each half wavefront folds its share of the pairs, and
+// the results meet in LDS.
+template <int VEC, int W, bool REVERSE>
+__device__ __forceinline__ void chunk_state(const ScanArgs &A, const ScanSpan &s, int unit, int c, bool live,
+                                            float (&pa)[2 * W][32 * VEC], float (&ph)[2 * W][32 * VEC], float *v)
+{
+    const int here = s.tile - s.tile0, n = max(REVERSE ? s.chunks - 1 - here : here, 0);
+    const int i0 = n * unit / (2 * W), i1 = n * (unit + 1) / (2 * W), hl = lane_id() & 31;
+    const int64_t C = A.channels;
     float a[VEC], h[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; e++) {
@@ -145,16 +221,16 @@ __device__ __forceinline__ void chunk_state(const ScanArgs &A, const ScanSpan &s
         h[e] = 0.f;
     }
     constexpr int kAhead = 8;    // pairs loaded before the first is needed
-    for (int64_t i = i0; i < i1; i += kAhead) {
+    for (int i = i0; i < i1; i += kAhead) {
         float ra[kAhead][VEC], rh[kAhead][VEC];
 #pragma unroll
         for (int j = 0; j < kAhead; j++) {
-            const int64_t k = i + j < i1 ? i + j : i1 - 1;
-            const int64_t t = s.tile0 + (REVERSE ? s.chunks - 1 - k : k);
+            const int k = i + j < i1 ? i + j : i1 - 1;
+            const int64_t t = (s.tile0 + (REVERSE ? s.chunks - 1 - k : k)) * C + (live ? c : 0);
 #pragma unroll
             for (int e = 0; e < VEC; e++) {
-                ra[j][e] = row_load<float>(A.sum_a, t, C, c + e);
-                rh[j][e] = row_load<float>(A.sum_h, t, C, c + e);
+                ra[j][e] = *gp(A.sum_a + t + e);
+                rh[j][e] = *gp(A.sum_h + t + e);
             }
         }
 #pragma unroll
@@ -168,78 +244,88 @@ __device__ __forceinline__ void chunk_state(const ScanArgs &A, const ScanSpan &s
     }
 #pragma unroll
     for (int e = 0; e < VEC; e++) {
-        pa[w][lane * VEC + e] = a[e];
-        ph[w][lane * VEC + e] = h[e];
+        pa[unit][hl * VEC + e] = a[e];
+        ph[unit][hl * VEC + e] = h[e];
     }
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < W; u++)
+    for (int u = 0; u < 2 * W; u++)
 #pragma unroll
-        for (int e = 0; e < VEC; e++) v[e] = fmaf(pa[u][lane * VEC + e], v[e], ph[u][lane * VEC + e]);
+        for (int e = 0; e < VEC; e++) v[e] = fmaf(pa[u][hl * VEC + e], v[e], ph[u][hl * VEC + e]);
     __syncthreads();
 }
 
-// W wavefronts walk a sample (or chunk) in blocks of W * kScanSteps rows: each
-// loads its own kScanSteps rows of 64 * VEC channels, scans them from a zero state
-// into (A, H) with h_out = A h_in + H, the W pairs meet in LDS, and each wavefront
-// applies its rows from the state that the pairs before it give.  One pass over the
-// data; the state stays in fp32 registers.  Rows past the end and masked ones load
-// some other row of the sample and count as a = 1, x = 0; the next block's rows are
-// loaded before this block's arithmetic.
+// rows that nobody owns give zero
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void zero_rows(void *p, const ScanSpan &s, int64_t C, int unit, int c, bool live)
+{
+    const float z[VEC] = {};
+    for (int t = s.begin; t < s.end; t += 2 * W) {
+        const Rows<T, VEC> r(p, C, t, min(s.end - t, 2 * W), unit, c, live);
+        r.store(0, z);
+    }
+}
+
+// W wavefronts walk a sample (or chunk) in blocks of 2 W kSteps rows: each half
+// wavefront loads its own kSteps rows of 32 * VEC channels (so a load covers two rows,
+// and 64 channels of bf16 are a workgroup's: there are enough workgroups to even out
+// samples of very different lengths), scans them from a zero state into (A, H) with
+// h_out = A h_in + H; two halves make a wavefront's pair, the W pairs meet in LDS, and
+// each half applies its rows from the state that the pairs before it give.  One pass
+// over the data; the state stays in fp32 registers.  Rows past the end and masked ones
+// count as a = 1, x = 0; the next block's rows are loaded before this block's last step.
 template <typename T, int VEC, int W, int PHASE>
-__global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_forward(ScanArgs A)
+__global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs A)
 {
     typedef Chan<T, VEC> CH;
     typedef typename CH::Raw Raw;
-    __shared__ float pa[2][W][64 * VEC], ph[2][W][64 * VEC];
-    const int lane = lane_id(), w = uniform((int)(threadIdx.x >> 6));
-    const uint32_t cw = (blockIdx.y * 64 + lane) * VEC;
-    const bool live = cw < (uint32_t)A.channels;
-    const uint32_t c = live ? cw : 0;      // lanes past the last channel repeat the first
+    constexpr int kRows = 2 * W * kSteps;
+    __shared__ float pa[2][2 * W][32 * VEC], ph[2][2 * W][32 * VEC];
+    const int lane = lane_id(), hl = lane & 31, half = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
+    const int unit = 2 * w + half, c = (blockIdx.y * 32 + hl) * VEC;
+    const bool live = c < A.channels;
     const int64_t C = A.channels;
     ScanSpan s;
     if (!scan_span(A, blockIdx.x, s)) return;
-    const T *x = static_cast<const T *>(A.x), *gate = static_cast<const T *>(A.gate);
-    T *y = static_cast<T *>(A.y);
     if (s.seg == 0 || s.seg == A.samples + 1) {
-        const float z[VEC] = {};
-        if (PHASE != kScanSum && live)
-            for (int64_t t = s.begin + w; t < s.end; t += W) row_store(y, t, C, c, CH::pack(z));
+        if (PHASE != kScanSum) zero_rows<T, VEC, W>(A.y, s, C, unit, c, live);
         return;
     }
     float h[VEC], ta[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
-        h[v] = PHASE != kScanSum && A.state ? A.state[(int64_t)(s.seg - 1) * C + c + v] : 0.f;
+        h[v] = PHASE != kScanSum && A.state && live ? A.state[(s.seg - 1) * C + c + v] : 0.f;
         ta[v] = 1.f;
     }
-    if (PHASE == kScanApply) chunk_state<VEC, W, false>(A, s, w, c, pa[0], ph[0], h);
+    if (PHASE == kScanApply) chunk_state<VEC, W, false>(A, s, unit, c, live, pa[0], ph[0], h);
 
-    Raw xn[kScanSteps], gn[kScanSteps];
-    uint32_t keep = 0;
-    auto load = [&](int64_t t0) {
-        const int64_t mine = t0 + w * kScanSteps;
-        keep = lane < kScanSteps && mine + lane < s.end ? (A.mask ? *gp(A.mask + mine + lane) : 1) : 0;
+    Raw xn[kSteps], gn[kSteps];
+    int keep = 0;
+    auto load = [&](int t0) {
+        const int row = t0 + unit * kSteps + (hl & (kSteps - 1));
+        keep = row < s.end ? (A.mask ? *gp(A.mask + row) : 1) : 0;
+        const int rows = min(s.end - t0, kRows);
+        const Rows<T, VEC> x(A.x, A.xs, t0, rows, unit * kSteps, c, live);
+        const Rows<T, VEC> g(A.gate, A.gs, t0, rows, unit * kSteps, c, live);
 #pragma unroll
-        for (int i = 0; i < kScanSteps; i++) {
-            const int64_t row = mine + i < s.end ? mine + i : s.end - 1;
-            xn[i] = row_load<Raw>(x, row, A.xs, c);
-            gn[i] = row_load<Raw>(gate, row, A.gs, c);
+        for (int i = 0; i < kSteps; i++) {
+            xn[i] = x.load(i);
+            gn[i] = g.load(i);
         }
     };
     if (s.begin < s.end) load(s.begin);
     int buf = 0;
-    for (int64_t t0 = s.begin; t0 < s.end; t0 += W * kScanSteps, buf ^= 1) {
-        const int64_t mine = t0 + w * kScanSteps;
-        const uint32_t bits = (uint32_t)__ballot(keep != 0);
-        float xs[kScanSteps][VEC], as[kScanSteps][VEC], la[VEC], lh[VEC];
+    for (int t0 = s.begin; t0 < s.end; t0 += kRows, buf ^= 1) {
+        const uint64_t all = __ballot(keep != 0);
+        const uint32_t bits = half ? (uint32_t)(all >> 32) : (uint32_t)all;
+        float xs[kSteps][VEC], as[kSteps][VEC], la[VEC], lh[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
             la[v] = 1.f;
             lh[v] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kScanSteps; i++) {
+        for (int i = 0; i < kSteps; i++) {
             const bool on = bits >> i & 1;
             CH::open(xn[i], xs[i]);
             CH::open(gn[i], as[i]);
@@ -252,11 +338,17 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_forward(ScanArgs 
                 la[v] *= as[i][v];
             }
         }
-        if (t0 + W * kScanSteps < s.end) load(t0 + W * kScanSteps);
+        if (t0 + kRows < s.end) load(t0 + kRows);
+        float oa[VEC], oh[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
-            pa[buf][w][lane * VEC + v] = la[v];
-            ph[buf][w][lane * VEC + v] = lh[v];
+            oa[v] = other_half(la[v]);
+            oh[v] = other_half(lh[v]);
+            // half 0's pair, then half 1's
+            if (half == 0) {
+                pa[buf][w][hl * VEC + v] = la[v] * oa[v];
+                ph[buf][w][hl * VEC + v] = fmaf(oa[v], lh[v], oh[v]);
+            }
         }
         __syncthreads();
         float in[VEC];
@@ -267,29 +359,35 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_forward(ScanArgs 
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 if (u == w) in[v] = h[v];
-                const float ua = pa[buf][u][lane * VEC + v];
-                h[v] = fmaf(ua, h[v], ph[buf][u][lane * VEC + v]);
+                const float ua = pa[buf][u][hl * VEC + v];
+                h[v] = fmaf(ua, h[v], ph[buf][u][hl * VEC + v]);
                 if (PHASE == kScanSum) ta[v] *= ua;
             }
         if (PHASE == kScanSum) continue;
+        const int mine = t0 + unit * kSteps;
+        const bool save = A.ckpt && live && mine < s.end;
+        const int64_t group = save ? saved_row(s, mine) * C + c : 0;
+        const Rows<T, VEC> y(A.y, C, t0, min(s.end - t0, kRows), unit * kSteps, c, live);
 #pragma unroll
-        for (int i = 0; i < kScanSteps; i++) {
-            if (A.ckpt && i % kSaved == 0 && live && mine + i < s.end)
+        for (int v = 0; v < VEC; v++) {
+            if (half) in[v] = fmaf(oa[v], in[v], oh[v]);
+            if (save) *gp(A.ckpt + group + v) = in[v];
+        }
 #pragma unroll
-                for (int v = 0; v < VEC; v++) row_store(A.ckpt, saved_row(s, mine + i), C, c + v, in[v]);
+        for (int i = 0; i < kSteps; i++) {
 #pragma unroll
             for (int v = 0; v < VEC; v++) in[v] = fmaf(as[i][v], in[v], xs[i][v]);
-            if (live && mine + i < s.end) row_store(y, mine + i, C, c, CH::pack(in));
+            y.store(i, in);
         }
     }
-    if (!live || w != 0) return;
+    if (!live || unit != 0) return;
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
         if (PHASE == kScanWhole || (PHASE == kScanApply && s.tile - s.tile0 >= s.chunks - 1))
-            A.last[(int64_t)(s.seg - 1) * C + c + v] = h[v];
+            A.last[(s.seg - 1) * C + c + v] = h[v];
         if (PHASE == kScanSum) {
-            row_store(A.sum_a, s.tile, C, c + v, ta[v]);
-            row_store(A.sum_h, s.tile, C, c + v, h[v]);
+            A.sum_a[s.tile * C + c + v] = ta[v];
+            A.sum_h[s.tile * C + c + v] = h[v];
         }
     }
 }
@@ -297,67 +395,67 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_forward(ScanArgs 
 // The backward pass walks the same blocks from the last to the first.  With
 // u_t = a_t g_t the carried quantity, g_t = dy_t + u_(t+1) is the gradient of h_t,
 // again a linear recurrence.  The states h_(t-1) that dgate needs are scanned again
-// from the saved state before each group of kSaved rows: an eighth of the states in
+// from the saved state before each group of kSteps rows: an eighth of the states in
 // fp32 is a quarter of what all of them in bf16 would cost, and exact.
 template <typename T, int VEC, int W, int PHASE>
-__global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_backward(ScanArgs A)
+__global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs A)
 {
     typedef Chan<T, VEC> CH;
     typedef typename CH::Raw Raw;
-    __shared__ float pa[2][W][64 * VEC], ph[2][W][64 * VEC];
-    const int lane = lane_id(), w = uniform((int)(threadIdx.x >> 6));
-    const uint32_t cw = (blockIdx.y * 64 + lane) * VEC;
-    const bool live = cw < (uint32_t)A.channels;
-    const uint32_t c = live ? cw : 0;
+    constexpr int kRows = 2 * W * kSteps;
+    __shared__ float pa[2][2 * W][32 * VEC], ph[2][2 * W][32 * VEC];
+    const int lane = lane_id(), hl = lane & 31, half = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
+    const int unit = 2 * w + half, c = (blockIdx.y * 32 + hl) * VEC;
+    const bool live = c < A.channels;
     const int64_t C = A.channels;
     ScanSpan s;
     if (!scan_span(A, blockIdx.x, s)) return;
-    const T *x = static_cast<const T *>(A.x), *gate = static_cast<const T *>(A.gate);
-    const T *dy = static_cast<const T *>(A.dy);
-    T *dx = static_cast<T *>(A.dx), *dgate = static_cast<T *>(A.dgate);
     if (s.seg == 0 || s.seg == A.samples + 1) {
-        const float z[VEC] = {};
-        if (PHASE != kScanSum && live)
-            for (int64_t t = s.begin + w; t < s.end; t += W) {
-                row_store(dx, t, C, c, CH::pack(z));
-                row_store(dgate, t, C, c, CH::pack(z));
-            }
+        if (PHASE != kScanSum) {
+            zero_rows<T, VEC, W>(A.dx, s, C, unit, c, live);
+            zero_rows<T, VEC, W>(A.dgate, s, C, unit, c, live);
+        }
         return;
     }
     float u[VEC], ta[VEC];
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
-        u[v] = PHASE != kScanSum && A.dlast ? A.dlast[(int64_t)(s.seg - 1) * C + c + v] : 0.f;
+        u[v] = PHASE != kScanSum && A.dlast && live ? A.dlast[(s.seg - 1) * C + c + v] : 0.f;
         ta[v] = 1.f;
     }
-    if (PHASE == kScanApply) chunk_state<VEC, W, true>(A, s, w, c, pa[0], ph[0], u);
+    if (PHASE == kScanApply) chunk_state<VEC, W, true>(A, s, unit, c, live, pa[0], ph[0], u);
 
-    constexpr int kRows = W * kBackSteps;
-    const int64_t blocks = s.end > s.begin ? (s.end - s.begin + kRows - 1) / kRows : 0;
-    Raw xn[kBackSteps], gn[kBackSteps], dn[kBackSteps];
+    const int blocks = (s.end - s.begin + kRows - 1) / kRows;
+    Raw xn[kSteps], gn[kSteps], dn[kSteps];
     float hn[VEC];
-    uint32_t keep = 0;
-    auto load = [&](int64_t b) {
-        const int64_t mine = s.begin + b * kRows + w * kBackSteps;
-        keep = lane < kBackSteps && mine + lane < s.end ? (A.mask ? *gp(A.mask + mine + lane) : 1) : 0;
+    int keep = 0;
+    auto load = [&](int b) {
+        const int t0 = s.begin + b * kRows, mine = t0 + unit * kSteps, row = mine + (hl & (kSteps - 1));
+        keep = row < s.end ? (A.mask ? *gp(A.mask + row) : 1) : 0;
+        const int rows = min(s.end - t0, kRows);
+        const Rows<T, VEC> x(A.x, A.xs, t0, rows, unit * kSteps, c, live);
+        const Rows<T, VEC> g(A.gate, A.gs, t0, rows, unit * kSteps, c, live);
+        const Rows<T, VEC> d(A.dy, C, t0, rows, unit * kSteps, c, live);
 #pragma unroll
-        for (int i = 0; i < kBackSteps; i++) {
-            const int64_t row = mine + i < s.end ? mine + i : s.end - 1;
-            if (PHASE != kScanSum) xn[i] = row_load<Raw>(x, row, A.xs, c);
-            gn[i] = row_load<Raw>(gate, row, A.gs, c);
-            dn[i] = row_load<Raw>(dy, row, C, c);
+        for (int i = 0; i < kSteps; i++) {
+            if (PHASE != kScanSum) xn[i] = x.load(i);
+            gn[i] = g.load(i);
+            dn[i] = d.load(i);
         }
+        if (PHASE == kScanSum) return;
+        const int64_t group = saved_row(s, mine < s.end ? mine : s.begin) * C + (live ? c : 0);
 #pragma unroll
-        for (int v = 0; v < VEC; v++)
-            if (PHASE != kScanSum)
-                hn[v] = row_load<float>(A.ckpt, saved_row(s, mine < s.end ? mine : s.begin), C, c + v);
+        for (int v = 0; v < VEC; v++) hn[v] = *gp(A.ckpt + group + v);
     };
     if (blocks) load(blocks - 1);
     int buf = 0;
-    for (int64_t b = blocks - 1; b >= 0; b--, buf ^= 1) {
-        const int64_t mine = s.begin + b * kRows + w * kBackSteps;
-        const uint32_t bits = (uint32_t)__ballot(keep != 0);
-        float xs[kBackSteps][VEC], as[kBackSteps][VEC], na[kBackSteps][VEC], ds[kBackSteps][VEC], hin[VEC];
+    for (int b = blocks - 1; b >= 0; b--, buf ^= 1) {
+        const int t0 = s.begin + b * kRows;
+        const uint64_t all = __ballot(keep != 0);
+        const uint32_t bits = half ? (uint32_t)(all >> 32) : (uint32_t)all;
+        // x and dy stay as they lie in memory until they are needed: half the registers in bf16
+        Raw xr[kSteps], dr[kSteps];
+        float as[kSteps][VEC], na[kSteps][VEC], hin[VEC];
         float la[VEC], lu[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
@@ -366,25 +464,31 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_backward(ScanArgs
             hin[v] = PHASE != kScanSum ? hn[v] : 0.f;
         }
 #pragma unroll
-        for (int i = kBackSteps - 1; i >= 0; i--) {
-            const bool on = bits >> i & 1, in = mine + i < s.end;
+        for (int i = kSteps - 1; i >= 0; i--) {
+            const bool on = bits >> i & 1;
+            float d[VEC];
             CH::open(gn[i], as[i]);
-            CH::open(dn[i], ds[i]);
-            if (PHASE != kScanSum) CH::open(xn[i], xs[i]);
+            CH::open(dn[i], d);          // zero past the end
+            dr[i] = dn[i];
+            if (PHASE != kScanSum) xr[i] = on ? xn[i] : Raw{};
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 sigmoid_pair(on ? as[i][v] : INFINITY, as[i][v], na[i][v]);
-                ds[i][v] = in ? ds[i][v] : 0.f;
-                if (PHASE != kScanSum) xs[i][v] = on ? xs[i][v] : 0.f;
-                lu[v] = as[i][v] * (ds[i][v] + lu[v]);
+                lu[v] = as[i][v] * (d[v] + lu[v]);
                 la[v] *= as[i][v];
             }
         }
         if (b > 0) load(b - 1);
+        float oa[VEC], ou[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; v++) {
-            pa[buf][w][lane * VEC + v] = la[v];
-            ph[buf][w][lane * VEC + v] = lu[v];
+            oa[v] = other_half(la[v]);
+            ou[v] = other_half(lu[v]);
+            // half 1's pair, then half 0's
+            if (half == 0) {
+                pa[buf][w][hl * VEC + v] = la[v] * oa[v];
+                ph[buf][w][hl * VEC + v] = fmaf(la[v], ou[v], lu[v]);
+            }
         }
         __syncthreads();
         float in[VEC];
@@ -395,44 +499,53 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 4 : 1) void scan_backward(ScanArgs
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 if (p == w) in[v] = u[v];
-                const float pv = pa[buf][p][lane * VEC + v];
-                u[v] = fmaf(pv, u[v], ph[buf][p][lane * VEC + v]);
+                const float pv = pa[buf][p][hl * VEC + v];
+                u[v] = fmaf(pv, u[v], ph[buf][p][hl * VEC + v]);
                 if (PHASE == kScanSum) ta[v] *= pv;
             }
         if (PHASE == kScanSum) continue;
-        // forward again: xs becomes h_(t-1) - x_t, what dgate multiplies
 #pragma unroll
-        for (int i = 0; i < kBackSteps; i++)
+        for (int v = 0; v < VEC; v++)
+            if (!half) in[v] = fmaf(oa[v], in[v], ou[v]);
+        // forward again: h_(t-1) - x_t, what dgate multiplies
+        float diff[kSteps][VEC];
+#pragma unroll
+        for (int i = 0; i < kSteps; i++) {
+            float x[VEC];
+            CH::open(xr[i], x);
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 const float before = hin[v];
-                hin[v] = fmaf(as[i][v], before, na[i][v] * xs[i][v]);
-                xs[i][v] = before - xs[i][v];
-            }
-#pragma unroll
-        for (int i = kBackSteps - 1; i >= 0; i--) {
-            float gx[VEC], gg[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; v++) {
-                const float g = ds[i][v] + in[v];
-                in[v] = as[i][v] * g;
-                gx[v] = na[i][v] * g;                        // a masked row has na = 0
-                gg[v] = as[i][v] * xs[i][v] * gx[v];
-            }
-            if (live && mine + i < s.end) {
-                row_store(dx, mine + i, C, c, CH::pack(gx));
-                row_store(dgate, mine + i, C, c, CH::pack(gg));
+                hin[v] = fmaf(as[i][v], before, na[i][v] * x[v]);
+                diff[i][v] = before - x[v];
             }
         }
+        const int rows = min(s.end - t0, kRows);
+        const Rows<T, VEC> dx(A.dx, C, t0, rows, unit * kSteps, c, live);
+        const Rows<T, VEC> dg(A.dgate, C, t0, rows, unit * kSteps, c, live);
+#pragma unroll
+        for (int i = kSteps - 1; i >= 0; i--) {
+            float gx[VEC], gg[VEC], d[VEC];
+            CH::open(dr[i], d);
+#pragma unroll
+            for (int v = 0; v < VEC; v++) {
+                const float g = d[v] + in[v];
+                in[v] = as[i][v] * g;
+                gx[v] = na[i][v] * g;                        // a masked row has na = 0
+                gg[v] = as[i][v] * diff[i][v] * gx[v];
+            }
+            dx.store(i, gx);
+            dg.store(i, gg);
+        }
     }
-    if (!live || w != 0) return;
+    if (!live || unit != 0) return;
 #pragma unroll
     for (int v = 0; v < VEC; v++) {
         if (A.dstate && (PHASE == kScanWhole || (PHASE == kScanApply && s.tile == s.tile0)))
-            A.dstate[(int64_t)(s.seg - 1) * C + c + v] = u[v];
+            A.dstate[(s.seg - 1) * C + c + v] = u[v];
         if (PHASE == kScanSum) {
-            row_store(A.sum_a, s.tile, C, c + v, ta[v]);
-            row_store(A.sum_h, s.tile, C, c + v, u[v]);
+            A.sum_a[s.tile * C + c + v] = ta[v];
+            A.sum_h[s.tile * C + c + v] = u[v];
         }
     }
 }
@@ -468,29 +581,35 @@ using namespace emb;
 namespace {
 
 struct ScanPlan {
-    int waves, vec;
-    int32_t chunk;               // cut samples into chunks
-    int64_t tiles, ckpt_rows;
+    int waves;
+    int32_t chunk, ordered;      // cut samples into chunks; walk the long ones first
+    int64_t tiles, saved;
 };
 
 // One workgroup walks a whole sample when the samples and channel blocks alone fill
-// the chip; otherwise samples are cut into chunks.
+// the chip, the longest first where that can matter; otherwise samples are cut into
+// chunks.
 ScanPlan scan_plan(const emb_recurrence *r)
 {
     ScanPlan p{};
     const int64_t mean = r->samples ? r->n / r->samples : 0;
-    p.waves = mean <= 32 ? 1 : 8;
-    const int64_t per = r->dtype == EMB_BF16 ? 128 : 64;
-    const int64_t blocks = (r->channels + per - 1) / per;
-    p.chunk = 0;
+    const int per = r->dtype == EMB_BF16 ? 64 : 32;      // channels a workgroup
+    const int64_t items = (int64_t)r->samples * ((r->channels + per - 1) / per);
+    p.waves = mean <= 32 ? 1 : kWaves;
     p.tiles = r->samples + 2;
-    if (r->samples * blocks < 512 && mean >= 1024) {
+    if (items < 512 && mean >= 1024) {
         p.chunk = 1;
         p.tiles = seg_tiles(r->n, r->samples, 1, kChunk);
+    } else if (items >= 256 && items <= 8192 && r->samples > 1 && r->samples <= kOrderMost && mean >= 256) {
+        p.ordered = 1;
     }
-    p.ckpt_rows = seg_tiles(r->n, r->samples, 1, kSaved);
+    p.saved = seg_tiles(r->n, r->samples, 1, kSteps);
     return p;
 }
+
+// the rows of a block lie within the 2^31 bytes that a buffer descriptor reaches
+constexpr int64_t kStrideMost = (int64_t(1) << 21) - 1;
+static_assert(kStrideMost * 4 * 2 * kWaves * kSteps < int64_t(1) << 31, "a block of rows fits a descriptor");
 
 emb_status scan_check(const emb_recurrence *r)
 {
@@ -501,8 +620,10 @@ emb_status scan_check(const emb_recurrence *r)
     if (r->channels > (1 << 20)) return fail(EMB_ERR_UNSUPPORTED, "recurrence: channels must be <= 2^20");
     if (r->n > kRowsMost || r->samples > (1 << 30))
         return fail(EMB_ERR_UNSUPPORTED, "recurrence: n must be <= 2^31 - 65536 and samples <= 2^30");
-    if (r->x_stride < 0 || r->gate_stride < 0)
-        return fail(EMB_ERR_INVALID_ARG, "recurrence: row strides must be >= 0");
+    if (r->n > 1 && (r->x_stride < r->channels || r->gate_stride < r->channels))
+        return fail(EMB_ERR_INVALID_ARG, "recurrence: row strides must be >= channels");
+    if (r->x_stride > kStrideMost || r->gate_stride > kStrideMost)
+        return fail(EMB_ERR_UNSUPPORTED, "recurrence: row strides must be < 2^21");
     return EMB_OK;
 }
 
@@ -521,7 +642,7 @@ size_t pad256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t scan_workspace(const emb_recurrence *r, const ScanPlan &p)
 {
-    return p.chunk ? 2 * pad256((size_t)p.tiles * r->channels * 4) : 0;
+    return p.chunk ? 2 * pad256((size_t)p.tiles * r->channels * 4) : p.ordered ? (size_t)p.tiles * 4 : 0;
 }
 
 // channels in pairs: an even count, and every row aligned to a pair
@@ -538,8 +659,10 @@ bool pairs_ok(const emb_recurrence *r, std::initializer_list<const void *> same)
 template <typename T, int VEC, int W>
 emb_status scan_launch_w(const ScanArgs &A, bool backward, hipStream_t st)
 {
-    const int64_t blocks = (A.channels + 64 * VEC - 1) / (64 * VEC);
+    const int64_t blocks = (A.channels + 32 * VEC - 1) / (32 * VEC);
     const dim3 grid((unsigned)A.tiles, (unsigned)blocks), block(64 * W);
+    if (A.order)
+        hipLaunchKernelGGL(scan_order, dim3((unsigned)((A.tiles + 31) / 32)), dim3(256), 0, st, A);
     if (A.chunk == 0) {
         if (backward) hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanWhole>), grid, block, 0, st, A);
         else hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanWhole>), grid, block, 0, st, A);
@@ -558,7 +681,7 @@ emb_status scan_launch_w(const ScanArgs &A, bool backward, hipStream_t st)
 template <typename T, int VEC>
 emb_status scan_launch_v(const ScanArgs &A, int waves, bool backward, hipStream_t st)
 {
-    return waves == 1 ? scan_launch_w<T, VEC, 1>(A, backward, st) : scan_launch_w<T, VEC, 8>(A, backward, st);
+    return waves == 1 ? scan_launch_w<T, VEC, 1>(A, backward, st) : scan_launch_w<T, VEC, kWaves>(A, backward, st);
 }
 
 emb_status scan_launch(const emb_recurrence *r, const ScanArgs &A, int waves, bool pairs, bool backward,
@@ -586,6 +709,7 @@ ScanArgs scan_args(const emb_recurrence *r, const ScanPlan &p, void *ws)
     A.channels = r->channels;
     A.chunk = p.chunk;
     A.tiles = p.tiles;
+    if (p.ordered) A.order = static_cast<int32_t *>(ws);
     if (p.chunk) {
         const size_t part = pad256((size_t)p.tiles * r->channels * 4);
         A.sum_a = reinterpret_cast<float *>(ws);
@@ -602,7 +726,7 @@ extern "C" emb_status emb_recurrence_query(const emb_recurrence *r, int64_t *sav
     if (s != EMB_OK) return s;
     if (!saved_rows || !workspace_bytes) return fail(EMB_ERR_INVALID_ARG, "recurrence: output pointers must be given");
     const ScanPlan p = scan_plan(r);
-    *saved_rows = p.ckpt_rows;
+    *saved_rows = p.saved;
     *workspace_bytes = scan_workspace(r, p);
     return EMB_OK;
 }
@@ -619,7 +743,7 @@ extern "C" emb_status emb_recurrence_forward(const emb_recurrence *r, void *y, f
     const ScanPlan p = scan_plan(r);
     if (workspace_bytes < scan_workspace(r, p) || (scan_workspace(r, p) && !aligned(workspace, 256)))
         return fail(EMB_ERR_WORKSPACE, "recurrence: the workspace is smaller than the query returned, or not 256-byte aligned");
-    if (p.chunk && !workspace) return fail(EMB_ERR_WORKSPACE, "recurrence: workspace is NULL");
+    if (scan_workspace(r, p) && !workspace) return fail(EMB_ERR_WORKSPACE, "recurrence: workspace is NULL");
     ScanArgs A = scan_args(r, p, workspace);
     A.y = y;
     A.last = last;
@@ -643,7 +767,7 @@ extern "C" emb_status emb_recurrence_backward(const emb_recurrence *r, const flo
     const ScanPlan p = scan_plan(r);
     if (workspace_bytes < scan_workspace(r, p) || (scan_workspace(r, p) && !aligned(workspace, 256)))
         return fail(EMB_ERR_WORKSPACE, "recurrence: the workspace is smaller than the query returned, or not 256-byte aligned");
-    if (p.chunk && !workspace) return fail(EMB_ERR_WORKSPACE, "recurrence: workspace is NULL");
+    if (scan_workspace(r, p) && !workspace) return fail(EMB_ERR_WORKSPACE, "recurrence: workspace is NULL");
     ScanArgs A = scan_args(r, p, workspace);
     A.dy = dy;
     A.dlast = dlast;
