@@ -763,9 +763,14 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     walk.start();
     B.put(A, kvh, lb, lbnd);
     R.range();
-    if (WM == 1) __syncthreads();     // the bias table; with WM = 4 the walk's barriers cover it
+    if (A.bias) __syncthreads();      // the bias table
     BucketRun run{0, INT32_MAX, INT32_MIN};
     float b_run = 0.f;
+    if (A.bias && walk.at < walk.end) {
+        // the first keys' bucket, while they are on their way
+        run.set(B, lbnd, B.bucket(sub_sat(R.r.lo, half_range(walk.pos_next).hi)));
+        b_run = lb[run.m * A.group + R.g] * A.c;
+    }
 
     float m = -INFINITY, l = 0.f;
     f32x16_t o[DP / 32];
@@ -986,9 +991,14 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     }
     // a row without keys has lse = -inf: exp2(score - inf) keeps its weights zero
     lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
-    if (WM == 1) __syncthreads();
+    if (A.bias) __syncthreads();      // the bias table
     BucketRun run{0, INT32_MAX, INT32_MIN};
     float b_run = 0.f;
+    if (A.bias && walk.at < walk.end) {
+        // the first keys' bucket, while they are on their way
+        run.set(B, lbnd, B.bucket(sub_sat(R.r.lo, half_range(walk.pos_next).hi)));
+        b_run = lb[run.m * A.group + R.g] * A.c;
+    }
 
     float e = 0.f;                         // sum p (dP - D)
     f32x16_t x[DP / 32];
@@ -1202,6 +1212,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     const bool in = r < s.rows;
     const int64_t key = s.base + (in ? r : s.rows - 1);
     const int kpos = A.bias && !idle ? *gp(A.kp + key) : 0;
+    const int qpos0 = A.bias && stages ? *gp(A.qp + q0) : 0;
     const bool live = in && !idle && (!A.mask || *gp(A.mask + key));
     Frag<T, DP> kf, vf;
     load_frag<T, DP>(kf, static_cast<const T *>(A.k) + (live ? key * A.ks + kvh * A.kh : 0), A.dim, A.vec, live);
@@ -1218,6 +1229,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         tell(0);
         look(next);
     }
+    if (A.bias) __syncthreads();      // the bias table
 
     f32x16_t dk[DP / 32], dv[DP / 32];
 #pragma unroll
@@ -1225,6 +1237,10 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     // score gradients of the bucket at hand, a sum per lane until the bucket changes
     BucketRun run{0, INT32_MAX, INT32_MIN};
     float b_run = live ? 0.f : -INFINITY, sum_run = 0.f;
+    if (A.bias && stages) {
+        run.set(B, lbnd, B.bucket(sub_sat(qpos0, kr.hi)));
+        b_run = live ? lb[run.m * A.group] * A.c : -INFINITY;
+    }
     // (an LDS addition without an answer; only this wavefront adds to its own row, in order)
     auto settle = [&](int m, float sum) {
         sum = wave_sum(sum);
