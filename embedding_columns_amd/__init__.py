@@ -691,27 +691,24 @@ def _rows_ptr(t, ndim):
 
 
 def _want(t, name, dtype, shape, device):
-    """Address of a contiguous tensor of exactly this type and shape; 0 for None."""
-    if t is None:
-        return 0
+    """Address of a contiguous tensor of exactly this type and shape on this device (an index)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dtype is not dtype or t.shape != shape or t.device != device:
-        raise ValueError(f"{name}: expected {dtype} {shape} on {device}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} {tuple(shape)} on GPU {device}, got "
+                     f"{t.dtype} {tuple(t.shape)} of strides {t.stride()} on {t.device}")
 
 
 def _same(first, *others):
-    dtype, device = first.dtype, first.device
+    """The device index that `first` and the others share, their common type being one we take."""
+    dtype, device = first.dtype, first.get_device()
     if dtype not in _SEQ_DTYPE:
         raise ValueError(f"the sequence operators take float32 or bfloat16, got {dtype}")
     for t in others:
-        if t.dtype is not dtype or t.device != device:
+        if t.dtype is not dtype or t.get_device() != device:
             raise ValueError("tensors of one call must share their type and device")
-    if device.index != torch.cuda.current_device():
+    if device != torch.cuda.current_device():
         raise ValueError("tensors must be on the current device")
     return device
 
@@ -730,8 +727,13 @@ def _mask_ptr(mask, n, device):
     return _want(mask, "mask", torch.uint8, (n,), device)
 
 
-def _scratch(nbytes, device):
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+def _scratch(nbytes, like):
+    return like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
+
+
+def _address(t):
+    """Of a tensor made here."""
+    return None if t is None else t.data_ptr()
 
 
 def _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos, scale):
@@ -777,11 +779,13 @@ class CrossAttention(torch.autograd.Function):
     def forward(ctx, q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, scale):
         desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
                                scale)
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        rest = torch.empty_like(out) if q.dtype is torch.bfloat16 else None
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        out = q.new_empty(q.shape)
+        rest = q.new_empty(q.shape) if q.dtype is torch.bfloat16 else None
+        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
         need, ctx.need = emb_attention_query(desc)
-        emb_attention_forward(desc, out, rest, lse, _scratch(need, q.device))
+        ws = _scratch(need, q)
+        _check(lib().emb_attention_forward(C.byref(desc), out.data_ptr(), _address(rest),
+                                           lse.data_ptr(), _address(ws), need, _stream()))
         # the saved tensors keep alive, and unchanged, what the descriptor points to
         ctx.save_for_backward(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos,
                               out, rest, lse)
@@ -792,26 +796,23 @@ class CrossAttention(torch.autograd.Function):
     def backward(ctx, dout):
         _second_order()
         q, k, _, bias, _, _, _, _, _, _, out, rest, lse = ctx.saved_tensors
-        device = q.device
         if dout.dtype is not q.dtype:
             raise TypeError("the output's gradient must have the output's type")
         if dout.stride(-1) != 1 and dout.shape[-1] > 1:
             dout = dout.contiguous()
         want = ctx.needs_input_grad
-        dq = torch.empty(q.shape, dtype=q.dtype, device=device)
+        dq = q.new_empty(q.shape)
         dk = dv = dbias = None
         if want[1] or want[2]:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=device)
-            dv = torch.empty(k.shape, dtype=q.dtype, device=device)
+            dk, dv = k.new_empty(k.shape), k.new_empty(k.shape)
         if bias is not None and want[3]:
-            dbias = torch.empty(bias.shape, dtype=torch.float32, device=device)
-        emb_attention_backward(ctx.desc, out, rest, lse, dout, dq, dk, dv, dbias,
-                               _scratch(ctx.need, device))
+            dbias = bias.new_empty(bias.shape)
+        ws = _scratch(ctx.need, q)
+        _check(lib().emb_attention_backward(
+            C.byref(ctx.desc), out.data_ptr(), _address(rest), lse.data_ptr(), _rows_ptr(dout, 3),
+            dout.stride(0), dout.stride(1), dq.data_ptr(), _address(dk), _address(dv),
+            _address(dbias), _address(ws), ctx.need, _stream()))
         return dq, dk, dv, dbias, None, None, None, None, None, None, None
-
-
-def _needs_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundaries=None,
@@ -826,13 +827,17 @@ def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundar
     ascending, positions int32).  scale: dim ** -0.5 unless given.  Returns
     [n_q, heads, dim]; a row without any key gives zero.  Differentiable in q, k, v and
     bias; runs on the current stream."""
-    if _needs_grad(q, k, v, bias):
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
+                                    (bias is not None and bias.requires_grad)):
         return CrossAttention.apply(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos,
                                     k_pos, scale)
     desc = _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos,
                            scale)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    emb_attention_forward(desc, out, None, None, _scratch(emb_attention_query(desc)[0], q.device))
+    out = q.new_empty(q.shape)
+    need = emb_attention_query(desc)[0]
+    ws = _scratch(need, q)
+    _check(lib().emb_attention_forward(C.byref(desc), out.data_ptr(), None, None, _address(ws), need,
+                                       _stream()))
     return out
 
 
@@ -848,7 +853,7 @@ def _recurrence_desc(x, gate, offsets, state, mask):
     return RecurrenceDesc.from_buffer_copy(_RECURRENCE.pack(
         _SEQ_DTYPE[x.dtype], samples, channels, 0, n, xp, gp, x.stride(0), gate.stride(0),
         _offsets_ptr(offsets, "offsets", dev), _mask_ptr(mask, n, dev),
-        _want(state, "state", torch.float32, (samples, channels), dev)))
+        0 if state is None else _want(state, "state", torch.float32, (samples, channels), dev)))
 
 
 class GatedRecurrence(torch.autograd.Function):
@@ -857,12 +862,13 @@ class GatedRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, state, offsets, mask):
         desc = _recurrence_desc(x, gate, offsets, state, mask)
-        device = x.device
-        y = torch.empty(x.shape, dtype=x.dtype, device=device)
-        last = torch.empty((desc.samples, desc.channels), dtype=torch.float32, device=device)
+        y = x.new_empty(x.shape)
+        last = x.new_empty((desc.samples, desc.channels), dtype=torch.float32)
         rows, ctx.need = emb_recurrence_query(desc)
-        saved = torch.empty((rows, desc.channels), dtype=torch.float32, device=device)
-        emb_recurrence_forward(desc, y, last, saved, _scratch(ctx.need, device))
+        saved = x.new_empty((rows, desc.channels), dtype=torch.float32)
+        ws = _scratch(ctx.need, x)
+        _check(lib().emb_recurrence_forward(C.byref(desc), y.data_ptr(), last.data_ptr(),
+                                            saved.data_ptr(), _address(ws), ctx.need, _stream()))
         # the saved tensors keep alive, and unchanged, what the descriptor points to
         ctx.save_for_backward(x, gate, state, offsets, mask, saved)
         ctx.desc = desc
@@ -873,19 +879,18 @@ class GatedRecurrence(torch.autograd.Function):
     def backward(ctx, dy, dlast):
         _second_order()
         x, _, state, _, _, saved = ctx.saved_tensors
-        device = x.device
         if dy is None:
-            dy = torch.zeros(x.shape, dtype=x.dtype, device=device)
+            dy = x.new_zeros(x.shape)
         if dy.dtype is not x.dtype:
             raise TypeError("the output's gradient must have the output's type")
-        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
-        dgate = torch.empty(x.shape, dtype=x.dtype, device=device)
-        dstate = None
+        dy, dlast = dy.contiguous(), None if dlast is None else dlast.contiguous()
+        dx, dgate, dstate = x.new_empty(x.shape), x.new_empty(x.shape), None
         if state is not None and ctx.needs_input_grad[2]:
-            dstate = torch.empty_like(state)
-        emb_recurrence_backward(ctx.desc, saved, dy.contiguous(),
-                                None if dlast is None else dlast.contiguous(), dx, dgate, dstate,
-                                _scratch(ctx.need, device))
+            dstate = state.new_empty(state.shape)
+        ws = _scratch(ctx.need, x)
+        _check(lib().emb_recurrence_backward(
+            C.byref(ctx.desc), saved.data_ptr(), dy.data_ptr(), _address(dlast), dx.data_ptr(),
+            dgate.data_ptr(), _address(dstate), _address(ws), ctx.need, _stream()))
         return dx, dgate, dstate, None, None
 
 
@@ -897,13 +902,16 @@ def gated_recurrence(x, gate, offsets, state=None, mask=None):
     mask: uint8 or bool [n], 0 keeps the state as it is.  Returns (y [n, channels], the
     states at every row, last fp32 [samples, channels], those after the last rows).
     Differentiable in x, gate and state; runs on the current stream."""
-    if _needs_grad(x, gate, state):
+    if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or
+                                    (state is not None and state.requires_grad)):
         return GatedRecurrence.apply(x, gate, state, offsets, mask)
     desc = _recurrence_desc(x, gate, offsets, state, mask)
-    device = x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=device)
-    last = torch.empty((desc.samples, desc.channels), dtype=torch.float32, device=device)
-    emb_recurrence_forward(desc, y, last, None, _scratch(emb_recurrence_query(desc)[1], device))
+    y = x.new_empty(x.shape)
+    last = x.new_empty((desc.samples, desc.channels), dtype=torch.float32)
+    need = emb_recurrence_query(desc)[1]
+    ws = _scratch(need, x)
+    _check(lib().emb_recurrence_forward(C.byref(desc), y.data_ptr(), last.data_ptr(), None,
+                                        _address(ws), need, _stream()))
     return y, last
 
 
@@ -911,18 +919,19 @@ def gated_recurrence_step(x, gate, state, out=None):
     """One step of the recurrence for a batch of states (serving): x, gate [rows, channels],
     state fp32 [rows, channels], updated in place; returns it in x's type.  Not
     differentiable."""
-    _rows_ptr(x, 2), _rows_ptr(gate, 2)
+    xp, gp = _rows_ptr(x, 2), _rows_ptr(gate, 2)
     dev = _same(x, gate)
     if gate.shape != x.shape:
         raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
-    if state is None:
-        raise TypeError("state: expected a torch.Tensor")
-    _want(state, "state", torch.float32, x.shape, dev)
+    sp = _want(state, "state", torch.float32, x.shape, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = x.new_empty(x.shape)
+        yp = out.data_ptr()
     else:
-        _want(out, "out", x.dtype, x.shape, dev)
-    if _needs_grad(x, gate, state):
+        yp = _want(out, "out", x.dtype, x.shape, dev)
+    if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
         raise ValueError("gated_recurrence_step has no gradient: use gated_recurrence")
-    emb_recurrence_step(x, gate, state, out)
+    rows, channels = x.shape
+    _check(lib().emb_recurrence_step(_SEQ_DTYPE[x.dtype], rows, channels, xp, x.stride(0), gp,
+                                     gate.stride(0), sp, yp, _stream()))
     return out
