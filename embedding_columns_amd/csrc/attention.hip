@@ -519,6 +519,12 @@ __device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *row, int dim,
     }
 }
 
+// Whether a block of products starts from its bias or gets it added.  bf16 products of a
+// head are 2 to 8 accumulations and the start costs nothing; fp32 products are four times
+// as many, and rounding each at the bias's size would cost the gradients a digit.
+template <typename T>
+constexpr bool kBiasFirst = sizeof(T) == 2;
+
 // Scores in units of log2 are t_i = c s_i + b with s_i the product (plus what the block
 // started from) and b a number per row: where all pairs of a block fall in one bucket the
 // bias is in b and costs nothing.  Where they do not, each boundary inside the block's
@@ -551,7 +557,7 @@ __device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, con
         x[4 * g + 3] = sub_sat(R.pos, k4.w);
     }
     wave_sync();
-    // s holds 0, or -inf where a key takes no part
+    // s holds 0 or products, or -inf where a key takes no part
     float v = mine[(lo + 1) * A.group];
     int edge = lbnd[lo];
     f32x16_t t;
@@ -796,12 +802,13 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
                 wave_sync();
             }
             b[u] = b_run;
+            if (!kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
             if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
                 const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
                 mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc[u], b[u], b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
-            products<T, DP>(sc[u], lk, u * 32, qf);
+            if (kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
         }
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
@@ -1019,12 +1026,13 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
 #pragma unroll
             for (int i = 0; i < 16; i++) dp[i] = -D;
             float b = b_run;
+            if (!kBiasFirst<T>) products<T, DP>(sc, lk, u * 32, qf);
             if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
                 const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
                 mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc, b, b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
-            products<T, DP>(sc, lk, u * 32, qf);
+            if (kBiasFirst<T>) products<T, DP>(sc, lk, u * 32, qf);
             products<T, DP>(dp, lv, u * 32, df);
             b -= lse;
 #pragma unroll
@@ -1136,7 +1144,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     __shared__ __align__(1024) u32x4_t lvk[kSpill ? 128 * TL::CH : 1];
     constexpr int kWords = 32 * TL::CH;
     __shared__ __align__(1024) u32x4_t lds[2][2][kWords];             // [stage & 1][q, dout]
-    __shared__ __align__(16) float first[2][32], ndelta[2][32];     // - lse / c (or -inf), - delta
+    __shared__ __align__(16) float nlse[2][32], ndelta[2][32];      // - lse in log2 (or -inf), - delta
     __shared__ __align__(16) int qpos[2][32];
     __shared__ int qlo[2], qhi[2];
     __shared__ int lbnd[kBucketsMax];
@@ -1193,8 +1201,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         if (A.bias) n_pos = *gp(A.qp + (n_in ? row : q1 - 1));
     };
     auto tell = [&](int to) {
-        // a row without keys, and one past the end, start at -inf: weights of zero
-        first[to][lane & 31] = n_in && n_lse != -INFINITY ? -n_lse * kLog2e / A.c : -INFINITY;
+        // a row without keys, and one past the end: weights of zero
+        nlse[to][lane & 31] = n_in && n_lse != -INFINITY ? -n_lse * kLog2e : -INFINITY;
         ndelta[to][lane & 31] = n_in ? -n_delta : 0.f;
         if (!A.bias) return;
         qpos[to][lane & 31] = n_pos;
@@ -1239,7 +1247,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     float b_run = live ? 0.f : -INFINITY, sum_run = 0.f;
     if (A.bias && stages) {
         run.set(B, lbnd, B.bucket(sub_sat(qpos0, kr.hi)));
-        b_run = live ? lb[run.m * A.group] * A.c : -INFINITY;
+        b_run = live ? lb[run.m * A.group] : -INFINITY;
     }
     // (an LDS addition without an answer; only this wavefront adds to its own row, in order)
     auto settle = [&](int m, float sum) {
@@ -1258,8 +1266,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         }
         const u32x4_t *lq = lds[cur][0], *ld = lds[cur][1];
         {
-            f32x16_t sc = block_order(first[cur]), dp = block_order(ndelta[cur]);
-            float b = b_run;
+            f32x16_t start, dp = block_order(ndelta[cur]);
+#pragma unroll
+            for (int i = 0; i < 16; i++) start[i] = b_run;
             int lo = run.m, hi = run.m;
             if (A.bias && ~run.covers(sub_sat(qlo[cur], kpos), sub_sat(qhi[cur], kpos)) != 0) {
                 // as mixed_bias, with one key and 16 rows a lane
@@ -1271,32 +1280,30 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                 }
                 run.set(B, lbnd, hi);
                 float v = lb[lo * A.group + now.g];
+                v = live ? v : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 16; i++) start[i] = v;
                 if (lo != hi) {
                     int x[16];
                     distances(qpos[cur], kpos, x);
-                    const float base = v;
-                    int edge = lbnd[lo];
-                    v = lb[(lo + 1) * A.group + now.g];
-                    f32x16_t t;
+                    for (int m = lo; m < hi; m++) {
+                        const int edge = lbnd[m];
+                        v = live ? lb[(m + 1) * A.group + now.g] : -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : base;
-                    for (int m = lo + 1; m < hi; m++) {
-                        edge = lbnd[m];
-                        v = lb[(m + 1) * A.group + now.g];
-#pragma unroll
-                        for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
+                        for (int i = 0; i < 16; i++) start[i] = x[i] >= edge ? v : start[i];
                     }
-                    sc += t;
                 }
-                b_run = live ? v * A.c : -INFINITY;
-                b = lo == hi ? b_run : live ? 0.f : -INFINITY;
+                b_run = v;
             }
+            f32x16_t sc = kBiasFirst<T> ? start : f32x16_t{};
             products<T, DP>(sc, lq, 0, kf);
+            if (!kBiasFirst<T>) sc += start;
+            const f32x16_t nl = block_order(nlse[cur]);
             if (kSpill) products<T, DP>(dp, ld, 0, lvk, 32 * w);
             else products<T, DP>(dp, ld, 0, vf);
 #pragma unroll
             for (int i = 0; i < 16; i++) {
-                sc[i] = exp2_fast(fmaf(sc[i], A.c, b));
+                sc[i] = exp2_fast(fmaf(sc[i], A.c, nl[i]));
                 dp[i] *= sc[i];
             }
             const typename Mma<T>::Pack p = Mma<T>::pack(sc), ds = Mma<T>::pack(dp);
