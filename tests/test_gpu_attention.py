@@ -94,6 +94,41 @@ def test_many_rows_few_keys(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(16, 16, 32), (16, 16, 64), (32, 16, 40), (16, 16, 128),
+                                                (16, 16, 33)])
+def test_large_batches_share_key_tiles(dtype, heads, kv_heads, dim):
+    """Enough rows for workgroups of 128 of them, whose wavefronts share their tiles of keys."""
+    d, dout = make(dtype, [1500, 37, 1000, 0, 2048], [70, 300, 129, 50, 0], heads, kv_heads, dim,
+                   buckets=9, masked=0.2, seed=22)
+    check(d, dout)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_large_batches_with_sorted_positions(dtype):
+    d, dout = make(dtype, [1500, 700, 1100], [200, 333, 65], 16, 16, 64, buckets=33, seed=23)
+    d["k_pos"] = torch.cat([torch.arange(n) for n in (200, 333, 65)]).int().cuda() * 40
+    d["q_pos"] = torch.cat([torch.arange(n) * 7 for n in (1500, 700, 1100)]).int().cuda()
+    edges = [-3000, -200, -7, -1] + [int(1.4 ** j) + j for j in range(28)]
+    d["boundaries"] = torch.tensor(edges, dtype=torch.int32, device="cuda")
+    check(d, dout)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_samples(dtype):
+    gen = torch.Generator().manual_seed(24)
+    q_len = torch.randint(0, 3, (4500,), generator=gen).tolist()
+    k_len = torch.randint(0, 6, (4500,), generator=gen).tolist()
+    check(*make(dtype, q_len, k_len, 1, 1, 16, buckets=3, masked=0.2, seed=25))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim", [32, 128])
+def test_the_largest_table(dtype, dim):
+    """256 buckets of 16 heads on one key head: the most that LDS holds beside the tiles."""
+    check(*make(dtype, [3, 9], [150, 40], 16, 1, dim, buckets=256, seed=26))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_sorted_positions(dtype):
     d, dout = make(dtype, [40, 200], [500, 700], 4, 4, 64, buckets=12, masked=0.1, seed=7)
     d["k_pos"] = torch.arange(1200, dtype=torch.int32, device="cuda")

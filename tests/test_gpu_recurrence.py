@@ -66,6 +66,21 @@ def test_long_sequences_are_split(dtype, lengths):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_samples_of_very_different_lengths(dtype):
+    """Enough long samples that the longest go first, empty and short ones among them."""
+    gen = torch.Generator().manual_seed(16)
+    lengths = torch.randint(0, 700, (130,), generator=gen).tolist()
+    lengths[3], lengths[50], lengths[129] = 0, 1, 0
+    check(*make(dtype, lengths, 130, masked=0.1, seed=17))
+
+
+def test_many_samples():
+    gen = torch.Generator().manual_seed(18)
+    lengths = torch.randint(0, 4, (5000,), generator=gen).tolist()
+    check(*make(F32, lengths, 3, masked=0.1, seed=19))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_without_state_or_mask_or_last_gradient(dtype):
     d, dy, _ = make(dtype, [40, 200], 34, state=False, seed=4)
     check(d, dy, None)
