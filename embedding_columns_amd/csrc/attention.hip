@@ -1577,11 +1577,13 @@ emb_status backward_run(const AttnArgs &A0, const AttnPlan &p, float *dbias, hip
     return launched("attention backward");
 }
 
+// a launch's threads are counted in 32 bits (and the grids are rounded up to a multiple
+// of the XCDs and chunks)
 bool grid_fits(const emb_attention *a, const AttnPlan &p)
 {
-    const double most = 2147483647.0;
+    const double most = 4294967295.0 / kAttnThreads - 1024;
     return (double)p.tiles * a->kv_heads * p.splits <= most && (double)p.key_tiles * a->kv_heads <= most &&
-           (double)a->n_q * a->heads <= most;
+           (double)a->n_q * a->heads <= (p.splits > 1 ? most : 2147483647.0);
 }
 
 }  // namespace
@@ -1610,7 +1612,7 @@ extern "C" emb_status emb_attention_forward(const emb_attention *a, void *out, v
     if (!out || !aligned(out, al) || !aligned(rest, al) || !aligned(lse, 4))
         return fail(EMB_ERR_INVALID_ARG, "attention: out must be given, out and rest aligned to four elements");
     const AttnPlan p = attn_plan(a);
-    if (!grid_fits(a, p)) return fail(EMB_ERR_UNSUPPORTED, "attention: more than 2^31 - 1 workgroups");
+    if (!grid_fits(a, p)) return fail(EMB_ERR_UNSUPPORTED, "attention: more than 2^24 - 1024 workgroups of rows");
     const size_t need = forward_workspace(a, p);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return fail(EMB_ERR_WORKSPACE, "attention: the workspace is smaller than the query returned, or not 256-byte aligned");
@@ -1655,7 +1657,7 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const void 
         return fail(EMB_ERR_INVALID_ARG, "attention: gradients must be aligned to four elements");
     if (dout_stride < 0 || dout_head_stride < 0) return fail(EMB_ERR_INVALID_ARG, "attention: strides must be >= 0");
     const AttnPlan p = attn_plan(a);
-    if (!grid_fits(a, p)) return fail(EMB_ERR_UNSUPPORTED, "attention: more than 2^31 - 1 workgroups");
+    if (!grid_fits(a, p)) return fail(EMB_ERR_UNSUPPORTED, "attention: more than 2^24 - 1024 workgroups of rows");
     const size_t need = backward_workspace(a, p);
     if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
         return fail(EMB_ERR_WORKSPACE, "attention: the workspace is smaller than the query returned, or not 256-byte aligned");

@@ -9,9 +9,8 @@ namespace emb {
 
 constexpr int kSteps = 8;        // consecutive rows a half wavefront holds in registers; the
                                  // forward saves the state before every such group
-constexpr int kWaves = 8;        // wavefronts of a workgroup on longer samples
+constexpr int kWaves = 8;        // most wavefronts of a workgroup
 constexpr int kChunk = 512;      // rows per chunk of a split scan
-constexpr int kOrderMost = 2048; // samples that scan_order sorts
 
 struct ScanArgs {
     const void *x, *gate;        // [n, channels], rows xs / gs elements apart
@@ -30,7 +29,6 @@ struct ScanArgs {
     int64_t n, tiles;
     int32_t samples, channels;
     int32_t chunk;               // samples are cut into chunks of kChunk rows
-    int32_t *order;              // segments, the longest first, or NULL
 };
 
 // sigmoid(g) and sigmoid(-g) = 1 - sigmoid(g), the small one without cancellation:
@@ -55,8 +53,7 @@ struct Chan<float, 1> {
 };
 template <>
 struct Chan<float, 2> {
-    typedef float2 Raw;
-    typedef i32x2_t Bits;
+    typedef float2 Raw;          // in the one-step form, whose rows lie in plain memory
     static __device__ __forceinline__ void open(Raw r, float *v)
     {
         v[0] = r.x;
@@ -91,10 +88,6 @@ __device__ __forceinline__ uint16_t buf_load(__amdgpu_buffer_rsrc_t r, int at, u
 {
     return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
 }
-__device__ __forceinline__ i32x2_t buf_load(__amdgpu_buffer_rsrc_t r, int at, i32x2_t)
-{
-    return __builtin_bit_cast(i32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
-}
 __device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int at, uint32_t v)
 {
     __builtin_amdgcn_raw_buffer_store_b32(v, r, at, 0, 0);
@@ -103,12 +96,6 @@ __device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int at, uint
 {
     __builtin_amdgcn_raw_buffer_store_b16(v, r, at, 0, 0);
 }
-__device__ __forceinline__ void buf_store(__amdgpu_buffer_rsrc_t r, int at, i32x2_t v)
-{
-    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, v), r, at, 0, 0);
-}
-
 // The rows of a block of the walk in one tensor, through a buffer descriptor that ends
 // with the sample (or chunk): rows past the end read zeros and drop stores, and so do
 // lanes past the last channel, whose offset lies past every end.
@@ -150,7 +137,7 @@ __device__ __forceinline__ bool scan_span(const ScanArgs &A, int block, ScanSpan
 {
     s.tile = block;
     if (A.chunk == 0) {
-        s.seg = A.order ? uniform(*gp(A.order + block)) : block;
+        s.seg = block;
         s.tile0 = block;
         s.chunks = 1;
         s.first = s.begin = uniform(seg_edge(A.off, A.samples, (int)A.n, s.seg));
@@ -166,27 +153,6 @@ __device__ __forceinline__ bool scan_span(const ScanArgs &A, int block, ScanSpan
     s.end = t.row0 + kChunk < t.rows ? s.begin + kChunk : t.base + t.rows;
     // an empty sample keeps its first chunk: it hands the state through
     return t.row0 < t.rows || (t.rows == 0 && t.row0 == 0);
-}
-
-// The segments in the order of their lengths, the longest first: a workgroup walks a
-// whole sample, and the long ones have to start early.  The place of a segment is the
-// number of those that go before it.
-__global__ __launch_bounds__(256) void scan_order(ScanArgs A)
-{
-    __shared__ int len[kOrderMost + 2];
-    const int n = A.samples + 2;
-    for (int j = threadIdx.x; j < n; j += 256)
-        len[j] = seg_edge(A.off, A.samples, (int)A.n, j + 1) - seg_edge(A.off, A.samples, (int)A.n, j);
-    __syncthreads();
-    // eight lanes a segment
-    const int i = min((int)(blockIdx.x * 32 + threadIdx.x / 8), n - 1), mine = len[i];
-    int before = 0;
-#pragma unroll 8
-    for (int j = threadIdx.x & 7; j < n; j += 8) before += len[j] > mine || (len[j] == mine && j < i);
-    before += __shfl_xor(before, 1);
-    before += __shfl_xor(before, 2);
-    before += __shfl_xor(before, 4);
-    if ((threadIdx.x & 7) == 0) A.order[before] = i;     // the last one's spare lanes repeat it
 }
 
 // The saved state of the group of kSteps rows that begins at `row`
@@ -280,7 +246,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
     typedef Chan<T, VEC> CH;
     typedef typename CH::Raw Raw;
     constexpr int kRows = 2 * W * kSteps;
-    __shared__ float pa[2][2 * W][32 * VEC], ph[2][2 * W][32 * VEC];
+    __shared__ float pa[2 * W][32 * VEC], ph[2 * W][32 * VEC];
     const int lane = lane_id(), hl = lane & 31, half = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
     const int unit = 2 * w + half, c = (blockIdx.y * 32 + hl) * VEC;
     const bool live = c < A.channels;
@@ -297,7 +263,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
         h[v] = PHASE != kScanSum && A.state && live ? A.state[(s.seg - 1) * C + c + v] : 0.f;
         ta[v] = 1.f;
     }
-    if (PHASE == kScanApply) chunk_state<VEC, W, false>(A, s, unit, c, live, pa[0], ph[0], h);
+    if (PHASE == kScanApply) chunk_state<VEC, W, false>(A, s, unit, c, live, pa, ph, h);
 
     Raw xn[kSteps], gn[kSteps];
     int keep = 0;
@@ -314,8 +280,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
         }
     };
     if (s.begin < s.end) load(s.begin);
-    int buf = 0;
-    for (int t0 = s.begin; t0 < s.end; t0 += kRows, buf ^= 1) {
+    int buf = 0;             // the pairs lie in either half in turn: one barrier a block
+    for (int t0 = s.begin; t0 < s.end; t0 += kRows, buf ^= W) {
         const uint64_t all = __ballot(keep != 0);
         const uint32_t bits = half ? (uint32_t)(all >> 32) : (uint32_t)all;
         float xs[kSteps][VEC], as[kSteps][VEC], la[VEC], lh[VEC];
@@ -346,8 +312,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
             oh[v] = other_half(lh[v]);
             // half 0's pair, then half 1's
             if (half == 0) {
-                pa[buf][w][hl * VEC + v] = la[v] * oa[v];
-                ph[buf][w][hl * VEC + v] = fmaf(oa[v], lh[v], oh[v]);
+                pa[buf + w][hl * VEC + v] = la[v] * oa[v];
+                ph[buf + w][hl * VEC + v] = fmaf(oa[v], lh[v], oh[v]);
             }
         }
         __syncthreads();
@@ -359,8 +325,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 if (u == w) in[v] = h[v];
-                const float ua = pa[buf][u][hl * VEC + v];
-                h[v] = fmaf(ua, h[v], ph[buf][u][hl * VEC + v]);
+                const float ua = pa[buf + u][hl * VEC + v];
+                h[v] = fmaf(ua, h[v], ph[buf + u][hl * VEC + v]);
                 if (PHASE == kScanSum) ta[v] *= ua;
             }
         if (PHASE == kScanSum) continue;
@@ -403,7 +369,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
     typedef Chan<T, VEC> CH;
     typedef typename CH::Raw Raw;
     constexpr int kRows = 2 * W * kSteps;
-    __shared__ float pa[2][2 * W][32 * VEC], ph[2][2 * W][32 * VEC];
+    __shared__ float pa[2 * W][32 * VEC], ph[2 * W][32 * VEC];
     const int lane = lane_id(), hl = lane & 31, half = lane >> 5, w = uniform((int)(threadIdx.x >> 6));
     const int unit = 2 * w + half, c = (blockIdx.y * 32 + hl) * VEC;
     const bool live = c < A.channels;
@@ -423,7 +389,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
         u[v] = PHASE != kScanSum && A.dlast && live ? A.dlast[(s.seg - 1) * C + c + v] : 0.f;
         ta[v] = 1.f;
     }
-    if (PHASE == kScanApply) chunk_state<VEC, W, true>(A, s, unit, c, live, pa[0], ph[0], u);
+    if (PHASE == kScanApply) chunk_state<VEC, W, true>(A, s, unit, c, live, pa, ph, u);
 
     const int blocks = (s.end - s.begin + kRows - 1) / kRows;
     Raw xn[kSteps], gn[kSteps], dn[kSteps];
@@ -448,8 +414,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
         for (int v = 0; v < VEC; v++) hn[v] = *gp(A.ckpt + group + v);
     };
     if (blocks) load(blocks - 1);
-    int buf = 0;
-    for (int b = blocks - 1; b >= 0; b--, buf ^= 1) {
+    int buf = 0;             // the pairs lie in either half in turn: one barrier a block
+    for (int b = blocks - 1; b >= 0; b--, buf ^= W) {
         const int t0 = s.begin + b * kRows;
         const uint64_t all = __ballot(keep != 0);
         const uint32_t bits = half ? (uint32_t)(all >> 32) : (uint32_t)all;
@@ -486,8 +452,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
             ou[v] = other_half(lu[v]);
             // half 1's pair, then half 0's
             if (half == 0) {
-                pa[buf][w][hl * VEC + v] = la[v] * oa[v];
-                ph[buf][w][hl * VEC + v] = fmaf(la[v], ou[v], lu[v]);
+                pa[buf + w][hl * VEC + v] = la[v] * oa[v];
+                ph[buf + w][hl * VEC + v] = fmaf(la[v], ou[v], lu[v]);
             }
         }
         __syncthreads();
@@ -499,8 +465,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
 #pragma unroll
             for (int v = 0; v < VEC; v++) {
                 if (p == w) in[v] = u[v];
-                const float pv = pa[buf][p][hl * VEC + v];
-                u[v] = fmaf(pv, u[v], ph[buf][p][hl * VEC + v]);
+                const float pv = pa[buf + p][hl * VEC + v];
+                u[v] = fmaf(pv, u[v], ph[buf + p][hl * VEC + v]);
                 if (PHASE == kScanSum) ta[v] *= pv;
             }
         if (PHASE == kScanSum) continue;
@@ -582,27 +548,32 @@ namespace {
 
 struct ScanPlan {
     int waves;
-    int32_t chunk, ordered;      // cut samples into chunks; walk the long ones first
+    int32_t chunk;               // cut samples into chunks
     int64_t tiles, saved;
 };
 
-// One workgroup walks a whole sample when the samples and channel blocks alone fill
-// the chip, the longest first where that can matter; otherwise samples are cut into
-// chunks.
+// How many wavefronts walk a sample, and whether samples are cut.  Times in us of a
+// training step (forward and backward) in bf16 over 256 channels, measured.
+// A workgroup's block of rows is 16 per wavefront, and a sample shorter than that
+// wastes the rest (about 256000 rows in all):
+//   mean length   4    16    32    64   128   256
+//   1 wavefront  389   236   248   271   320   378
+//   4           1383   439   285   236   257   288
+//   8           3405   996   553   350   268   271
+// Cutting reads x and gate (the backward: dy and gate) twice and costs two more launches,
+// but lets few samples fill the chip (samples x mean length, whole / cut): 1 x 65536
+// 2038 / 93, 16 x 8192 281 / 169; 64 x 4096 of very different lengths 707 / 432; and the
+// other side 32 x 512 25 / 63, 100 x 1024 of equal lengths 86 / 140, of very different
+// ones 210 / 155.  The lengths themselves are on the device: only their mean is known here.
 ScanPlan scan_plan(const emb_recurrence *r)
 {
     ScanPlan p{};
     const int64_t mean = r->samples ? r->n / r->samples : 0;
     const int per = r->dtype == EMB_BF16 ? 64 : 32;      // channels a workgroup
     const int64_t items = (int64_t)r->samples * ((r->channels + per - 1) / per);
-    p.waves = mean <= 32 ? 1 : kWaves;
-    p.tiles = r->samples + 2;
-    if (items < 512 && mean >= 1024) {
-        p.chunk = 1;
-        p.tiles = seg_tiles(r->n, r->samples, 1, kChunk);
-    } else if (items >= 256 && items <= 8192 && r->samples > 1 && r->samples <= kOrderMost && mean >= 256) {
-        p.ordered = 1;
-    }
+    p.waves = mean <= 32 ? 1 : mean <= 128 ? 4 : kWaves;
+    p.chunk = mean >= 1024 && items <= 256 && items * 8 <= mean;
+    p.tiles = p.chunk ? seg_tiles(r->n, r->samples, 1, kChunk) : r->samples + 2;
     p.saved = seg_tiles(r->n, r->samples, 1, kSteps);
     return p;
 }
@@ -642,7 +613,7 @@ size_t pad256(size_t x) { return (x + 255) & ~size_t(255); }
 
 size_t scan_workspace(const emb_recurrence *r, const ScanPlan &p)
 {
-    return p.chunk ? 2 * pad256((size_t)p.tiles * r->channels * 4) : p.ordered ? (size_t)p.tiles * 4 : 0;
+    return p.chunk ? 2 * pad256((size_t)p.tiles * r->channels * 4) : 0;
 }
 
 // channels in pairs: an even count, and every row aligned to a pair
@@ -656,32 +627,32 @@ bool pairs_ok(const emb_recurrence *r, std::initializer_list<const void *> same)
     return true;
 }
 
-template <typename T, int VEC, int W>
-emb_status scan_launch_w(const ScanArgs &A, bool backward, hipStream_t st)
+// a launch's threads in one dimension are counted in 32 bits
+constexpr int64_t kThreadsMost = (int64_t(1) << 32) - 1;
+
+template <typename T, int VEC, int W, int PHASE>
+void scan_launch_p(const ScanArgs &A, bool backward, hipStream_t st)
 {
     const int64_t blocks = (A.channels + 32 * VEC - 1) / (32 * VEC);
     const dim3 grid((unsigned)A.tiles, (unsigned)blocks), block(64 * W);
-    if (A.order)
-        hipLaunchKernelGGL(scan_order, dim3((unsigned)((A.tiles + 31) / 32)), dim3(256), 0, st, A);
-    if (A.chunk == 0) {
-        if (backward) hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanWhole>), grid, block, 0, st, A);
-        else hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanWhole>), grid, block, 0, st, A);
-    } else if (backward) {
-        hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanSum>), grid, block, 0, st, A);
-        hipLaunchKernelGGL((scan_backward<T, VEC, W, kScanApply>), grid, block, 0, st, A);
-    } else {
-        hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanSum>), grid, block, 0, st, A);
-        hipLaunchKernelGGL((scan_forward<T, VEC, W, kScanApply>), grid, block, 0, st, A);
-    }
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return fail(EMB_ERR_HIP, std::string("recurrence launch: ") + hipGetErrorString(e));
-    return EMB_OK;
+    if (backward) hipLaunchKernelGGL((scan_backward<T, VEC, W, PHASE>), grid, block, 0, st, A);
+    else hipLaunchKernelGGL((scan_forward<T, VEC, W, PHASE>), grid, block, 0, st, A);
 }
 
 template <typename T, int VEC>
 emb_status scan_launch_v(const ScanArgs &A, int waves, bool backward, hipStream_t st)
 {
-    return waves == 1 ? scan_launch_w<T, VEC, 1>(A, backward, st) : scan_launch_w<T, VEC, kWaves>(A, backward, st);
+    if (A.tiles > kThreadsMost / (64 * waves))
+        return fail(EMB_ERR_UNSUPPORTED, "recurrence: too many samples for one launch");
+    if (A.chunk) {                       // samples long enough for kWaves
+        scan_launch_p<T, VEC, kWaves, kScanSum>(A, backward, st);
+        scan_launch_p<T, VEC, kWaves, kScanApply>(A, backward, st);
+    } else if (waves == 1) scan_launch_p<T, VEC, 1, kScanWhole>(A, backward, st);
+    else if (waves == 4) scan_launch_p<T, VEC, 4, kScanWhole>(A, backward, st);
+    else scan_launch_p<T, VEC, kWaves, kScanWhole>(A, backward, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(EMB_ERR_HIP, std::string("recurrence launch: ") + hipGetErrorString(e));
+    return EMB_OK;
 }
 
 emb_status scan_launch(const emb_recurrence *r, const ScanArgs &A, int waves, bool pairs, bool backward,
@@ -709,7 +680,6 @@ ScanArgs scan_args(const emb_recurrence *r, const ScanPlan &p, void *ws)
     A.channels = r->channels;
     A.chunk = p.chunk;
     A.tiles = p.tiles;
-    if (p.ordered) A.order = static_cast<int32_t *>(ws);
     if (p.chunk) {
         const size_t part = pad256((size_t)p.tiles * r->channels * 4);
         A.sum_a = reinterpret_cast<float *>(ws);
@@ -800,7 +770,8 @@ extern "C" emb_status emb_recurrence_step(int32_t dtype, int64_t rows, int32_t c
     const bool pairs = pairs_ok(&r, {y}) && aligned(state, 8);
     const int64_t items = rows * (pairs ? channels / 2 : channels);
     const int64_t blocks = (items + 255) / 256;
-    if (blocks > 0x7FFFFFFF) return fail(EMB_ERR_UNSUPPORTED, "recurrence step: more than 2^31 - 1 blocks");
+    if (blocks > kThreadsMost / 256)
+        return fail(EMB_ERR_UNSUPPORTED, "recurrence step: more than 2^32 - 256 channels or pairs of them");
     const dim3 grid((unsigned)blocks), block(256);
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == EMB_BF16 && pairs)
