@@ -15,6 +15,13 @@
 // keys of the contraction are taken in that order; so probabilities never leave the
 // registers, and only the first operand (V, or K, Q, dO transposed) is read from LDS
 // in the matching order, by the transposing LDS load for bf16.
+//
+// Times below were measured on one MI355X, bf16, at these sizes:
+//   serving:  512 samples of 1..8 queries over 200..2000 keys, 4 heads of 64, 32 buckets
+//   lifelong: 4 samples of 1 query over 60000..131072 keys, 8 heads on 2 of 128
+//   many candidates: 32 samples of 100..500 queries over 200..2000 keys, 4 heads of 64, 32 buckets
+//   ranking:  64 samples of 20..100 queries over 200..2000 keys, 4 heads of 64, 32 buckets
+//   two sequences: 8 samples of 1500..2048 queries and keys, 8 heads of 128, 32 buckets
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -332,9 +339,10 @@ __device__ __forceinline__ Range half_range(int x)
 // The bias table of a key head's group, over scale, and the boundaries, in LDS: so an
 // entry can be where a block of products starts, and the scaling brings it back.  Finite
 // entries are held to +-kBiasMost, where fp32 still tells scores apart that differ by a
-// hundredth; a weight of e^-kBiasMost beside any other is zero.  The boundaries also in registers, one or more a lane, so that the bucket of a uniform
-// distance is a count over ballots.  Loads are issued first (take) and used later
-// (put): nothing they need depends on the offsets.
+// hundredth; a weight of e^-kBiasMost beside any other is zero.  The boundaries also in
+// registers, one or more a lane, so that the bucket of a uniform distance is a count over
+// ballots.  Loads are issued first (take) and used later (put): nothing they need depends
+// on the offsets.
 constexpr float kBiasMost = 1e5f;
 struct Bias {
     int b[kBucketsMax / 64];
@@ -521,7 +529,8 @@ __device__ __forceinline__ void load_frag(Frag<T, DP> &f, const T *row, int dim,
 
 // Whether a block of products starts from its bias or gets it added.  bf16 products of a
 // head are 2 to 8 accumulations and the start costs nothing; fp32 products are four times
-// as many, and rounding each at the bias's size would cost the gradients a digit.
+// as many, and rounding each at the bias's size would cost the gradients a digit (error of
+// an fp32 dbias against 64 bits: 2.2e-6 with the bias first, 4.3e-7 with it added).
 template <typename T>
 constexpr bool kBiasFirst = sizeof(T) == 2;
 
@@ -739,6 +748,16 @@ __device__ __forceinline__ float log_sum(float m, float l)
 // overflow, and the accumulators are rescaled only when it has to move.
 constexpr float kLag = 8.f;
 
+// One pass over the keys with the running maximum and sum of the softmax; scores and
+// weights stay in registers.  The weights enter their product in T, as the values do: a
+// relative error of up to 2^-8 each, independent ones, where the output's own rounding
+// is as large; their sum l is of the fp32 weights.
+// Serving 122 us (4.7 TB/s of its 576 MB) and lifelong 84 us and 5 us for the join (4.6
+// TB/s of 408 MB), where a large copy has 5.5: the reading bounds them.  Two sequences
+// 218 us, 458 TFLOP/s (without a bias 157): two wavefronts a SIMD alternate between
+// products and weights, and the blocks whose pairs fall into several buckets cost the
+// rest.  Many candidates 61 us, 154 TFLOP/s (without a bias 46): a workgroup has 9 steps
+// between its first loads (four dependent ones) and its join, and these do not overlap.
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_forward(AttnArgs A)
 {
@@ -906,7 +925,8 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
 }
 
 // Joins the splits of a row: a workgroup per (row, head), a lane per element, the
-// wavefronts take the splits in turn.
+// wavefronts take the splits in turn (there are splits only where rows are few).  A
+// launch's latency bounds it: 5 us for lifelong's 32 rows of 64 splits.
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 {
@@ -951,6 +971,9 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 // a sum of score gradients over many rows, each row's adding up to zero, and would drown
 // in that rounding: taken again from the probabilities in fp32, delta costs one addition
 // a pair.  (Correcting dq for it too, by sum_j p_ij k_j, would be a fourth product.)
+// dS enters its product in T, as q and k do.
+// The walk is the forward's, and so is what bounds it.  Two sequences 263 us, 569 TFLOP/s
+// of its three products (without a bias 202); ranking 50 us (41).
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_backward_q(AttnArgs A)
 {
@@ -1093,6 +1116,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     }
 }
 
+// dq and delta of a row from its splits, a workgroup per (row, head) as in attn_join
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 {
@@ -1135,7 +1159,14 @@ __device__ __forceinline__ void distances(const int *qpos, int kpos, int (&x)[16
 // after the other, 32 rows a stage: dk and dv need no sum across workgroups.  Rows
 // arrive in LDS a stage ahead, as the keys do in the other kernels.
 // Rows of 256 bytes leave V in LDS: with V in registers too they would need more than
-// 256, and past those the accumulators move back and forth (see KeyWalk::kWaves).
+// 256, and past those the accumulators move back and forth (see KeyWalk::kWaves; two
+// sequences 582 us with V in registers, 506 with it in LDS, when this was chosen).
+// Two sequences 466 us, 428 TFLOP/s of its four products (without a bias 340): products,
+// weights and the bias gradient's sums take turns in two wavefronts a SIMD.  A block in
+// one bucket adds its 16 score gradients to a sum in a register; the sum goes to LDS when
+// the bucket changes (LDS additions per pair instead: 1237 -> 2537 us).  Ranking 92 us
+// (63), 1.6 TB/s of the keys' 146 MB: with 2 or 3 stages a workgroup the time goes to
+// the latency of its first loads and of its stores.
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void attn_backward_k(AttnArgs A)
 {
@@ -1371,8 +1402,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         }
 }
 
-// dbias[m, head] = sum of the workgroups' parts, in a fixed order: a workgroup per
-// (head, 32 buckets), 32 tiles side by side
+// dbias[m, head] = sum of the workgroups' parts, in a fixed order (no atomics: the result
+// is the same every time): a workgroup per (head, 32 buckets), 32 tiles side by side.
+// 4 to 5 us: a launch's latency and a few dependent loads; 12 us for 2500 tiles.
 constexpr int kBiasJoin = 1024;
 __global__ __launch_bounds__(kBiasJoin) void attn_join_bias(AttnArgs A, float *dbias)
 {
@@ -1399,8 +1431,17 @@ namespace {
 
 size_t pad256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// How the kernels that walk the keys are cut: 32 or 128 query rows a workgroup, and
-// the number of workgroups that share the keys of one set of rows.
+// How the kernels that walk the keys are cut: 32 or 128 query rows a workgroup (WM = 1
+// or 4), and the number of workgroups that share the keys of one set of rows.
+// 128 rows read K and V from L2 a quarter as often, but leave rows unused in samples of
+// few and fill the chip only with enough sets of rows.  Forward in us, 32 / 128 rows:
+// two sequences 449 / 201 (944 sets of 128), many candidates 61 / 59 (364 sets), serving
+// 121 / 166, ranking 45 / 60; fp32 training of 16 samples of 1..64 queries 62 / 109 in
+// all three kernels.
+// Splits pay while the sets alone leave the chip's 512 places (two workgroups a CU) empty,
+// and cost partial results and a launch: lifelong with 1, 8, 32, 64 splits takes 1297,
+// 182, 88, 89 us, where many candidates with 2 take 99 us for 61, and ranking 236 for 193.
+// A split of under 256 keys would be two steps long.
 struct AttnPlan {
     int wm, splits;
     int64_t tiles, key_tiles;
@@ -1530,6 +1571,10 @@ AttnArgs attn_args(const emb_attention *a, const AttnPlan &p)
             wide_rows(a->v, a->v_stride, a->v_head_stride, a->dim, el);
     A.splits = p.splits;
     A.tiles = (int32_t)p.tiles;
+    // Neighbours in the order of work share keys (tiles of a sample) and so an XCD's L2:
+    // each XCD takes one run of them (ranking 193 us, against 205 in runs of 16).  Splits
+    // share nothing, and there few samples of unequal length even out in runs of 16
+    // (lifelong 98 us, against 131).
     A.chunk = p.splits > 1 ? 16 : 0;
     return A;
 }

@@ -10,7 +10,7 @@ namespace emb {
 constexpr int kSteps = 8;        // consecutive rows a half wavefront holds in registers; the
                                  // forward saves the state before every such group
 constexpr int kWaves = 8;        // most wavefronts of a workgroup
-constexpr int kChunk = 512;      // rows per chunk of a split scan
+constexpr int kChunk = 512;      // rows per chunk of a split scan (256 and 1024: no faster)
 
 struct ScanArgs {
     const void *x, *gate;        // [n, channels], rows xs / gs elements apart
@@ -240,6 +240,11 @@ __device__ __forceinline__ void zero_rows(void *p, const ScanSpan &s, int64_t C,
 // each half applies its rows from the state that the pairs before it give.  One pass
 // over the data; the state stays in fp32 registers.  Rows past the end and masked ones
 // count as a = 1, x = 0; the next block's rows are loaded before this block's last step.
+// 256 samples of 200..2000 rows, 256 channels, bf16, mask and states: 106 us, 4.0 TB/s of
+// its 423 MB (a large copy: 5.5), in registers for four wavefronts a SIMD (six: spills,
+// 212 us).  An exponential and a reciprocal an element keep the vector units half busy,
+// and samples of unequal length leave the chip emptying at the end.  Cut (two passes) one
+// fp32 sample of 65537 rows and 384 channels takes 45 us and 55 us.
 template <typename T, int VEC, int W, int PHASE>
 __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs A)
 {
@@ -363,6 +368,9 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
 // again a linear recurrence.  The states h_(t-1) that dgate needs are scanned again
 // from the saved state before each group of kSteps rows: an eighth of the states in
 // fp32 is a quarter of what all of them in bf16 would cost, and exact.
+// 128 samples of 200..2000 rows, 512 channels, bf16: 160 us, 3.4 TB/s of its 540 MB (the
+// forward that saves states 108 us); bounded as the forward is.  Cut, as above: 37 us and
+// 89 us.
 template <typename T, int VEC, int W, int PHASE>
 __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs A)
 {
@@ -516,6 +524,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
     }
 }
 
+// One row for each of a batch of states.  2.3 us for 64 states of 256 channels: a launch.
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void scan_step(const T *x, const T *gate, int64_t xs, int64_t gs,
                                                  float *state, T *y, int64_t rows, int64_t C)
