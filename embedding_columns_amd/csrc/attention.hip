@@ -34,6 +34,8 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kBucketsMax = 256;
@@ -51,7 +53,7 @@ struct AttnArgs {
     int32_t nq, nk;
     int32_t samples, heads, kv_heads, group, dim, buckets;
     float scale, rscale, c;                     // rscale = 1 / scale, c = scale * log2(e)
-    int32_t vec, ovec;                          // rows (of out) can be read 16 bytes at a time
+    int32_t vec, ovec, gvec;                    // rows (of out, of dk and dv) move in 16-byte pieces
     int32_t splits, chunk;
     int32_t tiles;
     void *out, *rest;                           // [n_q, heads, dim]; what rounding out left, or NULL
@@ -97,6 +99,12 @@ template <typename V>
 __device__ __forceinline__ V lds_read(uint32_t at)
 {
     return *(__attribute__((address_space(3))) const V *)(uintptr_t)at;
+}
+
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t at, V v)
+{
+    *(__attribute__((address_space(3))) V *)(uintptr_t)at = v;
 }
 
 // a row as a second operand: its even chunks in half 0, its odd ones in half 1
@@ -185,9 +193,13 @@ struct Mma<uint16_t> {
         for (int j = 0; j < 4; j++) s += bf16_lo(a[j]) * bf16_lo(b[j]) + bf16_hi(a[j]) * bf16_hi(b[j]);
         return s;
     }
+    static __device__ __forceinline__ u32x2_t pack4(const float *v)
+    {
+        return u32x2_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
+    }
     static __device__ __forceinline__ void store4(uint16_t *p, const float *v)
     {
-        *gp(reinterpret_cast<uint2 *>(p)) = make_uint2(bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3]));
+        *gp(reinterpret_cast<u32x2_t *>(p)) = pack4(v);
     }
     static __device__ __forceinline__ void store1(uint16_t *p, float v) { *gp(p) = bf16_rne(v); }
 };
@@ -231,9 +243,10 @@ struct Mma<float> {
         for (int j = 0; j < 4; j++) s = fmaf(__uint_as_float(a[j]), __uint_as_float(b[j]), s);
         return s;
     }
+    static __device__ __forceinline__ f32x4_t pack4(const float *v) { return f32x4_t{v[0], v[1], v[2], v[3]}; }
     static __device__ __forceinline__ void store4(float *p, const float *v)
     {
-        *gp(reinterpret_cast<float4 *>(p)) = make_float4(v[0], v[1], v[2], v[3]);
+        *gp(reinterpret_cast<f32x4_t *>(p)) = pack4(v);
     }
     static __device__ __forceinline__ void store1(float *p, float v) { *gp(p) = v; }
 };
@@ -1140,6 +1153,38 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 
 // ---------------------------------------------------------- backward: keys
 
+// 32 rows, one per lane & 31 and DP elements long as the products leave them (times f),
+// into memory rows `stride` elements apart: through a tile, so that neighbouring lanes
+// write neighbouring 16 bytes.  Rows from `rows` on are left out.
+template <typename T, int DP>
+__device__ __forceinline__ void store_rows(T *base, int64_t stride, int dim, bool vec, int rows,
+                                           const f32x16_t (&x)[DP / 32], float f, u32x4_t *tile)
+{
+    using TL = Tile<T, DP>;
+    const int l = lane_id(), r = l & 31, h = l >> 5;
+#pragma unroll
+    for (int d = 0; d < DP / 32; d++)
+#pragma unroll
+        for (int g = 0; g < 4; g++) {
+            const int col = 32 * d + 8 * g + 4 * h;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = f * x[d][4 * g + e];
+            if (vec) lds_write(lds_address(tile) + 16 * TL::at(r, col / TL::E) + col % TL::E * (int)sizeof(T), Mma<T>::pack4(v));
+            else if (r < rows) store_part(base + r * stride, col, dim, v);
+        }
+    if (!vec) return;
+    wave_sync();
+    constexpr int PER = 64 / TL::CH;                    // rows per store
+#pragma unroll
+    for (int j = 0; j < 32 / PER; j++) {
+        const int row = j * PER + l / TL::CH, c = (l % TL::CH) ^ swizzle<TL::CH>(row);
+        const u32x4_t v = tile[j * 64 + l];
+        if (row < rows && c * TL::E < dim) *gp(reinterpret_cast<u32x4_t *>(base + row * stride) + c) = v;
+    }
+    wave_sync();
+}
+
 // distances of 16 query rows (in the order of a block) from the lane's key
 __device__ __forceinline__ void distances(const int *qpos, int kpos, int (&x)[16])
 {
@@ -1383,23 +1428,13 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     if (A.dbias_part && stages == 0)
         for (int i = threadIdx.x; i < A.buckets * A.group; i += kAttnThreads)
             A.dbias_part[((int64_t)tile * A.heads + kvh * A.group) * A.buckets + i] = 0.f;
-    if (!in || idle || !A.dk) return;
-    T *pk = static_cast<T *>(A.dk) + (key * A.kv_heads + kvh) * A.dim;
-    T *pv = static_cast<T *>(A.dv) + (key * A.kv_heads + kvh) * A.dim;
-#pragma unroll
-    for (int d = 0; d < DP / 32; d++)
-#pragma unroll
-        for (int g = 0; g < 4; g++) {
-            const int col = 32 * d + 8 * g + 4 * h;
-            float a[4], b[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                a[e] = A.scale * dk[d][4 * g + e];
-                b[e] = dv[d][4 * g + e];
-            }
-            store_part(pk, col, A.dim, a);
-            store_part(pv, col, A.dim, b);
-        }
+    if (idle || !A.dk) return;
+    const int rows = s.rows - (s.row0 + 32 * w);
+    const int64_t at = ((int64_t)(s.base + s.row0 + 32 * w) * A.kv_heads + kvh) * A.dim;
+    u32x4_t *mine = lds[w >> 1][w & 1];
+    __syncthreads();                  // the last stage's rows are read
+    store_rows<T, DP>(static_cast<T *>(A.dk) + at, (int64_t)A.kv_heads * A.dim, A.dim, A.gvec, rows, dk, A.scale, mine);
+    store_rows<T, DP>(static_cast<T *>(A.dv) + at, (int64_t)A.kv_heads * A.dim, A.dim, A.gvec, rows, dv, 1.f, mine);
 }
 
 // dbias[m, head] = sum of the workgroups' parts, in a fixed order (no atomics: the result
@@ -1714,6 +1749,7 @@ extern "C" emb_status emb_attention_backward(const emb_attention *a, const void 
     A.out = const_cast<void *>(out);
     A.rest = const_cast<void *>(rest);
     A.ovec = wide_rows(out, a->dim, a->dim, a->dim, el) && wide_rows(rest, a->dim, a->dim, a->dim, el);
+    A.gvec = wide_rows(dk, a->dim, a->dim, a->dim, el) && wide_rows(dv, a->dim, a->dim, a->dim, el);
     A.lse = const_cast<float *>(lse);
     A.dq = dq;
     A.dk = dk;
