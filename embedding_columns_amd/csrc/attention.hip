@@ -1389,26 +1389,27 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                 typename Mma<T>::template Rows<DP>(lq, 0, d).times(dk[d], ds);
             }
             if (A.dbias_part) {
+                float all = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; i++) all += dp[i];
                 if (lo != hi) {
+                    // a bucket's sum is what lies below its upper boundary, less what lay
+                    // below the one before it
                     int x[16];
                     distances(qpos[cur], kpos, x);
+                    float under = 0.f;
                     for (int m = lo; m < hi; m++) {
                         const int edge = lbnd[m];
                         float sum = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const bool below = x[i] < edge;
-                            sum += below ? dp[i] : 0.f;
-                            dp[i] = below ? 0.f : dp[i];
-                        }
-                        settle(m, sum_run + sum);
+                        for (int i = 0; i < 16; i++) sum += x[i] < edge ? dp[i] : 0.f;
+                        settle(m, sum_run + (sum - under));
+                        under = sum;
                         sum_run = 0.f;
                     }
+                    all -= under;
                 }
-                float sum = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; i++) sum += dp[i];
-                sum_run += sum;
+                sum_run += all;
             }
         }
         const int last_m = run.m;
