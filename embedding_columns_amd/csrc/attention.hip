@@ -1206,12 +1206,12 @@ __device__ __forceinline__ void distances(const int *qpos, int kpos, int (&x)[16
 // Rows of 256 bytes leave V in LDS: with V in registers too they would need more than
 // 256, and past those the accumulators move back and forth (see KeyWalk::kWaves; two
 // sequences 582 us with V in registers, 506 with it in LDS, when this was chosen).
-// Two sequences 466 us, 428 TFLOP/s of its four products (without a bias 340): products,
+// Two sequences 459 us, 435 TFLOP/s of its four products (without a bias 284): products,
 // weights and the bias gradient's sums take turns in two wavefronts a SIMD.  A block in
 // one bucket adds its 16 score gradients to a sum in a register; the sum goes to LDS when
-// the bucket changes (LDS additions per pair instead: 1237 -> 2537 us).  Ranking 92 us
-// (63), 1.6 TB/s of the keys' 146 MB: with 2 or 3 stages a workgroup the time goes to
-// the latency of its first loads and of its stores.
+// the bucket changes (LDS additions per pair instead: 1237 -> 2537 us).  Ranking 87 us
+// (57), 1.7 TB/s of the keys' 146 MB: with 2 or 3 stages a workgroup the time goes to
+// the latency of its first loads and to blocks that span several buckets.
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void attn_backward_k(AttnArgs A)
 {

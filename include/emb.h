@@ -442,7 +442,7 @@ typedef struct emb_attention {   /* host */
     int32_t samples;
     int32_t buckets;             /* rows of the bias table, <= 256 and <= 4096 / (heads /     */
                                  /* kv_heads); 0: no bias                                    */
-    float scale;                 /* > 0                                                      */
+    float scale;                 /* 1e-18 .. 1e18                                            */
     int32_t reserved;
     int64_t n_q, n_k;            /* query rows, key rows                                     */
     const void *q;               /* [n_q, heads, dim]    elements of a head contiguous; rows  */
@@ -469,10 +469,12 @@ emb_status emb_attention_forward(const emb_attention *a, void *out, void *rest, 
 
 /* dq: [n_q, heads, dim]; dk, dv: [n_k, kv_heads, dim] (both, or both NULL); dbias: fp32
  * [buckets, heads] or NULL.  All contiguous, overwritten, and the same bits for the same
- * inputs.  out, rest (NULL for EMB_F32), lse: what the forward gave.  dout: as q, with its own strides. */
+ * inputs.  out, rest (NULL for EMB_F32), lse: what the forward gave.  dout: as q, with its
+ * own strides.  An entry of the bias beyond +-1e5 has the gradient of its score. */
 emb_status emb_attention_backward(const emb_attention *a, const void *out, const void *rest,
-                                  const float *lse, const void *dout, int64_t dout_stride, int64_t dout_head_stride, void *dq, void *dk,
-                                  void *dv, float *dbias, void *workspace, size_t workspace_bytes,
+                                  const float *lse, const void *dout, int64_t dout_stride,
+                                  int64_t dout_head_stride, void *dq, void *dk, void *dv,
+                                  float *dbias, void *workspace, size_t workspace_bytes,
                                   void *stream);
 
 /*
@@ -487,7 +489,7 @@ typedef struct emb_recurrence {  /* host */
     int32_t reserved;
     int64_t n;                   /* rows                                                     */
     const void *x, *gate;        /* [n, channels], rows x_stride / gate_stride elements apart */
-    int64_t x_stride, gate_stride;
+    int64_t x_stride, gate_stride;         /* < 2^21                                         */
     const int32_t *offsets;      /* [samples + 1]                                            */
     const uint8_t *mask;         /* [n] or NULL                                              */
     const float *state;          /* [samples, channels] or NULL (zero)                        */
