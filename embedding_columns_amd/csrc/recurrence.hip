@@ -257,7 +257,8 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
     const bool live = c < A.channels;
     const int64_t C = A.channels;
     ScanSpan s;
-    if (!scan_span(A, blockIdx.x, s)) return;
+    // the chunks' second pass begins with what the first read last (64 x 4096 rows: 437 -> 426 us)
+    if (!scan_span(A, PHASE == kScanApply ? gridDim.x - 1 - blockIdx.x : blockIdx.x, s)) return;
     if (s.seg == 0 || s.seg == A.samples + 1) {
         if (PHASE != kScanSum) zero_rows<T, VEC, W>(A.y, s, C, unit, c, live);
         return;
@@ -383,7 +384,7 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs
     const bool live = c < A.channels;
     const int64_t C = A.channels;
     ScanSpan s;
-    if (!scan_span(A, blockIdx.x, s)) return;
+    if (!scan_span(A, PHASE == kScanApply ? gridDim.x - 1 - blockIdx.x : blockIdx.x, s)) return;
     if (s.seg == 0 || s.seg == A.samples + 1) {
         if (PHASE != kScanSum) {
             zero_rows<T, VEC, W>(A.dx, s, C, unit, c, live);

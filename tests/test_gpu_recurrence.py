@@ -67,11 +67,22 @@ def test_long_sequences_are_split(dtype, lengths):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_samples_of_very_different_lengths(dtype):
-    """Enough long samples that the longest go first, empty and short ones among them."""
+    """Many samples, long, short and empty ones beside one another, none of them cut."""
     gen = torch.Generator().manual_seed(16)
     lengths = torch.randint(0, 700, (130,), generator=gen).tolist()
     lengths[3], lengths[50], lengths[129] = 0, 1, 0
     check(*make(dtype, lengths, 130, masked=0.1, seed=17))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("channels", [33, 96])
+def test_short_samples_with_a_long_one(dtype, channels):
+    """A mean between 33 and 128 rows: four wavefronts, and one sample of many of their blocks."""
+    gen = torch.Generator().manual_seed(20)
+    lengths = torch.randint(0, 100, (40,), generator=gen).tolist()
+    lengths[7], lengths[8], lengths[39] = 1300, 0, 64
+    assert 32 < sum(lengths) // 40 <= 128
+    check(*make(dtype, lengths, channels, masked=0.1, seed=21))
 
 
 def test_many_samples():
