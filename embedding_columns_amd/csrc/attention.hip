@@ -326,13 +326,12 @@ __device__ __forceinline__ float wave_sum(float x)
 struct Range {
     int lo, hi;
 };
-// of the 32 values of half 0, which half 1 repeats: the ends where they are in order, as
-// positions mostly are
-__device__ __forceinline__ Range half_range(int x)
+// of the 32 values of half u: the ends where they are in order, as positions mostly are
+__device__ __forceinline__ Range half_range(int x, int u = 0)
 {
     const int before = EMB_DPP(x, 0x138, 0xF);      // wave_shr:1, lane 0 keeps its own
-    if ((uint32_t)__ballot(before <= x) == 0xFFFFFFFFu)
-        return Range{__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 31)};
+    if (((uint32_t)(__ballot(before <= x) >> (32 * u)) | 1) == 0xFFFFFFFFu)
+        return Range{__builtin_amdgcn_readlane(x, 32 * u), __builtin_amdgcn_readlane(x, 32 * u + 31)};
     int a = x, b = x;
     a = min(a, EMB_DPP(a, 0xB1, 0xF));
     b = max(b, EMB_DPP(b, 0xB1, 0xF));
@@ -342,8 +341,8 @@ __device__ __forceinline__ Range half_range(int x)
     b = max(b, EMB_DPP(b, 0x141, 0xF));
     a = min(a, EMB_DPP(a, 0x140, 0xF));
     b = max(b, EMB_DPP(b, 0x140, 0xF));
-    return Range{min(__builtin_amdgcn_readlane(a, 0), __builtin_amdgcn_readlane(a, 16)),
-                 max(__builtin_amdgcn_readlane(b, 0), __builtin_amdgcn_readlane(b, 16))};
+    return Range{min(__builtin_amdgcn_readlane(a, 32 * u), __builtin_amdgcn_readlane(a, 32 * u + 16)),
+                 max(__builtin_amdgcn_readlane(b, 32 * u), __builtin_amdgcn_readlane(b, 32 * u + 16))};
 }
 #undef EMB_DPP
 
@@ -553,35 +552,36 @@ constexpr bool kBiasFirst = sizeof(T) == 2;
 // range is a compare and a select on what the block starts from, and b is zero.  This
 // is for blocks outside the bucket of `run`: afterwards `run` is the bucket of the
 // block's smallest distance and b_run its bias.
-// `kpos`: 32 words of LDS of this wavefront, `kp`: position of key lane & 31.
+// `kpos`: positions of the tile's keys in LDS, `pos`: the same, one a lane; u: which 32.
+// Everything that comes out of LDS is asked for together: the latency of this is what a
+// mixed block costs.
 __device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, const float *lb, const int *lbnd,
-                                           const Row &R, int *kpos, int kp, BucketRun &run, f32x16_t &s, float &b,
-                                           float &b_run)
+                                           const Row &R, const int *kpos, int pos, int u, BucketRun &run,
+                                           f32x16_t &s, float &b, float &b_run)
 {
-    const Range k = half_range(kp);
+    const int h = lane_id() >> 5;
+    int4 k4[4];
+#pragma unroll
+    for (int g = 0; g < 4; g++) k4[g] = *reinterpret_cast<const int4 *>(kpos + 32 * u + 8 * g + 4 * h);
+    const Range k = half_range(pos, u);
     const int lo = B.bucket(sub_sat(R.r.lo, k.hi)), hi = B.bucket(sub_sat(R.r.hi, k.lo));
     const float *mine = lb + R.g;
     const float base = mine[lo * A.group];
+    float v = mine[min(lo + 1, hi) * A.group];
+    int edge = lbnd[lo];                 // not read for the last bucket
     run.set(B, lbnd, lo);
     b = b_run = base * A.c;
     if (lo == hi) return;
     b = 0.f;
-    kpos[lane_id() & 31] = kp;
-    wave_sync();
     int x[16];
-    const int h = lane_id() >> 5;
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-        const int4 k4 = *reinterpret_cast<const int4 *>(kpos + 8 * g + 4 * h);
-        x[4 * g] = sub_sat(R.pos, k4.x);
-        x[4 * g + 1] = sub_sat(R.pos, k4.y);
-        x[4 * g + 2] = sub_sat(R.pos, k4.z);
-        x[4 * g + 3] = sub_sat(R.pos, k4.w);
+        x[4 * g] = sub_sat(R.pos, k4[g].x);
+        x[4 * g + 1] = sub_sat(R.pos, k4[g].y);
+        x[4 * g + 2] = sub_sat(R.pos, k4[g].z);
+        x[4 * g + 3] = sub_sat(R.pos, k4[g].w);
     }
-    wave_sync();
     // s holds 0 or products, or -inf where a key takes no part
-    float v = mine[(lo + 1) * A.group];
-    int edge = lbnd[lo];
     f32x16_t t;
 #pragma unroll
     for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : base;
@@ -767,7 +767,7 @@ constexpr float kLag = 8.f;
 // is as large; their sum l is of the fp32 weights.
 // Serving 122 us (4.7 TB/s of its 576 MB) and lifelong 84 us and 5 us for the join (4.6
 // TB/s of 408 MB), where a large copy has 5.5: the reading bounds them.  Two sequences
-// 218 us, 458 TFLOP/s (without a bias 157): two wavefronts a SIMD alternate between
+// 216 us, 462 TFLOP/s (without a bias 157): two wavefronts a SIMD alternate between
 // products and weights, and the blocks whose pairs fall into several buckets cost the
 // rest.  Many candidates 61 us, 154 TFLOP/s (without a bias 46): a workgroup has 9 steps
 // between its first loads (four dependent ones) and its join, and these do not overlap.
@@ -778,7 +778,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     constexpr int SUBS = KW::KT / 32;
     __shared__ __align__(1024) u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];    // 16 KB for sum_waves
     __shared__ int lbnd[kBucketsMax];
-    __shared__ __align__(16) int kpos[4][32];
+    __shared__ __align__(16) int kpos[4][32 * SUBS];
     __shared__ __align__(16) float kout[4][32];
     __shared__ float jm[4][32], jl[4][32];
     extern __shared__ float lb[];
@@ -822,6 +822,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         f32x16_t sc[SUBS];
         float b[SUBS], top = -INFINITY;
         uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : ~0ull;
+        if (~in_run) {
+            kpos[w][lane & (32 * SUBS - 1)] = walk.pos;
+            wave_sync();
+        }
 #pragma unroll
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
@@ -836,8 +840,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
             b[u] = b_run;
             if (!kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
             if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
-                const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
-                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc[u], b[u], b_run);
+                mixed_bias(A, B, lb, lbnd, R, kpos[w], walk.pos, u, run, sc[u], b[u], b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
             if (kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
@@ -985,7 +988,7 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 // in that rounding: taken again from the probabilities in fp32, delta costs one addition
 // a pair.  (Correcting dq for it too, by sum_j p_ij k_j, would be a fourth product.)
 // dS enters its product in T, as q and k do.
-// The walk is the forward's, and so is what bounds it.  Two sequences 263 us, 569 TFLOP/s
+// The walk is the forward's, and so is what bounds it.  Two sequences 261 us, 574 TFLOP/s
 // of its three products (without a bias 202); ranking 50 us (41).
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_backward_q(AttnArgs A)
@@ -995,7 +998,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     constexpr int SUBS = KW::KT / 32;
     __shared__ __align__(1024) u32x4_t lds[KW::kLds > 1024 ? KW::kLds : 1024];
     __shared__ int lbnd[kBucketsMax];
-    __shared__ __align__(16) int kpos[4][32];
+    __shared__ __align__(16) int kpos[4][32 * SUBS];
     __shared__ float jd[4][32];
     extern __shared__ float lb[];
 
@@ -1055,6 +1058,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         walk.enter();
         const u32x4_t *lk = walk.k_tile(), *lv = walk.v_tile();
         uint64_t in_run = A.bias ? run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos)) : ~0ull;
+        if (~in_run) {
+            kpos[w][lane & (32 * SUBS - 1)] = walk.pos;
+            wave_sync();
+        }
 #pragma unroll DP * sizeof(T) > 128 ? 1 : SUBS
         for (int u = 0; u < SUBS; u++) {
             const uint32_t keep = (uint32_t)(walk.keep >> (32 * u));
@@ -1064,8 +1071,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
             float b = b_run;
             if (!kBiasFirst<T>) products<T, DP>(sc, lk, u * 32, qf);
             if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
-                const int kp = SUBS == 2 ? __shfl(walk.pos, 32 * u + (lane & 31)) : walk.pos;
-                mixed_bias(A, B, lb, lbnd, R, kpos[w], kp, run, sc, b, b_run);
+                mixed_bias(A, B, lb, lbnd, R, kpos[w], walk.pos, u, run, sc, b, b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
             if (kBiasFirst<T>) products<T, DP>(sc, lk, u * 32, qf);
