@@ -423,11 +423,14 @@ struct BucketRun {
 // piece lands at to + 16 l.  `off` counts bytes from the descriptor's base (plus the
 // uniform `more`); an offset of kNowhere is out of the descriptor's range, reads no
 // memory and lands as zeros.  The load is asynchronous (vmcnt): the compiler does not
-// know of it, so the reader waits itself (arrived) before it reads.
+// know of it, so the reader waits itself (arrived) before it reads.  Nor does it look for
+// hazards in here: a scalar operand that a vector instruction wrote (readfirstlane, or a
+// register spilled to lanes) may be read five wait states later, and the move and the
+// s_nop are those five whatever came before.
 constexpr uint32_t kNowhere = 0x80000000u;
 __device__ __forceinline__ void load_to_lds(i32x4_t rsrc, uint32_t to, uint32_t off, uint32_t more)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(to), "v"(off), "s"(rsrc), "s"(more)
                  : "memory");
