@@ -772,6 +772,24 @@ def _second_order():
                            "cannot run with create_graph=True")
 
 
+def _places(tensors, rows):
+    """Where the tensors of a descriptor lie, and how those with strided rows (the first)."""
+    at = [t if t is None else t.data_ptr() for t in tensors]
+    for t in tensors[:rows]:
+        at += (t.dtype, t.stride())
+    return at
+
+
+def _given_back(saved, rows, count, places):
+    """Saved tensors as autograd hands them to a backward pass, and whether a descriptor of the
+    first `count` still holds.  Under saved-tensor hooks (activation checkpointing, offloading)
+    they are others than the forward saved, of the same values in a layout of the hook's choice;
+    the first `rows` may have strided rows."""
+    saved = [t if t is None or t.is_contiguous() or (i < rows and t.stride(-1) == 1)
+             else t.contiguous() for i, t in enumerate(saved)]
+    return saved, _places(saved[:count], rows) == places
+
+
 class CrossAttention(torch.autograd.Function):
     """cross_attention as an autograd node: gradients of q, k, v and the bias table."""
 
@@ -786,20 +804,22 @@ class CrossAttention(torch.autograd.Function):
         ws = _scratch(need, q)
         _check(lib().emb_attention_forward(C.byref(desc), out.data_ptr(), _address(rest),
                                            lse.data_ptr(), _address(ws), need, _stream()))
-        # the saved tensors keep alive, and unchanged, what the descriptor points to
-        ctx.save_for_backward(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos,
-                              out, rest, lse)
-        ctx.desc = desc
+        read = q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos
+        ctx.save_for_backward(*read, out, rest, lse)
+        ctx.desc, ctx.scale, ctx.places = desc, scale, _places(read, 3)
         return out
 
     @staticmethod
     def backward(ctx, dout):
         _second_order()
-        q, k, _, bias, _, _, _, _, _, _, out, rest, lse = ctx.saved_tensors
+        saved, in_place = _given_back(ctx.saved_tensors, 3, 10, ctx.places)
+        q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, out, rest, lse = saved
         if dout.dtype is not q.dtype:
             raise TypeError("the output's gradient must have the output's type")
         if dout.stride(-1) != 1 and dout.shape[-1] > 1:
             dout = dout.contiguous()
+        desc = ctx.desc if in_place else _attention_desc(
+            q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos, k_pos, ctx.scale)
         want = ctx.needs_input_grad
         dq = q.new_empty(q.shape)
         dk = dv = dbias = None
@@ -809,7 +829,7 @@ class CrossAttention(torch.autograd.Function):
             dbias = bias.new_empty(bias.shape)
         ws = _scratch(ctx.need, q)
         _check(lib().emb_attention_backward(
-            C.byref(ctx.desc), out.data_ptr(), _address(rest), lse.data_ptr(), _rows_ptr(dout, 3),
+            C.byref(desc), out.data_ptr(), _address(rest), lse.data_ptr(), _rows_ptr(dout, 3),
             dout.stride(0), dout.stride(1), dq.data_ptr(), _address(dk), _address(dv),
             _address(dbias), _address(ws), ctx.need, _stream()))
         return dq, dk, dv, dbias, None, None, None, None, None, None, None
@@ -869,16 +889,17 @@ class GatedRecurrence(torch.autograd.Function):
         ws = _scratch(ctx.need, x)
         _check(lib().emb_recurrence_forward(C.byref(desc), y.data_ptr(), last.data_ptr(),
                                             saved.data_ptr(), _address(ws), ctx.need, _stream()))
-        # the saved tensors keep alive, and unchanged, what the descriptor points to
-        ctx.save_for_backward(x, gate, state, offsets, mask, saved)
-        ctx.desc = desc
+        read = x, gate, state, offsets, mask
+        ctx.save_for_backward(*read, saved)
+        ctx.desc, ctx.places = desc, _places(read, 2)
         ctx.set_materialize_grads(False)
         return y, last
 
     @staticmethod
     def backward(ctx, dy, dlast):
         _second_order()
-        x, _, state, _, _, saved = ctx.saved_tensors
+        given, in_place = _given_back(ctx.saved_tensors, 2, 5, ctx.places)
+        x, gate, state, offsets, mask, saved = given
         if dy is None:
             dy = x.new_zeros(x.shape)
         if dy.dtype is not x.dtype:
@@ -887,9 +908,10 @@ class GatedRecurrence(torch.autograd.Function):
         dx, dgate, dstate = x.new_empty(x.shape), x.new_empty(x.shape), None
         if state is not None and ctx.needs_input_grad[2]:
             dstate = state.new_empty(state.shape)
+        desc = ctx.desc if in_place else _recurrence_desc(x, gate, offsets, state, mask)
         ws = _scratch(ctx.need, x)
         _check(lib().emb_recurrence_backward(
-            C.byref(ctx.desc), saved.data_ptr(), dy.data_ptr(), _address(dlast), dx.data_ptr(),
+            C.byref(desc), saved.data_ptr(), dy.data_ptr(), _address(dlast), dx.data_ptr(),
             dgate.data_ptr(), _address(dstate), _address(ws), ctx.need, _stream()))
         return dx, dgate, dstate, None, None
 
