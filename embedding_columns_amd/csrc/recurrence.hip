@@ -592,16 +592,25 @@ ScanPlan scan_plan(const emb_recurrence *r)
 constexpr int64_t kStrideMost = (int64_t(1) << 21) - 1;
 static_assert(kStrideMost * 4 * 2 * kWaves * kSteps < int64_t(1) << 31, "a block of rows fits a descriptor");
 
+// The stride of a single row leads nowhere, and may be anything (a transposed column's is 1,
+// a broadcast row's 0).  The kernels take the length of the rows' buffers from it, so there
+// it becomes the row's own length.
+emb_recurrence with_strides(const emb_recurrence *r)
+{
+    emb_recurrence own = *r;
+    if (own.n <= 1) own.x_stride = own.gate_stride = own.channels;
+    return own;
+}
+
 emb_status scan_check(const emb_recurrence *r)
 {
-    if (!r) return fail(EMB_ERR_INVALID_ARG, "recurrence descriptor is NULL");
     if (r->dtype != EMB_F32 && r->dtype != EMB_BF16) return fail(EMB_ERR_INVALID_ARG, "recurrence: unknown dtype");
     if (r->samples < 0 || r->n < 0) return fail(EMB_ERR_INVALID_ARG, "recurrence: samples and n must be >= 0");
     if (r->channels <= 0) return fail(EMB_ERR_INVALID_ARG, "recurrence: channels must be >= 1");
     if (r->channels > (1 << 20)) return fail(EMB_ERR_UNSUPPORTED, "recurrence: channels must be <= 2^20");
     if (r->n > kRowsMost || r->samples > (1 << 30))
         return fail(EMB_ERR_UNSUPPORTED, "recurrence: n must be <= 2^31 - 65536 and samples <= 2^30");
-    if (r->n > 1 && (r->x_stride < r->channels || r->gate_stride < r->channels))
+    if (r->x_stride < r->channels || r->gate_stride < r->channels)
         return fail(EMB_ERR_INVALID_ARG, "recurrence: row strides must be >= channels");
     if (r->x_stride > kStrideMost || r->gate_stride > kStrideMost)
         return fail(EMB_ERR_UNSUPPORTED, "recurrence: row strides must be < 2^21");
@@ -700,8 +709,10 @@ ScanArgs scan_args(const emb_recurrence *r, const ScanPlan &p, void *ws)
 
 }  // namespace
 
-extern "C" emb_status emb_recurrence_query(const emb_recurrence *r, int64_t *saved_rows, size_t *workspace_bytes)
+extern "C" emb_status emb_recurrence_query(const emb_recurrence *desc, int64_t *saved_rows, size_t *workspace_bytes)
 {
+    if (!desc) return fail(EMB_ERR_INVALID_ARG, "recurrence descriptor is NULL");
+    const emb_recurrence own = with_strides(desc), *r = &own;
     const emb_status s = scan_check(r);
     if (s != EMB_OK) return s;
     if (!saved_rows || !workspace_bytes) return fail(EMB_ERR_INVALID_ARG, "recurrence: output pointers must be given");
@@ -711,9 +722,11 @@ extern "C" emb_status emb_recurrence_query(const emb_recurrence *r, int64_t *sav
     return EMB_OK;
 }
 
-extern "C" emb_status emb_recurrence_forward(const emb_recurrence *r, void *y, float *last, float *saved,
+extern "C" emb_status emb_recurrence_forward(const emb_recurrence *desc, void *y, float *last, float *saved,
                                              void *workspace, size_t workspace_bytes, void *stream)
 {
+    if (!desc) return fail(EMB_ERR_INVALID_ARG, "recurrence descriptor is NULL");
+    const emb_recurrence own = with_strides(desc), *r = &own;
     emb_status s = scan_check(r);
     if (s == EMB_OK) s = scan_pointers(r);
     if (s != EMB_OK) return s;
@@ -731,10 +744,12 @@ extern "C" emb_status emb_recurrence_forward(const emb_recurrence *r, void *y, f
     return scan_launch(r, A, p.waves, pairs_ok(r, {y}), false, stream);
 }
 
-extern "C" emb_status emb_recurrence_backward(const emb_recurrence *r, const float *saved, const void *dy,
+extern "C" emb_status emb_recurrence_backward(const emb_recurrence *desc, const float *saved, const void *dy,
                                               const float *dlast, void *dx, void *dgate, float *dstate,
                                               void *workspace, size_t workspace_bytes, void *stream)
 {
+    if (!desc) return fail(EMB_ERR_INVALID_ARG, "recurrence descriptor is NULL");
+    const emb_recurrence own = with_strides(desc), *r = &own;
     emb_status s = scan_check(r);
     if (s == EMB_OK) s = scan_pointers(r);
     if (s != EMB_OK) return s;
@@ -770,6 +785,7 @@ extern "C" emb_status emb_recurrence_step(int32_t dtype, int64_t rows, int32_t c
     r.gate_stride = gate_stride;
     r.x = x;
     r.gate = gate;
+    r = with_strides(&r);
     const emb_status s = scan_check(&r);
     if (s != EMB_OK) return s;
     const size_t el = dtype == EMB_BF16 ? 2 : 4;
@@ -786,19 +802,19 @@ extern "C" emb_status emb_recurrence_step(int32_t dtype, int64_t rows, int32_t c
     const hipStream_t st = static_cast<hipStream_t>(stream);
     if (dtype == EMB_BF16 && pairs)
         hipLaunchKernelGGL((scan_step<uint16_t, 2>), grid, block, 0, st, static_cast<const uint16_t *>(x),
-                           static_cast<const uint16_t *>(gate), x_stride, gate_stride, state,
+                           static_cast<const uint16_t *>(gate), r.x_stride, r.gate_stride, state,
                            static_cast<uint16_t *>(y), rows, (int64_t)channels);
     else if (dtype == EMB_BF16)
         hipLaunchKernelGGL((scan_step<uint16_t, 1>), grid, block, 0, st, static_cast<const uint16_t *>(x),
-                           static_cast<const uint16_t *>(gate), x_stride, gate_stride, state,
+                           static_cast<const uint16_t *>(gate), r.x_stride, r.gate_stride, state,
                            static_cast<uint16_t *>(y), rows, (int64_t)channels);
     else if (pairs)
         hipLaunchKernelGGL((scan_step<float, 2>), grid, block, 0, st, static_cast<const float *>(x),
-                           static_cast<const float *>(gate), x_stride, gate_stride, state, static_cast<float *>(y),
+                           static_cast<const float *>(gate), r.x_stride, r.gate_stride, state, static_cast<float *>(y),
                            rows, (int64_t)channels);
     else
         hipLaunchKernelGGL((scan_step<float, 1>), grid, block, 0, st, static_cast<const float *>(x),
-                           static_cast<const float *>(gate), x_stride, gate_stride, state, static_cast<float *>(y),
+                           static_cast<const float *>(gate), r.x_stride, r.gate_stride, state, static_cast<float *>(y),
                            rows, (int64_t)channels);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(EMB_ERR_HIP, std::string("recurrence step launch: ") + hipGetErrorString(e));

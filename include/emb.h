@@ -489,7 +489,7 @@ typedef struct emb_recurrence {  /* host */
     int32_t reserved;
     int64_t n;                   /* rows                                                     */
     const void *x, *gate;        /* [n, channels], rows x_stride / gate_stride elements apart */
-    int64_t x_stride, gate_stride;         /* < 2^21                                         */
+    int64_t x_stride, gate_stride;         /* >= channels, < 2^21; not read where n <= 1     */
     const int32_t *offsets;      /* [samples + 1]                                            */
     const uint8_t *mask;         /* [n] or NULL                                              */
     const float *state;          /* [samples, channels] or NULL (zero)                        */
