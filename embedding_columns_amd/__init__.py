@@ -14,6 +14,7 @@ import os
 import struct
 
 import torch
+from torch.autograd import forward_ad
 
 __all__ = [
     "EmbError", "lib", "library_path", "ColumnDesc", "PlanOpts",
@@ -765,6 +766,16 @@ def _attention_desc(q, k, v, q_offsets, k_offsets, mask, bias, boundaries, q_pos
         _offsets_ptr(k_offsets, "k_offsets", dev), _mask_ptr(mask, nk, dev), pq, pk, pb, pt))
 
 
+def _no_tangents(*tensors):
+    """Raw addresses carry no forward-mode tangents, so a call that has one is refused."""
+    if getattr(forward_ad, "_current_level", 0) < 0:      # outside dual_level there are none
+        return
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise RuntimeError("the sequence operators have no forward-mode derivatives: a tangent "
+                               "of their inputs would be lost")
+
+
 def _second_order():
     """Backward passes run without grad mode, except under create_graph=True."""
     if torch.is_grad_enabled():
@@ -812,6 +823,7 @@ class CrossAttention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         _second_order()
+        _no_tangents(dout)
         saved, in_place = _given_back(ctx.saved_tensors, 3, 10, ctx.places)
         q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos, k_pos, out, rest, lse = saved
         if dout.dtype is not q.dtype:
@@ -847,6 +859,7 @@ def cross_attention(q, k, v, q_offsets, k_offsets, mask=None, bias=None, boundar
     ascending, positions int32).  scale: dim ** -0.5 unless given.  Returns
     [n_q, heads, dim]; a row without any key gives zero.  Differentiable in q, k, v and
     bias; runs on the current stream."""
+    _no_tangents(q, k, v, bias)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
                                     (bias is not None and bias.requires_grad)):
         return CrossAttention.apply(q, k, v, bias, q_offsets, k_offsets, mask, boundaries, q_pos,
@@ -898,6 +911,7 @@ class GatedRecurrence(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy, dlast):
         _second_order()
+        _no_tangents(dy, dlast)
         given, in_place = _given_back(ctx.saved_tensors, 2, 5, ctx.places)
         x, gate, state, offsets, mask, saved = given
         if dy is None:
@@ -924,6 +938,7 @@ def gated_recurrence(x, gate, offsets, state=None, mask=None):
     mask: uint8 or bool [n], 0 keeps the state as it is.  Returns (y [n, channels], the
     states at every row, last fp32 [samples, channels], those after the last rows).
     Differentiable in x, gate and state; runs on the current stream."""
+    _no_tangents(x, gate, state)
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or
                                     (state is not None and state.requires_grad)):
         return GatedRecurrence.apply(x, gate, state, offsets, mask)
@@ -941,6 +956,7 @@ def gated_recurrence_step(x, gate, state, out=None):
     """One step of the recurrence for a batch of states (serving): x, gate [rows, channels],
     state fp32 [rows, channels], updated in place; returns it in x's type.  Not
     differentiable."""
+    _no_tangents(x, gate, state)
     xp, gp = _rows_ptr(x, 2), _rows_ptr(gate, 2)
     dev = _same(x, gate)
     if gate.shape != x.shape:

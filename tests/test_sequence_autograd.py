@@ -129,3 +129,67 @@ def test_checkpointed_blocks_read_what_was_recomputed(calls):
     torch.utils.checkpoint.checkpoint(block, d["q"], use_reentrant=False).sum().backward()
     assert len(seen) == 2
     assert calls.last("emb_attention_backward")[0].q == seen[1]
+
+
+def direction(t):
+    return torch.ones_like(t)
+
+
+def test_forward_mode_is_refused(calls):
+    """No tangent is computed, so none may be lost without a word."""
+    fw = torch.autograd.forward_ad
+    for make, call, names in ((attention, E.cross_attention, ("q", "k", "v", "bias")),
+                              (recurrence, E.gated_recurrence, ("x", "gate", "state"))):
+        for name in names:
+            for grad in (False, True):
+                d = {n: t.detach().requires_grad_(grad and t.is_floating_point()) for n, t in make().items()}
+                with fw.dual_level():
+                    d[name] = fw.make_dual(d[name], direction(d[name]))
+                    with pytest.raises(RuntimeError, match="forward"):
+                        call(**d)
+                    with torch.no_grad(), pytest.raises(RuntimeError, match="forward"):
+                        call(**d)
+                    d[name] = fw.unpack_dual(d[name]).primal
+                    call(**d)                    # without a tangent it goes through
+    x = torch.randn(3, 4)
+    with fw.dual_level():
+        for i in range(3):
+            step = [x, x, x.clone()]
+            step[i] = fw.make_dual(step[i], x)
+            with pytest.raises(RuntimeError, match="forward"):
+                E.gated_recurrence_step(*step)
+        E.gated_recurrence_step(x, x, x.clone())
+
+
+def test_forward_mode_through_a_backward_pass_is_refused(calls):
+    fw = torch.autograd.forward_ad
+    d, r = attention(), recurrence()
+    out, (y, last) = E.cross_attention(**d), E.gated_recurrence(**r)
+    with fw.dual_level():
+        for outs, given, at in (([out], [torch.ones_like(out)], 0), ([y, last], [torch.ones_like(y), direction(last)], 0),
+                                ([y, last], [torch.ones_like(y), direction(last)], 1)):
+            given[at] = fw.make_dual(given[at], direction(given[at]))
+            with pytest.raises(RuntimeError, match="forward"):
+                torch.autograd.grad(outs, d["q"] if outs[0] is out else r["x"], given, retain_graph=True)
+
+
+def test_function_transforms_do_not_go_through(calls):
+    d = {n: t.detach() for n, t in attention().items()}
+
+    def of_q(q):
+        return E.cross_attention(**{**d, "q": q})
+    for call in (lambda: torch.func.jvp(of_q, (d["q"],), (direction(d["q"]),)),
+                 lambda: torch.func.grad(lambda q: of_q(q).sum())(d["q"]),
+                 lambda: torch.func.vmap(of_q)(d["q"][None])):
+        with pytest.raises(Exception):
+            call()
+    assert not any(name == "emb_attention_forward" for name, _, _ in calls.made)
+
+
+def test_second_derivatives_are_refused(calls):
+    out = E.cross_attention(**(d := attention()))
+    with pytest.raises(RuntimeError, match="first derivatives"):
+        torch.autograd.grad(out.sum(), d["q"], create_graph=True)
+    y, _ = E.gated_recurrence(**(r := recurrence()))
+    with pytest.raises(RuntimeError, match="first derivatives"):
+        torch.autograd.grad(y.sum(), r["x"], create_graph=True)
