@@ -952,6 +952,12 @@ def gated_recurrence(x, gate, offsets, state=None, mask=None):
     return y, last
 
 
+def _written(t):
+    """Tells autograd that a caller's tensor changed: a graph that saved it must not use it now."""
+    if not t.is_inference():             # inference tensors have no version
+        torch.autograd.graph.increment_version(t)
+
+
 def gated_recurrence_step(x, gate, state, out=None):
     """One step of the recurrence for a batch of states (serving): x, gate [rows, channels],
     state fp32 [rows, channels], updated in place; returns it in x's type.  Not
@@ -962,14 +968,18 @@ def gated_recurrence_step(x, gate, state, out=None):
     if gate.shape != x.shape:
         raise ValueError(f"x {tuple(x.shape)} and gate {tuple(gate.shape)} do not fit")
     sp = _want(state, "state", torch.float32, x.shape, dev)
-    if out is None:
+    given = out is not None
+    if given:
+        yp = _want(out, "out", x.dtype, x.shape, dev)
+    else:
         out = x.new_empty(x.shape)
         yp = out.data_ptr()
-    else:
-        yp = _want(out, "out", x.dtype, x.shape, dev)
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or state.requires_grad):
         raise ValueError("gated_recurrence_step has no gradient: use gated_recurrence")
     rows, channels = x.shape
     _check(lib().emb_recurrence_step(_SEQ_DTYPE[x.dtype], rows, channels, xp, x.stride(0), gp,
                                      gate.stride(0), sp, yp, _stream()))
+    _written(state)
+    if given:
+        _written(out)
     return out

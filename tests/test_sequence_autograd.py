@@ -193,3 +193,28 @@ def test_second_derivatives_are_refused(calls):
     y, _ = E.gated_recurrence(**(r := recurrence()))
     with pytest.raises(RuntimeError, match="first derivatives"):
         torch.autograd.grad(y.sum(), r["x"], create_graph=True)
+
+
+def test_a_step_tells_autograd_that_it_writes(calls):
+    """What a step overwrites, a graph that saved it may not use any more."""
+    x, state, out, w = torch.randn(3, 4), torch.randn(3, 4), torch.zeros(3, 4), torch.ones(3, 4)
+    w.requires_grad_()
+    for saved in (state, out):
+        graph = (w * saved).sum()
+        E.gated_recurrence_step(x, x, state, out=out)
+        with pytest.raises(RuntimeError, match="inplace"):
+            graph.backward()
+    versions = state._version, out._version
+    E.gated_recurrence_step(x, x, state, out=out)
+    assert (state._version, out._version) == (versions[0] + 1, versions[1] + 1)
+    assert x._version == 0
+
+
+def test_a_step_in_inference_mode(calls):
+    """There tensors have no versions, and ordinary ones may be mixed in."""
+    plain = torch.randn(3, 4)
+    with torch.inference_mode():
+        x, state = torch.randn(3, 4), torch.randn(3, 4)
+        assert E.gated_recurrence_step(x, x, state).shape == (3, 4)
+        E.gated_recurrence_step(x, x, plain, out=state)
+    E.gated_recurrence_step(x, x, state, out=plain)
