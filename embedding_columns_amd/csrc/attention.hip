@@ -555,12 +555,14 @@ constexpr bool kBiasFirst = sizeof(T) == 2;
 // range is a compare and a select on what the block starts from, and b is zero.  This
 // is for blocks outside the bucket of `run`: afterwards `run` is the bucket of the
 // block's smallest distance and b_run its bias.
-// `kpos`: positions of the tile's keys in LDS, `pos`: the same, one a lane; u: which 32.
+// `kpos`: positions of the tile's keys in LDS, `pos`: the same, one a lane; u: which 32;
+// all: no key of the block is at -inf already.
 // Everything that comes out of LDS is asked for together: the latency of this is what a
 // mixed block costs.
+template <typename T>
 __device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, const float *lb, const int *lbnd,
-                                           const Row &R, const int *kpos, int pos, int u, BucketRun &run,
-                                           f32x16_t &s, float &b, float &b_run)
+                                           const Row &R, const int *kpos, int pos, int u, bool all,
+                                           BucketRun &run, f32x16_t &s, float &b, float &b_run)
 {
     const int h = lane_id() >> 5;
     int4 k4[4];
@@ -584,7 +586,6 @@ __device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, con
         x[4 * g + 2] = sub_sat(R.pos, k4[g].z);
         x[4 * g + 3] = sub_sat(R.pos, k4[g].w);
     }
-    // s holds 0 or products, or -inf where a key takes no part
     f32x16_t t;
 #pragma unroll
     for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : base;
@@ -594,7 +595,15 @@ __device__ __forceinline__ void mixed_bias(const AttnArgs &A, const Bias &B, con
 #pragma unroll
         for (int i = 0; i < 16; i++) t[i] = x[i] >= edge ? v : t[i];
     }
-    s += t;
+    // s holds 0 or products, or -inf where a key takes no part: there whatever t holds, an
+    // infinity or NaN too
+    const f32x16_t with = kBiasFirst<T> ? t : s + t;
+    if (all) {
+        s = with;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; i++) s[i] = s[i] == -INFINITY ? s[i] : with[i];
+    }
 }
 
 // What the kernels that walk the keys share.  WM = 4: the four wavefronts take 32 query
@@ -843,9 +852,11 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
             b[u] = b_run;
             if (!kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
             if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
-                mixed_bias(A, B, lb, lbnd, R, kpos[w], walk.pos, u, run, sc[u], b[u], b_run);
+                mixed_bias<T>(A, B, lb, lbnd, R, kpos[w], walk.pos, u, keep == 0xFFFFFFFFu, run, sc[u], b[u],
+                              b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
+            b[u] = keep ? b[u] : 0.f;
             if (kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
         }
 #pragma unroll
@@ -1074,7 +1085,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
             float b = b_run;
             if (!kBiasFirst<T>) products<T, DP>(sc, lk, u * 32, qf);
             if (~in_run >> (32 * u) & 0xFFFFFFFFu) {
-                mixed_bias(A, B, lb, lbnd, R, kpos[w], walk.pos, u, run, sc, b, b_run);
+                mixed_bias<T>(A, B, lb, lbnd, R, kpos[w], walk.pos, u, true, run, sc, b, b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
             if (kBiasFirst<T>) products<T, DP>(sc, lk, u * 32, qf);
