@@ -1409,27 +1409,29 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                 typename Mma<T>::template Rows<DP>(lq, 0, d).times(dk[d], ds);
             }
             if (A.dbias_part) {
-                float all = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; i++) all += dp[i];
                 if (lo != hi) {
-                    // a bucket's sum is what lies below its upper boundary, less what lay
-                    // below the one before it
+                    // each bucket's own terms: what a boundary leaves below it is taken out.  (What
+                    // lies below one less what lay below the one before costs three operations a
+                    // pair, not four, but a small sum beside a large one would lose its digits.)
                     int x[16];
                     distances(qpos[cur], kpos, x);
-                    float under = 0.f;
                     for (int m = lo; m < hi; m++) {
                         const int edge = lbnd[m];
                         float sum = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 16; i++) sum += x[i] < edge ? dp[i] : 0.f;
-                        settle(m, sum_run + (sum - under));
-                        under = sum;
+                        for (int i = 0; i < 16; i++) {
+                            const bool below = x[i] < edge;
+                            sum += below ? dp[i] : 0.f;
+                            dp[i] = below ? 0.f : dp[i];
+                        }
+                        settle(m, sum_run + sum);
                         sum_run = 0.f;
                     }
-                    all -= under;
                 }
-                sum_run += all;
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; i++) sum += dp[i];
+                sum_run += sum;
             }
         }
         const int last_m = run.m;

@@ -32,3 +32,33 @@ def test_a_masked_key_brings_no_bias(dtype, entry, heads, kv_heads, q_len):
     got = run(d, dout)
     for name in want:
         assert torch.equal(got[name], want[name]), name
+
+
+def neighbours(dtype, keys):
+    """32 rows that share a block with buckets of their own: row i's keys in bucket i // 4."""
+    d, dout = make(dtype, [32], [keys], 1, 1, 32, buckets=8, seed=30)
+    d["k_pos"][:] = 0
+    d["q_pos"][:] = torch.arange(32, dtype=torch.int32) // 4
+    d["boundaries"] = torch.arange(1, 8, dtype=torch.int32, device="cuda")
+    return d, dout
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("junk", [math.nan, math.inf])
+@pytest.mark.parametrize("row", [0, 13, 31])
+def test_a_bucket_gets_its_own_gradients_alone(dtype, junk, row):
+    d, dout = neighbours(dtype, 32)
+    want = run(d, dout)["dbias"]
+    dout[row] = junk
+    got = run(d, dout)["dbias"]
+    others = torch.arange(8, device="cuda") != row // 4
+    assert torch.equal(got[others], want[others]) and not torch.isfinite(got[row // 4]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("large", [0, 3, 7])
+def test_a_small_bucket_beside_a_large_one(dtype, large):
+    """Each bucket's sum within the bound of its own terms."""
+    d, dout = neighbours(dtype, 150)
+    dout[4 * large:4 * large + 4] *= 2.0 ** 24
+    ref.check(run(d, dout)["dbias"], ref.attention(**d, dout=dout)["dbias"], "dbias")
