@@ -1037,6 +1037,10 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
     walk.start();
     B.put(A, kvh, lb, lbnd);
     R.range();
+    // a row without keys has no gradient, whatever arrives for its output
+    if (lse == -INFINITY)
+#pragma unroll
+        for (int c = 0; c < TL::CH / 2; c++) df[c] = u32x4_t{0, 0, 0, 0};
     {
         Frag<T, DP> of;
         load_frag<T, DP>(of, static_cast<const T *>(A.out) + row * A.dim, A.dim, A.ovec, R.live);
@@ -1175,10 +1179,11 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join_q(AttnArgs A)
 
 // 32 rows, one per lane & 31 and DP elements long as the products leave them (times f),
 // into memory rows `stride` elements apart: through a tile, so that neighbouring lanes
-// write neighbouring 16 bytes.  Rows from `rows` on are left out.
+// write neighbouring 16 bytes.  Rows from `rows` on are left out; a row that is not `live` is
+// zero.
 template <typename T, int DP>
 __device__ __forceinline__ void store_rows(T *base, int64_t stride, int dim, bool vec, int rows,
-                                           const f32x16_t (&x)[DP / 32], float f, u32x4_t *tile)
+                                           const f32x16_t (&x)[DP / 32], float f, bool live, u32x4_t *tile)
 {
     using TL = Tile<T, DP>;
     const int l = lane_id(), r = l & 31, h = l >> 5;
@@ -1191,15 +1196,22 @@ __device__ __forceinline__ void store_rows(T *base, int64_t stride, int dim, boo
 #pragma unroll
             for (int e = 0; e < 4; e++) v[e] = f * x[d][4 * g + e];
             if (vec) lds_write(lds_address(tile) + 16 * TL::at(r, col / TL::E) + col % TL::E * (int)sizeof(T), Mma<T>::pack4(v));
-            else if (r < rows) store_part(base + r * stride, col, dim, v);
+            else if (r < rows) {
+#pragma unroll
+                for (int e = 0; e < 4; e++) v[e] = live ? v[e] : 0.f;
+                store_part(base + r * stride, col, dim, v);
+            }
         }
     if (!vec) return;
+    const uint32_t alive = (uint32_t)__ballot(live);
     wave_sync();
     constexpr int PER = 64 / TL::CH;                    // rows per store
 #pragma unroll
     for (int j = 0; j < 32 / PER; j++) {
         const int row = j * PER + l / TL::CH, c = (l % TL::CH) ^ swizzle<TL::CH>(row);
-        const u32x4_t v = tile[j * 64 + l];
+        u32x4_t v = tile[j * 64 + l];
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = alive >> row & 1 ? v[e] : 0;
         if (row < rows && c * TL::E < dim) *gp(reinterpret_cast<u32x4_t *>(base + row * stride) + c) = v;
     }
     wave_sync();
@@ -1274,6 +1286,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         }
         return z;
     };
+    // a row without keys (lse = -inf) becomes zeros once it has arrived: its weights of zero
+    // must not meet an infinity or NaN
+    float b_lse = 0.f;
     auto bring = [&](const Stage &z, int to) {
         if (z.i >= stages) return;
         // wavefronts 0 and 1 bring the halves of q, 2 and 3 those of dout
@@ -1283,6 +1298,7 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
         const T *p = w < 2 ? static_cast<const T *>(A.q) + head * A.qh + (int64_t)row * A.qs
                            : static_cast<const T *>(A.dout) + head * A.dh + (int64_t)row * A.ds;
         bring_rows<T, DP, 16>(p, w < 2 ? A.qs : A.ds, A.dim, A.vec, keep, lds[to][w >> 1], half);
+        b_lse = *gp(A.lse + (int64_t)min(row + (lane & 15), q1 - 1) * A.heads + head);
     };
     float n_lse = 0.f, n_delta = 0.f;
     int n_pos = 0;
@@ -1347,13 +1363,16 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     }
     // (an LDS addition without an answer; only this wavefront adds to its own row, in order)
     auto settle = [&](int m, float sum) {
-        sum = wave_sum(sum);
+        sum = wave_sum(live ? sum : 0.f);
         if (lane == 0) __hip_atomic_fetch_add(&acc[w][m], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
     };
 
     for (; now.i < stages; now = next, next = then, then = after(then)) {
         const int cur = (int)(now.i & 1);
         arrived();
+        if (const uint32_t dead = (uint32_t)__ballot(b_lse == -INFINITY) & 0xFFFF)
+            for (int i = lane; i < 16 * TL::CH; i += 64)
+                if (dead >> (i / TL::CH) & 1) lds[cur][w >> 1][(w & 1) * 16 * TL::CH + i] = u32x4_t{0, 0, 0, 0};
         __syncthreads();
         bring(next, cur ^ 1);
         if (w == 0) {
@@ -1456,8 +1475,9 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
     const int64_t at = ((int64_t)(s.base + s.row0 + 32 * w) * A.kv_heads + kvh) * A.dim;
     u32x4_t *mine = lds[w >> 1][w & 1];
     __syncthreads();                  // the last stage's rows are read
-    store_rows<T, DP>(static_cast<T *>(A.dk) + at, (int64_t)A.kv_heads * A.dim, A.dim, A.gvec, rows, dk, A.scale, mine);
-    store_rows<T, DP>(static_cast<T *>(A.dv) + at, (int64_t)A.kv_heads * A.dim, A.dim, A.gvec, rows, dv, 1.f, mine);
+    store_rows<T, DP>(static_cast<T *>(A.dk) + at, (int64_t)A.kv_heads * A.dim, A.dim, A.gvec, rows, dk, A.scale, live,
+                      mine);
+    store_rows<T, DP>(static_cast<T *>(A.dv) + at, (int64_t)A.kv_heads * A.dim, A.dim, A.gvec, rows, dv, 1.f, live, mine);
 }
 
 // dbias[m, head] = sum of the workgroups' parts, in a fixed order (no atomics: the result

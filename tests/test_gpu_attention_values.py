@@ -34,6 +34,36 @@ def test_a_masked_key_brings_no_bias(dtype, entry, heads, kv_heads, q_len):
         assert torch.equal(got[name], want[name]), name
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("junk", [math.nan, math.inf])
+@pytest.mark.parametrize("heads,kv_heads,q_len", [(2, 1, [4, 40, 5]), (16, 16, [1500, 300, 1700])])
+def test_rows_without_keys_have_no_gradient(dtype, junk, heads, kv_heads, q_len):
+    """Whatever arrives as the gradient of an output that no key made."""
+    d, dout = make(dtype, q_len, [20, 200, 70], heads, kv_heads, 32, buckets=5, masked=0.1, seed=28)
+    rows = slice(q_len[0], q_len[0] + q_len[1])
+    d["mask"][20:220] = 0                             # the second sample's
+    d["bias"][4, 1] = -math.inf
+    d["boundaries"][3], d["q_pos"][1] = 5000, 10 ** 6      # the second row, of head 1 alone
+    want = run(d, dout)
+    assert not want["out"][rows].any() and not want["out"][1, 1].any()
+    dout[rows], dout[1, 1] = junk, junk
+    d["q"][rows] = junk
+    got = run(d, dout)
+    assert not got["dq"][rows].any() and not got["dk"][20:220].any() and not got["dv"][20:220].any()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_masked_keys_have_no_gradient(dtype):
+    """Not even from a row whose own gradient is not finite."""
+    d, dout = make(dtype, [4, 40], [90, 200], 2, 1, 32, buckets=5, masked=0.4, seed=29)
+    dout[2], dout[30, 1] = math.nan, math.inf
+    got = run(d, dout)
+    out = d["mask"] == 0
+    assert not got["dk"][out].any() and not got["dv"][out].any()
+
+
 def neighbours(dtype, keys):
     """32 rows that share a block with buckets of their own: row i's keys in bucket i // 4."""
     d, dout = make(dtype, [32], [keys], 1, 1, 32, buckets=8, seed=30)
