@@ -932,7 +932,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
         if (w != 0) return;
     } else {
         if (!R.live || !busy) return;
-        const float f2 = A.splits > 1 ? 1.f : inverse(l);
+        const float f2 = inverse(l);      // (128 rows a workgroup are never split)
 #pragma unroll
         for (int d = 0; d < DP / 32; d++)
 #pragma unroll
@@ -941,12 +941,11 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) v[e] = o[d][4 * g + e] * f2;
-                if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, v);
-                else store_out<T>(A, row, col, v);
+                store_out<T>(A, row, col, v);
             }
     }
     if (h != 0) return;
-    if (A.splits > 1) {
+    if (WM == 1 && A.splits > 1) {
         A.part_ml[2 * at] = m;
         A.part_ml[2 * at + 1] = l;
     } else if (A.lse) {
@@ -1140,12 +1139,11 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) v[i] = A.scale * x[d][4 * g + i];
-                if (A.splits > 1) Mma<float>::store4(A.part + at * DP + col, v);
-                else store_part(dq, col, A.dim, v);
+                store_part(dq, col, A.dim, v);
             }
     }
     if (h != 0) return;
-    if (A.splits > 1) {
+    if (WM == 1 && A.splits > 1) {
         A.part_ml[2 * at] = D;
         A.part_ml[2 * at + 1] = e;
     } else {
@@ -1535,7 +1533,8 @@ AttnPlan attn_plan(const emb_attention *a)
     auto sets = [&](int per) { return std::max(rows / per + busy / 2, busy) * a->kv_heads; };
     p.wm = sets(128) >= 384 && rows / samples > 64 ? 4 : 1;
     p.tiles = seg_tiles(a->n_q, a->samples, group, 32 * p.wm);
-    int64_t s = sets(32 * p.wm) > 0 ? 512 / sets(32 * p.wm) : 1;
+    // (the sets that 128 rows take already leave no place for a second split)
+    int64_t s = p.wm == 1 && sets(32) > 0 ? 512 / sets(32) : 1;
     s = std::min<int64_t>(s, keys / 256);
     p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, kSplitsMax));
     p.key_tiles = seg_tiles(a->n_k, a->samples, 1, 128);
