@@ -1,5 +1,6 @@
 """Gradients of the sequence operators under what training programs do around autograd:
-activation checkpointing, saved-tensor hooks, frozen inputs, captured backward passes."""
+activation checkpointing, saved-tensor hooks, frozen inputs, broadcast gradients, captured
+backward passes."""
 import pytest
 import torch
 import torch.utils.checkpoint
@@ -104,3 +105,72 @@ def test_checkpointing_and_offloading(dtype):
     for call in (lambda *t: torch.utils.checkpoint.checkpoint(block, *t, use_reentrant=False),
                  lambda *t: torch.utils.checkpoint.checkpoint(block, *t, use_reentrant=True), offloaded):
         assert all(torch.equal(a, b) for a, b in zip(gradients(call), want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [([3, 140], [90, 700]), ([1, 2], [9000, 5003])])
+def test_each_gradient_alone(dtype, shape):
+    """Frozen inputs change no bit of the others' gradients: the bias's without the keys' among them."""
+    d, dout = attention.make(dtype, *shape, 4, 2, 64, buckets=9, masked=0.2, seed=34)
+    out, leaves, given = attend(d, dout)
+    want = dict(zip(("q", "k", "v", "bias"), torch.autograd.grad(out, leaves, given)))
+    for name in want:
+        leaf = d[name].detach().clone().requires_grad_()
+        got = torch.autograd.grad(E.cross_attention(**{**d, name: leaf}), leaf, dout)[0]
+        assert torch.equal(got, want[name]), name
+    r, dy, dlast = recurrence.make(dtype, shape[1], 66, masked=0.2, seed=35)
+    outs, leaves, given = scan(r, dy, dlast)
+    want = dict(zip(("x", "gate", "state"), torch.autograd.grad(outs, leaves, given)))
+    for name in want:
+        leaf = r[name].detach().clone().requires_grad_()
+        got = torch.autograd.grad(list(E.gated_recurrence(**{**r, name: leaf})), leaf, [dy, dlast])[0]
+        assert torch.equal(got, want[name]), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_that_are_broadcast(dtype):
+    """A sum's gradient is one number seen from everywhere (strides of zero)."""
+    d, dout = attention.make(dtype, [3, 140], [90, 700], 4, 2, 64, buckets=9, masked=0.2, seed=36)
+    r, dy, dlast = recurrence.make(dtype, [90, 700], 66, masked=0.2, seed=37)
+    for make, one in ((lambda: attend(d, torch.ones_like(dout)), lambda t: t.sum()),
+                      (lambda: attend(d, torch.ones_like(dout)), lambda t: t.sum(2).sum()),
+                      (lambda: scan(r, torch.ones_like(dy), None), lambda t: t.sum()),
+                      (lambda: scan(r, torch.ones_like(dy), None), lambda t: t.sum(0).sum())):
+        outs, leaves, given = make()
+        out = outs[0] if isinstance(outs, list) else outs
+        want = torch.autograd.grad(out, leaves, given[:1])
+        outs, leaves, _ = make()
+        got = torch.autograd.grad(one(outs[0] if isinstance(outs, list) else outs), leaves)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_captured_training_step(dtype):
+    """Forward and backward in one graph, replayed on new values between eager work."""
+    d, dout = attention.make(dtype, [1, 150], [2000, 300], 4, 4, 64, buckets=9, masked=0.2, seed=38)
+    leaves = [d[n].clone().requires_grad_() for n in ("q", "k", "v", "bias")]
+
+    def step():
+        q, k, v, bias = leaves
+        y, last = E.gated_recurrence(k.flatten(1), v.flatten(1), d["k_offsets"], mask=d["mask"])
+        out = E.cross_attention(**{**d, "q": q, "k": y.view(k.shape), "v": v, "bias": bias})
+        return [out, last] + list(torch.autograd.grad([out, last], leaves, [dout, torch.ones_like(last)]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(3):
+        with torch.no_grad():
+            for t in leaves:
+                t.mul_(-1.25)
+        eager = step()
+        for t in captured:
+            t.detach().zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(captured, eager))
