@@ -777,11 +777,11 @@ constexpr float kLag = 8.f;
 // weights stay in registers.  The weights enter their product in T, as the values do: a
 // relative error of up to 2^-8 each, independent ones, where the output's own rounding
 // is as large; their sum l is of the fp32 weights.
-// Serving 122 us (4.7 TB/s of its 576 MB) and lifelong 84 us and 5 us for the join (4.6
+// Serving 122 us (4.7 TB/s of its 576 MB) and lifelong 85 us and 5 us for the join (4.5
 // TB/s of 408 MB), where a large copy has 5.5: the reading bounds them.  Two sequences
-// 216 us, 462 TFLOP/s (without a bias 157): two wavefronts a SIMD alternate between
+// 218 us, 458 TFLOP/s (without a bias 156): two wavefronts a SIMD alternate between
 // products and weights, and the blocks whose pairs fall into several buckets cost the
-// rest.  Many candidates 61 us, 154 TFLOP/s (without a bias 46): a workgroup has 9 steps
+// rest.  Many candidates 62 us, 151 TFLOP/s (without a bias 49): a workgroup has 9 steps
 // between its first loads (four dependent ones) and its join, and these do not overlap.
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_forward(AttnArgs A)
@@ -856,7 +856,7 @@ __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void at
                               b_run);
                 if (u + 1 < SUBS) in_run = run.covers(sub_sat(R.r.lo, walk.pos), sub_sat(R.r.hi, walk.pos));
             }
-            b[u] = keep ? b[u] : 0.f;
+            b[u] = keep ? b[u] : 0.f;         // a bias that only masked keys have
             if (kBiasFirst<T>) products<T, DP>(sc[u], lk, u * 32, qf);
         }
 #pragma unroll
@@ -1001,8 +1001,8 @@ __global__ __launch_bounds__(kAttnThreads) void attn_join(AttnArgs A)
 // in that rounding: taken again from the probabilities in fp32, delta costs one addition
 // a pair.  (Correcting dq for it too, by sum_j p_ij k_j, would be a fourth product.)
 // dS enters its product in T, as q and k do.
-// The walk is the forward's, and so is what bounds it.  Two sequences 261 us, 574 TFLOP/s
-// of its three products (without a bias 202); ranking 50 us (41).
+// The walk is the forward's, and so is what bounds it.  Two sequences 258 us, 580 TFLOP/s
+// of its three products (without a bias 198); ranking 52 us (43).
 template <typename T, int DP, int WM>
 __global__ __launch_bounds__(kAttnThreads, (KeyWalk<T, DP, WM>::kWaves)) void attn_backward_q(AttnArgs A)
 {
@@ -1236,12 +1236,14 @@ __device__ __forceinline__ void distances(const int *qpos, int kpos, int (&x)[16
 // Rows of 256 bytes leave V in LDS: with V in registers too they would need more than
 // 256, and past those the accumulators move back and forth (see KeyWalk::kWaves; two
 // sequences 582 us with V in registers, 506 with it in LDS, when this was chosen).
-// Two sequences 459 us, 435 TFLOP/s of its four products (without a bias 284): products,
-// weights and the bias gradient's sums take turns in two wavefronts a SIMD.  A block in
-// one bucket adds its 16 score gradients to a sum in a register; the sum goes to LDS when
-// the bucket changes (LDS additions per pair instead: 1237 -> 2537 us).  Ranking 87 us
-// (57), 1.7 TB/s of the keys' 146 MB: with 2 or 3 stages a workgroup the time goes to
-// the latency of its first loads and to blocks that span several buckets.
+// Two sequences 470 to 505 us by their positions, 395 to 425 TFLOP/s of its four products
+// (without a bias 284): products, weights and the bias gradient's sums take turns in two
+// wavefronts a SIMD.  A block in one bucket adds its 16 score gradients to a sum in a
+// register; the sum goes to LDS when the bucket changes (LDS additions per pair instead:
+// 1237 -> 2537 us).  Ranking 92 us (59), 1.6 TB/s of the keys' 146 MB: with 2 or 3 stages
+// a workgroup the time goes to the latency of its first loads and to blocks that span
+// several buckets.  Clearing rows without keys costs 1.5 of the 92 us, zeros for masked keys
+// 1.
 template <typename T, int DP>
 __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void attn_backward_k(AttnArgs A)
 {
@@ -1429,7 +1431,8 @@ __global__ __launch_bounds__(kAttnThreads, (DP * sizeof(T) <= 256 ? 2 : 1)) void
                 if (lo != hi) {
                     // each bucket's own terms: what a boundary leaves below it is taken out.  (What
                     // lies below one less what lay below the one before costs three operations a
-                    // pair, not four, but a small sum beside a large one would lose its digits.)
+                    // pair, not four, two sequences 461 us for 483; but a small sum beside a large
+                    // one would lose its digits.)
                     int x[16];
                     distances(qpos[cur], kpos, x);
                     for (int m = lo; m < hi; m++) {

@@ -244,7 +244,7 @@ __device__ __forceinline__ void zero_rows(void *p, const ScanSpan &s, int64_t C,
 // its 423 MB (a large copy: 5.5), in registers for four wavefronts a SIMD (six: spills,
 // 212 us).  An exponential and a reciprocal an element keep the vector units half busy,
 // and samples of unequal length leave the chip emptying at the end.  Cut (two passes) one
-// fp32 sample of 65537 rows and 384 channels takes 45 us and 55 us.
+// fp32 sample of 65537 rows and 384 channels takes 42 us and 54 us.
 template <typename T, int VEC, int W, int PHASE>
 __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs A)
 {
@@ -369,9 +369,9 @@ __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_forward(ScanArgs 
 // again a linear recurrence.  The states h_(t-1) that dgate needs are scanned again
 // from the saved state before each group of kSteps rows: an eighth of the states in
 // fp32 is a quarter of what all of them in bf16 would cost, and exact.
-// 128 samples of 200..2000 rows, 512 channels, bf16: 160 us, 3.4 TB/s of its 540 MB (the
-// forward that saves states 108 us); bounded as the forward is.  Cut, as above: 37 us and
-// 89 us.
+// 128 samples of 200..2000 rows, 512 channels, bf16: 150 to 163 us, 4.4 to 4.8 TB/s of the
+// 688 MB of x, gate, dy, dx and dgate and 34 MB of saved states (the forward that saves them
+// 106 to 111 us); bounded as the forward is.  Cut, as above: 35 us and 84 us.
 template <typename T, int VEC, int W, int PHASE>
 __global__ __launch_bounds__(64 * W, W == 1 ? 1 : 4) void scan_backward(ScanArgs A)
 {

@@ -431,9 +431,9 @@ emb_status emb_table_load(emb_table *table, const int64_t *keys, const int32_t *
  * h / (heads / kv_heads) of the sample's key rows j:
  *   s_ij = scale q_i.k_j + bias[bucket(q_pos_i - k_pos_j), h],  o_i = sum_j softmax_j(s_ij) v_j
  *   bucket(x) = #{m : boundaries[m] <= x}, as for EMB_COL_BUCKET; x saturates to int32.
- * Masked keys take no part, whatever their rows hold.  A query row without any key
- * gives o_i = 0 (and lse_i = -inf).  Finite entries of the bias beyond +-1e5 count as
- * +-1e5; -inf shuts a bucket.
+ * Masked keys take no part, whatever their rows or their bucket's bias hold.  A query row
+ * without any key gives o_i = 0 (and lse_i = -inf), and no gradient, whatever its own
+ * dout holds.  Finite entries of the bias beyond +-1e5 count as +-1e5; -inf shuts a bucket.
  */
 typedef struct emb_attention {   /* host */
     int32_t dtype;               /* EMB_F32 | EMB_BF16: q, k, v, out and their gradients      */
