@@ -32,6 +32,10 @@ __all__ = [
     "emb_recurrence_query", "emb_recurrence_forward", "emb_recurrence_backward",
     "emb_recurrence_step", "AttentionDesc", "RecurrenceDesc", "cross_attention",
     "gated_recurrence", "gated_recurrence_step", "CrossAttention", "GatedRecurrence",
+    "emb_delta_query", "emb_delta_forward", "emb_delta_backward", "emb_delta_step",
+    "emb_norm_query", "emb_norm_forward", "emb_norm_backward", "emb_rotary_turn",
+    "DeltaDesc", "NormDesc", "RotaryRows", "RotaryDesc", "gated_delta", "gated_delta_step",
+    "layer_norm", "rotary", "rotary_frequencies", "GatedDelta", "LayerNorm", "Rotary",
     "HASH", "IDENTITY", "BUCKET", "KEYED", "SUM", "MEAN", "F32", "BF16", "OPT_EMIT", "OPT_SGD",
     "OPT_ADAGRAD", "ROW_DROPPED", "ROW_DEFAULT", "STAT_COUNT",
 ]
@@ -94,6 +98,37 @@ class RecurrenceDesc(C.Structure):
                 ("offsets", C.c_void_p), ("mask", C.c_void_p), ("state", C.c_void_p)]
 
 
+class DeltaDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("samples", C.c_int32), ("key_heads", C.c_int32),
+                ("heads", C.c_int32), ("dk", C.c_int32), ("dv", C.c_int32), ("scale", C.c_float),
+                ("reserved", C.c_int32), ("n", C.c_int64), ("q", C.c_void_p), ("k", C.c_void_p),
+                ("v", C.c_void_p), ("gate", C.c_void_p), ("beta", C.c_void_p),
+                ("q_stride", C.c_int64), ("q_head_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("k_head_stride", C.c_int64), ("v_stride", C.c_int64),
+                ("v_head_stride", C.c_int64), ("gate_stride", C.c_int64),
+                ("beta_stride", C.c_int64), ("offsets", C.c_void_p), ("mask", C.c_void_p),
+                ("state", C.c_void_p)]
+
+
+class NormDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("channels", C.c_int32), ("inner", C.c_int32),
+                ("eps", C.c_float), ("rows", C.c_int64), ("x", C.c_void_p),
+                ("x_stride", C.c_int64), ("x_inner_stride", C.c_int64), ("weight", C.c_void_p),
+                ("bias", C.c_void_p)]
+
+
+class RotaryRows(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("pos", C.c_void_p), ("n", C.c_int64),
+                ("stride", C.c_int64), ("head_stride", C.c_int64), ("heads", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+class RotaryDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("layout", C.c_int32), ("dim", C.c_int32),
+                ("pairs", C.c_int32), ("scale", C.c_float), ("reserved", C.c_int32),
+                ("frequencies", C.c_void_p), ("q", RotaryRows), ("k", RotaryRows)]
+
+
 _lib = None
 _VP, _I32, _I64, _F = C.c_void_p, C.c_int32, C.c_int64, C.c_float
 _SIGS = {
@@ -137,6 +172,17 @@ _SIGS = {
     "emb_recurrence_backward": [C.POINTER(RecurrenceDesc), _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                 C.c_size_t, _VP],
     "emb_recurrence_step": [_I32, _I64, _I32, _VP, _I64, _VP, _I64, _VP, _VP, _VP],
+    "emb_delta_query": [C.POINTER(DeltaDesc), _I32, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t),
+                        C.POINTER(C.c_size_t)],
+    "emb_delta_forward": [C.POINTER(DeltaDesc), _VP, _VP, _VP, _VP, C.c_size_t, _VP],
+    "emb_delta_backward": [C.POINTER(DeltaDesc), _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP, _VP,
+                           _VP, _VP, _VP, C.c_size_t, _VP],
+    "emb_delta_step": [C.POINTER(DeltaDesc), _VP, _VP, _VP],
+    "emb_norm_query": [C.POINTER(NormDesc), C.POINTER(C.c_size_t)],
+    "emb_norm_forward": [C.POINTER(NormDesc), _VP, _VP, _VP],
+    "emb_norm_backward": [C.POINTER(NormDesc), _VP, _VP, _I64, _I64, _VP, _VP, _VP, _VP,
+                          C.c_size_t, _VP],
+    "emb_rotary_turn": [C.POINTER(RotaryDesc), _I32, _VP],
 }
 
 
@@ -396,6 +442,50 @@ def emb_recurrence_backward(desc, saved, dy, dlast, dx, dgate, dstate=None, work
     _check(lib().emb_recurrence_backward(C.byref(desc), _ptr(saved), _ptr(dy), _ptr(dlast),
                                          _ptr(dx), _ptr(dgate), _ptr(dstate), _ptr(workspace),
                                          _bytes(workspace), _stream(stream)))
+
+
+def emb_delta_query(desc, training=True):
+    sb, fb, bb = C.c_size_t(), C.c_size_t(), C.c_size_t()
+    _check(lib().emb_delta_query(C.byref(desc), 1 if training else 0, C.byref(sb), C.byref(fb),
+                                 C.byref(bb)))
+    return sb.value, fb.value, bb.value
+
+
+def emb_delta_forward(desc, o, last, saved=None, workspace=None, stream=None):
+    _check(lib().emb_delta_forward(C.byref(desc), _ptr(o), _ptr(last), _ptr(saved), _ptr(workspace),
+                                   _bytes(workspace), _stream(stream)))
+
+
+def emb_delta_backward(desc, saved, dout, dlast, dq, dk, dv, dgate, dbeta, dstate=None,
+                       workspace=None, stream=None):
+    _check(lib().emb_delta_backward(C.byref(desc), _ptr(saved), _rows_ptr(dout, 3), dout.stride(0),
+                                    dout.stride(1), _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv),
+                                    _ptr(dgate), _ptr(dbeta), _ptr(dstate), _ptr(workspace),
+                                    _bytes(workspace), _stream(stream)))
+
+
+def emb_delta_step(desc, state, o, stream=None):
+    _check(lib().emb_delta_step(C.byref(desc), _ptr(state), _ptr(o), _stream(stream)))
+
+
+def emb_norm_query(desc):
+    bb = C.c_size_t()
+    _check(lib().emb_norm_query(C.byref(desc), C.byref(bb)))
+    return bb.value
+
+
+def emb_norm_forward(desc, y, stats=None, stream=None):
+    _check(lib().emb_norm_forward(C.byref(desc), _ptr(y), _ptr(stats), _stream(stream)))
+
+
+def emb_norm_backward(desc, stats, dy, dx, dweight=None, dbias=None, workspace=None, stream=None):
+    _check(lib().emb_norm_backward(C.byref(desc), _ptr(stats), _rows_ptr(dy, dy.dim()), dy.stride(0),
+                                   dy.stride(1) if dy.dim() == 3 else 0, _ptr(dx), _ptr(dweight),
+                                   _ptr(dbias), _ptr(workspace), _bytes(workspace), _stream(stream)))
+
+
+def emb_rotary_turn(desc, back=False, stream=None):
+    _check(lib().emb_rotary_turn(C.byref(desc), 1 if back else 0, _stream(stream)))
 
 
 def emb_recurrence_step(x, gate, state, y, stream=None):
@@ -674,8 +764,14 @@ _SEQ_DTYPE = {torch.float32: F32, torch.bfloat16: BF16}
 # and these calls can be as short as the kernels they start.
 _ATTENTION = struct.Struct("6if i 2q 3Q 6q 7Q")
 _RECURRENCE = struct.Struct("4i q 2Q 2q 3Q")
+_DELTA = struct.Struct("6if i q 5Q 8q 3Q")
+_NORM = struct.Struct("3if q Q 2q 2Q")
+_ROTARY = struct.Struct("4if i Q 3Q 3q 2i 3Q 3q 2i")
 assert _ATTENTION.size == C.sizeof(AttentionDesc)
 assert _RECURRENCE.size == C.sizeof(RecurrenceDesc)
+assert _DELTA.size == C.sizeof(DeltaDesc)
+assert _NORM.size == C.sizeof(NormDesc)
+assert _ROTARY.size == C.sizeof(RotaryDesc)
 
 
 def _rows_ptr(t, ndim):
@@ -983,3 +1079,295 @@ def gated_recurrence_step(x, gate, state, out=None):
     if given:
         _written(out)
     return out
+
+
+def _delta_desc(q, k, v, gate, beta, offsets, state, mask, scale):
+    qp, kp, vp, gp, bp = (_rows_ptr(q, 3), _rows_ptr(k, 3), _rows_ptr(v, 3), _rows_ptr(gate, 2),
+                          _rows_ptr(beta, 2))
+    dev = _same(q, k, v, gate, beta)
+    n, key_heads, dk = q.shape
+    heads, dv = v.shape[1:]
+    if k.shape != q.shape or v.shape[0] != n or gate.shape != (n, heads) or beta.shape != gate.shape:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}, gate "
+                         f"{tuple(gate.shape)} and beta {tuple(beta.shape)} do not fit")
+    samples = po = ps = 0
+    if offsets is not None:                              # a step has none
+        samples = offsets.numel() - 1
+        po = _offsets_ptr(offsets, "offsets", dev)
+        if state is not None:
+            ps = _want(state, "state", torch.float32, (samples, heads, dk, dv), dev)
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    return DeltaDesc.from_buffer_copy(_DELTA.pack(
+        _SEQ_DTYPE[q.dtype], samples, key_heads, heads, dk, dv,
+        dk ** -0.5 if scale is None else scale, 0, n, qp, kp, vp, gp, bp, sq[0], sq[1], sk[0], sk[1],
+        sv[0], sv[1], gate.stride(0), beta.stride(0), po, _mask_ptr(mask, n, dev), ps))
+
+
+class GatedDelta(torch.autograd.Function):
+    """gated_delta as an autograd node: gradients of q, k, v, gate, beta and the first state."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, gate, beta, state, offsets, mask, scale):
+        desc = _delta_desc(q, k, v, gate, beta, offsets, state, mask, scale)
+        o = v.new_empty(v.shape)
+        last = v.new_empty((desc.samples, desc.heads, desc.dk, desc.dv), dtype=torch.float32)
+        kept, need, ctx.need = emb_delta_query(desc)
+        saved, ws = v.new_empty(max(kept, 1), dtype=torch.uint8), _scratch(need, v)
+        _check(lib().emb_delta_forward(C.byref(desc), o.data_ptr(), last.data_ptr(), saved.data_ptr(),
+                                       _address(ws), need, _stream()))
+        read = q, k, v, gate, beta, state, offsets, mask
+        ctx.save_for_backward(*read, saved)
+        ctx.desc, ctx.scale, ctx.places = desc, scale, _places(read, 5)
+        ctx.set_materialize_grads(False)
+        return o, last
+
+    @staticmethod
+    def backward(ctx, do, dlast):
+        _second_order()
+        _no_tangents(do, dlast)
+        given, in_place = _given_back(ctx.saved_tensors, 5, 8, ctx.places)
+        q, k, v, gate, beta, state, offsets, mask, saved = given
+        if do is None:
+            do = v.new_zeros(v.shape)
+        if do.dtype is not v.dtype:
+            raise TypeError("the output's gradient must have the output's type")
+        if do.stride(-1) != 1 and do.shape[-1] > 1:
+            do = do.contiguous()
+        dlast = None if dlast is None else dlast.contiguous()
+        dq, dk, dv, dgate, dbeta = (x.new_empty(x.shape) for x in (q, k, v, gate, beta))
+        dstate = None
+        if state is not None and ctx.needs_input_grad[5]:
+            dstate = state.new_empty(state.shape)
+        desc = ctx.desc if in_place else _delta_desc(q, k, v, gate, beta, offsets, state, mask, ctx.scale)
+        ws = _scratch(ctx.need, v)
+        _check(lib().emb_delta_backward(
+            C.byref(desc), saved.data_ptr(), do.data_ptr(), do.stride(0), do.stride(1),
+            _address(dlast), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dgate.data_ptr(),
+            dbeta.data_ptr(), _address(dstate), _address(ws), ctx.need, _stream()))
+        return dq, dk, dv, dgate, dbeta, dstate, None, None, None
+
+
+def gated_delta(q, k, v, gate, beta, offsets, state=None, mask=None, scale=None):
+    """The gated delta rule over every sample's rows: a state S [dk, dv] for each head, with
+    a_t = sigmoid(gate_t) and b_t = sigmoid(beta_t),
+
+        u_t = b_t (v_t - a_t S_(t-1)^T k_t),  S_t = a_t S_(t-1) + k_t u_t^T,  o_t = scale S_t^T q_t
+
+    q, k [n, key_heads, dk] (k of at most unit length keeps the state bounded), v [n, heads, dv],
+    gate and beta [n, heads] (all float32 or all bfloat16; heads a multiple of key_heads, dk and
+    dv <= 128; any strides with the last dimension contiguous); offsets: int32 [samples + 1];
+    state: fp32 [samples, heads, dk, dv] before the first rows (None: zero); mask: uint8 or bool
+    [n], 0 keeps the state as it is and gives zero; scale: dk ** -0.5 unless given.  Returns
+    (o [n, heads, dv], last fp32 [samples, heads, dk, dv], the states after the last rows).
+    Differentiable in q, k, v, gate, beta and state; runs on the current stream."""
+    _no_tangents(q, k, v, gate, beta, state)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
+                                    gate.requires_grad or beta.requires_grad or
+                                    (state is not None and state.requires_grad)):
+        return GatedDelta.apply(q, k, v, gate, beta, state, offsets, mask, scale)
+    desc = _delta_desc(q, k, v, gate, beta, offsets, state, mask, scale)
+    o = v.new_empty(v.shape)
+    last = v.new_empty((desc.samples, desc.heads, desc.dk, desc.dv), dtype=torch.float32)
+    need = emb_delta_query(desc, training=False)[1]
+    ws = _scratch(need, v)
+    _check(lib().emb_delta_forward(C.byref(desc), o.data_ptr(), last.data_ptr(), None, _address(ws),
+                                   need, _stream()))
+    return o, last
+
+
+def gated_delta_step(q, k, v, gate, beta, state, scale=None, out=None):
+    """One row of the gated delta rule for each of a batch of states (serving): q, k
+    [rows, key_heads, dk], v [rows, heads, dv], gate and beta [rows, heads], state fp32
+    [rows, heads, dk, dv], updated in place; returns o [rows, heads, dv].  Not differentiable."""
+    _no_tangents(q, k, v, gate, beta, state)
+    desc = _delta_desc(q, k, v, gate, beta, None, None, None, scale)
+    dev = v.get_device()
+    sp = _want(state, "state", torch.float32, (desc.n, desc.heads, desc.dk, desc.dv), dev)
+    given = out is not None
+    if given:
+        op = _want(out, "out", v.dtype, v.shape, dev)
+    else:
+        out = v.new_empty(v.shape)
+        op = out.data_ptr()
+    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, gate, beta, state)):
+        raise ValueError("gated_delta_step has no gradient: use gated_delta")
+    _check(lib().emb_delta_step(C.byref(desc), sp, op, _stream()))
+    _written(state)
+    if given:
+        _written(out)
+    return out
+
+
+def _norm_desc(x, weight, bias, eps):
+    xp = _rows_ptr(x, x.dim())
+    dev = _same(x)
+    channels = x.shape[-1]
+    pw = 0 if weight is None else _want(weight, "weight", torch.float32, (channels,), dev)
+    pb = 0 if bias is None else _want(bias, "bias", torch.float32, (channels,), dev)
+    if x.dim() == 2:
+        rows, inner, outer, between = x.shape[0], 1, x.stride(0), 0
+    elif x.is_contiguous():
+        rows, inner, outer, between = x.shape[0] * x.shape[1], 1, channels, 0
+    else:
+        rows, inner, (outer, between) = x.shape[0] * x.shape[1], max(x.shape[1], 1), x.stride()[:2]
+    return NormDesc.from_buffer_copy(_NORM.pack(_SEQ_DTYPE[x.dtype], channels, inner, eps, rows, xp,
+                                                outer, between, pw, pb))
+
+
+class LayerNorm(torch.autograd.Function):
+    """layer_norm as an autograd node: gradients of x, weight and bias."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps):
+        desc = _norm_desc(x, weight, bias, eps)
+        y = x.new_empty(x.shape)
+        stats = x.new_empty((desc.rows, 2), dtype=torch.float32)
+        _check(lib().emb_norm_forward(C.byref(desc), y.data_ptr(), stats.data_ptr(), _stream()))
+        read = x, weight, bias
+        ctx.save_for_backward(*read, stats)
+        ctx.desc, ctx.eps, ctx.places = desc, eps, _places(read, 1)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        _second_order()
+        _no_tangents(dy)
+        given, in_place = _given_back(ctx.saved_tensors, 1, 3, ctx.places)
+        x, weight, bias, stats = given
+        if dy.dtype is not x.dtype:
+            raise TypeError("the output's gradient must have the output's type")
+        desc = ctx.desc if in_place else _norm_desc(x, weight, bias, ctx.eps)
+        # rows of dy are counted as those of x are
+        if (dy.stride(-1) != 1 and dy.shape[-1] > 1) or (dy.dim() == 3 and desc.inner == 1):
+            dy = dy.contiguous()
+        outer, inner = ((desc.channels, 0) if dy.dim() == 3 and desc.inner == 1 else
+                        (dy.stride(0), dy.stride(1) if dy.dim() == 3 else 0))
+        dx = x.new_empty(x.shape)
+        dweight = weight.new_empty(weight.shape) if weight is not None and ctx.needs_input_grad[1] else None
+        dbias = bias.new_empty(bias.shape) if bias is not None and ctx.needs_input_grad[2] else None
+        need = emb_norm_query(desc) if dweight is not None or dbias is not None else 0
+        ws = _scratch(need, x)
+        _check(lib().emb_norm_backward(C.byref(desc), stats.data_ptr(), dy.data_ptr(), outer, inner,
+                                       dx.data_ptr(), _address(dweight), _address(dbias), _address(ws),
+                                       need, _stream()))
+        return dx, dweight, dbias, None
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """Layer norm over the last dimension: (x - mean) / sqrt(var + eps) * weight + bias.
+
+    x: float32 or bfloat16, [n, channels] or [n, heads, channels] with any strides and a contiguous
+    last dimension (other shapes as contiguous rows), channels <= 16384; weight, bias: fp32
+    [channels], learned, or None.  Statistics are fp32.  Differentiable in x, weight and bias;
+    runs on the current stream."""
+    if x.dim() not in (2, 3):
+        return layer_norm(x.reshape(-1, x.shape[-1]), weight, bias, eps).view(x.shape)
+    _no_tangents(x, weight, bias)
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad) or
+                                    (bias is not None and bias.requires_grad)):
+        return LayerNorm.apply(x, weight, bias, eps)
+    desc = _norm_desc(x, weight, bias, eps)
+    y = x.new_empty(x.shape)
+    _check(lib().emb_norm_forward(C.byref(desc), y.data_ptr(), None, _stream()))
+    return y
+
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _turn(sides, frequencies, layout, scale, back):
+    """Both sides [(x, pos), (x, pos) or (None, None)] turned; returns the new rows."""
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {tuple(_LAYOUTS)}, got {layout!r}")
+    given = [x for x, _ in sides if x is not None]
+    pack, out = [], []
+    for x, _ in sides:
+        if x is not None:
+            _rows_ptr(x, 3)
+    dev = _same(*given)
+    dim = given[0].shape[2]
+    for x, pos in sides:
+        if x is None:
+            out.append(None)
+            pack += [0] * 8
+            continue
+        if x.shape[2] != dim:
+            raise ValueError(f"q and k must have one head size, got {[tuple(t.shape) for t in given]}")
+        y = x.new_empty(x.shape)
+        out.append(y)
+        pack += [x.data_ptr(), y.data_ptr(), _want(pos, "positions", torch.int32, (x.shape[0],), dev),
+                 x.shape[0] if x.shape[1] else 0, x.stride(0), x.stride(1), x.shape[1], 0]
+    pf = _want(frequencies, "frequencies", torch.float64, (frequencies.numel(),), dev)
+    desc = RotaryDesc.from_buffer_copy(_ROTARY.pack(
+        _SEQ_DTYPE[given[0].dtype], _LAYOUTS[layout], dim, frequencies.numel(), scale, 0, pf, *pack))
+    _check(lib().emb_rotary_turn(C.byref(desc), 1 if back else 0, _stream()))
+    return out
+
+
+class Rotary(torch.autograd.Function):
+    """rotary as an autograd node: gradients of q and k, the turn back."""
+
+    @staticmethod
+    def forward(ctx, q, k, q_pos, k_pos, frequencies, layout, scale):
+        ctx.save_for_backward(q_pos, k_pos, frequencies)
+        ctx.how, ctx.dtype = (layout, scale), q.dtype
+        ctx.set_materialize_grads(False)
+        return tuple(_turn(((q, q_pos), (k, k_pos)), frequencies, layout, scale, False))
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        _second_order()
+        _no_tangents(dq, dk)
+        q_pos, k_pos, frequencies = (t if t is None else t.contiguous() for t in ctx.saved_tensors)
+        sides = []
+        for i, (d, pos) in enumerate(((dq, q_pos), (dk, k_pos))):
+            if d is None or not ctx.needs_input_grad[i]:
+                sides.append((None, None))
+                continue
+            if d.dtype is not ctx.dtype:
+                raise TypeError("the output's gradient must have the output's type")
+            sides.append((d if d.stride(-1) == 1 or d.shape[-1] == 1 else d.contiguous(), pos))
+        if all(x is None for x, _ in sides):
+            return (None,) * 7
+        dq, dk = _turn(sides, frequencies, *ctx.how, True)
+        return dq, dk, None, None, None, None, None
+
+
+def rotary(q, k, q_pos, k_pos, frequencies, layout="half", scale=1.0):
+    """Rotary positions: pair j of each head's first 2 * pairs elements turned by
+    pos * frequencies[j] radians and multiplied by scale; the others are copied.
+
+    q [n_q, heads, dim], k [n_k, kv_heads, dim] or None (float32 or bfloat16; dim <= 1024; any
+    strides with the last dimension contiguous); q_pos [n_q], k_pos [n_k]: int32, steps or
+    elapsed time (the angles of far positions are exact); frequencies: fp64 [pairs]
+    (rotary_frequencies makes them).  layout: "half", pairs (j, j + pairs), or "interleaved",
+    pairs (2 j, 2 j + 1).  Returns (q, k) turned.  Differentiable in q and k; runs on the current
+    stream."""
+    _no_tangents(q, k, frequencies)
+    if torch.is_grad_enabled():
+        if frequencies.requires_grad:
+            raise ValueError("rotary has no gradient of the frequencies")
+        if q.requires_grad or (k is not None and k.requires_grad):
+            return Rotary.apply(q, k, q_pos, k_pos, frequencies, layout, scale)
+    return tuple(_turn(((q, q_pos), (k, k_pos)), frequencies, layout, scale, False))
+
+
+def rotary_frequencies(dim, base=10000.0, factor=1.0, trained=None, low=1.0, high=32.0, device="cuda"):
+    """The fp64 frequencies base ** (-2 j / dim), j < dim / 2, for rotary positions over dim
+    elements of a head, slowed for sequences `factor` times as long: all of them by the whole
+    factor, or, where the `trained` length is given, a pair that turns `low` times over it or
+    fewer by the whole factor, one that turns `high` times or more not at all, and between them
+    by a share that grows evenly with the turns."""
+    if dim < 0 or dim % 2:
+        raise ValueError("rotary positions take an even count of elements")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    freq = base ** (-2.0 * torch.arange(dim // 2, dtype=torch.float64) / max(dim, 1))
+    if factor != 1.0:
+        keep = torch.zeros_like(freq)
+        if trained is not None:
+            if not 0 <= low < high:
+                raise ValueError("low must be below high")
+            keep = ((trained * freq / (2 * torch.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        freq = freq * (keep + (1.0 - keep) / factor)
+    return freq.to(device)

@@ -9,7 +9,7 @@ tmp="$out.tmp$$"
 obj="$(mktemp -d)"
 trap 'rm -rf "$obj"' EXIT
 jobs=()
-for src in plan.cpp forward.hip backward.hip table.hip noalloc.hip copy.hip attention.hip recurrence.hip; do
+for src in plan.cpp forward.hip backward.hip table.hip noalloc.hip copy.hip attention.hip recurrence.hip delta.hip norm.hip rotary.hip; do
     hipcc --offload-arch=gfx950 -O3 -std=c++17 -fPIC \
         -Xclang -target-feature -Xclang -packed-fp32-ops \
         -Wall -Wno-unused-function \

@@ -515,6 +515,118 @@ emb_status emb_recurrence_step(int32_t dtype, int64_t rows, int32_t channels, co
                                int64_t x_stride, const void *gate, int64_t gate_stride, float *state,
                                void *y, void *stream);
 
+/*
+ * Gated delta rule over each sample's rows: a recurrence whose state is a matrix S [dk, dv]
+ * for each sample and head, which forgets by a_t = sigmoid(gate_t) and writes the value
+ * v_t at the key k_t in place of what was read there, as far as b_t = sigmoid(beta_t) says:
+ *   u_t = b_t (v_t - a_t S_(t-1)^T k_t),  S_t = a_t S_(t-1) + k_t u_t^T,  o_t = scale S_t^T q_t
+ * from the sample's state (or zero).  Head h reads key head h / (heads / key_heads).  The
+ * state stays bounded for keys of at most unit length.  A masked row keeps the state and
+ * gives o_t = 0, whatever it holds, and has no gradient.
+ */
+typedef struct emb_delta {       /* host */
+    int32_t dtype;               /* EMB_F32 | EMB_BF16: all but the states, and their gradients */
+    int32_t samples;
+    int32_t key_heads, heads;    /* heads: a multiple of key_heads                           */
+    int32_t dk, dv;              /* 1 .. 128                                                 */
+    float scale;
+    int32_t reserved;
+    int64_t n;                   /* rows                                                     */
+    const void *q, *k;           /* [n, key_heads, dk]   elements of a head contiguous; rows  */
+    const void *v;               /* [n, heads, dv]       and heads any stride apart, given in */
+    const void *gate, *beta;     /* [n, heads]           elements (rows at most 2^21)         */
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+    int64_t gate_stride, beta_stride;      /* of rows                                        */
+    const int32_t *offsets;      /* [samples + 1]                                            */
+    const uint8_t *mask;         /* [n], 0 takes a row out; or NULL                           */
+    const float *state;          /* [samples, heads, dk, dv] or NULL (zero)                   */
+} emb_delta;
+
+/* training 0: saved_bytes and backward_bytes are 0.  saved_bytes: of `saved`; the others: of
+ * the workspaces of the forward (with `saved` if training) and of the backward. */
+emb_status emb_delta_query(const emb_delta *d, int32_t training, size_t *saved_bytes /* host */,
+                           size_t *forward_bytes /* host */, size_t *backward_bytes /* host */);
+
+/* o: [n, heads, dv]; last: fp32 [samples, heads, dk, dv], the states after the last rows;
+ * saved: for the backward, 256-byte aligned, or NULL.  All contiguous. */
+emb_status emb_delta_forward(const emb_delta *d, void *o, float *last, void *saved, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* saved: what the forward of the same descriptor left.  dout: as v, with its own strides;
+ * dlast: as last, or NULL (zero).  dq, dk, dv, dgate, dbeta: contiguous, overwritten, the same
+ * bits for the same inputs; dstate: as last, or NULL. */
+emb_status emb_delta_backward(const emb_delta *d, const void *saved, const void *dout, int64_t dout_stride,
+                              int64_t dout_head_stride, const float *dlast, void *dq, void *dk, void *dv,
+                              void *dgate, void *dbeta, float *dstate, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/* One row for each of n states (serving): state fp32 [n, heads, dk, dv] is updated in place,
+ * o [n, heads, dv] gets what is read.  The descriptor's samples, offsets, mask and state are
+ * not read. */
+emb_status emb_delta_step(const emb_delta *d, float *state, void *o, void *stream);
+
+/*
+ * Layer norm of rows x [rows, channels] (a row r lies at (r / inner) x_stride +
+ * (r % inner) x_inner_stride elements, its own elements contiguous):
+ *   xh = (x - mean) r,  r = 1 / sqrt(mean of (x - mean)^2 + eps),  y = xh weight + bias
+ */
+typedef struct emb_norm {        /* host */
+    int32_t dtype;               /* EMB_F32 | EMB_BF16: x, y and their gradients              */
+    int32_t channels;            /* 1 .. 16384                                               */
+    int32_t inner;               /* rows of the inner dimension (1: rows x_stride apart)      */
+    float eps;                   /* >= 0                                                     */
+    int64_t rows;                /* a multiple of inner                                      */
+    const void *x;
+    int64_t x_stride, x_inner_stride;
+    const float *weight, *bias;  /* [channels] or NULL (ones, zeros)                          */
+} emb_norm;
+
+/* backward_bytes: workspace of the backward call (host only). */
+emb_status emb_norm_query(const emb_norm *d, size_t *backward_bytes /* host */);
+
+/* y: [rows, channels] contiguous; stats: fp32 [rows, 2] for the backward (mean and r of each
+ * row), or NULL. */
+emb_status emb_norm_forward(const emb_norm *d, void *y, float *stats, void *stream);
+
+/* dy: rows as x, with its own strides; dx: [rows, channels] contiguous; dweight, dbias: fp32
+ * [channels], or NULL; the same bits for the same inputs.  workspace: 4-byte aligned, not
+ * used where both are NULL. */
+emb_status emb_norm_backward(const emb_norm *d, const float *stats, const void *dy, int64_t dy_stride,
+                             int64_t dy_inner_stride, void *dx, float *dweight, float *dbias,
+                             void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rotary positions of queries and keys: pair j of a head's first 2 pairs elements is turned
+ * by t = pos * frequencies[j] radians,
+ *   (a, b) -> scale (a cos t - b sin t, b cos t + a sin t),
+ * and the other elements are copied.  t is exact to 1e-9 radians for every int32 position.
+ * Frequencies beyond 1e9 in magnitude (and NaN) give NaN.
+ */
+enum { EMB_ROTARY_HALF = 0,          /* pairs (j, j + pairs)   */
+       EMB_ROTARY_INTERLEAVED = 1 }; /* pairs (2 j, 2 j + 1)   */
+
+typedef struct emb_rotary_rows { /* host */
+    const void *x;               /* [n, heads, dim], elements of a head contiguous            */
+    void *y;                     /* the same, contiguous                                     */
+    const int32_t *pos;          /* [n]                                                      */
+    int64_t n, stride, head_stride;        /* of x, in elements; n 0: no rows of this side     */
+    int32_t heads, reserved;     /* heads x dim < 2^16                                       */
+} emb_rotary_rows;
+
+typedef struct emb_rotary {      /* host */
+    int32_t dtype;               /* EMB_F32 | EMB_BF16                                       */
+    int32_t layout;              /* EMB_ROTARY_*                                             */
+    int32_t dim;                 /* 1 .. 1024                                                */
+    int32_t pairs;               /* 2 pairs <= dim                                           */
+    float scale;
+    int32_t reserved;
+    const double *frequencies;   /* [pairs], radians a position                              */
+    emb_rotary_rows q, k;
+} emb_rotary;
+
+/* back: the turn the other way, which is the gradient's. */
+emb_status emb_rotary_turn(const emb_rotary *r, int32_t back, void *stream);
+
 /* Message for the last non-OK status on this host thread. */
 const char *emb_last_error(void);
 
