@@ -44,11 +44,11 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kCut = 32;                 // rows of a chunk
+constexpr int kSpan = 1024;              // rows of a segment of a cut sample
 constexpr int kDeltaDim = 128;           // largest head size
-constexpr uint32_t kOut = 0x80000000u;   // an offset past every buffer: reads zero, writes nothing
 // the scalars of a chunk and head, in floats
 constexpr int kScB = 0, kScBG = 32, kScG = 64, kScW = 96, kScHi = 128, kScLo = 160, kScEnd = 192, kScKept = 193,
               kScalars = 256;
@@ -62,20 +62,22 @@ struct DeltaArgs {
     int32_t n, samples, key_heads, heads, group, dk, dv, slices;
     float scale;
     char *rec;                 // records of (tile, head): N, P, scalars (and N^T, P^T)
-    char *recT;                // records of (tile, key head): K^T (and Q^T)
-    int64_t rec_size, recT_size;
-    void *s0, *u;              // saved for the backward: states [tile, head, dkp, dvp], U [n, heads, dvp]
+    int64_t rec_size;
+    void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
+    int32_t cut;               // samples are cut into segments
+    int32_t moves_back;        // ... whose transposed matrices are wanted too
+    char *moves;               // of (segment, head): what it does to a state, as operands
+    int64_t move_size;
+    float *starts;             // of (segment, head): what it adds, then the state it begins with
     void *o;
     float *last;
     const void *dout;
     int64_t ds, dh;            // strides of dout
-    const void *dop;           // dout as [n, heads, dvp], possibly itself
-    int64_t dps, dph;
     const float *dlast;
     void *e, *z;               // E as s0, Z as u
     void *dq, *dk_, *dv_, *dgate, *dbeta;
     float *dstate;
-    int32_t vec;               // dq and dk rows move in pieces of 4
+    int32_t vec, ovec;         // dq and dk rows move in pieces of 4; o and dv rows in 16 bytes
 };
 
 // parts of the inputs, of what makes the states, and of what makes outputs alone
@@ -151,45 +153,17 @@ __device__ __forceinline__ u32x4_t buf16(__amdgpu_buffer_rsrc_t r, uint32_t at)
 {
     return __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)at, 0, 0));
 }
-__device__ __forceinline__ u32x2_t buf8(__amdgpu_buffer_rsrc_t r, uint32_t at)
-{
-    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0));
-}
 
 template <typename T>
 struct Row;
-// Rows in memory as operands, a row a lane: `at` is the byte offset of the lane's row (kOut for
-// a row that reads as zero); natural(): elements 16 b + 8 h + 0 .. 7, turned(): elements
-// 16 b + 8 (e >> 2) + 4 h + (e & 3), the order of a block's registers.
+// Rows in memory as operands, a row a lane: elements 16 b + 8 h + 0 .. 7 of the row at byte
+// offset `at` (kNowhere: a row that reads as zero).
 template <>
 struct Row<uint16_t> {
     typedef Part<1> Op;
     static __device__ __forceinline__ Op natural(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b)
     {
         return Op{{buf16(r, at + 32 * b + 16 * h)}};
-    }
-    static __device__ __forceinline__ Op turned(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b)
-    {
-        const u32x2_t x = buf8(r, at + 32 * b + 8 * h), y = buf8(r, at + 32 * b + 16 + 8 * h);
-        return Op{{u32x4_t{x[0], x[1], y[0], y[1]}}};
-    }
-    // the same as numbers
-    static __device__ __forceinline__ void floats(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b, float *f)
-    {
-        const Op o = turned(r, at, h, b);
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f[2 * j] = bf16_lo(o.p[0][j]);
-            f[2 * j + 1] = bf16_hi(o.p[0][j]);
-        }
-    }
-    static __device__ __forceinline__ float one(__amdgpu_buffer_rsrc_t r, uint32_t at)
-    {
-        return bf16_lo((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)at, 0, 0));
-    }
-    static __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t at, float v)
-    {
-        __builtin_amdgcn_raw_buffer_store_b16((short)bf16_rne(v), r, (int)at, 0, 0);
     }
     static __device__ __forceinline__ void put4(uint16_t *p, const float *v)
     {
@@ -216,24 +190,6 @@ struct Row<float> {
         read(r, at + 64 * b + 32 * h, at + 64 * b + 32 * h + 16, f);
         return split8<3>(f);
     }
-    static __device__ __forceinline__ void floats(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b, float *f)
-    {
-        read(r, at + 64 * b + 16 * h, at + 64 * b + 32 + 16 * h, f);
-    }
-    static __device__ __forceinline__ Op turned(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b)
-    {
-        float f[8];
-        floats(r, at, h, b, f);
-        return split8<3>(f);
-    }
-    static __device__ __forceinline__ float one(__amdgpu_buffer_rsrc_t r, uint32_t at)
-    {
-        return __int_as_float((int)__builtin_amdgcn_raw_buffer_load_b32(r, (int)at, 0, 0));
-    }
-    static __device__ __forceinline__ void put(__amdgpu_buffer_rsrc_t r, uint32_t at, float v)
-    {
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), r, (int)at, 0, 0);
-    }
     static __device__ __forceinline__ void put4(float *p, const float *v)
     {
         *gp(reinterpret_cast<f32x4_t *>(p)) = f32x4_t{v[0], v[1], v[2], v[3]};
@@ -249,16 +205,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
     return row_buffer(static_cast<const T *>(p) + elements, 0, 0x7FFFFFFF);
 }
 
-// Operands that lie in memory as the lanes take them: 64 x 16 bytes a part.
-template <int N>
-__device__ __forceinline__ Part<N> load_frag(const char *at, int index)
-{
-    Part<N> r;
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        r.p[i] = *gp(reinterpret_cast<const u32x4_t *>(at) + (index * N + i) * 64 + lane_id());
-    return r;
-}
+// Operands in memory as the lanes take them: 64 x 16 bytes a part.
 template <int N>
 __device__ __forceinline__ void store_frag(char *at, int index, const Part<N> &f)
 {
@@ -353,8 +300,8 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     *gp(reinterpret_cast<f32x4_t *>(rec + Rec<T>::sc) + l) = *reinterpret_cast<const f32x4_t *>(sc + 4 * l);
 
     const auto qb = buffer<T>(A.q, row * A.qs + key * A.qh), kb = buffer<T>(A.k, row * A.ks + key * A.kh);
-    const uint32_t qat = keep ? (uint32_t)(c * A.qs * sizeof(T)) : kOut;
-    const uint32_t kat = keep ? (uint32_t)(c * A.ks * sizeof(T)) : kOut;
+    const uint32_t qat = keep ? (uint32_t)(c * A.qs * sizeof(T)) : kNowhere;
+    const uint32_t kat = keep ? (uint32_t)(c * A.ks * sizeof(T)) : kNowhere;
     f32x16_t kk = zero16(), kq = zero16(), qk = zero16();      // a lane's row, the others in registers
 #pragma unroll
     for (int x = 0; x < 2 * KT; x++) {
@@ -426,93 +373,249 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
             store_frag<ST>(rec + Rec<T>::nt, kc, split8<ST>(f));
         }
     }
-    // K^T and Q^T: a lane has one element of every row
-    if (head % A.group) return;
-    char *recT = A.recT + ((int64_t)tile * A.key_heads + key) * A.recT_size;
-#pragma unroll
-    for (int side = 0; side < (TRAIN ? 2 : 1); side++)
-#pragma unroll
-        for (int t = 0; t < KT; t++)
-#pragma unroll
-            for (int kc = 0; kc < 2; kc++) {
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const int i = 16 * kc + 8 * (e >> 2) + (e & 3) + 4 * h;
-                    const uint32_t at = (uint32_t)((i * (side ? A.qs : A.ks) + 32 * t + c) * sizeof(T));
-                    f[e] = Row<T>::one(side ? qb : kb, kept >> i & 1 ? at : kOut);
-                }
-                store_frag<IN>(recT, (side * KT + t) * 2 + kc, split8<IN>(f));
-            }
 }
 
-// ----------------------------------------------------------------- the walks
+// ------------------------------------------------------------ chunks in LDS
 
-// One wavefront's part of a walk: 32 columns of one sample's and head's state.
-struct Walk {
-    int sample, head, key, slice, base, rows;
-    bool any;
+// The rows of a chunk lie in LDS as operands: 1 KB holds 16 bytes of 32 rows, lane l = 32 h + r
+// has row r; bf16: piece x has elements 16 x + 8 h + 0 .. 7, fp32: pieces 2 x and 2 x + 1 have
+// the first and the last four of these.  They arrive there asynchronously.
+template <typename T>
+struct Lds {
+    static constexpr int R = sizeof(T) / 2;              // pieces of 16 elements
+    static constexpr int kRows = 1024 * R;               // bytes of 32 rows x 16 elements
+
+    // 16 x + 8 h + 0 .. 7 of the lane's row
+    static __device__ __forceinline__ typename Row<T>::Op rows(uint32_t at, int x)
+    {
+        const uint32_t mine = at + 16 * lane_id() + x * kRows;
+        if constexpr (R == 1) return typename Row<T>::Op{{lds_read<u32x4_t>(mine)}};
+        else {
+            float f[8];
+            const u32x4_t a = lds_read<u32x4_t>(mine), b = lds_read<u32x4_t>(mine + 1024);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f[j] = __uint_as_float(a[j]);
+                f[4 + j] = __uint_as_float(b[j]);
+            }
+            return split8<3>(f);
+        }
+    }
+    // Where the lane's part of a column begins: element (lane & 31) of 32, of four rows in a row
+    // from row 4 h.  SWAP: lanes 4 .. 7 and 8 .. 11 of 16 change places.
+    template <bool SWAP>
+    static __device__ __forceinline__ uint32_t column()
+    {
+        const int l = lane_id(), h = l >> 5;
+        if constexpr (R == 1) {
+            // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
+            const int q = SWAP ? (l & 1) * 2 + (l >> 1 & 1) : l & 3, r = 4 * h + ((l & 15) >> 2);
+            return (l >> 4 & 1) * 1024 + ((q >> 1) * 32 + r) * 16 + (q & 1) * 8;
+        } else {
+            const int c = l & 31, d = SWAP ? (c & 19) | (c & 4) << 1 | (c & 8) >> 1 : c;
+            return ((d >> 4) * 2 + (d >> 2 & 1)) * 1024 + ((d >> 3 & 1) * 32 + 4 * h) * 16 + (d & 3) * 4;
+        }
+    }
+    // rows r0 + 4 h + 0 .. 3 of column 32 t + lane & 31
+    static __device__ __forceinline__ void four(uint32_t at, uint32_t column, int t, int r0, float *f)
+    {
+        const uint32_t from = at + column + t * 2 * kRows + r0 * 16;
+        if constexpr (R == 1) {
+            const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)(uintptr_t)from);
+#pragma unroll
+            for (int e = 0; e < 4; e++) f[e] = __uint_as_float((uint32_t)(uint16_t)v[e] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) f[e] = lds_read<float>(from + 16 * e);
+        }
+    }
+    // the same of all 32 rows, as a block
+    static __device__ __forceinline__ f32x16_t block(uint32_t at, uint32_t column, int t)
+    {
+        f32x16_t b;
+#pragma unroll
+        for (int g4 = 0; g4 < 4; g4++) {
+            float f[4];
+            four(at, column, t, 8 * g4, f);
+#pragma unroll
+            for (int e = 0; e < 4; e++) b[4 * g4 + e] = f[e];
+        }
+        return b;
+    }
+    // the rows transposed as an operand: rows 16 kc + kk(e, h) of column 32 t + lane & 31
+    static __device__ __forceinline__ typename Row<T>::Op turned(uint32_t at, uint32_t column, int t, int kc)
+    {
+        if constexpr (R == 1) {
+            u32x4_t w;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + column + t * 2 * kRows + (16 * kc + 8 * j) * 16));
+                const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
+                w[2 * j] = u[0];
+                w[2 * j + 1] = u[1];
+            }
+            return typename Row<T>::Op{{w}};
+        } else {
+            float f[8];
+            four(at, column, t, 16 * kc, f);
+            four(at, column, t, 16 * kc + 8, f + 4);
+            return split8<3>(f);
+        }
+    }
+    // elements 32 t + 8 g4 + 4 h + 0 .. 3 of the lane's row
+    static __device__ __forceinline__ void own(uint32_t at, int t, int g4, float *f)
+    {
+        const int l = lane_id(), h = l >> 5;
+        const uint32_t from = at + (2 * t + (g4 >> 1)) * kRows + ((g4 & 1) * 32 + (l & 31)) * 16;
+        if constexpr (R == 1) {
+            const u32x2_t w = lds_read<u32x2_t>(from + 8 * h);
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                f[2 * j] = bf16_lo(w[j]);
+                f[2 * j + 1] = bf16_hi(w[j]);
+            }
+        } else {
+            const u32x4_t w = lds_read<u32x4_t>(from + 1024 * h);
+#pragma unroll
+            for (int j = 0; j < 4; j++) f[j] = __uint_as_float(w[j]);
+        }
+    }
+    // Blocks whose columns lie in lanes, turned into rows by a wavefront's own scratch: fill()
+    // puts rows r0 .. r0 + 3 of the lane's column, row() takes 16 x + 8 h + 0 .. 7 of the lane's
+    // row, as it is stored.
+    static constexpr int kTurn = R == 1 ? 32 * 72 : 33 * 32 * 4;
+    struct Piece {
+        u32x4_t w[R];
+    };
+    static __device__ __forceinline__ void fill(uint32_t scratch, int r0, const float *f)
+    {
+        const int c = lane_id() & 31;
+        if constexpr (R == 1) lds_write(scratch + c * 72 + r0 * 2, u32x2_t{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])});
+        else
+#pragma unroll
+            for (int e = 0; e < 4; e++) lds_write(scratch + ((r0 + e) * 33 + c) * 4, f[e]);
+    }
+    static __device__ __forceinline__ Piece row(uint32_t scratch, int x)
+    {
+        const int l = lane_id(), h = l >> 5;
+        Piece p;
+        if constexpr (R == 1) {
+            const uint32_t mine = scratch + (8 * h + ((l & 15) >> 2)) * 72 + (16 * (l >> 4 & 1) + 4 * (l & 3)) * 2;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(mine + (16 * x + 4 * j) * 72));
+                const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
+                p.w[0][2 * j] = u[0];
+                p.w[0][2 * j + 1] = u[1];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                p.w[e >> 2][e & 3] = lds_read<uint32_t>(scratch + ((l & 31) * 33 + 16 * x + 8 * h + e) * 4);
+        }
+        return p;
+    }
 };
 
-// Blocks of the slices of one state are neighbours on one XCD, whose L2 then holds the
-// operands that they share.
-__device__ __forceinline__ Walk walk_of(const DeltaArgs &A)
+// The pieces of 1 KB that wavefront `wave` of `waves` brings: every waves-th
+__device__ __forceinline__ uint64_t share(int wave, int waves)
 {
-    Walk w;
-    const int64_t x = blockIdx.x & 7, i = blockIdx.x >> 3;
-    const int64_t pair = (i / A.slices) * 8 + x;
-    w.any = pair < (int64_t)A.samples * A.heads;
-    w.slice = (int)(i % A.slices);
-    w.sample = (int)(pair / A.heads);
-    w.head = (int)(pair % A.heads);
-    w.key = w.head / A.group;
-    w.base = w.rows = 0;
-    if (w.any) {
-        w.base = seg_edge(A.off, A.samples, A.n, w.sample + 1);
-        w.rows = max(seg_edge(A.off, A.samples, A.n, w.sample + 2) - w.base, 0);
-    }
-    return w;
+    uint64_t m = 0;
+    for (int i = wave; i < 64; i += waves) m |= 1ull << i;
+    return m;
 }
 
-__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
+// rows of `pieces` x 16 elements into LDS; `at`: the lane's row and half in bytes, or kNowhere
+template <typename T>
+__device__ __forceinline__ void bring_rows(i32x4_t rsrc, uint32_t at, uint32_t to, int pieces, uint64_t mine)
+{
+    for (int x = 0; x < pieces; x++)
+#pragma unroll
+        for (int j = 0; j < Lds<T>::R; j++) {
+            if (mine & 1) load_to_lds(rsrc, to, at, x * 16 * sizeof(T) + j * 16);
+            mine >>= 1;
+            to += 1024;
+        }
+}
+// `pieces` KB as they lie
+__device__ __forceinline__ void bring_flat(i32x4_t rsrc, uint32_t to, int pieces, uint64_t mine)
+{
+    for (int x = 0; x < pieces; x++, mine >>= 1, to += 1024)
+        if (mine & 1) load_to_lds(rsrc, to, 16 * lane_id(), x * 1024);
+}
 
-// a scalar for each of a block's rows
-__device__ __forceinline__ f32x16_t row_scalars(const float *p, int h)
+// the operand of a record in LDS
+template <int N>
+__device__ __forceinline__ Part<N> staged(uint32_t at, int index)
+{
+    Part<N> r;
+#pragma unroll
+    for (int i = 0; i < N; i++) r.p[i] = lds_read<u32x4_t>(at + (index * N + i) * 1024 + 16 * lane_id());
+    return r;
+}
+
+// a scalar for each of a block's rows, of a record in LDS
+__device__ __forceinline__ f32x16_t row_scalars(uint32_t at, int h)
 {
     f32x16_t r;
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++) {
-        const f32x4_t x = *gp(reinterpret_cast<const f32x4_t *>(p + 8 * g4 + 4 * h));
+        const f32x4_t x = lds_read<f32x4_t>(at + 32 * g4 + 16 * h);
 #pragma unroll
         for (int e = 0; e < 4; e++) r[4 * g4 + e] = x[e];
     }
     return r;
 }
 
-// a block of rows [32, 32 columns]: a column a lane, `rows` a bit for each row that is read
-// (or written); the others give zero
-template <typename T>
-__device__ __forceinline__ f32x16_t block_read(__amdgpu_buffer_rsrc_t r, int64_t stride, uint32_t rows, int h,
-                                               uint32_t col)
+// what this wavefront brought has arrived, then what the workgroup did
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
+
+// ----------------------------------------------------------------- the walks
+
+// Rows of one sample and head that a workgroup walks over: whole samples, or, where samples
+// are cut, segments of kSpan rows.
+struct Walk {
+    int head, key, base, rows, tile0;
+    int64_t matrix;          // number of the sample's and head's state
+    int64_t part;            // number of the segment's and head's record (cut samples)
+    bool any, first, last;
+};
+
+__device__ __forceinline__ Walk walk_of(const DeltaArgs &A)
 {
-    f32x16_t x;
-    const uint32_t bits = rows >> (4 * h), at = col + (uint32_t)(4 * h * stride * sizeof(T));
-#pragma unroll
-    for (int i = 0; i < 16; i++)
-        x[i] = Row<T>::one(r, (bits >> kk0(i) & 1) && col != kOut ? at + (uint32_t)(kk0(i) * stride * sizeof(T)) : kOut);
-    return x;
-}
-template <typename T>
-__device__ __forceinline__ void block_write(__amdgpu_buffer_rsrc_t r, int64_t stride, uint32_t rows, int h,
-                                            uint32_t col, const f32x16_t &x)
-{
-    const uint32_t bits = rows >> (4 * h), at = col + (uint32_t)(4 * h * stride * sizeof(T));
-#pragma unroll
-    for (int i = 0; i < 16; i++)
-        Row<T>::put(r, (bits >> kk0(i) & 1) && col != kOut ? at + (uint32_t)(kk0(i) * stride * sizeof(T)) : kOut, x[i]);
+    Walk w{};
+    int sample;
+    const int unit = (int)(blockIdx.x / (uint32_t)A.heads);
+    w.head = (int)(blockIdx.x - (uint32_t)unit * (uint32_t)A.heads);
+    w.key = w.head / A.group;
+    if (A.cut) {
+        const SegTile s = seg_find<kSpan>(A.off, A.n, nullptr, 0, A.samples, 1, unit);
+        w.any = s.row0 < s.rows && s.seg != 0 && s.seg != A.samples + 1;
+        sample = s.seg - 1;
+        w.base = s.base + s.row0;
+        w.rows = min(s.rows - s.row0, kSpan);
+        w.first = s.row0 == 0;
+        w.last = s.row0 + kSpan >= s.rows;
+        w.tile0 = first_tile(s.base, sample) + s.row0 / kCut;
+        w.part = (int64_t)unit * A.heads + w.head;
+    } else {
+        sample = unit;
+        w.any = w.first = w.last = true;
+        w.base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
+        w.rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - w.base, 0);
+        w.tile0 = first_tile(w.base, sample);
+    }
+    w.matrix = (int64_t)sample * A.heads + w.head;
+    return w;
 }
 
-// states [dk, dv] in memory
+// States [dk, dv] in memory.  Register 8 j + i of half h of block t is row 32 t + 16 j + 8 h + i:
+// the rows of K^T are taken in the order (SWAP) that makes it so, and then rows of K and Q are
+// met by the state's registers as they lie in memory.
 template <int KT>
 __device__ __forceinline__ void state_read(f32x16_t (&S)[KT], const float *p, int dk, int dv, int h, int col)
 {
@@ -520,7 +623,7 @@ __device__ __forceinline__ void state_read(f32x16_t (&S)[KT], const float *p, in
     for (int t = 0; t < KT; t++)
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-            const int r = 32 * t + kk0(i) + 4 * h;
+            const int r = 32 * t + 16 * (i >> 3) + 8 * h + (i & 7);
             S[t][i] = p && r < dk && col < dv ? *gp(p + r * dv + col) : 0.f;
         }
 }
@@ -531,158 +634,411 @@ __device__ __forceinline__ void state_write(const f32x16_t (&S)[KT], float *p, i
     for (int t = 0; t < KT; t++)
 #pragma unroll
         for (int i = 0; i < 16; i++) {
-            const int r = 32 * t + kk0(i) + 4 * h;
+            const int r = 32 * t + 16 * (i >> 3) + 8 * h + (i & 7);
             if (r < dk && col < dv) *gp(p + r * dv + col) = S[t][i];
         }
 }
 
-template <typename T, int KT, bool TRAIN>
-__global__ __launch_bounds__(64) void delta_scan(DeltaArgs A)
+// a wavefront's columns of a state as the gradients read them: rows as operands, 1 KB pieces
+// numbered (block of 32 rows, 16 columns)
+// (APART: the scratch has room for every block of rows, else for one).
+template <typename T, int KT, bool APART = true>
+__device__ __forceinline__ void state_keep(const f32x16_t (&S)[KT], uint32_t scratch, char *to, int slices, int slice)
 {
-    constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT;
+    const int h = lane_id() >> 5;
+    constexpr int kStep = APART ? Lds<T>::kTurn : 0, kBlocks = APART ? KT : 1;
+#pragma unroll
+    for (int t0 = 0; t0 < KT; t0 += kBlocks) {
+        wave_sync();
+#pragma unroll
+        for (int t = t0; t < t0 + kBlocks; t++)
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                float f[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++) f[e] = S[t][4 * q + e];
+                Lds<T>::fill(scratch + t * kStep, 16 * (q >> 1) + 8 * h + 4 * (q & 1), f);
+            }
+        wave_sync();
+#pragma unroll
+        for (int t = t0; t < t0 + kBlocks; t++)
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const auto p = Lds<T>::row(scratch + t * kStep, x);
+#pragma unroll
+                for (int j = 0; j < Lds<T>::R; j++)
+                    *gp(reinterpret_cast<u32x4_t *>(to + ((t * slices + slice) * 2 + x) * Lds<T>::kRows + j * 1024) + lane_id()) = p.w[j];
+            }
+    }
+}
+
+// a block of 32 rows x 32 columns as rows
+template <typename T>
+struct Rows32 {
+    typename Lds<T>::Piece p[2];
+
+    __device__ __forceinline__ void take(const f32x16_t &b, uint32_t scratch)
+    {
+        const int h = lane_id() >> 5;
+        wave_sync();
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            float f[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) f[e] = b[4 * q + e];
+            Lds<T>::fill(scratch, 8 * q + 4 * h, f);
+        }
+        wave_sync();
+#pragma unroll
+        for (int x = 0; x < 2; x++) p[x] = Lds<T>::row(scratch, x);
+    }
+    // as operands for the gradients
+    __device__ __forceinline__ void keep(char *to, int slice) const
+    {
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int j = 0; j < Lds<T>::R; j++)
+                *gp(reinterpret_cast<u32x4_t *>(to + (slice * 2 + x) * Lds<T>::kRows + j * 1024) + lane_id()) = p[x].w[j];
+    }
+    // columns 32 slice .. of rows `stride` apart, the first `left` of them
+    __device__ __forceinline__ void write(T *to, int64_t stride, int left, int slice, int dv, bool vec) const
+    {
+        const int l = lane_id(), r = l & 31;
+        if (r >= left) return;
+        constexpr int E = 16 / sizeof(T);                // elements of 16 bytes
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int j = 0; j < Lds<T>::R; j++) {
+                const int c = 32 * slice + 16 * x + 8 * (l >> 5) + j * E;
+                T *at = to + r * stride + c;
+                if (vec) {
+                    if (c < dv) *gp(reinterpret_cast<u32x4_t *>(at)) = p[x].w[j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        const uint32_t w = p[x].w[j][e * sizeof(T) / 4];
+                        if (c + e < dv) {
+                            if constexpr (sizeof(T) == 2) *gp(at + e) = (uint16_t)(e & 1 ? w >> 16 : w);
+                            else *gp(at + e) = __uint_as_float(w);
+                        }
+                    }
+                }
+            }
+    }
+};
+
+// What a walk has of a chunk in LDS.
+template <typename T, int KT>
+struct ScanLds {
+    static constexpr int q = 2 * KT * Lds<T>::kRows, rec = 2 * q, v = rec + Rec<T>::small;
+    // blocks of a wavefront's scratch: fp32 chunks leave room for one
+    static constexpr int blocks(bool train) { return train && sizeof(T) == 2 ? KT : 1; }
+    static __host__ __device__ int size(int slices) { return v + 2 * slices * Lds<T>::kRows; }
+};
+template <typename T, int KT>
+struct BackLds {
+    static constexpr int q = 2 * KT * Lds<T>::kRows, rec = 2 * q, o = rec + Rec<T>::whole - Rec<T>::sc;
+    static __host__ __device__ int size(int slices) { return o + 2 * slices * Lds<T>::kRows; }
+};
+
+// the bits of a chunk's rows that are kept (there, and not masked)
+template <typename T>
+__device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w, int chunk)
+{
+    const int left = min(w.rows - chunk * kCut, kCut);
+    if (chunk < 0 || left <= 0) return 0;
+    const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
+    return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::sc) + kScKept)) & low_bits(left);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t row_at(uint32_t kept, int64_t stride)
+{
+    const int l = lane_id(), r = l & 31;
+    return kept >> r & 1 ? (uint32_t)(r * stride * sizeof(T)) + (l >> 5) * 8 * (uint32_t)sizeof(T) : kNowhere;
+}
+
+template <typename T, int KT>
+__device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to,
+                                           uint64_t mine)
+{
+    typedef ScanLds<T, KT> L;
+    constexpr int R = Lds<T>::R, n = 2 * KT * R, m = Rec<T>::small / 1024;
+    const int64_t row = (int64_t)w.base + chunk * kCut;
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh), row_at<T>(kept, A.ks), to, 2 * KT, mine);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh), row_at<T>(kept, A.qs), to + L::q, 2 * KT,
+                  mine >> n);
+    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size), to + L::rec, m, mine >> 2 * n);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh), row_at<T>(kept, A.vs), to + L::v,
+                  2 * A.slices, mine >> (2 * n + m));
+}
+
+template <typename T, int KT>
+__device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to,
+                                           uint64_t mine)
+{
+    typedef BackLds<T, KT> L;
+    constexpr int R = Lds<T>::R, n = 2 * KT * R, m = (Rec<T>::whole - Rec<T>::sc) / 1024;
+    const int64_t row = (int64_t)w.base + chunk * kCut;
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh), row_at<T>(kept, A.ks), to, 2 * KT, mine);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh), row_at<T>(kept, A.qs), to + L::q, 2 * KT,
+                  mine >> n);
+    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size + Rec<T>::sc), to + L::rec, m,
+               mine >> 2 * n);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh), row_at<T>(kept, A.ds), to + L::o,
+                  2 * A.slices, mine >> (2 * n + m));
+}
+
+// Walks forward.  SUM: a segment's own part alone, what it does to the state as a matrix (a
+// wavefront for every 32 of its columns, behind those of the values) and what it adds.
+template <typename T, int KT, bool TRAIN, bool SUM>
+__global__ __launch_bounds__(SUM ? 512 : 256) void delta_scan(DeltaArgs A)
+{
+    constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT;
+    typedef ScanLds<T, KT> L;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int l = lane_id(), c = l & 31, h = l >> 5;
-    const int col = 32 * w.slice + c, dvp = 32 * A.slices;
-    const uint32_t colat = col < A.dv ? (uint32_t)(col * sizeof(T)) : kOut;
-    const int64_t matrix = ((int64_t)w.sample * A.heads + w.head) * A.dk * A.dv;
+    const int l = lane_id(), h = l >> 5, slice = uniform((int)(threadIdx.x >> 6));
+    const int col = 32 * slice + (l & 31), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const bool values = slice < A.slices;                // or columns of the segment's matrix
+    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * ScanLds<T, KT>::blocks(TRAIN) * Lds<T>::kTurn;
+    const uint64_t mine = share(slice, blockDim.x >> 6);
+    const uint32_t swapped = Lds<T>::template column<true>(), straight = Lds<T>::template column<false>();
+
     f32x16_t S[KT];
-    state_read<KT>(S, A.state ? A.state + matrix : nullptr, A.dk, A.dv, h, col);
-    const int tile0 = first_tile(w.base, w.sample);
-    for (int r0 = 0; r0 < w.rows; r0 += kCut) {
-        const int tile = tile0 + r0 / kCut;
-        const int64_t row = (int64_t)w.base + r0;
-        const int left = min(w.rows - r0, kCut);
-        const char *rec = A.rec + ((int64_t)tile * A.heads + w.head) * A.rec_size;
-        const char *recT = A.recT + ((int64_t)tile * A.key_heads + w.key) * A.recT_size;
-        const float *sc = reinterpret_cast<const float *>(rec + Rec<T>::sc);
-        const uint32_t kept = __float_as_uint(*gp(sc + kScKept)) & low_bits(left);
-        const float end = *gp(sc + kScEnd);
-        const auto qb = buffer<T>(A.q, row * A.qs + w.key * A.qh), kb = buffer<T>(A.k, row * A.ks + w.key * A.kh);
-        const uint32_t qat = kept >> c & 1 ? (uint32_t)(c * A.qs * sizeof(T)) : kOut;
-        const uint32_t kat = kept >> c & 1 ? (uint32_t)(c * A.ks * sizeof(T)) : kOut;
-        const f32x16_t V = block_read<T>(buffer<T>(A.v, row * A.vs + w.head * A.vh), A.vs, kept, h, colat);
-        if (TRAIN) {
-            const auto sb = buffer<T>(A.s0, ((int64_t)tile * A.heads + w.head) * (32 * KT) * dvp);
+    if (SUM) {
 #pragma unroll
-            for (int t = 0; t < KT; t++)
-                block_write<T>(sb, dvp, 0xFFFFFFFFu, h, (uint32_t)((32 * t * dvp + col) * sizeof(T)), S[t]);
-        }
+        for (int t = 0; t < KT; t++)
+#pragma unroll
+            for (int i = 0; i < 16; i++)
+                S[t][i] = !values && 32 * t + 16 * (i >> 3) + 8 * h + (i & 7) == col - 32 * A.slices ? 1.f : 0.f;
+    } else
+        state_read<KT>(S, A.cut ? A.starts + w.part * A.dk * A.dv : A.state ? A.state + w.matrix * A.dk * A.dv : nullptr, A.dk,
+                       A.dv, h, col);
+    uint32_t kept = kept_rows<T>(A, w, 0), next = kept_rows<T>(A, w, 1);
+    if (chunks) scan_bring<T, KT>(A, w, 0, kept, at0, mine);
+    Rows32<T> orows, urows;                              // of the chunk before: stored a step later,
+                                                         // so that no wait for rows waits for them
+    auto leave = [&](int chunk) {
+        const int64_t row = (int64_t)w.base + chunk * kCut;
+        orows.write(static_cast<T *>(A.o) + (row * A.heads + w.head) * A.dv, (int64_t)A.heads * A.dv, min(w.rows - chunk * kCut, kCut),
+                    slice, A.dv, A.ovec);
+        if (TRAIN)
+            urows.keep(static_cast<char *>(A.u) + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices * 2 * Lds<T>::kRows, slice);
+    };
+    for (int i = 0; i < chunks; i++) {
+        const uint32_t at = at0 + (i & 1) * stage;
+        meet();
+        kept = next;
+        if (!SUM && i) leave(i - 1);
+        if (i + 1 < chunks) scan_bring<T, KT>(A, w, i + 1, kept, at0 + (~i & 1) * stage, mine);
+        next = kept_rows<T>(A, w, i + 2);
+        if (TRAIN && !SUM)
+            state_keep<T, KT, (sizeof(T) == 2)>(S, scratch, static_cast<char *>(A.s0) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * 2 * Lds<T>::kRows,
+                              A.slices, slice);
+        const uint32_t sc = at + L::rec + Rec<T>::sc;
         f32x16_t X = zero16(), Y = zero16();
 #pragma unroll
         for (int x = 0; x < 2 * KT; x++) {
             const Part<ST> sp = operand<ST>(S[x / 2], x % 2);
-            mm<ST>(X, Row<T>::turned(kb, kat, h, x), sp);
-            mm<OUT>(Y, Row<T>::turned(qb, qat, h, x), sp);
+            mm<ST>(X, Lds<T>::rows(at, x), sp);
+            if (!SUM) mm<OUT>(Y, Lds<T>::rows(at + L::q, x), sp);
         }
-        const f32x16_t b = row_scalars(sc + kScB, h), bg = row_scalars(sc + kScBG, h), sg = row_scalars(sc + kScG, h),
-                       wt = row_scalars(sc + kScW, h);
-        f32x16_t U = zero16();
+        const f32x16_t b = row_scalars(sc + 4 * kScB, h), bg = row_scalars(sc + 4 * kScBG, h);
+        f32x16_t V = zero16(), U = zero16();
+        if (values) V = Lds<T>::block(at + L::v, straight, slice);
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            X[i] = fmaf(b[i], V[i], -bg[i] * X[i]);
-            Y[i] *= sg[i];
+        for (int r = 0; r < 16; r++) X[r] = fmaf(b[r], V[r], -bg[r] * X[r]);
+#pragma unroll
+        for (int kc = 0; kc < 2; kc++) mm<ST>(U, staged<ST>(at + L::rec + Rec<T>::n, kc), operand<ST>(X, kc));
+        if (!SUM) {
+            const f32x16_t sg = row_scalars(sc + 4 * kScG, h);
+#pragma unroll
+            for (int r = 0; r < 16; r++) Y[r] *= sg[r];
+#pragma unroll
+            for (int kc = 0; kc < 2; kc++) mm<OUT>(Y, staged<OUT>(at + L::rec + Rec<T>::p, kc), operand<OUT>(U, kc));
+            orows.take(Y, scratch);
+            if (TRAIN) urows.take(U, scratch);
         }
+        const f32x16_t wt = row_scalars(sc + 4 * kScW, h);
+        const float end = lds_read<float>(sc + 4 * kScEnd);
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<ST>(U, load_frag<ST>(rec + Rec<T>::n, kc), operand<ST>(X, kc));
-#pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<OUT>(Y, load_frag<OUT>(rec + Rec<T>::p, kc), operand<OUT>(U, kc));
-        block_write<T>(buffer<T>(A.o, (row * A.heads + w.head) * A.dv), (int64_t)A.heads * A.dv, low_bits(left), h,
-                       colat, Y);
-        if (TRAIN)
-            block_write<T>(buffer<T>(A.u, (row * A.heads + w.head) * dvp), (int64_t)A.heads * dvp, low_bits(left), h,
-                           (uint32_t)(col * sizeof(T)), U);
-#pragma unroll
-        for (int i = 0; i < 16; i++) U[i] *= wt[i];
-        Part<ST> up[2];
-#pragma unroll
-        for (int kc = 0; kc < 2; kc++) up[kc] = operand<ST>(U, kc);
+        for (int r = 0; r < 16; r++) U[r] *= wt[r];
+        const Part<ST> u0 = operand<ST>(U, 0), u1 = operand<ST>(U, 1);
 #pragma unroll
         for (int t = 0; t < KT; t++) {
 #pragma unroll
-            for (int i = 0; i < 16; i++) S[t][i] *= end;
-#pragma unroll
-            for (int kc = 0; kc < 2; kc++) mm<ST>(S[t], load_frag<IN>(recT, 2 * t + kc), up[kc]);
+            for (int r = 0; r < 16; r++) S[t][r] *= end;
+            mm<ST>(S[t], Lds<T>::turned(at, swapped, t, 0), u0);
+            mm<ST>(S[t], Lds<T>::turned(at, swapped, t, 1), u1);
         }
     }
-    state_write<KT>(S, A.last + matrix, A.dk, A.dv, h, col);
+    if (SUM) {
+        if (values) state_write<KT>(S, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, h, col);
+        else {
+            // the matrix as first operands (rows as they lie, the columns in pieces) and, for the
+            // backward, transposed
+            char *to = A.moves + w.part * A.move_size;
+            state_keep<float, KT, false>(S, at0 + 2 * stage + slice * Lds<float>::kTurn, to, KT, slice - A.slices);
+            if (A.moves_back)
+#pragma unroll
+                for (int t = 0; t < KT; t++)
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        *gp(reinterpret_cast<f32x4_t *>(to + KT * KT * 4096 + (((slice - A.slices) * KT + t) * 4 + j) * 1024) + l) =
+                            f32x4_t{S[t][4 * j], S[t][4 * j + 1], S[t][4 * j + 2], S[t][4 * j + 3]};
+        }
+        return;
+    }
+    if (chunks) leave(chunks - 1);
+    if (w.last) state_write<KT>(S, A.last + w.matrix * A.dk * A.dv, A.dk, A.dv, h, col);
 }
 
-template <typename T, int KT>
-__global__ __launch_bounds__(64) void delta_back(DeltaArgs A)
+// Walks backward, from the gradient of the last state.
+template <typename T, int KT, bool SUM>
+__global__ __launch_bounds__(256) void delta_back(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST;
+    typedef BackLds<T, KT> L;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int l = lane_id(), c = l & 31, h = l >> 5;
-    const int col = 32 * w.slice + c, dvp = 32 * A.slices;
-    const uint32_t colat = col < A.dv ? (uint32_t)(col * sizeof(T)) : kOut;
-    const int64_t matrix = ((int64_t)w.sample * A.heads + w.head) * A.dk * A.dv;
+    const int l = lane_id(), h = l >> 5, slice = uniform((int)(threadIdx.x >> 6));
+    const int col = 32 * slice + (l & 31), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * ScanLds<T, KT>::blocks(true) * Lds<T>::kTurn;
+    const uint64_t mine = share(slice, blockDim.x >> 6);
+    const uint32_t swapped = Lds<T>::template column<true>(), straight = Lds<T>::template column<false>();
+
     f32x16_t E[KT];
-    state_read<KT>(E, A.dlast ? A.dlast + matrix : nullptr, A.dk, A.dv, h, col);
-    const int tile0 = first_tile(w.base, w.sample);
-    for (int r0 = w.rows > 0 ? (w.rows - 1) / kCut * kCut : -1; r0 >= 0; r0 -= kCut) {
-        const int tile = tile0 + r0 / kCut;
-        const int64_t row = (int64_t)w.base + r0;
-        const int left = min(w.rows - r0, kCut);
-        const char *rec = A.rec + ((int64_t)tile * A.heads + w.head) * A.rec_size;
-        const char *recT = A.recT + ((int64_t)tile * A.key_heads + w.key) * A.recT_size;
-        const float *sc = reinterpret_cast<const float *>(rec + Rec<T>::sc);
-        const uint32_t kept = __float_as_uint(*gp(sc + kScKept)) & low_bits(left);
-        const float end = *gp(sc + kScEnd);
-        const auto kb = buffer<T>(A.k, row * A.ks + w.key * A.kh);
-        const uint32_t kat = kept >> c & 1 ? (uint32_t)(c * A.ks * sizeof(T)) : kOut;
-        f32x16_t D = block_read<T>(buffer<T>(A.dout, row * A.ds + w.head * A.dh), A.ds, kept, h, colat);
-        const auto eb = buffer<T>(A.e, ((int64_t)tile * A.heads + w.head) * (32 * KT) * dvp);
+    state_read<KT>(E, SUM ? nullptr : A.cut ? A.starts + w.part * A.dk * A.dv : A.dlast ? A.dlast + w.matrix * A.dk * A.dv : nullptr,
+                   A.dk, A.dv, h, col);
+    uint32_t kept = kept_rows<T>(A, w, chunks - 1), next = chunks > 1 ? kept_rows<T>(A, w, chunks - 2) : 0;
+    if (chunks) back_bring<T, KT>(A, w, chunks - 1, kept, at0 + (~chunks & 1) * stage, mine);
+    Rows32<T> vrows, zrows;
+    auto leave = [&](int chunk) {
+        const int64_t row = (int64_t)w.base + chunk * kCut;
+        vrows.write(static_cast<T *>(A.dv_) + (row * A.heads + w.head) * A.dv, (int64_t)A.heads * A.dv,
+                    min(w.rows - chunk * kCut, kCut), slice, A.dv, A.ovec);
+        zrows.keep(static_cast<char *>(A.z) + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices * 2 * Lds<T>::kRows, slice);
+    };
+    for (int i = chunks - 1; i >= 0; i--) {
+        const uint32_t at = at0 + (i & 1) * stage;
+        meet();
+        kept = next;
+        if (!SUM && i + 1 < chunks) leave(i + 1);
+        if (i) back_bring<T, KT>(A, w, i - 1, kept, at0 + (~i & 1) * stage, mine);
+        next = i > 1 ? kept_rows<T>(A, w, i - 2) : 0;
+        if (!SUM)
+            state_keep<T, KT, (sizeof(T) == 2)>(E, scratch, static_cast<char *>(A.e) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * 2 * Lds<T>::kRows,
+                              A.slices, slice);
+        const uint32_t sc = at + L::rec, rec = at + L::rec - Rec<T>::sc;
+        f32x16_t X = zero16(), Z = zero16();
 #pragma unroll
-        for (int t = 0; t < KT; t++)
-            block_write<T>(eb, dvp, 0xFFFFFFFFu, h, (uint32_t)((32 * t * dvp + col) * sizeof(T)), E[t]);
-        f32x16_t X = zero16();
+        for (int x = 0; x < 2 * KT; x++) mm<ST>(X, Lds<T>::rows(at, x), operand<ST>(E[x / 2], x % 2));
+        const f32x16_t wt = row_scalars(sc + 4 * kScW, h);
+        f32x16_t D = Lds<T>::block(at + L::o, straight, slice);
 #pragma unroll
-        for (int x = 0; x < 2 * KT; x++) mm<ST>(X, Row<T>::turned(kb, kat, h, x), operand<ST>(E[x / 2], x % 2));
-        const f32x16_t b = row_scalars(sc + kScB, h), bg = row_scalars(sc + kScBG, h), sg = row_scalars(sc + kScG, h),
-                       wt = row_scalars(sc + kScW, h);
+        for (int r = 0; r < 16; r++) X[r] *= wt[r];
 #pragma unroll
-        for (int i = 0; i < 16; i++) X[i] *= wt[i];
+        for (int kc = 0; kc < 2; kc++) mm<ST>(X, staged<ST>(rec + Rec<T>::pt, kc), operand<IN>(D, kc));
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<ST>(X, load_frag<ST>(rec + Rec<T>::pt, kc), operand<IN>(D, kc));
-        f32x16_t Z = zero16();
+        for (int kc = 0; kc < 2; kc++) mm<ST>(Z, staged<ST>(rec + Rec<T>::nt, kc), operand<ST>(X, kc));
+        const f32x16_t b = row_scalars(sc + 4 * kScB, h), bg = row_scalars(sc + 4 * kScBG, h), sg = row_scalars(sc + 4 * kScG, h);
+        const float end = lds_read<float>(sc + 4 * kScEnd);
+        if (!SUM) {
+            zrows.take(Z, scratch);
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<ST>(Z, load_frag<ST>(rec + Rec<T>::nt, kc), operand<ST>(X, kc));
-        block_write<T>(buffer<T>(A.z, (row * A.heads + w.head) * dvp), (int64_t)A.heads * dvp, low_bits(left), h,
-                       (uint32_t)(col * sizeof(T)), Z);
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-            X[i] = b[i] * Z[i];
-            Z[i] *= -bg[i];
-            D[i] *= sg[i];
+            for (int r = 0; r < 16; r++) X[r] = b[r] * Z[r];
+            vrows.take(X, scratch);
         }
-        block_write<T>(buffer<T>(A.dv_, (row * A.heads + w.head) * A.dv), (int64_t)A.heads * A.dv, low_bits(left), h,
-                       colat, X);
-        Part<ST> zp[2], dp[2];
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) {
-            zp[kc] = operand<ST>(Z, kc);
-            dp[kc] = operand<ST>(D, kc);
+        for (int r = 0; r < 16; r++) {
+            Z[r] *= -bg[r];
+            D[r] *= sg[r];
         }
+        const Part<ST> z0 = operand<ST>(Z, 0), z1 = operand<ST>(Z, 1), d0 = operand<ST>(D, 0), d1 = operand<ST>(D, 1);
 #pragma unroll
         for (int t = 0; t < KT; t++) {
 #pragma unroll
-            for (int i = 0; i < 16; i++) E[t][i] *= end;
-#pragma unroll
-            for (int kc = 0; kc < 2; kc++) {
-                mm<ST>(E[t], load_frag<IN>(recT, 2 * t + kc), zp[kc]);
-                mm<ST>(E[t], load_frag<IN>(recT, 2 * (KT + t) + kc), dp[kc]);
-            }
+            for (int r = 0; r < 16; r++) E[t][r] *= end;
+            mm<ST>(E[t], Lds<T>::turned(at, swapped, t, 0), z0);
+            mm<ST>(E[t], Lds<T>::turned(at, swapped, t, 1), z1);
+            mm<ST>(E[t], Lds<T>::turned(at + L::q, swapped, t, 0), d0);
+            mm<ST>(E[t], Lds<T>::turned(at + L::q, swapped, t, 1), d1);
         }
     }
-    if (A.dstate) state_write<KT>(E, A.dstate + matrix, A.dk, A.dv, h, col);
+    if (SUM) {
+        state_write<KT>(E, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, h, col);
+        return;
+    }
+    if (chunks) leave(0);
+    if (w.first && A.dstate) state_write<KT>(E, A.dstate + w.matrix * A.dk * A.dv, A.dk, A.dv, h, col);
+}
+
+// The states at the edges of a cut sample's segments, one after another: S' = move S + added
+// (BACK: from the last, with the move transposed).  A wavefront has 32 columns of a sample's
+// and head's state; the moves arrive in LDS one ahead.  What a segment adds is replaced by the
+// state that it begins with.
+template <int KT, bool BACK>
+__global__ __launch_bounds__(256) void delta_join(DeltaArgs A)
+{
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
+    constexpr int stage = KT * KT * 4096;
+    const int sample = blockIdx.x / (uint32_t)A.heads, head = blockIdx.x - (uint32_t)sample * (uint32_t)A.heads;
+    const int l = lane_id(), h = l >> 5, c = l & 31, slice = uniform((int)(threadIdx.x >> 6)), col = 32 * slice + c;
+    const int base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
+    const int rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - base, 0);
+    const int parts = (rows + kSpan - 1) / kSpan, part0 = base / kSpan + sample + 1;
+    const int64_t matrix = (int64_t)sample * A.heads + head;
+    const uint32_t at0 = lds_address(lds), spot = (h * 32 + ((c & 19) | (c & 4) << 1 | (c & 8) >> 1)) * 16;
+    const uint64_t mine = share(slice, blockDim.x >> 6);
+    const float *from = BACK ? A.dlast : A.state;
+    f32x16_t S[KT], next[KT];
+    state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, h, col);
+    auto number = [&](int j) { return (int64_t)(part0 + (BACK ? parts - 1 - j : j)) * A.heads + head; };
+    auto bring = [&](int j) {
+        bring_flat(row_rsrc(A.moves + number(j) * A.move_size + (BACK ? KT * KT * 4096 : 0)), at0 + (j & 1) * stage, stage / 1024, mine);
+    };
+    if (parts) bring(0);
+    for (int j = 0; j < parts; j++) {
+        float *added = A.starts + number(j) * A.dk * A.dv;
+        meet();
+        if (j + 1 < parts) bring(j + 1);
+        state_read<KT>(next, added, A.dk, A.dv, h, col);
+        state_write<KT>(S, added, A.dk, A.dv, h, col);
+        if (j + 1 == parts) break;
+        const uint32_t at = at0 + (j & 1) * stage + spot;
+        Part<3> sp[2 * KT];
+#pragma unroll
+        for (int x = 0; x < 2 * KT; x++) sp[x] = operand<3>(S[x / 2], x % 2);
+#pragma unroll
+        for (int t = 0; t < KT; t++) {
+#pragma unroll
+            for (int x = 0; x < 2 * KT; x++) {
+                float f[8];
+                const u32x4_t a = lds_read<u32x4_t>(at + (t * 2 * KT + x) * 2048), b = lds_read<u32x4_t>(at + (t * 2 * KT + x) * 2048 + 1024);
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    f[e] = __uint_as_float(a[e]);
+                    f[4 + e] = __uint_as_float(b[e]);
+                }
+                mm<3>(next[t], split8<3>(f), sp[x]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < KT; t++) S[t] = next[t];
+    }
+    if (parts) return;                                   // a sample without rows hands its state on
+    float *to = BACK ? A.dstate : A.last;
+    if (to) state_write<KT>(S, to + matrix * A.dk * A.dv, A.dk, A.dv, h, col);
 }
 
 // ----------------------------------------------------------------- gradients
 
-template <typename T>
-__device__ __forceinline__ float dot_parts(const Part<1> &a, const Part<1> &b)
+__device__ __forceinline__ float parts_dot(const Part<1> &a, const Part<1> &b)
 {
     float s = 0.f;
 #pragma unroll
@@ -690,8 +1046,7 @@ __device__ __forceinline__ float dot_parts(const Part<1> &a, const Part<1> &b)
         s += bf16_lo(a.p[0][j]) * bf16_lo(b.p[0][j]) + bf16_hi(a.p[0][j]) * bf16_hi(b.p[0][j]);
     return s;
 }
-template <typename T>
-__device__ __forceinline__ float dot_parts(const Part<3> &a, const Part<3> &b)
+__device__ __forceinline__ float parts_dot(const Part<3> &a, const Part<3> &b)
 {
     float s = 0.f;
 #pragma unroll
@@ -704,18 +1059,44 @@ __device__ __forceinline__ float dot_parts(const Part<3> &a, const Part<3> &b)
     return s;
 }
 
+// rows kept as operands, from memory
+template <typename T>
+__device__ __forceinline__ typename Row<T>::Op kept_operand(const char *at, int x)
+{
+    const u32x4_t *p = reinterpret_cast<const u32x4_t *>(at + x * Lds<T>::kRows) + lane_id();
+    if constexpr (Lds<T>::R == 1) return typename Row<T>::Op{{*gp(p)}};
+    else {
+        float f[8];
+        const u32x4_t a = *gp(p), b = *gp(p + 64);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            f[j] = __uint_as_float(a[j]);
+            f[4 + j] = __uint_as_float(b[j]);
+        }
+        return split8<3>(f);
+    }
+}
+
+template <typename T, int KT>
+struct GradLds {
+    static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, u = sc + 1024;
+    static __host__ __device__ int size(int slices) { return u + 3 * 2 * slices * Lds<T>::kRows; }
+};
+
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk, all of them the
 // products of rows with rows, the first dgate and dbeta.
 template <typename T, int KT>
 __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT;
+    constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT, R = Lds<T>::R;
+    typedef GradLds<T, KT> L;
+    extern __shared__ __attribute__((aligned(1024))) char lds[];
     __shared__ float red[KT][3][32];
     const int tile = blockIdx.x, key = blockIdx.y;
     const int wave = uniform((int)(threadIdx.x >> 6)), l = lane_id(), c = l & 31, h = l >> 5;
     const SegTile s = seg_find<kCut>(A.off, A.n, nullptr, 0, A.samples, 1, tile);
     if (s.row0 >= s.rows) return;
-    const int left = min(s.rows - s.row0, kCut), dvp = 32 * A.slices;
+    const int left = min(s.rows - s.row0, kCut);
     const int64_t row = (int64_t)s.base + s.row0;
     if (s.seg == 0 || s.seg == A.samples + 1) {          // rows of no sample
         const int g0 = key * A.group;
@@ -736,63 +1117,70 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
     }
     const bool valid = c < left;
     const bool keep = valid && (!A.mask || *gp(A.mask + row + c));
-    const auto qb = buffer<T>(A.q, row * A.qs + key * A.qh), kb = buffer<T>(A.k, row * A.ks + key * A.kh);
-    const uint32_t qat = keep ? (uint32_t)(c * A.qs * sizeof(T)) : kOut;
-    const uint32_t kat = keep ? (uint32_t)(c * A.ks * sizeof(T)) : kOut;
+    const uint32_t kept = (uint32_t)__ballot(keep);
+    const uint32_t at = lds_address(lds);
+    const uint64_t mine = share(wave, KT);
+    const uint32_t columns = Lds<T>::template column<false>();
+    auto bring = [&](int head) {
+        const int64_t number = (int64_t)tile * A.heads + head;
+        const int n = 2 * A.slices;
+        if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size + Rec<T>::sc), at + L::sc, 16 * l, 0);
+        bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * Lds<T>::kRows), at + L::u, n * R, mine);
+        bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * Lds<T>::kRows), at + L::u + n * Lds<T>::kRows, n * R, mine);
+        bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + head * A.dh), row_at<T>(kept, A.ds),
+                      at + L::u + 2 * n * Lds<T>::kRows, n, mine);
+    };
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + key * A.kh), row_at<T>(kept, A.ks), at, 2 * KT, mine);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + key * A.qh), row_at<T>(kept, A.qs), at + L::q, 2 * KT, mine);
+    bring(key * A.group);
+    meet();
     f32x16_t kk = zero16(), kq = zero16(), qk = zero16();
 #pragma unroll
     for (int x = 0; x < 2 * KT; x++) {
-        const auto K = Row<T>::natural(kb, kat, h, x), Q = Row<T>::natural(qb, qat, h, x);
+        const auto K = Lds<T>::rows(at, x), Q = Lds<T>::rows(at + L::q, x);
         mm<IN>(kk, K, K);
         mm<IN>(kq, K, Q);
         mm<IN>(qk, Q, K);
     }
-    float fq[16], fk[16];                                // the row's own elements of this wavefront's columns
-#pragma unroll
-    for (int x = 0; x < 2; x++) {
-        Row<T>::floats(qb, qat, h, 2 * wave + x, fq + 8 * x);
-        Row<T>::floats(kb, kat, h, 2 * wave + x, fk + 8 * x);
-    }
-    const char *recT = A.recT + ((int64_t)tile * A.key_heads + key) * A.recT_size;
     f32x16_t dq = zero16(), dk = zero16();               // transposed: a row a lane
     for (int g = 0; g < A.group; g++) {
         const int head = key * A.group + g;
-        const char *rec = A.rec + ((int64_t)tile * A.heads + head) * A.rec_size;
-        const float *sc = reinterpret_cast<const float *>(rec + Rec<T>::sc);
-        const float b = *gp(sc + kScB + c), bg = *gp(sc + kScBG + c), sg = *gp(sc + kScG + c), wt = *gp(sc + kScW + c),
-                    hi = *gp(sc + kScHi + c), lo = *gp(sc + kScLo + c), end = *gp(sc + kScEnd);
-        const int64_t m0 = (((int64_t)tile * A.heads + head) * (32 * KT) + 32 * wave) * dvp;
-        const auto sb = buffer<T>(A.s0, m0), eb = buffer<T>(A.e, m0);
-        const auto ub = buffer<T>(A.u, (row * A.heads + head) * dvp), zb = buffer<T>(A.z, (row * A.heads + head) * dvp);
-        const auto ob = buffer<T>(A.dop, row * A.dps + head * A.dph);
-        const uint32_t mat = (uint32_t)(c * dvp * sizeof(T));
-        const uint32_t uat = keep ? (uint32_t)((int64_t)c * A.heads * dvp * sizeof(T)) : kOut;
-        const uint32_t oat = keep ? (uint32_t)(c * A.dps * sizeof(T)) : kOut;
+        if (g) {
+            __syncthreads();                             // the head before is read
+            bring(head);
+            meet();
+        }
+        const int64_t number = (int64_t)tile * A.heads + head, n = 2 * A.slices;
+        const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<T>::kRows;
+        const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<T>::kRows;
+        const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * Lds<T>::kRows, oat = zat + n * Lds<T>::kRows;
         f32x16_t t1 = zero16(), t2 = zero16(), t3 = zero16();
         f32x16_t ud = zero16(), du = zero16(), uz = zero16(), zu = zero16();
         float inner = 0.f;
-        for (int x = 0; x < 2 * A.slices; x++) {
-            const auto S = Row<T>::natural(sb, mat, h, x), E = Row<T>::natural(eb, mat, h, x),
-                       U = Row<T>::natural(ub, uat, h, x), Z = Row<T>::natural(zb, uat, h, x),
-                       D = Row<T>::natural(ob, oat, h, x);
-            mm<IN>(t1, S, D);
-            mm<IN>(t2, S, Z);
-            mm<IN>(t3, E, U);
+        for (int x = 0; x < n; x++) {
+            const auto S = kept_operand<T>(S0, x), E = kept_operand<T>(E0, x);
+            const auto U = Lds<T>::rows(uat, x), Z = Lds<T>::rows(zat, x), D = Lds<T>::rows(oat, x);
             mm<IN>(ud, U, D);                            // u_j.dO_i, lane i
             mm<IN>(du, D, U);                            // dO_i.u_j, lane j
             mm<IN>(uz, U, Z);
             mm<IN>(zu, Z, U);
-            inner += dot_parts<T>(S, E);
+            mm<IN>(t1, S, D);
+            mm<IN>(t2, S, Z);
+            mm<IN>(t3, E, U);
+            inner += parts_dot(S, E);
         }
+        const float b = lds_read<float>(sc + 4 * (kScB + c)), bg = lds_read<float>(sc + 4 * (kScBG + c)),
+                    sg = lds_read<float>(sc + 4 * (kScG + c)), wt = lds_read<float>(sc + 4 * (kScW + c)),
+                    hi = lds_read<float>(sc + 4 * (kScHi + c)), lo = lds_read<float>(sc + 4 * (kScLo + c)),
+                    end = lds_read<float>(sc + 4 * kScEnd);
         // lane x: what k_y (or q_y) is taken with, in register y
         f32x16_t forq, fork, fromq;
         float across = 0.f, own = 0.f;                   // row sum of H less column sum; z.u of the row
 #pragma unroll
         for (int g4 = 0; g4 < 4; g4++) {
             const int y0 = 8 * g4 + 4 * h;
-            const f32x4_t yhi = *gp(reinterpret_cast<const f32x4_t *>(sc + kScHi + y0));
-            const f32x4_t ylo = *gp(reinterpret_cast<const f32x4_t *>(sc + kScLo + y0));
-            const f32x4_t yb = *gp(reinterpret_cast<const f32x4_t *>(sc + kScB + y0));
+            const f32x4_t yhi = lds_read<f32x4_t>(sc + 4 * (kScHi + y0)), ylo = lds_read<f32x4_t>(sc + 4 * (kScLo + y0)),
+                          yb = lds_read<f32x4_t>(sc + 4 * (kScB + y0));
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 const int y = y0 + e, r = 4 * g4 + e;
@@ -810,19 +1198,27 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
         }
 #pragma unroll
         for (int kc = 0; kc < 2; kc++) {
-            const Part<IN> kt = load_frag<IN>(recT, 2 * wave + kc), qt = load_frag<IN>(recT, 2 * (KT + wave) + kc);
+            const auto kt = Lds<T>::turned(at, columns, wave, kc), qt = Lds<T>::turned(at + L::q, columns, wave, kc);
             mm<OUT>(dq, kt, operand<OUT>(forq, kc));
             mm<OUT>(dk, kt, operand<OUT>(fork, kc));
             mm<OUT>(dk, qt, operand<OUT>(fromq, kc));
         }
+        // the row's own elements 32 wave + kk(i, h), which meet its sums with the states
         float dots = 0.f, writes = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const float x = sg * t1[i], y = -bg * t2[i], z = wt * t3[i];
-            dq[i] += x;
-            dk[i] += y + z;
-            dots += fmaf(x, fq[i], y * fk[i]);
-            writes = fmaf(z, fk[i], writes);
+        for (int g4 = 0; g4 < 4; g4++) {
+            float fq[4], fk[4];
+            Lds<T>::own(at + L::q, wave, g4, fq);
+            Lds<T>::own(at, wave, g4, fk);
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int i = 4 * g4 + e;
+                const float x = sg * t1[i], y = -bg * t2[i], z = wt * t3[i];
+                dq[i] += x;
+                dk[i] += y + z;
+                dots += fmaf(x, fq[e], y * fk[e]);
+                writes = fmaf(z, fk[e], writes);
+            }
         }
         dots = both(dots);
         writes = both(writes);
@@ -866,10 +1262,9 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
                 Row<T>::put1(static_cast<T *>(A.dbeta) + (row + c) * A.heads + head, db);
             }
         }
-        __syncthreads();
     }
     if (!valid) return;
-    const int64_t at = ((row + c) * A.key_heads + key) * A.dk;
+    const int64_t to = ((row + c) * A.key_heads + key) * A.dk;
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++) {
         const int x0 = 32 * wave + 8 * g4 + 4 * h;
@@ -881,14 +1276,14 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
         }
         if (A.vec) {
             if (x0 < A.dk) {
-                Row<T>::put4(static_cast<T *>(A.dq) + at + x0, a);
-                Row<T>::put4(static_cast<T *>(A.dk_) + at + x0, b);
+                Row<T>::put4(static_cast<T *>(A.dq) + to + x0, a);
+                Row<T>::put4(static_cast<T *>(A.dk_) + to + x0, b);
             }
         } else {
             for (int e = 0; e < 4; e++)
                 if (x0 + e < A.dk) {
-                    Row<T>::put1(static_cast<T *>(A.dq) + at + x0 + e, a[e]);
-                    Row<T>::put1(static_cast<T *>(A.dk_) + at + x0 + e, b[e]);
+                    Row<T>::put1(static_cast<T *>(A.dq) + to + x0 + e, a[e]);
+                    Row<T>::put1(static_cast<T *>(A.dk_) + to + x0 + e, b[e]);
                 }
         }
     }
@@ -1056,33 +1451,48 @@ struct DeltaPlan {
     size_t el;
     int kt, slices;
     int64_t tiles;
-    size_t rec, recT;                        // bytes of a record
-    size_t recs, recTs, states, us;          // bytes of all records, states and U
-    size_t q, k, o;                          // bytes of packed rows, 0 where they are read in place
+    bool cut;
+    size_t rec, move;                        // bytes of a record, of a segment's matrix
+    size_t recs, states, us, moves, starts;  // bytes of all of them
+    size_t q, k, v;                          // bytes of packed rows, 0 where they are read in place
     size_t saved, forward, backward;
 };
 
-DeltaPlan delta_plan(const emb_delta *d, bool train, bool any_layout)
+// Samples are cut into segments where there are too few of them, times the heads, to fill the
+// chip.  A cut walk is walked twice and its segments are joined one after another.
+bool delta_cut(const emb_delta *d)
+{
+    return d->samples && d->n / d->samples >= 2 * kSpan && (int64_t)d->samples * d->heads < 128;
+}
+
+DeltaPlan delta_plan(const emb_delta *d, bool train)
 {
     DeltaPlan p{};
     p.el = d->dtype == EMB_BF16 ? 2 : 4;
     p.kt = (d->dk + 31) / 32;
     p.slices = (d->dv + 31) / 32;
     p.tiles = seg_tiles(d->n, d->samples, 1, kCut);
-    const bool bf = d->dtype == EMB_BF16;
+    p.cut = delta_cut(d);
+    const bool bf = p.el == 2;
     p.rec = train ? (bf ? Rec<uint16_t>::whole : Rec<float>::whole) : (bf ? Rec<uint16_t>::small : Rec<float>::small);
-    p.recT = (size_t)p.kt * (train ? 2 : 1) * 2 * (bf ? 1 : 3) * 1024;
-    p.recs = pad256((size_t)p.tiles * d->heads * p.rec);
-    p.recTs = pad256((size_t)p.tiles * d->key_heads * p.recT);
-    p.states = pad256((size_t)p.tiles * d->heads * p.kt * 32 * p.slices * 32 * p.el);
-    p.us = pad256((size_t)d->n * d->heads * p.slices * 32 * p.el);
-    const size_t packed = pad256((size_t)d->n * d->key_heads * p.kt * 32 * p.el);
-    p.q = any_layout || !rows_ready(d->q, d->q_stride, d->q_head_stride, d->dk, p.el) ? packed : 0;
-    p.k = any_layout || !rows_ready(d->k, d->k_stride, d->k_head_stride, d->dk, p.el) ? packed : 0;
-    p.o = p.us;
-    p.saved = p.recs + p.recTs + p.states + p.us;
-    p.forward = (train ? 0 : p.recs + p.recTs) + p.q + p.k;
-    p.backward = p.states + p.us + p.q + p.k + p.o;
+    p.recs = (size_t)p.tiles * d->heads * p.rec;
+    p.us = (size_t)p.tiles * d->heads * p.slices * 1024 * p.el;
+    p.states = p.us * p.kt;
+    if (p.cut) {
+        const size_t segments = (size_t)seg_tiles(d->n, d->samples, 1, kSpan) * d->heads;
+        p.move = (size_t)p.kt * p.kt * 4096 * (train ? 2 : 1);
+        p.moves = segments * p.move;
+        p.starts = pad256(segments * d->dk * d->dv * 4);
+    }
+    const size_t keys = pad256((size_t)d->n * d->key_heads * p.kt * 32 * p.el);
+    p.q = rows_ready(d->q, d->q_stride, d->q_head_stride, d->dk, p.el) ? 0 : keys;
+    p.k = rows_ready(d->k, d->k_stride, d->k_head_stride, d->dk, p.el) ? 0 : keys;
+    const size_t values = pad256((size_t)d->n * d->heads * p.slices * 32 * p.el);
+    p.v = rows_ready(d->v, d->v_stride, d->v_head_stride, d->dv, p.el) ? 0 : values;
+    p.saved = p.recs + p.states + p.us + p.moves;
+    p.forward = (train ? 0 : p.recs + p.moves) + p.starts + p.q + p.k + p.v;
+    // the tensors that the backward gets may lie otherwise than the forward's did
+    p.backward = p.states + p.us + p.starts + 2 * keys + values;
     return p;
 }
 
@@ -1093,33 +1503,23 @@ emb_status delta_launched()
     return EMB_OK;
 }
 
-template <typename T>
-void delta_pack_rows(const void *x, int64_t xs, int64_t xh, void *y, int64_t n, int heads, int d, int padded, hipStream_t st)
+// rows as the kernels read them: in place, or packed into *ws, which moves on
+void delta_rows(const emb_delta *d, size_t packed, const void *&x, int64_t &xs, int64_t &xh, int heads, int dim, char *&ws,
+                hipStream_t st)
 {
-    const int64_t blocks = (n * heads * padded + 255) / 256;
-    if (blocks)
-        hipLaunchKernelGGL((delta_pack<T>), dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const T *>(x), xs, xh,
-                           static_cast<T *>(y), n, heads, d, padded);
-}
-
-// q and k as the kernels read them: in place, or packed into *ws, which moves on
-template <typename T>
-void delta_rows(const emb_delta *d, const DeltaPlan &p, DeltaArgs &A, char *&ws, hipStream_t st)
-{
-    if (p.q) {
-        delta_pack_rows<T>(d->q, d->q_stride, d->q_head_stride, ws, d->n, d->key_heads, d->dk, 32 * p.kt, st);
-        A.q = ws;
-        A.qh = 32 * p.kt;
-        A.qs = A.qh * d->key_heads;
-        ws += p.q;
-    }
-    if (p.k) {
-        delta_pack_rows<T>(d->k, d->k_stride, d->k_head_stride, ws, d->n, d->key_heads, d->dk, 32 * p.kt, st);
-        A.k = ws;
-        A.kh = 32 * p.kt;
-        A.ks = A.kh * d->key_heads;
-        ws += p.k;
-    }
+    if (!packed) return;
+    const int padded = (dim + 31) / 32 * 32;
+    const int64_t blocks = (d->n * heads * padded + 255) / 256;
+    if (blocks && d->dtype == EMB_BF16)
+        hipLaunchKernelGGL((delta_pack<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const uint16_t *>(x),
+                           xs, xh, reinterpret_cast<uint16_t *>(ws), d->n, heads, dim, padded);
+    else if (blocks)
+        hipLaunchKernelGGL((delta_pack<float>), dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const float *>(x), xs,
+                           xh, reinterpret_cast<float *>(ws), d->n, heads, dim, padded);
+    x = ws;
+    xh = padded;
+    xs = (int64_t)padded * heads;
+    ws += packed;
 }
 
 DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
@@ -1151,71 +1551,82 @@ DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
     A.slices = p.slices;
     A.scale = d->scale;
     A.rec_size = (int64_t)p.rec;
-    A.recT_size = (int64_t)p.recT;
+    A.cut = p.cut;
+    A.move_size = (int64_t)p.move;
     return A;
 }
 
-// records, states and U in the buffer that the forward leaves for the backward
+// records, states, U and the segments' matrices in the buffer that the forward leaves for the backward
 void delta_saved(const DeltaPlan &p, DeltaArgs &A, char *saved)
 {
     A.rec = saved;
-    A.recT = saved + p.recs;
-    A.s0 = saved + p.recs + p.recTs;
-    A.u = saved + p.recs + p.recTs + p.states;
+    A.s0 = saved + p.recs;
+    A.u = saved + p.recs + p.states;
+    A.moves = saved + p.recs + p.states + p.us;
 }
 
-int64_t walk_blocks(const emb_delta *d, const DeltaPlan &p)
+int64_t delta_walks(const emb_delta *d, const DeltaPlan &p)
 {
-    const int64_t pairs = ((int64_t)d->samples * d->heads + 7) / 8 * 8;
-    return pairs * p.slices;
+    return (p.cut ? seg_tiles(d->n, d->samples, 1, kSpan) : d->samples) * d->heads;
 }
 
 emb_status delta_sizes(const emb_delta *d, const DeltaPlan &p)
 {
     // a launch's threads in one dimension are counted in 32 bits
     const int64_t most = (int64_t(1) << 32) - 1, packed = d->n * d->heads * 128;
-    if (p.tiles > most / (64 * 4) || walk_blocks(d, p) > most / 64 || packed > most)
+    if (p.tiles > most / 256 || delta_walks(d, p) > most / 512 || packed > most)
         return fail(EMB_ERR_UNSUPPORTED, "delta rule: too many rows, samples and heads for one launch");
     return EMB_OK;
+}
+
+template <typename F>
+void delta_launch(F kernel, dim3 grid, int threads, size_t lds, const DeltaArgs &A, hipStream_t st)
+{
+    // more LDS than every chip has is asked for by name
+    if (lds > 65536)
+        (void)hipFuncSetAttribute(reinterpret_cast<const void *>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    hipLaunchKernelGGL(kernel, grid, dim3((unsigned)threads), lds, st, A);
 }
 
 template <typename T, int KT>
 void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool train, hipStream_t st)
 {
-    const dim3 all((unsigned)tiles, (unsigned)A.heads), walk((unsigned)walks), block(64);
-    if (train) {
-        hipLaunchKernelGGL((delta_prepare<T, KT, true>), all, block, 0, st, A);
-        if (walks) hipLaunchKernelGGL((delta_scan<T, KT, true>), walk, block, 0, st, A);
-    } else {
-        hipLaunchKernelGGL((delta_prepare<T, KT, false>), all, block, 0, st, A);
-        if (walks) hipLaunchKernelGGL((delta_scan<T, KT, false>), walk, block, 0, st, A);
+    typedef ScanLds<T, KT> L;
+    const dim3 all((unsigned)tiles, (unsigned)A.heads), walk((unsigned)walks);
+    const int stages = 2 * L::size(A.slices);
+    if (train) delta_launch(delta_prepare<T, KT, true>, all, 64, 0, A, st);
+    else delta_launch(delta_prepare<T, KT, false>, all, 64, 0, A, st);
+    if (!walks) return;
+    if (A.cut) {
+        const int waves = A.slices + KT;
+        delta_launch(delta_scan<T, KT, false, true>, walk, 64 * waves, stages + waves * Lds<float>::kTurn, A, st);
+        delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, 2 * KT * KT * 4096, A, st);
     }
+    const size_t lds = stages + A.slices * L::blocks(train) * Lds<T>::kTurn;
+    if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices, lds, A, st);
+    else delta_launch(delta_scan<T, KT, false, false>, walk, 64 * A.slices, lds, A, st);
 }
 
 template <typename T, int KT>
-void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, hipStream_t st)
+void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool, hipStream_t st)
 {
-    if (walks) hipLaunchKernelGGL((delta_back<T, KT>), dim3((unsigned)walks), dim3(64), 0, st, A);
-    hipLaunchKernelGGL((delta_grads<T, KT>), dim3((unsigned)tiles, (unsigned)A.key_heads), dim3(64 * KT), 0, st, A);
+    const dim3 walk((unsigned)walks);
+    const size_t lds = 2 * BackLds<T, KT>::size(A.slices) + A.slices * ScanLds<T, KT>::blocks(true) * Lds<T>::kTurn;
+    if (walks && A.cut) {
+        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices, lds, A, st);
+        delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, 2 * KT * KT * 4096, A, st);
+    }
+    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices, lds, A, st);
+    delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
 }
 
-template <typename T>
-void delta_forward_any(int kt, const DeltaArgs &A, int64_t tiles, int64_t walks, bool train, hipStream_t st)
-{
-    if (kt == 1) delta_forward_launch<T, 1>(A, tiles, walks, train, st);
-    else if (kt == 2) delta_forward_launch<T, 2>(A, tiles, walks, train, st);
-    else if (kt == 3) delta_forward_launch<T, 3>(A, tiles, walks, train, st);
-    else delta_forward_launch<T, 4>(A, tiles, walks, train, st);
-}
+#define EMB_DELTA_SIZES(NAME, T)                             \
+    (p.kt == 1   ? NAME<T, 1>(A, p.tiles, walks, train, st)  \
+     : p.kt == 2 ? NAME<T, 2>(A, p.tiles, walks, train, st)  \
+     : p.kt == 3 ? NAME<T, 3>(A, p.tiles, walks, train, st)  \
+                 : NAME<T, 4>(A, p.tiles, walks, train, st))
 
-template <typename T>
-void delta_backward_any(int kt, const DeltaArgs &A, int64_t tiles, int64_t walks, hipStream_t st)
-{
-    if (kt == 1) delta_backward_launch<T, 1>(A, tiles, walks, st);
-    else if (kt == 2) delta_backward_launch<T, 2>(A, tiles, walks, st);
-    else if (kt == 3) delta_backward_launch<T, 3>(A, tiles, walks, st);
-    else delta_backward_launch<T, 4>(A, tiles, walks, st);
-}
+bool rows16(const void *x, int dim, size_t el) { return dim * el % 16 == 0 && aligned(x, 16); }
 
 }  // namespace
 
@@ -1227,10 +1638,10 @@ extern "C" emb_status emb_delta_query(const emb_delta *d, int32_t training, size
     if (s != EMB_OK) return s;
     if (!saved_bytes || !forward_bytes || !backward_bytes)
         return fail(EMB_ERR_INVALID_ARG, "delta rule: output pointers must be given");
-    *saved_bytes = training ? delta_plan(d, true, false).saved : 0;
-    *forward_bytes = delta_plan(d, training != 0, false).forward;
-    // the tensors that the backward gets may lie otherwise than the forward's did
-    *backward_bytes = training ? delta_plan(d, true, true).backward : 0;
+    const DeltaPlan p = delta_plan(d, training != 0);
+    *saved_bytes = training ? p.saved : 0;
+    *forward_bytes = p.forward;
+    *backward_bytes = training ? p.backward : 0;
     return EMB_OK;
 }
 
@@ -1241,7 +1652,8 @@ extern "C" emb_status emb_delta_forward(const emb_delta *d, void *o, float *last
     emb_status s = delta_check(d);
     if (s == EMB_OK) s = delta_pointers(d);
     if (s != EMB_OK) return s;
-    const DeltaPlan p = delta_plan(d, saved != nullptr, false);
+    const bool train = saved != nullptr;
+    const DeltaPlan p = delta_plan(d, train);
     if ((d->n && !o) || (d->samples && !last) || !aligned(o, p.el) || !aligned(last, 4) || !aligned(saved, 256))
         return fail(EMB_ERR_INVALID_ARG, "delta rule: o and last must be given and aligned, saved to 256 bytes");
     if (workspace_bytes < p.forward || (p.forward && (!workspace || !aligned(workspace, 256))))
@@ -1252,21 +1664,23 @@ extern "C" emb_status emb_delta_forward(const emb_delta *d, void *o, float *last
     DeltaArgs A = delta_args(d, p);
     A.o = o;
     A.last = last;
+    A.ovec = rows16(o, d->dv, p.el);
+    A.moves_back = train;
     char *ws = static_cast<char *>(workspace);
-    if (saved) delta_saved(p, A, static_cast<char *>(saved));
+    if (train) delta_saved(p, A, static_cast<char *>(saved));
     else {
         A.rec = ws;
-        A.recT = ws + p.recs;
-        ws += p.recs + p.recTs;
+        A.moves = ws + p.recs;
+        ws += p.recs + p.moves;
     }
-    const int64_t walks = walk_blocks(d, p);
-    if (d->dtype == EMB_BF16) {
-        delta_rows<uint16_t>(d, p, A, ws, st);
-        delta_forward_any<uint16_t>(p.kt, A, p.tiles, walks, saved != nullptr, st);
-    } else {
-        delta_rows<float>(d, p, A, ws, st);
-        delta_forward_any<float>(p.kt, A, p.tiles, walks, saved != nullptr, st);
-    }
+    A.starts = reinterpret_cast<float *>(ws);
+    ws += p.starts;
+    delta_rows(d, p.q, A.q, A.qs, A.qh, d->key_heads, d->dk, ws, st);
+    delta_rows(d, p.k, A.k, A.ks, A.kh, d->key_heads, d->dk, ws, st);
+    delta_rows(d, p.v, A.v, A.vs, A.vh, d->heads, d->dv, ws, st);
+    const int64_t walks = delta_walks(d, p);
+    if (d->dtype == EMB_BF16) EMB_DELTA_SIZES(delta_forward_launch, uint16_t);
+    else EMB_DELTA_SIZES(delta_forward_launch, float);
     return delta_launched();
 }
 
@@ -1279,7 +1693,8 @@ extern "C" emb_status emb_delta_backward(const emb_delta *d, const void *saved, 
     emb_status s = delta_check(d);
     if (s == EMB_OK) s = delta_pointers(d);
     if (s != EMB_OK) return s;
-    DeltaPlan p = delta_plan(d, true, false);
+    const bool train = true;
+    const DeltaPlan p = delta_plan(d, train);
     if (!saved || !aligned(saved, 256)) return fail(EMB_ERR_INVALID_ARG, "delta rule: saved must be given, 256-byte aligned");
     if (d->n && (!dout || !dq || !dk || !dv || !dgate || !dbeta))
         return fail(EMB_ERR_INVALID_ARG, "delta rule: dout, dq, dk, dv, dgate and dbeta must be given");
@@ -1290,8 +1705,6 @@ extern "C" emb_status emb_delta_backward(const emb_delta *d, const void *saved, 
         return fail(EMB_ERR_INVALID_ARG, "delta rule: buffers must be aligned to their elements");
     if (dout_stride < 0 || dout_head_stride < 0) return fail(EMB_ERR_INVALID_ARG, "delta rule: strides must be >= 0");
     if (d->n > 1 && dout_stride > kDeltaStrideMost) return fail(EMB_ERR_UNSUPPORTED, "delta rule: row strides must be <= 2^21");
-    if (rows_ready(dout, dout_stride, dout_head_stride, d->dv, p.el)) p.o = 0;
-    p.backward = p.states + p.us + p.q + p.k + p.o;
     if (workspace_bytes < p.backward || (p.backward && (!workspace || !aligned(workspace, 256))))
         return fail(EMB_ERR_WORKSPACE, "delta rule: the workspace is smaller than the query returned, or not 256-byte aligned");
     s = delta_sizes(d, p);
@@ -1302,10 +1715,11 @@ extern "C" emb_status emb_delta_backward(const emb_delta *d, const void *saved, 
     char *ws = static_cast<char *>(workspace);
     A.e = ws;
     A.z = ws + p.states;
-    ws += p.states + p.us;
-    A.dout = A.dop = dout;
-    A.ds = A.dps = dout_stride;
-    A.dh = A.dph = dout_head_stride;
+    A.starts = reinterpret_cast<float *>(ws + p.states + p.us);
+    ws += p.states + p.us + p.starts;
+    A.dout = dout;
+    A.ds = dout_stride;
+    A.dh = dout_head_stride;
     A.dlast = dlast;
     A.dq = dq;
     A.dk_ = dk;
@@ -1314,19 +1728,15 @@ extern "C" emb_status emb_delta_backward(const emb_delta *d, const void *saved, 
     A.dbeta = dbeta;
     A.dstate = dstate;
     A.vec = d->dk % 4 == 0 && aligned(dq, 4 * p.el) && aligned(dk, 4 * p.el);
-    const int64_t walks = walk_blocks(d, p);
-    const bool bf = d->dtype == EMB_BF16;
-    if (bf) delta_rows<uint16_t>(d, p, A, ws, st);
-    else delta_rows<float>(d, p, A, ws, st);
-    if (p.o) {
-        if (bf) delta_pack_rows<uint16_t>(dout, dout_stride, dout_head_stride, ws, d->n, d->heads, d->dv, 32 * p.slices, st);
-        else delta_pack_rows<float>(dout, dout_stride, dout_head_stride, ws, d->n, d->heads, d->dv, 32 * p.slices, st);
-        A.dop = ws;
-        A.dph = 32 * p.slices;
-        A.dps = A.dph * d->heads;
-    }
-    if (bf) delta_backward_any<uint16_t>(p.kt, A, p.tiles, walks, st);
-    else delta_backward_any<float>(p.kt, A, p.tiles, walks, st);
+    A.ovec = rows16(dv, d->dv, p.el);
+    delta_rows(d, p.q, A.q, A.qs, A.qh, d->key_heads, d->dk, ws, st);
+    delta_rows(d, p.k, A.k, A.ks, A.kh, d->key_heads, d->dk, ws, st);
+    const size_t values = rows_ready(dout, dout_stride, dout_head_stride, d->dv, p.el)
+                              ? 0 : pad256((size_t)d->n * d->heads * p.slices * 32 * p.el);
+    delta_rows(d, values, A.dout, A.ds, A.dh, d->heads, d->dv, ws, st);
+    const int64_t walks = delta_walks(d, p);
+    if (d->dtype == EMB_BF16) EMB_DELTA_SIZES(delta_backward_launch, uint16_t);
+    else EMB_DELTA_SIZES(delta_backward_launch, float);
     return delta_launched();
 }
 

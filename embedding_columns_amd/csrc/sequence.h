@@ -77,6 +77,59 @@ __device__ __forceinline__ SegTile seg_find(const int32_t *off, int n, const int
     return s;
 }
 
+// ------------------------------------------------------ memory straight into LDS
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t lds_address(const void *p)
+{
+    return (uint32_t)uniform((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p);
+}
+
+// LDS by its address as a number.
+template <typename V>
+__device__ __forceinline__ V lds_read(uint32_t at)
+{
+    return *(__attribute__((address_space(3))) const V *)(uintptr_t)at;
+}
+
+template <typename V>
+__device__ __forceinline__ void lds_write(uint32_t at, V v)
+{
+    *(__attribute__((address_space(3))) V *)(uintptr_t)at = v;
+}
+
+
+// A 16-byte piece per lane from memory straight into 1 KB of LDS at `to`: lane l's
+// piece lands at to + 16 l.  `off` counts bytes from the descriptor's base (plus the
+// uniform `more`); an offset of kNowhere is out of the descriptor's range, reads no
+// memory and lands as zeros.  The load is asynchronous (vmcnt): the compiler does not
+// know of it, so the reader waits itself (arrived) before it reads.  Nor does it look for
+// hazards in here: a scalar operand that a vector instruction wrote (readfirstlane, or a
+// register spilled to lanes) may be read five wait states later, and the move and the
+// s_nop are those five whatever came before.
+constexpr uint32_t kNowhere = 0x80000000u;
+__device__ __forceinline__ void load_to_lds(i32x4_t rsrc, uint32_t to, uint32_t off, uint32_t more)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(off), "s"(rsrc), "s"(more)
+                 : "memory");
+}
+// ... and before the tile it read from is overwritten, its LDS reads have to be done too
+__device__ __forceinline__ void arrived() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ i32x4_t row_rsrc(const void *base)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    i32x4_t r;
+    r[0] = uniform((int)(uint32_t)b);
+    r[1] = uniform((int)(uint32_t)(b >> 32) & 0xFFFF);
+    r[2] = (int)kNowhere;
+    r[3] = kBufFlags;
+    return r;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -271,6 +271,31 @@ def test_long(dtype):
     check(t, call(t))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dk,dv", [(32, 32), (40, 72), (128, 96)])
+def test_few_long_samples(dk, dv, dtype):
+    """A few samples long enough to be walked in segments, which are joined afterwards."""
+    t = make([4300, 0, 3000, 1300], 1, 2, dk, dv, dtype, masked=0.05, seed=17, before=3, behind=2)
+    got = call(t)
+    check(t, got)
+    alone = call(t, train=False)
+    # the same samples among so many that none is cut: both sides' states are off by what a
+    # chunk's sums lose and a memory of some 50 rows passes on
+    many = 64
+    n = t["q"].shape[0]
+    cat = {x: torch.cat([t[x]] * many) for x in ("q", "k", "v", "gate", "beta", "do", "mask", "state", "dlast")}
+    off = torch.cat([t["offsets"].long()[:-1] + i * n for i in range(many)] + [t["offsets"].long()[-1:] + (many - 1) * n])
+    # each copy's last sample ends where the next one's first begins: the rows between are masked
+    nobody = torch.ones(n, dtype=torch.bool, device="cuda")
+    nobody[3:-2] = False
+    cat["mask"][nobody.repeat(many)] = 0
+    whole = call({**cat, "offsets": off.int()})
+    for name, a in {**got, **{x: alone[x] for x in alone}}.items():
+        b = whole[name][:a.shape[0]].double()
+        u = 2 * R.unit(dtype) if a.dtype is BF16 else (2 * (dk + dv) + 400) * R.E32
+        assert ((a.double() - b).norm() <= u * b.norm()).item(), (name, ((a.double() - b).norm() / b.norm()).item())
+
+
 def test_a_captured_step_of_training():
     t = make([100, 40], 2, 2, 64, 64, BF16, seed=15)
     want = call(t)
