@@ -23,11 +23,12 @@
 // Four kernels: delta_prepare (all chunks side by side) makes N, P and the scalars,
 // delta_scan walks the chunks of a sample, delta_back walks them backwards, delta_grads
 // (all chunks side by side) makes the gradients that need both sides' states.  The walks
-// take 32 columns of the state per wavefront, which never meet one another.
+// take 16 columns of the state per wavefront, which never meet one another.
 //
-// All products run on the matrix cores in 32 x 32 blocks (lane & 31 a column, register i of
-// half h = lane >> 5 the row kk(i, h) = 8 (i >> 2) + 4 h + (i & 3)), which is also how the
-// next product takes its second operand if its contraction runs in that order.  The state
+// All products run on the matrix cores, the walks' in blocks of 16 x 16 (lane & 15 a column,
+// register i of quarter g = lane >> 4 row 4 g + i), the others' in 32 x 32 (lane & 31 a column,
+// register i of half h = lane >> 5 row kk(i, h) = 8 (i >> 2) + 4 h + (i & 3)), which is also how
+// the next product takes its second operand if its contraction runs in that order.  The state
 // is fp32.  What enters a product is cut into bf16 parts, the first rounded from the value,
 // the next from what is left of it: inputs in bf16 are one part, fp32 ones three (24 bits);
 // the state and what makes it (N, U, Z, P^T) are three, so that the states that come out
@@ -35,6 +36,7 @@
 // that the gradients read are kept as one.  Products of parts whose bits lie below the last
 // part's are left out.
 #include <string>
+#include <type_traits>
 
 #include "sequence.h"
 
@@ -66,8 +68,8 @@ struct DeltaArgs {
     void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
     int32_t cut;               // samples are cut into segments
     int32_t moves_back;        // ... whose transposed matrices are wanted too
-    char *moves;               // of (segment, head): what it does to a state, as operands
-    int64_t move_size;
+    float *moves;              // of (segment, head): what it does to a state, [dk, dk] padded (and transposed)
+    int64_t move_size;         // in floats
     float *starts;             // of (segment, head): what it adds, then the state it begins with
     void *o;
     float *last;
@@ -129,6 +131,35 @@ __device__ __forceinline__ void mm(f32x16_t &acc, const Part<NA> &a, const Part<
             if (s - i >= 0 && s - i < NB)
                 acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a.p[i]),
                                                               __builtin_bit_cast(bf16x8_t, b.p[s - i]), acc, 0, 0, 0);
+}
+
+template <int ORD, int NA, int NB>
+__device__ __forceinline__ void mm(f32x4_t &acc, const Part<NA> &a, const Part<NB> &b)
+{
+#pragma unroll
+    for (int s = ORD - 1; s >= 0; s--)
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+            if (s - i >= 0 && s - i < NB)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a.p[i]),
+                                                              __builtin_bit_cast(bf16x8_t, b.p[s - i]), acc, 0, 0, 0);
+}
+
+// 32 rows x 16 columns of a walk: t[a][i] of quarter g is row 16 a + 4 g + i
+struct Block {
+    f32x4_t t[2];
+};
+
+__device__ __forceinline__ Block zero_block() { return Block{{{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}}; }
+
+// ... as a second operand, its rows contracted in the order 16 (e >> 2) + 4 g + (e & 3)
+template <int N>
+__device__ __forceinline__ Part<N> operand(const Block &x)
+{
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = x.t[e >> 2][e & 3];
+    return split8<N>(v);
 }
 
 __device__ __forceinline__ f32x16_t zero16()
@@ -302,38 +333,57 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     const auto qb = buffer<T>(A.q, row * A.qs + key * A.qh), kb = buffer<T>(A.k, row * A.ks + key * A.kh);
     const uint32_t qat = keep ? (uint32_t)(c * A.qs * sizeof(T)) : kNowhere;
     const uint32_t kat = keep ? (uint32_t)(c * A.ks * sizeof(T)) : kNowhere;
-    f32x16_t kk = zero16(), kq = zero16(), qk = zero16();      // a lane's row, the others in registers
+    f32x16_t kk = zero16(), kq = zero16();                     // a lane's row, the others in registers
 #pragma unroll
     for (int x = 0; x < 2 * KT; x++) {
         const auto K = Row<T>::natural(kb, kat, h, x), Q = Row<T>::natural(qb, qat, h, x);
         mm<IN>(kk, K, K);
         mm<IN>(kq, K, Q);                                      // k_j.q_i, lane i
-        if (TRAIN) mm<IN>(qk, Q, K);                           // q_i.k_j, lane j
     }
-    // P in rows of i, M into LDS, P^T in rows of j
-    f32x16_t P, PT;
+    // P and M as rows of i, in LDS; from there as first operands, and transposed
+    float m[16];
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++) {
         const int j0 = 8 * g4 + 4 * h;
         const f32x4_t ghi = *reinterpret_cast<const f32x4_t *>(sc + kScHi + j0);
         const f32x4_t glo = *reinterpret_cast<const f32x4_t *>(sc + kScLo + j0);
-        f32x4_t m;
+        f32x4_t p;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
             const int j = j0 + e, r = 4 * g4 + e;
-            // the rows up to the lane's, and (transposed) from the lane's on
             const float d = j <= c ? exp_of(hi - ghi[e], lo - glo[e]) : 0.f;
-            P[r] = j <= c ? A.scale * d * kq[r] : 0.f;
-            m[e] = j < c ? b * d * kk[r] : 0.f;
-            if (TRAIN) PT[r] = j >= c ? A.scale * exp_of(ghi[e] - hi, glo[e] - lo) * qk[r] : 0.f;
+            p[e] = j <= c ? A.scale * d * kq[r] : 0.f;
+            m[r] = j < c ? b * d * kk[r] : 0.f;
         }
-        *reinterpret_cast<f32x4_t *>(lds + c * kPitch + j0) = m;
+        *reinterpret_cast<f32x4_t *>(lds + c * kPitch + j0) = p;
     }
+    auto leave = [&](auto parts, int at, int back) {     // the matrix in LDS into the record
+        constexpr int N = decltype(parts)::value;
+        const int row = l & 15, g = l >> 4;
 #pragma unroll
-    for (int kc = 0; kc < 2; kc++) {
-        store_frag<OUT>(rec + Rec<T>::p, kc, operand<OUT>(P, kc));
-        if (TRAIN) store_frag<ST>(rec + Rec<T>::pt, kc, operand<ST>(PT, kc));
-    }
+        for (int a = 0; a < 2; a++) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const f32x4_t x = *reinterpret_cast<const f32x4_t *>(lds + (16 * a + row) * kPitch + 4 * e + 4 * g);
+#pragma unroll
+                for (int i = 0; i < 4; i++) f[e + i] = x[i];
+            }
+            store_frag<N>(rec + at, a, split8<N>(f));
+            if (TRAIN) {
+#pragma unroll
+                for (int e = 0; e < 8; e++) f[e] = lds[(16 * (e >> 2) + 4 * g + (e & 3)) * kPitch + 16 * a + row];
+                store_frag<ST>(rec + back, a, split8<ST>(f));
+            }
+        }
+    };
+    wave_sync();
+    leave(std::integral_constant<int, OUT>{}, Rec<T>::p, Rec<T>::pt);
+    wave_sync();
+#pragma unroll
+    for (int g4 = 0; g4 < 4; g4++)
+        *reinterpret_cast<f32x4_t *>(lds + c * kPitch + 8 * g4 + 4 * h) =
+            f32x4_t{m[4 * g4], m[4 * g4 + 1], m[4 * g4 + 2], m[4 * g4 + 3]};
     wave_sync();
     // N by forward substitution, a column a lane: n_i = [i = c] - sum over j < i of M_ij n_j
     float nn[32];
@@ -342,10 +392,10 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         float x = i == c ? 1.f : 0.f;
 #pragma unroll
         for (int j4 = 0; j4 < (i + 3) / 4; j4++) {
-            const f32x4_t m = *reinterpret_cast<const f32x4_t *>(lds + i * kPitch + 4 * j4);
+            const f32x4_t mi = *reinterpret_cast<const f32x4_t *>(lds + i * kPitch + 4 * j4);
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                if (4 * j4 + e < i) x = fmaf(-m[e], nn[4 * j4 + e], x);
+                if (4 * j4 + e < i) x = fmaf(-mi[e], nn[4 * j4 + e], x);
         }
         nn[i] = x;
     }
@@ -353,31 +403,12 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 #pragma unroll
     for (int i = 0; i < 16; i++) lds[(16 * h + i) * kPitch + c] = h ? nn[16 + i] : nn[i];
     wave_sync();
-#pragma unroll
-    for (int kc = 0; kc < 2; kc++) {
-        float f[8];
-        const f32x4_t x = *reinterpret_cast<const f32x4_t *>(lds + c * kPitch + 16 * kc + 4 * h);
-        const f32x4_t y = *reinterpret_cast<const f32x4_t *>(lds + c * kPitch + 16 * kc + 8 + 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            f[e] = x[e];
-            f[4 + e] = y[e];
-        }
-        store_frag<ST>(rec + Rec<T>::n, kc, split8<ST>(f));
-        if (TRAIN) {
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int i = 16 * kc + 8 * (e >> 2) + (e & 3);
-                f[e] = h ? nn[i + 4] : nn[i];
-            }
-            store_frag<ST>(rec + Rec<T>::nt, kc, split8<ST>(f));
-        }
-    }
+    leave(std::integral_constant<int, ST>{}, Rec<T>::n, Rec<T>::nt);
 }
 
 // ------------------------------------------------------------ chunks in LDS
 
-// The rows of a chunk lie in LDS as operands: 1 KB holds 16 bytes of 32 rows, lane l = 32 h + r
+// For the gradients the rows of a chunk lie in LDS as operands of 32 rows: 1 KB holds 16 bytes of 32 rows, lane l = 32 h + r
 // has row r; bf16: piece x has elements 16 x + 8 h + 0 .. 7, fp32: pieces 2 x and 2 x + 1 have
 // the first and the last four of these.  They arrive there asynchronously.
 template <typename T>
@@ -402,45 +433,18 @@ struct Lds {
         }
     }
     // Where the lane's part of a column begins: element (lane & 31) of 32, of four rows in a row
-    // from row 4 h.  SWAP: lanes 4 .. 7 and 8 .. 11 of 16 change places.
-    template <bool SWAP>
+    // from row 4 h.
     static __device__ __forceinline__ uint32_t column()
     {
         const int l = lane_id(), h = l >> 5;
         if constexpr (R == 1) {
             // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
-            const int q = SWAP ? (l & 1) * 2 + (l >> 1 & 1) : l & 3, r = 4 * h + ((l & 15) >> 2);
+            const int q = l & 3, r = 4 * h + ((l & 15) >> 2);
             return (l >> 4 & 1) * 1024 + ((q >> 1) * 32 + r) * 16 + (q & 1) * 8;
         } else {
-            const int c = l & 31, d = SWAP ? (c & 19) | (c & 4) << 1 | (c & 8) >> 1 : c;
-            return ((d >> 4) * 2 + (d >> 2 & 1)) * 1024 + ((d >> 3 & 1) * 32 + 4 * h) * 16 + (d & 3) * 4;
+            const int c = l & 31;
+            return ((c >> 4) * 2 + (c >> 2 & 1)) * 1024 + ((c >> 3 & 1) * 32 + 4 * h) * 16 + (c & 3) * 4;
         }
-    }
-    // rows r0 + 4 h + 0 .. 3 of column 32 t + lane & 31
-    static __device__ __forceinline__ void four(uint32_t at, uint32_t column, int t, int r0, float *f)
-    {
-        const uint32_t from = at + column + t * 2 * kRows + r0 * 16;
-        if constexpr (R == 1) {
-            const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)(uintptr_t)from);
-#pragma unroll
-            for (int e = 0; e < 4; e++) f[e] = __uint_as_float((uint32_t)(uint16_t)v[e] << 16);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; e++) f[e] = lds_read<float>(from + 16 * e);
-        }
-    }
-    // the same of all 32 rows, as a block
-    static __device__ __forceinline__ f32x16_t block(uint32_t at, uint32_t column, int t)
-    {
-        f32x16_t b;
-#pragma unroll
-        for (int g4 = 0; g4 < 4; g4++) {
-            float f[4];
-            four(at, column, t, 8 * g4, f);
-#pragma unroll
-            for (int e = 0; e < 4; e++) b[4 * g4 + e] = f[e];
-        }
-        return b;
     }
     // the rows transposed as an operand: rows 16 kc + kk(e, h) of column 32 t + lane & 31
     static __device__ __forceinline__ typename Row<T>::Op turned(uint32_t at, uint32_t column, int t, int kc)
@@ -458,8 +462,9 @@ struct Lds {
             return typename Row<T>::Op{{w}};
         } else {
             float f[8];
-            four(at, column, t, 16 * kc, f);
-            four(at, column, t, 16 * kc + 8, f + 4);
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                f[e] = lds_read<float>(at + column + t * 2 * kRows + (16 * kc + 8 * (e >> 2) + (e & 3)) * 16);
             return split8<3>(f);
         }
     }
@@ -481,69 +486,23 @@ struct Lds {
             for (int j = 0; j < 4; j++) f[j] = __uint_as_float(w[j]);
         }
     }
-    // Blocks whose columns lie in lanes, turned into rows by a wavefront's own scratch: fill()
-    // puts rows r0 .. r0 + 3 of the lane's column, row() takes 16 x + 8 h + 0 .. 7 of the lane's
-    // row, as it is stored.
-    static constexpr int kTurn = R == 1 ? 32 * 72 : 33 * 32 * 4;
-    struct Piece {
-        u32x4_t w[R];
-    };
-    static __device__ __forceinline__ void fill(uint32_t scratch, int r0, const float *f)
-    {
-        const int c = lane_id() & 31;
-        if constexpr (R == 1) lds_write(scratch + c * 72 + r0 * 2, u32x2_t{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])});
-        else
-#pragma unroll
-            for (int e = 0; e < 4; e++) lds_write(scratch + ((r0 + e) * 33 + c) * 4, f[e]);
-    }
-    static __device__ __forceinline__ Piece row(uint32_t scratch, int x)
-    {
-        const int l = lane_id(), h = l >> 5;
-        Piece p;
-        if constexpr (R == 1) {
-            const uint32_t mine = scratch + (8 * h + ((l & 15) >> 2)) * 72 + (16 * (l >> 4 & 1) + 4 * (l & 3)) * 2;
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(mine + (16 * x + 4 * j) * 72));
-                const u32x2_t u = __builtin_bit_cast(u32x2_t, v);
-                p.w[0][2 * j] = u[0];
-                p.w[0][2 * j + 1] = u[1];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                p.w[e >> 2][e & 3] = lds_read<uint32_t>(scratch + ((l & 31) * 33 + 16 * x + 8 * h + e) * 4);
-        }
-        return p;
-    }
 };
 
-// The pieces of 1 KB that wavefront `wave` of `waves` brings: every waves-th
-__device__ __forceinline__ uint64_t share(int wave, int waves)
-{
-    uint64_t m = 0;
-    for (int i = wave; i < 64; i += waves) m |= 1ull << i;
-    return m;
-}
-
-// rows of `pieces` x 16 elements into LDS; `at`: the lane's row and half in bytes, or kNowhere
+// Wavefront `wave` of `waves` brings every waves-th piece of 1 KB: rows of `pieces` KB (`at`: the
+// lane's row and half in bytes, or kNowhere) into operands, ...
 template <typename T>
-__device__ __forceinline__ void bring_rows(i32x4_t rsrc, uint32_t at, uint32_t to, int pieces, uint64_t mine)
+__device__ __forceinline__ void bring_rows(i32x4_t rsrc, uint32_t at, uint32_t to, int pieces, int wave, int waves)
 {
-    for (int x = 0; x < pieces; x++)
-#pragma unroll
-        for (int j = 0; j < Lds<T>::R; j++) {
-            if (mine & 1) load_to_lds(rsrc, to, at, x * 16 * sizeof(T) + j * 16);
-            mine >>= 1;
-            to += 1024;
-        }
+    constexpr int R = Lds<T>::R;
+#pragma unroll 1
+    for (int p = wave; p < pieces * R; p += waves)
+        load_to_lds(rsrc, to + p * 1024, at, R == 1 ? p * 32 : (p >> 1) * 64 + (p & 1) * 16);
 }
-// `pieces` KB as they lie
-__device__ __forceinline__ void bring_flat(i32x4_t rsrc, uint32_t to, int pieces, uint64_t mine)
+// ... or what lies so already
+__device__ __forceinline__ void bring_flat(i32x4_t rsrc, uint32_t to, int pieces, int wave, int waves)
 {
-    for (int x = 0; x < pieces; x++, mine >>= 1, to += 1024)
-        if (mine & 1) load_to_lds(rsrc, to, 16 * lane_id(), x * 1024);
+#pragma unroll 1
+    for (int p = wave; p < pieces; p += waves) load_to_lds(rsrc, to + p * 1024, 16 * lane_id(), p * 1024);
 }
 
 // the operand of a record in LDS
@@ -556,23 +515,202 @@ __device__ __forceinline__ Part<N> staged(uint32_t at, int index)
     return r;
 }
 
-// a scalar for each of a block's rows, of a record in LDS
-__device__ __forceinline__ f32x16_t row_scalars(uint32_t at, int h)
-{
-    f32x16_t r;
-#pragma unroll
-    for (int g4 = 0; g4 < 4; g4++) {
-        const f32x4_t x = lds_read<f32x4_t>(at + 32 * g4 + 16 * h);
-#pragma unroll
-        for (int e = 0; e < 4; e++) r[4 * g4 + e] = x[e];
-    }
-    return r;
-}
-
 // what this wavefront brought has arrived, then what the workgroup did
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
+
+template <typename T>
+__device__ __forceinline__ uint32_t row_at(uint32_t kept, int64_t stride)
+{
+    const int l = lane_id(), r = l & 31;
+    return kept >> r & 1 ? (uint32_t)(r * stride * sizeof(T)) + (l >> 5) * 8 * (uint32_t)sizeof(T) : kNowhere;
+}
+
+// For the walks the rows of a chunk lie in LDS as 16 rows x 32 elements a KB (fp32: two KB, the
+// first and the last four of every eight), a row's 4 pieces of 16 bytes side by side, piece g
+// of row r at g ^ (r >> 2): then neither 16 lanes that take a piece of 16 rows nor 16 that take
+// a column of 4 rows meet on a bank.
+template <typename T>
+struct Lane {
+    static constexpr int R = sizeof(T) / 2, kTile = 1024 * R;      // bytes of 16 rows x 32 elements
+    uint32_t rows, keys;     // where the lane's first operands begin: rows, and columns for the state's update
+    int r, q;                // (bf16) its row and quad of a column
+
+    __device__ __forceinline__ Lane()
+    {
+        const int l = lane_id(), g = l >> 4, i = l & 15;
+        rows = (i * 4 + (g ^ (i >> 2))) * 16;
+        r = 4 * g + (i >> 2);
+        q = i & 3;
+        // State rows are kept so that the registers of a block meet rows of K and Q as they lie in
+        // memory: t[a][i] of quarter g is row 8 g + 4 a + i.
+        if (R == 1) keys = (r * 4 + (q ^ g)) * 16;
+        else keys = (16 * g + ((i >> 2) ^ g)) * 16 + (i & 3) * 4;
+    }
+    // rows 16 a + lane & 15, elements 32 x + 8 g + 0 .. 7
+    __device__ __forceinline__ typename Row<T>::Op row(uint32_t at, int x, int a) const
+    {
+        const uint32_t from = at + rows + (x * 2 + a) * kTile;
+        if constexpr (R == 1) return typename Row<T>::Op{{lds_read<u32x4_t>(from)}};
+        else {
+            float f[8];
+            const u32x4_t lo = lds_read<u32x4_t>(from), hi = lds_read<u32x4_t>(from + 1024);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f[j] = __uint_as_float(lo[j]);
+                f[4 + j] = __uint_as_float(hi[j]);
+            }
+            return split8<3>(f);
+        }
+    }
+    // row 8 (i >> 2) + 4 a + (i & 3), i = lane & 15, of block x of the transposed rows
+    __device__ __forceinline__ typename Row<T>::Op column(uint32_t at, int x, int a) const
+    {
+        if constexpr (R == 1) {
+            // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
+            u32x4_t w;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + keys + (x * 2 + j) * kTile + 8 * a)));
+                w[2 * j] = v[0];
+                w[2 * j + 1] = v[1];
+            }
+            return typename Row<T>::Op{{w}};
+        } else {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) f[e] = lds_read<float>(at + keys + (x * 2 + (e >> 2)) * kTile + a * 1024 + (e & 3) * 64);
+            return split8<3>(f);
+        }
+    }
+    // where columns 16 slice .. begin, and these as a block
+    __device__ __forceinline__ uint32_t columns(int slice) const
+    {
+        const int l = lane_id(), g = l >> 4, i = l & 15, x = slice >> 1, odd = slice & 1;
+        if (R == 1) return (r * 4 + ((2 * odd + (q >> 1)) ^ g)) * 16 + (q & 1) * 8 + x * 2 * kTile;
+        const int c = 16 * odd + i;
+        return (16 * g + ((c >> 3) ^ g)) * 16 + (c >> 2 & 1) * 1024 + (c & 3) * 4 + x * 2 * kTile;
+    }
+    __device__ __forceinline__ Block block(uint32_t at, uint32_t columns) const
+    {
+        Block b;
+#pragma unroll
+        for (int a = 0; a < 2; a++)
+            if constexpr (R == 1) {
+                const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + columns + a * kTile));
+#pragma unroll
+                for (int e = 0; e < 4; e++) b.t[a][e] = __uint_as_float((uint32_t)(uint16_t)v[e] << 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; e++) b.t[a][e] = lds_read<float>(at + columns + a * kTile + 64 * e);
+            }
+        return b;
+    }
+};
+
+// Brings 32 rows of `blocks` x 32 elements into that order, every waves-th KB by this wavefront.
+template <typename T>
+__device__ __forceinline__ void bring_tiles(const T *from, int64_t stride, uint32_t kept, uint32_t to, int blocks, int wave,
+                                            int waves)
+{
+    constexpr int R = sizeof(T) / 2;
+    const i32x4_t rsrc = row_rsrc(from);
+    const int l = lane_id(), r = l >> 2, g = (l & 3) ^ (l >> 4);
+    const uint32_t at = (uint32_t)(r * stride * sizeof(T)) + g * 8 * (uint32_t)sizeof(T);
+    const uint32_t first = kept >> r & 1 ? at : kNowhere;
+    const uint32_t second = kept >> (16 + r) & 1 ? at + (uint32_t)(16 * stride * sizeof(T)) : kNowhere;
+#pragma unroll 1
+    for (int p = wave; p < 2 * blocks * R; p += waves) {
+        const int j = p % R, a = p / R & 1, x = p / (2 * R);
+        load_to_lds(rsrc, to + p * 1024, a ? second : first, x * 32 * sizeof(T) + j * 16);
+    }
+}
+
+// a scalar for each of a block's rows, of a record in LDS
+__device__ __forceinline__ Block row_scalars(uint32_t at)
+{
+    Block r;
+#pragma unroll
+    for (int a = 0; a < 2; a++) r.t[a] = lds_read<f32x4_t>(at + 64 * a + 16 * (lane_id() >> 4));
+    return r;
+}
+
+// Blocks whose columns lie in lanes, turned into rows by a wavefront's own scratch: fill() puts
+// rows r0 .. r0 + 3 of the lane's column, take() gets elements 8 h + 0 .. 7 of row lane & 31, as
+// they are stored.
+template <typename T>
+struct Turn {
+    static constexpr int R = sizeof(T) / 2, kBytes = R == 1 ? 16 * 72 : 32 * 17 * 4;
+    u32x4_t w[R];
+
+    static __device__ __forceinline__ void fill(uint32_t scratch, int r0, const f32x4_t &f)
+    {
+        const int c = lane_id() & 15;
+        if constexpr (R == 1) lds_write(scratch + c * 72 + r0 * 2, u32x2_t{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3])});
+        else
+#pragma unroll
+            for (int e = 0; e < 4; e++) lds_write(scratch + ((r0 + e) * 17 + c) * 4, f[e]);
+    }
+    __device__ __forceinline__ void take(uint32_t scratch)
+    {
+        const int l = lane_id(), h = l >> 5;
+        if constexpr (R == 1) {
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(
+                        scratch + (8 * h + 4 * j + ((l & 15) >> 2)) * 72 + (16 * (l >> 4 & 1) + 4 * (l & 3)) * 2)));
+                w[0][2 * j] = v[0];
+                w[0][2 * j + 1] = v[1];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) w[e >> 2][e & 3] = lds_read<uint32_t>(scratch + ((l & 31) * 17 + 8 * h + e) * 4);
+        }
+    }
+    __device__ __forceinline__ void turn(uint32_t scratch, const Block &b)
+    {
+        const int g = lane_id() >> 4;
+        wave_sync();
+#pragma unroll
+        for (int a = 0; a < 2; a++) fill(scratch, 16 * a + 4 * g, b.t[a]);
+        wave_sync();
+        take(scratch);
+    }
+    // as operands for the gradients
+    __device__ __forceinline__ void keep(char *to) const
+    {
+#pragma unroll
+        for (int j = 0; j < R; j++) *gp(reinterpret_cast<u32x4_t *>(to + j * 1024) + lane_id()) = w[j];
+    }
+    // columns 16 slice .. of rows `stride` apart, the first `left` of them
+    __device__ __forceinline__ void write(T *to, int64_t stride, int left, int slice, int dv, bool vec) const
+    {
+        const int l = lane_id(), r = l & 31;
+        if (r >= left) return;
+        constexpr int E = 16 / sizeof(T);                // elements of 16 bytes
+#pragma unroll
+        for (int j = 0; j < R; j++) {
+            const int c = 16 * slice + 8 * (l >> 5) + j * E;
+            T *at = to + r * stride + c;
+            if (vec) {
+                if (c < dv) *gp(reinterpret_cast<u32x4_t *>(at)) = w[j];
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const uint32_t x = w[j][e * sizeof(T) / 4];
+                    if (c + e < dv) {
+                        if constexpr (sizeof(T) == 2) *gp(at + e) = (uint16_t)(e & 1 ? x >> 16 : x);
+                        else *gp(at + e) = __uint_as_float(x);
+                    }
+                }
+            }
+        }
+    }
+};
 
 // ----------------------------------------------------------------- the walks
 
@@ -613,134 +751,82 @@ __device__ __forceinline__ Walk walk_of(const DeltaArgs &A)
     return w;
 }
 
-// States [dk, dv] in memory.  Register 8 j + i of half h of block t is row 32 t + 16 j + 8 h + i:
-// the rows of K^T are taken in the order (SWAP) that makes it so, and then rows of K and Q are
-// met by the state's registers as they lie in memory.
+// a wavefront's 16 columns of a state [dk, dv] in memory: t[a][i] of block x, quarter g is row
+// 32 x + 8 g + 4 a + i
 template <int KT>
-__device__ __forceinline__ void state_read(f32x16_t (&S)[KT], const float *p, int dk, int dv, int h, int col)
+__device__ __forceinline__ void state_read(Block (&S)[KT], const float *p, int dk, int dv, int col)
 {
+    const int g = lane_id() >> 4;
 #pragma unroll
-    for (int t = 0; t < KT; t++)
+    for (int x = 0; x < KT; x++)
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int r = 32 * t + 16 * (i >> 3) + 8 * h + (i & 7);
-            S[t][i] = p && r < dk && col < dv ? *gp(p + r * dv + col) : 0.f;
+        for (int i = 0; i < 8; i++) {
+            const int r = 32 * x + 8 * g + i;
+            S[x].t[i >> 2][i & 3] = p && r < dk && col < dv ? *gp(p + r * dv + col) : 0.f;
         }
 }
 template <int KT>
-__device__ __forceinline__ void state_write(const f32x16_t (&S)[KT], float *p, int dk, int dv, int h, int col)
+__device__ __forceinline__ void state_write(const Block (&S)[KT], float *p, int dk, int dv, int col)
 {
+    const int g = lane_id() >> 4;
 #pragma unroll
-    for (int t = 0; t < KT; t++)
+    for (int x = 0; x < KT; x++)
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const int r = 32 * t + 16 * (i >> 3) + 8 * h + (i & 7);
-            if (r < dk && col < dv) *gp(p + r * dv + col) = S[t][i];
+        for (int i = 0; i < 8; i++) {
+            const int r = 32 * x + 8 * g + i;
+            if (r < dk && col < dv) *gp(p + r * dv + col) = S[x].t[i >> 2][i & 3];
         }
 }
 
-// a wavefront's columns of a state as the gradients read them: rows as operands, 1 KB pieces
-// numbered (block of 32 rows, 16 columns)
-// (APART: the scratch has room for every block of rows, else for one).
-template <typename T, int KT, bool APART = true>
-__device__ __forceinline__ void state_keep(const f32x16_t (&S)[KT], uint32_t scratch, char *to, int slices, int slice)
-{
-    const int h = lane_id() >> 5;
-    constexpr int kStep = APART ? Lds<T>::kTurn : 0, kBlocks = APART ? KT : 1;
-#pragma unroll
-    for (int t0 = 0; t0 < KT; t0 += kBlocks) {
-        wave_sync();
-#pragma unroll
-        for (int t = t0; t < t0 + kBlocks; t++)
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                float f[4];
-#pragma unroll
-                for (int e = 0; e < 4; e++) f[e] = S[t][4 * q + e];
-                Lds<T>::fill(scratch + t * kStep, 16 * (q >> 1) + 8 * h + 4 * (q & 1), f);
-            }
-        wave_sync();
-#pragma unroll
-        for (int t = t0; t < t0 + kBlocks; t++)
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-                const auto p = Lds<T>::row(scratch + t * kStep, x);
-#pragma unroll
-                for (int j = 0; j < Lds<T>::R; j++)
-                    *gp(reinterpret_cast<u32x4_t *>(to + ((t * slices + slice) * 2 + x) * Lds<T>::kRows + j * 1024) + lane_id()) = p.w[j];
-            }
-    }
-}
-
-// a block of 32 rows x 32 columns as rows
+// The state as the gradients read it, rows as operands of 32 x 16 elements: a block is put into
+// the scratch and taken from there, bf16 blocks when all of them are in, fp32 ones, whose chunks
+// leave LDS for one, by themselves.
+template <typename T, int KT>
+constexpr int kScratchBlocks = sizeof(T) == 2 ? KT : 1;
 template <typename T>
-struct Rows32 {
-    typename Lds<T>::Piece p[2];
-
-    __device__ __forceinline__ void take(const f32x16_t &b, uint32_t scratch)
-    {
-        const int h = lane_id() >> 5;
+__device__ __forceinline__ void state_leave(uint32_t scratch, char *to, int x, int slices, int slice)
+{
+    Turn<T> rows;
+    rows.take(scratch);
+    rows.keep(to + (x * slices + slice) * Lds<T>::kRows);
+}
+template <typename T, int KT>
+__device__ __forceinline__ void state_put(uint32_t scratch, const Block &S, const u32x4_t &rounded, char *to, int x, int slices,
+                                          int slice)
+{
+    const int l = lane_id(), c = l & 15, g = l >> 4;
+    if constexpr (sizeof(T) == 2) {
+        scratch += x * Turn<T>::kBytes;
+        lds_write(scratch + c * 72 + 16 * g, u32x2_t{rounded[0], rounded[1]});
+        lds_write(scratch + c * 72 + 16 * g + 8, u32x2_t{rounded[2], rounded[3]});
+    } else {
         wave_sync();
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            float f[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) f[e] = b[4 * q + e];
-            Lds<T>::fill(scratch, 8 * q + 4 * h, f);
-        }
+        for (int a = 0; a < 2; a++) Turn<T>::fill(scratch, 8 * g + 4 * a, S.t[a]);
         wave_sync();
-#pragma unroll
-        for (int x = 0; x < 2; x++) p[x] = Lds<T>::row(scratch, x);
+        state_leave<T>(scratch, to, x, slices, slice);
     }
-    // as operands for the gradients
-    __device__ __forceinline__ void keep(char *to, int slice) const
-    {
+}
+template <typename T, int KT>
+__device__ __forceinline__ void state_keep(uint32_t scratch, char *to, int slices, int slice)
+{
+    if (sizeof(T) != 2) return;
+    wave_sync();
 #pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-            for (int j = 0; j < Lds<T>::R; j++)
-                *gp(reinterpret_cast<u32x4_t *>(to + (slice * 2 + x) * Lds<T>::kRows + j * 1024) + lane_id()) = p[x].w[j];
-    }
-    // columns 32 slice .. of rows `stride` apart, the first `left` of them
-    __device__ __forceinline__ void write(T *to, int64_t stride, int left, int slice, int dv, bool vec) const
-    {
-        const int l = lane_id(), r = l & 31;
-        if (r >= left) return;
-        constexpr int E = 16 / sizeof(T);                // elements of 16 bytes
-#pragma unroll
-        for (int x = 0; x < 2; x++)
-#pragma unroll
-            for (int j = 0; j < Lds<T>::R; j++) {
-                const int c = 32 * slice + 16 * x + 8 * (l >> 5) + j * E;
-                T *at = to + r * stride + c;
-                if (vec) {
-                    if (c < dv) *gp(reinterpret_cast<u32x4_t *>(at)) = p[x].w[j];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; e++) {
-                        const uint32_t w = p[x].w[j][e * sizeof(T) / 4];
-                        if (c + e < dv) {
-                            if constexpr (sizeof(T) == 2) *gp(at + e) = (uint16_t)(e & 1 ? w >> 16 : w);
-                            else *gp(at + e) = __uint_as_float(w);
-                        }
-                    }
-                }
-            }
-    }
-};
+    for (int x = 0; x < KT; x++) state_leave<T>(scratch + x * Turn<T>::kBytes, to, x, slices, slice);
+    wave_sync();
+}
 
 // What a walk has of a chunk in LDS.
 template <typename T, int KT>
 struct ScanLds {
-    static constexpr int q = 2 * KT * Lds<T>::kRows, rec = 2 * q, v = rec + Rec<T>::small;
-    // blocks of a wavefront's scratch: fp32 chunks leave room for one
-    static constexpr int blocks(bool train) { return train && sizeof(T) == 2 ? KT : 1; }
-    static __host__ __device__ int size(int slices) { return v + 2 * slices * Lds<T>::kRows; }
+    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = 2 * q, v = rec + Rec<T>::small;
+    static __host__ __device__ int size(int slices) { return v + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 template <typename T, int KT>
 struct BackLds {
-    static constexpr int q = 2 * KT * Lds<T>::kRows, rec = 2 * q, o = rec + Rec<T>::whole - Rec<T>::sc;
-    static __host__ __device__ int size(int slices) { return o + 2 * slices * Lds<T>::kRows; }
+    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = 2 * q, o = rec + Rec<T>::whole - Rec<T>::sc;
+    static __host__ __device__ int size(int slices) { return o + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 
 // the bits of a chunk's rows that are kept (there, and not masked)
@@ -753,287 +839,311 @@ __device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w,
     return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::sc) + kScKept)) & low_bits(left);
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t row_at(uint32_t kept, int64_t stride)
-{
-    const int l = lane_id(), r = l & 31;
-    return kept >> r & 1 ? (uint32_t)(r * stride * sizeof(T)) + (l >> 5) * 8 * (uint32_t)sizeof(T) : kNowhere;
-}
-
 template <typename T, int KT>
-__device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to,
-                                           uint64_t mine)
+__device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, int wave,
+                                           int waves)
 {
     typedef ScanLds<T, KT> L;
-    constexpr int R = Lds<T>::R, n = 2 * KT * R, m = Rec<T>::small / 1024;
     const int64_t row = (int64_t)w.base + chunk * kCut;
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh), row_at<T>(kept, A.ks), to, 2 * KT, mine);
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh), row_at<T>(kept, A.qs), to + L::q, 2 * KT,
-                  mine >> n);
-    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size), to + L::rec, m, mine >> 2 * n);
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh), row_at<T>(kept, A.vs), to + L::v,
-                  2 * A.slices, mine >> (2 * n + m));
+    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT, wave, waves);
+    bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT, wave, waves);
+    bring_tiles<T>(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh, A.vs, kept, to + L::v, (A.slices + 1) / 2, wave,
+                   waves);
+    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size), to + L::rec, Rec<T>::small / 1024,
+               wave, waves);
 }
 
 template <typename T, int KT>
-__device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to,
-                                           uint64_t mine)
+__device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, int wave,
+                                           int waves)
 {
     typedef BackLds<T, KT> L;
-    constexpr int R = Lds<T>::R, n = 2 * KT * R, m = (Rec<T>::whole - Rec<T>::sc) / 1024;
     const int64_t row = (int64_t)w.base + chunk * kCut;
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh), row_at<T>(kept, A.ks), to, 2 * KT, mine);
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh), row_at<T>(kept, A.qs), to + L::q, 2 * KT,
-                  mine >> n);
-    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size + Rec<T>::sc), to + L::rec, m,
-               mine >> 2 * n);
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh), row_at<T>(kept, A.ds), to + L::o,
-                  2 * A.slices, mine >> (2 * n + m));
+    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT, wave, waves);
+    bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT, wave, waves);
+    bring_tiles<T>(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh, A.ds, kept, to + L::o, (A.slices + 1) / 2, wave,
+                   waves);
+    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size + Rec<T>::sc), to + L::rec,
+               (Rec<T>::whole - Rec<T>::sc) / 1024, wave, waves);
 }
 
 // Walks forward.  SUM: a segment's own part alone, what it does to the state as a matrix (a
-// wavefront for every 32 of its columns, behind those of the values) and what it adds.
+// wavefront for every 16 of its columns, behind those of the values) and what it adds.
 template <typename T, int KT, bool TRAIN, bool SUM>
-__global__ __launch_bounds__(SUM ? 512 : 256) void delta_scan(DeltaArgs A)
+__global__ __launch_bounds__(SUM ? 1024 : 512) void delta_scan(DeltaArgs A)
 {
     constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT;
     typedef ScanLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int l = lane_id(), h = l >> 5, slice = uniform((int)(threadIdx.x >> 6));
-    const int col = 32 * slice + (l & 31), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const int slice = uniform((int)(threadIdx.x >> 6)), waves = uniform((int)(blockDim.x >> 6));
+    const int col = 16 * slice + (lane_id() & 15), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
     const bool values = slice < A.slices;                // or columns of the segment's matrix
-    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * ScanLds<T, KT>::blocks(TRAIN) * Lds<T>::kTurn;
-    const uint64_t mine = share(slice, blockDim.x >> 6);
-    const uint32_t swapped = Lds<T>::template column<true>(), straight = Lds<T>::template column<false>();
+    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * (TRAIN ? kScratchBlocks<T, KT> : 1) * Turn<T>::kBytes;
+    const Lane<T> lane;
+    const uint32_t columns = lane.columns(values ? slice : 0);
 
-    f32x16_t S[KT];
+    Block S[KT];
     if (SUM) {
 #pragma unroll
-        for (int t = 0; t < KT; t++)
+        for (int x = 0; x < KT; x++)
 #pragma unroll
-            for (int i = 0; i < 16; i++)
-                S[t][i] = !values && 32 * t + 16 * (i >> 3) + 8 * h + (i & 7) == col - 32 * A.slices ? 1.f : 0.f;
+            for (int i = 0; i < 8; i++)
+                S[x].t[i >> 2][i & 3] = !values && 32 * x + 8 * (lane_id() >> 4) + i == col - 16 * A.slices ? 1.f : 0.f;
     } else
         state_read<KT>(S, A.cut ? A.starts + w.part * A.dk * A.dv : A.state ? A.state + w.matrix * A.dk * A.dv : nullptr, A.dk,
-                       A.dv, h, col);
+                       A.dv, col);
     uint32_t kept = kept_rows<T>(A, w, 0), next = kept_rows<T>(A, w, 1);
-    if (chunks) scan_bring<T, KT>(A, w, 0, kept, at0, mine);
-    Rows32<T> orows, urows;                              // of the chunk before: stored a step later,
+    if (chunks) scan_bring<T, KT>(A, w, 0, kept, at0, slice, waves);
+    Turn<T> orows, urows;                                // of the chunk before: stored a step later,
                                                          // so that no wait for rows waits for them
     auto leave = [&](int chunk) {
         const int64_t row = (int64_t)w.base + chunk * kCut;
         orows.write(static_cast<T *>(A.o) + (row * A.heads + w.head) * A.dv, (int64_t)A.heads * A.dv, min(w.rows - chunk * kCut, kCut),
                     slice, A.dv, A.ovec);
         if (TRAIN)
-            urows.keep(static_cast<char *>(A.u) + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices * 2 * Lds<T>::kRows, slice);
+            urows.keep(static_cast<char *>(A.u) + (((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices + slice) * Lds<T>::kRows);
     };
     for (int i = 0; i < chunks; i++) {
         const uint32_t at = at0 + (i & 1) * stage;
         meet();
         kept = next;
         if (!SUM && i) leave(i - 1);
-        if (i + 1 < chunks) scan_bring<T, KT>(A, w, i + 1, kept, at0 + (~i & 1) * stage, mine);
+        if (i + 1 < chunks) scan_bring<T, KT>(A, w, i + 1, kept, at0 + (~i & 1) * stage, slice, waves);
         next = kept_rows<T>(A, w, i + 2);
-        if (TRAIN && !SUM)
-            state_keep<T, KT, (sizeof(T) == 2)>(S, scratch, static_cast<char *>(A.s0) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * 2 * Lds<T>::kRows,
-                              A.slices, slice);
         const uint32_t sc = at + L::rec + Rec<T>::sc;
-        f32x16_t X = zero16(), Y = zero16();
+        char *states = static_cast<char *>(A.s0) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * Lds<T>::kRows;
+        Block X = zero_block(), Y = zero_block(), U = zero_block(), V = zero_block();
 #pragma unroll
-        for (int x = 0; x < 2 * KT; x++) {
-            const Part<ST> sp = operand<ST>(S[x / 2], x % 2);
-            mm<ST>(X, Lds<T>::rows(at, x), sp);
-            if (!SUM) mm<OUT>(Y, Lds<T>::rows(at + L::q, x), sp);
+        for (int x = 0; x < KT; x++) {
+            const Part<ST> sp = operand<ST>(S[x]);
+            if (TRAIN && !SUM) state_put<T, KT>(scratch, S[x], sp.p[0], states, x, A.slices, slice);
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+                mm<ST>(X.t[a], lane.row(at, x, a), sp);
+                if (!SUM) mm<OUT>(Y.t[a], lane.row(at + L::q, x, a), sp);
+            }
         }
-        const f32x16_t b = row_scalars(sc + 4 * kScB, h), bg = row_scalars(sc + 4 * kScBG, h);
-        f32x16_t V = zero16(), U = zero16();
-        if (values) V = Lds<T>::block(at + L::v, straight, slice);
+        if (TRAIN && !SUM) state_keep<T, KT>(scratch, states, A.slices, slice);
+        const Block b = row_scalars(sc + 4 * kScB), bg = row_scalars(sc + 4 * kScBG);
+        if (values) V = lane.block(at + L::v, columns);
 #pragma unroll
-        for (int r = 0; r < 16; r++) X[r] = fmaf(b[r], V[r], -bg[r] * X[r]);
+        for (int a = 0; a < 2; a++)
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<ST>(U, staged<ST>(at + L::rec + Rec<T>::n, kc), operand<ST>(X, kc));
-        if (!SUM) {
-            const f32x16_t sg = row_scalars(sc + 4 * kScG, h);
+            for (int r = 0; r < 4; r++) X.t[a][r] = fmaf(b.t[a][r], V.t[a][r], -bg.t[a][r] * X.t[a][r]);
+        const Part<ST> xp = operand<ST>(X);
 #pragma unroll
-            for (int r = 0; r < 16; r++) Y[r] *= sg[r];
-#pragma unroll
-            for (int kc = 0; kc < 2; kc++) mm<OUT>(Y, staged<OUT>(at + L::rec + Rec<T>::p, kc), operand<OUT>(U, kc));
-            orows.take(Y, scratch);
-            if (TRAIN) urows.take(U, scratch);
-        }
-        const f32x16_t wt = row_scalars(sc + 4 * kScW, h);
+        for (int a = 0; a < 2; a++) mm<ST>(U.t[a], staged<ST>(at + L::rec + Rec<T>::n, a), xp);
+        const Block wt = row_scalars(sc + 4 * kScW);
         const float end = lds_read<float>(sc + 4 * kScEnd);
+        Block wu = U;
 #pragma unroll
-        for (int r = 0; r < 16; r++) U[r] *= wt[r];
-        const Part<ST> u0 = operand<ST>(U, 0), u1 = operand<ST>(U, 1);
+        for (int a = 0; a < 2; a++)
 #pragma unroll
-        for (int t = 0; t < KT; t++) {
+            for (int r = 0; r < 4; r++) wu.t[a][r] *= wt.t[a][r];
+        const Part<ST> up = operand<ST>(wu);
 #pragma unroll
-            for (int r = 0; r < 16; r++) S[t][r] *= end;
-            mm<ST>(S[t], Lds<T>::turned(at, swapped, t, 0), u0);
-            mm<ST>(S[t], Lds<T>::turned(at, swapped, t, 1), u1);
+        for (int x = 0; x < KT; x++)
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+#pragma unroll
+                for (int r = 0; r < 4; r++) S[x].t[a][r] *= end;
+                mm<ST>(S[x].t[a], lane.column(at, x, a), up);
+            }
+        if (!SUM) {
+            const Block sg = row_scalars(sc + 4 * kScG);
+            const Part<OUT> op = operand<OUT>(U);
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+#pragma unroll
+                for (int r = 0; r < 4; r++) Y.t[a][r] *= sg.t[a][r];
+                mm<OUT>(Y.t[a], staged<OUT>(at + L::rec + Rec<T>::p, a), op);
+            }
+            if (TRAIN) urows.turn(scratch, U);
+            orows.turn(scratch, Y);
         }
     }
     if (SUM) {
-        if (values) state_write<KT>(S, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, h, col);
+        if (values) state_write<KT>(S, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         else {
-            // the matrix as first operands (rows as they lie, the columns in pieces) and, for the
-            // backward, transposed
-            char *to = A.moves + w.part * A.move_size;
-            state_keep<float, KT, false>(S, at0 + 2 * stage + slice * Lds<float>::kTurn, to, KT, slice - A.slices);
+            // the matrix in rows, and, for the backward, in columns
+            float *to = A.moves + w.part * A.move_size;
+            state_write<KT>(S, to, 32 * KT, 32 * KT, col - 16 * A.slices);
             if (A.moves_back)
 #pragma unroll
-                for (int t = 0; t < KT; t++)
+                for (int x = 0; x < KT; x++)
 #pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        *gp(reinterpret_cast<f32x4_t *>(to + KT * KT * 4096 + (((slice - A.slices) * KT + t) * 4 + j) * 1024) + l) =
-                            f32x4_t{S[t][4 * j], S[t][4 * j + 1], S[t][4 * j + 2], S[t][4 * j + 3]};
+                    for (int a = 0; a < 2; a++)
+                        *gp(reinterpret_cast<f32x4_t *>(to + 1024 * KT * KT + (col - 16 * A.slices) * 32 * KT + 32 * x +
+                                                        8 * (lane_id() >> 4) + 4 * a)) = S[x].t[a];
         }
         return;
     }
     if (chunks) leave(chunks - 1);
-    if (w.last) state_write<KT>(S, A.last + w.matrix * A.dk * A.dv, A.dk, A.dv, h, col);
+    if (w.last) state_write<KT>(S, A.last + w.matrix * A.dk * A.dv, A.dk, A.dv, col);
 }
 
 // Walks backward, from the gradient of the last state.
 template <typename T, int KT, bool SUM>
-__global__ __launch_bounds__(256) void delta_back(DeltaArgs A)
+__global__ __launch_bounds__(512) void delta_back(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST;
     typedef BackLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int l = lane_id(), h = l >> 5, slice = uniform((int)(threadIdx.x >> 6));
-    const int col = 32 * slice + (l & 31), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
-    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * ScanLds<T, KT>::blocks(true) * Lds<T>::kTurn;
-    const uint64_t mine = share(slice, blockDim.x >> 6);
-    const uint32_t swapped = Lds<T>::template column<true>(), straight = Lds<T>::template column<false>();
+    const int slice = uniform((int)(threadIdx.x >> 6)), waves = uniform((int)(blockDim.x >> 6));
+    const int col = 16 * slice + (lane_id() & 15), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * kScratchBlocks<T, KT> * Turn<T>::kBytes;
+    const Lane<T> lane;
+    const uint32_t columns = lane.columns(slice);
 
-    f32x16_t E[KT];
+    Block E[KT];
     state_read<KT>(E, SUM ? nullptr : A.cut ? A.starts + w.part * A.dk * A.dv : A.dlast ? A.dlast + w.matrix * A.dk * A.dv : nullptr,
-                   A.dk, A.dv, h, col);
-    uint32_t kept = kept_rows<T>(A, w, chunks - 1), next = chunks > 1 ? kept_rows<T>(A, w, chunks - 2) : 0;
-    if (chunks) back_bring<T, KT>(A, w, chunks - 1, kept, at0 + (~chunks & 1) * stage, mine);
-    Rows32<T> vrows, zrows;
+                   A.dk, A.dv, col);
+    uint32_t kept = kept_rows<T>(A, w, chunks - 1), next = kept_rows<T>(A, w, chunks - 2);
+    if (chunks) back_bring<T, KT>(A, w, chunks - 1, kept, at0 + (~chunks & 1) * stage, slice, waves);
+    Turn<T> vrows, zrows;
     auto leave = [&](int chunk) {
         const int64_t row = (int64_t)w.base + chunk * kCut;
         vrows.write(static_cast<T *>(A.dv_) + (row * A.heads + w.head) * A.dv, (int64_t)A.heads * A.dv,
                     min(w.rows - chunk * kCut, kCut), slice, A.dv, A.ovec);
-        zrows.keep(static_cast<char *>(A.z) + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices * 2 * Lds<T>::kRows, slice);
+        zrows.keep(static_cast<char *>(A.z) + (((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices + slice) * Lds<T>::kRows);
     };
     for (int i = chunks - 1; i >= 0; i--) {
         const uint32_t at = at0 + (i & 1) * stage;
         meet();
         kept = next;
         if (!SUM && i + 1 < chunks) leave(i + 1);
-        if (i) back_bring<T, KT>(A, w, i - 1, kept, at0 + (~i & 1) * stage, mine);
-        next = i > 1 ? kept_rows<T>(A, w, i - 2) : 0;
-        if (!SUM)
-            state_keep<T, KT, (sizeof(T) == 2)>(E, scratch, static_cast<char *>(A.e) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * 2 * Lds<T>::kRows,
-                              A.slices, slice);
+        if (i) back_bring<T, KT>(A, w, i - 1, kept, at0 + (~i & 1) * stage, slice, waves);
+        next = kept_rows<T>(A, w, i - 2);
         const uint32_t sc = at + L::rec, rec = at + L::rec - Rec<T>::sc;
-        f32x16_t X = zero16(), Z = zero16();
+        char *states = static_cast<char *>(A.e) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * Lds<T>::kRows;
+        Block X = zero_block(), Z = zero_block();
 #pragma unroll
-        for (int x = 0; x < 2 * KT; x++) mm<ST>(X, Lds<T>::rows(at, x), operand<ST>(E[x / 2], x % 2));
-        const f32x16_t wt = row_scalars(sc + 4 * kScW, h);
-        f32x16_t D = Lds<T>::block(at + L::o, straight, slice);
+        for (int x = 0; x < KT; x++) {
+            const Part<ST> ep = operand<ST>(E[x]);
+            if (!SUM) state_put<T, KT>(scratch, E[x], ep.p[0], states, x, A.slices, slice);
 #pragma unroll
-        for (int r = 0; r < 16; r++) X[r] *= wt[r];
+            for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
+        }
+        if (!SUM) state_keep<T, KT>(scratch, states, A.slices, slice);
+        const Block wt = row_scalars(sc + 4 * kScW);
+        Block D = lane.block(at + L::o, columns);
+        const Part<IN> dp = operand<IN>(D);
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<ST>(X, staged<ST>(rec + Rec<T>::pt, kc), operand<IN>(D, kc));
+        for (int a = 0; a < 2; a++) {
 #pragma unroll
-        for (int kc = 0; kc < 2; kc++) mm<ST>(Z, staged<ST>(rec + Rec<T>::nt, kc), operand<ST>(X, kc));
-        const f32x16_t b = row_scalars(sc + 4 * kScB, h), bg = row_scalars(sc + 4 * kScBG, h), sg = row_scalars(sc + 4 * kScG, h);
+            for (int r = 0; r < 4; r++) X.t[a][r] *= wt.t[a][r];
+            mm<ST>(X.t[a], staged<ST>(rec + Rec<T>::pt, a), dp);
+        }
+        const Part<ST> xp = operand<ST>(X);
+#pragma unroll
+        for (int a = 0; a < 2; a++) mm<ST>(Z.t[a], staged<ST>(rec + Rec<T>::nt, a), xp);
+        const Block bg = row_scalars(sc + 4 * kScBG), sg = row_scalars(sc + 4 * kScG);
         const float end = lds_read<float>(sc + 4 * kScEnd);
+        Block gz = Z;
+#pragma unroll
+        for (int a = 0; a < 2; a++)
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                gz.t[a][r] *= -bg.t[a][r];
+                D.t[a][r] *= sg.t[a][r];
+            }
+        const Part<ST> zp = operand<ST>(gz), op = operand<ST>(D);
+#pragma unroll
+        for (int x = 0; x < KT; x++)
+#pragma unroll
+            for (int a = 0; a < 2; a++) {
+#pragma unroll
+                for (int r = 0; r < 4; r++) E[x].t[a][r] *= end;
+                mm<ST>(E[x].t[a], lane.column(at, x, a), zp);
+                mm<ST>(E[x].t[a], lane.column(at + L::q, x, a), op);
+            }
         if (!SUM) {
-            zrows.take(Z, scratch);
+            zrows.turn(scratch, Z);
+            const Block b = row_scalars(sc + 4 * kScB);
 #pragma unroll
-            for (int r = 0; r < 16; r++) X[r] = b[r] * Z[r];
-            vrows.take(X, scratch);
-        }
+            for (int a = 0; a < 2; a++)
 #pragma unroll
-        for (int r = 0; r < 16; r++) {
-            Z[r] *= -bg[r];
-            D[r] *= sg[r];
-        }
-        const Part<ST> z0 = operand<ST>(Z, 0), z1 = operand<ST>(Z, 1), d0 = operand<ST>(D, 0), d1 = operand<ST>(D, 1);
-#pragma unroll
-        for (int t = 0; t < KT; t++) {
-#pragma unroll
-            for (int r = 0; r < 16; r++) E[t][r] *= end;
-            mm<ST>(E[t], Lds<T>::turned(at, swapped, t, 0), z0);
-            mm<ST>(E[t], Lds<T>::turned(at, swapped, t, 1), z1);
-            mm<ST>(E[t], Lds<T>::turned(at + L::q, swapped, t, 0), d0);
-            mm<ST>(E[t], Lds<T>::turned(at + L::q, swapped, t, 1), d1);
+                for (int r = 0; r < 4; r++) Z.t[a][r] *= b.t[a][r];
+            vrows.turn(scratch, Z);
         }
     }
     if (SUM) {
-        state_write<KT>(E, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, h, col);
+        state_write<KT>(E, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         return;
     }
     if (chunks) leave(0);
-    if (w.first && A.dstate) state_write<KT>(E, A.dstate + w.matrix * A.dk * A.dv, A.dk, A.dv, h, col);
+    if (w.first && A.dstate) state_write<KT>(E, A.dstate + w.matrix * A.dk * A.dv, A.dk, A.dv, col);
 }
 
 // The states at the edges of a cut sample's segments, one after another: S' = move S + added
-// (BACK: from the last, with the move transposed).  A wavefront has 32 columns of a sample's
+// (BACK: from the last, with the move transposed).  A wavefront has 16 columns of a sample's
 // and head's state; the moves arrive in LDS one ahead.  What a segment adds is replaced by the
 // state that it begins with.
 template <int KT, bool BACK>
-__global__ __launch_bounds__(256) void delta_join(DeltaArgs A)
+__global__ __launch_bounds__(512) void delta_join(DeltaArgs A)
 {
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     constexpr int stage = KT * KT * 4096;
     const int sample = blockIdx.x / (uint32_t)A.heads, head = blockIdx.x - (uint32_t)sample * (uint32_t)A.heads;
-    const int l = lane_id(), h = l >> 5, c = l & 31, slice = uniform((int)(threadIdx.x >> 6)), col = 32 * slice + c;
+    const int l = lane_id(), g = l >> 4, slice = uniform((int)(threadIdx.x >> 6)), waves = uniform((int)(blockDim.x >> 6));
+    const int col = 16 * slice + (l & 15);
     const int base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
     const int rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - base, 0);
     const int parts = (rows + kSpan - 1) / kSpan, part0 = base / kSpan + sample + 1;
     const int64_t matrix = (int64_t)sample * A.heads + head;
-    const uint32_t at0 = lds_address(lds), spot = (h * 32 + ((c & 19) | (c & 4) << 1 | (c & 8) >> 1)) * 16;
-    const uint64_t mine = share(slice, blockDim.x >> 6);
+    const uint32_t at0 = lds_address(lds);
     const float *from = BACK ? A.dlast : A.state;
-    f32x16_t S[KT], next[KT];
-    state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, h, col);
+    Block S[KT], next[KT];
+    state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, col);
     auto number = [&](int j) { return (int64_t)(part0 + (BACK ? parts - 1 - j : j)) * A.heads + head; };
+    // a KB holds 4 of every 8 columns of 32 x .. of the 16 rows of a register block, a row a lane & 15
     auto bring = [&](int j) {
-        bring_flat(row_rsrc(A.moves + number(j) * A.move_size + (BACK ? KT * KT * 4096 : 0)), at0 + (j & 1) * stage, stage / 1024, mine);
+        const i32x4_t rsrc = row_rsrc(A.moves + number(j) * A.move_size + (BACK ? 1024 * KT * KT : 0));
+        const uint32_t mine = (uint32_t)((8 * ((l & 15) >> 2) + (l & 3)) * 32 * KT + 8 * g) * 4;
+#pragma unroll 1
+        for (int p = slice; p < stage / 1024; p += waves) {
+            const int c = p & 1, x = (p >> 1) % KT, a = (p >> 1) / KT & 1, y = (p >> 1) / (2 * KT);   // row block y, half a
+            load_to_lds(rsrc, at0 + (j & 1) * stage + p * 1024, mine, ((32 * y + 4 * a) * 32 * KT + 32 * x + 4 * c) * 4);
+        }
     };
     if (parts) bring(0);
     for (int j = 0; j < parts; j++) {
         float *added = A.starts + number(j) * A.dk * A.dv;
         meet();
         if (j + 1 < parts) bring(j + 1);
-        state_read<KT>(next, added, A.dk, A.dv, h, col);
-        state_write<KT>(S, added, A.dk, A.dv, h, col);
+        state_read<KT>(next, added, A.dk, A.dv, col);
+        state_write<KT>(S, added, A.dk, A.dv, col);
         if (j + 1 == parts) break;
-        const uint32_t at = at0 + (j & 1) * stage + spot;
-        Part<3> sp[2 * KT];
+        const uint32_t at = at0 + (j & 1) * stage + 16 * l;
+        Part<3> sp[KT];
 #pragma unroll
-        for (int x = 0; x < 2 * KT; x++) sp[x] = operand<3>(S[x / 2], x % 2);
+        for (int x = 0; x < KT; x++) sp[x] = operand<3>(S[x]);
 #pragma unroll
-        for (int t = 0; t < KT; t++) {
+        for (int y = 0; y < KT; y++)
 #pragma unroll
-            for (int x = 0; x < 2 * KT; x++) {
-                float f[8];
-                const u32x4_t a = lds_read<u32x4_t>(at + (t * 2 * KT + x) * 2048), b = lds_read<u32x4_t>(at + (t * 2 * KT + x) * 2048 + 1024);
+            for (int a = 0; a < 2; a++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    f[e] = __uint_as_float(a[e]);
-                    f[4 + e] = __uint_as_float(b[e]);
+                for (int x = 0; x < KT; x++) {
+                    float f[8];
+                    const uint32_t p = at + ((y * 2 + a) * KT + x) * 2048;
+                    const u32x4_t lo = lds_read<u32x4_t>(p), hi = lds_read<u32x4_t>(p + 1024);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        f[e] = __uint_as_float(lo[e]);
+                        f[4 + e] = __uint_as_float(hi[e]);
+                    }
+                    mm<3>(next[y].t[a], split8<3>(f), sp[x]);
                 }
-                mm<3>(next[t], split8<3>(f), sp[x]);
-            }
-        }
 #pragma unroll
-        for (int t = 0; t < KT; t++) S[t] = next[t];
+        for (int x = 0; x < KT; x++) S[x] = next[x];
     }
     if (parts) return;                                   // a sample without rows hands its state on
     float *to = BACK ? A.dstate : A.last;
-    if (to) state_write<KT>(S, to + matrix * A.dk * A.dv, A.dk, A.dv, h, col);
+    if (to) state_write<KT>(S, to + matrix * A.dk * A.dv, A.dk, A.dv, col);
 }
 
 // ----------------------------------------------------------------- gradients
@@ -1080,7 +1190,7 @@ __device__ __forceinline__ typename Row<T>::Op kept_operand(const char *at, int 
 template <typename T, int KT>
 struct GradLds {
     static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, u = sc + 1024;
-    static __host__ __device__ int size(int slices) { return u + 3 * 2 * slices * Lds<T>::kRows; }
+    static __host__ __device__ int size(int slices) { return u + 3 * slices * Lds<T>::kRows; }
 };
 
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk, all of them the
@@ -1119,19 +1229,18 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
     const bool keep = valid && (!A.mask || *gp(A.mask + row + c));
     const uint32_t kept = (uint32_t)__ballot(keep);
     const uint32_t at = lds_address(lds);
-    const uint64_t mine = share(wave, KT);
-    const uint32_t columns = Lds<T>::template column<false>();
+    const uint32_t columns = Lds<T>::column();
     auto bring = [&](int head) {
         const int64_t number = (int64_t)tile * A.heads + head;
-        const int n = 2 * A.slices;
+        const int n = A.slices;
         if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size + Rec<T>::sc), at + L::sc, 16 * l, 0);
-        bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * Lds<T>::kRows), at + L::u, n * R, mine);
-        bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * Lds<T>::kRows), at + L::u + n * Lds<T>::kRows, n * R, mine);
+        bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * Lds<T>::kRows), at + L::u, n * R, wave, KT);
+        bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * Lds<T>::kRows), at + L::u + n * Lds<T>::kRows, n * R, wave, KT);
         bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + head * A.dh), row_at<T>(kept, A.ds),
-                      at + L::u + 2 * n * Lds<T>::kRows, n, mine);
+                      at + L::u + 2 * n * Lds<T>::kRows, n, wave, KT);
     };
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + key * A.kh), row_at<T>(kept, A.ks), at, 2 * KT, mine);
-    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + key * A.qh), row_at<T>(kept, A.qs), at + L::q, 2 * KT, mine);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + key * A.kh), row_at<T>(kept, A.ks), at, 2 * KT, wave, KT);
+    bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + key * A.qh), row_at<T>(kept, A.qs), at + L::q, 2 * KT, wave, KT);
     bring(key * A.group);
     meet();
     f32x16_t kk = zero16(), kq = zero16(), qk = zero16();
@@ -1150,7 +1259,7 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
             bring(head);
             meet();
         }
-        const int64_t number = (int64_t)tile * A.heads + head, n = 2 * A.slices;
+        const int64_t number = (int64_t)tile * A.heads + head, n = A.slices;
         const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<T>::kRows;
         const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<T>::kRows;
         const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * Lds<T>::kRows, oat = zat + n * Lds<T>::kRows;
@@ -1470,13 +1579,13 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     DeltaPlan p{};
     p.el = d->dtype == EMB_BF16 ? 2 : 4;
     p.kt = (d->dk + 31) / 32;
-    p.slices = (d->dv + 31) / 32;
+    p.slices = (d->dv + 15) / 16;
     p.tiles = seg_tiles(d->n, d->samples, 1, kCut);
     p.cut = delta_cut(d);
     const bool bf = p.el == 2;
     p.rec = train ? (bf ? Rec<uint16_t>::whole : Rec<float>::whole) : (bf ? Rec<uint16_t>::small : Rec<float>::small);
     p.recs = (size_t)p.tiles * d->heads * p.rec;
-    p.us = (size_t)p.tiles * d->heads * p.slices * 1024 * p.el;
+    p.us = (size_t)p.tiles * d->heads * p.slices * 512 * p.el;
     p.states = p.us * p.kt;
     if (p.cut) {
         const size_t segments = (size_t)seg_tiles(d->n, d->samples, 1, kSpan) * d->heads;
@@ -1487,7 +1596,7 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     const size_t keys = pad256((size_t)d->n * d->key_heads * p.kt * 32 * p.el);
     p.q = rows_ready(d->q, d->q_stride, d->q_head_stride, d->dk, p.el) ? 0 : keys;
     p.k = rows_ready(d->k, d->k_stride, d->k_head_stride, d->dk, p.el) ? 0 : keys;
-    const size_t values = pad256((size_t)d->n * d->heads * p.slices * 32 * p.el);
+    const size_t values = pad256((size_t)d->n * d->heads * ((d->dv + 31) / 32 * 32) * p.el);
     p.v = rows_ready(d->v, d->v_stride, d->v_head_stride, d->dv, p.el) ? 0 : values;
     p.saved = p.recs + p.states + p.us + p.moves;
     p.forward = (train ? 0 : p.recs + p.moves) + p.starts + p.q + p.k + p.v;
@@ -1552,7 +1661,7 @@ DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
     A.scale = d->scale;
     A.rec_size = (int64_t)p.rec;
     A.cut = p.cut;
-    A.move_size = (int64_t)p.move;
+    A.move_size = (int64_t)p.move / 4;
     return A;
 }
 
@@ -1562,7 +1671,7 @@ void delta_saved(const DeltaPlan &p, DeltaArgs &A, char *saved)
     A.rec = saved;
     A.s0 = saved + p.recs;
     A.u = saved + p.recs + p.states;
-    A.moves = saved + p.recs + p.states + p.us;
+    A.moves = reinterpret_cast<float *>(saved + p.recs + p.states + p.us);
 }
 
 int64_t delta_walks(const emb_delta *d, const DeltaPlan &p)
@@ -1574,7 +1683,7 @@ emb_status delta_sizes(const emb_delta *d, const DeltaPlan &p)
 {
     // a launch's threads in one dimension are counted in 32 bits
     const int64_t most = (int64_t(1) << 32) - 1, packed = d->n * d->heads * 128;
-    if (p.tiles > most / 256 || delta_walks(d, p) > most / 512 || packed > most)
+    if (p.tiles > most / 256 || delta_walks(d, p) > most / 1024 || packed > most)
         return fail(EMB_ERR_UNSUPPORTED, "delta rule: too many rows, samples and heads for one launch");
     return EMB_OK;
 }
@@ -1591,18 +1700,16 @@ void delta_launch(F kernel, dim3 grid, int threads, size_t lds, const DeltaArgs 
 template <typename T, int KT>
 void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool train, hipStream_t st)
 {
-    typedef ScanLds<T, KT> L;
     const dim3 all((unsigned)tiles, (unsigned)A.heads), walk((unsigned)walks);
-    const int stages = 2 * L::size(A.slices);
+    const int stages = 2 * ScanLds<T, KT>::size(A.slices), join = 2 * KT * KT * 4096;
     if (train) delta_launch(delta_prepare<T, KT, true>, all, 64, 0, A, st);
     else delta_launch(delta_prepare<T, KT, false>, all, 64, 0, A, st);
     if (!walks) return;
     if (A.cut) {
-        const int waves = A.slices + KT;
-        delta_launch(delta_scan<T, KT, false, true>, walk, 64 * waves, stages + waves * Lds<float>::kTurn, A, st);
-        delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, 2 * KT * KT * 4096, A, st);
+        delta_launch(delta_scan<T, KT, false, true>, walk, 64 * (A.slices + 2 * KT), stages, A, st);
+        delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, join, A, st);
     }
-    const size_t lds = stages + A.slices * L::blocks(train) * Lds<T>::kTurn;
+    const int lds = stages + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
     if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices, lds, A, st);
     else delta_launch(delta_scan<T, KT, false, false>, walk, 64 * A.slices, lds, A, st);
 }
@@ -1611,12 +1718,12 @@ template <typename T, int KT>
 void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool, hipStream_t st)
 {
     const dim3 walk((unsigned)walks);
-    const size_t lds = 2 * BackLds<T, KT>::size(A.slices) + A.slices * ScanLds<T, KT>::blocks(true) * Lds<T>::kTurn;
+    const int stages = 2 * BackLds<T, KT>::size(A.slices), join = 2 * KT * KT * 4096;
     if (walks && A.cut) {
-        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices, lds, A, st);
-        delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, 2 * KT * KT * 4096, A, st);
+        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices, stages, A, st);
+        delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, join, A, st);
     }
-    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices, lds, A, st);
+    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices, stages + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
     delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
 }
 
@@ -1670,7 +1777,7 @@ extern "C" emb_status emb_delta_forward(const emb_delta *d, void *o, float *last
     if (train) delta_saved(p, A, static_cast<char *>(saved));
     else {
         A.rec = ws;
-        A.moves = ws + p.recs;
+        A.moves = reinterpret_cast<float *>(ws + p.recs);
         ws += p.recs + p.moves;
     }
     A.starts = reinterpret_cast<float *>(ws);
@@ -1732,7 +1839,7 @@ extern "C" emb_status emb_delta_backward(const emb_delta *d, const void *saved, 
     delta_rows(d, p.q, A.q, A.qs, A.qh, d->key_heads, d->dk, ws, st);
     delta_rows(d, p.k, A.k, A.ks, A.kh, d->key_heads, d->dk, ws, st);
     const size_t values = rows_ready(dout, dout_stride, dout_head_stride, d->dv, p.el)
-                              ? 0 : pad256((size_t)d->n * d->heads * p.slices * 32 * p.el);
+                              ? 0 : pad256((size_t)d->n * d->heads * ((d->dv + 31) / 32 * 32) * p.el);
     delta_rows(d, values, A.dout, A.ds, A.dh, d->heads, d->dv, ws, st);
     const int64_t walks = delta_walks(d, p);
     if (d->dtype == EMB_BF16) EMB_DELTA_SIZES(delta_backward_launch, uint16_t);
