@@ -517,6 +517,8 @@ __device__ __forceinline__ Part<N> staged(uint32_t at, int index)
 
 // what this wavefront brought has arrived, then what the workgroup did
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// ... of a wavefront that brings nothing, whose stores nobody in the workgroup waits for
+__device__ __forceinline__ void meet_others() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1; }
 
@@ -611,10 +613,9 @@ struct Lane {
     }
 };
 
-// Brings 32 rows of `blocks` x 32 elements into that order, every waves-th KB by this wavefront.
+// Brings 32 rows of `blocks` x 32 elements into that order.
 template <typename T>
-__device__ __forceinline__ void bring_tiles(const T *from, int64_t stride, uint32_t kept, uint32_t to, int blocks, int wave,
-                                            int waves)
+__device__ __forceinline__ void bring_tiles(const T *from, int64_t stride, uint32_t kept, uint32_t to, int blocks)
 {
     constexpr int R = sizeof(T) / 2;
     const i32x4_t rsrc = row_rsrc(from);
@@ -622,11 +623,11 @@ __device__ __forceinline__ void bring_tiles(const T *from, int64_t stride, uint3
     const uint32_t at = (uint32_t)(r * stride * sizeof(T)) + g * 8 * (uint32_t)sizeof(T);
     const uint32_t first = kept >> r & 1 ? at : kNowhere;
     const uint32_t second = kept >> (16 + r) & 1 ? at + (uint32_t)(16 * stride * sizeof(T)) : kNowhere;
-#pragma unroll 1
-    for (int p = wave; p < 2 * blocks * R; p += waves) {
-        const int j = p % R, a = p / R & 1, x = p / (2 * R);
-        load_to_lds(rsrc, to + p * 1024, a ? second : first, x * 32 * sizeof(T) + j * 16);
-    }
+    for (int x = 0; x < blocks; x++)
+#pragma unroll
+        for (int a = 0; a < 2; a++)
+#pragma unroll
+            for (int j = 0; j < R; j++, to += 1024) load_to_lds(rsrc, to, a ? second : first, x * 32 * sizeof(T) + j * 16);
 }
 
 // a scalar for each of a block's rows, of a record in LDS
@@ -686,25 +687,22 @@ struct Turn {
 #pragma unroll
         for (int j = 0; j < R; j++) *gp(reinterpret_cast<u32x4_t *>(to + j * 1024) + lane_id()) = w[j];
     }
-    // columns 16 slice .. of rows `stride` apart, the first `left` of them
-    __device__ __forceinline__ void write(T *to, int64_t stride, int left, int slice, int dv, bool vec) const
+    // columns c .. (the lane's, at `to`) of its row, where it is there
+    __device__ __forceinline__ void write(T *to, bool there, int c, int dv, bool vec) const
     {
-        const int l = lane_id(), r = l & 31;
-        if (r >= left) return;
+        if (!there) return;
         constexpr int E = 16 / sizeof(T);                // elements of 16 bytes
 #pragma unroll
         for (int j = 0; j < R; j++) {
-            const int c = 16 * slice + 8 * (l >> 5) + j * E;
-            T *at = to + r * stride + c;
             if (vec) {
-                if (c < dv) *gp(reinterpret_cast<u32x4_t *>(at)) = w[j];
+                if (c + j * E < dv) *gp(reinterpret_cast<u32x4_t *>(to + j * E)) = w[j];
             } else {
 #pragma unroll
                 for (int e = 0; e < E; e++) {
                     const uint32_t x = w[j][e * sizeof(T) / 4];
-                    if (c + e < dv) {
-                        if constexpr (sizeof(T) == 2) *gp(at + e) = (uint16_t)(e & 1 ? x >> 16 : x);
-                        else *gp(at + e) = __uint_as_float(x);
+                    if (c + j * E + e < dv) {
+                        if constexpr (sizeof(T) == 2) *gp(to + j * E + e) = (uint16_t)(e & 1 ? x >> 16 : x);
+                        else *gp(to + j * E + e) = __uint_as_float(x);
                     }
                 }
             }
@@ -817,7 +815,8 @@ __device__ __forceinline__ void state_keep(uint32_t scratch, char *to, int slice
     wave_sync();
 }
 
-// What a walk has of a chunk in LDS.
+// What a walk has of a chunk in LDS, and its last wavefront, which brings the chunks one ahead
+// and does nothing else.  SUM: no Q, no P, and V for the values alone.
 template <typename T, int KT>
 struct ScanLds {
     static constexpr int q = 2 * KT * Lane<T>::kTile, rec = 2 * q, v = rec + Rec<T>::small;
@@ -839,48 +838,65 @@ __device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w,
     return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::sc) + kScKept)) & low_bits(left);
 }
 
-template <typename T, int KT>
-__device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, int wave,
-                                           int waves)
+template <typename T, int KT, bool SUM>
+__device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, bool values)
 {
     typedef ScanLds<T, KT> L;
     const int64_t row = (int64_t)w.base + chunk * kCut;
-    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT, wave, waves);
-    bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT, wave, waves);
-    bring_tiles<T>(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh, A.vs, kept, to + L::v, (A.slices + 1) / 2, wave,
-                   waves);
-    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size), to + L::rec, Rec<T>::small / 1024,
-               wave, waves);
+    const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
+    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
+    if (!SUM) bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT);
+    if (values) bring_tiles<T>(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh, A.vs, kept, to + L::v, (A.slices + 1) / 2);
+    const i32x4_t rsrc = row_rsrc(rec);
+#pragma unroll
+    for (int p = 0; p < Rec<T>::small / 1024; p++)
+        if (!SUM || p * 1024 < Rec<T>::p || p * 1024 >= Rec<T>::sc)
+            load_to_lds(rsrc, to + L::rec + p * 1024, 16 * lane_id(), p * 1024);
 }
 
 template <typename T, int KT>
-__device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, int wave,
-                                           int waves)
+__device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to)
 {
     typedef BackLds<T, KT> L;
     const int64_t row = (int64_t)w.base + chunk * kCut;
-    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT, wave, waves);
-    bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT, wave, waves);
-    bring_tiles<T>(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh, A.ds, kept, to + L::o, (A.slices + 1) / 2, wave,
-                   waves);
-    bring_flat(row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size + Rec<T>::sc), to + L::rec,
-               (Rec<T>::whole - Rec<T>::sc) / 1024, wave, waves);
+    const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
+    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
+    bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT);
+    bring_tiles<T>(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh, A.ds, kept, to + L::o, (A.slices + 1) / 2);
+    const i32x4_t rsrc = row_rsrc(rec + Rec<T>::sc);
+#pragma unroll
+    for (int p = 0; p < (Rec<T>::whole - Rec<T>::sc) / 1024; p++)
+        load_to_lds(rsrc, to + L::rec + p * 1024, 16 * lane_id(), p * 1024);
 }
 
-// Walks forward.  SUM: a segment's own part alone, what it does to the state as a matrix (a
-// wavefront for every 16 of its columns, behind those of the values) and what it adds.
+// Walks forward.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
+// to the state, as a matrix (1: the walk without values from the identity).
 template <typename T, int KT, bool TRAIN, bool SUM>
-__global__ __launch_bounds__(SUM ? 1024 : 512) void delta_scan(DeltaArgs A)
+__global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
     constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT;
     typedef ScanLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int slice = uniform((int)(threadIdx.x >> 6)), waves = uniform((int)(blockDim.x >> 6));
-    const int col = 16 * slice + (lane_id() & 15), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
-    const bool values = slice < A.slices;                // or columns of the segment's matrix
-    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * (TRAIN ? kScratchBlocks<T, KT> : 1) * Turn<T>::kBytes;
+    const bool values = !SUM || blockIdx.y == 0;
+    const int slice = uniform((int)(threadIdx.x >> 6)), slices = values ? A.slices : 2 * KT;
+    const int stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const uint32_t at0 = lds_address(lds);
+    if (slice >= slices) {
+        if (slice > slices) return;                      // fewer columns of the one kind than of the other
+        uint32_t kept = kept_rows<T>(A, w, 0), next = kept_rows<T>(A, w, 1);
+        if (chunks) scan_bring<T, KT, SUM>(A, w, 0, kept, at0, values);
+        for (int i = 0; i < chunks; i++) {
+            meet();
+            kept = next;
+            if (i + 1 < chunks) scan_bring<T, KT, SUM>(A, w, i + 1, kept, at0 + (~i & 1) * stage, values);
+            next = kept_rows<T>(A, w, i + 2);
+        }
+        return;
+    }
+    const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
+    const uint32_t scratch = at0 + 2 * stage + slice * (TRAIN ? kScratchBlocks<T, KT> : 1) * Turn<T>::kBytes;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(values ? slice : 0);
 
@@ -889,31 +905,20 @@ __global__ __launch_bounds__(SUM ? 1024 : 512) void delta_scan(DeltaArgs A)
 #pragma unroll
         for (int x = 0; x < KT; x++)
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                S[x].t[i >> 2][i & 3] = !values && 32 * x + 8 * (lane_id() >> 4) + i == col - 16 * A.slices ? 1.f : 0.f;
+            for (int i = 0; i < 8; i++) S[x].t[i >> 2][i & 3] = !values && 32 * x + 8 * (l >> 4) + i == col ? 1.f : 0.f;
     } else
         state_read<KT>(S, A.cut ? A.starts + w.part * A.dk * A.dv : A.state ? A.state + w.matrix * A.dk * A.dv : nullptr, A.dk,
                        A.dv, col);
-    uint32_t kept = kept_rows<T>(A, w, 0), next = kept_rows<T>(A, w, 1);
-    if (chunks) scan_bring<T, KT>(A, w, 0, kept, at0, slice, waves);
-    Turn<T> orows, urows;                                // of the chunk before: stored a step later,
-                                                         // so that no wait for rows waits for them
-    auto leave = [&](int chunk) {
-        const int64_t row = (int64_t)w.base + chunk * kCut;
-        orows.write(static_cast<T *>(A.o) + (row * A.heads + w.head) * A.dv, (int64_t)A.heads * A.dv, min(w.rows - chunk * kCut, kCut),
-                    slice, A.dv, A.ovec);
-        if (TRAIN)
-            urows.keep(static_cast<char *>(A.u) + (((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices + slice) * Lds<T>::kRows);
-    };
+    // what leaves: the lane's piece of a row of o, of U and of the states, a chunk's step apart
+    const int64_t ostep = (int64_t)kCut * A.heads * A.dv, ustep = (int64_t)A.heads * A.slices * Lds<T>::kRows;
+    T *o = static_cast<T *>(A.o) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c;
+    const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
+    char *u = static_cast<char *>(A.u) + (number * A.slices + slice) * Lds<T>::kRows;
+    char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<T>::kRows;
     for (int i = 0; i < chunks; i++) {
         const uint32_t at = at0 + (i & 1) * stage;
-        meet();
-        kept = next;
-        if (!SUM && i) leave(i - 1);
-        if (i + 1 < chunks) scan_bring<T, KT>(A, w, i + 1, kept, at0 + (~i & 1) * stage, slice, waves);
-        next = kept_rows<T>(A, w, i + 2);
+        meet_others();
         const uint32_t sc = at + L::rec + Rec<T>::sc;
-        char *states = static_cast<char *>(A.s0) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * Lds<T>::kRows;
         Block X = zero_block(), Y = zero_block(), U = zero_block(), V = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
@@ -925,13 +930,12 @@ __global__ __launch_bounds__(SUM ? 1024 : 512) void delta_scan(DeltaArgs A)
                 if (!SUM) mm<OUT>(Y.t[a], lane.row(at + L::q, x, a), sp);
             }
         }
-        if (TRAIN && !SUM) state_keep<T, KT>(scratch, states, A.slices, slice);
         const Block b = row_scalars(sc + 4 * kScB), bg = row_scalars(sc + 4 * kScBG);
         if (values) V = lane.block(at + L::v, columns);
 #pragma unroll
         for (int a = 0; a < 2; a++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) X.t[a][r] = fmaf(b.t[a][r], V.t[a][r], -bg.t[a][r] * X.t[a][r]);
+            for (int e = 0; e < 4; e++) X.t[a][e] = fmaf(b.t[a][e], V.t[a][e], -bg.t[a][e] * X.t[a][e]);
         const Part<ST> xp = operand<ST>(X);
 #pragma unroll
         for (int a = 0; a < 2; a++) mm<ST>(U.t[a], staged<ST>(at + L::rec + Rec<T>::n, a), xp);
@@ -941,27 +945,36 @@ __global__ __launch_bounds__(SUM ? 1024 : 512) void delta_scan(DeltaArgs A)
 #pragma unroll
         for (int a = 0; a < 2; a++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) wu.t[a][r] *= wt.t[a][r];
+            for (int e = 0; e < 4; e++) wu.t[a][e] *= wt.t[a][e];
         const Part<ST> up = operand<ST>(wu);
 #pragma unroll
         for (int x = 0; x < KT; x++)
 #pragma unroll
             for (int a = 0; a < 2; a++) {
 #pragma unroll
-                for (int r = 0; r < 4; r++) S[x].t[a][r] *= end;
+                for (int e = 0; e < 4; e++) S[x].t[a][e] *= end;
                 mm<ST>(S[x].t[a], lane.column(at, x, a), up);
             }
         if (!SUM) {
+            if (TRAIN) state_keep<T, KT>(scratch, states, A.slices, slice);
             const Block sg = row_scalars(sc + 4 * kScG);
             const Part<OUT> op = operand<OUT>(U);
 #pragma unroll
             for (int a = 0; a < 2; a++) {
 #pragma unroll
-                for (int r = 0; r < 4; r++) Y.t[a][r] *= sg.t[a][r];
+                for (int e = 0; e < 4; e++) Y.t[a][e] *= sg.t[a][e];
                 mm<OUT>(Y.t[a], staged<OUT>(at + L::rec + Rec<T>::p, a), op);
             }
-            if (TRAIN) urows.turn(scratch, U);
-            orows.turn(scratch, Y);
+            Turn<T> rows;
+            if (TRAIN) {
+                rows.turn(scratch, U);
+                rows.keep(u);
+            }
+            rows.turn(scratch, Y);
+            rows.write(o, r < w.rows - i * kCut, c, A.dv, A.ovec);
+            o += ostep;
+            u += ustep;
+            states += KT * ustep;
         }
     }
     if (SUM) {
@@ -969,57 +982,61 @@ __global__ __launch_bounds__(SUM ? 1024 : 512) void delta_scan(DeltaArgs A)
         else {
             // the matrix in rows, and, for the backward, in columns
             float *to = A.moves + w.part * A.move_size;
-            state_write<KT>(S, to, 32 * KT, 32 * KT, col - 16 * A.slices);
+            state_write<KT>(S, to, 32 * KT, 32 * KT, col);
             if (A.moves_back)
 #pragma unroll
                 for (int x = 0; x < KT; x++)
 #pragma unroll
                     for (int a = 0; a < 2; a++)
-                        *gp(reinterpret_cast<f32x4_t *>(to + 1024 * KT * KT + (col - 16 * A.slices) * 32 * KT + 32 * x +
-                                                        8 * (lane_id() >> 4) + 4 * a)) = S[x].t[a];
+                        *gp(reinterpret_cast<f32x4_t *>(to + 1024 * KT * KT + col * 32 * KT + 32 * x + 8 * (l >> 4) + 4 * a)) = S[x].t[a];
         }
         return;
     }
-    if (chunks) leave(chunks - 1);
     if (w.last) state_write<KT>(S, A.last + w.matrix * A.dk * A.dv, A.dk, A.dv, col);
 }
 
 // Walks backward, from the gradient of the last state.
 template <typename T, int KT, bool SUM>
-__global__ __launch_bounds__(512) void delta_back(DeltaArgs A)
+__global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST;
     typedef BackLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int slice = uniform((int)(threadIdx.x >> 6)), waves = uniform((int)(blockDim.x >> 6));
-    const int col = 16 * slice + (lane_id() & 15), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
-    const uint32_t at0 = lds_address(lds), scratch = at0 + 2 * stage + slice * kScratchBlocks<T, KT> * Turn<T>::kBytes;
+    const int slice = uniform((int)(threadIdx.x >> 6)), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const uint32_t at0 = lds_address(lds);
+    if (slice == A.slices) {
+        uint32_t kept = kept_rows<T>(A, w, chunks - 1), next = kept_rows<T>(A, w, chunks - 2);
+        if (chunks) back_bring<T, KT>(A, w, chunks - 1, kept, at0 + (~chunks & 1) * stage);
+        for (int i = chunks - 1; i >= 0; i--) {
+            meet();
+            kept = next;
+            if (i) back_bring<T, KT>(A, w, i - 1, kept, at0 + (~i & 1) * stage);
+            next = kept_rows<T>(A, w, i - 2);
+        }
+        return;
+    }
+    const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
+    const uint32_t scratch = at0 + 2 * stage + slice * kScratchBlocks<T, KT> * Turn<T>::kBytes;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(slice);
 
     Block E[KT];
     state_read<KT>(E, SUM ? nullptr : A.cut ? A.starts + w.part * A.dk * A.dv : A.dlast ? A.dlast + w.matrix * A.dk * A.dv : nullptr,
                    A.dk, A.dv, col);
-    uint32_t kept = kept_rows<T>(A, w, chunks - 1), next = kept_rows<T>(A, w, chunks - 2);
-    if (chunks) back_bring<T, KT>(A, w, chunks - 1, kept, at0 + (~chunks & 1) * stage, slice, waves);
-    Turn<T> vrows, zrows;
-    auto leave = [&](int chunk) {
-        const int64_t row = (int64_t)w.base + chunk * kCut;
-        vrows.write(static_cast<T *>(A.dv_) + (row * A.heads + w.head) * A.dv, (int64_t)A.heads * A.dv,
-                    min(w.rows - chunk * kCut, kCut), slice, A.dv, A.ovec);
-        zrows.keep(static_cast<char *>(A.z) + (((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.slices + slice) * Lds<T>::kRows);
-    };
+    const int64_t vstep = (int64_t)kCut * A.heads * A.dv, zstep = (int64_t)A.heads * A.slices * Lds<T>::kRows;
+    T *dv = static_cast<T *>(A.dv_) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c + chunks * vstep;
+    const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
+    char *z = static_cast<char *>(A.z) + (number * A.slices + slice) * Lds<T>::kRows + chunks * zstep;
+    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<T>::kRows + chunks * KT * zstep;
     for (int i = chunks - 1; i >= 0; i--) {
         const uint32_t at = at0 + (i & 1) * stage;
-        meet();
-        kept = next;
-        if (!SUM && i + 1 < chunks) leave(i + 1);
-        if (i) back_bring<T, KT>(A, w, i - 1, kept, at0 + (~i & 1) * stage, slice, waves);
-        next = kept_rows<T>(A, w, i - 2);
+        meet_others();
+        dv -= vstep;
+        z -= zstep;
+        states -= KT * zstep;
         const uint32_t sc = at + L::rec, rec = at + L::rec - Rec<T>::sc;
-        char *states = static_cast<char *>(A.e) + ((int64_t)(w.tile0 + i) * A.heads + w.head) * KT * A.slices * Lds<T>::kRows;
         Block X = zero_block(), Z = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
@@ -1028,14 +1045,13 @@ __global__ __launch_bounds__(512) void delta_back(DeltaArgs A)
 #pragma unroll
             for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
         }
-        if (!SUM) state_keep<T, KT>(scratch, states, A.slices, slice);
         const Block wt = row_scalars(sc + 4 * kScW);
         Block D = lane.block(at + L::o, columns);
         const Part<IN> dp = operand<IN>(D);
 #pragma unroll
         for (int a = 0; a < 2; a++) {
 #pragma unroll
-            for (int r = 0; r < 4; r++) X.t[a][r] *= wt.t[a][r];
+            for (int e = 0; e < 4; e++) X.t[a][e] *= wt.t[a][e];
             mm<ST>(X.t[a], staged<ST>(rec + Rec<T>::pt, a), dp);
         }
         const Part<ST> xp = operand<ST>(X);
@@ -1047,9 +1063,9 @@ __global__ __launch_bounds__(512) void delta_back(DeltaArgs A)
 #pragma unroll
         for (int a = 0; a < 2; a++)
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                gz.t[a][r] *= -bg.t[a][r];
-                D.t[a][r] *= sg.t[a][r];
+            for (int e = 0; e < 4; e++) {
+                gz.t[a][e] *= -bg.t[a][e];
+                D.t[a][e] *= sg.t[a][e];
             }
         const Part<ST> zp = operand<ST>(gz), op = operand<ST>(D);
 #pragma unroll
@@ -1057,25 +1073,28 @@ __global__ __launch_bounds__(512) void delta_back(DeltaArgs A)
 #pragma unroll
             for (int a = 0; a < 2; a++) {
 #pragma unroll
-                for (int r = 0; r < 4; r++) E[x].t[a][r] *= end;
+                for (int e = 0; e < 4; e++) E[x].t[a][e] *= end;
                 mm<ST>(E[x].t[a], lane.column(at, x, a), zp);
                 mm<ST>(E[x].t[a], lane.column(at + L::q, x, a), op);
             }
         if (!SUM) {
-            zrows.turn(scratch, Z);
+            state_keep<T, KT>(scratch, states, A.slices, slice);
+            Turn<T> rows;
+            rows.turn(scratch, Z);
+            rows.keep(z);
             const Block b = row_scalars(sc + 4 * kScB);
 #pragma unroll
             for (int a = 0; a < 2; a++)
 #pragma unroll
-                for (int r = 0; r < 4; r++) Z.t[a][r] *= b.t[a][r];
-            vrows.turn(scratch, Z);
+                for (int e = 0; e < 4; e++) Z.t[a][e] *= b.t[a][e];
+            rows.turn(scratch, Z);
+            rows.write(dv, r < w.rows - i * kCut, c, A.dv, A.ovec);
         }
     }
     if (SUM) {
         state_write<KT>(E, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         return;
     }
-    if (chunks) leave(0);
     if (w.first && A.dstate) state_write<KT>(E, A.dstate + w.matrix * A.dk * A.dv, A.dk, A.dv, col);
 }
 
@@ -1196,7 +1215,7 @@ struct GradLds {
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk, all of them the
 // products of rows with rows, the first dgate and dbeta.
 template <typename T, int KT>
-__global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
+__global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT, R = Lds<T>::R;
     typedef GradLds<T, KT> L;
@@ -1706,12 +1725,14 @@ void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool
     else delta_launch(delta_prepare<T, KT, false>, all, 64, 0, A, st);
     if (!walks) return;
     if (A.cut) {
-        delta_launch(delta_scan<T, KT, false, true>, walk, 64 * (A.slices + 2 * KT), stages, A, st);
+        // wavefronts enough for either kind
+        const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
+        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * (most + 1), stages, A, st);
         delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, join, A, st);
     }
     const int lds = stages + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
-    if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices, lds, A, st);
-    else delta_launch(delta_scan<T, KT, false, false>, walk, 64 * A.slices, lds, A, st);
+    if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices + 64, lds, A, st);
+    else delta_launch(delta_scan<T, KT, false, false>, walk, 64 * A.slices + 64, lds, A, st);
 }
 
 template <typename T, int KT>
@@ -1720,10 +1741,10 @@ void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, boo
     const dim3 walk((unsigned)walks);
     const int stages = 2 * BackLds<T, KT>::size(A.slices), join = 2 * KT * KT * 4096;
     if (walks && A.cut) {
-        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices, stages, A, st);
+        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, stages, A, st);
         delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, join, A, st);
     }
-    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices, stages + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
+    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64, stages + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
     delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
 }
 
