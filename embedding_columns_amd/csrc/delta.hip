@@ -1100,49 +1100,56 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 
 // The states at the edges of a cut sample's segments, one after another: S' = move S + added
 // (BACK: from the last, with the move transposed).  A wavefront has 16 columns of a sample's
-// and head's state; the moves arrive in LDS one ahead.  What a segment adds is replaced by the
-// state that it begins with.
+// and head's state, the last brings the moves one ahead.  What a segment adds is replaced by
+// the state that it begins with.
 template <int KT, bool BACK>
-__global__ __launch_bounds__(512) void delta_join(DeltaArgs A)
+__global__ __launch_bounds__(576) void delta_join(DeltaArgs A)
 {
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     constexpr int stage = KT * KT * 4096;
     const int sample = blockIdx.x / (uint32_t)A.heads, head = blockIdx.x - (uint32_t)sample * (uint32_t)A.heads;
-    const int l = lane_id(), g = l >> 4, slice = uniform((int)(threadIdx.x >> 6)), waves = uniform((int)(blockDim.x >> 6));
-    const int col = 16 * slice + (l & 15);
+    const int l = lane_id(), g = l >> 4, slice = uniform((int)(threadIdx.x >> 6)), col = 16 * slice + (l & 15);
     const int base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
     const int rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - base, 0);
     const int parts = (rows + kSpan - 1) / kSpan, part0 = base / kSpan + sample + 1;
     const int64_t matrix = (int64_t)sample * A.heads + head;
     const uint32_t at0 = lds_address(lds);
-    const float *from = BACK ? A.dlast : A.state;
-    Block S[KT], next[KT];
-    state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, col);
     auto number = [&](int j) { return (int64_t)(part0 + (BACK ? parts - 1 - j : j)) * A.heads + head; };
-    // a KB holds 4 of every 8 columns of 32 x .. of the 16 rows of a register block, a row a lane & 15
-    auto bring = [&](int j) {
-        const i32x4_t rsrc = row_rsrc(A.moves + number(j) * A.move_size + (BACK ? 1024 * KT * KT : 0));
+    if (slice == A.slices) {
+        // a KB holds 4 of every 8 columns of 32 x .. of the 16 rows of a register block, a row a lane & 15
         const uint32_t mine = (uint32_t)((8 * ((l & 15) >> 2) + (l & 3)) * 32 * KT + 8 * g) * 4;
-#pragma unroll 1
-        for (int p = slice; p < stage / 1024; p += waves) {
-            const int c = p & 1, x = (p >> 1) % KT, a = (p >> 1) / KT & 1, y = (p >> 1) / (2 * KT);   // row block y, half a
-            load_to_lds(rsrc, at0 + (j & 1) * stage + p * 1024, mine, ((32 * y + 4 * a) * 32 * KT + 32 * x + 4 * c) * 4);
+        auto bring = [&](int j) {
+            const i32x4_t rsrc = row_rsrc(A.moves + number(j) * A.move_size + (BACK ? 1024 * KT * KT : 0));
+#pragma unroll
+            for (int p = 0; p < stage / 1024; p++) {
+                const int c = p & 1, x = (p >> 1) % KT, a = (p >> 1) / KT & 1, y = (p >> 1) / (2 * KT);   // row block y, half a
+                load_to_lds(rsrc, at0 + (j & 1) * stage + p * 1024, mine, ((32 * y + 4 * a) * 32 * KT + 32 * x + 4 * c) * 4);
+            }
+        };
+        if (parts > 1) bring(0);
+        for (int j = 0; j + 1 < parts; j++) {
+            meet();
+            if (j + 2 < parts) bring(j + 1);
         }
-    };
-    if (parts) bring(0);
+        return;
+    }
+    const float *from = BACK ? A.dlast : A.state;
+    Block S[KT], added[KT];
+    state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, col);
+    if (parts) state_read<KT>(added, A.starts + number(0) * A.dk * A.dv, A.dk, A.dv, col);
     for (int j = 0; j < parts; j++) {
-        float *added = A.starts + number(j) * A.dk * A.dv;
-        meet();
-        if (j + 1 < parts) bring(j + 1);
-        state_read<KT>(next, added, A.dk, A.dv, col);
-        state_write<KT>(S, added, A.dk, A.dv, col);
+        if (j + 1 < parts) meet_others();
+        state_write<KT>(S, A.starts + number(j) * A.dk * A.dv, A.dk, A.dv, col);
         if (j + 1 == parts) break;
         const uint32_t at = at0 + (j & 1) * stage + 16 * l;
         Part<3> sp[KT];
 #pragma unroll
         for (int x = 0; x < KT; x++) sp[x] = operand<3>(S[x]);
 #pragma unroll
-        for (int y = 0; y < KT; y++)
+        for (int y = 0; y < KT; y++) S[y] = added[y];
+        state_read<KT>(added, A.starts + number(j + 1) * A.dk * A.dv, A.dk, A.dv, col);
+#pragma unroll
+        for (int y = 0; y < KT; y++) {
 #pragma unroll
             for (int a = 0; a < 2; a++)
 #pragma unroll
@@ -1155,10 +1162,9 @@ __global__ __launch_bounds__(512) void delta_join(DeltaArgs A)
                         f[e] = __uint_as_float(lo[e]);
                         f[4 + e] = __uint_as_float(hi[e]);
                     }
-                    mm<3>(next[y].t[a], split8<3>(f), sp[x]);
+                    mm<3>(S[y].t[a], split8<3>(f), sp[x]);
                 }
-#pragma unroll
-        for (int x = 0; x < KT; x++) S[x] = next[x];
+        }
     }
     if (parts) return;                                   // a sample without rows hands its state on
     float *to = BACK ? A.dstate : A.last;
@@ -1167,60 +1173,47 @@ __global__ __launch_bounds__(512) void delta_join(DeltaArgs A)
 
 // ----------------------------------------------------------------- gradients
 
-__device__ __forceinline__ float parts_dot(const Part<1> &a, const Part<1> &b)
-{
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        s += bf16_lo(a.p[0][j]) * bf16_lo(b.p[0][j]) + bf16_hi(a.p[0][j]) * bf16_hi(b.p[0][j]);
-    return s;
-}
-__device__ __forceinline__ float parts_dot(const Part<3> &a, const Part<3> &b)
-{
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-        s += (bf16_lo(a.p[0][j]) + bf16_lo(a.p[1][j]) + bf16_lo(a.p[2][j])) *
-             (bf16_lo(b.p[0][j]) + bf16_lo(b.p[1][j]) + bf16_lo(b.p[2][j]));
-        s += (bf16_hi(a.p[0][j]) + bf16_hi(a.p[1][j]) + bf16_hi(a.p[2][j])) *
-             (bf16_hi(b.p[0][j]) + bf16_hi(b.p[1][j]) + bf16_hi(b.p[2][j]));
-    }
-    return s;
-}
+constexpr int kKeptMost = kDeltaDim / 16;
 
-// rows kept as operands, from memory
+// 32 rows x 16 elements kept as an operand in memory
 template <typename T>
-__device__ __forceinline__ typename Row<T>::Op kept_operand(const char *at, int x)
-{
-    const u32x4_t *p = reinterpret_cast<const u32x4_t *>(at + x * Lds<T>::kRows) + lane_id();
-    if constexpr (Lds<T>::R == 1) return typename Row<T>::Op{{*gp(p)}};
-    else {
-        float f[8];
-        const u32x4_t a = *gp(p), b = *gp(p + 64);
+struct Kept {
+    u32x4_t w[Lds<T>::R];
+
+    __device__ __forceinline__ void load(const char *at, int x)
+    {
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f[j] = __uint_as_float(a[j]);
-            f[4 + j] = __uint_as_float(b[j]);
-        }
-        return split8<3>(f);
+        for (int j = 0; j < Lds<T>::R; j++)
+            w[j] = *gp(reinterpret_cast<const u32x4_t *>(at + x * Lds<T>::kRows + j * 1024) + lane_id());
     }
-}
+    __device__ __forceinline__ typename Row<T>::Op operand() const
+    {
+        if constexpr (Lds<T>::R == 1) return typename Row<T>::Op{{w[0]}};
+        else {
+            float f[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) f[j] = __uint_as_float(w[j >> 2][j & 3]);
+            return split8<3>(f);
+        }
+    }
+};
 
 template <typename T, int KT>
 struct GradLds {
-    static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, u = sc + 1024;
+    static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, with = sc + 1024, u = with + 6 * Prec<T>::OUT * 1024;
     static __host__ __device__ int size(int slices) { return u + 3 * slices * Lds<T>::kRows; }
 };
 
-// One chunk and key head: wavefront w makes columns 32 w .. of dq and dk, all of them the
-// products of rows with rows, the first dgate and dbeta.
+// One chunk and key head: wavefront w makes columns 32 w .. of dq and dk.  What rows of K and Q
+// are taken with, D, D^T and B + B^T, is made by a wavefront each and handed over in LDS; the
+// first makes dgate and dbeta.
 template <typename T, int KT>
-__global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
+__global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT, R = Lds<T>::R;
     typedef GradLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
-    __shared__ float red[KT][3][32];
+    __shared__ float red[KT][3][32], cross[3][32], owns[32];
     const int tile = blockIdx.x, key = blockIdx.y;
     const int wave = uniform((int)(threadIdx.x >> 6)), l = lane_id(), c = l & 31, h = l >> 5;
     const SegTile s = seg_find<kCut>(A.off, A.n, nullptr, 0, A.samples, 1, tile);
@@ -1261,76 +1254,112 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
     bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + key * A.kh), row_at<T>(kept, A.ks), at, 2 * KT, wave, KT);
     bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + key * A.qh), row_at<T>(kept, A.qs), at + L::q, 2 * KT, wave, KT);
     bring(key * A.group);
-    meet();
-    f32x16_t kk = zero16(), kq = zero16(), qk = zero16();
-#pragma unroll
-    for (int x = 0; x < 2 * KT; x++) {
-        const auto K = Lds<T>::rows(at, x), Q = Lds<T>::rows(at + L::q, x);
-        mm<IN>(kk, K, K);
-        mm<IN>(kq, K, Q);
-        mm<IN>(qk, Q, K);
-    }
     f32x16_t dq = zero16(), dk = zero16();               // transposed: a row a lane
     for (int g = 0; g < A.group; g++) {
         const int head = key * A.group + g;
         if (g) {
             __syncthreads();                             // the head before is read
             bring(head);
-            meet();
         }
         const int64_t number = (int64_t)tile * A.heads + head, n = A.slices;
         const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<T>::kRows;
         const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<T>::kRows;
         const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * Lds<T>::kRows, oat = zat + n * Lds<T>::kRows;
-        f32x16_t t1 = zero16(), t2 = zero16(), t3 = zero16();
-        f32x16_t ud = zero16(), du = zero16(), uz = zero16(), zu = zero16();
-        float inner = 0.f;
-        for (int x = 0; x < n; x++) {
-            const auto S = kept_operand<T>(S0, x), E = kept_operand<T>(E0, x);
-            const auto U = Lds<T>::rows(uat, x), Z = Lds<T>::rows(zat, x), D = Lds<T>::rows(oat, x);
-            mm<IN>(ud, U, D);                            // u_j.dO_i, lane i
-            mm<IN>(du, D, U);                            // dO_i.u_j, lane j
-            mm<IN>(uz, U, Z);
-            mm<IN>(zu, Z, U);
-            mm<IN>(t1, S, D);
-            mm<IN>(t2, S, Z);
-            mm<IN>(t3, E, U);
-            inner += parts_dot(S, E);
-        }
+        // the states' rows are on their way while the chunk's own products are made
+        Kept<T> S[kKeptMost], E[kKeptMost];
+#pragma unroll
+        for (int x = 0; x < kKeptMost; x++)
+            if (x < n) {
+                S[x].load(S0, x);
+                E[x].load(E0, x);
+            }
+        meet();
         const float b = lds_read<float>(sc + 4 * (kScB + c)), bg = lds_read<float>(sc + 4 * (kScBG + c)),
                     sg = lds_read<float>(sc + 4 * (kScG + c)), wt = lds_read<float>(sc + 4 * (kScW + c)),
                     hi = lds_read<float>(sc + 4 * (kScHi + c)), lo = lds_read<float>(sc + 4 * (kScLo + c)),
                     end = lds_read<float>(sc + 4 * kScEnd);
-        // lane x: what k_y (or q_y) is taken with, in register y
-        f32x16_t forq, fork, fromq;
-        float across = 0.f, own = 0.f;                   // row sum of H less column sum; z.u of the row
+        // lane x: what k_y (or q_y) is taken with, in register y; `across`: the lane's row or
+        // column sum of H
 #pragma unroll
-        for (int g4 = 0; g4 < 4; g4++) {
-            const int y0 = 8 * g4 + 4 * h;
-            const f32x4_t yhi = lds_read<f32x4_t>(sc + 4 * (kScHi + y0)), ylo = lds_read<f32x4_t>(sc + 4 * (kScLo + y0)),
-                          yb = lds_read<f32x4_t>(sc + 4 * (kScB + y0));
+        for (int what = 0; what < 3; what++) {
+            if (what % KT != wave) continue;
+            f32x16_t p = zero16(), p2 = zero16(), k = zero16(), f;
+            for (int x = 0; x < n; x++) {
+                const auto U = Lds<T>::rows(uat, x), Z = Lds<T>::rows(what == 2 ? zat : oat, x);
+                if (what != 1) mm<IN>(p, U, Z);          // u_j.dO_i (or Z_i), lane i
+                if (what != 0) mm<IN>(what == 1 ? p : p2, Z, U);   // dO_i (or Z_i).u_j, lane j
+            }
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int y = y0 + e, r = 4 * g4 + e;
-                const bool before = y < c, after = y > c;
-                const float d = exp_of(before ? hi - yhi[e] : yhi[e] - hi, before ? lo - ylo[e] : ylo[e] - lo);
-                const float D = y <= c ? A.scale * d * ud[r] : 0.f;        // D_xy
-                const float DT = y >= c ? A.scale * d * du[r] : 0.f;       // D_yx
-                const float B = before ? -b * d * uz[r] : after ? -yb[e] * d * zu[r] : 0.f;   // B_xy or B_yx
-                forq[r] = D;
-                fromq[r] = DT;
-                fork[r] = B;
-                if (y == c) own += uz[r];
-                across += before ? fmaf(D, kq[r], B * kk[r]) : after ? -fmaf(DT, qk[r], B * kk[r]) : 0.f;
+            for (int x = 0; x < 2 * KT; x++) {
+                const auto K = Lds<T>::rows(at, x);
+                if (what == 2) mm<IN>(k, K, K);
+                else {
+                    const auto Q = Lds<T>::rows(at + L::q, x);
+                    if (what == 0) mm<IN>(k, K, Q);
+                    else mm<IN>(k, Q, K);
+                }
+            }
+            float across = 0.f, own = 0.f;               // own: z.u of the row
+#pragma unroll
+            for (int g4 = 0; g4 < 4; g4++) {
+                const int y0 = 8 * g4 + 4 * h;
+                const f32x4_t yhi = lds_read<f32x4_t>(sc + 4 * (kScHi + y0)), ylo = lds_read<f32x4_t>(sc + 4 * (kScLo + y0)),
+                              yb = lds_read<f32x4_t>(sc + 4 * (kScB + y0));
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int y = y0 + e, r = 4 * g4 + e;
+                    const bool before = y < c, after = y > c;
+                    const float dhi = hi - yhi[e], dlo = lo - ylo[e];
+                    if (what == 0) {                     // D_xy
+                        f[r] = !after ? A.scale * exp_of(dhi, dlo) * p[r] : 0.f;
+                        across += before ? f[r] * k[r] : 0.f;
+                    } else if (what == 1) {              // D_yx
+                        f[r] = !before ? A.scale * exp_of(-dhi, -dlo) * p[r] : 0.f;
+                        across -= after ? f[r] * k[r] : 0.f;
+                    } else {                             // B_xy or B_yx
+                        const float d = exp_of(before ? dhi : -dhi, before ? dlo : -dlo);
+                        f[r] = before ? -b * d * p[r] : after ? -yb[e] * d * p2[r] : 0.f;
+                        across += before ? f[r] * k[r] : -f[r] * k[r];
+                        if (y == c) own += p[r];
+                    }
+                }
+            }
+#pragma unroll
+            for (int kc = 0; kc < 2; kc++) {
+                const Part<OUT> o = operand<OUT>(f, kc);
+#pragma unroll
+                for (int i = 0; i < OUT; i++)
+                    lds_write(at + L::with + ((what * 2 + kc) * OUT + i) * 1024 + 16 * l, o.p[i]);
+            }
+            across = both(across);
+            if (h == 0) cross[what][c] = across;
+            if (what == 2) {
+                own = both(own);
+                if (h == 0) owns[c] = own;
             }
         }
+        __syncthreads();
 #pragma unroll
         for (int kc = 0; kc < 2; kc++) {
             const auto kt = Lds<T>::turned(at, columns, wave, kc), qt = Lds<T>::turned(at + L::q, columns, wave, kc);
-            mm<OUT>(dq, kt, operand<OUT>(forq, kc));
-            mm<OUT>(dk, kt, operand<OUT>(fork, kc));
-            mm<OUT>(dk, qt, operand<OUT>(fromq, kc));
+            mm<OUT>(dq, kt, staged<OUT>(at + L::with, kc));
+            mm<OUT>(dk, kt, staged<OUT>(at + L::with, 4 + kc));
+            mm<OUT>(dk, qt, staged<OUT>(at + L::with, 2 + kc));
         }
+        // with the states: rows of S and E by rows of dO, Z and U, and the rows' own products of S and E
+        f32x16_t t1 = zero16(), t2 = zero16(), t3 = zero16(), se = zero16();
+#pragma unroll
+        for (int x = 0; x < kKeptMost; x++)
+            if (x < n) {
+                const auto s0 = S[x].operand(), e0 = E[x].operand();
+                mm<IN>(t1, s0, Lds<T>::rows(oat, x));
+                mm<IN>(t2, s0, Lds<T>::rows(zat, x));
+                mm<IN>(t3, e0, Lds<T>::rows(uat, x));
+                mm<IN>(se, s0, e0);
+            }
+        float inner = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; i++) inner += kk0(i) + 4 * h == c ? se[i] : 0.f;
         // the row's own elements 32 wave + kk(i, h), which meet its sums with the states
         float dots = 0.f, writes = 0.f;
 #pragma unroll
@@ -1360,7 +1389,7 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
         }
         __syncthreads();
         if (wave == 0) {
-            float from = both(across), into = 0.f, state = 0.f;
+            float from = cross[0][c] + cross[1][c] + cross[2][c], into = 0.f, state = 0.f;
 #pragma unroll
             for (int w = 0; w < KT; w++) {
                 from += red[w][0][c];
@@ -1376,7 +1405,6 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
             }
             prefix = __shfl_up(prefix, 1, 32);           // of the rows before this one
             if (c == 0) prefix = 0.f;
-            own = both(own);
             if (valid && h == 0) {
                 float dg = 0.f, db = 0.f;
                 if (keep) {
@@ -1384,7 +1412,7 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
                     const float beta = Row<T>::get1(static_cast<const T *>(A.beta) + (row + c) * A.bs + head);
                     // a gate that forgets all has none, whatever the sums' rounding leaves
                     dg = expf(-gate) == INFINITY ? 0.f : (suffix + prefix + end * state) / (1.f + expf(gate));
-                    db = own / (1.f + expf(beta));
+                    db = owns[c] / (1.f + expf(beta));
                 }
                 Row<T>::put1(static_cast<T *>(A.dgate) + (row + c) * A.heads + head, dg);
                 Row<T>::put1(static_cast<T *>(A.dbeta) + (row + c) * A.heads + head, db);
@@ -1728,7 +1756,7 @@ void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool
         // wavefronts enough for either kind
         const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
         delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * (most + 1), stages, A, st);
-        delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, join, A, st);
+        delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
     }
     const int lds = stages + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
     if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices + 64, lds, A, st);
@@ -1742,7 +1770,7 @@ void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, boo
     const int stages = 2 * BackLds<T, KT>::size(A.slices), join = 2 * KT * KT * 4096;
     if (walks && A.cut) {
         delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, stages, A, st);
-        delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices, join, A, st);
+        delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
     }
     if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64, stages + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
     delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
