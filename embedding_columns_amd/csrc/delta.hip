@@ -63,7 +63,7 @@ struct DeltaArgs {
     const float *state;
     int32_t n, samples, key_heads, heads, group, dk, dv, slices;
     float scale;
-    char *rec;                 // records of (tile, head): N, P, scalars (and N^T, P^T)
+    char *rec;                 // records of (tile, head): N, P, scalars
     int64_t rec_size;
     void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
     int32_t cut;               // samples are cut into segments
@@ -82,16 +82,16 @@ struct DeltaArgs {
     int32_t vec, ovec;         // dq and dk rows move in pieces of 4; o and dv rows in 16 bytes
 };
 
-// parts of the inputs, of what makes the states, and of what makes outputs alone
+// parts of the inputs, of what makes the states, of what makes outputs alone, and of N - I
 template <typename T>
 struct Prec;
 template <>
 struct Prec<uint16_t> {
-    static constexpr int IN = 1, ST = 3, OUT = 2;
+    static constexpr int IN = 1, ST = 3, OUT = 2, NN = 3;
 };
 template <>
 struct Prec<float> {
-    static constexpr int IN = 3, ST = 3, OUT = 3;
+    static constexpr int IN = 3, ST = 3, OUT = 3, NN = 3;
 };
 
 __device__ __forceinline__ constexpr int kk0(int i) { return 8 * (i >> 2) + (i & 3); }   // + 4 h
@@ -236,22 +236,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
     return row_buffer(static_cast<const T *>(p) + elements, 0, 0x7FFFFFFF);
 }
 
-// Operands in memory as the lanes take them: 64 x 16 bytes a part.
-template <int N>
-__device__ __forceinline__ void store_frag(char *at, int index, const Part<N> &f)
-{
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        *gp(reinterpret_cast<u32x4_t *>(at) + (index * N + i) * 64 + lane_id()) = f.p[i];
-}
-
-// Where the pieces of a record lie: N, N^T and P^T of ST parts, P (which the state never
-// meets) of OUT, the scalars.
+// A record: N - I in NN parts, P in OUT, the scalars.  A part is 16 rows x 32 columns a KB, a
+// row's 4 pieces of 16 bytes side by side, piece g (columns 4 g .. and 16 + 4 g ..) of row r at
+// g ^ (r >> 2); see Lane.
 template <typename T>
 struct Rec {
-    static constexpr int kN = 2 * Prec<T>::ST * 1024, kP = 2 * Prec<T>::OUT * 1024;
-    static constexpr int n = 0, p = kN, sc = kN + kP, nt = sc + kScalars * 4, pt = nt + kN;
-    static constexpr int small = nt, whole = pt + kN;
+    static constexpr int n = 0, p = 2 * Prec<T>::NN * 1024, sc = p + 2 * Prec<T>::OUT * 1024, size = sc + kScalars * 4;
 };
 
 // e^(hi + lo): the product with log2(e) to more bits than one rounding
@@ -274,10 +264,10 @@ __device__ __forceinline__ int first_tile(int base, int sample) { return base / 
 
 // ----------------------------------------------------------------- prepare
 
-template <typename T, int KT, bool TRAIN>
+template <typename T, int KT>
 __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT;
+    constexpr int IN = Prec<T>::IN, NN = Prec<T>::NN, OUT = Prec<T>::OUT;
     constexpr int kPitch = 36;
     __shared__ __attribute__((aligned(16))) float lds[32 * kPitch];
     __shared__ __attribute__((aligned(16))) float sc[kScalars];
@@ -340,7 +330,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         mm<IN>(kk, K, K);
         mm<IN>(kq, K, Q);                                      // k_j.q_i, lane i
     }
-    // P and M as rows of i, in LDS; from there as first operands, and transposed
+    // P and M as rows of i, in LDS, and from there into the record
     float m[16];
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++) {
@@ -357,7 +347,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         }
         *reinterpret_cast<f32x4_t *>(lds + c * kPitch + j0) = p;
     }
-    auto leave = [&](auto parts, int at, int back) {     // the matrix in LDS into the record
+    auto leave = [&](auto parts, int at) {               // the matrix in LDS into the record
         constexpr int N = decltype(parts)::value;
         const int row = l & 15, g = l >> 4;
 #pragma unroll
@@ -369,16 +359,14 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 #pragma unroll
                 for (int i = 0; i < 4; i++) f[e + i] = x[i];
             }
-            store_frag<N>(rec + at, a, split8<N>(f));
-            if (TRAIN) {
+            const Part<N> p = split8<N>(f);
 #pragma unroll
-                for (int e = 0; e < 8; e++) f[e] = lds[(16 * (e >> 2) + 4 * g + (e & 3)) * kPitch + 16 * a + row];
-                store_frag<ST>(rec + back, a, split8<ST>(f));
-            }
+            for (int i = 0; i < N; i++)
+                *gp(reinterpret_cast<u32x4_t *>(rec + at + (2 * i + a) * 1024) + (row * 4 + (g ^ (row >> 2)))) = p.p[i];
         }
     };
     wave_sync();
-    leave(std::integral_constant<int, OUT>{}, Rec<T>::p, Rec<T>::pt);
+    leave(std::integral_constant<int, OUT>{}, Rec<T>::p);
     wave_sync();
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++)
@@ -401,9 +389,9 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     }
     wave_sync();
 #pragma unroll
-    for (int i = 0; i < 16; i++) lds[(16 * h + i) * kPitch + c] = h ? nn[16 + i] : nn[i];
+    for (int i = 0; i < 16; i++) lds[(16 * h + i) * kPitch + c] = 16 * h + i == c ? 0.f : h ? nn[16 + i] : nn[i];
     wave_sync();
-    leave(std::integral_constant<int, ST>{}, Rec<T>::n, Rec<T>::nt);
+    leave(std::integral_constant<int, NN>{}, Rec<T>::n);
 }
 
 // ------------------------------------------------------------ chunks in LDS
@@ -502,7 +490,8 @@ __device__ __forceinline__ void bring_rows(i32x4_t rsrc, uint32_t at, uint32_t t
 __device__ __forceinline__ void bring_flat(i32x4_t rsrc, uint32_t to, int pieces, int wave, int waves)
 {
 #pragma unroll 1
-    for (int p = wave; p < pieces; p += waves) load_to_lds(rsrc, to + p * 1024, 16 * lane_id(), p * 1024);
+    for (int p = wave; p < pieces; p += waves)
+        load_to_lds(rsrc, (uint32_t)uniform((int)(to + p * 1024)), 16 * lane_id(), (uint32_t)uniform(p * 1024));
 }
 
 // the operand of a record in LDS
@@ -537,6 +526,7 @@ template <typename T>
 struct Lane {
     static constexpr int R = sizeof(T) / 2, kTile = 1024 * R;      // bytes of 16 rows x 32 elements
     uint32_t rows, keys;     // where the lane's first operands begin: rows, and columns for the state's update
+    uint32_t turned;         // ... and columns of a record's matrix
     int r, q;                // (bf16) its row and quad of a column
 
     __device__ __forceinline__ Lane()
@@ -547,7 +537,8 @@ struct Lane {
         q = i & 3;
         // State rows are kept so that the registers of a block meet rows of K and Q as they lie in
         // memory: t[a][i] of quarter g is row 8 g + 4 a + i.
-        if (R == 1) keys = (r * 4 + (q ^ g)) * 16;
+        turned = (r * 4 + (q ^ g)) * 16;
+        if (R == 1) keys = turned;
         else keys = (16 * g + ((i >> 2) ^ g)) * 16 + (i & 3) * 4;
     }
     // rows 16 a + lane & 15, elements 32 x + 8 g + 0 .. 7
@@ -586,6 +577,30 @@ struct Lane {
             for (int e = 0; e < 8; e++) f[e] = lds_read<float>(at + keys + (x * 2 + (e >> 2)) * kTile + a * 1024 + (e & 3) * 64);
             return split8<3>(f);
         }
+    }
+    // rows 16 a .. of a record's matrix as an operand, and columns 16 a ..
+    template <int N>
+    __device__ __forceinline__ Part<N> matrix(uint32_t at, int a) const
+    {
+        Part<N> p;
+#pragma unroll
+        for (int i = 0; i < N; i++) p.p[i] = lds_read<u32x4_t>(at + rows + (2 * i + a) * 1024);
+        return p;
+    }
+    template <int N>
+    __device__ __forceinline__ Part<N> matrix_turned(uint32_t at, int a) const
+    {
+        Part<N> p;
+#pragma unroll
+        for (int i = 0; i < N; i++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + turned + (2 * i + j) * 1024 + 8 * a)));
+                p.p[i][2 * j] = v[0];
+                p.p[i][2 * j + 1] = v[1];
+            }
+        return p;
     }
     // where columns 16 slice .. begin, and these as a block
     __device__ __forceinline__ uint32_t columns(int slice) const
@@ -817,14 +832,15 @@ __device__ __forceinline__ void state_keep(uint32_t scratch, char *to, int slice
 
 // What a walk has of a chunk in LDS, and its last wavefront, which brings the chunks one ahead
 // and does nothing else.  SUM: no Q, no P, and V for the values alone.
-template <typename T, int KT>
+template <typename T, int KT, bool SUM>
 struct ScanLds {
-    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = 2 * q, v = rec + Rec<T>::small;
+    static constexpr int q = 2 * KT * Lane<T>::kTile, n = SUM ? q : 2 * q, p = n + Rec<T>::p, sc = SUM ? p : n + Rec<T>::sc,
+                         v = sc + kScalars * 4;
     static __host__ __device__ int size(int slices) { return v + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 template <typename T, int KT>
 struct BackLds {
-    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = 2 * q, o = rec + Rec<T>::whole - Rec<T>::sc;
+    static constexpr int q = 2 * KT * Lane<T>::kTile, n = 2 * q, p = n + Rec<T>::p, sc = n + Rec<T>::sc, o = sc + kScalars * 4;
     static __host__ __device__ int size(int slices) { return o + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 
@@ -841,7 +857,7 @@ __device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w,
 template <typename T, int KT, bool SUM>
 __device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, bool values)
 {
-    typedef ScanLds<T, KT> L;
+    typedef ScanLds<T, KT, SUM> L;
     const int64_t row = (int64_t)w.base + chunk * kCut;
     const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
     bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
@@ -849,9 +865,8 @@ __device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, in
     if (values) bring_tiles<T>(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh, A.vs, kept, to + L::v, (A.slices + 1) / 2);
     const i32x4_t rsrc = row_rsrc(rec);
 #pragma unroll
-    for (int p = 0; p < Rec<T>::small / 1024; p++)
-        if (!SUM || p * 1024 < Rec<T>::p || p * 1024 >= Rec<T>::sc)
-            load_to_lds(rsrc, to + L::rec + p * 1024, 16 * lane_id(), p * 1024);
+    for (int p = 0; p < (SUM ? Rec<T>::p : Rec<T>::size); p += 1024) load_to_lds(rsrc, to + L::n + p, 16 * lane_id(), p);
+    if (SUM) load_to_lds(rsrc, to + L::sc, 16 * lane_id(), Rec<T>::sc);
 }
 
 template <typename T, int KT>
@@ -863,10 +878,18 @@ __device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, in
     bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
     bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT);
     bring_tiles<T>(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh, A.ds, kept, to + L::o, (A.slices + 1) / 2);
-    const i32x4_t rsrc = row_rsrc(rec + Rec<T>::sc);
+    const i32x4_t rsrc = row_rsrc(rec);
 #pragma unroll
-    for (int p = 0; p < (Rec<T>::whole - Rec<T>::sc) / 1024; p++)
-        load_to_lds(rsrc, to + L::rec + p * 1024, 16 * lane_id(), p * 1024);
+    for (int p = 0; p < Rec<T>::size; p += 1024) load_to_lds(rsrc, to + L::n + p, 16 * lane_id(), p);
+}
+
+// Where element (row, col) of a segment's matrix lies, in floats: KBs of 16 rows (one block of
+// registers of a state) x every second 4 of 32 columns, first operands of delta_join.
+template <int KT>
+__device__ __forceinline__ int move_at(int row, int col)
+{
+    const int y = row >> 5, a = row >> 2 & 1, m = (row >> 3 & 3) * 4 + (row & 3), x = col >> 5, g = col >> 3 & 3, c = col >> 2 & 1;
+    return (((y * 2 + a) * KT + x) * 2 + c) * 256 + (g * 16 + m) * 4 + (col & 3);
 }
 
 // Walks forward.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
@@ -874,8 +897,8 @@ __device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, in
 template <typename T, int KT, bool TRAIN, bool SUM>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
-    constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT;
-    typedef ScanLds<T, KT> L;
+    constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
+    typedef ScanLds<T, KT, SUM> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
@@ -918,8 +941,8 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
     for (int i = 0; i < chunks; i++) {
         const uint32_t at = at0 + (i & 1) * stage;
         meet_others();
-        const uint32_t sc = at + L::rec + Rec<T>::sc;
-        Block X = zero_block(), Y = zero_block(), U = zero_block(), V = zero_block();
+        const uint32_t sc = at + L::sc;
+        Block X = zero_block(), Y = zero_block(), V = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<ST> sp = operand<ST>(S[x]);
@@ -937,8 +960,9 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 #pragma unroll
             for (int e = 0; e < 4; e++) X.t[a][e] = fmaf(b.t[a][e], V.t[a][e], -bg.t[a][e] * X.t[a][e]);
         const Part<ST> xp = operand<ST>(X);
+        Block U = X;                                     // N is I and what the record has
 #pragma unroll
-        for (int a = 0; a < 2; a++) mm<ST>(U.t[a], staged<ST>(at + L::rec + Rec<T>::n, a), xp);
+        for (int a = 0; a < 2; a++) mm<ST>(U.t[a], lane.template matrix<NN>(at + L::n, a), xp);
         const Block wt = row_scalars(sc + 4 * kScW);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block wu = U;
@@ -963,7 +987,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
             for (int a = 0; a < 2; a++) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) Y.t[a][e] *= sg.t[a][e];
-                mm<OUT>(Y.t[a], staged<OUT>(at + L::rec + Rec<T>::p, a), op);
+                mm<OUT>(Y.t[a], lane.template matrix<OUT>(at + L::p, a), op);
             }
             Turn<T> rows;
             if (TRAIN) {
@@ -980,15 +1004,19 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
     if (SUM) {
         if (values) state_write<KT>(S, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         else {
-            // the matrix in rows, and, for the backward, in columns
+            // the matrix, and for the backward its transpose, as delta_join takes them
             float *to = A.moves + w.part * A.move_size;
-            state_write<KT>(S, to, 32 * KT, 32 * KT, col);
+            const int g = l >> 4;
+#pragma unroll
+            for (int x = 0; x < KT; x++)
+#pragma unroll
+                for (int i = 0; i < 8; i++) *gp(to + move_at<KT>(32 * x + 8 * g + i, col)) = S[x].t[i >> 2][i & 3];
             if (A.moves_back)
 #pragma unroll
                 for (int x = 0; x < KT; x++)
 #pragma unroll
                     for (int a = 0; a < 2; a++)
-                        *gp(reinterpret_cast<f32x4_t *>(to + 1024 * KT * KT + col * 32 * KT + 32 * x + 8 * (l >> 4) + 4 * a)) = S[x].t[a];
+                        *gp(reinterpret_cast<f32x4_t *>(to + 1024 * KT * KT + move_at<KT>(col, 32 * x + 8 * g + 4 * a))) = S[x].t[a];
         }
         return;
     }
@@ -999,7 +1027,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 template <typename T, int KT, bool SUM>
 __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST;
+    constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
     typedef BackLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
@@ -1036,8 +1064,8 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
         dv -= vstep;
         z -= zstep;
         states -= KT * zstep;
-        const uint32_t sc = at + L::rec, rec = at + L::rec - Rec<T>::sc;
-        Block X = zero_block(), Z = zero_block();
+        const uint32_t sc = at + L::sc;
+        Block X = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<ST> ep = operand<ST>(E[x]);
@@ -1052,11 +1080,12 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
         for (int a = 0; a < 2; a++) {
 #pragma unroll
             for (int e = 0; e < 4; e++) X.t[a][e] *= wt.t[a][e];
-            mm<ST>(X.t[a], staged<ST>(rec + Rec<T>::pt, a), dp);
+            mm<ST>(X.t[a], lane.template matrix_turned<OUT>(at + L::p, a), dp);
         }
         const Part<ST> xp = operand<ST>(X);
+        Block Z = X;
 #pragma unroll
-        for (int a = 0; a < 2; a++) mm<ST>(Z.t[a], staged<ST>(rec + Rec<T>::nt, a), xp);
+        for (int a = 0; a < 2; a++) mm<ST>(Z.t[a], lane.template matrix_turned<NN>(at + L::n, a), xp);
         const Block bg = row_scalars(sc + 4 * kScBG), sg = row_scalars(sc + 4 * kScG);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block gz = Z;
@@ -1108,7 +1137,8 @@ __global__ __launch_bounds__(576) void delta_join(DeltaArgs A)
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     constexpr int stage = KT * KT * 4096;
     const int sample = blockIdx.x / (uint32_t)A.heads, head = blockIdx.x - (uint32_t)sample * (uint32_t)A.heads;
-    const int l = lane_id(), g = l >> 4, slice = uniform((int)(threadIdx.x >> 6)), col = 16 * slice + (l & 15);
+    constexpr int back = BACK ? 1024 * KT * KT : 0;      // the transposed matrices lie behind the others
+    const int l = lane_id(), slice = uniform((int)(threadIdx.x >> 6)), col = 16 * slice + (l & 15);
     const int base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
     const int rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - base, 0);
     const int parts = (rows + kSpan - 1) / kSpan, part0 = base / kSpan + sample + 1;
@@ -1116,44 +1146,33 @@ __global__ __launch_bounds__(576) void delta_join(DeltaArgs A)
     const uint32_t at0 = lds_address(lds);
     auto number = [&](int j) { return (int64_t)(part0 + (BACK ? parts - 1 - j : j)) * A.heads + head; };
     if (slice == A.slices) {
-        // a KB holds 4 of every 8 columns of 32 x .. of the 16 rows of a register block, a row a lane & 15
-        const uint32_t mine = (uint32_t)((8 * ((l & 15) >> 2) + (l & 3)) * 32 * KT + 8 * g) * 4;
-        auto bring = [&](int j) {
-            const i32x4_t rsrc = row_rsrc(A.moves + number(j) * A.move_size + (BACK ? 1024 * KT * KT : 0));
-#pragma unroll
-            for (int p = 0; p < stage / 1024; p++) {
-                const int c = p & 1, x = (p >> 1) % KT, a = (p >> 1) / KT & 1, y = (p >> 1) / (2 * KT);   // row block y, half a
-                load_to_lds(rsrc, at0 + (j & 1) * stage + p * 1024, mine, ((32 * y + 4 * a) * 32 * KT + 32 * x + 4 * c) * 4);
-            }
-        };
-        if (parts > 1) bring(0);
+        if (parts > 1) bring_flat(row_rsrc(A.moves + number(0) * A.move_size + back), at0, stage / 1024, 0, 1);
         for (int j = 0; j + 1 < parts; j++) {
             meet();
-            if (j + 2 < parts) bring(j + 1);
+            if (j + 2 < parts)
+                bring_flat(row_rsrc(A.moves + number(j + 1) * A.move_size + back), at0 + (~j & 1) * stage, stage / 1024, 0, 1);
         }
         return;
     }
     const float *from = BACK ? A.dlast : A.state;
-    Block S[KT], added[KT];
+    // what is added is read two segments ahead, so that its wait is not one for the stores between
+    Block S[KT], added[KT], next[KT];
     state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, col);
     if (parts) state_read<KT>(added, A.starts + number(0) * A.dk * A.dv, A.dk, A.dv, col);
-    for (int j = 0; j < parts; j++) {
-        if (j + 1 < parts) meet_others();
-        state_write<KT>(S, A.starts + number(j) * A.dk * A.dv, A.dk, A.dv, col);
-        if (j + 1 == parts) break;
+    if (parts > 1) state_read<KT>(next, A.starts + number(1) * A.dk * A.dv, A.dk, A.dv, col);
+    if (parts) state_write<KT>(S, A.starts + number(0) * A.dk * A.dv, A.dk, A.dv, col);
+    for (int j = 0; j + 1 < parts; j++) {
+        Block after[KT];
+        meet_others();
+        if (j + 2 < parts) state_read<KT>(after, A.starts + number(j + 2) * A.dk * A.dv, A.dk, A.dv, col);
         const uint32_t at = at0 + (j & 1) * stage + 16 * l;
-        Part<3> sp[KT];
 #pragma unroll
-        for (int x = 0; x < KT; x++) sp[x] = operand<3>(S[x]);
+        for (int x = 0; x < KT; x++) {
+            const Part<3> sp = operand<3>(S[x]);
 #pragma unroll
-        for (int y = 0; y < KT; y++) S[y] = added[y];
-        state_read<KT>(added, A.starts + number(j + 1) * A.dk * A.dv, A.dk, A.dv, col);
+            for (int y = 0; y < KT; y++)
 #pragma unroll
-        for (int y = 0; y < KT; y++) {
-#pragma unroll
-            for (int a = 0; a < 2; a++)
-#pragma unroll
-                for (int x = 0; x < KT; x++) {
+                for (int a = 0; a < 2; a++) {
                     float f[8];
                     const uint32_t p = at + ((y * 2 + a) * KT + x) * 2048;
                     const u32x4_t lo = lds_read<u32x4_t>(p), hi = lds_read<u32x4_t>(p + 1024);
@@ -1162,9 +1181,16 @@ __global__ __launch_bounds__(576) void delta_join(DeltaArgs A)
                         f[e] = __uint_as_float(lo[e]);
                         f[4 + e] = __uint_as_float(hi[e]);
                     }
-                    mm<3>(S[y].t[a], split8<3>(f), sp[x]);
+                    mm<3>(added[y].t[a], split8<3>(f), sp);
                 }
         }
+#pragma unroll
+        for (int x = 0; x < KT; x++) {
+            S[x] = added[x];
+            added[x] = next[x];
+            next[x] = after[x];
+        }
+        state_write<KT>(S, A.starts + number(j + 1) * A.dk * A.dv, A.dk, A.dv, col);
     }
     if (parts) return;                                   // a sample without rows hands its state on
     float *to = BACK ? A.dstate : A.last;
@@ -1630,7 +1656,7 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     p.tiles = seg_tiles(d->n, d->samples, 1, kCut);
     p.cut = delta_cut(d);
     const bool bf = p.el == 2;
-    p.rec = train ? (bf ? Rec<uint16_t>::whole : Rec<float>::whole) : (bf ? Rec<uint16_t>::small : Rec<float>::small);
+    p.rec = bf ? Rec<uint16_t>::size : Rec<float>::size;
     p.recs = (size_t)p.tiles * d->heads * p.rec;
     p.us = (size_t)p.tiles * d->heads * p.slices * 512 * p.el;
     p.states = p.us * p.kt;
@@ -1748,14 +1774,13 @@ template <typename T, int KT>
 void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool train, hipStream_t st)
 {
     const dim3 all((unsigned)tiles, (unsigned)A.heads), walk((unsigned)walks);
-    const int stages = 2 * ScanLds<T, KT>::size(A.slices), join = 2 * KT * KT * 4096;
-    if (train) delta_launch(delta_prepare<T, KT, true>, all, 64, 0, A, st);
-    else delta_launch(delta_prepare<T, KT, false>, all, 64, 0, A, st);
+    const int stages = 2 * ScanLds<T, KT, false>::size(A.slices), join = 2 * KT * KT * 4096;
+    delta_launch(delta_prepare<T, KT>, all, 64, 0, A, st);
     if (!walks) return;
     if (A.cut) {
         // wavefronts enough for either kind
         const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
-        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * (most + 1), stages, A, st);
+        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * (most + 1), 2 * ScanLds<T, KT, true>::size(A.slices), A, st);
         delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
     }
     const int lds = stages + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
