@@ -187,15 +187,11 @@ __device__ __forceinline__ u32x4_t buf16(__amdgpu_buffer_rsrc_t r, uint32_t at)
 
 template <typename T>
 struct Row;
-// Rows in memory as operands, a row a lane: elements 16 b + 8 h + 0 .. 7 of the row at byte
-// offset `at` (kNowhere: a row that reads as zero).
+// Eight elements in memory as a lane's part of an operand (at kNowhere: zeros), and single ones.
 template <>
 struct Row<uint16_t> {
     typedef Part<1> Op;
-    static __device__ __forceinline__ Op natural(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b)
-    {
-        return Op{{buf16(r, at + 32 * b + 16 * h)}};
-    }
+    static __device__ __forceinline__ Op eight(__amdgpu_buffer_rsrc_t r, uint32_t at) { return Op{{buf16(r, at)}}; }
     static __device__ __forceinline__ void put4(uint16_t *p, const float *v)
     {
         *gp(reinterpret_cast<u32x2_t *>(p)) = u32x2_t{bf16x2_rne(v[0], v[1]), bf16x2_rne(v[2], v[3])};
@@ -206,19 +202,15 @@ struct Row<uint16_t> {
 template <>
 struct Row<float> {
     typedef Part<3> Op;
-    static __device__ __forceinline__ void read(__amdgpu_buffer_rsrc_t r, uint32_t x, uint32_t y, float *f)
+    static __device__ __forceinline__ Op eight(__amdgpu_buffer_rsrc_t r, uint32_t at)
     {
-        const u32x4_t a = buf16(r, x), b = buf16(r, y);
+        float f[8];
+        const u32x4_t a = buf16(r, at), b = buf16(r, at + 16);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             f[j] = __uint_as_float(a[j]);
             f[4 + j] = __uint_as_float(b[j]);
         }
-    }
-    static __device__ __forceinline__ Op natural(__amdgpu_buffer_rsrc_t r, uint32_t at, int h, int b)
-    {
-        float f[8];
-        read(r, at + 64 * b + 32 * h, at + 64 * b + 32 * h + 16, f);
         return split8<3>(f);
     }
     static __device__ __forceinline__ void put4(float *p, const float *v)
@@ -326,7 +318,8 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     f32x16_t kk = zero16(), kq = zero16();                     // a lane's row, the others in registers
 #pragma unroll
     for (int x = 0; x < 2 * KT; x++) {
-        const auto K = Row<T>::natural(kb, kat, h, x), Q = Row<T>::natural(qb, qat, h, x);
+        const uint32_t at = (uint32_t)((16 * x + 8 * h) * sizeof(T));
+        const auto K = Row<T>::eight(kb, kat + at), Q = Row<T>::eight(qb, qat + at);
         mm<IN>(kk, K, K);
         mm<IN>(kq, K, Q);                                      // k_j.q_i, lane i
     }
@@ -670,6 +663,11 @@ struct Turn {
 #pragma unroll
             for (int e = 0; e < 4; e++) lds_write(scratch + ((r0 + e) * 17 + c) * 4, f[e]);
     }
+    // bf16: the same of two words of a part
+    static __device__ __forceinline__ void fill2(uint32_t scratch, int r0, uint32_t x, uint32_t y)
+    {
+        lds_write(scratch + (lane_id() & 15) * 72 + r0 * 2, u32x2_t{x, y});
+    }
     __device__ __forceinline__ void take(uint32_t scratch)
     {
         const int l = lane_id(), h = l >> 5;
@@ -695,6 +693,27 @@ struct Turn {
         for (int a = 0; a < 2; a++) fill(scratch, 16 * a + 4 * g, b.t[a]);
         wave_sync();
         take(scratch);
+    }
+    // a block's rows for the gradients, fp32 or as two parts of bf16, 2 KB
+    static __device__ __forceinline__ void leave(uint32_t scratch, const Block &b, const u32x4_t &hi, const u32x4_t &lo, char *to)
+    {
+        Turn rows;
+        if constexpr (R == 2) {
+            rows.turn(scratch, b);
+            rows.keep(to);
+        } else {
+            const int g = lane_id() >> 4;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const u32x4_t &w = i ? lo : hi;
+                wave_sync();
+                fill2(scratch, 4 * g, w[0], w[1]);
+                fill2(scratch, 16 + 4 * g, w[2], w[3]);
+                wave_sync();
+                rows.take(scratch);
+                rows.keep(to + 1024 * i);
+            }
+        }
     }
     // as operands for the gradients
     __device__ __forceinline__ void keep(char *to) const
@@ -830,18 +849,13 @@ __device__ __forceinline__ void state_keep(uint32_t scratch, char *to, int slice
     wave_sync();
 }
 
-// What a walk has of a chunk in LDS, and its last wavefront, which brings the chunks one ahead
-// and does nothing else.  SUM: no Q, no P, and V for the values alone.
+// A walk's workgroup.  A wavefront has 16 columns of the state, and one more brings the chunks, one
+// ahead, and does nothing else.  SUM walks take no Q and no P.
 template <typename T, int KT, bool SUM>
-struct ScanLds {
+struct WalkLds {
     static constexpr int q = 2 * KT * Lane<T>::kTile, n = SUM ? q : 2 * q, p = n + Rec<T>::p, sc = SUM ? p : n + Rec<T>::sc,
                          v = sc + kScalars * 4;
-    static __host__ __device__ int size(int slices) { return v + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
-};
-template <typename T, int KT>
-struct BackLds {
-    static constexpr int q = 2 * KT * Lane<T>::kTile, n = 2 * q, p = n + Rec<T>::p, sc = n + Rec<T>::sc, o = sc + kScalars * 4;
-    static __host__ __device__ int size(int slices) { return o + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
+    static __host__ __device__ constexpr int size(int slices) { return v + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 
 // the bits of a chunk's rows that are kept (there, and not masked)
@@ -854,33 +868,33 @@ __device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w,
     return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::sc) + kScKept)) & low_bits(left);
 }
 
-template <typename T, int KT, bool SUM>
-__device__ __forceinline__ void scan_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to, bool values)
+// The wavefront that brings the chunks, in the order chunk(0), chunk(1), ... (steps of the walk);
+// values: of v, or of the output's gradient
+template <typename T, int KT, bool SUM, typename Chunk>
+__device__ __forceinline__ void bring_chunks(const DeltaArgs &A, const Walk &w, int chunks, const Chunk &chunk, uint32_t at0,
+                                             const void *values, int64_t vs, int64_t vh)
 {
-    typedef ScanLds<T, KT, SUM> L;
-    const int64_t row = (int64_t)w.base + chunk * kCut;
-    const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
-    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
-    if (!SUM) bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT);
-    if (values) bring_tiles<T>(static_cast<const T *>(A.v) + row * A.vs + w.head * A.vh, A.vs, kept, to + L::v, (A.slices + 1) / 2);
-    const i32x4_t rsrc = row_rsrc(rec);
+    typedef WalkLds<T, KT, SUM> L;
+    auto bring = [&](int s, uint32_t kept) {
+        const int64_t row = (int64_t)w.base + chunk(s) * kCut;
+        const uint32_t to = at0 + (s & 1) * L::size(A.slices);
+        bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
+        if (!SUM) bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT);
+        if (values) bring_tiles<T>(static_cast<const T *>(values) + row * vs + w.head * vh, vs, kept, to + L::v, (A.slices + 1) / 2);
+        const i32x4_t rsrc = row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk(s)) * A.heads + w.head) * A.rec_size);
 #pragma unroll
-    for (int p = 0; p < (SUM ? Rec<T>::p : Rec<T>::size); p += 1024) load_to_lds(rsrc, to + L::n + p, 16 * lane_id(), p);
-    if (SUM) load_to_lds(rsrc, to + L::sc, 16 * lane_id(), Rec<T>::sc);
-}
-
-template <typename T, int KT>
-__device__ __forceinline__ void back_bring(const DeltaArgs &A, const Walk &w, int chunk, uint32_t kept, uint32_t to)
-{
-    typedef BackLds<T, KT> L;
-    const int64_t row = (int64_t)w.base + chunk * kCut;
-    const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
-    bring_tiles<T>(static_cast<const T *>(A.k) + row * A.ks + w.key * A.kh, A.ks, kept, to, KT);
-    bring_tiles<T>(static_cast<const T *>(A.q) + row * A.qs + w.key * A.qh, A.qs, kept, to + L::q, KT);
-    bring_tiles<T>(static_cast<const T *>(A.dout) + row * A.ds + w.head * A.dh, A.ds, kept, to + L::o, (A.slices + 1) / 2);
-    const i32x4_t rsrc = row_rsrc(rec);
-#pragma unroll
-    for (int p = 0; p < Rec<T>::size; p += 1024) load_to_lds(rsrc, to + L::n + p, 16 * lane_id(), p);
+        for (int p = 0; p < (SUM ? Rec<T>::p : Rec<T>::size); p += 1024) load_to_lds(rsrc, to + L::n + p, 16 * lane_id(), p);
+        if (SUM) load_to_lds(rsrc, to + L::sc, 16 * lane_id(), Rec<T>::sc);
+    };
+    if (!chunks) return;
+    uint32_t kept = kept_rows<T>(A, w, chunk(0)), next = kept_rows<T>(A, w, chunks > 1 ? chunk(1) : -1);
+    bring(0, kept);
+    for (int s = 0; s < chunks; s++) {
+        meet();
+        kept = next;
+        if (s + 1 < chunks) bring(s + 1, kept);
+        next = kept_rows<T>(A, w, s + 2 < chunks ? chunk(s + 2) : -1);
+    }
 }
 
 // Where element (row, col) of a segment's matrix lies, in floats: KBs of 16 rows (one block of
@@ -898,28 +912,21 @@ template <typename T, int KT, bool TRAIN, bool SUM>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
     constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
-    typedef ScanLds<T, KT, SUM> L;
+    typedef WalkLds<T, KT, SUM> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
     const bool values = !SUM || blockIdx.y == 0;
     const int slice = uniform((int)(threadIdx.x >> 6)), slices = values ? A.slices : 2 * KT;
-    const int stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const int chunks = (w.rows + kCut - 1) / kCut;
     const uint32_t at0 = lds_address(lds);
     if (slice >= slices) {
-        if (slice > slices) return;                      // fewer columns of the one kind than of the other
-        uint32_t kept = kept_rows<T>(A, w, 0), next = kept_rows<T>(A, w, 1);
-        if (chunks) scan_bring<T, KT, SUM>(A, w, 0, kept, at0, values);
-        for (int i = 0; i < chunks; i++) {
-            meet();
-            kept = next;
-            if (i + 1 < chunks) scan_bring<T, KT, SUM>(A, w, i + 1, kept, at0 + (~i & 1) * stage, values);
-            next = kept_rows<T>(A, w, i + 2);
-        }
-        return;
+        auto order = [](int s) { return s; };
+        if (slice == slices) bring_chunks<T, KT, SUM>(A, w, chunks, order, at0, values ? A.v : nullptr, A.vs, A.vh);
+        return;                                          // the rest: fewer columns of one kind than of the other
     }
     const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
-    const uint32_t scratch = at0 + 2 * stage + slice * (TRAIN ? kScratchBlocks<T, KT> : 1) * Turn<T>::kBytes;
+    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * (TRAIN ? kScratchBlocks<T, KT> : 1) * Turn<T>::kBytes;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(values ? slice : 0);
 
@@ -933,15 +940,15 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         state_read<KT>(S, A.cut ? A.starts + w.part * A.dk * A.dv : A.state ? A.state + w.matrix * A.dk * A.dv : nullptr, A.dk,
                        A.dv, col);
     // what leaves: the lane's piece of a row of o, of U and of the states, a chunk's step apart
-    const int64_t ostep = (int64_t)kCut * A.heads * A.dv, ustep = (int64_t)A.heads * A.slices * Lds<T>::kRows;
+    const int64_t ostep = (int64_t)kCut * A.heads * A.dv, ustep = (int64_t)A.heads * A.slices * 2048,
+                  sstep = (int64_t)A.heads * KT * A.slices * Lds<T>::kRows;
     T *o = static_cast<T *>(A.o) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c;
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
-    char *u = static_cast<char *>(A.u) + (number * A.slices + slice) * Lds<T>::kRows;
+    char *u = static_cast<char *>(A.u) + (number * A.slices + slice) * 2048;
     char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<T>::kRows;
     for (int i = 0; i < chunks; i++) {
-        const uint32_t at = at0 + (i & 1) * stage;
         meet_others();
-        const uint32_t sc = at + L::sc;
+        const uint32_t at = at0 + (i & 1) * L::size(A.slices), sc = at + L::sc;
         Block X = zero_block(), Y = zero_block(), V = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
@@ -989,16 +996,13 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
                 for (int e = 0; e < 4; e++) Y.t[a][e] *= sg.t[a][e];
                 mm<OUT>(Y.t[a], lane.template matrix<OUT>(at + L::p, a), op);
             }
+            if (TRAIN) Turn<T>::leave(scratch, U, op.p[0], op.p[1], u);
             Turn<T> rows;
-            if (TRAIN) {
-                rows.turn(scratch, U);
-                rows.keep(u);
-            }
             rows.turn(scratch, Y);
             rows.write(o, r < w.rows - i * kCut, c, A.dv, A.ovec);
             o += ostep;
             u += ustep;
-            states += KT * ustep;
+            states += sstep;
         }
     }
     if (SUM) {
@@ -1028,43 +1032,37 @@ template <typename T, int KT, bool SUM>
 __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
-    typedef BackLds<T, KT> L;
+    typedef WalkLds<T, KT, false> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
     if (!w.any) return;
-    const int slice = uniform((int)(threadIdx.x >> 6)), stage = L::size(A.slices), chunks = (w.rows + kCut - 1) / kCut;
+    const int slice = uniform((int)(threadIdx.x >> 6)), chunks = (w.rows + kCut - 1) / kCut;
     const uint32_t at0 = lds_address(lds);
     if (slice == A.slices) {
-        uint32_t kept = kept_rows<T>(A, w, chunks - 1), next = kept_rows<T>(A, w, chunks - 2);
-        if (chunks) back_bring<T, KT>(A, w, chunks - 1, kept, at0 + (~chunks & 1) * stage);
-        for (int i = chunks - 1; i >= 0; i--) {
-            meet();
-            kept = next;
-            if (i) back_bring<T, KT>(A, w, i - 1, kept, at0 + (~i & 1) * stage);
-            next = kept_rows<T>(A, w, i - 2);
-        }
+        bring_chunks<T, KT, false>(A, w, chunks, [=](int s) { return chunks - 1 - s; }, at0, A.dout, A.ds, A.dh);
         return;
     }
     const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
-    const uint32_t scratch = at0 + 2 * stage + slice * kScratchBlocks<T, KT> * Turn<T>::kBytes;
+    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratchBlocks<T, KT> * Turn<T>::kBytes;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(slice);
 
     Block E[KT];
     state_read<KT>(E, SUM ? nullptr : A.cut ? A.starts + w.part * A.dk * A.dv : A.dlast ? A.dlast + w.matrix * A.dk * A.dv : nullptr,
                    A.dk, A.dv, col);
-    const int64_t vstep = (int64_t)kCut * A.heads * A.dv, zstep = (int64_t)A.heads * A.slices * Lds<T>::kRows;
+    const int64_t vstep = (int64_t)kCut * A.heads * A.dv, zstep = (int64_t)A.heads * A.slices * 2048,
+                  sstep = (int64_t)A.heads * KT * A.slices * Lds<T>::kRows;
     T *dv = static_cast<T *>(A.dv_) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c + chunks * vstep;
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
-    char *z = static_cast<char *>(A.z) + (number * A.slices + slice) * Lds<T>::kRows + chunks * zstep;
-    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<T>::kRows + chunks * KT * zstep;
-    for (int i = chunks - 1; i >= 0; i--) {
-        const uint32_t at = at0 + (i & 1) * stage;
+    char *z = static_cast<char *>(A.z) + (number * A.slices + slice) * 2048 + chunks * zstep;
+    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<T>::kRows + chunks * sstep;
+    for (int s = 0; s < chunks; s++) {
         meet_others();
+        const int i = chunks - 1 - s;
+        const uint32_t at = at0 + (s & 1) * L::size(A.slices), sc = at + L::sc;
         dv -= vstep;
         z -= zstep;
-        states -= KT * zstep;
-        const uint32_t sc = at + L::sc;
+        states -= sstep;
         Block X = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
@@ -1074,7 +1072,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
             for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
         }
         const Block wt = row_scalars(sc + 4 * kScW);
-        Block D = lane.block(at + L::o, columns);
+        Block D = lane.block(at + L::v, columns);
         const Part<IN> dp = operand<IN>(D);
 #pragma unroll
         for (int a = 0; a < 2; a++) {
@@ -1108,9 +1106,9 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
             }
         if (!SUM) {
             state_keep<T, KT>(scratch, states, A.slices, slice);
+            const Part<OUT> kept = operand<OUT>(Z);
+            Turn<T>::leave(scratch, Z, kept.p[0], kept.p[1], z);
             Turn<T> rows;
-            rows.turn(scratch, Z);
-            rows.keep(z);
             const Block b = row_scalars(sc + 4 * kScB);
 #pragma unroll
             for (int a = 0; a < 2; a++)
@@ -1224,10 +1222,18 @@ struct Kept {
     }
 };
 
+// rows of U or Z in LDS as an operand: 2 KB a 16 columns
+template <typename T>
+__device__ __forceinline__ Part<sizeof(T) == 2 ? 2 : 3> written(uint32_t at, int x)
+{
+    if constexpr (sizeof(T) == 2) return staged<2>(at, x);
+    else return Lds<T>::rows(at, x);
+}
+
 template <typename T, int KT>
 struct GradLds {
     static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, with = sc + 1024, u = with + 6 * Prec<T>::OUT * 1024;
-    static __host__ __device__ int size(int slices) { return u + 3 * slices * Lds<T>::kRows; }
+    static __host__ __device__ int size(int slices) { return u + slices * (2 * 2048 + Lds<T>::kRows); }
 };
 
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk.  What rows of K and Q
@@ -1236,7 +1242,7 @@ struct GradLds {
 template <typename T, int KT>
 __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT, R = Lds<T>::R;
+    constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT;
     typedef GradLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     __shared__ float red[KT][3][32], cross[3][32], owns[32];
@@ -1272,10 +1278,10 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
         const int64_t number = (int64_t)tile * A.heads + head;
         const int n = A.slices;
         if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size + Rec<T>::sc), at + L::sc, 16 * l, 0);
-        bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * Lds<T>::kRows), at + L::u, n * R, wave, KT);
-        bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * Lds<T>::kRows), at + L::u + n * Lds<T>::kRows, n * R, wave, KT);
+        bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * 2048), at + L::u, 2 * n, wave, KT);
+        bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * 2048), at + L::u + n * 2048, 2 * n, wave, KT);
         bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + head * A.dh), row_at<T>(kept, A.ds),
-                      at + L::u + 2 * n * Lds<T>::kRows, n, wave, KT);
+                      at + L::u + 2 * n * 2048, n, wave, KT);
     };
     bring_rows<T>(row_rsrc(static_cast<const T *>(A.k) + row * A.ks + key * A.kh), row_at<T>(kept, A.ks), at, 2 * KT, wave, KT);
     bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + key * A.qh), row_at<T>(kept, A.qs), at + L::q, 2 * KT, wave, KT);
@@ -1290,7 +1296,7 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
         const int64_t number = (int64_t)tile * A.heads + head, n = A.slices;
         const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<T>::kRows;
         const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<T>::kRows;
-        const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * Lds<T>::kRows, oat = zat + n * Lds<T>::kRows;
+        const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * 2048, oat = zat + n * 2048;
         // the states' rows are on their way while the chunk's own products are made
         Kept<T> S[kKeptMost], E[kKeptMost];
 #pragma unroll
@@ -1311,9 +1317,16 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
             if (what % KT != wave) continue;
             f32x16_t p = zero16(), p2 = zero16(), k = zero16(), f;
             for (int x = 0; x < n; x++) {
-                const auto U = Lds<T>::rows(uat, x), Z = Lds<T>::rows(what == 2 ? zat : oat, x);
-                if (what != 1) mm<IN>(p, U, Z);          // u_j.dO_i (or Z_i), lane i
-                if (what != 0) mm<IN>(what == 1 ? p : p2, Z, U);   // dO_i (or Z_i).u_j, lane j
+                const auto U = written<T>(uat, x);
+                if (what == 2) {
+                    const auto Z = written<T>(zat, x);
+                    mm<OUT>(p, U, Z);                    // u_j.z_i, lane i
+                    mm<OUT>(p2, Z, U);                   // z_i.u_j, lane j
+                } else {
+                    const auto D = Lds<T>::rows(oat, x);
+                    if (what == 0) mm<OUT>(p, U, D);     // u_j.dO_i, lane i
+                    else mm<OUT>(p, D, U);               // dO_i.u_j, lane j
+                }
             }
 #pragma unroll
             for (int x = 0; x < 2 * KT; x++) {
@@ -1379,8 +1392,8 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
             if (x < n) {
                 const auto s0 = S[x].operand(), e0 = E[x].operand();
                 mm<IN>(t1, s0, Lds<T>::rows(oat, x));
-                mm<IN>(t2, s0, Lds<T>::rows(zat, x));
-                mm<IN>(t3, e0, Lds<T>::rows(uat, x));
+                mm<OUT>(t2, s0, written<T>(zat, x));
+                mm<OUT>(t3, e0, written<T>(uat, x));
                 mm<IN>(se, s0, e0);
             }
         float inner = 0.f;
@@ -1658,8 +1671,8 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     const bool bf = p.el == 2;
     p.rec = bf ? Rec<uint16_t>::size : Rec<float>::size;
     p.recs = (size_t)p.tiles * d->heads * p.rec;
-    p.us = (size_t)p.tiles * d->heads * p.slices * 512 * p.el;
-    p.states = p.us * p.kt;
+    p.us = (size_t)p.tiles * d->heads * p.slices * 2048;
+    p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 512 * p.el;
     if (p.cut) {
         const size_t segments = (size_t)seg_tiles(d->n, d->samples, 1, kSpan) * d->heads;
         p.move = (size_t)p.kt * p.kt * 4096 * (train ? 2 : 1);
@@ -1773,17 +1786,18 @@ void delta_launch(F kernel, dim3 grid, int threads, size_t lds, const DeltaArgs 
 template <typename T, int KT>
 void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool train, hipStream_t st)
 {
-    const dim3 all((unsigned)tiles, (unsigned)A.heads), walk((unsigned)walks);
-    const int stages = 2 * ScanLds<T, KT, false>::size(A.slices), join = 2 * KT * KT * 4096;
-    delta_launch(delta_prepare<T, KT>, all, 64, 0, A, st);
+    const dim3 walk((unsigned)walks);
+    const int join = 2 * KT * KT * 4096;
+    delta_launch(delta_prepare<T, KT>, dim3((unsigned)tiles, (unsigned)A.heads), 64, 0, A, st);
     if (!walks) return;
     if (A.cut) {
         // wavefronts enough for either kind
         const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
-        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * (most + 1), 2 * ScanLds<T, KT, true>::size(A.slices), A, st);
+        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * most + 64, 2 * WalkLds<T, KT, true>::size(A.slices),
+                     A, st);
         delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
     }
-    const int lds = stages + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
+    const int lds = 2 * WalkLds<T, KT, false>::size(A.slices) + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
     if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices + 64, lds, A, st);
     else delta_launch(delta_scan<T, KT, false, false>, walk, 64 * A.slices + 64, lds, A, st);
 }
@@ -1792,12 +1806,14 @@ template <typename T, int KT>
 void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool, hipStream_t st)
 {
     const dim3 walk((unsigned)walks);
-    const int stages = 2 * BackLds<T, KT>::size(A.slices), join = 2 * KT * KT * 4096;
+    const int lds = 2 * WalkLds<T, KT, false>::size(A.slices), join = 2 * KT * KT * 4096;
     if (walks && A.cut) {
-        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, stages, A, st);
+        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, lds, A, st);
         delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
     }
-    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64, stages + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
+    if (walks)
+        delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64,
+                     lds + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
     delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
 }
 
