@@ -4,9 +4,15 @@
 //
 // The bound is reading x (and dy) and writing y (or dx) once: a row stays in registers, as it
 // came, between its sums, which are taken of the centred values and in fp32.  A row is read by
-// 1 .. 64 lanes (several rows share a wavefront) or by 4 or 16 wavefronts, 16 bytes a lane and
-// piece.  Workgroups walk over rows; in the backward each keeps its share of dw and db in
-// registers, leaves one row of them, and a second kernel adds these up in a fixed order.
+// 1 .. 64 lanes (several rows share a wavefront) or by up to 16 wavefronts, 16 bytes a lane and
+// piece.  Workgroups walk over rows, with weight and bias in registers (read again for each
+// row they cost as much of the caches as x: 74 us for what takes 55) and, where registers last,
+// the next row on its way; in the backward each keeps its share of dw and db in registers,
+// leaves one row of them, and a second kernel adds these up in a fixed order.
+//
+// 140771 rows of 512 in bf16: forward 55 us (288 MB, 5.3 TB/s), backward with its sums 88 us (432
+// MB, 4.9 TB/s).  8191 of 5000 in fp32: 61 us (328 MB, 5.4 TB/s) and 108 us (491 MB, 4.6 TB/s; the
+// workgroups' sums are another 41 MB).  50 rows of 256: 3 us, a launch.
 #include <cmath>
 #include <string>
 
@@ -17,7 +23,6 @@ namespace emb {
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kNormChannels = 16384;
-constexpr int kNormGroups = 1024;        // most workgroups of the backward: rows of partial sums
 
 struct NormArgs {
     const void *x;
@@ -75,13 +80,14 @@ struct Piece<float> {
     }
 };
 
-// elements at .. at + E - 1 of a row, zeros behind its end
-template <typename T>
+// Elements at .. at + E - 1 of a row, zeros behind its end.  WHOLE: rows are whole pieces.
+template <typename T, bool WHOLE>
 __device__ __forceinline__ u32x4_t piece_read(const T *row, int at, int channels)
 {
     constexpr int E = Piece<T>::E;
     typedef typename Piece<T>::Raw Raw;
-    if (at + E <= channels) return gp(reinterpret_cast<const Raw *>(row + at))->w;
+    if (WHOLE ? at < channels : at + E <= channels) return gp(reinterpret_cast<const Raw *>(row + at))->w;
+    if (WHOLE) return u32x4_t{0, 0, 0, 0};
     union {
         u32x4_t w;
         T e[E];
@@ -92,7 +98,7 @@ __device__ __forceinline__ u32x4_t piece_read(const T *row, int at, int channels
         if (at + i < channels) u.e[i] = *gp(row + at + i);
     return u.w;
 }
-template <typename T>
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void piece_write(T *row, int at, int channels, const float *f)
 {
     constexpr int E = Piece<T>::E;
@@ -102,7 +108,7 @@ __device__ __forceinline__ void piece_write(T *row, int at, int channels, const 
         T e[E];
     } u;
     u.w = Piece<T>::shut(f);
-    if (at + E <= channels) {
+    if (WHOLE || at + E <= channels) {
         gp(reinterpret_cast<Raw *>(row + at))->w = u.w;
         return;
     }
@@ -111,48 +117,46 @@ __device__ __forceinline__ void piece_write(T *row, int at, int channels, const 
         if (at + i < channels) *gp(row + at + i) = u.e[i];
 }
 // the same of fp32 parameters; `fill` where there are none or behind the end
-template <int E>
+template <int E, bool WHOLE>
 __device__ __forceinline__ void param_read(const float *p, int at, int channels, float fill, float *f)
 {
     typedef Piece<float>::Raw Raw;
 #pragma unroll
     for (int i = 0; i < E; i++) f[i] = fill;
     if (!p) return;
-    if (at + E <= channels) {
+    if (WHOLE ? at < channels : at + E <= channels) {
 #pragma unroll
         for (int j = 0; j < E; j += 4) {
             const u32x4_t v = gp(reinterpret_cast<const Raw *>(p + at + j))->w;
 #pragma unroll
             for (int e = 0; e < 4; e++) f[j + e] = __uint_as_float(v[e]);
         }
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int i = 0; i < E; i++)
             if (at + i < channels) f[i] = *gp(p + at + i);
     }
 }
 
-// Sums over the lanes of a row, the same in all of them.  W wavefronts a row meet in LDS, at
-// `turn`'s place of two, so that one barrier a sum is enough.
-template <int W, int N>
+// Sums over the lanes of a row, the same in all of them.  The wavefronts of a row meet in
+// LDS, at `turn`'s place of two, so that one barrier a sum is enough.
+template <bool MANY, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], int lanes, float (*meet)[16][N], int turn)
 {
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1)
-        if (m < lanes)
+        if (MANY || m < lanes)
 #pragma unroll
             for (int i = 0; i < N; i++) v[i] += __shfl_xor(v[i], m, 64);
-    if (W == 1) return;
-    const int wave = threadIdx.x >> 6;
+    if (!MANY) return;
     if (lane_id() == 0)
 #pragma unroll
-        for (int i = 0; i < N; i++) meet[turn][wave][i] = v[i];
+        for (int i = 0; i < N; i++) meet[turn][threadIdx.x >> 6][i] = v[i];
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; i++) {
         float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; w++) s += meet[turn][w][i];
+        for (int w = 0; w < (int)(blockDim.x >> 6); w++) s += meet[turn][w][i];
         v[i] = s;
     }
 }
@@ -164,28 +168,42 @@ __device__ __forceinline__ int64_t norm_at(int64_t r, int inner, int64_t so, int
     return o * so + (r - o * inner) * si;
 }
 
-// W: wavefronts of a row (1: four rows or sets of rows a workgroup), CH: pieces of a lane
-template <typename T, int W, int CH>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_forward(NormArgs A)
+// A row's pieces of a lane, as they lie in memory; zeros behind its end and of no row.
+template <typename T, int CH, bool WHOLE>
+__device__ __forceinline__ void row_read(u32x4_t (&raw)[CH], const void *x, int64_t r, int64_t rows, int inner, int64_t so,
+                                         int64_t si, int mine, int lanes, int channels)
+{
+    const T *row = static_cast<const T *>(x) + (r < rows ? norm_at(r, inner, so, si) : 0);
+#pragma unroll
+    for (int j = 0; j < CH; j++)
+        raw[j] = r < rows ? piece_read<T, WHOLE>(row, (mine + j * lanes) * Piece<T>::E, channels) : u32x4_t{0, 0, 0, 0};
+}
+
+// MANY: a workgroup's wavefronts share a row, otherwise each has one or several; CH: pieces of a
+// lane.  The next row is on its way while this one is summed; weight and bias stay in registers.
+template <typename T, bool MANY, int CH, bool WHOLE>
+__global__ __launch_bounds__(MANY ? 1024 : 256) void norm_forward(NormArgs A)
 {
     typedef Piece<T> P;
     constexpr int E = P::E;
     __shared__ float meet[2][16][1];
-    const int lanes = W == 1 ? A.lanes : 64 * W;
-    const int mine = threadIdx.x & (lanes - 1);          // the lane's place in its row
-    const int per = W == 1 ? 256 / lanes : 1;            // rows of a workgroup at a time
-    const int own = W == 1 ? threadIdx.x / lanes : 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < A.rows; r0 += (int64_t)gridDim.x * per) {
-        const int64_t r = r0 + own;
-        const bool there = r < A.rows;
-        const T *x = static_cast<const T *>(A.x) + (there ? norm_at(r, A.inner, A.xs, A.xi) : 0);
-        u32x4_t raw[CH];
-        float sum[1] = {0.f};
+    const int lanes = MANY ? (int)blockDim.x : A.lanes;
+    const int mine = MANY ? threadIdx.x : threadIdx.x & (lanes - 1);          // the lane's place in its row
+    const int per = MANY ? 1 : 256 / lanes;            // rows of a workgroup at a time
+    const int own = MANY ? 0 : threadIdx.x / lanes;
+    const int64_t step = (int64_t)gridDim.x * per;
+    float w[CH][E], b[CH][E];
 #pragma unroll
-        for (int j = 0; j < CH; j++) {
-            const int at = (mine + j * lanes) * E;
-            raw[j] = there ? piece_read<T>(x, at, A.channels) : u32x4_t{0, 0, 0, 0};
-        }
+    for (int j = 0; j < CH; j++) {
+        param_read<E, WHOLE>(A.w, (mine + j * lanes) * E, A.channels, 1.f, w[j]);
+        param_read<E, WHOLE>(A.b, (mine + j * lanes) * E, A.channels, 0.f, b[j]);
+    }
+    int64_t r = (int64_t)blockIdx.x * per + own;
+    u32x4_t raw[CH], next[CH];
+    row_read<T, CH, WHOLE>(raw, A.x, r, A.rows, A.inner, A.xs, A.xi, mine, lanes, A.channels);
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < A.rows; r0 += step, r += step) {
+        row_read<T, CH, WHOLE>(next, A.x, r + step, A.rows, A.inner, A.xs, A.xi, mine, lanes, A.channels);
+        float sum[1] = {0.f};
 #pragma unroll
         for (int j = 0; j < CH; j++) {
             float f[E];
@@ -193,7 +211,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_forward(NormArgs A
 #pragma unroll
             for (int e = 0; e < E; e++) sum[0] += f[e];
         }
-        row_sums<W, 1>(sum, lanes, meet, 0);
+        row_sums<MANY, 1>(sum, lanes, meet, 0);
         const float mean = sum[0] * A.part;
         float sq[1] = {0.f};
 #pragma unroll
@@ -207,94 +225,106 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_forward(NormArgs A
                 sq[0] = fmaf(d, d, sq[0]);
             }
         }
-        row_sums<W, 1>(sq, lanes, meet, 1);
+        row_sums<MANY, 1>(sq, lanes, meet, 1);
         const float rstd = 1.f / sqrtf(fmaf(sq[0], A.part, A.eps));
-        if (!there) continue;
-        if (A.stats && mine == 0) {
-            A.stats[2 * r] = mean;
-            A.stats[2 * r + 1] = rstd;
-        }
-        T *y = static_cast<T *>(A.y) + r * A.channels;
+        if (r < A.rows) {
+            if (A.stats && mine == 0) {
+                A.stats[2 * r] = mean;
+                A.stats[2 * r + 1] = rstd;
+            }
+            T *y = static_cast<T *>(A.y) + r * A.channels;
 #pragma unroll
-        for (int j = 0; j < CH; j++) {
-            const int at = (mine + j * lanes) * E;
-            if (at >= A.channels) continue;
-            float f[E], w[E], b[E];
-            P::open(raw[j], f);
-            param_read<E>(A.w, at, A.channels, 1.f, w);
-            param_read<E>(A.b, at, A.channels, 0.f, b);
+            for (int j = 0; j < CH; j++) {
+                const int at = (mine + j * lanes) * E;
+                if (at >= A.channels) continue;
+                float f[E];
+                P::open(raw[j], f);
 #pragma unroll
-            for (int e = 0; e < E; e++) f[e] = fmaf((f[e] - mean) * rstd, w[e], b[e]);
-            piece_write<T>(y, at, A.channels, f);
+                for (int e = 0; e < E; e++) f[e] = fmaf((f[e] - mean) * rstd, w[j][e], b[j][e]);
+                piece_write<T, WHOLE>(y, at, A.channels, f);
+            }
         }
+#pragma unroll
+        for (int j = 0; j < CH; j++) raw[j] = next[j];
     }
 }
 
-template <typename T, int W, int CH>
-__global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_backward(NormArgs A)
+template <typename T, bool MANY, int CH, bool WHOLE>
+__global__ __launch_bounds__(MANY ? 1024 : 256) void norm_backward(NormArgs A)
 {
     typedef Piece<T> P;
     constexpr int E = P::E;
+    constexpr bool AHEAD = CH * E <= 8;                  // the next row is on its way
     __shared__ float meet[2][16][2];
-    __shared__ __attribute__((aligned(16))) float join[W == 1 ? 256 * E : 1];
-    const int lanes = W == 1 ? A.lanes : 64 * W;
-    const int mine = threadIdx.x & (lanes - 1);
-    const int per = W == 1 ? 256 / lanes : 1;
-    const int own = W == 1 ? threadIdx.x / lanes : 0;
-    float dw[CH][E], db[CH][E];
+    __shared__ __attribute__((aligned(16))) float join[MANY ? 1 : 256 * E];
+    const int lanes = MANY ? (int)blockDim.x : A.lanes;
+    const int mine = MANY ? threadIdx.x : threadIdx.x & (lanes - 1);
+    const int per = MANY ? 1 : 256 / lanes;
+    const int own = MANY ? 0 : threadIdx.x / lanes;
+    const int64_t step = (int64_t)gridDim.x * per;
+    float dw[CH][E], db[CH][E], w[CH][E];
 #pragma unroll
-    for (int j = 0; j < CH; j++)
+    for (int j = 0; j < CH; j++) {
 #pragma unroll
         for (int e = 0; e < E; e++) dw[j][e] = db[j][e] = 0.f;
+        param_read<E, WHOLE>(A.w, (mine + j * lanes) * E, A.channels, 1.f, w[j]);
+    }
     int turn = 0;
-    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < A.rows; r0 += (int64_t)gridDim.x * per) {
-        const int64_t r = r0 + own;
-        const bool there = r < A.rows;
-        const T *x = static_cast<const T *>(A.x) + (there ? norm_at(r, A.inner, A.xs, A.xi) : 0);
-        const T *dy = static_cast<const T *>(A.dy) + (there ? norm_at(r, A.inner, A.ds, A.di) : 0);
-        u32x4_t rx[CH], rd[CH];
-#pragma unroll
-        for (int j = 0; j < CH; j++) {
-            const int at = (mine + j * lanes) * E;
-            rx[j] = there ? piece_read<T>(x, at, A.channels) : u32x4_t{0, 0, 0, 0};
-            rd[j] = there ? piece_read<T>(dy, at, A.channels) : u32x4_t{0, 0, 0, 0};
-        }
-        const float mean = there ? *gp(A.stats + 2 * r) : 0.f, rstd = there ? *gp(A.stats + 2 * r + 1) : 0.f;
+    int64_t r = (int64_t)blockIdx.x * per + own;
+    u32x4_t rx[CH], rd[CH], nx[CH], nd[CH];
+    float mean, rstd, nmean, nrstd;
+    auto read = [&](int64_t r, u32x4_t(&rx)[CH], u32x4_t(&rd)[CH], float &mean, float &rstd) {
+        row_read<T, CH, WHOLE>(rx, A.x, r, A.rows, A.inner, A.xs, A.xi, mine, lanes, A.channels);
+        row_read<T, CH, WHOLE>(rd, A.dy, r, A.rows, A.inner, A.ds, A.di, mine, lanes, A.channels);
+        mean = r < A.rows ? *gp(A.stats + 2 * r) : 0.f;
+        rstd = r < A.rows ? *gp(A.stats + 2 * r + 1) : 0.f;
+    };
+    if (AHEAD) read(r, rx, rd, mean, rstd);
+    for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < A.rows; r0 += step, r += step) {
+        if (AHEAD) read(r + step, nx, nd, nmean, nrstd);
+        else read(r, rx, rd, mean, rstd);
         float sums[2] = {0.f, 0.f};                      // of g and of g xh
 #pragma unroll
         for (int j = 0; j < CH; j++) {
             const int at = (mine + j * lanes) * E;
-            float f[E], d[E], w[E];
+            float f[E], d[E];
             P::open(rx[j], f);
             P::open(rd[j], d);
-            param_read<E>(A.w, at, A.channels, 1.f, w);
 #pragma unroll
             for (int e = 0; e < E; e++) {
                 const float xh = (f[e] - mean) * rstd;
-                const float g = at + e < A.channels ? d[e] * w[e] : 0.f;
+                const float g = at + e < A.channels ? d[e] * w[j][e] : 0.f;
                 sums[0] += g;
                 sums[1] = at + e < A.channels ? fmaf(g, xh, sums[1]) : sums[1];
                 dw[j][e] = fmaf(d[e], xh, dw[j][e]);
                 db[j][e] += d[e];
             }
         }
-        row_sums<W, 2>(sums, lanes, meet, turn);
+        row_sums<MANY, 2>(sums, lanes, meet, turn);
         turn ^= 1;
-        if (!there) continue;
-        const float mg = sums[0] * A.part, mgx = sums[1] * A.part;
-        T *dx = static_cast<T *>(A.dx) + r * A.channels;
+        if (r < A.rows) {
+            const float mg = sums[0] * A.part, mgx = sums[1] * A.part;
+            T *dx = static_cast<T *>(A.dx) + r * A.channels;
+#pragma unroll
+            for (int j = 0; j < CH; j++) {
+                const int at = (mine + j * lanes) * E;
+                if (at >= A.channels) continue;
+                float f[E], d[E];
+                P::open(rx[j], f);
+                P::open(rd[j], d);
+#pragma unroll
+                for (int e = 0; e < E; e++) f[e] = rstd * (fmaf(d[e], w[j][e], -mg) - (f[e] - mean) * rstd * mgx);
+                piece_write<T, WHOLE>(dx, at, A.channels, f);
+            }
+        }
+        if (!AHEAD) continue;
 #pragma unroll
         for (int j = 0; j < CH; j++) {
-            const int at = (mine + j * lanes) * E;
-            if (at >= A.channels) continue;
-            float f[E], d[E], w[E];
-            P::open(rx[j], f);
-            P::open(rd[j], d);
-            param_read<E>(A.w, at, A.channels, 1.f, w);
-#pragma unroll
-            for (int e = 0; e < E; e++) f[e] = rstd * (fmaf(d[e], w[e], -mg) - (f[e] - mean) * rstd * mgx);
-            piece_write<T>(dx, at, A.channels, f);
+            rx[j] = nx[j];
+            rd[j] = nd[j];
         }
+        mean = nmean;
+        rstd = nrstd;
     }
     // one row of sums a workgroup
     for (int which = 0; which < 2; which++) {
@@ -306,7 +336,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_backward(NormArgs 
 #pragma unroll
             for (int e = 0; e < E; e++) s[e] = which ? db[j][e] : dw[j][e];
             const int at = (mine + j * lanes) * E;
-            if (W == 1) {                                // the rows side by side in the workgroup
+            if (!MANY) {                                 // the rows side by side in the workgroup
                 __syncthreads();
 #pragma unroll
                 for (int e = 0; e < E; e++) join[threadIdx.x * E + e] = s[e];
@@ -373,7 +403,11 @@ emb_status norm_pointers(const emb_norm *d, const void *y, const void *z)
     return EMB_OK;
 }
 
-// Lanes, wavefronts and pieces of a row.
+// A row of up to 1024 channels is one wavefront's or a part's of one, a longer one is a workgroup's
+// with a wavefront for every 1024: 16 channels a lane at most, the most whose sums, weights and
+// pieces fit in the registers.  8 a lane and twice the wavefronts was slower where that makes one
+// wavefront two (60000 rows of 768 in bf16, backward: 83 us, here 56; 30000 of 1024: 49 and 39)
+// and no faster above (8191 of 5000 in fp32: 105 and 108).
 struct NormPlan {
     int waves, pieces, lanes;
     int64_t at_once, groups;             // rows of a workgroup at a time; workgroups that have one
@@ -386,12 +420,23 @@ NormPlan norm_plan(const emb_norm *d)
     const int n = (d->channels + E - 1) / E;
     p.lanes = 1;
     while (p.lanes < 64 && p.lanes < n) p.lanes *= 2;
-    p.waves = n <= 256 ? 1 : n <= 1024 ? 4 : 16;
-    const int per = p.waves == 1 ? p.lanes : 64 * p.waves;
-    p.pieces = n <= per ? 1 : n <= 2 * per ? 2 : 4;
+    p.waves = (d->channels + 1023) / 1024;
+    p.pieces = p.waves > 1 || n > 128 ? 16 / E : n > 64 ? 2 : 1;
     p.at_once = p.waves == 1 ? 256 / p.lanes : 1;
     p.groups = (d->rows + p.at_once - 1) / p.at_once;
     return p;
+}
+
+// Workgroups.  The forward takes what keeps the card busy to the end (140771 rows of 512 bf16: 1024
+// workgroups 73 us, 8192 55, one a set of rows 62; 4000 of 16384: 1024 of 16 wavefronts 53 us,
+// 4096 60).  Each of the backward writes sums of its own, which norm_total reads again: no more
+// than run at the same time (140771 x 512: 512 109 us, 768 88, 1024 88, 1536 108; 30000 x 1024: 39 at
+// 768, 44 at 1024; 8191 x 5000 fp32, 5 wavefronts: 256 114, 512 108, 1024 122; 4000 x 16384: 256 100, 512 123).
+int64_t norm_groups(const NormPlan &p, bool backward)
+{
+    const int64_t most = backward ? p.waves == 1 ? 768 : 256 * (p.waves < 10 ? 10 / p.waves : 1)
+                                  : p.waves == 1 ? 8192 : 16384 / p.waves;
+    return p.groups < most ? p.groups : most;
 }
 
 NormArgs norm_args(const emb_norm *d, const NormPlan &p)
@@ -411,24 +456,24 @@ NormArgs norm_args(const emb_norm *d, const NormPlan &p)
     return A;
 }
 
-template <typename T, int W, int CH>
-void norm_launch_one(const NormArgs &A, int64_t groups, bool backward, hipStream_t st)
+template <typename T, bool MANY, int CH>
+void norm_launch_one(const NormArgs &A, int waves, int64_t groups, bool backward, hipStream_t st)
 {
-    const dim3 grid((unsigned)groups), block(W == 1 ? 256 : 64 * W);
-    if (backward) hipLaunchKernelGGL((norm_backward<T, W, CH>), grid, block, 0, st, A);
-    else hipLaunchKernelGGL((norm_forward<T, W, CH>), grid, block, 0, st, A);
+    const dim3 grid((unsigned)groups), block(MANY ? 64 * waves : 256);
+    const bool whole = A.channels % Piece<T>::E == 0;
+    const auto kernel = backward ? whole ? norm_backward<T, MANY, CH, true> : norm_backward<T, MANY, CH, false>
+                                 : whole ? norm_forward<T, MANY, CH, true> : norm_forward<T, MANY, CH, false>;
+    hipLaunchKernelGGL(kernel, grid, block, 0, st, A);
 }
 
 template <typename T>
 void norm_launch(const NormArgs &A, const NormPlan &p, int64_t groups, bool backward, hipStream_t st)
 {
-    if (p.waves == 1 && p.pieces == 1) norm_launch_one<T, 1, 1>(A, groups, backward, st);
-    else if (p.waves == 1 && p.pieces == 2) norm_launch_one<T, 1, 2>(A, groups, backward, st);
-    else if (p.waves == 1) norm_launch_one<T, 1, 4>(A, groups, backward, st);
-    else if (p.waves == 4 && p.pieces <= 2) norm_launch_one<T, 4, 2>(A, groups, backward, st);
-    else if (p.waves == 4) norm_launch_one<T, 4, 4>(A, groups, backward, st);
-    else if (sizeof(T) == 2 || p.pieces <= 2) norm_launch_one<T, 16, 2>(A, groups, backward, st);
-    else if constexpr (sizeof(T) == 4) norm_launch_one<T, 16, 4>(A, groups, backward, st);
+    constexpr int most = 16 / Piece<T>::E;
+    if (p.waves > 1) norm_launch_one<T, true, most>(A, p.waves, groups, backward, st);
+    else if (p.pieces == 1) norm_launch_one<T, false, 1>(A, 1, groups, backward, st);
+    else if (p.pieces == 2) norm_launch_one<T, false, 2>(A, 1, groups, backward, st);
+    else norm_launch_one<T, false, most>(A, 1, groups, backward, st);
 }
 
 emb_status norm_launched()
@@ -440,8 +485,7 @@ emb_status norm_launched()
 
 size_t norm_workspace(const emb_norm *d, const NormPlan &p)
 {
-    const int64_t groups = p.groups < kNormGroups ? p.groups : kNormGroups;
-    return (size_t)groups * 2 * d->channels * 4;
+    return (size_t)norm_groups(p, true) * 2 * d->channels * 4;
 }
 
 }  // namespace
@@ -468,8 +512,7 @@ extern "C" emb_status emb_norm_forward(const emb_norm *d, void *y, float *stats,
     NormArgs A = norm_args(d, p);
     A.y = y;
     A.stats = stats;
-    const int64_t most = 8192;
-    const int64_t groups = p.groups < most ? p.groups : most;
+    const int64_t groups = norm_groups(p, false);
     if (d->dtype == EMB_BF16) norm_launch<uint16_t>(A, p, groups, false, static_cast<hipStream_t>(stream));
     else norm_launch<float>(A, p, groups, false, static_cast<hipStream_t>(stream));
     return norm_launched();
@@ -492,7 +535,7 @@ extern "C" emb_status emb_norm_backward(const emb_norm *d, const float *stats, c
     if (sums && d->rows && (workspace_bytes < norm_workspace(d, p) || !workspace || !aligned(workspace, 4)))
         return fail(EMB_ERR_WORKSPACE, "layer norm: the workspace is smaller than the query returned, or not 4-byte aligned");
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const int64_t groups = p.groups < kNormGroups ? p.groups : kNormGroups;
+    const int64_t groups = norm_groups(p, true);
     if (groups) {
         NormArgs A = norm_args(d, p);
         A.stats = const_cast<float *>(stats);
