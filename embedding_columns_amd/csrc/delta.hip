@@ -68,8 +68,8 @@ struct DeltaArgs {
     void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
     int32_t cut;               // samples are cut into segments
     int32_t moves_back;        // ... whose transposed matrices are wanted too
-    float *moves;              // of (segment, head): what it does to a state, [dk, dk] padded (and transposed)
-    int64_t move_size;         // in floats
+    uint16_t *moves;           // of (segment, head): what it does to a state, in parts (and transposed)
+    int64_t move_size;
     float *starts;             // of (segment, head): what it adds, then the state it begins with
     void *o;
     float *last;
@@ -785,29 +785,32 @@ __device__ __forceinline__ Walk walk_of(const DeltaArgs &A)
 
 // a wavefront's 16 columns of a state [dk, dv] in memory: t[a][i] of block x, quarter g is row
 // 32 x + 8 g + 4 a + i
+// the lane's place in a state; columns behind the last are out of its buffer, as are rows
+__device__ __forceinline__ uint32_t state_lane(int dv, int col)
+{
+    return col < dv ? (uint32_t)(8 * (lane_id() >> 4) * dv + col) * 4 : kNowhere;
+}
 template <int KT>
 __device__ __forceinline__ void state_read(Block (&S)[KT], const float *p, int dk, int dv, int col)
 {
-    const int g = lane_id() >> 4;
+    const auto from = row_buffer(p, 0, p ? dk * dv * 4 : 0);
+    const uint32_t at = state_lane(dv, col);
 #pragma unroll
     for (int x = 0; x < KT; x++)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int r = 32 * x + 8 * g + i;
-            S[x].t[i >> 2][i & 3] = p && r < dk && col < dv ? *gp(p + r * dv + col) : 0.f;
-        }
+        for (int i = 0; i < 8; i++)
+            S[x].t[i >> 2][i & 3] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(from, at + (32 * x + i) * dv * 4, 0, 0));
 }
 template <int KT>
 __device__ __forceinline__ void state_write(const Block (&S)[KT], float *p, int dk, int dv, int col)
 {
-    const int g = lane_id() >> 4;
+    const auto to = row_buffer(p, 0, dk * dv * 4);
+    const uint32_t at = state_lane(dv, col);
 #pragma unroll
     for (int x = 0; x < KT; x++)
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int r = 32 * x + 8 * g + i;
-            if (r < dk && col < dv) *gp(p + r * dv + col) = S[x].t[i >> 2][i & 3];
-        }
+        for (int i = 0; i < 8; i++)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[x].t[i >> 2][i & 3]), to, at + (32 * x + i) * dv * 4, 0, 0);
 }
 
 // The state as the gradients read it, rows as operands of 32 x 16 elements: a block is put into
@@ -897,13 +900,18 @@ __device__ __forceinline__ void bring_chunks(const DeltaArgs &A, const Walk &w, 
     }
 }
 
-// Where element (row, col) of a segment's matrix lies, in floats: KBs of 16 rows (one block of
-// registers of a state) x every second 4 of 32 columns, first operands of delta_join.
+// elements of a segment's matrix in its three parts
+template <int KT>
+constexpr int kMove = 3 * 1024 * KT * KT;
+
+// Where element (row, col) of a segment's matrix lies, in bf16, the first of its 3 parts, which
+// are 512 apart: KBs of 16 rows (one block of registers of a state) x 32 columns, first operands
+// of delta_join, those of the same columns side by side.
 template <int KT>
 __device__ __forceinline__ int move_at(int row, int col)
 {
-    const int y = row >> 5, a = row >> 2 & 1, m = (row >> 3 & 3) * 4 + (row & 3), x = col >> 5, g = col >> 3 & 3, c = col >> 2 & 1;
-    return (((y * 2 + a) * KT + x) * 2 + c) * 256 + (g * 16 + m) * 4 + (col & 3);
+    const int y = row >> 5, a = row >> 2 & 1, m = (row >> 3 & 3) * 4 + (row & 3);
+    return (((col >> 5) * KT + y) * 2 + a) * 3 * 512 + ((col >> 3 & 3) * 16 + m) * 8 + (col & 7);
 }
 
 // Walks forward.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
@@ -1009,18 +1017,20 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         if (values) state_write<KT>(S, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         else {
             // the matrix, and for the backward its transpose, as delta_join takes them
-            float *to = A.moves + w.part * A.move_size;
+            uint16_t *to = A.moves + w.part * A.move_size;
             const int g = l >> 4;
 #pragma unroll
-            for (int x = 0; x < KT; x++)
+            for (int x = 0; x < KT; x++) {
+                const Part<3> parts = operand<3>(S[x]);
 #pragma unroll
-                for (int i = 0; i < 8; i++) *gp(to + move_at<KT>(32 * x + 8 * g + i, col)) = S[x].t[i >> 2][i & 3];
-            if (A.moves_back)
+                for (int n = 0; n < 3; n++) {
 #pragma unroll
-                for (int x = 0; x < KT; x++)
-#pragma unroll
-                    for (int a = 0; a < 2; a++)
-                        *gp(reinterpret_cast<f32x4_t *>(to + 1024 * KT * KT + move_at<KT>(col, 32 * x + 8 * g + 4 * a))) = S[x].t[a];
+                    for (int i = 0; i < 8; i++)
+                        *gp(to + move_at<KT>(32 * x + 8 * g + i, col) + 512 * n) = (uint16_t)(parts.p[n][i >> 1] >> 16 * (i & 1));
+                    if (A.moves_back)
+                        *gp(reinterpret_cast<u32x4_t *>(to + kMove<KT> + move_at<KT>(col, 32 * x + 8 * g) + 512 * n)) = parts.p[n];
+                }
+            }
         }
         return;
     }
@@ -1127,69 +1137,81 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 
 // The states at the edges of a cut sample's segments, one after another: S' = move S + added
 // (BACK: from the last, with the move transposed).  A wavefront has 16 columns of a sample's
-// and head's state, the last brings the moves one ahead.  What a segment adds is replaced by
-// the state that it begins with.
+// and head's state, four of them (one a SIMD) share a workgroup and a fifth that brings the
+// moves, 32 of their columns at a time and several such steps ahead (three: 75 us for the below).  They come in the parts that
+// the products take: cut into them by every wavefront again, they took most of the time (64
+// segments of 64 x 128: 190 us, and 69 us so).  What a segment adds is replaced by the state
+// that it begins with.
+constexpr int kJoined = 4;
+// steps on their way behind the one that is waited for (at most 63 loads are counted), and places
+template <int KT>
+constexpr int kJoinAhead = KT == 1 ? 6 : 10 / KT;
+template <int KT>
+constexpr int kJoinRing = kJoinAhead<KT> + 2;
+
 template <int KT, bool BACK>
-__global__ __launch_bounds__(576) void delta_join(DeltaArgs A)
+__global__ __launch_bounds__(64 * kJoined + 64) void delta_join(DeltaArgs A)
 {
     extern __shared__ __attribute__((aligned(1024))) char lds[];
-    constexpr int stage = KT * KT * 4096;
+    constexpr int pieces = 6 * KT, stage = pieces * 1024;
     const int sample = blockIdx.x / (uint32_t)A.heads, head = blockIdx.x - (uint32_t)sample * (uint32_t)A.heads;
-    constexpr int back = BACK ? 1024 * KT * KT : 0;      // the transposed matrices lie behind the others
-    const int l = lane_id(), slice = uniform((int)(threadIdx.x >> 6)), col = 16 * slice + (l & 15);
+    const int l = lane_id(), wave = uniform((int)(threadIdx.x >> 6)), slice = blockIdx.y * kJoined + wave, col = 16 * slice + (l & 15);
     const int base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
     const int rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - base, 0);
     const int parts = (rows + kSpan - 1) / kSpan, part0 = base / kSpan + sample + 1;
     const int64_t matrix = (int64_t)sample * A.heads + head;
     const uint32_t at0 = lds_address(lds);
     auto number = [&](int j) { return (int64_t)(part0 + (BACK ? parts - 1 - j : j)) * A.heads + head; };
-    if (slice == A.slices) {
-        if (parts > 1) bring_flat(row_rsrc(A.moves + number(0) * A.move_size + back), at0, stage / 1024, 0, 1);
-        for (int j = 0; j + 1 < parts; j++) {
-            meet();
-            if (j + 2 < parts)
-                bring_flat(row_rsrc(A.moves + number(j + 1) * A.move_size + back), at0 + (~j & 1) * stage, stage / 1024, 0, 1);
+    if (wave == kJoined) {
+        const int steps = (parts - 1) * KT;
+        int j = 0, x = 0, place = 0;                     // of the step that is asked for next
+        auto bring = [&] {
+            const i32x4_t rsrc = row_rsrc(A.moves + number(j) * A.move_size + (BACK ? kMove<KT> : 0) + x * (stage / 2));
+            const uint32_t to = (uint32_t)uniform((int)(at0 + place * stage));
+#pragma unroll
+            for (int p = 0; p < pieces; p++) load_to_lds(rsrc, to + p * 1024, 16 * l, p * 1024);
+            if (++x == KT) x = 0, j++;
+            if (++place == kJoinRing<KT>) place = 0;
+        };
+        for (int s = 0; s < min(steps, kJoinAhead<KT> + 1); s++) bring();
+        for (int s = 0; s < steps; s++) {
+            // step s is there if only the ones behind it, asked for already, may be missing
+            if (s + kJoinAhead<KT> < steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kJoinAhead<KT> * pieces) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            meet_others();                               // and everyone is done with step s - 1
+            if (s + kJoinAhead<KT> + 1 < steps) bring();
         }
         return;
     }
+    if (slice >= A.slices) return;
     const float *from = BACK ? A.dlast : A.state;
-    // what is added is read two segments ahead, so that its wait is not one for the stores between
-    Block S[KT], added[KT], next[KT];
+    // What is added is read two segments ahead, so that its wait is not one for the stores between.
+    // Registers change roles instead of places: a copy would wait for what is on its way.
+    Block S[KT], one[KT], two[KT], three[KT];
     state_read<KT>(S, from ? from + matrix * A.dk * A.dv : nullptr, A.dk, A.dv, col);
-    if (parts) state_read<KT>(added, A.starts + number(0) * A.dk * A.dv, A.dk, A.dv, col);
-    if (parts > 1) state_read<KT>(next, A.starts + number(1) * A.dk * A.dv, A.dk, A.dv, col);
+    if (parts) state_read<KT>(one, A.starts + number(0) * A.dk * A.dv, A.dk, A.dv, col);
+    if (parts > 1) state_read<KT>(two, A.starts + number(1) * A.dk * A.dv, A.dk, A.dv, col);
     if (parts) state_write<KT>(S, A.starts + number(0) * A.dk * A.dv, A.dk, A.dv, col);
-    for (int j = 0; j + 1 < parts; j++) {
-        Block after[KT];
-        meet_others();
+    int place = 0;
+    auto step = [&](int j, const Block(&S)[KT], Block(&added)[KT], Block(&after)[KT]) {
+        if (j + 1 >= parts) return false;
         if (j + 2 < parts) state_read<KT>(after, A.starts + number(j + 2) * A.dk * A.dv, A.dk, A.dv, col);
-        const uint32_t at = at0 + (j & 1) * stage + 16 * l;
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<3> sp = operand<3>(S[x]);
+            meet_others();
+            const uint32_t at = at0 + place * stage;
+            if (++place == kJoinRing<KT>) place = 0;
 #pragma unroll
             for (int y = 0; y < KT; y++)
 #pragma unroll
-                for (int a = 0; a < 2; a++) {
-                    float f[8];
-                    const uint32_t p = at + ((y * 2 + a) * KT + x) * 2048;
-                    const u32x4_t lo = lds_read<u32x4_t>(p), hi = lds_read<u32x4_t>(p + 1024);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        f[e] = __uint_as_float(lo[e]);
-                        f[4 + e] = __uint_as_float(hi[e]);
-                    }
-                    mm<3>(added[y].t[a], split8<3>(f), sp);
-                }
+                for (int a = 0; a < 2; a++) mm<3>(added[y].t[a], staged<3>(at, 2 * y + a), sp);
         }
-#pragma unroll
-        for (int x = 0; x < KT; x++) {
-            S[x] = added[x];
-            added[x] = next[x];
-            next[x] = after[x];
-        }
-        state_write<KT>(S, A.starts + number(j + 1) * A.dk * A.dv, A.dk, A.dv, col);
-    }
+        state_write<KT>(added, A.starts + number(j + 1) * A.dk * A.dv, A.dk, A.dv, col);
+        return true;
+    };
+    for (int j = 0;; j += 4)
+        if (!step(j, S, one, three) || !step(j + 1, one, two, S) || !step(j + 2, two, three, one) || !step(j + 3, three, S, two)) break;
     if (parts) return;                                   // a sample without rows hands its state on
     float *to = BACK ? A.dstate : A.last;
     if (to) state_write<KT>(S, to + matrix * A.dk * A.dv, A.dk, A.dv, col);
@@ -1675,7 +1697,7 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 512 * p.el;
     if (p.cut) {
         const size_t segments = (size_t)seg_tiles(d->n, d->samples, 1, kSpan) * d->heads;
-        p.move = (size_t)p.kt * p.kt * 4096 * (train ? 2 : 1);
+        p.move = (size_t)p.kt * p.kt * 6144 * (train ? 2 : 1);
         p.moves = segments * p.move;
         p.starts = pad256(segments * d->dk * d->dv * 4);
     }
@@ -1747,7 +1769,7 @@ DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
     A.scale = d->scale;
     A.rec_size = (int64_t)p.rec;
     A.cut = p.cut;
-    A.move_size = (int64_t)p.move / 4;
+    A.move_size = (int64_t)p.move / 2;
     return A;
 }
 
@@ -1757,7 +1779,7 @@ void delta_saved(const DeltaPlan &p, DeltaArgs &A, char *saved)
     A.rec = saved;
     A.s0 = saved + p.recs;
     A.u = saved + p.recs + p.states;
-    A.moves = reinterpret_cast<float *>(saved + p.recs + p.states + p.us);
+    A.moves = reinterpret_cast<uint16_t *>(saved + p.recs + p.states + p.us);
 }
 
 int64_t delta_walks(const emb_delta *d, const DeltaPlan &p)
@@ -1787,7 +1809,8 @@ template <typename T, int KT>
 void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool train, hipStream_t st)
 {
     const dim3 walk((unsigned)walks);
-    const int join = 2 * KT * KT * 4096;
+    const int join = kJoinRing<KT> * KT * 6144;
+    const dim3 joins((unsigned)(A.samples * A.heads), (unsigned)((A.slices + kJoined - 1) / kJoined));
     delta_launch(delta_prepare<T, KT>, dim3((unsigned)tiles, (unsigned)A.heads), 64, 0, A, st);
     if (!walks) return;
     if (A.cut) {
@@ -1795,7 +1818,7 @@ void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool
         const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
         delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * most + 64, 2 * WalkLds<T, KT, true>::size(A.slices),
                      A, st);
-        delta_launch(delta_join<KT, false>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
+        delta_launch(delta_join<KT, false>, joins, 64 * kJoined + 64, join, A, st);
     }
     const int lds = 2 * WalkLds<T, KT, false>::size(A.slices) + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
     if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices + 64, lds, A, st);
@@ -1806,10 +1829,11 @@ template <typename T, int KT>
 void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool, hipStream_t st)
 {
     const dim3 walk((unsigned)walks);
-    const int lds = 2 * WalkLds<T, KT, false>::size(A.slices), join = 2 * KT * KT * 4096;
+    const int lds = 2 * WalkLds<T, KT, false>::size(A.slices), join = kJoinRing<KT> * KT * 6144;
+    const dim3 joins((unsigned)(A.samples * A.heads), (unsigned)((A.slices + kJoined - 1) / kJoined));
     if (walks && A.cut) {
         delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, lds, A, st);
-        delta_launch(delta_join<KT, true>, dim3((unsigned)(A.samples * A.heads)), 64 * A.slices + 64, join, A, st);
+        delta_launch(delta_join<KT, true>, joins, 64 * kJoined + 64, join, A, st);
     }
     if (walks)
         delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64,
@@ -1867,7 +1891,7 @@ extern "C" emb_status emb_delta_forward(const emb_delta *d, void *o, float *last
     if (train) delta_saved(p, A, static_cast<char *>(saved));
     else {
         A.rec = ws;
-        A.moves = reinterpret_cast<float *>(ws + p.recs);
+        A.moves = reinterpret_cast<uint16_t *>(ws + p.recs);
         ws += p.recs + p.moves;
     }
     A.starts = reinterpret_cast<float *>(ws);
