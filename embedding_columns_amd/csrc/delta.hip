@@ -51,9 +51,9 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 constexpr int kCut = 32;                 // rows of a chunk
 constexpr int kSpan = 1024;              // rows of a segment of a cut sample
 constexpr int kDeltaDim = 128;           // largest head size
-// the scalars of a chunk and head, in floats
-constexpr int kScB = 0, kScBG = 32, kScG = 64, kScW = 96, kScHi = 128, kScLo = 160, kScEnd = 192, kScKept = 193,
-              kScalars = 256;
+// the scalars of a chunk and head, in floats: what the walks take, and what the gradients take too
+constexpr int kScB = 0, kScBG = 32, kScG = 64, kScW = 96, kScEnd = 127, kScWalk = 128, kScHi = 128, kScLo = 160,
+              kScKept = 192, kScalars = 256;
 
 struct DeltaArgs {
     const void *q, *k, *v, *gate, *beta;            // rows and heads any stride apart (elements)
@@ -145,6 +145,21 @@ __device__ __forceinline__ void mm(f32x4_t &acc, const Part<NA> &a, const Part<N
                                                               __builtin_bit_cast(bf16x8_t, b.p[s - i]), acc, 0, 0, 0);
 }
 
+// ... over 16 elements, the first or the second half of b's
+template <int ORD, int NA, int NB>
+__device__ __forceinline__ void mm_half(f32x4_t &acc, const u32x2_t (&a)[NA], const Part<NB> &b, int half)
+{
+#pragma unroll
+    for (int s = ORD - 1; s >= 0; s--)
+#pragma unroll
+        for (int i = 0; i < NA; i++)
+            if (s - i >= 0 && s - i < NB) {
+                const u32x4_t w = b.p[s - i];
+                acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(
+                    __builtin_bit_cast(s16x4_t, a[i]), __builtin_bit_cast(s16x4_t, u32x2_t{w[2 * half], w[2 * half + 1]}), acc, 0, 0, 0);
+            }
+}
+
 // 32 rows x 16 columns of a walk: t[a][i] of quarter g is row 16 a + 4 g + i
 struct Block {
     f32x4_t t[2];
@@ -228,13 +243,20 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
     return row_buffer(static_cast<const T *>(p) + elements, 0, 0x7FFFFFFF);
 }
 
-// A record: N - I in NN parts, P in OUT, the scalars.  A part is 16 rows x 32 columns a KB, a
-// row's 4 pieces of 16 bytes side by side, piece g (columns 4 g .. and 16 + 4 g ..) of row r at
-// g ^ (r >> 2); see Lane.
+// A record: the scalars of the walks, N - I in NN parts, P in OUT, the other scalars.  The matrices
+// are triangular.  A part is rows 16 .. in a KB, a row's 4 pieces of 16 bytes side by side, piece g
+// (columns 4 g .. and 16 + 4 g ..) of row r at g ^ (r >> 2), see Lane, and columns .. 15 of the
+// other rows in 512 bytes, pieces of 8 bytes, g of row r at g ^ (r >> 3) * 2 (so that 32 lanes that
+// read 16 rows meet every bank once).  Whole matrices took 11 KB of bf16 records for 8.5, and
+// delta_histories 421 us for 374.
+constexpr int kMatrix = 3 * 512;
 template <typename T>
 struct Rec {
-    static constexpr int n = 0, p = 2 * Prec<T>::NN * 1024, sc = p + 2 * Prec<T>::OUT * 1024, size = sc + kScalars * 4;
+    static constexpr int sc = 0, n = kScWalk * 4, p = n + Prec<T>::NN * kMatrix, more = p + Prec<T>::OUT * kMatrix,
+                         size = more + (kScalars - kScWalk) * 4;
 };
+__device__ __forceinline__ uint32_t matrix_above(int row, int quad) { return 1024 + (row * 4 + (quad ^ (row >> 3) * 2)) * 8; }
+__device__ __forceinline__ uint32_t matrix_below(int row, int piece) { return (row * 4 + (piece ^ (row >> 2))) * 16; }
 
 // e^(hi + lo): the product with log2(e) to more bits than one rounding
 __device__ __forceinline__ float exp_of(float hi, float lo)
@@ -302,15 +324,17 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         sc[kScB + c] = b;
         sc[kScBG + c] = b * G;
         sc[kScG + c] = A.scale * G;
-        sc[kScW + c] = W;
+        sc[kScW + c] = c == 31 ? G : W;                  // W of the last row is 1: G_32 is there
         sc[kScHi + c] = hi;
         sc[kScLo + c] = lo;
-        if (c == 31) sc[kScEnd] = G;
-        if (c == 30) sc[kScKept] = __uint_as_float(kept);
+        if (c == 31) sc[kScKept] = __uint_as_float(kept);
     }
     wave_sync();
     char *rec = A.rec + ((int64_t)tile * A.heads + head) * A.rec_size;
-    *gp(reinterpret_cast<f32x4_t *>(rec + Rec<T>::sc) + l) = *reinterpret_cast<const f32x4_t *>(sc + 4 * l);
+    // what only the gradients take is left for them alone
+    if (l < kScWalk / 4 || A.s0 || l == kScKept / 4)
+        *gp(reinterpret_cast<f32x4_t *>(rec + (l < kScWalk / 4 ? Rec<T>::sc : Rec<T>::more - kScWalk * 4)) + l) =
+            *reinterpret_cast<const f32x4_t *>(sc + 4 * l);
 
     const auto qb = buffer<T>(A.q, row * A.qs + key * A.qh), kb = buffer<T>(A.k, row * A.ks + key * A.kh);
     const uint32_t qat = keep ? (uint32_t)(c * A.qs * sizeof(T)) : kNowhere;
@@ -354,8 +378,11 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
             }
             const Part<N> p = split8<N>(f);
 #pragma unroll
-            for (int i = 0; i < N; i++)
-                *gp(reinterpret_cast<u32x4_t *>(rec + at + (2 * i + a) * 1024) + (row * 4 + (g ^ (row >> 2)))) = p.p[i];
+            for (int i = 0; i < N; i++) {
+                char *to = rec + at + i * kMatrix;
+                if (a) *gp(reinterpret_cast<u32x4_t *>(to + matrix_below(row, g))) = p.p[i];
+                else *gp(reinterpret_cast<u32x2_t *>(to + matrix_above(row, g))) = u32x2_t{p.p[i][0], p.p[i][1]};
+            }
         }
     };
     wave_sync();
@@ -519,7 +546,7 @@ template <typename T>
 struct Lane {
     static constexpr int R = sizeof(T) / 2, kTile = 1024 * R;      // bytes of 16 rows x 32 elements
     uint32_t rows, keys;     // where the lane's first operands begin: rows, and columns for the state's update
-    uint32_t turned;         // ... and columns of a record's matrix
+    uint32_t above, turned, turned_above;   // ... and rows and columns of a record's matrix
     int r, q;                // (bf16) its row and quad of a column
 
     __device__ __forceinline__ Lane()
@@ -528,9 +555,11 @@ struct Lane {
         rows = (i * 4 + (g ^ (i >> 2))) * 16;
         r = 4 * g + (i >> 2);
         q = i & 3;
+        above = matrix_above(i, g);
+        turned_above = matrix_above(r, q);
         // State rows are kept so that the registers of a block meet rows of K and Q as they lie in
         // memory: t[a][i] of quarter g is row 8 g + 4 a + i.
-        turned = (r * 4 + (q ^ g)) * 16;
+        turned = matrix_below(r, q);
         if (R == 1) keys = turned;
         else keys = (16 * g + ((i >> 2) ^ g)) * 16 + (i & 3) * 4;
     }
@@ -554,12 +583,10 @@ struct Lane {
     __device__ __forceinline__ typename Row<T>::Op column(uint32_t at, int x, int a) const
     {
         if constexpr (R == 1) {
-            // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
             u32x4_t w;
 #pragma unroll
             for (int j = 0; j < 2; j++) {
-                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + keys + (x * 2 + j) * kTile + 8 * a)));
+                const u32x2_t v = __builtin_bit_cast(u32x2_t, column4(at + keys + (x * 2 + j) * kTile + 8 * a));
                 w[2 * j] = v[0];
                 w[2 * j + 1] = v[1];
             }
@@ -571,29 +598,39 @@ struct Lane {
             return split8<3>(f);
         }
     }
-    // rows 16 a .. of a record's matrix as an operand, and columns 16 a ..
-    template <int N>
-    __device__ __forceinline__ Part<N> matrix(uint32_t at, int a) const
+    // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
+    static __device__ __forceinline__ s16x4_t column4(uint32_t at)
     {
-        Part<N> p;
-#pragma unroll
-        for (int i = 0; i < N; i++) p.p[i] = lds_read<u32x4_t>(at + rows + (2 * i + a) * 1024);
-        return p;
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t *)(uintptr_t)at);
     }
-    template <int N>
-    __device__ __forceinline__ Part<N> matrix_turned(uint32_t at, int a) const
+    // acc += a record's matrix times x, and the matrix transposed times x
+    template <int ORD, int N, int NB>
+    __device__ __forceinline__ void matrix(Block &acc, uint32_t at, const Part<NB> &x) const
     {
-        Part<N> p;
+        u32x2_t upper[N];
+        Part<N> lower;
 #pragma unroll
-        for (int i = 0; i < N; i++)
+        for (int i = 0; i < N; i++) {
+            upper[i] = lds_read<u32x2_t>(at + above + i * kMatrix);
+            lower.p[i] = lds_read<u32x4_t>(at + rows + i * kMatrix);
+        }
+        mm_half<ORD>(acc.t[0], upper, x, 0);
+        mm<ORD>(acc.t[1], lower, x);
+    }
+    template <int ORD, int N, int NB>
+    __device__ __forceinline__ void matrix_turned(Block &acc, uint32_t at, const Part<NB> &x) const
+    {
+        Part<N> left;
+        u32x2_t right[N];
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const u32x2_t v = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + turned + (2 * i + j) * 1024 + 8 * a)));
-                p.p[i][2 * j] = v[0];
-                p.p[i][2 * j + 1] = v[1];
-            }
-        return p;
+        for (int i = 0; i < N; i++) {
+            const uint32_t from = at + i * kMatrix;
+            const u32x2_t y = __builtin_bit_cast(u32x2_t, column4(from + turned_above)), z = __builtin_bit_cast(u32x2_t, column4(from + turned));
+            left.p[i] = u32x4_t{y[0], y[1], z[0], z[1]};
+            right[i] = __builtin_bit_cast(u32x2_t, column4(from + turned + 8));
+        }
+        mm<ORD>(acc.t[0], left, x);
+        mm_half<ORD>(acc.t[1], right, x, 1);
     }
     // where columns 16 slice .. begin, and these as a block
     __device__ __forceinline__ uint32_t columns(int slice) const
@@ -609,8 +646,7 @@ struct Lane {
 #pragma unroll
         for (int a = 0; a < 2; a++)
             if constexpr (R == 1) {
-                const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t *)(uintptr_t)(at + columns + a * kTile));
+                const s16x4_t v = column4(at + columns + a * kTile);
 #pragma unroll
                 for (int e = 0; e < 4; e++) b.t[a][e] = __uint_as_float((uint32_t)(uint16_t)v[e] << 16);
             } else {
@@ -644,6 +680,14 @@ __device__ __forceinline__ Block row_scalars(uint32_t at)
     Block r;
 #pragma unroll
     for (int a = 0; a < 2; a++) r.t[a] = lds_read<f32x4_t>(at + 64 * a + 16 * (lane_id() >> 4));
+    return r;
+}
+
+// W: its last place in a record is G_32's
+__device__ __forceinline__ Block row_weights(uint32_t sc)
+{
+    Block r = row_scalars(sc + 4 * kScW);
+    if (lane_id() >> 4 == 3) r.t[1][3] = 1.f;
     return r;
 }
 
@@ -856,8 +900,8 @@ __device__ __forceinline__ void state_keep(uint32_t scratch, char *to, int slice
 // ahead, and does nothing else.  SUM walks take no Q and no P.
 template <typename T, int KT, bool SUM>
 struct WalkLds {
-    static constexpr int q = 2 * KT * Lane<T>::kTile, n = SUM ? q : 2 * q, p = n + Rec<T>::p, sc = SUM ? p : n + Rec<T>::sc,
-                         v = sc + kScalars * 4;
+    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = SUM ? q : 2 * q, sc = rec + Rec<T>::sc, n = rec + Rec<T>::n,
+                         p = rec + Rec<T>::p, pieces = ((SUM ? Rec<T>::p : Rec<T>::more) + 1023) / 1024, v = rec + pieces * 1024;
     static __host__ __device__ constexpr int size(int slices) { return v + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 
@@ -868,7 +912,7 @@ __device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w,
     const int left = min(w.rows - chunk * kCut, kCut);
     if (chunk < 0 || left <= 0) return 0;
     const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
-    return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::sc) + kScKept)) & low_bits(left);
+    return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::more) + kScKept - kScWalk)) & low_bits(left);
 }
 
 // The wavefront that brings the chunks, in the order chunk(0), chunk(1), ... (steps of the walk);
@@ -886,8 +930,7 @@ __device__ __forceinline__ void bring_chunks(const DeltaArgs &A, const Walk &w, 
         if (values) bring_tiles<T>(static_cast<const T *>(values) + row * vs + w.head * vh, vs, kept, to + L::v, (A.slices + 1) / 2);
         const i32x4_t rsrc = row_rsrc(A.rec + ((int64_t)(w.tile0 + chunk(s)) * A.heads + w.head) * A.rec_size);
 #pragma unroll
-        for (int p = 0; p < (SUM ? Rec<T>::p : Rec<T>::size); p += 1024) load_to_lds(rsrc, to + L::n + p, 16 * lane_id(), p);
-        if (SUM) load_to_lds(rsrc, to + L::sc, 16 * lane_id(), Rec<T>::sc);
+        for (int p = 0; p < L::pieces; p++) load_to_lds(rsrc, to + L::rec + p * 1024, 16 * lane_id(), p * 1024);
     };
     if (!chunks) return;
     uint32_t kept = kept_rows<T>(A, w, chunk(0)), next = kept_rows<T>(A, w, chunks > 1 ? chunk(1) : -1);
@@ -976,9 +1019,8 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
             for (int e = 0; e < 4; e++) X.t[a][e] = fmaf(b.t[a][e], V.t[a][e], -bg.t[a][e] * X.t[a][e]);
         const Part<ST> xp = operand<ST>(X);
         Block U = X;                                     // N is I and what the record has
-#pragma unroll
-        for (int a = 0; a < 2; a++) mm<ST>(U.t[a], lane.template matrix<NN>(at + L::n, a), xp);
-        const Block wt = row_scalars(sc + 4 * kScW);
+        lane.template matrix<ST, NN>(U, at + L::n, xp);
+        const Block wt = row_weights(sc);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block wu = U;
 #pragma unroll
@@ -1002,8 +1044,8 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
             for (int a = 0; a < 2; a++) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) Y.t[a][e] *= sg.t[a][e];
-                mm<OUT>(Y.t[a], lane.template matrix<OUT>(at + L::p, a), op);
             }
+            lane.template matrix<OUT, OUT>(Y, at + L::p, op);
             if (TRAIN) Turn<T>::leave(scratch, U, op.p[0], op.p[1], u);
             Turn<T> rows;
             rows.turn(scratch, Y);
@@ -1081,19 +1123,18 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 #pragma unroll
             for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
         }
-        const Block wt = row_scalars(sc + 4 * kScW);
+        const Block wt = row_weights(sc);
         Block D = lane.block(at + L::v, columns);
         const Part<IN> dp = operand<IN>(D);
 #pragma unroll
         for (int a = 0; a < 2; a++) {
 #pragma unroll
             for (int e = 0; e < 4; e++) X.t[a][e] *= wt.t[a][e];
-            mm<ST>(X.t[a], lane.template matrix_turned<OUT>(at + L::p, a), dp);
         }
+        lane.template matrix_turned<ST, OUT>(X, at + L::p, dp);
         const Part<ST> xp = operand<ST>(X);
         Block Z = X;
-#pragma unroll
-        for (int a = 0; a < 2; a++) mm<ST>(Z.t[a], lane.template matrix_turned<NN>(at + L::n, a), xp);
+        lane.template matrix_turned<ST, NN>(Z, at + L::n, xp);
         const Block bg = row_scalars(sc + 4 * kScBG), sg = row_scalars(sc + 4 * kScG);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block gz = Z;
@@ -1299,7 +1340,7 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
     auto bring = [&](int head) {
         const int64_t number = (int64_t)tile * A.heads + head;
         const int n = A.slices;
-        if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size + Rec<T>::sc), at + L::sc, 16 * l, 0);
+        if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size), at + L::sc, 16 * l + (l < kScWalk / 4 ? Rec<T>::sc : Rec<T>::more - kScWalk * 4), 0);
         bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * 2048), at + L::u, 2 * n, wave, KT);
         bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * 2048), at + L::u + n * 2048, 2 * n, wave, KT);
         bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + head * A.dh), row_at<T>(kept, A.ds),
@@ -1329,7 +1370,7 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
             }
         meet();
         const float b = lds_read<float>(sc + 4 * (kScB + c)), bg = lds_read<float>(sc + 4 * (kScBG + c)),
-                    sg = lds_read<float>(sc + 4 * (kScG + c)), wt = lds_read<float>(sc + 4 * (kScW + c)),
+                    sg = lds_read<float>(sc + 4 * (kScG + c)), wt = c == 31 ? 1.f : lds_read<float>(sc + 4 * (kScW + c)),
                     hi = lds_read<float>(sc + 4 * (kScHi + c)), lo = lds_read<float>(sc + 4 * (kScLo + c)),
                     end = lds_read<float>(sc + 4 * kScEnd);
         // lane x: what k_y (or q_y) is taken with, in register y; `across`: the lane's row or
@@ -1676,10 +1717,18 @@ struct DeltaPlan {
 };
 
 // Samples are cut into segments where there are too few of them, times the heads, to fill the
-// chip.  A cut walk is walked twice and its segments are joined one after another.
+// chip.  A cut walk is walked twice and its segments are joined one after another.  Heads of 64 in
+// bf16, forward / with the backward, in us, uncut and cut:
+//   walks x rows      4 x 2048         4 x 4096         32 x 2048       64 x 2048        64 x 4096
+//   uncut / cut       88, 210          162, 383         94, 243         99, 285          181, 546
+//                     89, 206          94, 214          97, 243         114, 297         169, 514
+//   walks x rows      4 x 16384        32 x 16384       64 x 16384      128 x 4096       128 x 16384
+//   uncut / cut       592, 1444        669, 1745        728, 2093       241, 734         878, 2785
+//                     114, 278         328, 885         621, 1731       299, 921         1166, 3304
 bool delta_cut(const emb_delta *d)
 {
-    return d->samples && d->n / d->samples >= 2 * kSpan && (int64_t)d->samples * d->heads < 128;
+    const int64_t walks = (int64_t)d->samples * d->heads;
+    return d->samples && walks <= 64 && d->n / d->samples >= (walks <= 32 ? 2 : 4) * kSpan;
 }
 
 DeltaPlan delta_plan(const emb_delta *d, bool train)
