@@ -4,7 +4,11 @@ of the behaviours, candidates attend to them with a bias by elapsed time, and a 
 loss trains everything, the tables by the stage's own sparse Adagrad.  Afterwards the
 same model serves one new event and one candidate at a time.
 
-    python examples/sequence_ranking.py [--steps N]
+    python examples/sequence_ranking.py [--steps N] [--encoder recurrence|delta]
+
+With --encoder delta the states are matrices: rows are normed, keys and queries of the gated
+delta rule and of the attention are turned by the time of their event, and a stored state takes
+one event by the rule's single step.
 
 Synthetic data: a candidate is clicked iff it equals an item of the last hour.
 Needs the GPU and the built library; prints the loss and how many are told right."""
@@ -72,10 +76,15 @@ class Ranker(torch.nn.Module):
         offsets = torch.arange(self.most + 1, dtype=torch.int32, device=ids.device).clamp(max=n)
         return self.stage(offsets, ids=ids)[:n]
 
-    def encode(self, rows, offsets):
+    def encode(self, rows, offsets, pos):
         x, gate = self.gates(rows).split(DIM, dim=1)
         states, last = E.gated_recurrence(x, gate, offsets)
         return self.key_values(rows, states), last
+
+    def step(self, rows, last, pos):
+        """One new event for each stored state, which is updated; and what it adds to k and v."""
+        x, gate = self.gates(rows).split(DIM, dim=1)
+        return self.key_values(rows, E.gated_recurrence_step(x, gate, last))
 
     def key_values(self, rows, states):
         k, v = self.keys(torch.cat([rows, states], 1)).split(DIM, dim=1)
@@ -90,15 +99,48 @@ class Ranker(torch.nn.Module):
     def forward(self, b):
         n = b.items.numel()
         rows = self.rows(torch.cat([b.items, b.cands]))     # one lookup, one update of the table
-        kv, _ = self.encode(rows[:n], b.ko)
+        kv, _ = self.encode(rows[:n], b.ko, b.k_pos)
         return self.rank(rows[n:], b.qo, b.q_pos, kv, b.ko, b.k_pos)
 
 
-def main(steps=300, samples=128, quiet=False):
+class DeltaRanker(Ranker):
+    """The same with matrix states over normed rows, and positions in keys and queries."""
+
+    def __init__(self, dev, most):
+        super().__init__(dev, most)
+        self.gates = torch.nn.Linear(DIM, 3 * DIM + 2 * HEADS, device=dev)   # q, k, v, gate and beta
+        self.scale, self.shift = (torch.nn.Parameter(x(DIM, device=dev)) for x in (torch.ones, torch.zeros))
+        self.frequencies = E.rotary_frequencies(DIM // HEADS, base=1e4, device=dev) / 60   # a turn is minutes and more
+
+    def inputs(self, rows, pos):
+        made = self.gates(E.layer_norm(rows, self.scale, self.shift))
+        q, k, v, gate, beta = made.split([DIM, DIM, DIM, HEADS, HEADS], dim=1)
+        q, k, v = (x.view(-1, HEADS, DIM // HEADS) for x in (q, k, v))
+        k = torch.nn.functional.normalize(k, dim=-1)
+        q, k = E.rotary(q, k, pos, pos, self.frequencies)
+        return q, k, v, gate + 3.0, beta                   # mostly remembering
+
+    def encode(self, rows, offsets, pos):
+        states, last = E.gated_delta(*self.inputs(rows, pos), offsets)
+        return self.key_values(rows, states.reshape(-1, DIM)), last
+
+    def step(self, rows, last, pos):
+        states = E.gated_delta_step(*self.inputs(rows, pos), last)
+        return self.key_values(rows, states.reshape(-1, DIM))
+
+    def rank(self, cand_rows, qo, q_pos, kv, ko, k_pos):
+        q = self.query(cand_rows).view(-1, HEADS, DIM // HEADS)
+        q, k = E.rotary(q, kv[0], q_pos, k_pos, self.frequencies)
+        read = E.cross_attention(q, k, kv[1], qo, ko, bias=self.bias, boundaries=self.boundaries,
+                                 q_pos=q_pos, k_pos=k_pos).reshape(-1, DIM)
+        return self.score(torch.cat([read * cand_rows, read], 1))[:, 0]
+
+
+def main(steps=300, samples=128, quiet=False, encoder="recurrence"):
     dev = torch.device("cuda")
     torch.manual_seed(1)
     gen = torch.Generator().manual_seed(2)
-    model = Ranker(dev, most=samples * 70)
+    model = {"recurrence": Ranker, "delta": DeltaRanker}[encoder](dev, most=samples * 70)
     opt = torch.optim.Adam(model.parameters(), lr=3e-3)
     for step in range(steps):
         b = batch(samples, gen, dev)
@@ -113,13 +155,11 @@ def main(steps=300, samples=128, quiet=False):
         right = float(((model(b) > 0) == (b.label > 0.5)).float().mean())
         # serving: a stored state takes one event, one candidate reads the longer sequence
         rows = model.rows(b.items)
-        kv, last = model.encode(rows, b.ko)
+        kv, last = model.encode(rows, b.ko, b.k_pos)
         event = torch.randint(0, ITEMS, (samples,), generator=gen).to(dev)
         event_rows = model.rows(event)
-        x, gate = model.gates(event_rows).split(DIM, dim=1)
-        state = last.clone()
-        states = E.gated_recurrence_step(x, gate, state)
-        new_kv = model.key_values(event_rows, states)
+        now = torch.full((samples,), 100_000, dtype=torch.int32, device=dev)
+        new_kv = model.step(event_rows, last.clone(), now - 30)
         ends = b.ko[1:].long()
         at = torch.arange(samples, device=dev)
         spots = torch.ones(len(b.items) + samples, dtype=torch.bool, device=dev)
@@ -131,7 +171,6 @@ def main(steps=300, samples=128, quiet=False):
             return t
         ko = (b.ko + torch.arange(samples + 1, device=dev)).int()
         one = torch.arange(samples + 1, dtype=torch.int32, device=dev)
-        now = torch.full((samples,), 100_000, dtype=torch.int32, device=dev)
         scores = model.rank(event_rows, one, now, [grown(o, n) for o, n in zip(kv, new_kv)], ko,
                             grown(b.k_pos, now - 30))
     repeat = float((scores > 0).float().mean())
@@ -143,4 +182,6 @@ def main(steps=300, samples=128, quiet=False):
 if __name__ == "__main__":
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=300)
-    main(ap.parse_args().steps)
+    ap.add_argument("--encoder", choices=("recurrence", "delta"), default="recurrence")
+    args = ap.parse_args()
+    main(args.steps, encoder=args.encoder)
