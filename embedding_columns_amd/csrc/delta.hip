@@ -25,6 +25,13 @@
 // (all chunks side by side) makes the gradients that need both sides' states.  The walks
 // take 16 columns of the state per wavefront, which never meet one another.
 //
+// What passes between them costs more than the rows themselves: what bounds the four is bytes,
+// then a walk's chain of dependent products.  bf16, 287434 rows in 256 samples, 4 heads of
+// 64 x 64: prepare 133 us (0.59 GB, 4.5 TB/s), scan 242 us (0.95 GB, 3.9 TB/s).  With
+// gradients, 68548 rows in 64 samples, 4 heads of 128 x 128: prepare 59 us, scan 200 us and back
+// 224 us (0.8 GB each; the longest of 256 walks on 256 CUs is twice the mean), grads 305 us
+// (1.25 GB, 4.1 TB/s).
+//
 // All products run on the matrix cores, the walks' in blocks of 16 x 16 (lane & 15 a column,
 // register i of quarter g = lane >> 4 row 4 g + i), the others' in 32 x 32 (lane & 31 a column,
 // register i of half h = lane >> 5 row kk(i, h) = 8 (i >> 2) + 4 h + (i & 3)), which is also how
@@ -32,8 +39,9 @@
 // is fp32.  What enters a product is cut into bf16 parts, the first rounded from the value,
 // the next from what is left of it: inputs in bf16 are one part, fp32 ones three (24 bits);
 // the state and what makes it (N, U, Z, P^T) are three, so that the states that come out
-// are fp32's; what only bf16 outputs are made of is two (16 bits), and the states, U and Z
-// that the gradients read are kept as one.  Products of parts whose bits lie below the last
+// are fp32's; what only bf16 outputs are made of is two (16 bits), as are the U and Z
+// that the gradients read (one made dgate's error 4.4e-3 for 2.9e-3); the states they read
+// are kept as one.  Products of parts whose bits lie below the last
 // part's are left out.
 #include <string>
 #include <type_traits>
@@ -278,6 +286,9 @@ __device__ __forceinline__ int first_tile(int base, int sample) { return base / 
 
 // ----------------------------------------------------------------- prepare
 
+// A chunk's scalars, P and N, a wavefront a chunk and head.  Sums of log a are fp64: they reach
+// 32 x 200, and what e^ is taken of are their differences.  N comes by forward substitution, a
+// column a lane, which keeps fp32's accuracy where keys repeat (powers of M do not).
 template <typename T, int KT>
 __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 {
@@ -957,7 +968,9 @@ __device__ __forceinline__ int move_at(int row, int col)
     return (((col >> 5) * KT + y) * 2 + a) * 3 * 512 + ((col >> 3 & 3) * 16 + m) * 8 + (col & 7);
 }
 
-// Walks forward.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
+// Walks forward, a workgroup a sample and head.  Half the columns a workgroup, twice the workgroups,
+// evened unequal samples out but read K, Q and records twice: train_delta's four kernels 764 us
+// and 852 so, a long history's 392 and 440.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
 // to the state, as a matrix (1: the walk without values from the identity).
 template <typename T, int KT, bool TRAIN, bool SUM>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
@@ -1179,10 +1192,10 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 // The states at the edges of a cut sample's segments, one after another: S' = move S + added
 // (BACK: from the last, with the move transposed).  A wavefront has 16 columns of a sample's
 // and head's state, four of them (one a SIMD) share a workgroup and a fifth that brings the
-// moves, 32 of their columns at a time and several such steps ahead (three: 75 us for the below).  They come in the parts that
-// the products take: cut into them by every wavefront again, they took most of the time (64
-// segments of 64 x 128: 190 us, and 69 us so).  What a segment adds is replaced by the state
-// that it begins with.
+// moves, 32 of their columns at a time and up to kJoinAhead such steps ahead (three: 75 us for
+// the below).  They come in the parts that the products take: cut into them by every wavefront
+// again, they took most of the time.  64 segments of 64 x 128: 190 us then, 69 us so, a latency of
+// 1.1 us a segment.  What a segment adds is replaced by the state that it begins with.
 constexpr int kJoined = 4;
 // steps on their way behind the one that is waited for (at most 63 loads are counted), and places
 template <int KT>
@@ -1301,7 +1314,7 @@ struct GradLds {
 
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk.  What rows of K and Q
 // are taken with, D, D^T and B + B^T, is made by a wavefront each and handed over in LDS; the
-// first makes dgate and dbeta.
+// first makes dgate and dbeta.  Bound by what it reads, half of it the two sides' states.
 template <typename T, int KT>
 __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(DeltaArgs A)
 {

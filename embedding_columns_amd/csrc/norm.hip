@@ -6,13 +6,13 @@
 // came, between its sums, which are taken of the centred values and in fp32.  A row is read by
 // 1 .. 64 lanes (several rows share a wavefront) or by up to 16 wavefronts, 16 bytes a lane and
 // piece.  Workgroups walk over rows, with weight and bias in registers (read again for each
-// row they cost as much of the caches as x: 74 us for what takes 55) and, where registers last,
+// row they cost as much of the caches as x: 74 us for what takes 57) and, where registers last,
 // the next row on its way; in the backward each keeps its share of dw and db in registers,
 // leaves one row of them, and a second kernel adds these up in a fixed order.
 //
-// 140771 rows of 512 in bf16: forward 55 us (288 MB, 5.3 TB/s), backward with its sums 88 us (432
-// MB, 4.9 TB/s).  8191 of 5000 in fp32: 61 us (328 MB, 5.4 TB/s) and 108 us (491 MB, 4.6 TB/s; the
-// workgroups' sums are another 41 MB).  50 rows of 256: 3 us, a launch.
+// 140771 rows of 512 in bf16: forward 57 us (288 MB, 5.0 TB/s), backward 86 us (432 MB, 5.0 TB/s) and
+// 5 us for the sums.  8191 of 5000 in fp32: 59 us (328 MB, 5.6 TB/s), 99 us (491 MB, 5.0 TB/s) and
+// 6 us.  50 rows of 256: 3.6 us, a launch.
 #include <cmath>
 #include <string>
 

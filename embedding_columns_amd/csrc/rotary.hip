@@ -12,6 +12,8 @@
 //
 // The bound is reading and writing every element once.  A workgroup takes some rows, makes
 // their cosines and sines once in LDS, and turns all heads with them, 16 bytes a lane.
+// 28528 rows of 8 heads of 128 in bf16: 21 us (117 MB, 5.5 TB/s); 65838 rows of 3 and 6 heads, 24
+// of 40 elements, in fp32: 20.5 us (64 MB, 3.1 TB/s; heads end inside 64 bytes).
 #include <cmath>
 #include <string>
 
