@@ -27,7 +27,7 @@
 //
 // What passes between them costs more than the rows themselves: what bounds the four is bytes,
 // then a walk's chain of dependent products.  bf16, 287434 rows in 256 samples, 4 heads of
-// 64 x 64: prepare 133 us (0.59 GB, 4.5 TB/s), scan 242 us (0.95 GB, 3.9 TB/s).  With
+// 64 x 64: prepare 133 us (0.59 GB, 4.5 TB/s), scan 206 us (0.95 GB, 4.6 TB/s).  With
 // gradients, 68548 rows in 64 samples, 4 heads of 128 x 128: prepare 59 us, scan 200 us and back
 // 224 us (0.8 GB each; the longest of 256 walks on 256 CUs is twice the mean), grads 305 us
 // (1.25 GB, 4.1 TB/s).
@@ -74,6 +74,8 @@ struct DeltaArgs {
     char *rec;                 // records of (tile, head): N, P, scalars
     int64_t rec_size;
     void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
+    int32_t *order;            // samples from the longest on, or NULL: as they are
+    int32_t ranks;             // workgroups of delta_prepare that make it
     int32_t cut;               // samples are cut into segments
     int32_t moves_back;        // ... whose transposed matrices are wanted too
     uint16_t *moves;           // of (segment, head): what it does to a state, in parts (and transposed)
@@ -286,6 +288,28 @@ __device__ __forceinline__ int first_tile(int base, int sample) { return base / 
 
 // ----------------------------------------------------------------- prepare
 
+// Walks begin in the order of their lengths, the longest first, since what begins last ends last
+// (delta_histories' scan: 242 us in the samples' own order, 206 so).  A lane counts the samples
+// that come before its own; wavefronts beside the chunks' do it.  Lengths from 2^20 on count as one.
+constexpr int kRanked = 1024;
+__device__ __forceinline__ void delta_order(const DeltaArgs &A, int block)
+{
+    const int l = lane_id(), own = 64 * block + l;
+    auto key = [&](int s) {                              // no two are equal
+        const int rows = seg_edge(A.off, A.samples, A.n, s + 2) - seg_edge(A.off, A.samples, A.n, s + 1);
+        return s < A.samples ? min(max(rows, 0), (1 << 20) - 1) * kRanked + kRanked - 1 - s : -1;
+    };
+    const int mine = key(own);
+    int before = 0, next = key(l);
+    for (int s0 = 0; s0 < A.samples; s0 += 64) {
+        const int theirs = next;
+        next = key(s0 + 64 + l);
+#pragma unroll
+        for (int j = 0; j < 64; j++) before += __builtin_amdgcn_readlane(theirs, j) > mine ? 1 : 0;
+    }
+    if (own < A.samples) *gp(A.order + before) = own;
+}
+
 // A chunk's scalars, P and N, a wavefront a chunk and head.  Sums of log a are fp64: they reach
 // 32 x 200, and what e^ is taken of are their differences.  N comes by forward substitution, a
 // column a lane, which keeps fp32's accuracy where keys repeat (powers of M do not).
@@ -296,7 +320,11 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     constexpr int kPitch = 36;
     __shared__ __attribute__((aligned(16))) float lds[32 * kPitch];
     __shared__ __attribute__((aligned(16))) float sc[kScalars];
-    const int tile = blockIdx.x, head = blockIdx.y, key = head / A.group;
+    const int tile = (int)blockIdx.x - A.ranks, head = blockIdx.y, key = head / A.group;
+    if (tile < 0) {
+        if (head == 0) delta_order(A, blockIdx.x);
+        return;
+    }
     const int l = lane_id(), c = l & 31, h = l >> 5;
     const SegTile s = seg_find<kCut>(A.off, A.n, nullptr, 0, A.samples, 1, tile);
     if (s.row0 >= s.rows) return;
@@ -828,7 +856,7 @@ __device__ __forceinline__ Walk walk_of(const DeltaArgs &A)
         w.tile0 = first_tile(s.base, sample) + s.row0 / kCut;
         w.part = (int64_t)unit * A.heads + w.head;
     } else {
-        sample = unit;
+        sample = A.order ? uniform(*gp(A.order + unit)) : unit;
         w.any = w.first = w.last = true;
         w.base = uniform(seg_edge(A.off, A.samples, A.n, sample + 1));
         w.rows = max(uniform(seg_edge(A.off, A.samples, A.n, sample + 2)) - w.base, 0);
@@ -1725,6 +1753,8 @@ struct DeltaPlan {
     bool cut;
     size_t rec, move;                        // bytes of a record, of a segment's matrix
     size_t recs, states, us, moves, starts;  // bytes of all of them
+    int ranks;                               // workgroups that order the samples
+    size_t order;
     size_t q, k, v;                          // bytes of packed rows, 0 where they are read in place
     size_t saved, forward, backward;
 };
@@ -1763,13 +1793,22 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
         p.moves = segments * p.move;
         p.starts = pad256(segments * d->dk * d->dv * 4);
     }
+    // Where there are more walks than CUs.  Forward / with the backward in us, the samples' own order
+    // and the longest first: 256 x 200..2000 rows, 4 heads of 64: 371, 1444 and 344, 1335; 300 x
+    // 10..3000, 1 head: 203, 703 and 177, 606; 1024 x 50..800, 4 heads: 561, 2183 and 551, 2152;
+    // 256 x 1000: the same.  More and shorter samples are even enough by themselves (4000 x 20..200,
+    // 4 heads: 599, 2342 and 610, 2383).
+    if (!p.cut && (int64_t)d->samples * d->heads > 256 && d->samples <= kRanked && d->n / d->samples >= 64) {
+        p.ranks = (d->samples + 63) / 64;
+        p.order = (size_t)p.ranks * 256;
+    }
     const size_t keys = pad256((size_t)d->n * d->key_heads * p.kt * 32 * p.el);
     p.q = rows_ready(d->q, d->q_stride, d->q_head_stride, d->dk, p.el) ? 0 : keys;
     p.k = rows_ready(d->k, d->k_stride, d->k_head_stride, d->dk, p.el) ? 0 : keys;
     const size_t values = pad256((size_t)d->n * d->heads * ((d->dv + 31) / 32 * 32) * p.el);
     p.v = rows_ready(d->v, d->v_stride, d->v_head_stride, d->dv, p.el) ? 0 : values;
-    p.saved = p.recs + p.states + p.us + p.moves;
-    p.forward = (train ? 0 : p.recs + p.moves) + p.starts + p.q + p.k + p.v;
+    p.saved = p.order + p.recs + p.states + p.us + p.moves;
+    p.forward = (train ? 0 : p.order + p.recs + p.moves) + p.starts + p.q + p.k + p.v;
     // the tensors that the backward gets may lie otherwise than the forward's did
     p.backward = p.states + p.us + p.starts + 2 * keys + values;
     return p;
@@ -1835,13 +1874,15 @@ DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
     return A;
 }
 
-// records, states, U and the segments' matrices in the buffer that the forward leaves for the backward
+// the samples' order, records, states, U and the segments' matrices in the buffer that the forward
+// leaves for the backward
 void delta_saved(const DeltaPlan &p, DeltaArgs &A, char *saved)
 {
-    A.rec = saved;
-    A.s0 = saved + p.recs;
-    A.u = saved + p.recs + p.states;
-    A.moves = reinterpret_cast<uint16_t *>(saved + p.recs + p.states + p.us);
+    A.order = p.order ? reinterpret_cast<int32_t *>(saved) : nullptr;
+    A.rec = saved + p.order;
+    A.s0 = A.rec + p.recs;
+    A.u = A.rec + p.recs + p.states;
+    A.moves = reinterpret_cast<uint16_t *>(A.rec + p.recs + p.states + p.us);
 }
 
 int64_t delta_walks(const emb_delta *d, const DeltaPlan &p)
@@ -1873,7 +1914,7 @@ void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool
     const dim3 walk((unsigned)walks);
     const int join = kJoinRing<KT> * KT * 6144;
     const dim3 joins((unsigned)(A.samples * A.heads), (unsigned)((A.slices + kJoined - 1) / kJoined));
-    delta_launch(delta_prepare<T, KT>, dim3((unsigned)tiles, (unsigned)A.heads), 64, 0, A, st);
+    delta_launch(delta_prepare<T, KT>, dim3((unsigned)(A.ranks + tiles), (unsigned)A.heads), 64, 0, A, st);
     if (!walks) return;
     if (A.cut) {
         // wavefronts enough for either kind
@@ -1949,12 +1990,14 @@ extern "C" emb_status emb_delta_forward(const emb_delta *d, void *o, float *last
     A.last = last;
     A.ovec = rows16(o, d->dv, p.el);
     A.moves_back = train;
+    A.ranks = p.ranks;
     char *ws = static_cast<char *>(workspace);
     if (train) delta_saved(p, A, static_cast<char *>(saved));
     else {
-        A.rec = ws;
-        A.moves = reinterpret_cast<uint16_t *>(ws + p.recs);
-        ws += p.recs + p.moves;
+        A.order = p.order ? reinterpret_cast<int32_t *>(ws) : nullptr;
+        A.rec = ws + p.order;
+        A.moves = reinterpret_cast<uint16_t *>(A.rec + p.recs);
+        ws += p.order + p.recs + p.moves;
     }
     A.starts = reinterpret_cast<float *>(ws);
     ws += p.starts;
