@@ -41,7 +41,7 @@
 // the state and what makes it (N, U, Z, P^T) are three, so that the states that come out
 // are fp32's; what only bf16 outputs are made of is two (16 bits), as are the U and Z
 // that the gradients read (with one, dgate is off by up to 4.4e-3, then 2.9e-3); the states they read
-// are kept as one.  Products of parts whose bits lie below the last
+// are kept as one, and in a small call whole.  Products of parts whose bits lie below the last
 // part's are left out.
 #include <string>
 #include <type_traits>
@@ -76,6 +76,7 @@ struct DeltaArgs {
     void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
     int32_t *order;            // samples from the longest on, or NULL: as they are
     int32_t ranks;             // workgroups of delta_prepare that make it
+    int32_t whole;             // states are kept in fp32
     int32_t cut;               // samples are cut into segments
     int32_t moves_back;        // ... whose transposed matrices are wanted too
     uint16_t *moves;           // of (segment, head): what it does to a state, in parts (and transposed)
@@ -901,6 +902,10 @@ __device__ __forceinline__ void state_write(const Block (&S)[KT], float *p, int 
 // leave LDS for one, by themselves.
 template <typename T, int KT>
 constexpr int kScratchBlocks = sizeof(T) == 2 ? KT : 1;
+// a wavefront's scratch: for rows of T, and in training for states kept as W
+template <typename T, typename W, int KT, bool TRAIN>
+constexpr int kScratch = TRAIN && kScratchBlocks<W, KT> * Turn<W>::kBytes > Turn<T>::kBytes ? kScratchBlocks<W, KT> * Turn<W>::kBytes
+                                                                                             : Turn<T>::kBytes;
 template <typename T>
 __device__ __forceinline__ void state_leave(uint32_t scratch, char *to, int x, int slices, int slice)
 {
@@ -1000,7 +1005,7 @@ __device__ __forceinline__ int move_at(int row, int col)
 // evened unequal samples out but read K, Q and records twice: train_delta's four kernels 764 us
 // and 852 so, a long history's 392 and 440.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
 // to the state, as a matrix (1: the walk without values from the identity).
-template <typename T, int KT, bool TRAIN, bool SUM>
+template <typename T, int KT, bool TRAIN, bool SUM, typename W>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
     constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
@@ -1018,7 +1023,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         return;                                          // the rest: fewer columns of one kind than of the other
     }
     const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
-    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * (TRAIN ? kScratchBlocks<T, KT> : 1) * Turn<T>::kBytes;
+    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratch<T, W, KT, TRAIN>;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(values ? slice : 0);
 
@@ -1033,11 +1038,11 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
                        A.dv, col);
     // what leaves: the lane's piece of a row of o, of U and of the states, a chunk's step apart
     const int64_t ostep = (int64_t)kCut * A.heads * A.dv, ustep = (int64_t)A.heads * A.slices * 2048,
-                  sstep = (int64_t)A.heads * KT * A.slices * Lds<T>::kRows;
+                  sstep = (int64_t)A.heads * KT * A.slices * Lds<W>::kRows;
     T *o = static_cast<T *>(A.o) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c;
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
     char *u = static_cast<char *>(A.u) + (number * A.slices + slice) * 2048;
-    char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<T>::kRows;
+    char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<W>::kRows;
     for (int i = 0; i < chunks; i++) {
         meet_others();
         const uint32_t at = at0 + (i & 1) * L::size(A.slices), sc = at + L::sc;
@@ -1045,7 +1050,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<ST> sp = operand<ST>(S[x]);
-            if (TRAIN && !SUM) state_put<T, KT>(scratch, S[x], sp.p[0], states, x, A.slices, slice);
+            if (TRAIN && !SUM) state_put<W, KT>(scratch, S[x], sp.p[0], states, x, A.slices, slice);
 #pragma unroll
             for (int a = 0; a < 2; a++) {
                 mm<ST>(X.t[a], lane.row(at, x, a), sp);
@@ -1078,7 +1083,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
                 mm<ST>(S[x].t[a], lane.column(at, x, a), up);
             }
         if (!SUM) {
-            if (TRAIN) state_keep<T, KT>(scratch, states, A.slices, slice);
+            if (TRAIN) state_keep<W, KT>(scratch, states, A.slices, slice);
             const Block sg = row_scalars(sc + 4 * kScG);
             const Part<OUT> op = operand<OUT>(U);
 #pragma unroll
@@ -1121,7 +1126,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 }
 
 // Walks backward, from the gradient of the last state.
-template <typename T, int KT, bool SUM>
+template <typename T, int KT, bool SUM, typename W>
 __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
@@ -1136,7 +1141,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
         return;
     }
     const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
-    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratchBlocks<T, KT> * Turn<T>::kBytes;
+    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratch<T, W, KT, true>;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(slice);
 
@@ -1144,11 +1149,11 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
     state_read<KT>(E, SUM ? nullptr : A.cut ? A.starts + w.part * A.dk * A.dv : A.dlast ? A.dlast + w.matrix * A.dk * A.dv : nullptr,
                    A.dk, A.dv, col);
     const int64_t vstep = (int64_t)kCut * A.heads * A.dv, zstep = (int64_t)A.heads * A.slices * 2048,
-                  sstep = (int64_t)A.heads * KT * A.slices * Lds<T>::kRows;
+                  sstep = (int64_t)A.heads * KT * A.slices * Lds<W>::kRows;
     T *dv = static_cast<T *>(A.dv_) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c + chunks * vstep;
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
     char *z = static_cast<char *>(A.z) + (number * A.slices + slice) * 2048 + chunks * zstep;
-    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<T>::kRows + chunks * sstep;
+    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<W>::kRows + chunks * sstep;
     for (int s = 0; s < chunks; s++) {
         meet_others();
         const int i = chunks - 1 - s;
@@ -1160,7 +1165,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<ST> ep = operand<ST>(E[x]);
-            if (!SUM) state_put<T, KT>(scratch, E[x], ep.p[0], states, x, A.slices, slice);
+            if (!SUM) state_put<W, KT>(scratch, E[x], ep.p[0], states, x, A.slices, slice);
 #pragma unroll
             for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
         }
@@ -1197,7 +1202,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
                 mm<ST>(E[x].t[a], lane.column(at + L::q, x, a), op);
             }
         if (!SUM) {
-            state_keep<T, KT>(scratch, states, A.slices, slice);
+            state_keep<W, KT>(scratch, states, A.slices, slice);
             const Part<OUT> kept = operand<OUT>(Z);
             Turn<T>::leave(scratch, Z, kept.p[0], kept.p[1], z);
             Turn<T> rows;
@@ -1343,13 +1348,14 @@ struct GradLds {
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk.  What rows of K and Q
 // are taken with, D, D^T and B + B^T, is made by a wavefront each and handed over in LDS; the
 // first makes dgate and dbeta.  Bound by what it reads, half of it the two sides' states.
-template <typename T, int KT>
-__global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(DeltaArgs A)
+template <typename T, int KT, typename W>
+__global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT;
     typedef GradLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
-    constexpr bool EXACT = sizeof(T) == 2;               // fp32's states are kept as they are
+    constexpr int SO = sizeof(W) == sizeof(T) ? IN : 2;  // orders of products with states
+    constexpr bool EXACT = sizeof(W) == 2;               // states that are kept as they are need it not
     __shared__ float red[KT][3][32], cross[3][32], cols[2][2][32], owns[32];
     const int tile = blockIdx.x, key = blockIdx.y;
     const int wave = uniform((int)(threadIdx.x >> 6)), l = lane_id(), c = l & 31, h = l >> 5;
@@ -1399,11 +1405,11 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
             bring(head);
         }
         const int64_t number = (int64_t)tile * A.heads + head, n = A.slices;
-        const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<T>::kRows;
-        const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<T>::kRows;
+        const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<W>::kRows;
+        const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<W>::kRows;
         const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * 2048, oat = zat + n * 2048;
         // the states' rows are on their way while the chunk's own products are made
-        Kept<T> S[kKeptMost], E[kKeptMost];
+        Kept<W> S[kKeptMost], E[kKeptMost];
 #pragma unroll
         for (int x = 0; x < kKeptMost; x++)
             if (x < n) {
@@ -1514,10 +1520,10 @@ __global__ __launch_bounds__(64 * KT, sizeof(T) == 2 ? 2 : 1) void delta_grads(D
         for (int x = 0; x < kKeptMost; x++)
             if (x < n) {
                 const auto s0 = S[x].operand(), e0 = E[x].operand();
-                mm<IN>(t1, s0, Lds<T>::rows(oat, x));
+                mm<SO>(t1, s0, Lds<T>::rows(oat, x));
                 mm<OUT>(t2, s0, written<T>(zat, x));
                 mm<OUT>(t3, e0, written<T>(uat, x));
-                mm<IN>(se, s0, e0);
+                mm<SO>(se, s0, e0);
             }
         float inner = 0.f;
 #pragma unroll
@@ -1777,7 +1783,7 @@ struct DeltaPlan {
     size_t el;
     int kt, slices;
     int64_t tiles;
-    bool cut;
+    bool cut, whole;                         // whole: states are kept in fp32 for the gradients
     size_t rec, move;                        // bytes of a record, of a segment's matrix
     size_t recs, states, us, moves, starts;  // bytes of all of them
     int ranks;                               // workgroups that order the samples
@@ -1813,7 +1819,14 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     p.rec = bf ? Rec<uint16_t>::size : Rec<float>::size;
     p.recs = (size_t)p.tiles * d->heads * p.rec;
     p.us = (size_t)p.tiles * d->heads * p.slices * 2048;
-    p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 512 * p.el;
+    p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 1024;
+    // The states that bf16 gradients read are kept in fp32 where they are few, and so the sums of a
+    // few rows are as exact as bf16 shows (dgate 1.7e-3 to 2.0e-3 off, dk 1.7e-3; kept in bf16 2.0e-3 to
+    // 2.6e-3, and 4.4e-3 where large first and last states met in 20 short samples; dk 2.3e-3).
+    // Kept in bf16 and in fp32, a step of training in us: 1.6 MB in bf16 167, 167; 7.5 MB 168, 168 to 178;
+    // 16 MB 238, 263; 24 MB 173, 190; 66 MB 239, 345; 293 MB 781, 1195.
+    p.whole = !bf || p.states <= (size_t(1) << 24);
+    if (p.whole) p.states *= 2;
     if (p.cut) {
         const size_t segments = (size_t)seg_tiles(d->n, d->samples, 1, kSpan) * d->heads;
         p.move = (size_t)p.kt * p.kt * 6144 * (train ? 2 : 1);
@@ -1897,6 +1910,7 @@ DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
     A.scale = d->scale;
     A.rec_size = (int64_t)p.rec;
     A.cut = p.cut;
+    A.whole = p.whole;
     A.move_size = (int64_t)p.move / 2;
     return A;
 }
@@ -1946,13 +1960,15 @@ void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool
     if (A.cut) {
         // wavefronts enough for either kind
         const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
-        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * most + 64, 2 * WalkLds<T, KT, true>::size(A.slices),
+        delta_launch(delta_scan<T, KT, false, true, T>, dim3((unsigned)walks, 2), 64 * most + 64, 2 * WalkLds<T, KT, true>::size(A.slices),
                      A, st);
         delta_launch(delta_join<KT, false>, joins, 64 * kJoined + 64, join, A, st);
     }
-    const int lds = 2 * WalkLds<T, KT, false>::size(A.slices) + A.slices * Turn<T>::kBytes * (train ? kScratchBlocks<T, KT> : 1);
-    if (train) delta_launch(delta_scan<T, KT, true, false>, walk, 64 * A.slices + 64, lds, A, st);
-    else delta_launch(delta_scan<T, KT, false, false>, walk, 64 * A.slices + 64, lds, A, st);
+    const int stages = 2 * WalkLds<T, KT, false>::size(A.slices), threads = 64 * A.slices + 64;
+    if (!train) delta_launch(delta_scan<T, KT, false, false, T>, walk, threads, stages + A.slices * kScratch<T, T, KT, false>, A, st);
+    else if (A.whole)
+        delta_launch(delta_scan<T, KT, true, false, float>, walk, threads, stages + A.slices * kScratch<T, float, KT, true>, A, st);
+    else delta_launch(delta_scan<T, KT, true, false, T>, walk, threads, stages + A.slices * kScratch<T, T, KT, true>, A, st);
 }
 
 template <typename T, int KT>
@@ -1962,13 +1978,18 @@ void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, boo
     const int lds = 2 * WalkLds<T, KT, false>::size(A.slices), join = kJoinRing<KT> * KT * 6144;
     const dim3 joins((unsigned)(A.samples * A.heads), (unsigned)((A.slices + kJoined - 1) / kJoined));
     if (walks && A.cut) {
-        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, lds, A, st);
+        delta_launch(delta_back<T, KT, true, T>, walk, 64 * A.slices + 64, lds, A, st);
         delta_launch(delta_join<KT, true>, joins, 64 * kJoined + 64, join, A, st);
     }
-    if (walks)
-        delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64,
-                     lds + A.slices * Turn<T>::kBytes * kScratchBlocks<T, KT>, A, st);
-    delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
+    auto rest = [&](auto kept) {
+        typedef decltype(kept) W;
+        if (walks)
+            delta_launch(delta_back<T, KT, false, W>, walk, 64 * A.slices + 64, lds + A.slices * kScratch<T, W, KT, true>, A, st);
+        delta_launch(delta_grads<T, KT, W>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A,
+                     st);
+    };
+    if (A.whole) rest(float{});
+    else rest(T{});
 }
 
 #define EMB_DELTA_SIZES(NAME, T)                             \

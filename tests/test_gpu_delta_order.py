@@ -54,3 +54,11 @@ def test_a_sample_is_what_it_is_alone():
         for name, x in call(one).items():
             where = slice(s, s + 1) if name in ("last", "dstate") else rows
             assert torch.equal(x, got[name][where]), (s, name)
+
+
+@pytest.mark.parametrize("samples", [8, 40])
+def test_states_kept_either_way(samples):
+    """bf16 gradients with the states before the chunks kept in fp32 (few of them) and in bf16."""
+    gen = torch.Generator().manual_seed(samples)
+    t = make(torch.randint(20, 200, (samples,), generator=gen).tolist(), 1, 4, 128, 128, BF16, masked=0.1, seed=samples)
+    check(t, call(t))
