@@ -27,10 +27,10 @@
 //
 // What passes between them costs more than the rows themselves: what bounds the four is bytes,
 // then a walk's chain of dependent products.  bf16, 287434 rows in 256 samples, 4 heads of
-// 64 x 64: prepare 133 us (0.59 GB, 4.5 TB/s), scan 206 us (0.95 GB, 4.6 TB/s).  With
+// 64 x 64: prepare 133 us (0.59 GB, 4.5 TB/s), scan 207 us (0.95 GB, 4.6 TB/s).  With
 // gradients, 68548 rows in 64 samples, 4 heads of 128 x 128: prepare 59 us, scan 200 us and back
-// 224 us (0.8 GB each; the longest of 256 walks on 256 CUs is twice the mean), grads 305 us
-// (1.25 GB, 4.1 TB/s).
+// 220 us (0.8 GB each; the longest of 256 walks on 256 CUs is twice the mean), grads 311 us
+// (1.25 GB, 4.0 TB/s).
 //
 // All products run on the matrix cores, the walks' in blocks of 16 x 16 (lane & 15 a column,
 // register i of quarter g = lane >> 4 row 4 g + i), the others' in 32 x 32 (lane & 31 a column,
