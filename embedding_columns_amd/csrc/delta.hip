@@ -40,9 +40,8 @@
 // the next from what is left of it: inputs in bf16 are one part, fp32 ones three (24 bits);
 // the state and what makes it (N, U, Z, P^T) are three, so that the states that come out
 // are fp32's; what only bf16 outputs are made of is two (16 bits), as are the U and Z
-// that the gradients read (with one, dgate is off by up to 4.4e-3, then 2.9e-3); the states they read
-// are kept as one, and in a small call whole.  Products of parts whose bits lie below the last
-// part's are left out.
+// that the gradients read (with one, dgate is off by up to 4.4e-3, then 2.9e-3).  The states they
+// read are kept in fp32.  Products of parts whose bits lie below the last part's are left out.
 #include <string>
 #include <type_traits>
 
@@ -73,10 +72,9 @@ struct DeltaArgs {
     float scale;
     char *rec;                 // records of (tile, head): N, P, scalars
     int64_t rec_size;
-    void *s0, *u;              // saved for the backward, of (tile, head): the state before, and U, as operands
+    void *s0, *u;              // saved for the backward, of (tile, head): the state before in fp32, and U, as operands
     int32_t *order;            // samples from the longest on, or NULL: as they are
     int32_t ranks;             // workgroups of delta_prepare that make it
-    int32_t whole;             // states are kept in fp32
     int32_t cut;               // samples are cut into segments
     int32_t moves_back;        // ... whose transposed matrices are wanted too
     uint16_t *moves;           // of (segment, head): what it does to a state, in parts (and transposed)
@@ -897,47 +895,20 @@ __device__ __forceinline__ void state_write(const Block (&S)[KT], float *p, int 
             __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[x].t[i >> 2][i & 3]), to, at + (32 * x + i) * dv * 4, 0, 0);
 }
 
-// The state as the gradients read it, rows as operands of 32 x 16 elements: a block is put into
-// the scratch and taken from there, bf16 blocks when all of them are in, fp32 ones, whose chunks
-// leave LDS for one, by themselves.
-template <typename T, int KT>
-constexpr int kScratchBlocks = sizeof(T) == 2 ? KT : 1;
-// a wavefront's scratch: for rows of T, and in training for states kept as W
-template <typename T, typename W, int KT, bool TRAIN>
-constexpr int kScratch = TRAIN && kScratchBlocks<W, KT> * Turn<W>::kBytes > Turn<T>::kBytes ? kScratchBlocks<W, KT> * Turn<W>::kBytes
-                                                                                             : Turn<T>::kBytes;
-template <typename T>
-__device__ __forceinline__ void state_leave(uint32_t scratch, char *to, int x, int slices, int slice)
+// a wavefront's scratch: for rows of T, and in training for the state's in fp32
+template <typename T, bool TRAIN>
+constexpr int kScratch = TRAIN ? Turn<float>::kBytes : Turn<T>::kBytes;
+// Block x of the state as the gradients read it, fp32 rows as operands of 32 x 16 elements.
+__device__ __forceinline__ void state_keep(uint32_t scratch, const Block &S, char *to, int x, int slices, int slice)
 {
-    Turn<T> rows;
+    const int g = lane_id() >> 4;
+    Turn<float> rows;
+    wave_sync();
+#pragma unroll
+    for (int a = 0; a < 2; a++) Turn<float>::fill(scratch, 8 * g + 4 * a, S.t[a]);
+    wave_sync();
     rows.take(scratch);
-    rows.keep(to + (x * slices + slice) * Lds<T>::kRows);
-}
-template <typename T, int KT>
-__device__ __forceinline__ void state_put(uint32_t scratch, const Block &S, const u32x4_t &rounded, char *to, int x, int slices,
-                                          int slice)
-{
-    const int l = lane_id(), c = l & 15, g = l >> 4;
-    if constexpr (sizeof(T) == 2) {
-        scratch += x * Turn<T>::kBytes;
-        lds_write(scratch + c * 72 + 16 * g, u32x2_t{rounded[0], rounded[1]});
-        lds_write(scratch + c * 72 + 16 * g + 8, u32x2_t{rounded[2], rounded[3]});
-    } else {
-        wave_sync();
-#pragma unroll
-        for (int a = 0; a < 2; a++) Turn<T>::fill(scratch, 8 * g + 4 * a, S.t[a]);
-        wave_sync();
-        state_leave<T>(scratch, to, x, slices, slice);
-    }
-}
-template <typename T, int KT>
-__device__ __forceinline__ void state_keep(uint32_t scratch, char *to, int slices, int slice)
-{
-    if (sizeof(T) != 2) return;
-    wave_sync();
-#pragma unroll
-    for (int x = 0; x < KT; x++) state_leave<T>(scratch + x * Turn<T>::kBytes, to, x, slices, slice);
-    wave_sync();
+    rows.keep(to + (x * slices + slice) * Lds<float>::kRows);
 }
 
 // A walk's workgroup.  A wavefront has 16 columns of the state, and one more brings the chunks, one
@@ -1005,7 +976,7 @@ __device__ __forceinline__ int move_at(int row, int col)
 // evened unequal samples out but read K, Q and records twice: train_delta's four kernels 764 us
 // and 852 so, a long history's 392 and 440.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
 // to the state, as a matrix (1: the walk without values from the identity).
-template <typename T, int KT, bool TRAIN, bool SUM, typename W>
+template <typename T, int KT, bool TRAIN, bool SUM>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
     constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
@@ -1023,7 +994,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         return;                                          // the rest: fewer columns of one kind than of the other
     }
     const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
-    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratch<T, W, KT, TRAIN>;
+    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratch<T, TRAIN>;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(values ? slice : 0);
 
@@ -1038,11 +1009,11 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
                        A.dv, col);
     // what leaves: the lane's piece of a row of o, of U and of the states, a chunk's step apart
     const int64_t ostep = (int64_t)kCut * A.heads * A.dv, ustep = (int64_t)A.heads * A.slices * 2048,
-                  sstep = (int64_t)A.heads * KT * A.slices * Lds<W>::kRows;
+                  sstep = (int64_t)A.heads * KT * A.slices * Lds<float>::kRows;
     T *o = static_cast<T *>(A.o) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c;
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
     char *u = static_cast<char *>(A.u) + (number * A.slices + slice) * 2048;
-    char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<W>::kRows;
+    char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<float>::kRows;
     for (int i = 0; i < chunks; i++) {
         meet_others();
         const uint32_t at = at0 + (i & 1) * L::size(A.slices), sc = at + L::sc;
@@ -1050,7 +1021,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<ST> sp = operand<ST>(S[x]);
-            if (TRAIN && !SUM) state_put<W, KT>(scratch, S[x], sp.p[0], states, x, A.slices, slice);
+            if (TRAIN && !SUM) state_keep(scratch, S[x], states, x, A.slices, slice);
 #pragma unroll
             for (int a = 0; a < 2; a++) {
                 mm<ST>(X.t[a], lane.row(at, x, a), sp);
@@ -1083,7 +1054,6 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
                 mm<ST>(S[x].t[a], lane.column(at, x, a), up);
             }
         if (!SUM) {
-            if (TRAIN) state_keep<W, KT>(scratch, states, A.slices, slice);
             const Block sg = row_scalars(sc + 4 * kScG);
             const Part<OUT> op = operand<OUT>(U);
 #pragma unroll
@@ -1126,7 +1096,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 }
 
 // Walks backward, from the gradient of the last state.
-template <typename T, int KT, bool SUM, typename W>
+template <typename T, int KT, bool SUM>
 __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
@@ -1141,7 +1111,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
         return;
     }
     const int l = lane_id(), r = l & 31, c = 16 * slice + 8 * (l >> 5), col = 16 * slice + (l & 15);
-    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratch<T, W, KT, true>;
+    const uint32_t scratch = at0 + 2 * L::size(A.slices) + slice * kScratch<T, true>;
     const Lane<T> lane;
     const uint32_t columns = lane.columns(slice);
 
@@ -1149,11 +1119,11 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
     state_read<KT>(E, SUM ? nullptr : A.cut ? A.starts + w.part * A.dk * A.dv : A.dlast ? A.dlast + w.matrix * A.dk * A.dv : nullptr,
                    A.dk, A.dv, col);
     const int64_t vstep = (int64_t)kCut * A.heads * A.dv, zstep = (int64_t)A.heads * A.slices * 2048,
-                  sstep = (int64_t)A.heads * KT * A.slices * Lds<W>::kRows;
+                  sstep = (int64_t)A.heads * KT * A.slices * Lds<float>::kRows;
     T *dv = static_cast<T *>(A.dv_) + ((int64_t)(w.base + r) * A.heads + w.head) * A.dv + c + chunks * vstep;
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
     char *z = static_cast<char *>(A.z) + (number * A.slices + slice) * 2048 + chunks * zstep;
-    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<W>::kRows + chunks * sstep;
+    char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<float>::kRows + chunks * sstep;
     for (int s = 0; s < chunks; s++) {
         meet_others();
         const int i = chunks - 1 - s;
@@ -1165,7 +1135,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 #pragma unroll
         for (int x = 0; x < KT; x++) {
             const Part<ST> ep = operand<ST>(E[x]);
-            if (!SUM) state_put<W, KT>(scratch, E[x], ep.p[0], states, x, A.slices, slice);
+            if (!SUM) state_keep(scratch, E[x], states, x, A.slices, slice);
 #pragma unroll
             for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
         }
@@ -1202,7 +1172,6 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
                 mm<ST>(E[x].t[a], lane.column(at + L::q, x, a), op);
             }
         if (!SUM) {
-            state_keep<W, KT>(scratch, states, A.slices, slice);
             const Part<OUT> kept = operand<OUT>(Z);
             Turn<T>::leave(scratch, Z, kept.p[0], kept.p[1], z);
             Turn<T> rows;
@@ -1308,26 +1277,22 @@ __global__ __launch_bounds__(64 * kJoined + 64) void delta_join(DeltaArgs A)
 
 constexpr int kKeptMost = kDeltaDim / 16;
 
-// 32 rows x 16 elements kept as an operand in memory
-template <typename T>
+// 32 rows x 16 elements of a state kept as an operand in memory
 struct Kept {
-    u32x4_t w[Lds<T>::R];
+    u32x4_t w[2];
 
     __device__ __forceinline__ void load(const char *at, int x)
     {
 #pragma unroll
-        for (int j = 0; j < Lds<T>::R; j++)
-            w[j] = *gp(reinterpret_cast<const u32x4_t *>(at + x * Lds<T>::kRows + j * 1024) + lane_id());
+        for (int j = 0; j < 2; j++)
+            w[j] = *gp(reinterpret_cast<const u32x4_t *>(at + x * Lds<float>::kRows + j * 1024) + lane_id());
     }
-    __device__ __forceinline__ typename Row<T>::Op operand() const
+    __device__ __forceinline__ Part<3> operand() const
     {
-        if constexpr (Lds<T>::R == 1) return typename Row<T>::Op{{w[0]}};
-        else {
-            float f[8];
+        float f[8];
 #pragma unroll
-            for (int j = 0; j < 8; j++) f[j] = __uint_as_float(w[j >> 2][j & 3]);
-            return split8<3>(f);
-        }
+        for (int j = 0; j < 8; j++) f[j] = __uint_as_float(w[j >> 2][j & 3]);
+        return split8<3>(f);
     }
 };
 
@@ -1348,15 +1313,13 @@ struct GradLds {
 // One chunk and key head: wavefront w makes columns 32 w .. of dq and dk.  What rows of K and Q
 // are taken with, D, D^T and B + B^T, is made by a wavefront each and handed over in LDS; the
 // first makes dgate and dbeta.  Bound by what it reads, half of it the two sides' states.
-template <typename T, int KT, typename W>
-__global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(DeltaArgs A)
+template <typename T, int KT>
+__global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
 {
     constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT;
     typedef GradLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
-    constexpr int SO = sizeof(W) == sizeof(T) ? IN : 2;  // orders of products with states
-    constexpr bool EXACT = sizeof(W) == 2;               // states that are kept as they are need it not
-    __shared__ float red[KT][3][32], cross[3][32], cols[2][2][32], owns[32];
+    __shared__ float red[KT][3][32], cross[3][32], owns[32];
     const int tile = blockIdx.x, key = blockIdx.y;
     const int wave = uniform((int)(threadIdx.x >> 6)), l = lane_id(), c = l & 31, h = l >> 5;
     const SegTile s = seg_find<kCut>(A.off, A.n, nullptr, 0, A.samples, 1, tile);
@@ -1405,11 +1368,11 @@ __global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(D
             bring(head);
         }
         const int64_t number = (int64_t)tile * A.heads + head, n = A.slices;
-        const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<W>::kRows;
-        const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<W>::kRows;
+        const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<float>::kRows;
+        const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<float>::kRows;
         const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * 2048, oat = zat + n * 2048;
         // the states' rows are on their way while the chunk's own products are made
-        Kept<W> S[kKeptMost], E[kKeptMost];
+        Kept S[kKeptMost], E[kKeptMost];
 #pragma unroll
         for (int x = 0; x < kKeptMost; x++)
             if (x < n) {
@@ -1450,7 +1413,6 @@ __global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(D
                 }
             }
             float across = 0.f, own = 0.f;               // own: z.u of the row
-            float below = 0.f, size = 0.f;               // of the lane's column, from the row itself on
 #pragma unroll
             for (int g4 = 0; g4 < 4; g4++) {
                 const int y0 = 8 * g4 + 4 * h;
@@ -1466,20 +1428,13 @@ __global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(D
                         across += before ? f[r] * k[r] : 0.f;
                     } else if (what == 1) {              // D_yx
                         f[r] = !before ? A.scale * exp_of(-dhi, -dlo) * p[r] : 0.f;
-                        const float x = f[r] * k[r];
-                        across -= after ? x : 0.f;
-                        if (EXACT) {
-                            below += x;
-                            size += fabsf(x);
-                        }
+                        across -= after ? f[r] * k[r] : 0.f;
                     } else {                             // B_xy or B_yx
                         const float d = exp_of(before ? dhi : -dhi, before ? dlo : -dlo);
                         f[r] = before ? -b * d * p[r] : after ? -yb[e] * d * p2[r] : 0.f;
-                        const float x = f[r] * k[r], above = before ? x : 0.f;
-                        across += above;
-                        below += x - above;
+                        const float x = f[r] * k[r];
+                        across += before ? x : -x;
                         if (y == c) own += p[r];
-                        if (EXACT) size += fabsf(x);
                     }
                 }
             }
@@ -1490,17 +1445,8 @@ __global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(D
                 for (int i = 0; i < OUT; i++)
                     lds_write(at + L::with + ((what * 2 + kc) * OUT + i) * 1024 + 16 * l, o.p[i]);
             }
-            if (what == 2) across -= below;
             across = both(across);
             if (h == 0) cross[what][c] = across;
-            if (EXACT && what) {
-                below = both(below);
-                size = both(size);
-                if (h == 0) {
-                    cols[what - 1][0][c] = below;
-                    cols[what - 1][1][c] = size;
-                }
-            }
             if (what == 2) {
                 own = both(own);
                 if (h == 0) owns[c] = own;
@@ -1520,10 +1466,10 @@ __global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(D
         for (int x = 0; x < kKeptMost; x++)
             if (x < n) {
                 const auto s0 = S[x].operand(), e0 = E[x].operand();
-                mm<SO>(t1, s0, Lds<T>::rows(oat, x));
+                mm<OUT>(t1, s0, Lds<T>::rows(oat, x));
                 mm<OUT>(t2, s0, written<T>(zat, x));
                 mm<OUT>(t3, e0, written<T>(uat, x));
-                mm<SO>(se, s0, e0);
+                mm<OUT>(se, s0, e0);
             }
         float inner = 0.f;
 #pragma unroll
@@ -1563,14 +1509,6 @@ __global__ __launch_bounds__(64 * KT, sizeof(W) == 2 ? 2 : 1) void delta_grads(D
                 from += red[w][0][c];
                 into += red[w][1][c];
                 state += red[w][2][c];
-            }
-            // What row j brings by its write, W_j k_j.(E u_j), is dU_j.u_j less what O takes of it,
-            //   z_j.u_j - sum of B_ij k_i.k_j (i > j) - sum of D_ij q_i.k_j (i >= j),
-            // without the rounding of E (bf16: dgate's error 2.8e-3 and 2.9e-3, 2.0e-3 and
-            // 2.6e-3 so).  Where that is a small rest of its parts, the product with E has more of it.
-            if (EXACT) {
-                const float rest = owns[c] - cols[0][0][c] - cols[1][0][c];
-                if (fabsf(rest) * 64.f > fabsf(owns[c]) + cols[0][1][c] + cols[1][1][c]) into = rest;
             }
             float suffix = from, prefix = into;
 #pragma unroll
@@ -1783,7 +1721,7 @@ struct DeltaPlan {
     size_t el;
     int kt, slices;
     int64_t tiles;
-    bool cut, whole;                         // whole: states are kept in fp32 for the gradients
+    bool cut;
     size_t rec, move;                        // bytes of a record, of a segment's matrix
     size_t recs, states, us, moves, starts;  // bytes of all of them
     int ranks;                               // workgroups that order the samples
@@ -1819,14 +1757,7 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     p.rec = bf ? Rec<uint16_t>::size : Rec<float>::size;
     p.recs = (size_t)p.tiles * d->heads * p.rec;
     p.us = (size_t)p.tiles * d->heads * p.slices * 2048;
-    p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 1024;
-    // The states that bf16 gradients read are kept in fp32 where they are few, and so the sums of a
-    // few rows are as exact as bf16 shows (dgate 1.7e-3 to 2.0e-3 off, dk 1.7e-3; kept in bf16 2.0e-3 to
-    // 2.6e-3, and 4.4e-3 where large first and last states met in 20 short samples; dk 2.3e-3).
-    // Kept in bf16 and in fp32, a step of training in us: 1.6 MB in bf16 167, 167; 7.5 MB 168, 168 to 178;
-    // 16 MB 238, 263; 24 MB 173, 190; 66 MB 239, 345; 293 MB 781, 1195.
-    p.whole = !bf || p.states <= (size_t(1) << 24);
-    if (p.whole) p.states *= 2;
+    p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 2048;
     if (p.cut) {
         const size_t segments = (size_t)seg_tiles(d->n, d->samples, 1, kSpan) * d->heads;
         p.move = (size_t)p.kt * p.kt * 6144 * (train ? 2 : 1);
@@ -1910,7 +1841,6 @@ DeltaArgs delta_args(const emb_delta *d, const DeltaPlan &p)
     A.scale = d->scale;
     A.rec_size = (int64_t)p.rec;
     A.cut = p.cut;
-    A.whole = p.whole;
     A.move_size = (int64_t)p.move / 2;
     return A;
 }
@@ -1960,15 +1890,13 @@ void delta_forward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, bool
     if (A.cut) {
         // wavefronts enough for either kind
         const int most = A.slices > 2 * KT ? A.slices : 2 * KT;
-        delta_launch(delta_scan<T, KT, false, true, T>, dim3((unsigned)walks, 2), 64 * most + 64, 2 * WalkLds<T, KT, true>::size(A.slices),
+        delta_launch(delta_scan<T, KT, false, true>, dim3((unsigned)walks, 2), 64 * most + 64, 2 * WalkLds<T, KT, true>::size(A.slices),
                      A, st);
         delta_launch(delta_join<KT, false>, joins, 64 * kJoined + 64, join, A, st);
     }
     const int stages = 2 * WalkLds<T, KT, false>::size(A.slices), threads = 64 * A.slices + 64;
-    if (!train) delta_launch(delta_scan<T, KT, false, false, T>, walk, threads, stages + A.slices * kScratch<T, T, KT, false>, A, st);
-    else if (A.whole)
-        delta_launch(delta_scan<T, KT, true, false, float>, walk, threads, stages + A.slices * kScratch<T, float, KT, true>, A, st);
-    else delta_launch(delta_scan<T, KT, true, false, T>, walk, threads, stages + A.slices * kScratch<T, T, KT, true>, A, st);
+    if (train) delta_launch(delta_scan<T, KT, true, false>, walk, threads, stages + A.slices * kScratch<T, true>, A, st);
+    else delta_launch(delta_scan<T, KT, false, false>, walk, threads, stages + A.slices * kScratch<T, false>, A, st);
 }
 
 template <typename T, int KT>
@@ -1978,18 +1906,11 @@ void delta_backward_launch(const DeltaArgs &A, int64_t tiles, int64_t walks, boo
     const int lds = 2 * WalkLds<T, KT, false>::size(A.slices), join = kJoinRing<KT> * KT * 6144;
     const dim3 joins((unsigned)(A.samples * A.heads), (unsigned)((A.slices + kJoined - 1) / kJoined));
     if (walks && A.cut) {
-        delta_launch(delta_back<T, KT, true, T>, walk, 64 * A.slices + 64, lds, A, st);
+        delta_launch(delta_back<T, KT, true>, walk, 64 * A.slices + 64, lds, A, st);
         delta_launch(delta_join<KT, true>, joins, 64 * kJoined + 64, join, A, st);
     }
-    auto rest = [&](auto kept) {
-        typedef decltype(kept) W;
-        if (walks)
-            delta_launch(delta_back<T, KT, false, W>, walk, 64 * A.slices + 64, lds + A.slices * kScratch<T, W, KT, true>, A, st);
-        delta_launch(delta_grads<T, KT, W>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A,
-                     st);
-    };
-    if (A.whole) rest(float{});
-    else rest(T{});
+    if (walks) delta_launch(delta_back<T, KT, false>, walk, 64 * A.slices + 64, lds + A.slices * kScratch<T, true>, A, st);
+    delta_launch(delta_grads<T, KT>, dim3((unsigned)tiles, (unsigned)A.key_heads), 64 * KT, GradLds<T, KT>::size(A.slices), A, st);
 }
 
 #define EMB_DELTA_SIZES(NAME, T)                             \
