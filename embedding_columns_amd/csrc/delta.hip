@@ -252,7 +252,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
     return row_buffer(static_cast<const T *>(p) + elements, 0, 0x7FFFFFFF);
 }
 
-// A record: the scalars of the walks, N - I in NN parts, P in OUT, the other scalars.  The matrices
+// A record: the scalars of the walks, N - I in NN parts, P in ST, the other scalars.  The matrices
 // are triangular.  A part is rows 16 .. in a KB, a row's 4 pieces of 16 bytes side by side, piece g
 // (columns 4 g .. and 16 + 4 g ..) of row r at g ^ (r >> 2), see Lane, and columns .. 15 of the
 // other rows in 512 bytes, pieces of 8 bytes, g of row r at g ^ (r >> 3) * 2 (so that 32 lanes that
@@ -261,7 +261,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
 constexpr int kMatrix = 3 * 512;
 template <typename T>
 struct Rec {
-    static constexpr int sc = 0, n = kScWalk * 4, p = n + Prec<T>::NN * kMatrix, more = p + Prec<T>::OUT * kMatrix,
+    static constexpr int sc = 0, n = kScWalk * 4, p = n + Prec<T>::NN * kMatrix, more = p + Prec<T>::ST * kMatrix,
                          size = more + (kScalars - kScWalk) * 4;
 };
 __device__ __forceinline__ uint32_t matrix_above(int row, int quad) { return 1024 + (row * 4 + (quad ^ (row >> 3) * 2)) * 8; }
@@ -315,7 +315,7 @@ __device__ __forceinline__ void delta_order(const DeltaArgs &A, int block)
 template <typename T, int KT>
 __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, NN = Prec<T>::NN, OUT = Prec<T>::OUT;
+    constexpr int IN = Prec<T>::IN, NN = Prec<T>::NN, ST = Prec<T>::ST;
     constexpr int kPitch = 36;
     __shared__ __attribute__((aligned(16))) float lds[32 * kPitch];
     __shared__ __attribute__((aligned(16))) float sc[kScalars];
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         }
     };
     wave_sync();
-    leave(std::integral_constant<int, OUT>{}, Rec<T>::p);
+    leave(std::integral_constant<int, ST>{}, Rec<T>::p);
     wave_sync();
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++)
@@ -1147,7 +1147,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 #pragma unroll
             for (int e = 0; e < 4; e++) X.t[a][e] *= wt.t[a][e];
         }
-        lane.template matrix_turned<ST, OUT>(X, at + L::p, dp);
+        lane.template matrix_turned<ST, ST>(X, at + L::p, dp);
         const Part<ST> xp = operand<ST>(X);
         Block Z = X;
         lane.template matrix_turned<ST, NN>(Z, at + L::n, xp);

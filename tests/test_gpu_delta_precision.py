@@ -1,5 +1,6 @@
-"""The gated delta rule's arithmetic: fp32 results are within a few roundings of the 64-bit form's
-over a whole tensor; a sample's results do not depend on what else is in the call."""
+"""The gated delta rule's arithmetic: the states of bf16 calls are those of fp32 calls with the same
+numbers, to the bit; fp32 results are within a few roundings of the 64-bit form's over a whole
+tensor; a sample's results do not depend on what else is in the call."""
 import pytest
 import torch
 
@@ -21,6 +22,10 @@ def alone(t, s):
     return one, rows
 
 
+def as_f32(t):
+    return {**t, **{x: t[x].float() for x in ROWS}}
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_a_sample_in_a_large_batch(dtype):
     """The same bits alone and among so many that what is kept for the gradients passes 32 MB."""
@@ -36,6 +41,22 @@ def test_a_sample_in_a_large_batch(dtype):
 
 CASES = [([100, 65, 2, 0], 2, 2, 32, 32), ([37, 70], 1, 2, 40, 72), ([300, 77], 1, 2, 16, 128), ([90] * 20, 4, 4, 128, 128),
          ([200, 333], 2, 4, 64, 64), ([150], 1, 1, 96, 24), ([4300, 3000], 1, 1, 64, 32)]
+
+
+def both(case, seed, strong=False):
+    lens, kh, h, dk, dv = case
+    t = make(lens, kh, h, dk, dv, BF16, masked=0.05, seed=seed)
+    if strong:                                           # states that the rows' own writes are small beside
+        t["state"] *= 8.0
+        t["dlast"] *= 8.0
+    return call(t), call(as_f32(t))
+
+
+@pytest.mark.parametrize("case", CASES)
+def test_bf16_states_are_fp32s(case):
+    got, want = both(case, 22)
+    for name in ("last", "dstate"):
+        assert torch.equal(got[name], want[name]), name
 
 
 @pytest.mark.parametrize("strong", [False, True])
