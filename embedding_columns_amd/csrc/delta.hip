@@ -37,13 +37,12 @@
 // register i of half h = lane >> 5 row kk(i, h) = 8 (i >> 2) + 4 h + (i & 3)), which is also how
 // the next product takes its second operand if its contraction runs in that order.  The state
 // is fp32.  What enters a product is cut into bf16 parts, the first rounded from the value,
-// the next from what is left of it: inputs in bf16 are one part, fp32 ones three (24 bits);
-// the state and what makes it (N, U, Z, P^T) are three, so that the states that come out
-// are fp32's; what only bf16 outputs are made of is two (16 bits), as are the U and Z
-// that the gradients read (with one, dgate is off by up to 4.4e-3, then 2.9e-3).  The states they
-// read are kept in fp32.  Products of parts whose bits lie below the last part's are left out.
+// the next from what is left of it: inputs in bf16 are one part, all else three (24 bits).
+// Products of parts whose bits lie below the last part's are left out.  What passes between the
+// kernels is fp32 or three parts, so that a bf16 call computes what an fp32 call does from the same
+// numbers, to the bit, and rounds it once (what only bf16 outputs are made of in two parts, 16 bits:
+// 0.3 % of a bf16 output's elements one step away).
 #include <string>
-#include <type_traits>
 
 #include "sequence.h"
 
@@ -91,17 +90,10 @@ struct DeltaArgs {
     int32_t vec, ovec;         // dq and dk rows move in pieces of 4; o and dv rows in 16 bytes
 };
 
-// parts of the inputs, of what makes the states, of what makes outputs alone, and of N - I
+// parts of the inputs and of what is made of them
 template <typename T>
-struct Prec;
-template <>
-struct Prec<uint16_t> {
-    static constexpr int IN = 1, ST = 3, OUT = 2, NN = 3;
-};
-template <>
-struct Prec<float> {
-    static constexpr int IN = 3, ST = 3, OUT = 3, NN = 3;
-};
+constexpr int kIn = sizeof(T) == 2 ? 1 : 3;
+constexpr int kParts = 3;
 
 __device__ __forceinline__ constexpr int kk0(int i) { return 8 * (i >> 2) + (i & 3); }   // + 4 h
 
@@ -252,17 +244,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void *p, int64_t 
     return row_buffer(static_cast<const T *>(p) + elements, 0, 0x7FFFFFFF);
 }
 
-// A record: the scalars of the walks, N - I in NN parts, P in ST, the other scalars.  The matrices
+// A record: the scalars of the walks, N - I and P in their parts, the other scalars.  The matrices
 // are triangular.  A part is rows 16 .. in a KB, a row's 4 pieces of 16 bytes side by side, piece g
 // (columns 4 g .. and 16 + 4 g ..) of row r at g ^ (r >> 2), see Lane, and columns .. 15 of the
 // other rows in 512 bytes, pieces of 8 bytes, g of row r at g ^ (r >> 3) * 2 (so that 32 lanes that
-// read 16 rows meet every bank once).  Whole matrices took 11 KB of bf16 records for 8.5, and
-// delta_histories 421 us for 374.
+// read 16 rows meet every bank once).  10 KB; with whole matrices it would be 13.
 constexpr int kMatrix = 3 * 512;
-template <typename T>
 struct Rec {
-    static constexpr int sc = 0, n = kScWalk * 4, p = n + Prec<T>::NN * kMatrix, more = p + Prec<T>::ST * kMatrix,
-                         size = more + (kScalars - kScWalk) * 4;
+    static constexpr int sc = 0, n = kScWalk * 4, p = n + kParts * kMatrix, more = p + kParts * kMatrix, size = more + (kScalars - kScWalk) * 4;
 };
 __device__ __forceinline__ uint32_t matrix_above(int row, int quad) { return 1024 + (row * 4 + (quad ^ (row >> 3) * 2)) * 8; }
 __device__ __forceinline__ uint32_t matrix_below(int row, int piece) { return (row * 4 + (piece ^ (row >> 2))) * 16; }
@@ -315,7 +304,6 @@ __device__ __forceinline__ void delta_order(const DeltaArgs &A, int block)
 template <typename T, int KT>
 __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, NN = Prec<T>::NN, ST = Prec<T>::ST;
     constexpr int kPitch = 36;
     __shared__ __attribute__((aligned(16))) float lds[32 * kPitch];
     __shared__ __attribute__((aligned(16))) float sc[kScalars];
@@ -371,7 +359,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     char *rec = A.rec + ((int64_t)tile * A.heads + head) * A.rec_size;
     // what only the gradients take is left for them alone
     if (l < kScWalk / 4 || A.s0 || l == kScKept / 4)
-        *gp(reinterpret_cast<f32x4_t *>(rec + (l < kScWalk / 4 ? Rec<T>::sc : Rec<T>::more - kScWalk * 4)) + l) =
+        *gp(reinterpret_cast<f32x4_t *>(rec + (l < kScWalk / 4 ? Rec::sc : Rec::more - kScWalk * 4)) + l) =
             *reinterpret_cast<const f32x4_t *>(sc + 4 * l);
 
     const auto qb = buffer<T>(A.q, row * A.qs + key * A.qh), kb = buffer<T>(A.k, row * A.ks + key * A.kh);
@@ -382,8 +370,8 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
     for (int x = 0; x < 2 * KT; x++) {
         const uint32_t at = (uint32_t)((16 * x + 8 * h) * sizeof(T));
         const auto K = Row<T>::eight(kb, kat + at), Q = Row<T>::eight(qb, qat + at);
-        mm<IN>(kk, K, K);
-        mm<IN>(kq, K, Q);                                      // k_j.q_i, lane i
+        mm<kIn<T>>(kk, K, K);
+        mm<kIn<T>>(kq, K, Q);                                  // k_j.q_i, lane i
     }
     // P and M as rows of i, in LDS, and from there into the record
     float m[16];
@@ -402,8 +390,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         }
         *reinterpret_cast<f32x4_t *>(lds + c * kPitch + j0) = p;
     }
-    auto leave = [&](auto parts, int at) {               // the matrix in LDS into the record
-        constexpr int N = decltype(parts)::value;
+    auto leave = [&](int at) {                           // the matrix in LDS into the record
         const int row = l & 15, g = l >> 4;
 #pragma unroll
         for (int a = 0; a < 2; a++) {
@@ -414,9 +401,9 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 #pragma unroll
                 for (int i = 0; i < 4; i++) f[e + i] = x[i];
             }
-            const Part<N> p = split8<N>(f);
+            const Part<kParts> p = split8<kParts>(f);
 #pragma unroll
-            for (int i = 0; i < N; i++) {
+            for (int i = 0; i < kParts; i++) {
                 char *to = rec + at + i * kMatrix;
                 if (a) *gp(reinterpret_cast<u32x4_t *>(to + matrix_below(row, g))) = p.p[i];
                 else *gp(reinterpret_cast<u32x2_t *>(to + matrix_above(row, g))) = u32x2_t{p.p[i][0], p.p[i][1]};
@@ -424,7 +411,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
         }
     };
     wave_sync();
-    leave(std::integral_constant<int, ST>{}, Rec<T>::p);
+    leave(Rec::p);
     wave_sync();
 #pragma unroll
     for (int g4 = 0; g4 < 4; g4++)
@@ -449,7 +436,7 @@ __global__ __launch_bounds__(64) void delta_prepare(DeltaArgs A)
 #pragma unroll
     for (int i = 0; i < 16; i++) lds[(16 * h + i) * kPitch + c] = 16 * h + i == c ? 0.f : h ? nn[16 + i] : nn[i];
     wave_sync();
-    leave(std::integral_constant<int, NN>{}, Rec<T>::n);
+    leave(Rec::n);
 }
 
 // ------------------------------------------------------------ chunks in LDS
@@ -745,11 +732,6 @@ struct Turn {
 #pragma unroll
             for (int e = 0; e < 4; e++) lds_write(scratch + ((r0 + e) * 17 + c) * 4, f[e]);
     }
-    // bf16: the same of two words of a part
-    static __device__ __forceinline__ void fill2(uint32_t scratch, int r0, uint32_t x, uint32_t y)
-    {
-        lds_write(scratch + (lane_id() & 15) * 72 + r0 * 2, u32x2_t{x, y});
-    }
     __device__ __forceinline__ void take(uint32_t scratch)
     {
         const int l = lane_id(), h = l >> 5;
@@ -775,27 +757,6 @@ struct Turn {
         for (int a = 0; a < 2; a++) fill(scratch, 16 * a + 4 * g, b.t[a]);
         wave_sync();
         take(scratch);
-    }
-    // a block's rows for the gradients, fp32 or as two parts of bf16, 2 KB
-    static __device__ __forceinline__ void leave(uint32_t scratch, const Block &b, const u32x4_t &hi, const u32x4_t &lo, char *to)
-    {
-        Turn rows;
-        if constexpr (R == 2) {
-            rows.turn(scratch, b);
-            rows.keep(to);
-        } else {
-            const int g = lane_id() >> 4;
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const u32x4_t &w = i ? lo : hi;
-                wave_sync();
-                fill2(scratch, 4 * g, w[0], w[1]);
-                fill2(scratch, 16 + 4 * g, w[2], w[3]);
-                wave_sync();
-                rows.take(scratch);
-                rows.keep(to + 1024 * i);
-            }
-        }
     }
     // as operands for the gradients
     __device__ __forceinline__ void keep(char *to) const
@@ -898,7 +859,13 @@ __device__ __forceinline__ void state_write(const Block (&S)[KT], float *p, int 
 // a wavefront's scratch: for rows of T, and in training for the state's in fp32
 template <typename T, bool TRAIN>
 constexpr int kScratch = TRAIN ? Turn<float>::kBytes : Turn<T>::kBytes;
-// Block x of the state as the gradients read it, fp32 rows as operands of 32 x 16 elements.
+// A block's rows as the gradients read them, in fp32, 2 KB, and block x of the state.
+__device__ __forceinline__ void rows_keep(uint32_t scratch, const Block &b, char *to)
+{
+    Turn<float> rows;
+    rows.turn(scratch, b);
+    rows.keep(to);
+}
 __device__ __forceinline__ void state_keep(uint32_t scratch, const Block &S, char *to, int x, int slices, int slice)
 {
     const int g = lane_id() >> 4;
@@ -915,8 +882,8 @@ __device__ __forceinline__ void state_keep(uint32_t scratch, const Block &S, cha
 // ahead, and does nothing else.  SUM walks take no Q and no P.
 template <typename T, int KT, bool SUM>
 struct WalkLds {
-    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = SUM ? q : 2 * q, sc = rec + Rec<T>::sc, n = rec + Rec<T>::n,
-                         p = rec + Rec<T>::p, pieces = ((SUM ? Rec<T>::p : Rec<T>::more) + 1023) / 1024, v = rec + pieces * 1024;
+    static constexpr int q = 2 * KT * Lane<T>::kTile, rec = SUM ? q : 2 * q, sc = rec + Rec::sc, n = rec + Rec::n,
+                         p = rec + Rec::p, pieces = ((SUM ? Rec::p : Rec::more) + 1023) / 1024, v = rec + pieces * 1024;
     static __host__ __device__ constexpr int size(int slices) { return v + (slices + 1) / 2 * 2 * Lane<T>::kTile; }
 };
 
@@ -927,7 +894,7 @@ __device__ __forceinline__ uint32_t kept_rows(const DeltaArgs &A, const Walk &w,
     const int left = min(w.rows - chunk * kCut, kCut);
     if (chunk < 0 || left <= 0) return 0;
     const char *rec = A.rec + ((int64_t)(w.tile0 + chunk) * A.heads + w.head) * A.rec_size;
-    return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec<T>::more) + kScKept - kScWalk)) & low_bits(left);
+    return __float_as_uint(*gp(reinterpret_cast<const float *>(rec + Rec::more) + kScKept - kScWalk)) & low_bits(left);
 }
 
 // The wavefront that brings the chunks, in the order chunk(0), chunk(1), ... (steps of the walk);
@@ -979,7 +946,6 @@ __device__ __forceinline__ int move_at(int row, int col)
 template <typename T, int KT, bool TRAIN, bool SUM>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
-    constexpr int ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
     typedef WalkLds<T, KT, SUM> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
@@ -1020,12 +986,12 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         Block X = zero_block(), Y = zero_block(), V = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
-            const Part<ST> sp = operand<ST>(S[x]);
+            const Part<kParts> sp = operand<kParts>(S[x]);
             if (TRAIN && !SUM) state_keep(scratch, S[x], states, x, A.slices, slice);
 #pragma unroll
             for (int a = 0; a < 2; a++) {
-                mm<ST>(X.t[a], lane.row(at, x, a), sp);
-                if (!SUM) mm<OUT>(Y.t[a], lane.row(at + L::q, x, a), sp);
+                mm<kParts>(X.t[a], lane.row(at, x, a), sp);
+                if (!SUM) mm<kParts>(Y.t[a], lane.row(at + L::q, x, a), sp);
             }
         }
         const Block b = row_scalars(sc + 4 * kScB), bg = row_scalars(sc + 4 * kScBG);
@@ -1034,9 +1000,9 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         for (int a = 0; a < 2; a++)
 #pragma unroll
             for (int e = 0; e < 4; e++) X.t[a][e] = fmaf(b.t[a][e], V.t[a][e], -bg.t[a][e] * X.t[a][e]);
-        const Part<ST> xp = operand<ST>(X);
+        const Part<kParts> xp = operand<kParts>(X);
         Block U = X;                                     // N is I and what the record has
-        lane.template matrix<ST, NN>(U, at + L::n, xp);
+        lane.template matrix<kParts, kParts>(U, at + L::n, xp);
         const Block wt = row_weights(sc);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block wu = U;
@@ -1044,25 +1010,25 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         for (int a = 0; a < 2; a++)
 #pragma unroll
             for (int e = 0; e < 4; e++) wu.t[a][e] *= wt.t[a][e];
-        const Part<ST> up = operand<ST>(wu);
+        const Part<kParts> up = operand<kParts>(wu);
 #pragma unroll
         for (int x = 0; x < KT; x++)
 #pragma unroll
             for (int a = 0; a < 2; a++) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) S[x].t[a][e] *= end;
-                mm<ST>(S[x].t[a], lane.column(at, x, a), up);
+                mm<kParts>(S[x].t[a], lane.column(at, x, a), up);
             }
         if (!SUM) {
             const Block sg = row_scalars(sc + 4 * kScG);
-            const Part<OUT> op = operand<OUT>(U);
+            const Part<kParts> op = operand<kParts>(U);
 #pragma unroll
             for (int a = 0; a < 2; a++) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) Y.t[a][e] *= sg.t[a][e];
             }
-            lane.template matrix<OUT, OUT>(Y, at + L::p, op);
-            if (TRAIN) Turn<T>::leave(scratch, U, op.p[0], op.p[1], u);
+            lane.template matrix<kParts, kParts>(Y, at + L::p, op);
+            if (TRAIN) rows_keep(scratch, U, u);
             Turn<T> rows;
             rows.turn(scratch, Y);
             rows.write(o, r < w.rows - i * kCut, c, A.dv, A.ovec);
@@ -1099,7 +1065,6 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 template <typename T, int KT, bool SUM>
 __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, ST = Prec<T>::ST, OUT = Prec<T>::OUT, NN = Prec<T>::NN;
     typedef WalkLds<T, KT, false> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     const Walk w = walk_of(A);
@@ -1134,23 +1099,23 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
         Block X = zero_block();
 #pragma unroll
         for (int x = 0; x < KT; x++) {
-            const Part<ST> ep = operand<ST>(E[x]);
+            const Part<kParts> ep = operand<kParts>(E[x]);
             if (!SUM) state_keep(scratch, E[x], states, x, A.slices, slice);
 #pragma unroll
-            for (int a = 0; a < 2; a++) mm<ST>(X.t[a], lane.row(at, x, a), ep);
+            for (int a = 0; a < 2; a++) mm<kParts>(X.t[a], lane.row(at, x, a), ep);
         }
         const Block wt = row_weights(sc);
         Block D = lane.block(at + L::v, columns);
-        const Part<IN> dp = operand<IN>(D);
+        const Part<kIn<T>> dp = operand<kIn<T>>(D);
 #pragma unroll
         for (int a = 0; a < 2; a++) {
 #pragma unroll
             for (int e = 0; e < 4; e++) X.t[a][e] *= wt.t[a][e];
         }
-        lane.template matrix_turned<ST, ST>(X, at + L::p, dp);
-        const Part<ST> xp = operand<ST>(X);
+        lane.template matrix_turned<kParts, kParts>(X, at + L::p, dp);
+        const Part<kParts> xp = operand<kParts>(X);
         Block Z = X;
-        lane.template matrix_turned<ST, NN>(Z, at + L::n, xp);
+        lane.template matrix_turned<kParts, kParts>(Z, at + L::n, xp);
         const Block bg = row_scalars(sc + 4 * kScBG), sg = row_scalars(sc + 4 * kScG);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block gz = Z;
@@ -1161,19 +1126,18 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
                 gz.t[a][e] *= -bg.t[a][e];
                 D.t[a][e] *= sg.t[a][e];
             }
-        const Part<ST> zp = operand<ST>(gz), op = operand<ST>(D);
+        const Part<kParts> zp = operand<kParts>(gz), op = operand<kParts>(D);
 #pragma unroll
         for (int x = 0; x < KT; x++)
 #pragma unroll
             for (int a = 0; a < 2; a++) {
 #pragma unroll
                 for (int e = 0; e < 4; e++) E[x].t[a][e] *= end;
-                mm<ST>(E[x].t[a], lane.column(at, x, a), zp);
-                mm<ST>(E[x].t[a], lane.column(at + L::q, x, a), op);
+                mm<kParts>(E[x].t[a], lane.column(at, x, a), zp);
+                mm<kParts>(E[x].t[a], lane.column(at + L::q, x, a), op);
             }
         if (!SUM) {
-            const Part<OUT> kept = operand<OUT>(Z);
-            Turn<T>::leave(scratch, Z, kept.p[0], kept.p[1], z);
+            rows_keep(scratch, Z, z);
             Turn<T> rows;
             const Block b = row_scalars(sc + 4 * kScB);
 #pragma unroll
@@ -1296,17 +1260,9 @@ struct Kept {
     }
 };
 
-// rows of U or Z in LDS as an operand: 2 KB a 16 columns
-template <typename T>
-__device__ __forceinline__ Part<sizeof(T) == 2 ? 2 : 3> written(uint32_t at, int x)
-{
-    if constexpr (sizeof(T) == 2) return staged<2>(at, x);
-    else return Lds<T>::rows(at, x);
-}
-
 template <typename T, int KT>
 struct GradLds {
-    static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, with = sc + 1024, u = with + 6 * Prec<T>::OUT * 1024;
+    static constexpr int q = 2 * KT * Lds<T>::kRows, sc = 2 * q, with = sc + 1024, u = with + 6 * kParts * 1024;
     static __host__ __device__ int size(int slices) { return u + slices * (2 * 2048 + Lds<T>::kRows); }
 };
 
@@ -1316,7 +1272,6 @@ struct GradLds {
 template <typename T, int KT>
 __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
 {
-    constexpr int IN = Prec<T>::IN, OUT = Prec<T>::OUT;
     typedef GradLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
     __shared__ float red[KT][3][32], cross[3][32], owns[32];
@@ -1351,7 +1306,7 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
     auto bring = [&](int head) {
         const int64_t number = (int64_t)tile * A.heads + head;
         const int n = A.slices;
-        if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size), at + L::sc, 16 * l + (l < kScWalk / 4 ? Rec<T>::sc : Rec<T>::more - kScWalk * 4), 0);
+        if (wave == 0) load_to_lds(row_rsrc(A.rec + number * A.rec_size), at + L::sc, 16 * l + (l < kScWalk / 4 ? Rec::sc : Rec::more - kScWalk * 4), 0);
         bring_flat(row_rsrc(static_cast<const char *>(A.u) + number * n * 2048), at + L::u, 2 * n, wave, KT);
         bring_flat(row_rsrc(static_cast<const char *>(A.z) + number * n * 2048), at + L::u + n * 2048, 2 * n, wave, KT);
         bring_rows<T>(row_rsrc(static_cast<const T *>(A.dout) + row * A.ds + head * A.dh), row_at<T>(kept, A.ds),
@@ -1391,25 +1346,25 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
             if (what % KT != wave) continue;
             f32x16_t p = zero16(), p2 = zero16(), k = zero16(), f;
             for (int x = 0; x < n; x++) {
-                const auto U = written<T>(uat, x);
+                const auto U = Lds<float>::rows(uat, x);
                 if (what == 2) {
-                    const auto Z = written<T>(zat, x);
-                    mm<OUT>(p, U, Z);                    // u_j.z_i, lane i
-                    mm<OUT>(p2, Z, U);                   // z_i.u_j, lane j
+                    const auto Z = Lds<float>::rows(zat, x);
+                    mm<kParts>(p, U, Z);                 // u_j.z_i, lane i
+                    mm<kParts>(p2, Z, U);                // z_i.u_j, lane j
                 } else {
                     const auto D = Lds<T>::rows(oat, x);
-                    if (what == 0) mm<OUT>(p, U, D);     // u_j.dO_i, lane i
-                    else mm<OUT>(p, D, U);               // dO_i.u_j, lane j
+                    if (what == 0) mm<kParts>(p, U, D); // u_j.dO_i, lane i
+                    else mm<kParts>(p, D, U);            // dO_i.u_j, lane j
                 }
             }
 #pragma unroll
             for (int x = 0; x < 2 * KT; x++) {
                 const auto K = Lds<T>::rows(at, x);
-                if (what == 2) mm<IN>(k, K, K);
+                if (what == 2) mm<kIn<T>>(k, K, K);
                 else {
                     const auto Q = Lds<T>::rows(at + L::q, x);
-                    if (what == 0) mm<IN>(k, K, Q);
-                    else mm<IN>(k, Q, K);
+                    if (what == 0) mm<kIn<T>>(k, K, Q);
+                    else mm<kIn<T>>(k, Q, K);
                 }
             }
             float across = 0.f, own = 0.f;               // own: z.u of the row
@@ -1440,10 +1395,10 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
             }
 #pragma unroll
             for (int kc = 0; kc < 2; kc++) {
-                const Part<OUT> o = operand<OUT>(f, kc);
+                const Part<kParts> o = operand<kParts>(f, kc);
 #pragma unroll
-                for (int i = 0; i < OUT; i++)
-                    lds_write(at + L::with + ((what * 2 + kc) * OUT + i) * 1024 + 16 * l, o.p[i]);
+                for (int i = 0; i < kParts; i++)
+                    lds_write(at + L::with + ((what * 2 + kc) * kParts + i) * 1024 + 16 * l, o.p[i]);
             }
             across = both(across);
             if (h == 0) cross[what][c] = across;
@@ -1456,9 +1411,9 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
 #pragma unroll
         for (int kc = 0; kc < 2; kc++) {
             const auto kt = Lds<T>::turned(at, columns, wave, kc), qt = Lds<T>::turned(at + L::q, columns, wave, kc);
-            mm<OUT>(dq, kt, staged<OUT>(at + L::with, kc));
-            mm<OUT>(dk, kt, staged<OUT>(at + L::with, 4 + kc));
-            mm<OUT>(dk, qt, staged<OUT>(at + L::with, 2 + kc));
+            mm<kParts>(dq, kt, staged<kParts>(at + L::with, kc));
+            mm<kParts>(dk, kt, staged<kParts>(at + L::with, 4 + kc));
+            mm<kParts>(dk, qt, staged<kParts>(at + L::with, 2 + kc));
         }
         // with the states: rows of S and E by rows of dO, Z and U, and the rows' own products of S and E
         f32x16_t t1 = zero16(), t2 = zero16(), t3 = zero16(), se = zero16();
@@ -1466,10 +1421,10 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
         for (int x = 0; x < kKeptMost; x++)
             if (x < n) {
                 const auto s0 = S[x].operand(), e0 = E[x].operand();
-                mm<OUT>(t1, s0, Lds<T>::rows(oat, x));
-                mm<OUT>(t2, s0, written<T>(zat, x));
-                mm<OUT>(t3, e0, written<T>(uat, x));
-                mm<OUT>(se, s0, e0);
+                mm<kParts>(t1, s0, Lds<T>::rows(oat, x));
+                mm<kParts>(t2, s0, Lds<float>::rows(zat, x));
+                mm<kParts>(t3, e0, Lds<float>::rows(uat, x));
+                mm<kParts>(se, s0, e0);
             }
         float inner = 0.f;
 #pragma unroll
@@ -1753,8 +1708,7 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     p.slices = (d->dv + 15) / 16;
     p.tiles = seg_tiles(d->n, d->samples, 1, kCut);
     p.cut = delta_cut(d);
-    const bool bf = p.el == 2;
-    p.rec = bf ? Rec<uint16_t>::size : Rec<float>::size;
+    p.rec = Rec::size;
     p.recs = (size_t)p.tiles * d->heads * p.rec;
     p.us = (size_t)p.tiles * d->heads * p.slices * 2048;
     p.states = (size_t)p.tiles * d->heads * p.slices * p.kt * 2048;

@@ -1,6 +1,6 @@
-"""The gated delta rule's arithmetic: the states of bf16 calls are those of fp32 calls with the same
-numbers, to the bit; fp32 results are within a few roundings of the 64-bit form's over a whole
-tensor; a sample's results do not depend on what else is in the call."""
+"""The gated delta rule's arithmetic: bf16 calls compute what fp32 calls do from the same numbers,
+to the bit, and round it once; fp32 results are within a few roundings of the 64-bit form's over
+a whole tensor; a sample's results do not depend on what else is in the call."""
 import pytest
 import torch
 
@@ -60,12 +60,21 @@ def test_bf16_states_are_fp32s(case):
 
 
 @pytest.mark.parametrize("strong", [False, True])
+@pytest.mark.parametrize("case", CASES)
+def test_bf16_is_fp32_rounded_once(case, strong):
+    got, want = both(case, 23, strong)
+    for name in want:
+        x = want[name] if name in ("last", "dstate") else want[name].to(BF16)
+        assert torch.equal(got[name], x), (name, ((got[name] != x).double().mean()).item())
+
+
+@pytest.mark.parametrize("strong", [False, True])
 @pytest.mark.parametrize("case", CASES[:6])
 def test_fp32_over_whole_tensors(case, strong):
     """A chunk's rows pass some eight stages whose roundings are 2^-24 of their terms each (in rows,
-    in the state and in what meets them), and a state that remembers some 50 rows passes two chunks: as independent
-    errors sqrt(16) 2^-24 of the terms' length.  The terms are longer than their sum by at most
-    what the 64-bit form's magnitudes (absolute values throughout) are; 4 times as much is let through."""
+    in the state and in what meets them), and a state that remembers some 50 rows passes two
+    chunks: as independent errors sqrt(16) 2^-24 of the terms' length.  Four times as much is let
+    through, for terms that are longer than their sum."""
     lens, kh, h, dk, dv = case
     t = make(lens, kh, h, dk, dv, F32, masked=0.05, seed=24)
     if strong:
