@@ -623,6 +623,34 @@ struct Lane {
             return split8<3>(f);
         }
     }
+    // elements 32 x + 8 g + 0 .. 7 of row r, for the lanes of quarter g, and element c
+    static __device__ __forceinline__ void eight(uint32_t at, int r, int x, float *f)
+    {
+        const int g = lane_id() >> 4, i = r & 15;
+        const uint32_t from = at + (x * 2 + (r >> 4)) * kTile + (i * 4 + (g ^ (i >> 2))) * 16;
+        const u32x4_t a = lds_read<u32x4_t>(from);
+        if constexpr (R == 1) {
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f[2 * j] = bf16_lo(a[j]);
+                f[2 * j + 1] = bf16_hi(a[j]);
+            }
+        } else {
+            const u32x4_t b = lds_read<u32x4_t>(from + 1024);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                f[j] = __uint_as_float(a[j]);
+                f[4 + j] = __uint_as_float(b[j]);
+            }
+        }
+    }
+    static __device__ __forceinline__ float one(uint32_t at, int r, int c)
+    {
+        const int i = r & 15, e = c & 7;
+        const uint32_t from = at + ((c >> 5) * 2 + (r >> 4)) * kTile + (i * 4 + ((c >> 3 & 3) ^ (i >> 2))) * 16;
+        if constexpr (R == 1) return bf16_lo((uint32_t)lds_read<uint16_t>(from + 2 * e));
+        else return lds_read<float>(from + (e >> 2) * 1024 + (e & 3) * 4);
+    }
     // sixteen lanes read 4 rows of 16 elements and get a column of 4 each
     static __device__ __forceinline__ s16x4_t column4(uint32_t at)
     {
@@ -925,6 +953,118 @@ __device__ __forceinline__ void bring_chunks(const DeltaArgs &A, const Walk &w, 
     }
 }
 
+// Values that are not finite.  A chunk's matrices have zeros where a row has nothing of another,
+// and zero times NaN or infinity is NaN: as products they would carry a row's NaN to rows before it.  A wavefront
+// whose U (backward: Z) is not finite throughout takes that chunk and all behind it row by row, as the rule is
+// written.
+__device__ __forceinline__ bool any_spoiled(const Block &b)
+{
+    float x = 0.f;
+#pragma unroll
+    for (int a = 0; a < 2; a++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) x = fmaf(b.t[a][e], 0.f, x);
+    return __ballot(x != x) != 0;
+}
+
+// sum over the quarters, which share a column
+__device__ __forceinline__ float quarters(float x)
+{
+    x += __shfl_xor(x, 16, 64);
+    return x + __shfl_xor(x, 32, 64);
+}
+
+// a row's share in a block: row r of the lane's column
+__device__ __forceinline__ void put_row(Block &b, int r, float x)
+{
+#pragma unroll
+    for (int a = 0; a < 2; a++)
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (16 * a + 4 * (lane_id() >> 4) + e == r) b.t[a][e] = x;
+}
+
+template <typename T>
+__device__ __forceinline__ float logistic_at(const void *p, int64_t at)
+{
+    return 1.f / (1.f + expf(-Row<T>::get1(static_cast<const T *>(p) + at)));
+}
+
+// f(row in the chunk, a, b) for a chunk's kept rows, from the first or from the last on
+template <typename T, bool BACK, typename F>
+__device__ __forceinline__ void by_rows(const DeltaArgs &A, const Walk &w, int chunk, const F &f)
+{
+    const uint32_t kept = kept_rows<T>(A, w, chunk);
+#pragma unroll 1
+    for (int i = 0; i < kCut; i++) {
+        const int r = BACK ? kCut - 1 - i : i;
+        if (!(kept >> r & 1)) continue;
+        const int64_t row = (int64_t)w.base + chunk * kCut + r;
+        f(r, logistic_at<T>(A.gate, row * A.gs + w.head), logistic_at<T>(A.beta, row * A.bs + w.head));
+    }
+}
+
+// s = f(s, k) for the lane's numbers s of a state, k that of row r of K or Q (at `at`) there; rows of the
+// state that are not there stay zeros
+template <typename T, int KT, typename F>
+__device__ __forceinline__ void state_rows(Block (&S)[KT], uint32_t at, int r, int dk, const F &f)
+{
+#pragma unroll
+    for (int x = 0; x < KT; x++) {
+        float k[8];
+        Lane<T>::eight(at, r, x, k);
+        int rows = dk - 32 * x - 8 * (lane_id() >> 4);
+        asm volatile("" : "+v"(rows));                   // not made ahead of the loop over rows
+#pragma unroll
+        for (int i = 0; i < 8; i++) S[x].t[i >> 2][i & 3] = i < rows ? f(S[x].t[i >> 2][i & 3], k[i]) : S[x].t[i >> 2][i & 3];
+    }
+}
+
+template <typename T, int KT>
+__device__ __forceinline__ void scan_rows(const DeltaArgs &A, const Walk &w, int chunk, uint32_t at, int col, Block (&S)[KT],
+                                          Block &U, Block &Y)
+{
+    typedef WalkLds<T, KT, false> L;
+    U = Y = zero_block();
+    by_rows<T, false>(A, w, chunk, [&](int r, float a, float b) {
+        float held = 0.f, out = 0.f;
+        state_rows<T>(S, at, r, A.dk, [&](float s, float k) {
+            s *= a;
+            held = fmaf(s, k, held);
+            return s;
+        });
+        const float u = b * (Lane<T>::one(at + L::v, r, col) - quarters(held));
+        state_rows<T>(S, at, r, A.dk, [&](float s, float k) { return fmaf(k, u, s); });
+        state_rows<T>(S, at + L::q, r, A.dk, [&](float s, float q) {
+            out = fmaf(s, q, out);
+            return s;
+        });
+        put_row(U, r, u);
+        put_row(Y, r, A.scale * quarters(out));
+    });
+}
+
+template <typename T, int KT>
+__device__ __forceinline__ void back_rows(const DeltaArgs &A, const Walk &w, int chunk, uint32_t at, int col, Block (&E)[KT],
+                                          Block &Z, Block &dV)
+{
+    typedef WalkLds<T, KT, false> L;
+    Z = dV = zero_block();
+    by_rows<T, true>(A, w, chunk, [&](int r, float a, float b) {
+        const float d = A.scale * Lane<T>::one(at + L::v, r, col);
+        float z = 0.f;
+        state_rows<T>(E, at + L::q, r, A.dk, [&](float e, float q) { return fmaf(q, d, e); });
+        state_rows<T>(E, at, r, A.dk, [&](float e, float k) {
+            z = fmaf(e, k, z);
+            return e;
+        });
+        z = quarters(z);
+        state_rows<T>(E, at, r, A.dk, [&](float e, float k) { return a * fmaf(-k, b * z, e); });
+        put_row(Z, r, z);
+        put_row(dV, r, b * z);
+    });
+}
+
 // elements of a segment's matrix in its three parts
 template <int KT>
 constexpr int kMove = 3 * 1024 * KT * KT;
@@ -980,7 +1120,17 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
     char *u = static_cast<char *>(A.u) + (number * A.slices + slice) * 2048;
     char *states = static_cast<char *>(A.s0) + number * KT * A.slices * Lds<float>::kRows;
-    for (int i = 0; i < chunks; i++) {
+    auto leave = [&](int chunk, const Block &U, const Block &Y) {
+        if (TRAIN) rows_keep(scratch, U, u);
+        Turn<T> rows;
+        rows.turn(scratch, Y);
+        rows.write(o, r < w.rows - chunk * kCut, c, A.dv, A.ovec);
+        o += ostep;
+        u += ustep;
+        states += sstep;
+    };
+    int i = 0;
+    for (; i < chunks; i++) {
         meet_others();
         const uint32_t at = at0 + (i & 1) * L::size(A.slices), sc = at + L::sc;
         Block X = zero_block(), Y = zero_block(), V = zero_block();
@@ -1003,6 +1153,7 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
         const Part<kParts> xp = operand<kParts>(X);
         Block U = X;                                     // N is I and what the record has
         lane.template matrix<kParts, kParts>(U, at + L::n, xp);
+        if (!SUM && __builtin_expect(any_spoiled(U), 0)) break;
         const Block wt = row_weights(sc);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block wu = U;
@@ -1028,15 +1179,22 @@ __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
                 for (int e = 0; e < 4; e++) Y.t[a][e] *= sg.t[a][e];
             }
             lane.template matrix<kParts, kParts>(Y, at + L::p, op);
-            if (TRAIN) rows_keep(scratch, U, u);
-            Turn<T> rows;
-            rows.turn(scratch, Y);
-            rows.write(o, r < w.rows - i * kCut, c, A.dv, A.ovec);
-            o += ostep;
-            u += ustep;
-            states += sstep;
+            leave(i, U, Y);
         }
     }
+    if (!SUM)
+#pragma unroll 1
+        for (bool there = true; i < chunks; i++, there = false) {
+            if (!there) {                                // the chunk that ended the loop above is there already
+                meet_others();
+                if (TRAIN)
+#pragma unroll
+                    for (int x = 0; x < KT; x++) state_keep(scratch, S[x], states, x, A.slices, slice);
+            }
+            Block U, Y;
+            scan_rows<T, KT>(A, w, i, at0 + (i & 1) * L::size(A.slices), col, S, U, Y);
+            leave(i, U, Y);
+        }
     if (SUM) {
         if (values) state_write<KT>(S, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         else {
@@ -1089,9 +1247,15 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
     const int64_t number = (int64_t)w.tile0 * A.heads + w.head;
     char *z = static_cast<char *>(A.z) + (number * A.slices + slice) * 2048 + chunks * zstep;
     char *states = static_cast<char *>(A.e) + number * KT * A.slices * Lds<float>::kRows + chunks * sstep;
-    for (int s = 0; s < chunks; s++) {
+    auto leave = [&](int chunk, const Block &Z, const Block &dV) {
+        rows_keep(scratch, Z, z);
+        Turn<T> rows;
+        rows.turn(scratch, dV);
+        rows.write(dv, r < w.rows - chunk * kCut, c, A.dv, A.ovec);
+    };
+    int s = 0;
+    for (; s < chunks; s++) {
         meet_others();
-        const int i = chunks - 1 - s;
         const uint32_t at = at0 + (s & 1) * L::size(A.slices), sc = at + L::sc;
         dv -= vstep;
         z -= zstep;
@@ -1116,6 +1280,7 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
         const Part<kParts> xp = operand<kParts>(X);
         Block Z = X;
         lane.template matrix_turned<kParts, kParts>(Z, at + L::n, xp);
+        if (!SUM && __builtin_expect(any_spoiled(Z), 0)) break;
         const Block bg = row_scalars(sc + 4 * kScBG), sg = row_scalars(sc + 4 * kScG);
         const float end = lds_read<float>(sc + 4 * kScEnd);
         Block gz = Z;
@@ -1137,17 +1302,30 @@ __global__ __launch_bounds__(576) void delta_back(DeltaArgs A)
                 mm<kParts>(E[x].t[a], lane.column(at + L::q, x, a), op);
             }
         if (!SUM) {
-            rows_keep(scratch, Z, z);
-            Turn<T> rows;
             const Block b = row_scalars(sc + 4 * kScB);
+            Block dV = Z;
 #pragma unroll
             for (int a = 0; a < 2; a++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) Z.t[a][e] *= b.t[a][e];
-            rows.turn(scratch, Z);
-            rows.write(dv, r < w.rows - i * kCut, c, A.dv, A.ovec);
+                for (int e = 0; e < 4; e++) dV.t[a][e] *= b.t[a][e];
+            leave(chunks - 1 - s, Z, dV);
         }
     }
+    if (!SUM)
+#pragma unroll 1
+        for (bool there = true; s < chunks; s++, there = false) {
+            if (!there) {
+                meet_others();
+                dv -= vstep;
+                z -= zstep;
+                states -= sstep;
+#pragma unroll
+                for (int x = 0; x < KT; x++) state_keep(scratch, E[x], states, x, A.slices, slice);
+            }
+            Block Z, dV;
+            back_rows<T, KT>(A, w, chunks - 1 - s, at0 + (s & 1) * L::size(A.slices), col, E, Z, dV);
+            leave(chunks - 1 - s, Z, dV);
+        }
     if (SUM) {
         state_write<KT>(E, A.starts + w.part * A.dk * A.dv, A.dk, A.dv, col);
         return;
@@ -1316,6 +1494,7 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
     bring_rows<T>(row_rsrc(static_cast<const T *>(A.q) + row * A.qs + key * A.qh), row_at<T>(kept, A.qs), at + L::q, 2 * KT, wave, KT);
     bring(key * A.group);
     f32x16_t dq = zero16(), dk = zero16();               // transposed: a row a lane
+    bool spoiled = false;
     for (int g = 0; g < A.group; g++) {
         const int head = key * A.group + g;
         if (g) {
@@ -1483,8 +1662,105 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
                     dg = expf(-gate) == INFINITY ? 0.f : (suffix + prefix + end * state) / (1.f + expf(gate));
                     db = owns[c] / (1.f + expf(beta));
                 }
+                spoiled = spoiled || fmaf(dg, 0.f, db * 0.f) != 0.f;
                 Row<T>::put1(static_cast<T *>(A.dgate) + (row + c) * A.heads + head, dg);
                 Row<T>::put1(static_cast<T *>(A.dbeta) + (row + c) * A.heads + head, db);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i++) spoiled = spoiled || fmaf(dq[i], 0.f, dk[i] * 0.f) != 0.f;
+    if (__builtin_expect(__syncthreads_or(spoiled), 0)) {
+        // Something is not finite, and as products that reaches rows it has no part in: the chunk again by
+        // the rule's own derivative, row by row from the last, the state before each made again.
+        dq = dk = zero16();
+        const T *kr = static_cast<const T *>(A.k) + row * A.ks + key * A.kh, *qr = static_cast<const T *>(A.q) + row * A.qs + key * A.qh;
+        const int own = 32 * wave + c;                   // the lane's row of a state
+        const bool there = own < A.dk;
+        for (int g = 0; g < A.group; g++) {
+            const int head = key * A.group + g, n = A.slices;
+            const int64_t number = (int64_t)tile * A.heads + head;
+            const uint32_t uat = at + L::u, zat = uat + n * 2048, oat = zat + n * 2048;
+            __syncthreads();
+            bring(head);
+            meet();
+            if (l < kCut) red[wave][0][l] = red[wave][1][l] = 0.f;
+            // 16 columns at a time; rows of operands hold elements 8 h + 0 .. 7 of row r in lane 32 h + r
+#pragma unroll 1
+            for (int x = 0; x < n; x++) {
+                float E[8], S[8], u[8], z[8], o[8];
+                auto state = [&](const void *from, float (&f)[8]) {
+                    Kept s;
+                    s.load(static_cast<const char *>(from) + (number * KT + wave) * n * Lds<float>::kRows, x);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) f[e] = there ? __uint_as_float(s.w[e >> 2][e & 3]) : 0.f;
+                };
+                auto fp32 = [&](uint32_t from, int r, float (&f)[8]) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) f[e] = lds_read<float>(from + x * 2048 + (e >> 2) * 1024 + (32 * h + r) * 16 + (e & 3) * 4);
+                };
+                state(A.e, E);
+#pragma unroll 1
+                for (int t = left - 1; t >= 0; t--) {
+                    if (!(kept >> t & 1)) continue;
+                    const float kt = there ? Row<T>::get1(kr + t * A.ks + own) : 0.f, qt = there ? Row<T>::get1(qr + t * A.qs + own) : 0.f;
+                    const float a = logistic_at<T>(A.gate, (row + t) * A.gs + head), b = logistic_at<T>(A.beta, (row + t) * A.bs + head);
+                    state(A.s0, S);
+#pragma unroll 1
+                    for (int j = 0; j < t; j++) {
+                        if (!(kept >> j & 1)) continue;
+                        const float kj = there ? Row<T>::get1(kr + j * A.ks + own) : 0.f;
+                        const float aj = logistic_at<T>(A.gate, (row + j) * A.gs + head);
+                        fp32(uat, j, u);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) S[e] = fmaf(kj, u[e], aj * S[e]);
+                    }
+                    fp32(uat, t, u);
+                    fp32(zat, t, z);
+                    if constexpr (sizeof(T) == 4) fp32(oat, t, o);
+                    else
+#pragma unroll
+                        for (int e = 0; e < 8; e++) o[e] = bf16_lo((uint32_t)lds_read<uint16_t>(oat + x * 1024 + (32 * h + t) * 16 + e * 2));
+                    float sq = 0.f, sk = 0.f, da = 0.f, zu = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        if (!there || 16 * x + 8 * h + e >= A.dv) continue;
+                        const float d = A.scale * o[e], bz = b * z[e], held = a * S[e];
+                        const float f = fmaf(qt, d, E[e]), rest = fmaf(-kt, bz, f);
+                        sq = fmaf(fmaf(kt, u[e], held), d, sq);
+                        sk = fmaf(f, u[e], fmaf(-held, bz, sk));
+                        da = fmaf(rest, S[e], da);
+                        E[e] = a * rest;
+                        zu = fmaf(z[e], u[e], zu);
+                    }
+                    sq = both(sq);
+                    sk = both(sk);
+                    zu = both(zu);
+#pragma unroll
+                    for (int m = 1; m < 32; m *= 2) da += __shfl_xor(da, m, 64);
+                    da = both(da);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {       // rows of the state into registers, of the chunk into lanes
+                        const float y = __shfl(sq, kk0(i) + 4 * h, 64), v = __shfl(sk, kk0(i) + 4 * h, 64);
+                        dq[i] += c == t ? y : 0.f;
+                        dk[i] += c == t ? v : 0.f;
+                    }
+                    if (l == 0) {                        // row 0 of a state is always there
+                        red[wave][0][t] += da;
+                        red[wave][1][t] += zu;
+                    }
+                }
+            }
+            __syncthreads();
+            if (wave == 0 && h == 0 && keep) {
+                float da = 0.f;
+#pragma unroll
+                for (int w = 0; w < KT; w++) da += red[w][0][c];
+                const float gate = Row<T>::get1(static_cast<const T *>(A.gate) + (row + c) * A.gs + head);
+                const float beta = Row<T>::get1(static_cast<const T *>(A.beta) + (row + c) * A.bs + head);
+                const float a = 1.f / (1.f + expf(-gate));
+                Row<T>::put1(static_cast<T *>(A.dgate) + (row + c) * A.heads + head, a * da / (1.f + expf(gate)));
+                Row<T>::put1(static_cast<T *>(A.dbeta) + (row + c) * A.heads + head, red[0][1][c] / (1.f + expf(beta)));
             }
         }
     }
