@@ -1417,8 +1417,6 @@ __global__ __launch_bounds__(64 * kJoined + 64) void delta_join(DeltaArgs A)
 
 // ----------------------------------------------------------------- gradients
 
-constexpr int kKeptMost = kDeltaDim / 16;
-
 // 32 rows x 16 elements of a state kept as an operand in memory
 struct Kept {
     u32x4_t w[2];
@@ -1448,7 +1446,7 @@ struct GradLds {
 // are taken with, D, D^T and B + B^T, is made by a wavefront each and handed over in LDS; the
 // first makes dgate and dbeta.  Bound by what it reads, half of it the two sides' states.
 template <typename T, int KT>
-__global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
+__global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
 {
     typedef GradLds<T, KT> L;
     extern __shared__ __attribute__((aligned(1024))) char lds[];
@@ -1505,14 +1503,6 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
         const char *S0 = static_cast<const char *>(A.s0) + (number * KT + wave) * n * Lds<float>::kRows;
         const char *E0 = static_cast<const char *>(A.e) + (number * KT + wave) * n * Lds<float>::kRows;
         const uint32_t sc = at + L::sc, uat = at + L::u, zat = uat + n * 2048, oat = zat + n * 2048;
-        // the states' rows are on their way while the chunk's own products are made
-        Kept S[kKeptMost], E[kKeptMost];
-#pragma unroll
-        for (int x = 0; x < kKeptMost; x++)
-            if (x < n) {
-                S[x].load(S0, x);
-                E[x].load(E0, x);
-            }
         meet();
         const float b = lds_read<float>(sc + 4 * (kScB + c)), bg = lds_read<float>(sc + 4 * (kScBG + c)),
                     sg = lds_read<float>(sc + 4 * (kScG + c)), wt = c == 31 ? 1.f : lds_read<float>(sc + 4 * (kScW + c)),
@@ -1587,6 +1577,11 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
             }
         }
         __syncthreads();
+        // the states' rows: 16 columns a step, the next step's on their way (all of them on their way from
+        // the start: one wavefront a SIMD instead of two)
+        Kept S[2], E[2];
+        S[0].load(S0, 0);
+        E[0].load(E0, 0);
 #pragma unroll
         for (int kc = 0; kc < 2; kc++) {
             const auto kt = Lds<T>::turned(at, columns, wave, kc), qt = Lds<T>::turned(at + L::q, columns, wave, kc);
@@ -1595,19 +1590,25 @@ __global__ __launch_bounds__(64 * KT) void delta_grads(DeltaArgs A)
             mm<kParts>(dk, qt, staged<kParts>(at + L::with, 2 + kc));
         }
         // with the states: rows of S and E by rows of dO, Z and U, and the rows' own products of S and E
-        f32x16_t t1 = zero16(), t2 = zero16(), t3 = zero16(), se = zero16();
+        f32x16_t t1 = zero16(), t2 = zero16(), t3 = zero16();
+        float inner = 0.f;
+#pragma unroll 1
+        for (int x0 = 0; x0 < n; x0 += 2)
 #pragma unroll
-        for (int x = 0; x < kKeptMost; x++)
-            if (x < n) {
-                const auto s0 = S[x].operand(), e0 = E[x].operand();
+            for (int i = 0; i < 2; i++) {
+                const int x = x0 + i;
+                if (x >= n) break;
+                if (x + 1 < n) {
+                    S[1 - i].load(S0, x + 1);
+                    E[1 - i].load(E0, x + 1);
+                }
+                const auto s0 = S[i].operand();
                 mm<kParts>(t1, s0, Lds<T>::rows(oat, x));
                 mm<kParts>(t2, s0, Lds<float>::rows(zat, x));
-                mm<kParts>(t3, e0, Lds<float>::rows(uat, x));
-                mm<kParts>(se, s0, e0);
-            }
-        float inner = 0.f;
+                mm<kParts>(t3, E[i].operand(), Lds<float>::rows(uat, x));
 #pragma unroll
-        for (int i = 0; i < 16; i++) inner += kk0(i) + 4 * h == c ? se[i] : 0.f;
+                for (int j = 0; j < 8; j++) inner = fmaf(__uint_as_float(S[i].w[j >> 2][j & 3]), __uint_as_float(E[i].w[j >> 2][j & 3]), inner);
+            }
         // the row's own elements 32 wave + kk(i, h), which meet its sums with the states
         float dots = 0.f, writes = 0.f;
 #pragma unroll
