@@ -46,9 +46,12 @@ struct RotaryArgs {
     float scale, sign;
 };
 
-// a frequency (radians a step) as a fraction of a turn in units of 2^-64; 1 / (2 pi) in two doubles
+// a frequency (radians a step) as a fraction of a turn in units of 2^-64; 1 / (2 pi) in two doubles.
+// What hi has beyond its whole turns has to be of hi as it is rounded (contracted into the product
+// it would hold what lo holds).
 __device__ __forceinline__ uint64_t turn_of(double f)
 {
+#pragma clang fp contract(off)
     constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
     const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
     const double part = hi - floor(hi);
