@@ -6,7 +6,8 @@
 //
 // Angles.  Positions are int32 and may be elapsed seconds, so pos * frequency in fp32 would
 // lose the angle.  A frequency becomes a 64-bit fraction of a turn, whose product with the
-// position wraps at whole turns by itself: what is left is exact but for 2^-64 |pos| turns.
+// position wraps at whole turns by itself: what is left is exact but for 2^-64 |pos| turns (7e-10
+// radians at most).
 // Its top 32 bits split into a quadrant and an angle within +-pi/4, where the Taylor series
 // of sine (to the 9th power) and cosine (to the 10th) are within 3e-9 of them.
 //
@@ -47,15 +48,16 @@ struct RotaryArgs {
 };
 
 // a frequency (radians a step) as a fraction of a turn in units of 2^-64; 1 / (2 pi) in two doubles.
-// What hi has beyond its whole turns has to be of hi as it is rounded (contracted into the product
-// it would hold what lo holds).
+// Of its magnitude: hi less its whole turns is exact for hi >= 0 alone, and has to be of hi as it is
+// rounded (contracted into the product it would hold what lo holds).
 __device__ __forceinline__ uint64_t turn_of(double f)
 {
 #pragma clang fp contract(off)
     constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
-    const double hi = f * kHi, lo = fma(f, kHi, -hi) + f * kLo;
+    const double m = fabs(f), hi = m * kHi, lo = fma(m, kHi, -hi) + m * kLo;
     const double part = hi - floor(hi);
-    return (uint64_t)(part * 0x1p64) + (uint64_t)(int64_t)(lo * 0x1p64);
+    const uint64_t turn = (uint64_t)rint(part * 0x1p64) + (uint64_t)(int64_t)rint(lo * 0x1p64);
+    return f < 0. ? 0 - turn : turn;
 }
 
 __device__ __forceinline__ void turned(uint64_t turn, int pos, float &c, float &s)

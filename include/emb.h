@@ -599,8 +599,8 @@ emb_status emb_norm_backward(const emb_norm *d, const float *stats, const void *
  * Rotary positions of queries and keys: pair j of a head's first 2 pairs elements is turned
  * by t = pos * frequencies[j] radians,
  *   (a, b) -> scale (a cos t - b sin t, b cos t + a sin t),
- * and the other elements are copied.  t is exact to 1e-9 radians for every int32 position.
- * Frequencies beyond 1e9 in magnitude (and NaN) give NaN.
+ * and the other elements are copied.  Sines and cosines are within 2e-7 of t's for every int32
+ * position.  Frequencies may be negative; beyond 1e9 in magnitude (and NaN) they give NaN.
  */
 enum { EMB_ROTARY_HALF = 0,          /* pairs (j, j + pairs)   */
        EMB_ROTARY_INTERLEAVED = 1 }; /* pairs (2 j, 2 j + 1)   */

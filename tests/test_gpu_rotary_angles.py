@@ -1,5 +1,5 @@
-"""Rotary positions' angles at the ends of the positions' range, for frequencies of any size, against
-angles reduced in whole numbers."""
+"""Rotary positions' angles at the ends of the positions' range, for frequencies of either sign and
+any size, against angles reduced in whole numbers."""
 from fractions import Fraction
 
 import pytest
@@ -25,7 +25,7 @@ def angles(pos, freq):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
-@pytest.mark.parametrize("sign", [1.0])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
 def test_far_positions(sign, layout, dtype):
     """The angle's own rounding to fp32 (up to pi / 4: 5e-8) and the sine's and cosine's are 1e-7,
     two products and a sum follow."""
@@ -53,3 +53,11 @@ def test_far_positions(sign, layout, dtype):
         bound += R.unit(dtype) * want.abs()
         assert (off <= bound).all(), float((off / bound).max())
 
+
+def test_a_negative_frequency_turns_back():
+    """To the bit what the negative position turns."""
+    gen = torch.Generator().manual_seed(42)
+    q = torch.randn(50, 1, 2 * len(FREQUENCIES), generator=gen).cuda()
+    p = torch.randint(-2 ** 31 + 1, 2 ** 31, (50,), generator=gen).int().cuda()
+    f = torch.tensor(FREQUENCIES, dtype=torch.float64, device="cuda")
+    assert torch.equal(E.rotary(q, None, p, None, -f)[0], E.rotary(q, None, -p, None, f)[0])
