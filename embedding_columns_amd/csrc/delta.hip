@@ -1799,12 +1799,12 @@ template <typename T>
 __global__ __launch_bounds__(256) void delta_pack(const T *x, int64_t xs, int64_t xh, T *y, int64_t n, int heads, int d,
                                                   int padded)
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n * heads * padded) return;
-    const int c = (int)(i % padded);
-    const int64_t rh = i / padded;
-    const int64_t r = rh / heads, h = rh % heads;
-    *gp(y + i) = c < d ? *gp(x + r * xs + h * xh + c) : T(0);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n * heads * padded; i += (int64_t)gridDim.x * 256) {
+        const int c = (int)(i % padded);
+        const int64_t rh = i / padded;
+        const int64_t r = rh / heads, h = rh % heads;
+        *gp(y + i) = c < d ? *gp(x + r * xs + h * xh + c) : T(0);
+    }
 }
 
 // ------------------------------------------------------------------ one step
@@ -2024,12 +2024,14 @@ emb_status delta_launched()
 }
 
 // rows as the kernels read them: in place, or packed into *ws, which moves on
+constexpr int64_t kPackMost = int64_t(1) << 22;          // workgroups: below a launch's 2^32 threads
 void delta_rows(const emb_delta *d, size_t packed, const void *&x, int64_t &xs, int64_t &xh, int heads, int dim, char *&ws,
                 hipStream_t st)
 {
     if (!packed) return;
     const int padded = (dim + 31) / 32 * 32;
-    const int64_t blocks = (d->n * heads * padded + 255) / 256;
+    int64_t blocks = (d->n * heads * padded + 255) / 256;
+    if (blocks > kPackMost) blocks = kPackMost;
     if (blocks && d->dtype == EMB_BF16)
         hipLaunchKernelGGL((delta_pack<uint16_t>), dim3((unsigned)blocks), dim3(256), 0, st, static_cast<const uint16_t *>(x),
                            xs, xh, reinterpret_cast<uint16_t *>(ws), d->n, heads, dim, padded);
@@ -2092,12 +2094,13 @@ int64_t delta_walks(const emb_delta *d, const DeltaPlan &p)
     return (p.cut ? seg_tiles(d->n, d->samples, 1, kSpan) : d->samples) * d->heads;
 }
 
-emb_status delta_sizes(const emb_delta *d, const DeltaPlan &p)
+emb_status delta_sizes(const emb_delta *d, const DeltaPlan &p, bool train)
 {
     // a launch's threads in one dimension are counted in 32 bits
-    const int64_t most = (int64_t(1) << 32) - 1, packed = d->n * d->heads * 128;
-    if (p.tiles > most / 256 || delta_walks(d, p) > most / 1024 || packed > most)
-        return fail(EMB_ERR_UNSUPPORTED, "delta rule: too many rows, samples and heads for one launch");
+    const int64_t most = (int64_t(1) << 32) - 1, tiles = p.tiles + p.ranks;
+    const int slices = p.cut && p.slices < 2 * p.kt ? 2 * p.kt : p.slices;
+    if (tiles > most / (64 * (train ? p.kt : 1)) || delta_walks(d, p) > most / (64 * slices + 64))
+        return fail(EMB_ERR_UNSUPPORTED, "delta rule: too many rows, or samples x heads, for one launch");
     return EMB_OK;
 }
 
@@ -2158,11 +2161,13 @@ extern "C" emb_status emb_delta_query(const emb_delta *d, int32_t training, size
                                       size_t *backward_bytes)
 {
     if (!d) return fail(EMB_ERR_INVALID_ARG, "delta rule descriptor is NULL");
-    const emb_status s = delta_check(d);
+    emb_status s = delta_check(d);
     if (s != EMB_OK) return s;
     if (!saved_bytes || !forward_bytes || !backward_bytes)
         return fail(EMB_ERR_INVALID_ARG, "delta rule: output pointers must be given");
     const DeltaPlan p = delta_plan(d, training != 0);
+    s = delta_sizes(d, p, training != 0);
+    if (s != EMB_OK) return s;
     *saved_bytes = training ? p.saved : 0;
     *forward_bytes = p.forward;
     *backward_bytes = training ? p.backward : 0;
@@ -2182,7 +2187,7 @@ extern "C" emb_status emb_delta_forward(const emb_delta *d, void *o, float *last
         return fail(EMB_ERR_INVALID_ARG, "delta rule: o and last must be given and aligned, saved to 256 bytes");
     if (workspace_bytes < p.forward || (p.forward && (!workspace || !aligned(workspace, 256))))
         return fail(EMB_ERR_WORKSPACE, "delta rule: the workspace is smaller than the query returned, or not 256-byte aligned");
-    s = delta_sizes(d, p);
+    s = delta_sizes(d, p, train);
     if (s != EMB_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     DeltaArgs A = delta_args(d, p);
@@ -2233,7 +2238,7 @@ extern "C" emb_status emb_delta_backward(const emb_delta *d, const void *saved, 
     if (d->n > 1 && dout_stride > kDeltaStrideMost) return fail(EMB_ERR_UNSUPPORTED, "delta rule: row strides must be <= 2^21");
     if (workspace_bytes < p.backward || (p.backward && (!workspace || !aligned(workspace, 256))))
         return fail(EMB_ERR_WORKSPACE, "delta rule: the workspace is smaller than the query returned, or not 256-byte aligned");
-    s = delta_sizes(d, p);
+    s = delta_sizes(d, p, train);
     if (s != EMB_OK) return s;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     DeltaArgs A = delta_args(d, p);
