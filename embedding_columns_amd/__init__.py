@@ -1138,12 +1138,15 @@ class GatedDelta(torch.autograd.Function):
         dstate = None
         if state is not None and ctx.needs_input_grad[5]:
             dstate = state.new_empty(state.shape)
-        desc = ctx.desc if in_place else _delta_desc(q, k, v, gate, beta, offsets, state, mask, ctx.scale)
-        ws = _scratch(ctx.need, v)
+        desc, need = ctx.desc, ctx.need
+        if not in_place:                                 # rows that lie otherwise may have to be packed
+            desc = _delta_desc(q, k, v, gate, beta, offsets, state, mask, ctx.scale)
+            need = emb_delta_query(desc)[2]
+        ws = _scratch(need, v)
         _check(lib().emb_delta_backward(
             C.byref(desc), saved.data_ptr(), do.data_ptr(), do.stride(0), do.stride(1),
             _address(dlast), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dgate.data_ptr(),
-            dbeta.data_ptr(), _address(dstate), _address(ws), ctx.need, _stream()))
+            dbeta.data_ptr(), _address(dstate), _address(ws), need, _stream()))
         return dq, dk, dv, dgate, dbeta, dstate, None, None, None
 
 

@@ -1963,14 +1963,18 @@ struct DeltaPlan {
 };
 
 // Samples are cut into segments where there are too few of them, times the heads, to fill the
-// chip.  A cut walk is walked twice and its segments are joined one after another.  Heads of 64 in
-// bf16, forward / with the backward, in us, uncut and cut:
-//   walks x rows      4 x 2048         4 x 4096         32 x 2048       64 x 2048        64 x 4096
-//   uncut / cut       88, 210          162, 383         94, 243         99, 285          181, 546
-//                     89, 206          94, 214          97, 243         114, 297         169, 514
-//   walks x rows      4 x 16384        32 x 16384       64 x 16384      128 x 4096       128 x 16384
-//   uncut / cut       592, 1444        669, 1745        728, 2093       241, 734         878, 2785
-//                     114, 278         328, 885         621, 1731       299, 921         1166, 3304
+// chip.  A cut walk is walked twice and its segments are joined one after another.  Uncut and
+// cut, forward / with the backward, in us, 4 heads of dk x dv:
+//   walks x rows      4 x 2048         4 x 16384        32 x 2048       64 x 2048        64 x 4096        128 x 4096
+//   bf16 64 x 64      101, 257         696, 1784        106, 297        112, 350         207, 674         246, 930
+//                     95, 231          119, 305         103, 275        117, 344         171, 602         281, 1061
+//   bf16 128 x 128    183, 495         1349, 3694       189, 601        205, 777         394, 1536        464, 2187
+//                     171, 443         227, 630         186, 544        238, 787         415, 1443        693, 2514
+//   fp32 64 x 64      194, 440         1435, 3231       202, 511        210, 598         407, 1176        451, 1543
+//                     173, 405         200, 509         182, 482        217, 607         335, 1049        524, 1778
+//   fp32 128 x 128    462, 1019        3577, 7939       475, 1202       491, 1415        972, 2801        1066, 3668
+//                     408, 937         467, 1213        425, 1125       595, 1510        1039, 2815       1671, 4713
+// 4 x 1024 rows take half as long uncut in all of them.
 bool delta_cut(const emb_delta *d)
 {
     const int64_t walks = (int64_t)d->samples * d->heads;
@@ -2011,8 +2015,7 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
     p.v = rows_ready(d->v, d->v_stride, d->v_head_stride, d->dv, p.el) ? 0 : values;
     p.saved = p.order + p.recs + p.states + p.us + p.moves;
     p.forward = (train ? 0 : p.order + p.recs + p.moves) + p.starts + p.q + p.k + p.v;
-    // the tensors that the backward gets may lie otherwise than the forward's did
-    p.backward = p.states + p.us + p.starts + 2 * keys + values;
+    p.backward = p.states + p.us + p.starts + p.q + p.k + values;        // how dout lies is not known here
     return p;
 }
 

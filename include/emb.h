@@ -543,8 +543,8 @@ typedef struct emb_delta {       /* host */
 } emb_delta;
 
 /* training 0: saved_bytes and backward_bytes are 0.  saved_bytes: of `saved`; the others: of
- * the workspaces of the forward (with `saved` if training) and of the backward.  What the query
- * takes, the calls take: n at most 2^31 - 65536, and (n / 32 + samples + 2) x 64, in training x dk / 32
+ * the workspaces of the forward (with `saved` if training) and of the backward; they go by how the
+ * descriptor's rows lie, since some have to be packed.  What the query takes, the calls take: n at most 2^31 - 65536, and (n / 32 + samples + 2) x 64, in training x dk / 32
  * rounded up, and samples x heads x (64 + 4 dv rounded up to 64) below 2^32. */
 emb_status emb_delta_query(const emb_delta *d, int32_t training, size_t *saved_bytes /* host */,
                            size_t *forward_bytes /* host */, size_t *backward_bytes /* host */);

@@ -36,3 +36,13 @@ def test_what_a_launch_holds(L, kw, training):  # noqa: F811
 def test_what_it_does_not(L, kw, training):  # noqa: F811
     assert statuses(delta(**kw), training) == (2, 2)
     assert "too many" in E.emb_last_error()
+
+
+def test_workspaces_go_by_what_is_packed(L):  # noqa: F811
+    """Keys and queries that are read in place take no room in the backward's workspace."""
+    n, rows = 1000, 1000 * 2 * 64 * 2
+    ready = E.emb_delta_query(delta(n=n))
+    one, two = E.emb_delta_query(delta(n=n, k=4100)), E.emb_delta_query(delta(n=n, k=4100, q=4100))
+    assert ready[0] == one[0] == two[0]
+    for i in (1, 2):
+        assert rows <= one[i] - ready[i] < rows + 256 and two[i] - one[i] == one[i] - ready[i]
