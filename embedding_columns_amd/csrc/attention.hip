@@ -87,9 +87,9 @@ struct Tile {
     static __device__ __forceinline__ int at(int r, int c) { return r * CH + (c ^ swizzle<CH>(r)); }
 };
 
-// LDS addresses of a tile: the lane's part is one number, and chunk and row of a read
-// come in as a constant xor and a constant offset (the swizzle is a xor of row bits, and
-// tiles are aligned to a row).  So a read costs one xor and no register that outlives it.
+// The products below read tiles by LDS address (lds_read): the lane's part is one number, and chunk
+// and row of a read come in as a constant xor and a constant offset (the swizzle is a xor of row
+// bits, and tiles are aligned to a row).  So a read costs one xor and no register that outlives it.
 
 // a row as a second operand: its even chunks in half 0, its odd ones in half 1
 template <typename T, int DP>

@@ -20,8 +20,6 @@
 
 namespace emb {
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-
 constexpr int kNormChannels = 16384;
 
 struct NormArgs {
@@ -43,41 +41,8 @@ struct NormArgs {
 
 // 16 bytes of a row that may start anywhere an element may
 template <typename T>
-struct Piece;
-template <>
-struct Piece<uint16_t> {
-    static constexpr int E = 8;
-    struct __attribute__((packed, aligned(2))) Raw {
-        u32x4_t w;
-    };
-    static __device__ __forceinline__ void open(const u32x4_t &w, float *f)
-    {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f[2 * j] = bf16_lo(w[j]);
-            f[2 * j + 1] = bf16_hi(w[j]);
-        }
-    }
-    static __device__ __forceinline__ u32x4_t shut(const float *f)
-    {
-        return u32x4_t{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])};
-    }
-};
-template <>
-struct Piece<float> {
-    static constexpr int E = 4;
-    struct __attribute__((packed, aligned(4))) Raw {
-        u32x4_t w;
-    };
-    static __device__ __forceinline__ void open(const u32x4_t &w, float *f)
-    {
-#pragma unroll
-        for (int j = 0; j < 4; j++) f[j] = __uint_as_float(w[j]);
-    }
-    static __device__ __forceinline__ u32x4_t shut(const float *f)
-    {
-        return u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-    }
+struct __attribute__((packed, aligned(sizeof(T)))) Raw {
+    u32x4_t w;
 };
 
 // Elements at .. at + E - 1 of a row, zeros behind its end.  WHOLE: rows are whole pieces.
@@ -85,8 +50,7 @@ template <typename T, bool WHOLE>
 __device__ __forceinline__ u32x4_t piece_read(const T *row, int at, int channels)
 {
     constexpr int E = Piece<T>::E;
-    typedef typename Piece<T>::Raw Raw;
-    if (WHOLE ? at < channels : at + E <= channels) return gp(reinterpret_cast<const Raw *>(row + at))->w;
+    if (WHOLE ? at < channels : at + E <= channels) return gp(reinterpret_cast<const Raw<T> *>(row + at))->w;
     if (WHOLE) return u32x4_t{0, 0, 0, 0};
     union {
         u32x4_t w;
@@ -102,14 +66,13 @@ template <typename T, bool WHOLE>
 __device__ __forceinline__ void piece_write(T *row, int at, int channels, const float *f)
 {
     constexpr int E = Piece<T>::E;
-    typedef typename Piece<T>::Raw Raw;
     union {
         u32x4_t w;
         T e[E];
     } u;
     u.w = Piece<T>::shut(f);
     if (WHOLE || at + E <= channels) {
-        gp(reinterpret_cast<Raw *>(row + at))->w = u.w;
+        gp(reinterpret_cast<Raw<T> *>(row + at))->w = u.w;
         return;
     }
 #pragma unroll
@@ -120,14 +83,13 @@ __device__ __forceinline__ void piece_write(T *row, int at, int channels, const 
 template <int E, bool WHOLE>
 __device__ __forceinline__ void param_read(const float *p, int at, int channels, float fill, float *f)
 {
-    typedef Piece<float>::Raw Raw;
 #pragma unroll
     for (int i = 0; i < E; i++) f[i] = fill;
     if (!p) return;
     if (WHOLE ? at < channels : at + E <= channels) {
 #pragma unroll
         for (int j = 0; j < E; j += 4) {
-            const u32x4_t v = gp(reinterpret_cast<const Raw *>(p + at + j))->w;
+            const u32x4_t v = gp(reinterpret_cast<const Raw<float> *>(p + at + j))->w;
 #pragma unroll
             for (int e = 0; e < 4; e++) f[j + e] = __uint_as_float(v[e]);
         }

@@ -22,9 +22,6 @@
 
 namespace emb {
 
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
 constexpr int kRotaryDim = 1024;       // largest head
 constexpr int kRotaryTable = 1024;     // angles of a workgroup
 constexpr int kRotaryThreads = 256;
@@ -77,48 +74,21 @@ __device__ __forceinline__ void turned(uint64_t turn, int pos, float &c, float &
 // i / d for i < 2^16 with magic = ceil(2^32 / d) (0: d is one)
 __device__ __forceinline__ int over(int i, int magic) { return magic ? (int)__umulhi((uint32_t)i, (uint32_t)magic) : i; }
 
-// 16 bytes as numbers and back
+// an element as a number and back
+__device__ __forceinline__ float open1(uint16_t x) { return bf16_lo((uint32_t)x); }
+__device__ __forceinline__ float open1(float x) { return x; }
 template <typename T>
-struct Pieces;
-template <>
-struct Pieces<uint16_t> {
-    static constexpr int E = 8;
-    static __device__ __forceinline__ void open(u32x4_t w, float *f)
-    {
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            f[2 * j] = bf16_lo(w[j]);
-            f[2 * j + 1] = bf16_hi(w[j]);
-        }
-    }
-    static __device__ __forceinline__ u32x4_t shut(const float *f)
-    {
-        return u32x4_t{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])};
-    }
-    static __device__ __forceinline__ float open1(uint16_t x) { return bf16_lo((uint32_t)x); }
-    static __device__ __forceinline__ uint16_t shut1(float x) { return bf16_rne(x); }
-};
-template <>
-struct Pieces<float> {
-    static constexpr int E = 4;
-    static __device__ __forceinline__ void open(u32x4_t w, float *f)
-    {
-#pragma unroll
-        for (int j = 0; j < 4; j++) f[j] = __uint_as_float(w[j]);
-    }
-    static __device__ __forceinline__ u32x4_t shut(const float *f)
-    {
-        return u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
-    }
-    static __device__ __forceinline__ float open1(float x) { return x; }
-    static __device__ __forceinline__ float shut1(float x) { return x; }
-};
+__device__ __forceinline__ T shut1(float x)
+{
+    if constexpr (sizeof(T) == 2) return bf16_rne(x);
+    else return x;
+}
 
 // WIDE: heads in pieces of 16 bytes, else pair by pair; HALF: pairs (j, j + pairs).
 template <typename T, bool WIDE, bool HALF>
 __global__ __launch_bounds__(kRotaryThreads) void rotary_turn(RotaryArgs A)
 {
-    typedef Pieces<T> P;
+    typedef Piece<T> P;
     constexpr int E = P::E;
     __shared__ __attribute__((aligned(16))) float cs[kRotaryTable], sn[kRotaryTable];
     const bool second = blockIdx.x >= A.blocks0;
@@ -187,9 +157,9 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_turn(RotaryArgs A)
                 *gp(reinterpret_cast<u32x4_t *>(dst + i * E)) = out;
             } else if (i < A.pairs) {
                 const int at = HALF ? i : 2 * i, bt = HALF ? i + A.pairs : 2 * i + 1;
-                const float a = P::open1(*gp(src + at)), b = P::open1(*gp(src + bt)), cc = c[i], ss = s[i];
-                *gp(dst + at) = P::shut1(a * cc - b * ss);
-                *gp(dst + bt) = P::shut1(b * cc + a * ss);
+                const float a = open1(*gp(src + at)), b = open1(*gp(src + bt)), cc = c[i], ss = s[i];
+                *gp(dst + at) = shut1<T>(a * cc - b * ss);
+                *gp(dst + bt) = shut1<T>(b * cc + a * ss);
             } else {
                 const int at = A.pairs + i;
                 *gp(dst + at) = *gp(src + at);

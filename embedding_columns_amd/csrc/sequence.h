@@ -1,5 +1,6 @@
-// sequence.h -- what the sequence operators (attention.hip, recurrence.hip) share:
-// cutting jagged rows into tiles, and the edges of a segment.
+// sequence.h -- what the sequence and encoder operators (attention.hip, recurrence.hip, delta.hip,
+// norm.hip, rotary.hip) share: cutting jagged rows into tiles, the edges of a segment, LDS by
+// address, rows in pieces of 16 bytes.
 #pragma once
 
 #include "device.h"
@@ -99,7 +100,6 @@ __device__ __forceinline__ void lds_write(uint32_t at, V v)
     *(__attribute__((address_space(3))) V *)(uintptr_t)at = v;
 }
 
-
 // A 16-byte piece per lane from memory straight into 1 KB of LDS at `to`: lane l's
 // piece lands at to + 16 l.  `off` counts bytes from the descriptor's base (plus the
 // uniform `more`); an offset of kNowhere is out of the descriptor's range, reads no
@@ -136,5 +136,38 @@ constexpr float kLn2 = 0.6931471805599453f;
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 __device__ __forceinline__ uint16_t bf16_rne(float x) { return (uint16_t)bf16x2_rne(x, 0.f); }
+
+// 16 bytes of a row as numbers and back
+template <typename T>
+struct Piece;
+template <>
+struct Piece<uint16_t> {
+    static constexpr int E = 8;
+    static __device__ __forceinline__ void open(const u32x4_t &w, float *f)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            f[2 * j] = bf16_lo(w[j]);
+            f[2 * j + 1] = bf16_hi(w[j]);
+        }
+    }
+    static __device__ __forceinline__ u32x4_t shut(const float *f)
+    {
+        return u32x4_t{bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7])};
+    }
+};
+template <>
+struct Piece<float> {
+    static constexpr int E = 4;
+    static __device__ __forceinline__ void open(const u32x4_t &w, float *f)
+    {
+#pragma unroll
+        for (int j = 0; j < 4; j++) f[j] = __uint_as_float(w[j]);
+    }
+    static __device__ __forceinline__ u32x4_t shut(const float *f)
+    {
+        return u32x4_t{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    }
+};
 
 }  // namespace emb
