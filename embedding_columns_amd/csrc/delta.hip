@@ -27,10 +27,10 @@
 //
 // What passes between them costs more than the rows themselves: what bounds the four is bytes,
 // then a walk's chain of dependent products.  bf16, 287434 rows in 256 samples, 4 heads of
-// 64 x 64: prepare 133 us (0.59 GB, 4.5 TB/s), scan 207 us (0.95 GB, 4.6 TB/s).  With
-// gradients, 68548 rows in 64 samples, 4 heads of 128 x 128: prepare 59 us, scan 200 us and back
-// 220 us (0.8 GB each; the longest of 256 walks on 256 CUs is twice the mean), grads 311 us
-// (1.25 GB, 4.0 TB/s).
+// 64 x 64: prepare 142 us (0.64 GB, 4.5 TB/s), scan 229 us (0.93 GB, 4.0 TB/s).  With
+// gradients, 68548 rows in 64 samples, 4 heads of 128 x 128: prepare 63 us, scan 316 us and back
+// 342 us (1.07 GB each; the longest of 256 walks on 256 CUs is twice the mean), grads 525 us
+// (1.75 GB, 3.3 TB/s).
 //
 // All products run on the matrix cores, the walks' in blocks of 16 x 16 (lane & 15 a column,
 // register i of quarter g = lane >> 4 row 4 g + i), the others' in 32 x 32 (lane & 31 a column,
@@ -277,7 +277,7 @@ __device__ __forceinline__ int first_tile(int base, int sample) { return base / 
 // ----------------------------------------------------------------- prepare
 
 // Walks begin in the order of their lengths, the longest first, since what begins last ends last
-// (delta_histories' scan: 242 us in the samples' own order, 206 so).  A lane counts the samples
+// (256 samples of 200..2000 rows, the scan: 289 us in the samples' own order, 232 so).  A lane counts the samples
 // that come before its own; wavefronts beside the chunks' do it.  Lengths from 2^20 on count as one.
 constexpr int kRanked = 1024;
 __device__ __forceinline__ void delta_order(const DeltaArgs &A, int block)
@@ -1080,9 +1080,10 @@ __device__ __forceinline__ int move_at(int row, int col)
 }
 
 // Walks forward, a workgroup a sample and head.  Half the columns a workgroup, twice the workgroups,
-// evened unequal samples out but read K, Q and records twice: train_delta's four kernels 764 us
-// and 852 so, a long history's 392 and 440.  SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does
-// to the state, as a matrix (1: the walk without values from the identity).
+// evened unequal samples out but read K, Q and records twice (with states kept in bf16, a step of
+// training of 64 samples with 4 heads of 128: 764 us and 852 so, a long history forward 392 and 440).
+// SUM: a segment's own part alone, what it adds (blockIdx.y 0) and what it does to the state, as a
+// matrix (1: the walk without values from the identity).
 template <typename T, int KT, bool TRAIN, bool SUM>
 __global__ __launch_bounds__(576) void delta_scan(DeltaArgs A)
 {
@@ -1675,9 +1676,13 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
         // Something is not finite, and as products that reaches rows it has no part in: the chunk again by
         // the rule's own derivative, row by row from the last, the state before each made again.
         dq = dk = zero16();
-        const T *kr = static_cast<const T *>(A.k) + row * A.ks + key * A.kh, *qr = static_cast<const T *>(A.q) + row * A.qs + key * A.qh;
         const int own = 32 * wave + c;                   // the lane's row of a state
         const bool there = own < A.dk;
+        auto element = [&](uint32_t from, int r) {       // its element of row r of K or Q (zero where it is not there)
+            const uint32_t in = (32 * (own >> 3 & 1) + r) * 16;
+            if constexpr (sizeof(T) == 4) return lds_read<float>(from + (own >> 4) * 2048 + (own >> 2 & 1) * 1024 + in + (own & 3) * 4);
+            else return bf16_lo((uint32_t)lds_read<uint16_t>(from + (own >> 4) * 1024 + in + (own & 7) * 2));
+        };
         for (int g = 0; g < A.group; g++) {
             const int head = key * A.group + g, n = A.slices;
             const int64_t number = (int64_t)tile * A.heads + head;
@@ -1686,6 +1691,8 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
             bring(head);
             meet();
             if (l < kCut) red[wave][0][l] = red[wave][1][l] = 0.f;
+            if (wave == 0 && keep) cross[h][c] = logistic_at<T>(h ? A.beta : A.gate, (row + c) * (h ? A.bs : A.gs) + head);
+            __syncthreads();
             // 16 columns at a time; rows of operands hold elements 8 h + 0 .. 7 of row r in lane 32 h + r
 #pragma unroll 1
             for (int x = 0; x < n; x++) {
@@ -1704,14 +1711,12 @@ __global__ __launch_bounds__(64 * KT, 2) void delta_grads(DeltaArgs A)
 #pragma unroll 1
                 for (int t = left - 1; t >= 0; t--) {
                     if (!(kept >> t & 1)) continue;
-                    const float kt = there ? Row<T>::get1(kr + t * A.ks + own) : 0.f, qt = there ? Row<T>::get1(qr + t * A.qs + own) : 0.f;
-                    const float a = logistic_at<T>(A.gate, (row + t) * A.gs + head), b = logistic_at<T>(A.beta, (row + t) * A.bs + head);
+                    const float kt = element(at, t), qt = element(at + L::q, t), a = cross[0][t], b = cross[1][t];
                     state(A.s0, S);
 #pragma unroll 1
                     for (int j = 0; j < t; j++) {
                         if (!(kept >> j & 1)) continue;
-                        const float kj = there ? Row<T>::get1(kr + j * A.ks + own) : 0.f;
-                        const float aj = logistic_at<T>(A.gate, (row + j) * A.gs + head);
+                        const float kj = element(at, j), aj = cross[0][j];
                         fp32(uat, j, u);
 #pragma unroll
                         for (int e = 0; e < 8; e++) S[e] = fmaf(kj, u[e], aj * S[e]);
@@ -2000,10 +2005,10 @@ DeltaPlan delta_plan(const emb_delta *d, bool train)
         p.starts = pad256(segments * d->dk * d->dv * 4);
     }
     // Where there are more walks than CUs.  Forward / with the backward in us, the samples' own order
-    // and the longest first: 256 x 200..2000 rows, 4 heads of 64: 371, 1444 and 344, 1335; 300 x
-    // 10..3000, 1 head: 203, 703 and 177, 606; 1024 x 50..800, 4 heads: 561, 2183 and 551, 2152;
+    // and the longest first, bf16 heads of 64: 256 x 200..2000 rows, 4 heads: 473, 1906 and 420, 1813; 300 x
+    // 10..3000, 1 head: 225, 899 and 193, 765; 1024 x 50..800, 4 heads: 580, 2697 and 564, 2663;
     // 256 x 1000: the same.  More and shorter samples are even enough by themselves (4000 x 20..200,
-    // 4 heads: 599, 2342 and 610, 2383).
+    // 4 heads: 632, 3018 and 646, 3082).
     if (!p.cut && (int64_t)d->samples * d->heads > 256 && d->samples <= kRanked && d->n / d->samples >= 64) {
         p.ranks = (d->samples + 63) / 64;
         p.order = (size_t)p.ranks * 256;
