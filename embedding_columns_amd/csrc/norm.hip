@@ -10,9 +10,9 @@
 // the next row on its way; in the backward each keeps its share of dw and db in registers,
 // leaves one row of them, and a second kernel adds these up in a fixed order.
 //
-// 140771 rows of 512 in bf16: forward 57 us (288 MB, 5.0 TB/s), backward 86 us (432 MB, 5.0 TB/s) and
-// 5 us for the sums.  8191 of 5000 in fp32: 59 us (328 MB, 5.6 TB/s), 99 us (491 MB, 5.0 TB/s) and
-// 6 us.  50 rows of 256: 3.6 us, a launch.
+// 140771 rows of 512 in bf16: forward 58 us (288 MB, 5.0 TB/s), backward 87 us (432 MB, 5.0 TB/s) and
+// 5 us for the sums.  8191 of 5000 in fp32: 61 us (328 MB, 5.4 TB/s), 102 us (491 MB, 4.8 TB/s) and
+// 6 us.  50 rows of 256: 3.8 us, a launch.
 #include <cmath>
 #include <string>
 

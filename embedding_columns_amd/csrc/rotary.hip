@@ -7,14 +7,13 @@
 // Angles.  Positions are int32 and may be elapsed seconds, so pos * frequency in fp32 would
 // lose the angle.  A frequency becomes a 64-bit fraction of a turn, whose product with the
 // position wraps at whole turns by itself: what is left is exact but for 2^-64 |pos| turns (7e-10
-// radians at most).
-// Its top 32 bits split into a quadrant and an angle within +-pi/4, where the Taylor series
-// of sine (to the 9th power) and cosine (to the 10th) are within 3e-9 of them.
+// radians at most).  Its top 32 bits split into a quadrant and an angle within +-pi/4, where the
+// Taylor series of sine (to the 9th power) and cosine (to the 10th) are within 3e-9 of them.
 //
 // The bound is reading and writing every element once.  A workgroup takes some rows, makes
 // their cosines and sines once in LDS, and turns all heads with them, 16 bytes a lane.
-// 28528 rows of 8 heads of 128 in bf16: 20.5 us (117 MB, 5.7 TB/s); 65838 rows of 3 and 6 heads, 24
-// of 40 elements, in fp32: 14.8 us (64 MB, 4.3 TB/s).
+// 28528 rows of 8 heads of 128 in bf16: 21 us (117 MB, 5.6 TB/s); 65838 rows of 3 and 6 heads, 24
+// of 40 elements, in fp32: 16.7 us (64 MB, 3.8 TB/s).
 #include <cmath>
 #include <string>
 
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_turn(RotaryArgs A)
     const int64_t row0 = (int64_t)(blockIdx.x - (second ? A.blocks0 : 0)) * A.rows;
     const int rows = (int)min((int64_t)A.rows, S.n - row0);
     // a pair a thread, as many rows side by side as there is room for (a thread that makes all rows
-    // of its pair: 20.5 us for the second example above)
+    // of its pair: 20.5 us at least for the second example above, 14.8 so)
     for (int p = threadIdx.x & ((1 << A.shift) - 1); p < A.pairs; p += 1 << A.shift) {
         const double f = *gp(A.freq + p);
         const bool far = !(fabs(f) <= 1e9);

@@ -522,7 +522,8 @@ emb_status emb_recurrence_step(int32_t dtype, int64_t rows, int32_t channels, co
  *   u_t = b_t (v_t - a_t S_(t-1)^T k_t),  S_t = a_t S_(t-1) + k_t u_t^T,  o_t = scale S_t^T q_t
  * from the sample's state (or zero).  Head h reads key head h / (heads / key_heads).  The
  * state stays bounded for keys of at most unit length.  A masked row keeps the state and
- * gives o_t = 0, whatever it holds, and has no gradient.
+ * gives o_t = 0, whatever it holds, and has no gradient.  NaN and infinities in kept rows or
+ * states reach what the formula takes them to, and nothing else.
  */
 typedef struct emb_delta {       /* host */
     int32_t dtype;               /* EMB_F32 | EMB_BF16: all but the states, and their gradients */
